@@ -654,3 +654,10 @@ def spherical(points: torch.Tensor, sph_min: Sequence[float], sph_cell: Sequence
     with torch.cuda.device(points.device):
         s.run(points)
         return s.outputs()
+
+
+# ---------------------------------------------------------- token operators --
+# (imported last: they use the library handle and the checks above)
+
+from .tokens import (attend, attend_grad, embed, embed_grad, gated_scan,  # noqa: E402,F401
+                     gated_scan_grad)
