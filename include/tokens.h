@@ -143,7 +143,7 @@ int tok_attend_grad(const tok_attention* args, const void* q, const void* k, con
  * TOK_SCAN_RUN tokens, [tok_scan_runs(t), width] float32, for tok_scan_grad.
  * Limits: t < 2^31, 1 <= width <= 65536, 1 <= docs <= 2^20.
  */
-#define TOK_SCAN_RUN 32
+#define TOK_SCAN_RUN 16
 int64_t tok_scan_runs(int64_t t);
 int64_t tok_scan_workspace_bytes(int64_t t, int64_t width);
 int tok_scan(const void* gate, const void* x, int32_t dtype, int64_t t, int64_t width,

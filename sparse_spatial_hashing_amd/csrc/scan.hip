@@ -27,7 +27,10 @@ struct ScanArgs {
     void* ggate;
     void* gx;
     float* grad_state;        // may be null
+    float* mul;               // [chunks, width]: what each chunk does to a state, then (add)
+    float* add;               // the state that enters it
     int t, width, docs, reverse;
+    int chunk, chunks;        // steps of a chunk (a multiple of kRun)
 };
 
 // a = sigmoid(f) and 1 - a, each to a few units in its last place: the smaller
@@ -40,91 +43,441 @@ __device__ __forceinline__ void gates(float f, float& a, float& keep) {
     keep = f >= 0.0f ? lo : hi;
 }
 
-// One thread per document and channel, along the document. Step s of the scan
-// over all tokens is token s, or t - 1 - s in reverse.
-template <typename T>
-__global__ __launch_bounds__(256) void k_scan_doc(ScanArgs a) {
-    const int c = blockIdx.y * blockDim.x + threadIdx.x;
-    const int range = blockIdx.x;
-    if (c >= a.width) return;
-    const int lo = tok_boundary(a.offsets, a.docs, a.t, range);
-    const int hi = max(lo, tok_boundary(a.offsets, a.docs, a.t, range + 1));
-    const bool doc = range >= 1 && range <= a.docs;
-    float h = doc && a.state ? a.state[(long long)(range - 1) * a.width + c] : 0.0f;
-    for (int k = 0; k < hi - lo; ++k) {
-        const int token = a.reverse ? hi - 1 - k : lo + k;
-        const long long at = (long long)token * a.width + c;
-        if (a.carry) {
-            const int s = a.reverse ? a.t - 1 - token : token;
-            if (s % kRun == 0) a.carry[(long long)(s / kRun) * a.width + c] = h;
+// Steps: step s of the scan over all tokens is token s, or t - 1 - s in
+// reverse. `Doc` is the range of steps [begin, end) of the document (or of the
+// tokens of no document: doc < 0) that holds a step.
+struct Doc {
+    int begin, end, doc;
+};
+
+// Walks the documents of a chunk: lane i holds boundary base + i, so going to
+// the next document reads no memory. Every lane of the wavefront calls at().
+struct Walk {
+    int range = -1, base = 0, bound = 0;
+
+    __device__ __forceinline__ Doc of(const ScanArgs& a, int next, int r) {
+        if (range < 0 || r < base || r + 1 >= base + kWave) {
+            base = next > 0 ? r : r + 2 - kWave;
+            bound = tok_boundary(a.offsets, a.docs, a.t, base + (int)__lane_id());
         }
-        if (doc) {
-            float g, keep;
-            gates((float)((const T*)a.gate)[at], g, keep);
-            h = __builtin_fmaf(g, h, keep * (float)((const T*)a.x)[at]);
-        }
-        ((T*)a.y)[at] = (T)h;
+        const int lo = __builtin_amdgcn_readlane(bound, r - base);
+        const int hi = max(lo, __builtin_amdgcn_readlane(bound, r - base + 1));
+        Doc d;
+        d.begin = a.reverse ? a.t - hi : lo;
+        d.end = a.reverse ? a.t - lo : hi;
+        d.doc = r >= 1 && r <= a.docs ? r - 1 : -1;
+        return d;
     }
-    if (doc && a.last) a.last[(long long)(range - 1) * a.width + c] = h;
+    // The document of a step; next: where the following one lies (+1 or -1).
+    __device__ __forceinline__ Doc at(const ScanArgs& a, int step, int next) {
+        if (range >= 0) {
+            // the neighbours first: empty documents are passed over
+            for (int r = range + next; r >= 0 && r <= a.docs + 1 && r >= range - 64 && r <= range + 64;
+                 r += next) {
+                const Doc d = of(a, next, r);
+                if (d.begin <= step && step < d.end) {
+                    range = r;
+                    return d;
+                }
+            }
+        }
+        const int r = tok_range(a.offsets, a.docs, a.t, a.reverse ? a.t - 1 - step : step);
+        Doc d = of(a, next, r);
+        range = r;
+        // only offsets that decrease end here: one step at a time
+        if (step < d.begin || step >= d.end) d.begin = step, d.end = step + 1, d.doc = -1;
+        return d;
+    }
+};
+
+template <int V>
+__device__ __forceinline__ void state_of(const float* state, const Doc& d, int width, int c,
+                                         float (&h)[V]) {
+    if (d.doc >= 0 && state) {
+        Pack<float, V>::load(state + (long long)d.doc * width + c, h);
+    } else {
+#pragma unroll
+        for (int j = 0; j < V; ++j) h[j] = 0.0f;
+    }
 }
 
-// The same backward, run by run from the document's end: the states inside a
-// run are computed again from the state before it.
-template <typename T>
-__global__ __launch_bounds__(256) void k_scan_doc_grad(ScanArgs a) {
-    const int c = blockIdx.y * blockDim.x + threadIdx.x;
-    const int range = blockIdx.x;
-    if (c >= a.width) return;
-    const int lo = tok_boundary(a.offsets, a.docs, a.t, range);
-    const int hi = max(lo, tok_boundary(a.offsets, a.docs, a.t, range + 1));
-    const bool doc = range >= 1 && range <= a.docs;
-    if (!doc) {
-        for (int token = lo; token < hi; ++token) {
-            const long long at = (long long)token * a.width + c;
-            ((T*)a.ggate)[at] = (T)0.0f;
-            ((T*)a.gx)[at] = (T)0.0f;
+// Elements of V channels of one step.
+template <typename T, int V>
+struct Steps {
+    const T* base;      // step 0, this thread's channels
+    long long stride;   // to the next step
+    __device__ __forceinline__ Steps(const ScanArgs& a, const void* p, int c)
+        : base((const T*)p + (a.reverse ? (long long)(a.t - 1) * a.width : 0) + c),
+          stride(a.reverse ? -(long long)a.width : a.width) {}
+    __device__ __forceinline__ const T* at(int s) const { return base + s * stride; }
+};
+
+// What a chunk of steps does to the state that enters it: h -> mul h + add.
+// A document that starts in the chunk forgets what came before (mul = 0).
+template <typename T, int V>
+__global__ __launch_bounds__(256) void k_scan_sum(ScanArgs a) {
+    constexpr int kBatch = 8;
+    const int c = (blockIdx.y * blockDim.x + threadIdx.x) * V;
+    const int begin = blockIdx.x * a.chunk, end = min(a.t, begin + a.chunk);
+    const bool on = c < a.width;
+    const Steps<T, V> gate(a, a.gate, on ? c : 0), x(a, a.x, on ? c : 0);
+    float mul[V], add[V];
+#pragma unroll
+    for (int j = 0; j < V; ++j) mul[j] = 1.0f, add[j] = 0.0f;
+    Walk walk;
+    for (int s = begin; s < end;) {
+        const Doc d = walk.at(a, s, a.reverse ? -1 : 1);
+        if (s == d.begin) {
+            state_of<V>(a.state, d, a.width, on ? c : 0, add);
+#pragma unroll
+            for (int j = 0; j < V; ++j) mul[j] = 0.0f;
         }
+        const int e = min(d.end, end);
+        if (d.doc < 0) {
+            s = e;
+            continue;
+        }
+        for (; s < e; s += kBatch) {
+            const int m = min(kBatch, e - s);
+            float g[kBatch][V], y[kBatch][V];
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k) Pack<T, V>::load(gate.at(s + min(k, m - 1)), g[k]);
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k) Pack<T, V>::load(x.at(s + min(k, m - 1)), y[k]);
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k) {
+                const bool in = k < m;
+#pragma unroll
+                for (int j = 0; j < V; ++j) {
+                    float f, keep;
+                    gates(g[k][j], f, keep);
+                    add[j] = in ? __builtin_fmaf(f, add[j], keep * y[k][j]) : add[j];
+                    mul[j] = in ? mul[j] * f : mul[j];
+                }
+            }
+        }
+        s = e;
+    }
+    if (on) {
+        const long long at = (long long)blockIdx.x * a.width + c;
+        Pack<float, V>::store(a.mul + at, mul);
+        Pack<float, V>::store(a.add + at, add);
+    }
+}
+
+// The same for the gradient, which runs from the last step to the first:
+// back -> mul back + add, with d = back + grad_y and back = a d at each step.
+template <typename T, int V>
+__global__ __launch_bounds__(256) void k_scan_sum_grad(ScanArgs a) {
+    constexpr int kBatch = 8;
+    const int c = (blockIdx.y * blockDim.x + threadIdx.x) * V;
+    const int begin = blockIdx.x * a.chunk, end = min(a.t, begin + a.chunk);
+    const bool on = c < a.width;
+    const Steps<T, V> gate(a, a.gate, on ? c : 0), grad(a, a.gy, on ? c : 0);
+    float mul[V], add[V];
+#pragma unroll
+    for (int j = 0; j < V; ++j) mul[j] = 1.0f, add[j] = 0.0f;
+    Walk walk;
+    for (int s = end; s > begin;) {
+        const Doc d = walk.at(a, s - 1, a.reverse ? 1 : -1);
+        if (s == d.end) {
+            state_of<V>(a.grad_last, d, a.width, on ? c : 0, add);
+#pragma unroll
+            for (int j = 0; j < V; ++j) mul[j] = 0.0f;
+        }
+        const int b = max(d.begin, begin);
+        if (d.doc < 0) {
+            s = b;
+            continue;
+        }
+        for (; s > b; s -= kBatch) {
+            const int m = min(kBatch, s - b);
+            float g[kBatch][V], y[kBatch][V];
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k) Pack<T, V>::load(gate.at(s - 1 - min(k, m - 1)), g[k]);
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k) Pack<T, V>::load(grad.at(s - 1 - min(k, m - 1)), y[k]);
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k) {
+                const bool in = k < m;
+#pragma unroll
+                for (int j = 0; j < V; ++j) {
+                    float f, keep;
+                    gates(g[k][j], f, keep);
+                    add[j] = in ? (add[j] + y[k][j]) * f : add[j];
+                    mul[j] = in ? mul[j] * f : mul[j];
+                }
+            }
+        }
+        s = b;
+    }
+    if (on) {
+        const long long at = (long long)blockIdx.x * a.width + c;
+        Pack<float, V>::store(a.mul + at, mul);
+        Pack<float, V>::store(a.add + at, add);
+    }
+}
+
+// The state that enters each chunk, over the chunks' (mul, add), in place of
+// add: 16 channels of a block, 64 threads along the chunks, each first over
+// its own share, then one after another over the shares, then over its own
+// again. grad: from the last chunk to the first.
+template <bool GRAD>
+__global__ __launch_bounds__(1024) void k_scan_join(ScanArgs a) {
+    constexpr int kBatch = 8;
+    __shared__ float muls[64][16], adds[64][16];
+    const int lane = threadIdx.x & 15, part = threadIdx.x >> 4;
+    const int c = blockIdx.x * 16 + lane;
+    const bool on = c < a.width;
+    const int per = (a.chunks + 63) / 64;
+    const int k0 = min(a.chunks, part * per), k1 = min(a.chunks, k0 + per);
+    auto at = [&](int k) {
+        return (long long)(GRAD ? a.chunks - 1 - k : k) * a.width + (on ? c : 0);
+    };
+    float mul = 1.0f, add = 0.0f;
+    for (int k = k0; k < k1; k += kBatch) {
+        float u[kBatch], v[kBatch];
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) {
+            u[j] = a.mul[at(min(k + j, k1 - 1))];
+            v[j] = a.add[at(min(k + j, k1 - 1))];
+        }
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) {
+            if (k + j >= k1) break;
+            add = __builtin_fmaf(u[j], add, v[j]);
+            mul *= u[j];
+        }
+    }
+    muls[part][lane] = mul;
+    adds[part][lane] = add;
+    __syncthreads();
+    float h = 0.0f;  // nothing enters the first chunk: it starts a range
+    for (int p = 0; p < part; ++p) h = __builtin_fmaf(muls[p][lane], h, adds[p][lane]);
+    for (int k = k0; k < k1; k += kBatch) {
+        float u[kBatch], v[kBatch];
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) {
+            u[j] = a.mul[at(min(k + j, k1 - 1))];
+            v[j] = a.add[at(min(k + j, k1 - 1))];
+        }
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) {
+            if (k + j >= k1) break;
+            if (on) a.add[at(k + j)] = h;
+            h = __builtin_fmaf(u[j], h, v[j]);
+        }
+    }
+}
+
+// Documents of no tokens pass their state through: kEmpty of them per block
+// past the chunks' own.
+constexpr int kEmpty = 64;
+
+template <int V>
+__device__ __forceinline__ void pass_empty(const ScanArgs& a, const float* from, float* to, int c) {
+    if (!to || c >= a.width) return;
+    const int first = ((int)blockIdx.x - a.chunks) * kEmpty;
+    for (int doc = first; doc < min(a.docs, first + kEmpty); ++doc) {
+        const int lo = tok_boundary(a.offsets, a.docs, a.t, doc + 1);
+        if (tok_boundary(a.offsets, a.docs, a.t, doc + 2) > lo) continue;
+        float h[V];
+        const Doc d = {0, 0, doc};
+        state_of<V>(from, d, a.width, c, h);
+        Pack<float, V>::store(to + (long long)doc * a.width + c, h);
+    }
+}
+
+// The recurrence over a chunk of steps, from the state that enters it.
+template <typename T, int V>
+__global__ __launch_bounds__(256) void k_scan_run(ScanArgs a) {
+    constexpr int kBatch = 8;
+    const int c = (blockIdx.y * blockDim.x + threadIdx.x) * V;
+    const int begin = blockIdx.x * a.chunk, end = min(a.t, begin + a.chunk);
+    if ((int)blockIdx.x >= a.chunks) {
+        pass_empty<V>(a, a.state, a.last, c);
         return;
     }
-    const long long own = (long long)(range - 1) * a.width + c;
-    const float h0 = a.state ? a.state[own] : 0.0f;
-    float back = a.grad_last ? a.grad_last[own] : 0.0f;
-    const int s0 = a.reverse ? a.t - hi : lo;      // the document's steps
-    const int s1 = a.reverse ? a.t - lo : hi;
-    for (int end = s1; end > s0;) {
-        const int run = (end - 1) / kRun;
-        const int begin = max(run * kRun, s0);
-        float h = begin == s0 ? h0 : a.carry[(long long)run * a.width + c];
-        float before[kRun];
+    const bool on = c < a.width;
+    const Steps<T, V> gate(a, a.gate, on ? c : 0), x(a, a.x, on ? c : 0), y(a, a.y, on ? c : 0);
+    float h[V];
+#pragma unroll
+    for (int j = 0; j < V; ++j) h[j] = 0.0f;
+    if (a.chunks > 1 && on) Pack<float, V>::load(a.add + (long long)blockIdx.x * a.width + c, h);
+    Walk walk;
+    Doc d = {0, 0, -1};
+    for (int s = begin; s < end;) {
+        if (s == begin || s == d.end) {
+            d = walk.at(a, s, a.reverse ? -1 : 1);
+            if (s == d.begin) state_of<V>(a.state, d, a.width, on ? c : 0, h);
+        }
+        if (a.carry && s % kRun == 0 && on)
+            Pack<float, V>::store(a.carry + (long long)(s / kRun) * a.width + c, h);
+        const int e = min(min(d.end, end), (s / kRun + 1) * kRun);
+        if (d.doc < 0) {
+            float zero[V];
+#pragma unroll
+            for (int j = 0; j < V; ++j) zero[j] = 0.0f;
+            for (; s < e; ++s)
+                if (on) Pack<T, V>::store((T*)y.at(s), zero);
+            continue;
+        }
+        for (; s < e; s += kBatch) {
+            const int m = min(kBatch, e - s);
+            float g[kBatch][V], z[kBatch][V];
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k) Pack<T, V>::load(gate.at(s + min(k, m - 1)), g[k]);
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k) Pack<T, V>::load(x.at(s + min(k, m - 1)), z[k]);
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k) {
+                const bool in = k < m;
+#pragma unroll
+                for (int j = 0; j < V; ++j) {
+                    float f, keep;
+                    gates(g[k][j], f, keep);
+                    h[j] = in ? __builtin_fmaf(f, h[j], keep * z[k][j]) : h[j];
+                }
+                if (on && in) Pack<T, V>::store((T*)y.at(s + k), h);
+            }
+        }
+        s = e;
+        if (s == d.end && a.last && on)
+            Pack<float, V>::store(a.last + (long long)d.doc * a.width + c, h);
+    }
+}
+
+// The gradient over a chunk of steps, a run of kRun at a time from its last:
+// the states inside a run are computed again from the state before it.
+template <typename T, int V>
+__global__ __launch_bounds__(256) void k_scan_run_grad(ScanArgs a) {
+    const int c = (blockIdx.y * blockDim.x + threadIdx.x) * V;
+    const int begin = blockIdx.x * a.chunk, end = min(a.t, begin + a.chunk);
+    if ((int)blockIdx.x >= a.chunks) {
+        pass_empty<V>(a, a.grad_last, a.grad_state, c);
+        return;
+    }
+    const bool on = c < a.width;
+    const int cc = on ? c : 0;
+    const Steps<T, V> gate(a, a.gate, cc), x(a, a.x, cc), grad(a, a.gy, cc);
+    const Steps<T, V> ggate(a, a.ggate, cc), gx(a, a.gx, cc);
+    float back[V];
+#pragma unroll
+    for (int j = 0; j < V; ++j) back[j] = 0.0f;
+    if (a.chunks > 1 && on) Pack<float, V>::load(a.add + (long long)blockIdx.x * a.width + c, back);
+    Walk walk;
+    Doc d = {0, 0, -1};
+    for (int s = end; s > begin;) {
+        if (s == end || s == d.begin) {
+            d = walk.at(a, s - 1, a.reverse ? 1 : -1);
+            if (s == d.end) state_of<V>(a.grad_last, d, a.width, cc, back);
+        }
+        const int b = max(max(d.begin, begin), (s - 1) / kRun * kRun);
+        if (d.doc < 0) {
+            float zero[V];
+#pragma unroll
+            for (int j = 0; j < V; ++j) zero[j] = 0.0f;
+            for (; s > b; --s)
+                if (on) {
+                    Pack<T, V>::store((T*)ggate.at(s - 1), zero);
+                    Pack<T, V>::store((T*)gx.at(s - 1), zero);
+                }
+            continue;
+        }
+        const int m = s - b;
+        typename Pack<T, V>::vec g[kRun], z[kRun], w[kRun];
+#pragma unroll
+        for (int k = 0; k < kRun; ++k) g[k] = Pack<T, V>::raw(gate.at(b + min(k, m - 1)));
+#pragma unroll
+        for (int k = 0; k < kRun; ++k) z[k] = Pack<T, V>::raw(x.at(b + min(k, m - 1)));
+#pragma unroll
+        for (int k = 0; k < kRun; ++k) w[k] = Pack<T, V>::raw(grad.at(b + min(k, m - 1)));
+        float h[V], before[kRun][V];
+        if (b == d.begin)
+            state_of<V>(a.state, d, a.width, cc, h);
+        else
+            Pack<float, V>::load(a.carry + (long long)(b / kRun) * a.width + cc, h);
 #pragma unroll
         for (int k = 0; k < kRun; ++k) {
-            before[k] = h;
-            const int s = begin + k;
-            if (s < end) {
-                const int token = a.reverse ? a.t - 1 - s : s;
-                const long long at = (long long)token * a.width + c;
-                float g, keep;
-                gates((float)((const T*)a.gate)[at], g, keep);
-                h = __builtin_fmaf(g, h, keep * (float)((const T*)a.x)[at]);
+            float f[V], y[V];
+            Pack<T, V>::wide(g[k], f);
+            Pack<T, V>::wide(z[k], y);
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                before[k][j] = h[j];
+                float fa, keep;
+                gates(f[j], fa, keep);
+                h[j] = __builtin_fmaf(fa, h[j], keep * y[j]);
             }
         }
 #pragma unroll
         for (int k = kRun - 1; k >= 0; --k) {
-            const int s = begin + k;
-            if (s < end) {
-                const int token = a.reverse ? a.t - 1 - s : s;
-                const long long at = (long long)token * a.width + c;
-                float g, keep;
-                gates((float)((const T*)a.gate)[at], g, keep);
-                const float d = back + (float)((const T*)a.gy)[at];
-                ((T*)a.ggate)[at] = (T)(d * (before[k] - (float)((const T*)a.x)[at]) * (g * keep));
-                ((T*)a.gx)[at] = (T)(d * keep);
-                back = d * g;
+            if (k >= m) continue;
+            float f[V], y[V], q[V], p[V], r[V];
+            Pack<T, V>::wide(g[k], f);
+            Pack<T, V>::wide(z[k], y);
+            Pack<T, V>::wide(w[k], q);
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                float fa, keep;
+                // computed again, not kept for the whole run since the sweep above
+                asm("" : "+v"(f[j]));
+                gates(f[j], fa, keep);
+                const float dh = back[j] + q[j];
+                p[j] = dh * (before[k][j] - y[j]) * (fa * keep);
+                r[j] = dh * keep;
+                back[j] = dh * fa;
+            }
+            if (on) {
+                Pack<T, V>::store((T*)ggate.at(b + k), p);
+                Pack<T, V>::store((T*)gx.at(b + k), r);
             }
         }
-        end = begin;
+        s = b;
+        if (s == d.begin && a.grad_state && on)
+            Pack<float, V>::store(a.grad_state + (long long)d.doc * a.width + c, back);
     }
-    if (a.grad_state) a.grad_state[own] = back;
+}
+
+// Forward, where documents are short: one block row per range, one thread per
+// channel, along the document.
+template <typename T, int V>
+__global__ __launch_bounds__(256) void k_scan_doc(ScanArgs a) {
+    constexpr int kBatch = 4;
+    const int c = (blockIdx.y * blockDim.x + threadIdx.x) * V;
+    if (c >= a.width) return;
+    const int range = blockIdx.x;
+    const int lo = tok_boundary(a.offsets, a.docs, a.t, range);
+    const int hi = max(lo, tok_boundary(a.offsets, a.docs, a.t, range + 1));
+    const Doc d = {a.reverse ? a.t - hi : lo, a.reverse ? a.t - lo : hi,
+                   range >= 1 && range <= a.docs ? range - 1 : -1};
+    const Steps<T, V> gate(a, a.gate, c), x(a, a.x, c), y(a, a.y, c);
+    float h[V];
+    state_of<V>(a.state, d, a.width, c, h);
+    for (int s = d.begin; s < d.end; s += kBatch) {
+        const int m = min(kBatch, d.end - s);
+        float g[kBatch][V], z[kBatch][V];
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) Pack<T, V>::load(gate.at(s + min(k, m - 1)), g[k]);
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) Pack<T, V>::load(x.at(s + min(k, m - 1)), z[k]);
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+            if (k >= m) break;
+            if (a.carry && (s + k) % kRun == 0)
+                Pack<float, V>::store(a.carry + (long long)((s + k) / kRun) * a.width + c, h);
+            if (d.doc >= 0) {
+#pragma unroll
+                for (int j = 0; j < V; ++j) {
+                    float f, keep;
+                    gates(g[k][j], f, keep);
+                    h[j] = __builtin_fmaf(f, h[j], keep * z[k][j]);
+                }
+            }
+            Pack<T, V>::store((T*)y.at(s + k), h);
+        }
+    }
+    if (d.doc >= 0 && a.last) Pack<float, V>::store(a.last + (long long)d.doc * a.width + c, h);
 }
 
 bool check(int dtype, long long t, long long width, const int32_t* offsets, int32_t docs,
@@ -134,22 +487,76 @@ bool check(int dtype, long long t, long long width, const int32_t* offsets, int3
            (reverse == 0 || reverse == 1);
 }
 
-template <typename T>
-int run(const ScanArgs& a, bool grad, hipStream_t stream) {
-    const dim3 block(a.width >= 256 ? 256 : (a.width + 63) / 64 * 64);
-    const dim3 grid((unsigned)(a.docs + 2), (unsigned)((a.width + block.x - 1) / block.x));
-    if (grad)
-        k_scan_doc_grad<T><<<grid, block, 0, stream>>>(a);
-    else
-        k_scan_doc<T><<<grid, block, 0, stream>>>(a);
+// Steps per chunk. Short chunks fill the card (a wavefront walks a chunk of
+// 64 lanes of channels), long ones keep the chunks' sums few.
+int chunk_of(long long t) {
+    int chunk = 32;
+    while (chunk < 1024 && (t + chunk - 1) / chunk > 4096) chunk *= 2;
+    return chunk;
+}
+
+template <typename T, int V, bool GRAD>
+int run(ScanArgs a, hipStream_t stream) {
+    const int lanes = (a.width / V + kWave - 1) / kWave * kWave;
+    const dim3 block(lanes < 256 ? lanes : 256);
+    const unsigned slabs = (unsigned)((a.width / V + block.x - 1) / block.x);
+    // Documents of a few tokens (a decoding step): one launch over documents.
+    if (!GRAD && a.t <= 4096 && a.t <= 8ll * a.docs) {
+        k_scan_doc<T, V><<<dim3(a.docs + 2, slabs), block, 0, stream>>>(a);
+    } else {
+        if (a.chunks > 1) {
+            const dim3 grid((unsigned)a.chunks, slabs), join((unsigned)((a.width + 15) / 16));
+            if constexpr (GRAD) {
+                k_scan_sum_grad<T, V><<<grid, block, 0, stream>>>(a);
+                k_scan_join<true><<<join, dim3(1024), 0, stream>>>(a);
+            } else {
+                k_scan_sum<T, V><<<grid, block, 0, stream>>>(a);
+                k_scan_join<false><<<join, dim3(1024), 0, stream>>>(a);
+            }
+        }
+        const dim3 grid((unsigned)(a.chunks + (a.docs + kEmpty - 1) / kEmpty), slabs);
+        if constexpr (GRAD)
+            k_scan_run_grad<T, V><<<grid, block, 0, stream>>>(a);
+        else
+            k_scan_run<T, V><<<grid, block, 0, stream>>>(a);
+    }
     const hipError_t e = hipGetLastError();
     return e == hipSuccess ? VOX_OK : ssh_hip_fail(e);
 }
 
-int dispatch(int dtype, const ScanArgs& a, bool grad, hipStream_t stream) {
-    if (dtype == TOK_F32) return run<float>(a, grad, stream);
-    if (dtype == TOK_BF16) return run<bf16_t>(a, grad, stream);
-    return run<f16_t>(a, grad, stream);
+// Channels per thread: as many as leave a wavefront's lanes in use, with
+// pieces of at most 8 bytes that every array is aligned for. `most` bounds
+// the registers.
+template <typename T>
+int dispatch_type(const ScanArgs& a, bool grad, hipStream_t stream) {
+    const void* elems[] = {a.gate, a.x, a.gy, a.y, a.ggate, a.gx};
+    const void* floats[] = {a.state, a.last, a.carry, a.grad_last, a.grad_state};
+    int v = sizeof(T) == 4 || grad ? 2 : 4;
+    auto fits = [&](int n) {
+        if (a.width % n || (n > 1 && a.width / n < kWave)) return false;
+        for (const void* p : elems)
+            if ((size_t)p % (n * sizeof(T))) return false;
+        for (const void* p : floats)
+            if ((size_t)p % (n * 4)) return false;
+        return true;
+    };
+    while (v > 1 && !fits(v)) v /= 2;
+    if (grad) return v == 2 ? run<T, 2, true>(a, stream) : run<T, 1, true>(a, stream);
+    if constexpr (sizeof(T) == 2)
+        if (v == 4) return run<T, 4, false>(a, stream);
+    return v == 2 ? run<T, 2, false>(a, stream) : run<T, 1, false>(a, stream);
+}
+
+int dispatch(int dtype, ScanArgs& a, bool grad, void* workspace, hipStream_t stream) {
+    a.chunk = chunk_of(a.t);
+    a.chunks = (int)((a.t + (long long)a.chunk - 1) / a.chunk);
+    a.mul = (float*)workspace;
+    a.add = a.mul + (long long)a.chunks * a.width;
+    // sum and add are written in pieces too
+    if (((size_t)a.add & 15) != 0) a.add += 4 - (((size_t)a.add & 15) >> 2);
+    if (dtype == TOK_F32) return dispatch_type<float>(a, grad, stream);
+    if (dtype == TOK_BF16) return dispatch_type<bf16_t>(a, grad, stream);
+    return dispatch_type<f16_t>(a, grad, stream);
 }
 
 }  // namespace
@@ -162,7 +569,8 @@ int64_t tok_scan_runs(int64_t t) {
 
 int64_t tok_scan_workspace_bytes(int64_t t, int64_t width) {
     if (t < 0 || t > kMaxTokens || width < 1 || width > kMaxWidth) return VOX_EINVAL;
-    return 256;
+    const long long chunk = chunk_of(t), chunks = (t + chunk - 1) / chunk;
+    return chunks <= 1 ? 256 : (chunks * width * 8 + 16 + 255) / 256 * 256;
 }
 
 int tok_scan(const void* gate, const void* x, int32_t dtype, int64_t t, int64_t width,
@@ -178,7 +586,7 @@ int tok_scan(const void* gate, const void* x, int32_t dtype, int64_t t, int64_t 
     a.gate = gate, a.x = x, a.offsets = offsets, a.state = state, a.y = y, a.last = last_state;
     a.carry = carry;
     a.t = (int)t, a.width = (int)width, a.docs = docs, a.reverse = reverse;
-    return dispatch(dtype, a, false, stream);
+    return dispatch(dtype, a, false, workspace, stream);
 }
 
 int tok_scan_grad(const void* grad_y, const void* gate, const void* x, const float* carry,
@@ -196,7 +604,7 @@ int tok_scan_grad(const void* grad_y, const void* gate, const void* x, const flo
     a.carry = const_cast<float*>(carry);
     a.grad_last = grad_last, a.ggate = grad_gate, a.gx = grad_x, a.grad_state = grad_state;
     a.t = (int)t, a.width = (int)width, a.docs = docs, a.reverse = reverse;
-    return dispatch(dtype, a, true, stream);
+    return dispatch(dtype, a, true, workspace, stream);
 }
 
 }  // extern "C"

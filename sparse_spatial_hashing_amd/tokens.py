@@ -24,7 +24,7 @@ import torch
 
 from . import VoxError, _check, library
 
-TOK_SCAN_RUN = 32           # tokens per saved state (``carry``) of the recurrence
+TOK_SCAN_RUN = 16           # tokens per saved state (``carry``) of the recurrence
 _DTYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
 _lib = library()
 
