@@ -50,6 +50,11 @@ typedef float acc16 __attribute__((ext_vector_type(16)));
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kLowest = -3.402823466e+38f;
+// The backward's weights are computed 2^kLift too large and the sums put right
+// at the end: bf16 has the range, and weights that exp2 would flush to zero
+// keep their gradient. fp16's largest weights times a gradient would overflow.
+constexpr float kLift = ATT_F16 ? 0.0f : 24.0f;
+constexpr float kUnlift = ATT_F16 ? 1.0f : 0x1p-24f;
 constexpr float kRescale = 8.0f;  // running maximum may lag by this much (base 2)
 
 __device__ __forceinline__ acc16 mma(vec8 a, vec8 b, acc16 c) {
@@ -456,7 +461,8 @@ __global__ __launch_bounds__(64 * NW, NW == 4 ? 2 : 1) void k_att_forward(AttArg
         }
         return;
     }
-    const float inv = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);  // NaN stays
+    const float inv = 1.0f / l;
+    const bool none = l == 0.0f;  // sees no key: zeros, whatever the tiles held
     elem* out = (elem*)a.out + at * a.width;
 #pragma unroll
     for (int b = 0; b < kBlocks; ++b)
@@ -466,7 +472,7 @@ __global__ __launch_bounds__(64 * NW, NW == 4 ? 2 : 1) void k_att_forward(AttArg
             if (c >= a.width) continue;
             vec4 x;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) x[j] = (elem)(o[b][4 * q + j] * inv);
+            for (int j = 0; j < 4; ++j) x[j] = none ? (elem)0.0f : (elem)(o[b][4 * q + j] * inv);
             *(vec4*)(out + c) = x;
         }
     if (a.lse && half == 0)
@@ -492,12 +498,13 @@ __global__ __launch_bounds__(256) void k_att_join(AttArgs a) {
             y = __builtin_fmaf(w, p.y, y);
         }
     }
-    const float inv = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);
+    const float inv = 1.0f / l;
+    const bool none = l == 0.0f;
     typedef elem vec2 __attribute__((ext_vector_type(2)));
     if (2 * lane < a.width) {
         vec2 r;
-        r[0] = (elem)(x * inv);
-        r[1] = (elem)(y * inv);
+        r[0] = none ? (elem)0.0f : (elem)(x * inv);
+        r[1] = none ? (elem)0.0f : (elem)(y * inv);
         *(vec2*)((elem*)a.out + at * a.width + 2 * lane) = r;
     }
     if (a.lse && lane == 0)
@@ -507,7 +514,12 @@ __global__ __launch_bounds__(256) void k_att_join(AttArgs a) {
 // ---- grad_q ----------------------------------------------------------------
 // With P = exp2(score - lse), delta = sum(grad_out * out) and dP = grad_out V^T:
 // dS = P (dP - delta) (times 1 - tanh^2 under a cap), grad_q = scale dS K. The
-// same transposed products as the forward's, one more for dP.
+// same transposed products as the forward's, one more for dP, and one for P K:
+// out is rounded, so its delta is off by up to half a step of |grad_out|.|out|,
+// and where one key has nearly all the weight dP - delta is smaller than that.
+// The error is r = sum P (dP - delta), known at the end of the row; there
+// grad_q loses r P K, and grad_k and grad_v get the delta that is right in
+// 32 bits.
 
 template <bool GENERAL, int NW, int BN>
 __global__ __launch_bounds__(64 * NW, NW == 4 ? 2 : 1) void k_att_grad_q(AttArgs a) {
@@ -548,14 +560,14 @@ __global__ __launch_bounds__(64 * NW, NW == 4 ? 2 : 1) void k_att_grad_q(AttArgs
         for (int j = 0; j < 8; ++j) delta = __builtin_fmaf((float)gf[k][j], (float)of[j], delta);
     }
     delta += other_half(delta);
-    if (row.real && half == 0) a.delta[at] = delta;
-    const float lse2 = a.lse[at] * kLog2e;
+    const float lse2 = a.lse[at] * kLog2e - kLift;
 
-    acc16 o[kBlocks];
+    acc16 o[kBlocks], pk[kBlocks];
+    float rest = 0.0f;
 #pragma unroll
     for (int b = 0; b < kBlocks; ++b)
 #pragma unroll
-        for (int r = 0; r < 16; ++r) o[b][r] = 0.0f;
+        for (int r = 0; r < 16; ++r) o[b][r] = pk[b][r] = 0.0f;
 
     Stage<BN, NT> sk, sv;
     uint2 sp = make_uint2(0, 0);
@@ -595,29 +607,43 @@ __global__ __launch_bounds__(64 * NW, NW == 4 ? 2 : 1) void k_att_grad_q(AttArgs
             }
             scores<GENERAL, true>(a, s, bent, row, kpx + 32 * nb, kpy + 32 * nb, half);
 #pragma unroll
-            for (int r = 0; r < 16; ++r) s[r] = exp2_(s[r] - lse2) * (dp[r] - delta);
-            if (GENERAL && a.cap2 > 0.0f) {
-                // 1 - tanh^2 = 4 b (1 - b) with b = 1 / (e + 1)
-#pragma unroll
-                for (int r = 0; r < 16; ++r)
-                    s[r] *= 4.0f * bent[r] * (1.0f - bent[r]);
-            }
+            for (int r = 0; r < 16; ++r) s[r] = exp2_(s[r] - lse2);
             if (masked) {
                 const int left = row.limit - (t * BN + 32 * nb) - 4 * half;
 #pragma unroll
                 for (int r = 0; r < 16; ++r)
-                    if (8 * (r / 4) + r % 4 >= left) s[r] = 0.0f;
+                    if (8 * (r / 4) + r % 4 >= left) s[r] = dp[r] = 0.0f;
+            }
+#pragma unroll
+            for (int r = 0; r < 16; ++r) {
+                dp[r] = s[r] * (dp[r] - delta);
+                rest += dp[r];
+            }
+            if (GENERAL && a.cap2 > 0.0f) {
+                // 1 - tanh^2 = 4 b (1 - b) with b = 1 / (e + 1)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) {
+                    const float flat = 4.0f * bent[r] * (1.0f - bent[r]);
+                    dp[r] *= flat;
+                    s[r] *= flat;
+                }
             }
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
-                const vec8 p = round8(s, c);
+                const vec8 ds = round8(dp, c), p = round8(s, c);
 #pragma unroll
-                for (int b = 0; b < kBlocks; ++b)
-                    o[b] = mma(lds_transposed(tk, 32 * nb + 16 * c, b, lane), p, o[b]);
+                for (int b = 0; b < kBlocks; ++b) {
+                    const vec8 kt = lds_transposed(tk, 32 * nb + 16 * c, b, lane);
+                    o[b] = mma(kt, ds, o[b]);
+                    pk[b] = mma(kt, p, pk[b]);
+                }
             }
         }
     }
+    rest = (rest + other_half(rest)) * kUnlift;
     if (!row.real) return;
+    const bool none = a.lse[at] == -__builtin_inff();  // saw no key: no gradient
+    if (half == 0) a.delta[at] = delta + rest;
     elem* out = (elem*)a.gq + at * a.width;
 #pragma unroll
     for (int b = 0; b < kBlocks; ++b)
@@ -627,7 +653,8 @@ __global__ __launch_bounds__(64 * NW, NW == 4 ? 2 : 1) void k_att_grad_q(AttArgs
             if (c >= a.width) continue;
             vec4 x;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) x[j] = (elem)(o[b][4 * q + j] * a.scale);
+            for (int j = 0; j < 4; ++j) x[j] = none ? (elem)0.0f
+                            : (elem)(__builtin_fmaf(-rest, pk[b][4 * q + j], o[b][4 * q + j]) * (a.scale * kUnlift));
             *(vec4*)(out + c) = x;
         }
 }
@@ -703,7 +730,7 @@ __global__ __launch_bounds__(64 * NW, 1) void k_att_grad_kv(AttArgs a) {
         if (threadIdx.x < BM) {
             const Row w = get_row<GENERAL>(a, d, kvh, t * BM + threadIdx.x);
             const long long at = w.token * a.heads + w.head;
-            s_lse = a.lse[at] * kLog2e;
+            s_lse = a.lse[at] * kLog2e - kLift;
             s_delta = a.delta[at];
             s_slope = w.slope2;
             s_limit = w.limit;
@@ -819,8 +846,8 @@ __global__ __launch_bounds__(64 * NW, 1) void k_att_grad_kv(AttArgs a) {
             vec4 x, y;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                x[j] = (elem)(gk[b][4 * q + j] * a.scale);
-                y[j] = (elem)gv[b][4 * q + j];
+                x[j] = (elem)(gk[b][4 * q + j] * (a.scale * kUnlift));
+                y[j] = (elem)(gv[b][4 * q + j] * kUnlift);
             }
             *(vec4*)(outk + c) = x;
             *(vec4*)(outv + c) = y;

@@ -113,7 +113,17 @@ struct Steps {
 };
 
 // What a chunk of steps does to the state that enters it: h -> mul h + add.
-// A document that starts in the chunk forgets what came before (mul = 0).
+// A document that starts in the chunk forgets what came before: mul = -0, which
+// no product of gates gives and which stays under them, so that not even a NaN
+// passes.
+constexpr float kForget = -0.0f;
+
+__device__ __forceinline__ bool forgets(float mul) { return __float_as_uint(mul) == 0x80000000u; }
+
+__device__ __forceinline__ float enter(float mul, float add, float h) {
+    return forgets(mul) ? add : __builtin_fmaf(mul, h, add);
+}
+
 template <typename T, int V>
 __global__ __launch_bounds__(256) void k_scan_sum(ScanArgs a) {
     constexpr int kBatch = 8;
@@ -130,7 +140,7 @@ __global__ __launch_bounds__(256) void k_scan_sum(ScanArgs a) {
         if (s == d.begin) {
             state_of<V>(a.state, d, a.width, on ? c : 0, add);
 #pragma unroll
-            for (int j = 0; j < V; ++j) mul[j] = 0.0f;
+            for (int j = 0; j < V; ++j) mul[j] = kForget;
         }
         const int e = min(d.end, end);
         if (d.doc < 0) {
@@ -183,7 +193,7 @@ __global__ __launch_bounds__(256) void k_scan_sum_grad(ScanArgs a) {
         if (s == d.end) {
             state_of<V>(a.grad_last, d, a.width, on ? c : 0, add);
 #pragma unroll
-            for (int j = 0; j < V; ++j) mul[j] = 0.0f;
+            for (int j = 0; j < V; ++j) mul[j] = kForget;
         }
         const int b = max(d.begin, begin);
         if (d.doc < 0) {
@@ -245,15 +255,15 @@ __global__ __launch_bounds__(1024) void k_scan_join(ScanArgs a) {
 #pragma unroll
         for (int j = 0; j < kBatch; ++j) {
             if (k + j >= k1) break;
-            add = __builtin_fmaf(u[j], add, v[j]);
-            mul *= u[j];
+            add = enter(u[j], v[j], add);
+            mul = forgets(u[j]) ? u[j] : mul * u[j];
         }
     }
     muls[part][lane] = mul;
     adds[part][lane] = add;
     __syncthreads();
     float h = 0.0f;  // nothing enters the first chunk: it starts a range
-    for (int p = 0; p < part; ++p) h = __builtin_fmaf(muls[p][lane], h, adds[p][lane]);
+    for (int p = 0; p < part; ++p) h = enter(muls[p][lane], adds[p][lane], h);
     for (int k = k0; k < k1; k += kBatch) {
         float u[kBatch], v[kBatch];
 #pragma unroll
@@ -265,7 +275,7 @@ __global__ __launch_bounds__(1024) void k_scan_join(ScanArgs a) {
         for (int j = 0; j < kBatch; ++j) {
             if (k + j >= k1) break;
             if (on) a.add[at(k + j)] = h;
-            h = __builtin_fmaf(u[j], h, v[j]);
+            h = enter(u[j], v[j], h);
         }
     }
 }
@@ -579,6 +589,7 @@ int tok_scan(const void* gate, const void* x, int32_t dtype, int64_t t, int64_t 
              hipStream_t stream) {
     if (!check(dtype, t, width, offsets, docs, reverse)) return VOX_EINVAL;
     if (t && (!gate || !x || !y)) return VOX_EINVAL;
+    if (((size_t)gate | (size_t)x | (size_t)y) % tok_elem_bytes(dtype)) return VOX_EINVAL;
     if (!workspace || ((size_t)workspace & 255) ||
         workspace_bytes < tok_scan_workspace_bytes(t, width))
         return VOX_EWORKSPACE;
@@ -596,6 +607,9 @@ int tok_scan_grad(const void* grad_y, const void* gate, const void* x, const flo
                   hipStream_t stream) {
     if (!check(dtype, t, width, offsets, docs, reverse)) return VOX_EINVAL;
     if (t && (!grad_y || !gate || !x || !carry || !grad_gate || !grad_x)) return VOX_EINVAL;
+    if (((size_t)grad_y | (size_t)gate | (size_t)x | (size_t)grad_gate | (size_t)grad_x) %
+        tok_elem_bytes(dtype))
+        return VOX_EINVAL;
     if (!workspace || ((size_t)workspace & 255) ||
         workspace_bytes < tok_scan_workspace_bytes(t, width))
         return VOX_EWORKSPACE;
