@@ -4,10 +4,14 @@
 //
 // The gradient sorts (row, token) pairs by row with stable passes from the
 // lowest digit up, so the tokens of a row come out in token order, and sums
-// equal rows over runs of kRun sorted pairs, one wavefront per run:
+// equal rows over runs of sorted pairs, a group of lanes per run:
+//   k_eg_small    up to kSmall tokens: one block sorts in LDS while the others
+//                 clear the gradient; or
+//   k_eg_zero, and per digit
 //   k_eg_count    digits of each tile of pairs, counted
 //   k_eg_prefix   one block per digit: where each tile's entries of it start
 //   k_eg_scatter  pairs to their places (ranks by ballots, in input order)
+//   then
 //   k_eg_reduce   sums of rows that start and end in a run go out; a row cut
 //                 by a run's border leaves partial sums
 //   k_eg_join     partial sums of a cut row added in order
@@ -23,11 +27,13 @@ namespace {
 
 constexpr int kBlock = 256;
 constexpr int kWaves = kBlock / kWave;
-constexpr int kPer = 16;                   // pairs per thread of a sort tile
+constexpr int kPer = 8;                    // pairs per thread of a sort tile
 constexpr int kTile = kBlock * kPer;
 constexpr int kMaxBits = 9;                // bits of a digit, at most
 constexpr int kMaxDigits = 1 << kMaxBits;
-constexpr int kRun = 64;                   // sorted pairs per wavefront of the reduction
+constexpr int kSmall = 16384;              // tokens that one block sorts
+constexpr int kSmallBlock = 1024;
+constexpr int kBatch = 8;                  // rows in flight per group of lanes
 constexpr long long kMaxN = 1ll << 27;
 constexpr long long kMaxRows = 1ll << 24;
 constexpr long long kMaxWidth = 65536;
@@ -69,24 +75,32 @@ __device__ __forceinline__ unsigned key_of(const Id* ids, long long i, long long
 }
 
 template <typename Id, bool FIRST>
+__device__ __forceinline__ uint2 pair_of(const Id* ids, const uint2* pairs, long long i,
+                                         long long rows) {
+    if (FIRST) return make_uint2(key_of(ids, i, rows), (unsigned)i);
+    return pairs[i];
+}
+
+template <typename Id, bool FIRST>
 __global__ __launch_bounds__(kBlock) void k_eg_count(const Id* __restrict__ ids,
-                                                     const unsigned* __restrict__ keys,
-                                                     long long n, long long rows, int shift,
-                                                     int bits, int tiles,
+                                                     const uint2* __restrict__ pairs, long long n,
+                                                     long long rows, int shift, int bits, int tiles,
                                                      unsigned* __restrict__ counts) {
     __shared__ unsigned hist[kMaxDigits];
     const int digits = 1 << bits;
     for (int d = threadIdx.x; d < digits; d += kBlock) hist[d] = 0;
     __syncthreads();
     const long long base = (long long)blockIdx.x * kTile;
+    unsigned key[kPer];
 #pragma unroll
     for (int k = 0; k < kPer; ++k) {
         const long long i = base + k * kBlock + threadIdx.x;
-        if (i < n) {
-            const unsigned key = FIRST ? key_of(ids, i, rows) : keys[i];
-            atomicAdd(&hist[(key >> shift) & (digits - 1)], 1u);
-        }
+        key[k] = pair_of<Id, FIRST>(ids, pairs, i < n ? i : n - 1, rows).x;
     }
+#pragma unroll
+    for (int k = 0; k < kPer; ++k)
+        if (base + k * kBlock + threadIdx.x < n)
+            atomicAdd(&hist[(key[k] >> shift) & (digits - 1)], 1u);
     __syncthreads();
     for (int d = threadIdx.x; d < digits; d += kBlock)
         counts[(long long)d * tiles + blockIdx.x] = hist[d];
@@ -110,41 +124,45 @@ __global__ __launch_bounds__(kBlock) void k_eg_prefix(unsigned* __restrict__ cou
     if (threadIdx.x == 0) totals[blockIdx.x] = run;
 }
 
+// The tile is put in order in LDS first, so that the entries of a digit go out
+// together.
 template <typename Id, bool FIRST>
 __global__ __launch_bounds__(kBlock) void k_eg_scatter(
-    const Id* __restrict__ ids, const unsigned* __restrict__ keys,
-    const unsigned* __restrict__ tokens, long long n, long long rows, int shift, int bits,
-    int tiles, const unsigned* __restrict__ counts, const unsigned* __restrict__ totals,
-    unsigned* __restrict__ out_keys, unsigned* __restrict__ out_tokens) {
+    const Id* __restrict__ ids, const uint2* __restrict__ pairs, long long n, long long rows,
+    int shift, int bits, int tiles, const unsigned* __restrict__ counts,
+    const unsigned* __restrict__ totals, uint2* __restrict__ out) {
     __shared__ unsigned wsum[kWsumWords];
-    __shared__ unsigned base[kMaxDigits];
+    __shared__ unsigned base[kMaxDigits];       // place of a digit's entries less their place here
     __shared__ unsigned seen[kWaves][kMaxDigits];
+    __shared__ uint2 local[kTile];
     const int digits = 1 << bits;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    for (int d = threadIdx.x; d < kWaves * kMaxDigits; d += kBlock) (&seen[0][0])[d] = 0;
-    // where this tile's entries of each digit start
-    static_assert(kMaxDigits <= 2 * kBlock, "two digits per thread");
-    {
-        const int d = 2 * threadIdx.x;
-        const unsigned u = d < digits ? totals[d] : 0u, v = d + 1 < digits ? totals[d + 1] : 0u;
-        unsigned total;
-        const unsigned ex = block_excl_scan<kWaves>(u + v, wsum, &total);
-        if (d < digits) base[d] = ex + counts[(long long)d * tiles + blockIdx.x];
-        if (d + 1 < digits) base[d + 1] = ex + u + counts[(long long)(d + 1) * tiles + blockIdx.x];
-    }
-    __syncthreads();
     // wavefront w ranks its kPer * 64 consecutive pairs in order
     const long long first = (long long)blockIdx.x * kTile + wave * (kPer * kWave);
-    unsigned key[kPer], rank[kPer];
+    uint2 pair[kPer];
+    unsigned rank[kPer];
 #pragma unroll
     for (int k = 0; k < kPer; ++k) {
         const long long i = first + k * kWave + lane;
-        key[k] = i < n ? (FIRST ? key_of(ids, i, rows) : keys[i]) : 0u;
+        pair[k] = pair_of<Id, FIRST>(ids, pairs, i < n ? i : n - 1, rows);
     }
+    for (int d = threadIdx.x; d < kWaves * kMaxDigits; d += kBlock) (&seen[0][0])[d] = 0;
+    static_assert(kMaxDigits <= 2 * kBlock, "two digits per thread");
+    const int d0 = 2 * threadIdx.x;
+    {
+        // where this tile's entries of each digit go
+        const unsigned u = d0 < digits ? totals[d0] : 0u, v = d0 + 1 < digits ? totals[d0 + 1] : 0u;
+        unsigned total;
+        const unsigned ex = block_excl_scan<kWaves>(u + v, wsum, &total);
+        if (d0 < digits) base[d0] = ex + counts[(long long)d0 * tiles + blockIdx.x];
+        if (d0 + 1 < digits)
+            base[d0 + 1] = ex + u + counts[(long long)(d0 + 1) * tiles + blockIdx.x];
+    }
+    __syncthreads();
 #pragma unroll
     for (int k = 0; k < kPer; ++k) {
         const bool valid = first + k * kWave + lane < n;
-        const unsigned d = (key[k] >> shift) & (digits - 1);
+        const unsigned d = (pair[k].x >> shift) & (digits - 1);
         const unsigned long long m = match_mask(d, valid, bits);
         const unsigned before = valid ? seen[wave][d] : 0u;
         rank[k] = before + (unsigned)__popcll(m & lanes_below(lane));
@@ -154,153 +172,310 @@ __global__ __launch_bounds__(kBlock) void k_eg_scatter(
         asm volatile("" ::: "memory");
     }
     __syncthreads();
-    for (int d = threadIdx.x; d < digits; d += kBlock) {
-        unsigned s = base[d];
+    {
+        // where each wavefront's entries of a digit go in the tile
+        unsigned c[2][kWaves], sum[2] = {0u, 0u};
 #pragma unroll
-        for (int w = 0; w < kWaves; ++w) {
-            const unsigned c = seen[w][d];
-            seen[w][d] = s;
-            s += c;
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int w = 0; w < kWaves; ++w) {
+                c[j][w] = d0 + j < digits ? seen[w][d0 + j] : 0u;
+                sum[j] += c[j][w];
+            }
+        unsigned total;
+        unsigned at = block_excl_scan<kWaves>(sum[0] + sum[1], wsum, &total);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            if (d0 + j < digits) base[d0 + j] -= at;
+#pragma unroll
+            for (int w = 0; w < kWaves; ++w) {
+                if (d0 + j < digits) seen[w][d0 + j] = at;
+                at += c[j][w];
+            }
         }
     }
     __syncthreads();
 #pragma unroll
+    for (int k = 0; k < kPer; ++k)
+        if (first + k * kWave + lane < n)
+            local[seen[wave][(pair[k].x >> shift) & (digits - 1)] + rank[k]] = pair[k];
+    __syncthreads();
+    const int count = (int)(n - (long long)blockIdx.x * kTile < kTile
+                                ? n - (long long)blockIdx.x * kTile : (long long)kTile);
+#pragma unroll
     for (int k = 0; k < kPer; ++k) {
-        const long long i = first + k * kWave + lane;
-        if (i < n) {
-            const unsigned d = (key[k] >> shift) & (digits - 1);
-            const unsigned at = seen[wave][d] + rank[k];
-            out_keys[at] = key[k];
-            out_tokens[at] = FIRST ? (unsigned)i : tokens[i];
+        const int at = k * kBlock + threadIdx.x;
+        if (at < count) {
+            const uint2 p = local[at];
+            out[base[(p.x >> shift) & (digits - 1)] + at] = p;
         }
     }
 }
 
 // ------------------------------------------------------------------ reduce --
 
-__global__ __launch_bounds__(kBlock) void k_eg_zero(uint4* __restrict__ out, long long pieces,
-                                                    unsigned char* __restrict__ tail, int bytes) {
-    const long long step = (long long)gridDim.x * kBlock;
-    for (long long p = (long long)blockIdx.x * kBlock + threadIdx.x; p < pieces; p += step)
+__device__ __forceinline__ void clear(uint4* out, long long pieces, unsigned char* tail, int bytes,
+                                      long long block, long long blocks, int threads) {
+    const long long step = blocks * threads;
+    for (long long p = block * threads + threadIdx.x; p < pieces; p += step)
         out[p] = make_uint4(0, 0, 0, 0);
-    if (blockIdx.x == 0 && (int)threadIdx.x < bytes) tail[threadIdx.x] = 0;
+    if (block == 0 && (int)threadIdx.x < bytes) tail[threadIdx.x] = 0;
 }
 
-// One wavefront per run and slab of 64 * N columns: lane l holds columns
-// N l .. N l + N - 1 of the slab.
+__global__ __launch_bounds__(kBlock) void k_eg_zero(uint4* __restrict__ out, long long pieces,
+                                                    unsigned char* __restrict__ tail, int bytes) {
+    clear(out, pieces, tail, bytes, blockIdx.x, gridDim.x, kBlock);
+}
+
+// Block 0 sorts all n <= kSmall pairs, kept in registers and put in order
+// through LDS; the other blocks clear the gradient meanwhile.
+template <typename Id>
+__global__ __launch_bounds__(kSmallBlock) void k_eg_small(const Id* __restrict__ ids, int n,
+                                                          long long rows, int passes, int bits_all,
+                                                          uint2* __restrict__ out_pairs,
+                                                          uint4* __restrict__ out, long long pieces,
+                                                          unsigned char* __restrict__ tail,
+                                                          int bytes) {
+    constexpr int W = kSmallBlock / kWave, E = kSmall / kSmallBlock;
+    __shared__ uint2 local[kSmall];
+    __shared__ unsigned short seen[W][kMaxDigits];
+    __shared__ unsigned wsum[kWsumWords];
+    if (blockIdx.x > 0) {
+        clear(out, pieces, tail, bytes, blockIdx.x - 1, gridDim.x - 1, kSmallBlock);
+        return;
+    }
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int per = (n + kSmallBlock - 1) / kSmallBlock;  // <= E pairs per thread
+    const int first = wave * (per * kWave) + lane;
+    uint2 pair[E];
+    unsigned rank[E];
+#pragma unroll
+    for (int k = 0; k < E; ++k) {
+        pair[k] = make_uint2(0, 0);
+        if (k < per) {
+            const int i = first + k * kWave;
+            pair[k] = make_uint2(key_of(ids, i < n ? i : n - 1, rows), (unsigned)i);
+        }
+    }
+    int shift = 0;
+    for (int q = 0; q < passes; ++q) {
+        const int bits = (bits_all - shift + passes - q - 1) / (passes - q);
+        const int digits = 1 << bits;
+        for (int d = threadIdx.x; d < W * kMaxDigits / 2; d += kSmallBlock)
+            ((unsigned*)&seen[0][0])[d] = 0;
+        __syncthreads();
+#pragma unroll
+        for (int k = 0; k < E; ++k) {
+            if (k < per) {
+                const bool valid = first + k * kWave < n;
+                const unsigned d = (pair[k].x >> shift) & (digits - 1);
+                const unsigned long long m = match_mask(d, valid, bits);
+                const unsigned before = valid ? seen[wave][d] : 0u;
+                rank[k] = before + (unsigned)__popcll(m & lanes_below(lane));
+                if (valid && (m & lanes_above(lane)) == 0)
+                    seen[wave][d] = (unsigned short)(before + (unsigned)__popcll(m));
+                asm volatile("" ::: "memory");
+            }
+        }
+        __syncthreads();
+        {
+            static_assert(kMaxDigits <= kSmallBlock, "a digit per thread");
+            const int d = threadIdx.x;
+            unsigned c[W], sum = 0;
+#pragma unroll
+            for (int w = 0; w < W; ++w) {
+                c[w] = d < digits ? seen[w][d] : 0u;
+                sum += c[w];
+            }
+            unsigned total;
+            unsigned at = block_excl_scan<W>(sum, wsum, &total);
+#pragma unroll
+            for (int w = 0; w < W; ++w) {
+                if (d < digits) seen[w][d] = (unsigned short)at;  // < kSmall
+                at += c[w];
+            }
+        }
+        __syncthreads();
+        const bool last = q + 1 == passes;
+#pragma unroll
+        for (int k = 0; k < E; ++k) {
+            if (k < per && first + k * kWave < n) {
+                const unsigned at = seen[wave][(pair[k].x >> shift) & (digits - 1)] + rank[k];
+                if (last)
+                    out_pairs[at] = pair[k];
+                else
+                    local[at] = pair[k];
+            }
+        }
+        if (last) break;
+        __syncthreads();
+#pragma unroll
+        for (int k = 0; k < E; ++k) {
+            if (k < per && first + k * kWave < n) pair[k] = local[first + k * kWave];
+        }
+        shift += bits;
+        __syncthreads();
+    }
+}
+
+struct Sums {
+    const uint2* pairs;   // sorted
+    long long n;
+    unsigned rows;
+    int width, run;       // run: pairs per run, a multiple of kBatch
+    int lanes_log;        // lanes of a group
+    float scale;
+    float* head;          // [runs, width]: of a row that began in an earlier run
+    float* tail;          // [runs, width]: of a row that goes on in the next one
+};
+
+constexpr unsigned kNone = 0xffffffffu;
+
+// A group of lanes per run and slab of columns: lane l of the group holds
+// columns N l .. N l + N - 1.
 template <typename T, int N>
 __global__ __launch_bounds__(kBlock) void k_eg_reduce(const T* __restrict__ grad, long long stride,
-                                                      const unsigned* __restrict__ keys,
-                                                      const unsigned* __restrict__ tokens,
-                                                      long long n, unsigned rows, int width,
-                                                      float scale, T* __restrict__ out,
-                                                      float* __restrict__ head,
-                                                      float* __restrict__ tail) {
-    constexpr int kBatch = 8;
-    const int lane = threadIdx.x & 63;
-    const long long run = (long long)blockIdx.x * kWaves + (threadIdx.x >> 6);
-    const long long p0 = run * kRun;
-    if (p0 >= n) return;
-    const int count = (int)(n - p0 < kRun ? n - p0 : (long long)kRun);
-    const int col = (blockIdx.y * kWave + lane) * N;
-    const bool mine = col < width;
-    const unsigned my_key = lane < count ? keys[p0 + lane] : rows;
-    const unsigned my_token = lane < count ? tokens[p0 + lane] : 0u;
-    const unsigned prev = p0 > 0 ? keys[p0 - 1] : 0xffffffffu;
-    const unsigned next = p0 + kRun < n ? keys[p0 + kRun] : 0xffffffffu;
-
+                                                      Sums a, T* __restrict__ out) {
+    const int tid = blockIdx.x * kBlock + threadIdx.x;
+    const long long run = tid >> a.lanes_log;
+    const long long p0 = run * a.run;
+    if (p0 >= a.n) return;
+    const int count = (int)(a.n - p0 < a.run ? a.n - p0 : (long long)a.run);
+    const int col = ((blockIdx.y << a.lanes_log) + (tid & ((1 << a.lanes_log) - 1))) * N;
+    if (col >= a.width) return;
     float acc[N];
 #pragma unroll
     for (int j = 0; j < N; ++j) acc[j] = 0.0f;
-    bool cut = __builtin_amdgcn_readlane((int)my_key, 0) == (int)prev;  // began in an earlier run
-    for (int b = 0; b < kRun; b += kBatch) {
-        if (b >= count || __builtin_amdgcn_readlane((int)my_key, b) == (int)rows) break;
-        float x[kBatch][N];
+    bool cut = p0 > 0 && a.pairs[p0 - 1].x == a.pairs[p0].x;  // began in an earlier run
+    for (int b = 0; b < count; b += kBatch) {
+        uint2 pr[kBatch + 1];
 #pragma unroll
-        for (int k = 0; k < kBatch; ++k) {
-            const unsigned token = (unsigned)__builtin_amdgcn_readlane((int)my_token, b + k);
-#pragma unroll
-            for (int j = 0; j < N; ++j) x[k][j] = 0.0f;
-            if (mine) Pack<T, N>::load(grad + (long long)token * stride + col, x[k]);
+        for (int k = 0; k <= kBatch; ++k) {
+            const long long p = p0 + b + k;
+            pr[k] = p < a.n ? a.pairs[p] : make_uint2(kNone, 0);
         }
+        if (pr[0].x >= a.rows) break;  // no row, and so is what follows
+        typename Pack<T, N>::vec x[kBatch];
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k)
+            x[k] = Pack<T, N>::raw(grad + (long long)(pr[k].x < a.rows ? pr[k].y : pr[0].y) * stride + col);
 #pragma unroll
         for (int k = 0; k < kBatch; ++k) {
-            const int p = b + k;
-            const unsigned key = (unsigned)__builtin_amdgcn_readlane((int)my_key, p);
-            if (p >= count || key == rows) break;
+            const unsigned key = pr[k].x;
+            if (key < a.rows && b + k < count) {
+                float y[N];
+                Pack<T, N>::wide(x[k], y);
 #pragma unroll
-            for (int j = 0; j < N; ++j) acc[j] += x[k][j];
-            const unsigned after =
-                p + 1 < kRun ? (unsigned)__builtin_amdgcn_readlane((int)my_key, (p + 1) & 63) : next;
-            const bool open = p + 1 == kRun && after == key;
-            if (after != key || open) {
-                if (mine) {
+                for (int j = 0; j < N; ++j) acc[j] += y[j];
+                const bool open = b + k + 1 == a.run && pr[k + 1].x == key;
+                if (pr[k + 1].x != key || open) {
                     if (!cut && !open) {
-                        float y[N];
 #pragma unroll
-                        for (int j = 0; j < N; ++j) y[j] = acc[j] * scale;
-                        Pack<T, N>::store(out + (long long)key * width + col, y);
+                        for (int j = 0; j < N; ++j) y[j] = acc[j] * a.scale;
+                        Pack<T, N>::store(out + (long long)key * a.width + col, y);
                     } else {
-                        Pack<float, N>::store((cut ? head : tail) + run * width + col, acc);
+                        Pack<float, N>::store((cut ? a.head : a.tail) + run * a.width + col, acc);
                     }
-                }
-                cut = false;
+                    cut = false;
 #pragma unroll
-                for (int j = 0; j < N; ++j) acc[j] = 0.0f;
+                    for (int j = 0; j < N; ++j) acc[j] = 0.0f;
+                }
             }
         }
     }
 }
 
-// One wavefront per run whose last row goes on in the next one and began in it.
+// Sum of heads [r0, r1) in order.
+template <int N>
+__device__ __forceinline__ void add_heads(const Sums& a, long long r0, long long r1, int col,
+                                          float (&acc)[N]) {
+    for (long long r = r0; r < r1; r += kBatch) {
+        float x[kBatch][N];
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+            const long long q = r + k < r1 ? r + k : r1 - 1;
+            Pack<float, N>::load(a.head + q * a.width + col, x[k]);
+        }
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k)
+#pragma unroll
+            for (int j = 0; j < N; ++j) acc[j] += r + k < r1 ? x[k][j] : 0.0f;
+    }
+}
+
+// A group of lanes per run whose last row began in it and goes on in the next.
+// Rows of more than kLong runs are summed by all groups of the block, each a
+// share of the runs, and the shares in order.
 template <typename T, int N>
-__global__ __launch_bounds__(kBlock) void k_eg_join(const unsigned* __restrict__ keys, long long n,
-                                                    unsigned rows, int width, float scale,
-                                                    T* __restrict__ out,
-                                                    const float* __restrict__ head,
-                                                    const float* __restrict__ tail) {
-    const int lane = threadIdx.x & 63;
-    const long long run = (long long)blockIdx.x * kWaves + (threadIdx.x >> 6);
-    const long long p0 = run * kRun;
-    if (p0 + kRun >= n) return;
-    const unsigned key = keys[p0 + kRun];
-    if (key == rows || keys[p0 + kRun - 1] != key) return;
-    if (keys[p0] == key && p0 > 0 && keys[p0 - 1] == key) return;  // began earlier
-    const int col = (blockIdx.y * kWave + lane) * N;
-    const bool mine = col < width;
-    const long long runs = (n + kRun - 1) / kRun;
-    // runs [run + 1, end) hold more of the row
-    long long end = run + 2;
-    for (;;) {
-        const long long r = end + lane;
-        const unsigned long long same = __ballot(r < runs && keys[r * kRun] == key);
-        if (same == ~0ull) {
-            end += 64;
-            continue;
-        }
-        end += __ffsll((long long)~same) - 1;
-        break;
-    }
-    if (!mine) return;
-    float acc[N];
-    Pack<float, N>::load(tail + run * width + col, acc);
-    for (long long r = run + 1; r < end; r += 8) {
-        float x[8][N];
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            const long long q = r + k < end ? r + k : end - 1;
-            Pack<float, N>::load(head + q * width + col, x[k]);
-        }
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-            if (r + k < end) {
-#pragma unroll
-                for (int j = 0; j < N; ++j) acc[j] += x[k][j];
+__global__ __launch_bounds__(kBlock) void k_eg_join(Sums a, T* __restrict__ out) {
+    constexpr int kLong = 32;
+    __shared__ long long list[kBlock][2];
+    __shared__ int listed;
+    __shared__ float part[kBlock][N];
+    if (threadIdx.x == 0) listed = 0;
+    __syncthreads();
+    const int lanes = 1 << a.lanes_log, groups = kBlock >> a.lanes_log;
+    const int lane = threadIdx.x & (lanes - 1), group = threadIdx.x >> a.lanes_log;
+    const long long run = (long long)blockIdx.x * groups + group;
+    const long long runs = (a.n + a.run - 1) / a.run;
+    const long long p1 = (run + 1) * a.run;  // the next run's first pair
+    const int col = ((blockIdx.y << a.lanes_log) + lane) * N;
+    const bool on = col < a.width;
+    auto first_key = [&](long long r) { return r < runs ? a.pairs[r * a.run].x : kNone; };
+    if (p1 < a.n) {
+        const unsigned key = a.pairs[p1].x;
+        const long long p0 = run * a.run;
+        const bool began = !(a.pairs[p0].x == key && p0 > 0 && a.pairs[p0 - 1].x == key);
+        if (key < a.rows && a.pairs[p1 - 1].x == key && began) {
+            // heads [run + 1, end): runs that start with the row
+            long long end = run + 2, step = 1;
+            while (first_key(end + step - 1) == key) end += step, step *= 2;
+            while (step > 1) {
+                step /= 2;
+                if (first_key(end + step - 1) == key) end += step;
             }
-    }
+            if (end - run > kLong) {
+                if (lane == 0) {
+                    const int at = atomicAdd(&listed, 1);
+                    list[at][0] = run;
+                    list[at][1] = end;
+                }
+            } else if (on) {
+                float acc[N];
+                Pack<float, N>::load(a.tail + run * a.width + col, acc);
+                add_heads<N>(a, run + 1, end, col, acc);
 #pragma unroll
-    for (int j = 0; j < N; ++j) acc[j] *= scale;
-    Pack<T, N>::store(out + (long long)key * width + col, acc);
+                for (int j = 0; j < N; ++j) acc[j] *= a.scale;
+                Pack<T, N>::store(out + (long long)key * a.width + col, acc);
+            }
+        }
+    }
+    __syncthreads();
+    for (int k = 0; k < listed; ++k) {
+        const long long from = list[k][0], end = list[k][1], heads = end - from - 1;
+        const long long share = (heads + groups - 1) / groups;
+        const long long r0 = from + 1 + group * share < end ? from + 1 + group * share : end;
+        const long long r1 = r0 + share < end ? r0 + share : end;
+        float acc[N];
+#pragma unroll
+        for (int j = 0; j < N; ++j) acc[j] = 0.0f;
+        if (on) {
+            if (group == 0) Pack<float, N>::load(a.tail + from * a.width + col, acc);
+            add_heads<N>(a, r0, r1, col, acc);
+#pragma unroll
+            for (int j = 0; j < N; ++j) part[threadIdx.x][j] = acc[j];
+        }
+        __syncthreads();
+        if (on && group == 0) {
+            for (int g = 1; g < groups; ++g)
+#pragma unroll
+                for (int j = 0; j < N; ++j) acc[j] += part[(g << a.lanes_log) + lane][j];
+#pragma unroll
+            for (int j = 0; j < N; ++j) acc[j] *= a.scale;
+            Pack<T, N>::store(out + (long long)a.pairs[(from + 1) * a.run].x * a.width + col, acc);
+        }
+        __syncthreads();
+    }
 }
 
 // -------------------------------------------------------------------- host --
@@ -352,10 +527,10 @@ int embed_type(const void* table, long long rows, long long width, long long str
 }
 
 struct GradPlan {
-    int passes, bits[4], shift[4];
-    int tiles;
+    int passes, bits_all, bits[4], shift[4];
+    int tiles, run;
     long long runs;
-    long long keys[2], tokens[2], counts, totals, head, tail, bytes;  // workspace offsets
+    long long pairs[2], counts, totals, head, tail, bytes;  // workspace offsets
 };
 
 bool grad_plan(long long n, long long rows, long long width, GradPlan* p) {
@@ -363,6 +538,7 @@ bool grad_plan(long long n, long long rows, long long width, GradPlan* p) {
         return false;
     int bits = 1;
     while ((rows >> bits) != 0) ++bits;  // keys 0 .. rows
+    p->bits_all = bits;
     p->passes = (bits + kMaxBits - 1) / kMaxBits;
     int at = 0;
     for (int q = 0; q < p->passes; ++q) {
@@ -371,19 +547,18 @@ bool grad_plan(long long n, long long rows, long long width, GradPlan* p) {
         at += p->bits[q];
     }
     p->tiles = (int)((n + kTile - 1) / kTile);
-    p->runs = (n + kRun - 1) / kRun;
+    // few tokens: short runs, or too few groups of lanes have work
+    p->run = n <= kSmall ? 8 : n <= 262144 ? 32 : 64;
+    p->runs = (n + p->run - 1) / p->run;
     long long o = 0;
     auto take = [&](long long bytes) {
         const long long here = o;
         o += (bytes + 255) / 256 * 256;
         return here;
     };
-    for (int k = 0; k < 2; ++k) {
-        p->keys[k] = take(4 * n);
-        p->tokens[k] = take(4 * n);
-    }
-    p->counts = take(4ll * kMaxDigits * p->tiles);
-    p->totals = take(4ll * kMaxDigits);
+    for (int k = 0; k < 2; ++k) p->pairs[k] = k == 0 || n > kSmall ? take(8 * n) : 0;
+    p->counts = n > kSmall ? take(4ll * kMaxDigits * p->tiles) : 0;
+    p->totals = n > kSmall ? take(4ll * kMaxDigits) : 0;
     p->head = take(4 * p->runs * width);
     p->tail = take(4 * p->runs * width);
     p->bytes = o < 256 ? 256 : o;
@@ -393,37 +568,34 @@ bool grad_plan(long long n, long long rows, long long width, GradPlan* p) {
 template <typename Id, bool FIRST>
 int sort_pass(const GradPlan& p, int q, const void* ids, long long n, long long rows, char* ws,
               hipStream_t stream) {
-    const unsigned* ik = (const unsigned*)(ws + p.keys[(q + 1) & 1]);
-    const unsigned* it = (const unsigned*)(ws + p.tokens[(q + 1) & 1]);
-    unsigned* ok = (unsigned*)(ws + p.keys[q & 1]);
-    unsigned* ot = (unsigned*)(ws + p.tokens[q & 1]);
+    const uint2* in = (const uint2*)(ws + p.pairs[(q + 1) & 1]);
+    uint2* out = (uint2*)(ws + p.pairs[q & 1]);
     unsigned* counts = (unsigned*)(ws + p.counts);
     unsigned* totals = (unsigned*)(ws + p.totals);
     const dim3 tiles((unsigned)p.tiles), block(kBlock);
-    k_eg_count<Id, FIRST><<<tiles, block, 0, stream>>>((const Id*)ids, ik, n, rows, p.shift[q],
+    k_eg_count<Id, FIRST><<<tiles, block, 0, stream>>>((const Id*)ids, in, n, rows, p.shift[q],
                                                        p.bits[q], p.tiles, counts);
     k_eg_prefix<<<dim3(1u << p.bits[q]), block, 0, stream>>>(counts, p.tiles, totals);
-    k_eg_scatter<Id, FIRST><<<tiles, block, 0, stream>>>((const Id*)ids, ik, it, n, rows,
-                                                         p.shift[q], p.bits[q], p.tiles, counts,
-                                                         totals, ok, ot);
+    k_eg_scatter<Id, FIRST><<<tiles, block, 0, stream>>>((const Id*)ids, in, n, rows, p.shift[q],
+                                                         p.bits[q], p.tiles, counts, totals, out);
     return fail(hipGetLastError());
 }
 
 template <typename T, int N>
 int reduce_run(const GradPlan& p, const void* grad, long long stride, long long n, long long rows,
                long long width, float scale, void* out, char* ws, hipStream_t stream) {
-    const int last = (p.passes - 1) & 1;
-    const unsigned* keys = (const unsigned*)(ws + p.keys[last]);
-    const unsigned* tokens = (const unsigned*)(ws + p.tokens[last]);
-    float* head = (float*)(ws + p.head);
-    float* tail = (float*)(ws + p.tail);
-    const dim3 grid((unsigned)((p.runs + kWaves - 1) / kWaves),
-                    (unsigned)((width + kWave * N - 1) / (kWave * N)));
-    k_eg_reduce<T, N><<<grid, dim3(kBlock), 0, stream>>>((const T*)grad, stride, keys, tokens, n,
-                                                         (unsigned)rows, (int)width, scale,
-                                                         (T*)out, head, tail);
-    k_eg_join<T, N><<<grid, dim3(kBlock), 0, stream>>>(keys, n, (unsigned)rows, (int)width, scale,
-                                                       (T*)out, head, tail);
+    Sums a;
+    a.pairs = (const uint2*)(ws + p.pairs[n <= kSmall ? 0 : (p.passes - 1) & 1]);
+    a.n = n, a.rows = (unsigned)rows, a.width = (int)width, a.run = p.run, a.scale = scale;
+    a.head = (float*)(ws + p.head), a.tail = (float*)(ws + p.tail);
+    const long long pieces = width / N;
+    a.lanes_log = 0;
+    while ((1 << a.lanes_log) < pieces && a.lanes_log < 6) ++a.lanes_log;
+    const int groups = kBlock >> a.lanes_log;
+    const dim3 grid((unsigned)((p.runs + groups - 1) / groups),
+                    (unsigned)((pieces + (1 << a.lanes_log) - 1) >> a.lanes_log));
+    k_eg_reduce<T, N><<<grid, dim3(kBlock), 0, stream>>>((const T*)grad, stride, a, (T*)out);
+    k_eg_join<T, N><<<grid, dim3(kBlock), 0, stream>>>(a, (T*)out);
     return fail(hipGetLastError());
 }
 
@@ -431,24 +603,40 @@ template <typename T>
 int grad_type(const GradPlan& p, const void* grad, long long stride, const void* ids, int id_bytes,
               long long n, long long rows, long long width, float scale, void* out, char* ws,
               hipStream_t stream) {
-    const long long bytes = rows * width * (long long)sizeof(T);
-    const long long blocks = bytes / (16 * kBlock) + 1;
-    k_eg_zero<<<dim3((unsigned)(blocks < 2048 ? blocks : 2048)), dim3(kBlock), 0, stream>>>(
-        (uint4*)out, bytes / 16, (unsigned char*)out + bytes / 16 * 16, (int)(bytes % 16));
-    int rc = fail(hipGetLastError());
-    if (rc != VOX_OK || n == 0) return rc;
-    for (int q = 0; q < p.passes; ++q) {
-        if (q > 0)
-            rc = sort_pass<int32_t, false>(p, q, nullptr, n, rows, ws, stream);
-        else if (id_bytes == 4)
-            rc = sort_pass<int32_t, true>(p, q, ids, n, rows, ws, stream);
+    const long long bytes = rows * width * (long long)sizeof(T), pieces = bytes / 16;
+    unsigned char* tail = (unsigned char*)out + pieces * 16;
+    int rc;
+    if (n > 0 && n <= kSmall) {
+        const long long blocks = pieces / (4 * kSmallBlock) + 1;
+        const dim3 grid((unsigned)(1 + (blocks < 255 ? blocks : 255)));
+        if (id_bytes == 4)
+            k_eg_small<int32_t><<<grid, dim3(kSmallBlock), 0, stream>>>(
+                (const int32_t*)ids, (int)n, rows, p.passes, p.bits_all, (uint2*)(ws + p.pairs[0]),
+                (uint4*)out, pieces, tail, (int)(bytes % 16));
         else
-            rc = sort_pass<int64_t, true>(p, q, ids, n, rows, ws, stream);
-        if (rc != VOX_OK) return rc;
+            k_eg_small<int64_t><<<grid, dim3(kSmallBlock), 0, stream>>>(
+                (const int64_t*)ids, (int)n, rows, p.passes, p.bits_all, (uint2*)(ws + p.pairs[0]),
+                (uint4*)out, pieces, tail, (int)(bytes % 16));
+        rc = fail(hipGetLastError());
+    } else {
+        const long long blocks = pieces / kBlock + 1;
+        k_eg_zero<<<dim3((unsigned)(blocks < 2048 ? blocks : 2048)), dim3(kBlock), 0, stream>>>(
+            (uint4*)out, pieces, tail, (int)(bytes % 16));
+        rc = fail(hipGetLastError());
+        for (int q = 0; n > 0 && rc == VOX_OK && q < p.passes; ++q) {
+            if (q > 0)
+                rc = sort_pass<int32_t, false>(p, q, nullptr, n, rows, ws, stream);
+            else if (id_bytes == 4)
+                rc = sort_pass<int32_t, true>(p, q, ids, n, rows, ws, stream);
+            else
+                rc = sort_pass<int64_t, true>(p, q, ids, n, rows, ws, stream);
+        }
     }
-    // as few elements per lane as leave one slab of columns
-    const int most = width <= 64 ? 1 : width <= 128 ? 2 : 4;
-    switch (piece(grad, out, width, stride, sizeof(T), most)) {
+    if (rc != VOX_OK || n == 0) return rc;
+    switch (piece(grad, out, width, stride, sizeof(T), 8)) {
+        case 8:
+            if constexpr (sizeof(T) == 2)
+                return reduce_run<T, 8>(p, grad, stride, n, rows, width, scale, out, ws, stream);
         case 4: return reduce_run<T, 4>(p, grad, stride, n, rows, width, scale, out, ws, stream);
         case 2: return reduce_run<T, 2>(p, grad, stride, n, rows, width, scale, out, ws, stream);
         default: return reduce_run<T, 1>(p, grad, stride, n, rows, width, scale, out, ws, stream);

@@ -229,32 +229,37 @@ __global__ __launch_bounds__(256) void k_scan_sum_grad(ScanArgs a) {
 }
 
 // The state that enters each chunk, over the chunks' (mul, add), in place of
-// add: 16 channels of a block, 64 threads along the chunks, each first over
-// its own share, then one after another over the shares, then over its own
-// again. grad: from the last chunk to the first.
+// add: 8 channels of a block, 128 threads along the chunks, each first over its
+// own share, then over the shares before it, then over its own again. Up to
+// kHeld chunks of a share stay in registers, all loaded at once: with the 4096
+// chunks at most that chunk_of() makes of up to 4 M tokens, none is read twice.
+// grad: from the last chunk to the first.
+constexpr int kParts = 128, kHeld = 32;
+
 template <bool GRAD>
 __global__ __launch_bounds__(1024) void k_scan_join(ScanArgs a) {
-    constexpr int kBatch = 8;
-    __shared__ float muls[64][16], adds[64][16];
-    const int lane = threadIdx.x & 15, part = threadIdx.x >> 4;
-    const int c = blockIdx.x * 16 + lane;
+    __shared__ float muls[kParts][8], adds[kParts][8];
+    const int lane = threadIdx.x & 7, part = threadIdx.x >> 3;
+    const int c = blockIdx.x * 8 + lane;
     const bool on = c < a.width;
-    const int per = (a.chunks + 63) / 64;
+    const int per = (a.chunks + kParts - 1) / kParts;
     const int k0 = min(a.chunks, part * per), k1 = min(a.chunks, k0 + per);
     auto at = [&](int k) {
         return (long long)(GRAD ? a.chunks - 1 - k : k) * a.width + (on ? c : 0);
     };
-    float mul = 1.0f, add = 0.0f;
-    for (int k = k0; k < k1; k += kBatch) {
-        float u[kBatch], v[kBatch];
+    float u[kHeld], v[kHeld];
+    auto load = [&](int k) {
 #pragma unroll
-        for (int j = 0; j < kBatch; ++j) {
-            u[j] = a.mul[at(min(k + j, k1 - 1))];
-            v[j] = a.add[at(min(k + j, k1 - 1))];
+        for (int j = 0; j < kHeld; ++j) {
+            u[j] = 1.0f, v[j] = 0.0f;
+            if (k + j < k1) u[j] = a.mul[at(k + j)], v[j] = a.add[at(k + j)];
         }
+    };
+    float mul = 1.0f, add = 0.0f;
+    for (int k = k0; k < k1; k += kHeld) {
+        load(k);
 #pragma unroll
-        for (int j = 0; j < kBatch; ++j) {
-            if (k + j >= k1) break;
+        for (int j = 0; j < kHeld; ++j) {
             add = enter(u[j], v[j], add);
             mul = forgets(u[j]) ? u[j] : mul * u[j];
         }
@@ -263,18 +268,13 @@ __global__ __launch_bounds__(1024) void k_scan_join(ScanArgs a) {
     adds[part][lane] = add;
     __syncthreads();
     float h = 0.0f;  // nothing enters the first chunk: it starts a range
+#pragma unroll 8
     for (int p = 0; p < part; ++p) h = enter(muls[p][lane], adds[p][lane], h);
-    for (int k = k0; k < k1; k += kBatch) {
-        float u[kBatch], v[kBatch];
+    for (int k = k0; k < k1; k += kHeld) {
+        if (k1 - k0 > kHeld) load(k);
 #pragma unroll
-        for (int j = 0; j < kBatch; ++j) {
-            u[j] = a.mul[at(min(k + j, k1 - 1))];
-            v[j] = a.add[at(min(k + j, k1 - 1))];
-        }
-#pragma unroll
-        for (int j = 0; j < kBatch; ++j) {
-            if (k + j >= k1) break;
-            if (on) a.add[at(k + j)] = h;
+        for (int j = 0; j < kHeld; ++j) {
+            if (on && k + j < k1) a.add[at(k + j)] = h;
             h = enter(u[j], v[j], h);
         }
     }
@@ -515,7 +515,7 @@ int run(ScanArgs a, hipStream_t stream) {
         k_scan_doc<T, V><<<dim3(a.docs + 2, slabs), block, 0, stream>>>(a);
     } else {
         if (a.chunks > 1) {
-            const dim3 grid((unsigned)a.chunks, slabs), join((unsigned)((a.width + 15) / 16));
+            const dim3 grid((unsigned)a.chunks, slabs), join((unsigned)((a.width + 7) / 8));
             if constexpr (GRAD) {
                 k_scan_sum_grad<T, V><<<grid, block, 0, stream>>>(a);
                 k_scan_join<true><<<join, dim3(1024), 0, stream>>>(a);
