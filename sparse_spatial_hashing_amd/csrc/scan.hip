@@ -27,7 +27,7 @@ struct ScanArgs {
     void* ggate;
     void* gx;
     float* grad_state;        // may be null
-    float* mul;               // [chunks, width]: what each chunk does to a state, then (add)
+    float* mul;               // sum_at(): what each chunk does to a state, then (add)
     float* add;               // the state that enters it
     int t, width, docs, reverse;
     int chunk, chunks;        // steps of a chunk (a multiple of kRun)
@@ -118,6 +118,12 @@ struct Steps {
 // passes.
 constexpr float kForget = -0.0f;
 
+// (mul, add) of chunk k, channel c: 8 channels of all chunks together, which
+// is what a block of k_scan_join reads.
+__device__ __forceinline__ long long sum_at(const ScanArgs& a, int k, int c) {
+    return ((long long)(c >> 3) * a.chunks + k) * 8 + (c & 7);
+}
+
 __device__ __forceinline__ bool forgets(float mul) { return __float_as_uint(mul) == 0x80000000u; }
 
 __device__ __forceinline__ float enter(float mul, float add, float h) {
@@ -169,7 +175,7 @@ __global__ __launch_bounds__(256) void k_scan_sum(ScanArgs a) {
         s = e;
     }
     if (on) {
-        const long long at = (long long)blockIdx.x * a.width + c;
+        const long long at = sum_at(a, blockIdx.x, c);
         Pack<float, V>::store(a.mul + at, mul);
         Pack<float, V>::store(a.add + at, add);
     }
@@ -222,7 +228,7 @@ __global__ __launch_bounds__(256) void k_scan_sum_grad(ScanArgs a) {
         s = b;
     }
     if (on) {
-        const long long at = (long long)blockIdx.x * a.width + c;
+        const long long at = sum_at(a, blockIdx.x, c);
         Pack<float, V>::store(a.mul + at, mul);
         Pack<float, V>::store(a.add + at, add);
     }
@@ -245,7 +251,7 @@ __global__ __launch_bounds__(1024) void k_scan_join(ScanArgs a) {
     const int per = (a.chunks + kParts - 1) / kParts;
     const int k0 = min(a.chunks, part * per), k1 = min(a.chunks, k0 + per);
     auto at = [&](int k) {
-        return (long long)(GRAD ? a.chunks - 1 - k : k) * a.width + (on ? c : 0);
+        return sum_at(a, GRAD ? a.chunks - 1 - k : k, on ? c : 0);
     };
     float u[kHeld], v[kHeld];
     auto load = [&](int k) {
@@ -313,7 +319,7 @@ __global__ __launch_bounds__(256) void k_scan_run(ScanArgs a) {
     float h[V];
 #pragma unroll
     for (int j = 0; j < V; ++j) h[j] = 0.0f;
-    if (a.chunks > 1 && on) Pack<float, V>::load(a.add + (long long)blockIdx.x * a.width + c, h);
+    if (a.chunks > 1 && on) Pack<float, V>::load(a.add + sum_at(a, blockIdx.x, c), h);
     Walk walk;
     Doc d = {0, 0, -1};
     for (int s = begin; s < end;) {
@@ -374,7 +380,7 @@ __global__ __launch_bounds__(256) void k_scan_run_grad(ScanArgs a) {
     float back[V];
 #pragma unroll
     for (int j = 0; j < V; ++j) back[j] = 0.0f;
-    if (a.chunks > 1 && on) Pack<float, V>::load(a.add + (long long)blockIdx.x * a.width + c, back);
+    if (a.chunks > 1 && on) Pack<float, V>::load(a.add + sum_at(a, blockIdx.x, c), back);
     Walk walk;
     Doc d = {0, 0, -1};
     for (int s = end; s > begin;) {
@@ -561,9 +567,7 @@ int dispatch(int dtype, ScanArgs& a, bool grad, void* workspace, hipStream_t str
     a.chunk = chunk_of(a.t);
     a.chunks = (int)((a.t + (long long)a.chunk - 1) / a.chunk);
     a.mul = (float*)workspace;
-    a.add = a.mul + (long long)a.chunks * a.width;
-    // sum and add are written in pieces too
-    if (((size_t)a.add & 15) != 0) a.add += 4 - (((size_t)a.add & 15) >> 2);
+    a.add = a.mul + a.chunks * ((a.width + 7ll) / 8 * 8);
     if (dtype == TOK_F32) return dispatch_type<float>(a, grad, stream);
     if (dtype == TOK_BF16) return dispatch_type<bf16_t>(a, grad, stream);
     return dispatch_type<f16_t>(a, grad, stream);
@@ -580,7 +584,7 @@ int64_t tok_scan_runs(int64_t t) {
 int64_t tok_scan_workspace_bytes(int64_t t, int64_t width) {
     if (t < 0 || t > kMaxTokens || width < 1 || width > kMaxWidth) return VOX_EINVAL;
     const long long chunk = chunk_of(t), chunks = (t + chunk - 1) / chunk;
-    return chunks <= 1 ? 256 : (chunks * width * 8 + 16 + 255) / 256 * 256;
+    return chunks <= 1 ? 256 : (chunks * ((width + 7) / 8 * 64) + 255) / 256 * 256;
 }
 
 int tok_scan(const void* gate, const void* x, int32_t dtype, int64_t t, int64_t width,
