@@ -115,8 +115,8 @@ typedef struct tok_attention {
     int64_t q_pos_stride[2], k_pos_stride[2];                   /* token, axis */
 } tok_attention;
 
-/* Bytes of workspace for tok_attend / tok_attend_grad, or VOX_EINVAL. The
- * workspace needs no initial contents, 256-byte aligned. */
+/* Bytes of workspace for tok_attend / tok_attend_grad (0: NULL will do), or
+ * VOX_EINVAL. The workspace needs no initial contents, 256-byte aligned. */
 int64_t tok_attend_workspace_bytes(const tok_attention* args);
 int64_t tok_attend_grad_workspace_bytes(const tok_attention* args);
 
@@ -141,6 +141,8 @@ int tok_attend_grad(const tok_attention* args, const void* q, const void* k, con
  * tokens). Tokens of no document get y = 0 and no gradient. The state is held
  * in float32. carry (or NULL) receives the state before each run of
  * TOK_SCAN_RUN tokens, [tok_scan_runs(t), width] float32, for tok_scan_grad.
+ * The workspace (0 bytes: NULL will do) needs no initial contents, 256-byte
+ * aligned.
  * Limits: t < 2^31, 1 <= width <= 65536, 1 <= docs <= 2^20.
  */
 #define TOK_SCAN_RUN 16

@@ -7,6 +7,7 @@
 #include <math.h>
 
 #include "attend.h"
+#include "token_ops.h"
 
 int ssh_hip_fail(hipError_t e);  // records the error for vox_last_hip_error()
 
@@ -112,14 +113,14 @@ extern "C" {
 int64_t tok_attend_workspace_bytes(const tok_attention* t) {
     if (!check(t)) return VOX_EINVAL;
     const Cut c = cut(*t);
-    if (c.nsplit == 1) return 256;
+    if (c.nsplit == 1) return 0;
     const long long rows = t->tq * t->heads;
     return round256(c.nsplit * rows * t->width * 4) + round256(c.nsplit * rows * 8);
 }
 
 int64_t tok_attend_grad_workspace_bytes(const tok_attention* t) {
     if (!check(t)) return VOX_EINVAL;
-    return round256(t->tq * t->heads * 4) + 256;
+    return round256(t->tq * t->heads * 4);
 }
 
 int tok_attend(const tok_attention* t, const void* q, const void* k, const void* v, void* out,
@@ -128,9 +129,7 @@ int tok_attend(const tok_attention* t, const void* q, const void* k, const void*
     if (t->tq == 0) return VOX_OK;
     if (!q || !out || (t->tk && (!k || !v))) return VOX_EINVAL;
     if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(out)) return VOX_EINVAL;
-    if (!workspace || ((size_t)workspace & 255) ||
-        workspace_bytes < tok_attend_workspace_bytes(t))
-        return VOX_EWORKSPACE;
+    if (!workspace_ok(workspace, workspace_bytes, tok_attend_workspace_bytes(t))) return VOX_EWORKSPACE;
     const Cut c = cut(*t);
     AttArgs a = make_args(*t, c);
     a.q = q, a.k = k, a.v = v, a.out = out, a.lse = lse;
@@ -153,9 +152,7 @@ int tok_attend_grad(const tok_attention* t, const void* q, const void* k, const 
     const void* all[] = {q, k, v, out, grad_out, grad_q, grad_k, grad_v};
     for (const void* p : all)
         if (!aligned16(p)) return VOX_EINVAL;
-    if (!workspace || ((size_t)workspace & 255) ||
-        workspace_bytes < tok_attend_grad_workspace_bytes(t))
-        return VOX_EWORKSPACE;
+    if (!workspace_ok(workspace, workspace_bytes, tok_attend_grad_workspace_bytes(t))) return VOX_EWORKSPACE;
     const Cut c = cut(*t);
     AttArgs a = make_args(*t, c);
     a.q = q, a.k = k, a.v = v, a.o = out, a.lse = const_cast<float*>(lse), a.g = grad_out;

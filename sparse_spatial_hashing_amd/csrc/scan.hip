@@ -584,7 +584,7 @@ int64_t tok_scan_runs(int64_t t) {
 int64_t tok_scan_workspace_bytes(int64_t t, int64_t width) {
     if (t < 0 || t > kMaxTokens || width < 1 || width > kMaxWidth) return VOX_EINVAL;
     const long long chunk = chunk_of(t), chunks = (t + chunk - 1) / chunk;
-    return chunks <= 1 ? 256 : (chunks * ((width + 7) / 8 * 64) + 255) / 256 * 256;
+    return chunks <= 1 ? 0 : (chunks * ((width + 7) / 8 * 64) + 255) / 256 * 256;
 }
 
 int tok_scan(const void* gate, const void* x, int32_t dtype, int64_t t, int64_t width,
@@ -594,8 +594,7 @@ int tok_scan(const void* gate, const void* x, int32_t dtype, int64_t t, int64_t 
     if (!check(dtype, t, width, offsets, docs, reverse)) return VOX_EINVAL;
     if (t && (!gate || !x || !y)) return VOX_EINVAL;
     if (((size_t)gate | (size_t)x | (size_t)y) % tok_elem_bytes(dtype)) return VOX_EINVAL;
-    if (!workspace || ((size_t)workspace & 255) ||
-        workspace_bytes < tok_scan_workspace_bytes(t, width))
+    if (!workspace_ok(workspace, workspace_bytes, tok_scan_workspace_bytes(t, width)))
         return VOX_EWORKSPACE;
     ScanArgs a = {};
     a.gate = gate, a.x = x, a.offsets = offsets, a.state = state, a.y = y, a.last = last_state;
@@ -614,8 +613,7 @@ int tok_scan_grad(const void* grad_y, const void* gate, const void* x, const flo
     if (((size_t)grad_y | (size_t)gate | (size_t)x | (size_t)grad_gate | (size_t)grad_x) %
         tok_elem_bytes(dtype))
         return VOX_EINVAL;
-    if (!workspace || ((size_t)workspace & 255) ||
-        workspace_bytes < tok_scan_workspace_bytes(t, width))
+    if (!workspace_ok(workspace, workspace_bytes, tok_scan_workspace_bytes(t, width)))
         return VOX_EWORKSPACE;
     ScanArgs a = {};
     a.gate = gate, a.x = x, a.gy = grad_y, a.offsets = offsets, a.state = state;

@@ -16,6 +16,11 @@ inline bool tok_dtype_ok(int dtype) {
     return dtype == TOK_F32 || dtype == TOK_BF16 || dtype == TOK_F16;
 }
 
+// NULL will do where nothing is needed.
+inline bool workspace_ok(const void* p, long long bytes, long long need) {
+    return need == 0 || (p && ((size_t)p & 255) == 0 && bytes >= need);
+}
+
 // N elements moved at once.
 template <typename T, int N>
 struct Pack {

@@ -18,6 +18,7 @@ device, with outputs and workspace allocated by torch.
 from __future__ import annotations
 
 import ctypes
+import struct
 from typing import Optional, Tuple
 
 import torch
@@ -44,9 +45,15 @@ class _Attention(ctypes.Structure):
                 ("q_pos_stride", ctypes.c_int64 * 2), ("k_pos_stride", ctypes.c_int64 * 2)]
 
 
+# The same layout, packed at once: filling the structure field by field costs
+# more than the call it is for.
+_PACK = struct.Struct("@4i2q2i3P2f3P2i12q")
+assert _PACK.size == ctypes.sizeof(_Attention)
+
+
 def _declare(lib) -> None:
     vp, i64, i32, f32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_float
-    at = ctypes.POINTER(_Attention)
+    at = vp                  # tok_attention: packed bytes, or a reference to the structure
     for name, result, args in (
             ("tok_embed", i32, [vp, i64, i64, i64, i32, vp, i32, i64, f32, vp, vp]),
             ("tok_embed_grad_workspace_bytes", i64, [i64, i64, i64]),
@@ -108,33 +115,31 @@ def _ptr(t: Optional[torch.Tensor]):
     return None if t is None else t.data_ptr()
 
 
+def _address(t: Optional[torch.Tensor]) -> int:
+    return 0 if t is None else t.data_ptr()
+
+
 def _size(n: int, what: str) -> int:
     if n < 0:
         raise VoxError(int(n), what)
-    return int(n)
+    return n
 
 
-class _Launch:
-    """The device and current stream of a call, and its workspace."""
+def _call(f, what: str, like: torch.Tensor, *args) -> None:
+    """f(*args, stream) on the current stream of the tensor's device."""
+    index = like.device.index
+    stream = torch._C._cuda_getCurrentRawStream(index)
+    if torch._C._cuda_getDevice() == index:
+        rc = f(*args, stream)
+    else:
+        with torch.cuda.device(index):
+            rc = f(*args, stream)
+    if rc:
+        _check(rc, what)
 
-    def __init__(self, like: torch.Tensor):
-        self.device = like.device
-        self._guard = None
-        if torch.cuda.current_device() != like.device.index:
-            self._guard = torch.cuda.device(like.device)
 
-    def __enter__(self):
-        if self._guard is not None:
-            self._guard.__enter__()
-        self.stream = torch.cuda.current_stream(self.device).cuda_stream
-        return self
-
-    def __exit__(self, *exc):
-        if self._guard is not None:
-            self._guard.__exit__(*exc)
-
-    def workspace(self, nbytes: int) -> torch.Tensor:
-        return torch.empty((nbytes + 255) // 256 * 256, dtype=torch.uint8, device=self.device)
+def _workspace(nbytes: int, like: torch.Tensor) -> Optional[torch.Tensor]:
+    return like.new_empty(nbytes, dtype=torch.uint8) if nbytes else None
 
 
 # ------------------------------------------------------------------ embedding --
@@ -154,15 +159,12 @@ def _embed(table: torch.Tensor, ids: torch.Tensor, scale: float) -> torch.Tensor
     if table.stride(1) != 1 and table.shape[1] > 1 or table.stride(0) < 0:
         table = table.contiguous()
     rows, width = table.shape
-    out = torch.empty((*ids.shape, width), dtype=table.dtype, device=table.device)
-    with _Launch(table) as on:
-        _check(_lib.tok_embed(table.data_ptr(), rows, width, table.stride(0), dtype, ids.data_ptr(),
-                              ids.element_size(), ids.numel(), scale, out.data_ptr(), on.stream),
-               "tok_embed")
+    out = table.new_empty((*ids.shape, width))
+    _call(_lib.tok_embed, "tok_embed", table, table.data_ptr(), rows, width, table.stride(0), dtype,
+          ids.data_ptr(), ids.element_size(), ids.numel(), scale, out.data_ptr())
     return out
 
 
-@torch.no_grad()
 def embed_grad(grad: torch.Tensor, ids: torch.Tensor, rows: int, *,
                scale: float = 1.0) -> torch.Tensor:
     """Gradient of ``embed``'s table: [rows, width] in grad's type, row r the
@@ -180,13 +182,10 @@ def embed_grad(grad: torch.Tensor, ids: torch.Tensor, rows: int, *,
         flat = flat.contiguous()
     nbytes = _size(_lib.tok_embed_grad_workspace_bytes(n, rows, width),
                    "tok_embed_grad_workspace_bytes")
-    out = torch.empty((rows, width), dtype=grad.dtype, device=grad.device)
-    with _Launch(grad) as on:
-        ws = on.workspace(nbytes)
-        _check(_lib.tok_embed_grad(flat.data_ptr(), flat.stride(0), dtype, ids.data_ptr(),
-                                   ids.element_size(), n, rows, width, float(scale),
-                                   out.data_ptr(), ws.data_ptr(), ws.numel(), on.stream),
-               "tok_embed_grad")
+    out, ws = grad.new_empty((rows, width)), _workspace(nbytes, grad)
+    _call(_lib.tok_embed_grad, "tok_embed_grad", grad, flat.data_ptr(), flat.stride(0), dtype,
+          ids.data_ptr(), ids.element_size(), n, rows, width, float(scale), out.data_ptr(),
+          _ptr(ws), nbytes)
     return out
 
 
@@ -281,37 +280,31 @@ def _attention(q, k, v, q_offsets, k_offsets, scale, cap, slopes, q_pos, k_pos, 
             raise ValueError("q_pos and k_pos must have as many axes")
     elif q_pos is not None or k_pos is not None:
         raise ValueError("positions need slopes")
-    a = _Attention(dtype=_DTYPES[q.dtype], heads=heads, kv_heads=kv_heads, width=width, tq=tq, tk=tk,
-                   docs=docs, mask=int(bool(causal) or prefix is not None),
-                   q_offsets=_ptr(q_offsets), k_offsets=_ptr(k_offsets), prefix=_ptr(prefix),
-                   scale=scale, cap=float(cap), slopes=_ptr(slopes), axes=axes,
-                   q_stride=q.stride()[:2], k_stride=k.stride()[:2], v_stride=v.stride()[:2])
-    if axes:
-        a.q_pos, a.k_pos = _ptr(q_pos), _ptr(k_pos)
-        a.q_pos_stride, a.k_pos_stride = q_pos.stride(), k_pos.stride()
+    g_stride = (0, 0)
     if grad is not None:
         grad = _heads("grad_out", grad, q)
         if grad.shape != q.shape:
             raise ValueError(f"grad_out must have q's shape {tuple(q.shape)}")
-        a.g_stride = grad.stride()[:2]
+        g_stride = grad.stride()[:2]
+    a = _PACK.pack(
+        _DTYPES[q.dtype], heads, kv_heads, width, tq, tk, docs, bool(causal) or prefix is not None,
+        _address(q_offsets), _address(k_offsets), _address(prefix), scale, cap, _address(slopes),
+        _address(q_pos), _address(k_pos), axes, 0, *q.stride()[:2], *k.stride()[:2], *v.stride()[:2],
+        *g_stride, *(q_pos.stride() if axes else (0, 0)), *(k_pos.stride() if axes else (0, 0)))
     return a, (q, k, v, grad, q_offsets, k_offsets, prefix, slopes, q_pos, k_pos)
 
 
 def _attend(q, k, v, want_lse, **more):
     a, kept = _attention(q, k, v, **more)
     q, k, v = kept[:3]
-    nbytes = _size(_lib.tok_attend_workspace_bytes(ctypes.byref(a)), "tok_attend_workspace_bytes")
-    out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device) if want_lse else None
-    with _Launch(q) as on:
-        ws = on.workspace(nbytes)
-        _check(_lib.tok_attend(ctypes.byref(a), q.data_ptr(), k.data_ptr(), v.data_ptr(),
-                               out.data_ptr(), _ptr(lse), ws.data_ptr(), ws.numel(), on.stream),
-               "tok_attend")
+    nbytes = _size(_lib.tok_attend_workspace_bytes(a), "tok_attend_workspace_bytes")
+    out, ws = q.new_empty(q.shape), _workspace(nbytes, q)
+    lse = q.new_empty(q.shape[:2], dtype=torch.float32) if want_lse else None
+    _call(_lib.tok_attend, "tok_attend", q, a, q.data_ptr(), k.data_ptr(), v.data_ptr(),
+          out.data_ptr(), _ptr(lse), _ptr(ws), nbytes)
     return out, lse
 
 
-@torch.no_grad()
 def attend_grad(grad_out: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
                 out: torch.Tensor, lse: torch.Tensor, *,
                 q_offsets: Optional[torch.Tensor] = None,
@@ -333,15 +326,12 @@ def attend_grad(grad_out: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: tor
     out, lse = out.contiguous(), lse.contiguous()
     if out.data_ptr() % 16:
         out = out.clone()
-    nbytes = _size(_lib.tok_attend_grad_workspace_bytes(ctypes.byref(a)),
-                   "tok_attend_grad_workspace_bytes")
-    gq, gk, gv = (torch.empty(t.shape, dtype=q.dtype, device=q.device) for t in (q, k, v))
-    with _Launch(q) as on:
-        ws = on.workspace(nbytes)
-        _check(_lib.tok_attend_grad(ctypes.byref(a), q.data_ptr(), k.data_ptr(), v.data_ptr(),
-                                    out.data_ptr(), lse.data_ptr(), g.data_ptr(), gq.data_ptr(),
-                                    gk.data_ptr(), gv.data_ptr(), ws.data_ptr(), ws.numel(),
-                                    on.stream), "tok_attend_grad")
+    nbytes = _size(_lib.tok_attend_grad_workspace_bytes(a), "tok_attend_grad_workspace_bytes")
+    gq, gk, gv = q.new_empty(q.shape), k.new_empty(k.shape), k.new_empty(k.shape)
+    ws = _workspace(nbytes, q)
+    _call(_lib.tok_attend_grad, "tok_attend_grad", q, a, q.data_ptr(), k.data_ptr(), v.data_ptr(),
+          out.data_ptr(), lse.data_ptr(), g.data_ptr(), gq.data_ptr(), gk.data_ptr(), gv.data_ptr(),
+          _ptr(ws), nbytes)
     return gq, gk, gv
 
 
@@ -411,22 +401,17 @@ def _scan(gate, x, offsets, state, reverse, want_carry):
     dtype, gate, x, offsets, docs = _scan_args(gate, x, offsets)
     t, width = x.shape
     state = _state("state", state, docs, width, x)
-    y = torch.empty((t, width), dtype=x.dtype, device=x.device)
-    last = torch.empty((docs, width), dtype=torch.float32, device=x.device)
+    y, last = x.new_empty((t, width)), x.new_empty((docs, width), dtype=torch.float32)
     carry = None
     if want_carry:
-        carry = torch.empty((_size(_lib.tok_scan_runs(t), "tok_scan_runs"), width),
-                            dtype=torch.float32, device=x.device)
+        carry = x.new_empty((-(-t // TOK_SCAN_RUN), width), dtype=torch.float32)
     nbytes = _size(_lib.tok_scan_workspace_bytes(t, width), "tok_scan_workspace_bytes")
-    with _Launch(x) as on:
-        ws = on.workspace(nbytes)
-        _check(_lib.tok_scan(gate.data_ptr(), x.data_ptr(), dtype, t, width, _ptr(offsets), docs,
-                             int(bool(reverse)), _ptr(state), y.data_ptr(), last.data_ptr(),
-                             _ptr(carry), ws.data_ptr(), ws.numel(), on.stream), "tok_scan")
+    ws = _workspace(nbytes, x)
+    _call(_lib.tok_scan, "tok_scan", x, gate.data_ptr(), x.data_ptr(), dtype, t, width, _ptr(offsets),
+          docs, bool(reverse), _ptr(state), y.data_ptr(), last.data_ptr(), _ptr(carry), _ptr(ws), nbytes)
     return y, last, carry
 
 
-@torch.no_grad()
 def gated_scan_grad(grad_y: torch.Tensor, gate: torch.Tensor, x: torch.Tensor,
                     carry: torch.Tensor, offsets: Optional[torch.Tensor] = None, *,
                     state: Optional[torch.Tensor] = None,
@@ -447,16 +432,13 @@ def gated_scan_grad(grad_y: torch.Tensor, gate: torch.Tensor, x: torch.Tensor,
     carry = carry.contiguous()
     state = _state("state", state, docs, width, x)
     grad_state = _state("grad_state", grad_state, docs, width, x)
-    gg, gx = torch.empty_like(gate), torch.empty_like(x)
-    gs = torch.empty((docs, width), dtype=torch.float32, device=x.device)
+    gg, gx = gate.new_empty((t, width)), x.new_empty((t, width))
+    gs = x.new_empty((docs, width), dtype=torch.float32)
     nbytes = _size(_lib.tok_scan_workspace_bytes(t, width), "tok_scan_workspace_bytes")
-    with _Launch(x) as on:
-        ws = on.workspace(nbytes)
-        _check(_lib.tok_scan_grad(grad_y.data_ptr(), gate.data_ptr(), x.data_ptr(),
-                                  carry.data_ptr(), dtype, t, width, _ptr(offsets), docs,
-                                  int(bool(reverse)), _ptr(state), _ptr(grad_state),
-                                  gg.data_ptr(), gx.data_ptr(), gs.data_ptr(), ws.data_ptr(),
-                                  ws.numel(), on.stream), "tok_scan_grad")
+    ws = _workspace(nbytes, x)
+    _call(_lib.tok_scan_grad, "tok_scan_grad", x, grad_y.data_ptr(), gate.data_ptr(), x.data_ptr(),
+          carry.data_ptr(), dtype, t, width, _ptr(offsets), docs, bool(reverse), _ptr(state),
+          _ptr(grad_state), gg.data_ptr(), gx.data_ptr(), gs.data_ptr(), _ptr(ws), nbytes)
     return gg, gx, gs
 
 
