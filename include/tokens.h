@@ -91,7 +91,8 @@ int tok_embed_grad(const void* grad, int64_t grad_stride, int32_t dtype, const v
  * value that is not finite may reach every query of it.
  * Positions are int32 in [0, 65535] (values outside are clamped), 1 to 3 axes,
  * any strides. width: a multiple of 8, at most 128. Token and head strides of
- * q, k, v are multiples of 8 elements and the bases 16-byte aligned; out,
+ * q, k, v are multiples of 8 elements, the token strides below 2^25 elements
+ * and the bases 16-byte aligned; out,
  * lse [tq, heads] and the gradients are contiguous, grad_out as q.
  */
 typedef struct tok_attention {

@@ -34,7 +34,7 @@ struct AttArgs {
     int tiles;            // row tiles (forward, dQ) or key tiles (dK dV) over all documents
     float scale;          // > 0
     float scale2;         // scale * log2(e)
-    float cap_in;         // 2 log2(e) scale / cap
+    float cap_in;         // scale / cap
     float cap2;           // cap * log2(e); 0: no cap
 };
 
@@ -42,14 +42,13 @@ enum AttPass { kAttForward = 0, kAttGradQ = 1, kAttGradKV = 2 };
 
 // One pass with these elements and padded width; waves: wavefronts of a block
 // (1 or 4). Defined once per (type, padded width).
-typedef hipError_t (*AttLaunch)(AttPass pass, const AttArgs& a, bool general, int waves,
-                                hipStream_t stream);
-hipError_t att_launch_bf16_32(AttPass, const AttArgs&, bool, int, hipStream_t);
-hipError_t att_launch_bf16_64(AttPass, const AttArgs&, bool, int, hipStream_t);
-hipError_t att_launch_bf16_128(AttPass, const AttArgs&, bool, int, hipStream_t);
-hipError_t att_launch_f16_32(AttPass, const AttArgs&, bool, int, hipStream_t);
-hipError_t att_launch_f16_64(AttPass, const AttArgs&, bool, int, hipStream_t);
-hipError_t att_launch_f16_128(AttPass, const AttArgs&, bool, int, hipStream_t);
+typedef hipError_t (*AttLaunch)(AttPass pass, const AttArgs& a, int waves, hipStream_t stream);
+hipError_t att_launch_bf16_32(AttPass, const AttArgs&, int, hipStream_t);
+hipError_t att_launch_bf16_64(AttPass, const AttArgs&, int, hipStream_t);
+hipError_t att_launch_bf16_128(AttPass, const AttArgs&, int, hipStream_t);
+hipError_t att_launch_f16_32(AttPass, const AttArgs&, int, hipStream_t);
+hipError_t att_launch_f16_64(AttPass, const AttArgs&, int, hipStream_t);
+hipError_t att_launch_f16_128(AttPass, const AttArgs&, int, hipStream_t);
 
 constexpr int kAttRows = 32;  // query rows (or keys) of a wavefront
 

@@ -15,6 +15,12 @@ namespace {
 
 constexpr long long kMaxElems = 0x7fffffffll;
 constexpr int kMaxDocs = 1 << 20;
+constexpr long long kMaxStride = 1ll << 25;
+
+// 16-byte pieces; a tile of 64 tokens spans less than 2^32 bytes.
+bool stride_ok(const int64_t s[2]) {
+    return s[0] % 8 == 0 && s[1] % 8 == 0 && s[0] >= 0 && s[1] >= 0 && s[0] < kMaxStride;
+}
 
 bool check(const tok_attention* t) {
     if (!t || (t->dtype != TOK_BF16 && t->dtype != TOK_F16)) return false;
@@ -32,7 +38,7 @@ bool check(const tok_attention* t) {
     if (t->axes && (!t->slopes || (t->tq && !t->q_pos) || (t->tk && !t->k_pos))) return false;
     const int64_t* strides[3] = {t->q_stride, t->k_stride, t->v_stride};
     for (const int64_t* s : strides)
-        if (s[0] % 8 || s[1] % 8 || s[0] < 0 || s[1] < 0) return false;
+        if (!stride_ok(s)) return false;
     return true;
 }
 
@@ -91,18 +97,17 @@ AttArgs make_args(const tok_attention& t, const Cut& c) {
     const double log2e = 1.4426950408889634;
     a.scale = t.scale;
     a.scale2 = (float)(t.scale * log2e);
-    a.cap_in = t.cap > 0.0f ? (float)(2.0 * log2e * t.scale / t.cap) : 0.0f;
+    a.cap_in = t.cap > 0.0f ? (float)((double)t.scale / t.cap) : 0.0f;
     a.cap2 = (float)(t.cap * log2e);
     return a;
 }
 
 int run(const tok_attention& t, AttPass pass, const AttArgs& a, int waves, hipStream_t stream) {
-    const bool general = t.axes > 0 || t.cap > 0.0f;
     const int wide = t.width <= 32 ? 0 : t.width <= 64 ? 1 : 2;
     static const AttLaunch launches[2][3] = {
         {att_launch_bf16_32, att_launch_bf16_64, att_launch_bf16_128},
         {att_launch_f16_32, att_launch_f16_64, att_launch_f16_128}};
-    const hipError_t e = launches[t.dtype == TOK_F16][wide](pass, a, general, waves, stream);
+    const hipError_t e = launches[t.dtype == TOK_F16][wide](pass, a, waves, stream);
     return e == hipSuccess ? VOX_OK : ssh_hip_fail(e);
 }
 
@@ -144,8 +149,7 @@ int tok_attend_grad(const tok_attention* t, const void* q, const void* k, const 
                     void* grad_k, void* grad_v, void* workspace, int64_t workspace_bytes,
                     hipStream_t stream) {
     if (!check(t)) return VOX_EINVAL;
-    if (t->g_stride[0] % 8 || t->g_stride[1] % 8 || t->g_stride[0] < 0 || t->g_stride[1] < 0)
-        return VOX_EINVAL;
+    if (!stride_ok(t->g_stride)) return VOX_EINVAL;
     if (t->tq == 0 && t->tk == 0) return VOX_OK;
     if (t->tq && (!q || !out || !lse || !grad_out || !grad_q)) return VOX_EINVAL;
     if (t->tk && (!k || !v || !grad_k || !grad_v)) return VOX_EINVAL;

@@ -182,50 +182,90 @@ __device__ __forceinline__ uint2 pack_pos(const int* pos, long long st, long lon
     return r;
 }
 
-// |a - b| summed over the axes, as a float: the sums of absolute differences
-// are added to the bits of 2^23, whose last place is one.
-__device__ __forceinline__ float distance(unsigned ax, unsigned ay, unsigned bx, unsigned by,
-                                          bool three) {
-    unsigned d = __builtin_amdgcn_sad_u16(ax, bx, 0x4b000000u);
-    if (three) d = __builtin_amdgcn_sad_u16(ay, by, d);
-    return __uint_as_float(d) - 8388608.0f;
+// |a - b| summed over the axes.
+template <int AX>
+__device__ __forceinline__ float distance(uint2 p, unsigned x, unsigned y) {
+    unsigned d = __builtin_amdgcn_sad_u16(p.x, x, 0u);
+    if (AX == 3) d = __builtin_amdgcn_sad_u16(p.y, y, d);
+    return (float)d;
 }
 
-// cap tanh(z / cap) in base 2, from e = exp(2 z / cap): tanh = 1 - 2 / (e + 1)
-// (e = inf and e = 0 give 1 and -1).
-__device__ __forceinline__ float bend(float s, float cap_in) {
-    return __builtin_amdgcn_rcpf(exp2_(s * cap_in) + 1.0f);
+// tanh(u), u = score / cap, for a block's scores at once: where all are small,
+// u times a polynomial in u^2 (the minimax one of relative error 1.3e-8 on
+// |u| <= 0.5, found by the exchange method) in 6 instructions a score; else
+// 1 - 2 / (exp(2 u) + 1), right at both ends (exp = 0 and inf), whose two
+// transcendentals alone take the time of 8.
+constexpr float kSmallTanh = 0.5f;
+
+__device__ __forceinline__ float tanh_small(float u) {
+    const float w = u * u;
+    float r = __builtin_fmaf(0.017135007f, w, -0.052986074f);
+    r = __builtin_fmaf(r, w, 0.13324779f);
+    r = __builtin_fmaf(r, w, -0.33333069f);
+    return __builtin_fmaf(u * w, r, u);
 }
 
-// A tile of ROWS rows of k or v (or q, grad_out) on its way from HBM to LDS:
-// NT threads, each some 16-byte chunks, held in registers while the tile
-// before it is worked on.
-template <int ROWS, int NT>
-struct Stage {
-    static constexpr int kPer = (ROWS * kChunks + NT - 1) / NT;
-    static constexpr bool kEven = ROWS * kChunks % NT == 0;
-    uint4 x[kPer];
-
-    // row(r): element offset of tile row r (always a row that may be read)
-    template <typename Row>
-    __device__ __forceinline__ void load(const void* base, int width, Row row) {
+__device__ __forceinline__ void cap_block(const AttArgs& a, acc16& s) {
+    float far = 0.0f;
 #pragma unroll
-        for (int p = 0; p < kPer; ++p) {
-            const int at = p * NT + threadIdx.x;
-            const int r = at / kChunks, c = at % kChunks;
-            x[p] = make_uint4(0, 0, 0, 0);
-            if (c * 8 < width && (kEven || r < ROWS)) x[p] = *(const uint4*)((const elem*)base + row(r) + c * 8);
-        }
+    for (int r = 0; r < 16; ++r) s[r] *= a.cap_in;
+#pragma unroll
+    for (int r = 0; r < 16; ++r) far = fmaxf(far, fabsf(s[r]));
+    if (!__any(!(far <= kSmallTanh))) {
+#pragma unroll
+        for (int r = 0; r < 16; ++r) s[r] = tanh_small(s[r]);
+    } else {
+#pragma unroll
+        for (int r = 0; r < 16; ++r)
+            s[r] = __builtin_fmaf(
+                -2.0f, __builtin_amdgcn_rcpf(exp2_(s[r] * (2.0f * kLog2e)) + 1.0f), 1.0f);
     }
-    __device__ __forceinline__ void store(uint4* tile) const {
+}
+
+// A tile of ROWS rows of k or v (or q, grad_out), brought from HBM into LDS
+// without passing registers: a wavefront's load puts 64 consecutive 16-byte
+// chunks of LDS, so the XOR of swz() is on the side of the source. Rows past
+// the last are copies of it; chunks past the width keep the zeros of clear().
+// load() only starts the loads: landed() and a barrier come before a read.
+template <int ROWS, int NT>
+struct Tile {
+    static constexpr int kPer = (ROWS * kChunks + NT - 1) / NT;
+    static_assert(ROWS * kChunks % 64 == 0 && NT % kChunks == 0, "whole wavefronts and rows");
+
+    static __device__ __forceinline__ void clear(uint4* tile, int width) {
+        if (width == W) return;
+        for (int p = threadIdx.x; p < ROWS * kChunks; p += NT) tile[p] = make_uint4(0, 0, 0, 0);
+    }
+    // rows: that exist from `base` on (>= 1), stride in elements
+    static __device__ __forceinline__ void load(uint4* tile, const elem* base, long long stride,
+                                                int rows, int width) {
+        typedef const __attribute__((address_space(1))) void* source;
+        typedef __attribute__((address_space(3))) void* target;
+        const int r0 = threadIdx.x / kChunks, at = threadIdx.x % kChunks;
+        const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+        const bool whole = rows >= ROWS;
 #pragma unroll
         for (int p = 0; p < kPer; ++p) {
-            const int at = p * NT + threadIdx.x;
-            const int r = at / kChunks, c = at % kChunks;
-            if (kEven || r < ROWS) tile[r * kChunks + (c ^ swz(r))] = x[p];
+            const int r = p * (NT / kChunks) + r0;
+            const int c = at ^ swz(r);
+            // offsets inside a tile fit 32 bits: the host bounds the stride
+            const unsigned off = (unsigned)(whole ? r : min(r, rows - 1)) * (unsigned)(2 * stride) + 16u * c;
+            uint4* to = tile + p * NT + wave * 64;
+            if (p * NT + wave * 64 < ROWS * kChunks && (width == W || c * 8 < width))
+                __builtin_amdgcn_global_load_lds((source)((const char*)base + off), (target)to, 16, 0, 0);
         }
     }
 };
+
+// The lane again, as a value the compiler computes LDS addresses from where
+// they are used: kept over the loop, a width of 128 has more of them than
+// registers.
+__device__ __forceinline__ int fresh(int lane) {
+    if (W == 128) asm volatile("" : "+v"(lane));
+    return lane;
+}
+
+__device__ __forceinline__ void landed() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
 
 __device__ __forceinline__ vec8 load_chunk(const elem* row, int c, int width) {
     return c * 8 < width ? *(const vec8*)(row + c * 8) : zero8();
@@ -241,7 +281,7 @@ struct Row {
     uint2 pos;
 };
 
-template <bool GENERAL>
+template <int AX>
 __device__ __forceinline__ Row get_row(const AttArgs& a, const Range& d, int kvh, int r) {
     Row w;
     const int rows = d.lq * a.group;
@@ -253,56 +293,42 @@ __device__ __forceinline__ Row get_row(const AttArgs& a, const Range& d, int kvh
     w.limit = w.real ? key_limit(a, d, w.i) : 0;
     w.slope2 = 0.0f;
     w.pos = make_uint2(0, 0);
-    if (GENERAL && a.axes) {
+    if (AX) {
         w.slope2 = a.slopes[w.head] * kLog2e;
         w.pos = pack_pos(a.q_pos, a.qp_st, a.qp_sa, a.axes, w.token);
     }
     return w;
 }
 
-// Base-2 scores of a 32-key block in place. GENERAL: cap and distance.
-// kpx, kpy: the block's packed key positions. bent (or null) receives 1 / (e + 1).
-template <bool GENERAL, bool KEEP>
+// Base-2 scores less `sub` of a 32-key block, in place. AX: 0 no bias, 2 one or
+// two axes, 3 three. kpx, kpy: the block's packed key positions. CAP: bent
+// receives tanh(score / cap).
+template <int AX, bool CAP>
 __device__ __forceinline__ void scores(const AttArgs& a, acc16& s, acc16& bent, const Row& row,
-                                       const unsigned* kpx, const unsigned* kpy, int half) {
-    if (!GENERAL) {
+                                       float sub, const unsigned* kpx, const unsigned* kpy, int half) {
+    acc16 t;
+    if (AX) {
 #pragma unroll
-        for (int r = 0; r < 16; ++r) s[r] *= a.scale2;
-        return;
-    }
-    if (a.cap2 > 0.0f) {
-#pragma unroll
-        for (int r = 0; r < 16; ++r) {
-            const float b = bend(s[r], a.cap_in);
-            if (KEEP) bent[r] = b;
-            s[r] = __builtin_fmaf(-2.0f * a.cap2, b, a.cap2);
+        for (int q = 0; q < 4; ++q) {
+            const uint4 x = *(const uint4*)(kpx + 8 * q + 4 * half);
+            uint4 y = make_uint4(0, 0, 0, 0);
+            if (AX == 3) y = *(const uint4*)(kpy + 8 * q + 4 * half);
+            t[4 * q + 0] = __builtin_fmaf(-row.slope2, distance<AX>(row.pos, x.x, y.x), -sub);
+            t[4 * q + 1] = __builtin_fmaf(-row.slope2, distance<AX>(row.pos, x.y, y.y), -sub);
+            t[4 * q + 2] = __builtin_fmaf(-row.slope2, distance<AX>(row.pos, x.z, y.z), -sub);
+            t[4 * q + 3] = __builtin_fmaf(-row.slope2, distance<AX>(row.pos, x.w, y.w), -sub);
         }
     } else {
 #pragma unroll
-        for (int r = 0; r < 16; ++r) s[r] *= a.scale2;
+        for (int r = 0; r < 16; ++r) t[r] = -sub;
     }
-    if (a.axes) {
-        if (a.axes < 3) {
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const uint4 x = *(const uint4*)(kpx + 8 * q + 4 * half);
-                s[4 * q + 0] = __builtin_fmaf(-row.slope2, distance(row.pos.x, 0, x.x, 0, false), s[4 * q + 0]);
-                s[4 * q + 1] = __builtin_fmaf(-row.slope2, distance(row.pos.x, 0, x.y, 0, false), s[4 * q + 1]);
-                s[4 * q + 2] = __builtin_fmaf(-row.slope2, distance(row.pos.x, 0, x.z, 0, false), s[4 * q + 2]);
-                s[4 * q + 3] = __builtin_fmaf(-row.slope2, distance(row.pos.x, 0, x.w, 0, false), s[4 * q + 3]);
-            }
-        } else {
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const uint4 x = *(const uint4*)(kpx + 8 * q + 4 * half);
-                const uint4 y = *(const uint4*)(kpy + 8 * q + 4 * half);
-                s[4 * q + 0] = __builtin_fmaf(-row.slope2, distance(row.pos.x, row.pos.y, x.x, y.x, true), s[4 * q + 0]);
-                s[4 * q + 1] = __builtin_fmaf(-row.slope2, distance(row.pos.x, row.pos.y, x.y, y.y, true), s[4 * q + 1]);
-                s[4 * q + 2] = __builtin_fmaf(-row.slope2, distance(row.pos.x, row.pos.y, x.z, y.z, true), s[4 * q + 2]);
-                s[4 * q + 3] = __builtin_fmaf(-row.slope2, distance(row.pos.x, row.pos.y, x.w, y.w, true), s[4 * q + 3]);
-            }
-        }
+    if (CAP) {
+        cap_block(a, s);
+        bent = s;
     }
+    const float by = CAP ? a.cap2 : a.scale2;
+#pragma unroll
+    for (int r = 0; r < 16; ++r) s[r] = __builtin_fmaf(s[r], by, t[r]);
 }
 
 // Scores of keys from `limit` on become -inf; key0: the block's first key.
@@ -322,14 +348,18 @@ __device__ __forceinline__ long long xcd_block(long long bid, long long n) {
 }
 
 // ---- forward ---------------------------------------------------------------
+// Scores are computed less the running maximum m of the tiles before, so the
+// largest of a tile says how far m lags; up to 2^kRescale nothing is rescaled.
+// Key tiles are loaded one ahead into the other half of LDS.
 
-template <bool GENERAL, int NW, int BN>
+template <int AX, bool CAP, int NW, int BN>
 __global__ __launch_bounds__(64 * NW, NW == 4 ? 2 : 1) void k_att_forward(AttArgs a) {
     constexpr int NT = 64 * NW;
     constexpr int NB = BN / 32;
-    __shared__ __align__(16) uint4 tk[BN * kChunks];
-    __shared__ __align__(16) uint4 tv[BN * kChunks];
-    __shared__ __align__(16) unsigned kpx[GENERAL ? BN : 4], kpy[GENERAL ? BN : 4];
+    typedef Tile<BN, NT> KeyTile;
+    __shared__ __align__(16) uint4 tk[2][BN * kChunks];
+    __shared__ __align__(16) uint4 tv[2][BN * kChunks];
+    __shared__ __align__(16) unsigned kpx[2][AX ? BN : 4], kpy[2][AX == 3 ? BN : 4];
 
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, half = lane >> 5;
     long long id = xcd_block(blockIdx.x, gridDim.x);
@@ -345,7 +375,7 @@ __global__ __launch_bounds__(64 * NW, NW == 4 ? 2 : 1) void k_att_forward(AttArg
     const long long row0l = (long long)(tile - first) * kAttRows * NW;
     if (row0l < 0 || row0l >= rows) return;
     const int row0 = (int)row0l;
-    const Row row = get_row<GENERAL>(a, d, kvh, row0 + wave * kAttRows + (lane & 31));
+    const Row row = get_row<AX>(a, d, kvh, row0 + wave * kAttRows + (lane & 31));
 
     // the block's keys: up to its last row's limit, this split's share of the tiles
     const int last = min(row0 + kAttRows * NW, rows) - 1;
@@ -354,6 +384,23 @@ __global__ __launch_bounds__(64 * NW, NW == 4 ? 2 : 1) void k_att_forward(AttArg
     const int t1 = (int)((long long)tiles * (split + 1) / a.nsplit);
     // keys every row of the block sees (rows past the end hold nothing that is kept)
     const int common = key_limit(a, d, row0 / a.group);
+
+    const elem* k0 = (const elem*)a.k + (long long)kvh * a.k_sh + d.klo * a.k_st;
+    const elem* v0 = (const elem*)a.v + (long long)kvh * a.v_sh + d.klo * a.v_st;
+    uint2 sp = make_uint2(0, 0);
+    auto fetch = [&](int t) {
+        KeyTile::load(tk[t & 1], k0 + (long long)t * BN * a.k_st, a.k_st, d.lk - t * BN, a.width);
+        KeyTile::load(tv[t & 1], v0 + (long long)t * BN * a.v_st, a.v_st, d.lk - t * BN, a.width);
+        if (AX && threadIdx.x < BN)
+            sp = pack_pos(a.k_pos, a.kp_st, a.kp_sa, a.axes,
+                          d.klo + min(t * BN + (int)threadIdx.x, d.lk - 1));
+    };
+    for (int b = 0; b < 2; ++b) {
+        KeyTile::clear(tk[b], a.width);
+        KeyTile::clear(tv[b], a.width);
+    }
+    if (a.width < W) __syncthreads();
+    if (t0 < t1) fetch(t0);
 
     vec8 qf[kSteps];
     const elem* qrow = (const elem*)a.q + row.token * a.q_st + row.head * a.q_sh;
@@ -365,32 +412,16 @@ __global__ __launch_bounds__(64 * NW, NW == 4 ? 2 : 1) void k_att_forward(AttArg
     for (int b = 0; b < kBlocks; ++b)
 #pragma unroll
         for (int r = 0; r < 16; ++r) o[b][r] = 0.0f;
-    float m = kLowest, l = 0.0f;
+    float m = 0.0f, l = 0.0f;
 
-    Stage<BN, NT> sk, sv;
-    uint2 sp = make_uint2(0, 0);
-    auto fetch = [&](int t) {
-        const long long k0 = (long long)kvh * a.k_sh, v0 = (long long)kvh * a.v_sh;
-        sk.load(a.k, a.width, [&](int r) {
-            return k0 + (long long)(d.klo + min(t * BN + r, d.lk - 1)) * a.k_st;
-        });
-        sv.load(a.v, a.width, [&](int r) {
-            return v0 + (long long)(d.klo + min(t * BN + r, d.lk - 1)) * a.v_st;
-        });
-        if (GENERAL && a.axes && threadIdx.x < BN)
-            sp = pack_pos(a.k_pos, a.kp_st, a.kp_sa, a.axes,
-                          d.klo + min(t * BN + (int)threadIdx.x, d.lk - 1));
-    };
-    if (t0 < t1) fetch(t0);
     for (int t = t0; t < t1; ++t) {
-        __syncthreads();
-        sk.store(tk);
-        sv.store(tv);
-        if (GENERAL && threadIdx.x < BN) {
-            kpx[threadIdx.x] = sp.x;
-            kpy[threadIdx.x] = sp.y;
+        const int buf = t & 1;
+        if (AX && threadIdx.x < BN) {
+            kpx[buf][threadIdx.x] = sp.x;
+            if (AX == 3) kpy[buf][threadIdx.x] = sp.y;
         }
-        __syncthreads();
+        landed();
+        __syncthreads();  // this tile is there, and all are done with the one before
         if (t + 1 < t1) fetch(t + 1);
 
         acc16 s[NB];
@@ -400,9 +431,13 @@ __global__ __launch_bounds__(64 * NW, NW == 4 ? 2 : 1) void k_att_forward(AttArg
             for (int r = 0; r < 16; ++r) s[nb][r] = 0.0f;
 #pragma unroll
             for (int k = 0; k < kSteps; ++k)
-                s[nb] = mma(lds_chunk(tk, 32 * nb + (lane & 31), 2 * k + half), qf[k], s[nb]);
+                s[nb] = mma(lds_chunk(tk[buf], 32 * nb + (lane & 31), 2 * k + half), qf[k], s[nb]);
+        }
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) {
             acc16 none;
-            scores<GENERAL, false>(a, s[nb], none, row, kpx + 32 * nb, kpy + 32 * nb, half);
+            scores<AX, CAP>(a, s[nb], none, row, m, kpx[buf] + (AX ? 32 * nb : 0),
+                            kpy[buf] + (AX == 3 ? 32 * nb : 0), half);
         }
         if ((t + 1) * BN > common) {
 #pragma unroll
@@ -413,22 +448,30 @@ __global__ __launch_bounds__(64 * NW, NW == 4 ? 2 : 1) void k_att_forward(AttArg
         for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
             for (int r = 0; r < 16; ++r) top = fmaxf(top, s[nb][r]);
-        top = fmaxf(top, other_half(top));
-        if (__any(top > m + kRescale)) {
-            const float mn = fmaxf(m, top);
-            const float w = exp2_(m - mn);
-            m = mn;
-            l *= w;
+        if (t == t0 || __any(top > kRescale)) {
+            top = fmaxf(top, other_half(top));
+            // a row's visible keys are its document's first ones: it sees some
+            // in the first tile or none at all
+            const float up = t == t0 ? (top > -__builtin_inff() ? top : 0.0f) : fmaxf(top, 0.0f);
+            m += up;
+            if (t > t0) {
+                const float w = exp2_(-up);
+                l *= w;
 #pragma unroll
-            for (int b = 0; b < kBlocks; ++b)
+                for (int b = 0; b < kBlocks; ++b)
 #pragma unroll
-                for (int r = 0; r < 16; ++r) o[b][r] *= w;
+                    for (int r = 0; r < 16; ++r) o[b][r] *= w;
+            }
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) s[nb][r] -= up;
         }
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) {
 #pragma unroll
             for (int r = 0; r < 16; ++r) {
-                s[nb][r] = exp2_(s[nb][r] - m);
+                s[nb][r] = exp2_(s[nb][r]);
                 l += s[nb][r];
             }
 #pragma unroll
@@ -436,12 +479,13 @@ __global__ __launch_bounds__(64 * NW, NW == 4 ? 2 : 1) void k_att_forward(AttArg
                 const vec8 p = round8(s[nb], c);
 #pragma unroll
                 for (int b = 0; b < kBlocks; ++b)
-                    o[b] = mma(lds_transposed(tv, 32 * nb + 16 * c, b, lane), p, o[b]);
+                    o[b] = mma(lds_transposed(tv[buf], 32 * nb + 16 * c, b, lane), p, o[b]);
             }
         }
     }
     l += other_half(l);
     if (!row.real) return;
+    const bool none = l == 0.0f;  // sees no key: zeros, whatever the tiles held
     const long long at = row.token * a.heads + row.head;
     if (a.nsplit > 1) {
         const long long n = (long long)a.tq * a.heads;
@@ -452,17 +496,17 @@ __global__ __launch_bounds__(64 * NW, NW == 4 ? 2 : 1) void k_att_forward(AttArg
             for (int q = 0; q < 4; ++q) {
                 const int c = 32 * b + 8 * q + 4 * half;
                 if (c < a.width)
-                    *(float4*)(part + c) = make_float4(o[b][4 * q], o[b][4 * q + 1],
-                                                       o[b][4 * q + 2], o[b][4 * q + 3]);
+                    *(float4*)(part + c) =
+                        none ? make_float4(0, 0, 0, 0)
+                             : make_float4(o[b][4 * q], o[b][4 * q + 1], o[b][4 * q + 2], o[b][4 * q + 3]);
             }
         if (half == 0) {
-            a.part_ml[2 * ((long long)split * n + at)] = m;
+            a.part_ml[2 * ((long long)split * n + at)] = none ? kLowest : m;
             a.part_ml[2 * ((long long)split * n + at) + 1] = l;
         }
         return;
     }
     const float inv = 1.0f / l;
-    const bool none = l == 0.0f;  // sees no key: zeros, whatever the tiles held
     elem* out = (elem*)a.out + at * a.width;
 #pragma unroll
     for (int b = 0; b < kBlocks; ++b)
@@ -476,7 +520,7 @@ __global__ __launch_bounds__(64 * NW, NW == 4 ? 2 : 1) void k_att_forward(AttArg
             *(vec4*)(out + c) = x;
         }
     if (a.lse && half == 0)
-        a.lse[at] = l == 0.0f ? -__builtin_inff() : (m + __builtin_amdgcn_logf(l)) * kLn2;
+        a.lse[at] = none ? -__builtin_inff() : (m + __builtin_amdgcn_logf(l)) * kLn2;
 }
 
 // Splits of a row joined in order: one wavefront per row, lanes over the width.
@@ -521,13 +565,14 @@ __global__ __launch_bounds__(256) void k_att_join(AttArgs a) {
 // grad_q loses r P K, and grad_k and grad_v get the delta that is right in
 // 32 bits.
 
-template <bool GENERAL, int NW, int BN>
+template <int AX, bool CAP, int NW, int BN>
 __global__ __launch_bounds__(64 * NW, NW == 4 ? 2 : 1) void k_att_grad_q(AttArgs a) {
     constexpr int NT = 64 * NW;
     constexpr int NB = BN / 32;
-    __shared__ __align__(16) uint4 tk[BN * kChunks];
-    __shared__ __align__(16) uint4 tv[BN * kChunks];
-    __shared__ __align__(16) unsigned kpx[GENERAL ? BN : 4], kpy[GENERAL ? BN : 4];
+    typedef Tile<BN, NT> KeyTile;
+    __shared__ __align__(16) uint4 tk[2][BN * kChunks];
+    __shared__ __align__(16) uint4 tv[2][BN * kChunks];
+    __shared__ __align__(16) unsigned kpx[2][AX ? BN : 4], kpy[2][AX == 3 ? BN : 4];
 
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, half = lane >> 5;
     const long long id = xcd_block(blockIdx.x, gridDim.x);
@@ -540,10 +585,27 @@ __global__ __launch_bounds__(64 * NW, NW == 4 ? 2 : 1) void k_att_grad_q(AttArgs
     const long long row0l = (long long)(tile - first) * kAttRows * NW;
     if (row0l < 0 || row0l >= rows) return;
     const int row0 = (int)row0l;
-    const Row row = get_row<GENERAL>(a, d, kvh, row0 + wave * kAttRows + (lane & 31));
+    const Row row = get_row<AX>(a, d, kvh, row0 + wave * kAttRows + (lane & 31));
     const int last = min(row0 + kAttRows * NW, rows) - 1;
     const int t1 = (key_limit(a, d, last / a.group) + BN - 1) / BN;
     const int common = row0 + kAttRows * NW <= rows ? key_limit(a, d, row0 / a.group) : 0;
+
+    const elem* k0 = (const elem*)a.k + (long long)kvh * a.k_sh + d.klo * a.k_st;
+    const elem* v0 = (const elem*)a.v + (long long)kvh * a.v_sh + d.klo * a.v_st;
+    uint2 sp = make_uint2(0, 0);
+    auto fetch = [&](int t) {
+        KeyTile::load(tk[t & 1], k0 + (long long)t * BN * a.k_st, a.k_st, d.lk - t * BN, a.width);
+        KeyTile::load(tv[t & 1], v0 + (long long)t * BN * a.v_st, a.v_st, d.lk - t * BN, a.width);
+        if (AX && threadIdx.x < BN)
+            sp = pack_pos(a.k_pos, a.kp_st, a.kp_sa, a.axes,
+                          d.klo + min(t * BN + (int)threadIdx.x, d.lk - 1));
+    };
+    for (int b = 0; b < 2; ++b) {
+        KeyTile::clear(tk[b], a.width);
+        KeyTile::clear(tv[b], a.width);
+    }
+    if (a.width < W) __syncthreads();
+    if (t1 > 0) fetch(0);
 
     const long long at = row.token * a.heads + row.head;
     vec8 qf[kSteps], gf[kSteps];
@@ -569,45 +631,31 @@ __global__ __launch_bounds__(64 * NW, NW == 4 ? 2 : 1) void k_att_grad_q(AttArgs
 #pragma unroll
         for (int r = 0; r < 16; ++r) o[b][r] = pk[b][r] = 0.0f;
 
-    Stage<BN, NT> sk, sv;
-    uint2 sp = make_uint2(0, 0);
-    auto fetch = [&](int t) {
-        const long long k0 = (long long)kvh * a.k_sh, v0 = (long long)kvh * a.v_sh;
-        sk.load(a.k, a.width, [&](int r) {
-            return k0 + (long long)(d.klo + min(t * BN + r, d.lk - 1)) * a.k_st;
-        });
-        sv.load(a.v, a.width, [&](int r) {
-            return v0 + (long long)(d.klo + min(t * BN + r, d.lk - 1)) * a.v_st;
-        });
-        if (GENERAL && a.axes && threadIdx.x < BN)
-            sp = pack_pos(a.k_pos, a.kp_st, a.kp_sa, a.axes,
-                          d.klo + min(t * BN + (int)threadIdx.x, d.lk - 1));
-    };
-    if (t1 > 0) fetch(0);
     for (int t = 0; t < t1; ++t) {
-        __syncthreads();
-        sk.store(tk);
-        sv.store(tv);
-        if (GENERAL && threadIdx.x < BN) {
-            kpx[threadIdx.x] = sp.x;
-            kpy[threadIdx.x] = sp.y;
+        const int buf = t & 1;
+        if (AX && threadIdx.x < BN) {
+            kpx[buf][threadIdx.x] = sp.x;
+            if (AX == 3) kpy[buf][threadIdx.x] = sp.y;
         }
+        landed();
         __syncthreads();
         if (t + 1 < t1) fetch(t + 1);
         const bool masked = (t + 1) * BN > common;
+        const int ln = fresh(lane);
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) {
             acc16 s, dp, bent;
 #pragma unroll
-            for (int r = 0; r < 16; ++r) s[r] = dp[r] = 0.0f;
+            for (int r = 0; r < 16; ++r) s[r] = 0.0f, dp[r] = -delta;
 #pragma unroll
             for (int k = 0; k < kSteps; ++k) {
-                s = mma(lds_chunk(tk, 32 * nb + (lane & 31), 2 * k + half), qf[k], s);
-                dp = mma(lds_chunk(tv, 32 * nb + (lane & 31), 2 * k + half), gf[k], dp);
+                s = mma(lds_chunk(tk[buf], 32 * nb + (ln & 31), 2 * k + (ln >> 5)), qf[k], s);
+                dp = mma(lds_chunk(tv[buf], 32 * nb + (ln & 31), 2 * k + (ln >> 5)), gf[k], dp);
             }
-            scores<GENERAL, true>(a, s, bent, row, kpx + 32 * nb, kpy + 32 * nb, half);
+            scores<AX, CAP>(a, s, bent, row, lse2, kpx[buf] + (AX ? 32 * nb : 0),
+                            kpy[buf] + (AX == 3 ? 32 * nb : 0), half);
 #pragma unroll
-            for (int r = 0; r < 16; ++r) s[r] = exp2_(s[r] - lse2);
+            for (int r = 0; r < 16; ++r) s[r] = exp2_(s[r]);
             if (masked) {
                 const int left = row.limit - (t * BN + 32 * nb) - 4 * half;
 #pragma unroll
@@ -616,14 +664,13 @@ __global__ __launch_bounds__(64 * NW, NW == 4 ? 2 : 1) void k_att_grad_q(AttArgs
             }
 #pragma unroll
             for (int r = 0; r < 16; ++r) {
-                dp[r] = s[r] * (dp[r] - delta);
+                dp[r] *= s[r];
                 rest += dp[r];
             }
-            if (GENERAL && a.cap2 > 0.0f) {
-                // 1 - tanh^2 = 4 b (1 - b) with b = 1 / (e + 1)
+            if (CAP) {
 #pragma unroll
                 for (int r = 0; r < 16; ++r) {
-                    const float flat = 4.0f * bent[r] * (1.0f - bent[r]);
+                    const float flat = __builtin_fmaf(-bent[r], bent[r], 1.0f);
                     dp[r] *= flat;
                     s[r] *= flat;
                 }
@@ -633,7 +680,7 @@ __global__ __launch_bounds__(64 * NW, NW == 4 ? 2 : 1) void k_att_grad_q(AttArgs
                 const vec8 ds = round8(dp, c), p = round8(s, c);
 #pragma unroll
                 for (int b = 0; b < kBlocks; ++b) {
-                    const vec8 kt = lds_transposed(tk, 32 * nb + 16 * c, b, lane);
+                    const vec8 kt = lds_transposed(tk[buf], 32 * nb + 16 * c, b, ln);
                     o[b] = mma(kt, ds, o[b]);
                     pk[b] = mma(kt, p, pk[b]);
                 }
@@ -653,26 +700,28 @@ __global__ __launch_bounds__(64 * NW, NW == 4 ? 2 : 1) void k_att_grad_q(AttArgs
             if (c >= a.width) continue;
             vec4 x;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) x[j] = none ? (elem)0.0f
+            for (int j = 0; j < 4; ++j)
+                x[j] = none ? (elem)0.0f
                             : (elem)(__builtin_fmaf(-rest, pk[b][4 * q + j], o[b][4 * q + j]) * (a.scale * kUnlift));
             *(vec4*)(out + c) = x;
         }
 }
 
 // ---- grad_k and grad_v -------------------------------------------------------
-// A wavefront owns 32 keys and runs over the document's query rows, all heads
-// of the group: S = Q K^T and dP = grad_out V^T with a lane's column one key,
-// so P and dS are operand B of grad_v^T = grad_out^T P and grad_k^T = Q^T dS.
+// A wavefront owns 32 keys and runs over the document's queries, one head of
+// the group after another: S = Q K^T and dP = grad_out V^T with a lane's column
+// one key, so P and dS are operand B of grad_v^T = grad_out^T P and
+// grad_k^T = Q^T dS.
 
-template <bool GENERAL, int NW>
-__global__ __launch_bounds__(64 * NW, 1) void k_att_grad_kv(AttArgs a) {
+template <int AX, bool CAP, int NW>
+__global__ __launch_bounds__(64 * NW, NW == 4 && W < 128 ? 2 : 1) void k_att_grad_kv(AttArgs a) {
     constexpr int NT = 64 * NW;
     constexpr int BM = 32;
-    __shared__ __align__(16) uint4 tq[BM * kChunks];
-    __shared__ __align__(16) uint4 tg[BM * kChunks];
-    __shared__ __align__(16) float rlse[BM], rdelta[BM], rslope[BM];
-    __shared__ __align__(16) int rlimit[BM];
-    __shared__ __align__(16) unsigned rpx[BM], rpy[BM];
+    typedef Tile<BM, NT> RowTile;
+    __shared__ __align__(16) uint4 tq[2][BM * kChunks];
+    __shared__ __align__(16) uint4 tg[2][BM * kChunks];
+    __shared__ __align__(16) float rlse[2][BM], rdelta[2][BM];
+    __shared__ __align__(16) unsigned rpx[2][BM], rpy[2][BM];
 
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, half = lane >> 5;
     const long long id = xcd_block(blockIdx.x, gridDim.x);
@@ -687,8 +736,35 @@ __global__ __launch_bounds__(64 * NW, 1) void k_att_grad_kv(AttArgs a) {
     const int key0 = (int)key0l;
     const int key = key0 + wave * kAttRows + (lane & 31);
     const long long token = d.klo + min(key, lk - 1);
-    // keys of no document are read by nobody: no rows
-    const int rows = d.lk > 0 ? d.lq * a.group : 0;
+    if (d.lk == 0) d.lq = 0;  // keys of no document are read by nobody: no rows
+
+    // the first query that sees the block's first key (limits grow with the query)
+    int i0 = 0;
+    if (a.mask && d.prefix <= key0) i0 = max(0, key0 - (d.lk - d.lq));
+    const int first_tile = i0 / BM, per_head = max(0, (d.lq + BM - 1) / BM - first_tile);
+    const int t1 = per_head * a.group;
+
+    float s_lse = 0.0f, s_delta = 0.0f;
+    uint2 s_pos = make_uint2(0, 0);
+    auto fetch = [&](int t) {
+        const int g = t / per_head, i = (first_tile + t % per_head) * BM, head = kvh * a.group + g;
+        RowTile::load(tq[t & 1], (const elem*)a.q + (long long)head * a.q_sh + (long long)(d.qlo + i) * a.q_st,
+                      a.q_st, d.lq - i, a.width);
+        RowTile::load(tg[t & 1], (const elem*)a.g + (long long)head * a.g_sh + (long long)(d.qlo + i) * a.g_st,
+                      a.g_st, d.lq - i, a.width);
+        if (threadIdx.x < BM) {
+            const long long q = d.qlo + min(i + (int)threadIdx.x, d.lq - 1);
+            s_lse = a.lse[q * a.heads + head] * kLog2e - kLift;
+            s_delta = a.delta[q * a.heads + head];
+            if (AX) s_pos = pack_pos(a.q_pos, a.qp_st, a.qp_sa, a.axes, q);
+        }
+    };
+    for (int b = 0; b < 2; ++b) {
+        RowTile::clear(tq[b], a.width);
+        RowTile::clear(tg[b], a.width);
+    }
+    if (a.width < W) __syncthreads();
+    if (t1 > 0) fetch(0);
 
     vec8 kf[kSteps], vf[kSteps];
     const elem* krow = (const elem*)a.k + token * a.k_st + kvh * a.k_sh;
@@ -699,7 +775,7 @@ __global__ __launch_bounds__(64 * NW, 1) void k_att_grad_kv(AttArgs a) {
         vf[k] = load_chunk(vrow, 2 * k + half, a.width);
     }
     uint2 kpos = make_uint2(0, 0);
-    if (GENERAL && a.axes && rows) kpos = pack_pos(a.k_pos, a.kp_st, a.kp_sa, a.axes, token);
+    if (AX && t1 > 0) kpos = pack_pos(a.k_pos, a.kp_st, a.kp_sa, a.axes, token);
 
     acc16 gk[kBlocks], gv[kBlocks];
 #pragma unroll
@@ -707,103 +783,65 @@ __global__ __launch_bounds__(64 * NW, 1) void k_att_grad_kv(AttArgs a) {
 #pragma unroll
         for (int r = 0; r < 16; ++r) gk[b][r] = gv[b][r] = 0.0f;
 
-    // the first query that sees the block's first key (limits grow with the query)
-    int i0 = 0;
-    if (a.mask && d.prefix <= key0) i0 = max(0, key0 - (d.lk - d.lq));
-    const int t0 = i0 * a.group / BM, t1 = (rows + BM - 1) / BM;
-
-    Stage<BM, NT> sq, sg;
-    float s_lse = 0.0f, s_delta = 0.0f, s_slope = 0.0f;
-    int s_limit = 0;
-    uint2 s_pos = make_uint2(0, 0);
-    auto fetch = [&](int t) {
-        sq.load(a.q, a.width, [&](int r) {
-            const int rr = min(t * BM + r, rows - 1);
-            return (long long)(d.qlo + rr / a.group) * a.q_st +
-                   (long long)(kvh * a.group + rr % a.group) * a.q_sh;
-        });
-        sg.load(a.g, a.width, [&](int r) {
-            const int rr = min(t * BM + r, rows - 1);
-            return (long long)(d.qlo + rr / a.group) * a.g_st +
-                   (long long)(kvh * a.group + rr % a.group) * a.g_sh;
-        });
+    int g = 0, i = first_tile * BM;
+    for (int t = 0; t < t1; ++t) {
+        const int buf = t & 1;
         if (threadIdx.x < BM) {
-            const Row w = get_row<GENERAL>(a, d, kvh, t * BM + threadIdx.x);
-            const long long at = w.token * a.heads + w.head;
-            s_lse = a.lse[at] * kLog2e - kLift;
-            s_delta = a.delta[at];
-            s_slope = w.slope2;
-            s_limit = w.limit;
-            s_pos = w.pos;
+            rlse[buf][threadIdx.x] = s_lse;
+            rdelta[buf][threadIdx.x] = -s_delta;
+            if (AX) rpx[buf][threadIdx.x] = s_pos.x;
+            if (AX == 3) rpy[buf][threadIdx.x] = s_pos.y;
         }
-    };
-    if (t0 < t1) fetch(t0);
-    for (int t = t0; t < t1; ++t) {
-        __syncthreads();
-        sq.store(tq);
-        sg.store(tg);
-        if (threadIdx.x < BM) {
-            rlse[threadIdx.x] = s_lse;
-            rdelta[threadIdx.x] = s_delta;
-            rlimit[threadIdx.x] = s_limit;
-            if (GENERAL) {
-                rslope[threadIdx.x] = s_slope;
-                rpx[threadIdx.x] = s_pos.x;
-                rpy[threadIdx.x] = s_pos.y;
-            }
-        }
+        landed();
         __syncthreads();
         if (t + 1 < t1) fetch(t + 1);
 
-        acc16 s, dp, bent;
+        const int ln = fresh(lane);
+        acc16 s, dp, bent, sub;
 #pragma unroll
-        for (int r = 0; r < 16; ++r) s[r] = dp[r] = 0.0f;
+        for (int r = 0; r < 16; ++r) s[r] = 0.0f;
 #pragma unroll
-        for (int k = 0; k < kSteps; ++k) {
-            s = mma(lds_chunk(tq, lane & 31, 2 * k + half), kf[k], s);
-            dp = mma(lds_chunk(tg, lane & 31, 2 * k + half), vf[k], dp);
-        }
-        if (GENERAL && a.cap2 > 0.0f) {
-#pragma unroll
-            for (int r = 0; r < 16; ++r) {
-                bent[r] = bend(s[r], a.cap_in);
-                s[r] = __builtin_fmaf(-2.0f * a.cap2, bent[r], a.cap2);
-            }
-        } else {
-#pragma unroll
-            for (int r = 0; r < 16; ++r) s[r] *= a.scale2;
-        }
-        if (GENERAL && a.axes) {
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const float4 sl = *(const float4*)(rslope + 8 * q + 4 * half);
-                const uint4 x = *(const uint4*)(rpx + 8 * q + 4 * half);
-                const uint4 y = *(const uint4*)(rpy + 8 * q + 4 * half);
-                s[4 * q + 0] = __builtin_fmaf(-sl.x, distance(kpos.x, kpos.y, x.x, y.x, true), s[4 * q + 0]);
-                s[4 * q + 1] = __builtin_fmaf(-sl.y, distance(kpos.x, kpos.y, x.y, y.y, true), s[4 * q + 1]);
-                s[4 * q + 2] = __builtin_fmaf(-sl.z, distance(kpos.x, kpos.y, x.z, y.z, true), s[4 * q + 2]);
-                s[4 * q + 3] = __builtin_fmaf(-sl.w, distance(kpos.x, kpos.y, x.w, y.w, true), s[4 * q + 3]);
-            }
-        }
-        // every row of the tile sees every key of the block?
-        const bool masked = (t + 1) * BM > rows ||
-                            key_limit(a, d, t * BM / a.group) < min(key0 + kAttRows * NW, lk);
+        for (int k = 0; k < kSteps; ++k)
+            s = mma(lds_chunk(tq[buf], ln & 31, 2 * k + (ln >> 5)), kf[k], s);
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-            const float4 ls = *(const float4*)(rlse + 8 * q + 4 * half);
-            s[4 * q + 0] = exp2_(s[4 * q + 0] - ls.x);
-            s[4 * q + 1] = exp2_(s[4 * q + 1] - ls.y);
-            s[4 * q + 2] = exp2_(s[4 * q + 2] - ls.z);
-            s[4 * q + 3] = exp2_(s[4 * q + 3] - ls.w);
+            const float4 ls = *(const float4*)(rlse[buf] + 8 * q + 4 * half);
+            sub[4 * q + 0] = -ls.x, sub[4 * q + 1] = -ls.y, sub[4 * q + 2] = -ls.z, sub[4 * q + 3] = -ls.w;
         }
-        if (masked) {
+        if (CAP) {
+            cap_block(a, s);
+            bent = s;
+        }
+        if (AX) {
+            const float slope2 = a.slopes[kvh * a.group + g] * kLog2e;
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
-                const int4 lim = *(const int4*)(rlimit + 8 * q + 4 * half);
-                if (key >= lim.x) s[4 * q + 0] = 0.0f;
-                if (key >= lim.y) s[4 * q + 1] = 0.0f;
-                if (key >= lim.z) s[4 * q + 2] = 0.0f;
-                if (key >= lim.w) s[4 * q + 3] = 0.0f;
+                const uint4 x = *(const uint4*)(rpx[buf] + 8 * q + 4 * half);
+                uint4 y = make_uint4(0, 0, 0, 0);
+                if (AX == 3) y = *(const uint4*)(rpy[buf] + 8 * q + 4 * half);
+                sub[4 * q + 0] = __builtin_fmaf(-slope2, distance<AX>(kpos, x.x, y.x), sub[4 * q + 0]);
+                sub[4 * q + 1] = __builtin_fmaf(-slope2, distance<AX>(kpos, x.y, y.y), sub[4 * q + 1]);
+                sub[4 * q + 2] = __builtin_fmaf(-slope2, distance<AX>(kpos, x.z, y.z), sub[4 * q + 2]);
+                sub[4 * q + 3] = __builtin_fmaf(-slope2, distance<AX>(kpos, x.w, y.w), sub[4 * q + 3]);
+            }
+        }
+        const float by = CAP ? a.cap2 : a.scale2;
+#pragma unroll
+        for (int r = 0; r < 16; ++r) s[r] = exp2_(__builtin_fmaf(s[r], by, sub[r]));
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const float4 de = *(const float4*)(rdelta[buf] + 8 * q + 4 * half);
+            dp[4 * q + 0] = de.x, dp[4 * q + 1] = de.y, dp[4 * q + 2] = de.z, dp[4 * q + 3] = de.w;
+        }
+#pragma unroll
+        for (int k = 0; k < kSteps; ++k)
+            dp = mma(lds_chunk(tg[buf], ln & 31, 2 * k + (ln >> 5)), vf[k], dp);
+        // every row of the tile sees every key of the block?
+        if (i + BM > d.lq || key_limit(a, d, i) < min(key0 + kAttRows * NW, lk)) {
+#pragma unroll
+            for (int r = 0; r < 16; ++r) {
+                const int q = i + 8 * (r / 4) + 4 * half + r % 4;
+                if (q >= d.lq || key >= key_limit(a, d, q)) s[r] = dp[r] = 0.0f;
             }
         }
 #pragma unroll
@@ -811,27 +849,23 @@ __global__ __launch_bounds__(64 * NW, 1) void k_att_grad_kv(AttArgs a) {
             const vec8 p = round8(s, c);
 #pragma unroll
             for (int b = 0; b < kBlocks; ++b)
-                gv[b] = mma(lds_transposed(tg, 16 * c, b, lane), p, gv[b]);
+                gv[b] = mma(lds_transposed(tg[buf], 16 * c, b, ln), p, gv[b]);
         }
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            const float4 de = *(const float4*)(rdelta + 8 * q + 4 * half);
-            dp[4 * q + 0] = s[4 * q + 0] * (dp[4 * q + 0] - de.x);
-            dp[4 * q + 1] = s[4 * q + 1] * (dp[4 * q + 1] - de.y);
-            dp[4 * q + 2] = s[4 * q + 2] * (dp[4 * q + 2] - de.z);
-            dp[4 * q + 3] = s[4 * q + 3] * (dp[4 * q + 3] - de.w);
-        }
-        if (GENERAL && a.cap2 > 0.0f) {
+        for (int r = 0; r < 16; ++r) dp[r] *= s[r];
+        if (CAP) {
 #pragma unroll
-            for (int r = 0; r < 16; ++r) dp[r] *= 4.0f * bent[r] * (1.0f - bent[r]);
+            for (int r = 0; r < 16; ++r) dp[r] *= __builtin_fmaf(-bent[r], bent[r], 1.0f);
         }
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-            const vec8 p = round8(dp, c);
+            const vec8 ds = round8(dp, c);
 #pragma unroll
             for (int b = 0; b < kBlocks; ++b)
-                gk[b] = mma(lds_transposed(tq, 16 * c, b, lane), p, gk[b]);
+                gk[b] = mma(lds_transposed(tq[buf], 16 * c, b, ln), ds, gk[b]);
         }
+        i += BM;
+        if (i >= d.lq) i = first_tile * BM, ++g;
     }
     if (key >= lk) return;
     const long long at = token * a.kv_heads + kvh;
@@ -854,15 +888,16 @@ __global__ __launch_bounds__(64 * NW, 1) void k_att_grad_kv(AttArgs a) {
         }
 }
 
-template <bool GENERAL, int NW>
+template <int AX, bool CAP, int NW>
 hipError_t launch(AttPass pass, const AttArgs& a, hipStream_t stream) {
-    constexpr int BN = NW == 4 ? 64 : 32;
+    // keys of a tile: 64 where two tiles of k and v, twice, leave LDS for two blocks
+    constexpr int BN = NW == 4 && W <= 64 ? 64 : 32;
     const dim3 block(64 * NW);
     const long long blocks = (long long)a.tiles * a.kv_heads * (pass == kAttForward ? a.nsplit : 1);
     if (blocks <= 0 || blocks > 0x7fffffffll) return hipErrorInvalidValue;
     const dim3 grid((unsigned)blocks);
     if (pass == kAttForward) {
-        k_att_forward<GENERAL, NW, BN><<<grid, block, 0, stream>>>(a);
+        k_att_forward<AX, CAP, NW, BN><<<grid, block, 0, stream>>>(a);
         if (a.nsplit > 1) {
             const hipError_t e = hipGetLastError();
             if (e != hipSuccess) return e;
@@ -870,11 +905,16 @@ hipError_t launch(AttPass pass, const AttArgs& a, hipStream_t stream) {
             k_att_join<<<dim3((unsigned)((n + 3) / 4)), dim3(256), 0, stream>>>(a);
         }
     } else if (pass == kAttGradQ) {
-        k_att_grad_q<GENERAL, NW, BN><<<grid, block, 0, stream>>>(a);
+        k_att_grad_q<AX, CAP, NW, BN><<<grid, block, 0, stream>>>(a);
     } else {
-        k_att_grad_kv<GENERAL, NW><<<grid, block, 0, stream>>>(a);
+        k_att_grad_kv<AX, CAP, NW><<<grid, block, 0, stream>>>(a);
     }
     return hipGetLastError();
+}
+
+template <int AX, bool CAP>
+hipError_t launch_waves(AttPass pass, const AttArgs& a, int waves, hipStream_t stream) {
+    return waves == 4 ? launch<AX, CAP, 4>(pass, a, stream) : launch<AX, CAP, 1>(pass, a, stream);
 }
 
 }  // namespace
@@ -887,10 +927,15 @@ hipError_t launch(AttPass pass, const AttArgs& a, hipStream_t stream) {
 #define ATT_NAME ATT_JOIN(bf16, ATT_WIDTH)
 #endif
 
-__attribute__((visibility("hidden"))) hipError_t ATT_NAME(AttPass pass, const AttArgs& a,
-                                                          bool general, int waves,
+__attribute__((visibility("hidden"))) hipError_t ATT_NAME(AttPass pass, const AttArgs& a, int waves,
                                                           hipStream_t stream) {
-    if (waves == 4)
-        return general ? launch<true, 4>(pass, a, stream) : launch<false, 4>(pass, a, stream);
-    return general ? launch<true, 1>(pass, a, stream) : launch<false, 1>(pass, a, stream);
+    const bool cap = a.cap2 > 0.0f;
+    if (a.axes == 0)
+        return cap ? launch_waves<0, true>(pass, a, waves, stream)
+                   : launch_waves<0, false>(pass, a, waves, stream);
+    if (a.axes < 3)
+        return cap ? launch_waves<2, true>(pass, a, waves, stream)
+                   : launch_waves<2, false>(pass, a, waves, stream);
+    return cap ? launch_waves<3, true>(pass, a, waves, stream)
+               : launch_waves<3, false>(pass, a, waves, stream);
 }

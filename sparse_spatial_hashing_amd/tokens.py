@@ -219,9 +219,10 @@ def _heads(name: str, t: torch.Tensor, like: Optional[torch.Tensor] = None) -> t
     _floating(name, t, (torch.bfloat16, torch.float16), like)
     if t.dim() != 3:
         raise ValueError(f"{name} must be [tokens, heads, width]")
-    # 16-byte pieces: copy what is laid out otherwise
-    if t.numel() and (t.stride(2) != 1 or t.stride(0) % 8 or t.stride(1) % 8 or t.stride(0) < 0
-                      or t.stride(1) < 0 or t.data_ptr() % 16):
+    # 16-byte pieces, tokens less than 64 MiB apart: copy what is laid out otherwise
+    by_token, by_head, by_element = t.stride()
+    if (by_element != 1 or by_token & 7 or by_head & 7 or by_token >= 1 << 25 or t.data_ptr() & 15
+            or by_token < 0 or by_head < 0) and t.numel():
         t = t.clone(memory_format=torch.contiguous_format)
     return t
 
