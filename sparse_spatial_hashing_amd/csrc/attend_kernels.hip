@@ -143,7 +143,7 @@ __device__ __forceinline__ int find_range(const int* offsets, int docs, int tota
         lo += (cnt - 1) * step;
         n = min(step, n - (cnt - 1) * step);
     }
-    *first_tile = first;
+    *first_tile = __builtin_amdgcn_readfirstlane(first);
     return __builtin_amdgcn_readfirstlane(lo);
 }
 
@@ -239,21 +239,34 @@ struct Tile {
     // rows: that exist from `base` on (>= 1), stride in elements
     static __device__ __forceinline__ void load(uint4* tile, const elem* base, long long stride,
                                                 int rows, int width) {
-        typedef const __attribute__((address_space(1))) void* source;
-        typedef __attribute__((address_space(3))) void* target;
         const int r0 = threadIdx.x / kChunks, at = threadIdx.x % kChunks;
         const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-        const bool whole = rows >= ROWS;
+        constexpr int kStep = NT / kChunks;  // rows from one load to the next
+        const unsigned to = lds_address(tile) + 1024u * wave;
+        if (rows >= ROWS && width == W) {
+#pragma unroll
+            for (int p = 0; p < kPer; ++p)
+                if (p * NT + wave * 64 < ROWS * kChunks)
+                    start(to + 16u * NT * p, base + (long long)p * kStep * stride,
+                          (unsigned)r0 * (unsigned)(2 * stride) + 16u * (at ^ swz(p * kStep + r0)));
+            return;
+        }
 #pragma unroll
         for (int p = 0; p < kPer; ++p) {
-            const int r = p * (NT / kChunks) + r0;
-            const int c = at ^ swz(r);
-            // offsets inside a tile fit 32 bits: the host bounds the stride
-            const unsigned off = (unsigned)(whole ? r : min(r, rows - 1)) * (unsigned)(2 * stride) + 16u * c;
-            uint4* to = tile + p * NT + wave * 64;
-            if (p * NT + wave * 64 < ROWS * kChunks && (width == W || c * 8 < width))
-                __builtin_amdgcn_global_load_lds((source)((const char*)base + off), (target)to, 16, 0, 0);
+            const int r = p * kStep + r0, c = at ^ swz(r);
+            if (p * NT + wave * 64 < ROWS * kChunks && c * 8 < width)
+                start(to + 16u * NT * p, base, (unsigned)min(r, rows - 1) * (unsigned)(2 * stride) + 16u * c);
         }
+    }
+    static __device__ __forceinline__ unsigned lds_address(const uint4* p) {
+        return (unsigned)(size_t)(__attribute__((address_space(3))) const char*)p;
+    }
+    // 64 chunks to LDS from `to` on. Written out: the compiler would wait for
+    // the load before the next read of any LDS. Offsets inside a tile fit 32
+    // bits: the host bounds the stride.
+    static __device__ __forceinline__ void start(unsigned to, const elem* base, unsigned offset) {
+        asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
+                     :: "s"(to), "v"(offset), "s"(base) : "memory");
     }
 };
 
@@ -263,6 +276,21 @@ struct Tile {
 __device__ __forceinline__ int fresh(int lane) {
     if (W == 128) asm volatile("" : "+v"(lane));
     return lane;
+}
+
+// Nothing moves across: reads of LDS written above it are under way before
+// what is below, however few registers the compiler would rather use.
+__device__ __forceinline__ void fence() { __builtin_amdgcn_sched_barrier(0); }
+
+// The operands A of a product over the width with 32 rows of a tile.
+__device__ __forceinline__ void read_rows(const uint4* tile, int row0, int lane, vec8 (&x)[kSteps]) {
+#pragma unroll
+    for (int k = 0; k < kSteps; ++k) x[k] = lds_chunk(tile, row0 + (lane & 31), 2 * k + (lane >> 5));
+}
+// The operands A of the transposed product over 16 rows of a tile.
+__device__ __forceinline__ void read_columns(const uint4* tile, int row0, int lane, vec8 (&x)[kBlocks]) {
+#pragma unroll
+    for (int b = 0; b < kBlocks; ++b) x[b] = lds_transposed(tile, row0, b, lane);
 }
 
 __device__ __forceinline__ void landed() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
@@ -353,7 +381,7 @@ __device__ __forceinline__ long long xcd_block(long long bid, long long n) {
 // Key tiles are loaded one ahead into the other half of LDS.
 
 template <int AX, bool CAP, int NW, int BN>
-__global__ __launch_bounds__(64 * NW, NW == 4 ? 2 : 1) void k_att_forward(AttArgs a) {
+__global__ __launch_bounds__(64 * NW, 2) void k_att_forward(AttArgs a) {
     constexpr int NT = 64 * NW;
     constexpr int NB = BN / 32;
     typedef Tile<BN, NT> KeyTile;
@@ -424,15 +452,21 @@ __global__ __launch_bounds__(64 * NW, NW == 4 ? 2 : 1) void k_att_forward(AttArg
         __syncthreads();  // this tile is there, and all are done with the one before
         if (t + 1 < t1) fetch(t + 1);
 
+        const int ln = fresh(lane);
         acc16 s[NB];
+        vec8 kf[NB][kSteps], vf[2][kBlocks];
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) read_rows(tk[buf], 32 * nb, ln, kf[nb]);
+        fence();
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) {
 #pragma unroll
             for (int r = 0; r < 16; ++r) s[nb][r] = 0.0f;
 #pragma unroll
-            for (int k = 0; k < kSteps; ++k)
-                s[nb] = mma(lds_chunk(tk[buf], 32 * nb + (lane & 31), 2 * k + half), qf[k], s[nb]);
+            for (int k = 0; k < kSteps; ++k) s[nb] = mma(kf[nb][k], qf[k], s[nb]);
         }
+        read_columns(tv[buf], 0, ln, vf[0]);
+        fence();
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) {
             acc16 none;
@@ -476,10 +510,12 @@ __global__ __launch_bounds__(64 * NW, NW == 4 ? 2 : 1) void k_att_forward(AttArg
             }
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
+                // the next 16 keys' values while these are worked on
+                if (2 * nb + c + 1 < 2 * NB) read_columns(tv[buf], 32 * nb + 16 * (c + 1), ln, vf[(c + 1) & 1]);
                 const vec8 p = round8(s[nb], c);
+                fence();
 #pragma unroll
-                for (int b = 0; b < kBlocks; ++b)
-                    o[b] = mma(lds_transposed(tv[buf], 32 * nb + 16 * c, b, lane), p, o[b]);
+                for (int b = 0; b < kBlocks; ++b) o[b] = mma(vf[c][b], p, o[b]);
             }
         }
     }
@@ -566,7 +602,7 @@ __global__ __launch_bounds__(256) void k_att_join(AttArgs a) {
 // 32 bits.
 
 template <int AX, bool CAP, int NW, int BN>
-__global__ __launch_bounds__(64 * NW, NW == 4 ? 2 : 1) void k_att_grad_q(AttArgs a) {
+__global__ __launch_bounds__(64 * NW, NW == 4 && W < 128 ? 2 : 1) void k_att_grad_q(AttArgs a) {
     constexpr int NT = 64 * NW;
     constexpr int NB = BN / 32;
     typedef Tile<BN, NT> KeyTile;
@@ -645,13 +681,19 @@ __global__ __launch_bounds__(64 * NW, NW == 4 ? 2 : 1) void k_att_grad_q(AttArgs
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) {
             acc16 s, dp, bent;
+            vec8 rows[kSteps], kt[2][kBlocks];
+            read_rows(tk[buf], 32 * nb, ln, rows);
+            fence();
 #pragma unroll
             for (int r = 0; r < 16; ++r) s[r] = 0.0f, dp[r] = -delta;
 #pragma unroll
-            for (int k = 0; k < kSteps; ++k) {
-                s = mma(lds_chunk(tk[buf], 32 * nb + (ln & 31), 2 * k + (ln >> 5)), qf[k], s);
-                dp = mma(lds_chunk(tv[buf], 32 * nb + (ln & 31), 2 * k + (ln >> 5)), gf[k], dp);
-            }
+            for (int k = 0; k < kSteps; ++k) s = mma(rows[k], qf[k], s);
+            read_rows(tv[buf], 32 * nb, ln, rows);
+            fence();
+#pragma unroll
+            for (int k = 0; k < kSteps; ++k) dp = mma(rows[k], gf[k], dp);
+            read_columns(tk[buf], 32 * nb, ln, kt[0]);
+            fence();
             scores<AX, CAP>(a, s, bent, row, lse2, kpx[buf] + (AX ? 32 * nb : 0),
                             kpy[buf] + (AX == 3 ? 32 * nb : 0), half);
 #pragma unroll
@@ -677,12 +719,13 @@ __global__ __launch_bounds__(64 * NW, NW == 4 ? 2 : 1) void k_att_grad_q(AttArgs
             }
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
+                if (c == 0) read_columns(tk[buf], 32 * nb + 16, ln, kt[1]);
                 const vec8 ds = round8(dp, c), p = round8(s, c);
+                fence();
 #pragma unroll
                 for (int b = 0; b < kBlocks; ++b) {
-                    const vec8 kt = lds_transposed(tk[buf], 32 * nb + 16 * c, b, ln);
-                    o[b] = mma(kt, ds, o[b]);
-                    pk[b] = mma(kt, p, pk[b]);
+                    o[b] = mma(kt[c][b], ds, o[b]);
+                    pk[b] = mma(kt[c][b], p, pk[b]);
                 }
             }
         }
@@ -798,16 +841,29 @@ __global__ __launch_bounds__(64 * NW, NW == 4 && W < 128 ? 2 : 1) void k_att_gra
 
         const int ln = fresh(lane);
         acc16 s, dp, bent, sub;
+        vec8 rows[kSteps], col[2][kBlocks];
+        read_rows(tq[buf], 0, ln, rows);
+        fence();
 #pragma unroll
         for (int r = 0; r < 16; ++r) s[r] = 0.0f;
 #pragma unroll
-        for (int k = 0; k < kSteps; ++k)
-            s = mma(lds_chunk(tq[buf], ln & 31, 2 * k + (ln >> 5)), kf[k], s);
+        for (int k = 0; k < kSteps; ++k) s = mma(rows[k], kf[k], s);
+        read_rows(tg[buf], 0, ln, rows);
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
             const float4 ls = *(const float4*)(rlse[buf] + 8 * q + 4 * half);
             sub[4 * q + 0] = -ls.x, sub[4 * q + 1] = -ls.y, sub[4 * q + 2] = -ls.z, sub[4 * q + 3] = -ls.w;
         }
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const float4 de = *(const float4*)(rdelta[buf] + 8 * q + 4 * half);
+            dp[4 * q + 0] = de.x, dp[4 * q + 1] = de.y, dp[4 * q + 2] = de.z, dp[4 * q + 3] = de.w;
+        }
+        fence();
+#pragma unroll
+        for (int k = 0; k < kSteps; ++k) dp = mma(rows[k], vf[k], dp);
+        read_columns(tg[buf], 0, ln, col[0]);
+        fence();
         if (CAP) {
             cap_block(a, s);
             bent = s;
@@ -828,14 +884,6 @@ __global__ __launch_bounds__(64 * NW, NW == 4 && W < 128 ? 2 : 1) void k_att_gra
         const float by = CAP ? a.cap2 : a.scale2;
 #pragma unroll
         for (int r = 0; r < 16; ++r) s[r] = exp2_(__builtin_fmaf(s[r], by, sub[r]));
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            const float4 de = *(const float4*)(rdelta[buf] + 8 * q + 4 * half);
-            dp[4 * q + 0] = de.x, dp[4 * q + 1] = de.y, dp[4 * q + 2] = de.z, dp[4 * q + 3] = de.w;
-        }
-#pragma unroll
-        for (int k = 0; k < kSteps; ++k)
-            dp = mma(lds_chunk(tg[buf], ln & 31, 2 * k + (ln >> 5)), vf[k], dp);
         // every row of the tile sees every key of the block?
         if (i + BM > d.lq || key_limit(a, d, i) < min(key0 + kAttRows * NW, lk)) {
 #pragma unroll
@@ -846,10 +894,14 @@ __global__ __launch_bounds__(64 * NW, NW == 4 && W < 128 ? 2 : 1) void k_att_gra
         }
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
+            if (c == 0)
+                read_columns(tg[buf], 16, ln, col[1]);
+            else
+                read_columns(tq[buf], 0, ln, col[0]);
             const vec8 p = round8(s, c);
+            fence();
 #pragma unroll
-            for (int b = 0; b < kBlocks; ++b)
-                gv[b] = mma(lds_transposed(tg[buf], 16 * c, b, ln), p, gv[b]);
+            for (int b = 0; b < kBlocks; ++b) gv[b] = mma(col[c][b], p, gv[b]);
         }
 #pragma unroll
         for (int r = 0; r < 16; ++r) dp[r] *= s[r];
@@ -859,10 +911,11 @@ __global__ __launch_bounds__(64 * NW, NW == 4 && W < 128 ? 2 : 1) void k_att_gra
         }
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
+            if (c == 0) read_columns(tq[buf], 16, ln, col[1]);
             const vec8 ds = round8(dp, c);
+            fence();
 #pragma unroll
-            for (int b = 0; b < kBlocks; ++b)
-                gk[b] = mma(lds_transposed(tq[buf], 16 * c, b, ln), ds, gk[b]);
+            for (int b = 0; b < kBlocks; ++b) gk[b] = mma(col[c][b], ds, gk[b]);
         }
         i += BM;
         if (i >= d.lq) i = first_tile * BM, ++g;
