@@ -172,14 +172,24 @@ __device__ __forceinline__ int key_limit(const AttArgs& a, const Range& d, int i
     return clampi(max(d.prefix, min(d.lk, i + d.lk - d.lq + 1)), 0, d.lk);
 }
 
-// Positions packed for sad_u16: .x the last two axes, .y the first of three.
-__device__ __forceinline__ uint2 pack_pos(const int* pos, long long st, long long sa, int axes,
-                                          long long token) {
-    const int* p = pos + token * st;
-    uint2 r = make_uint2((unsigned)clampi(p[0], 0, 65535), 0u);
-    if (axes >= 2) r.x |= (unsigned)clampi(p[sa], 0, 65535) << 16;
-    if (axes >= 3) r.y = (unsigned)clampi(p[2 * sa], 0, 65535);
+// A token's position as it is in memory, and packed for sad_u16: .x the last
+// two axes, .y the first of three. Apart, so that a position fetched ahead is
+// first waited for where it is packed.
+template <int AX>
+__device__ __forceinline__ int3 load_pos(const int* pos, long long st, long long sa, int axes,
+                                         long long token) {
+    int3 r = make_int3(0, 0, 0);
+    if (AX) {
+        const int* p = pos + token * st;
+        r.x = p[0];
+        if (axes >= 2) r.y = p[sa];
+        if (AX == 3) r.z = p[2 * sa];
+    }
     return r;
+}
+__device__ __forceinline__ uint2 pack_pos(int3 p) {
+    return make_uint2((unsigned)clampi(p.x, 0, 65535) | (unsigned)clampi(p.y, 0, 65535) << 16,
+                      (unsigned)clampi(p.z, 0, 65535));
 }
 
 // |a - b| summed over the axes.
@@ -295,6 +305,14 @@ __device__ __forceinline__ void read_columns(const uint4* tile, int row0, int la
 
 __device__ __forceinline__ void landed() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
 
+// Values loaded before a loop are waited for before it: inside, the wait would
+// be for the tile under way as well, each time round.
+template <int N>
+__device__ __forceinline__ void settle(vec8 (&x)[N]) {
+#pragma unroll
+    for (int k = 0; k < N; ++k) asm volatile("" : "+v"(x[k]));
+}
+
 __device__ __forceinline__ vec8 load_chunk(const elem* row, int c, int width) {
     return c * 8 < width ? *(const vec8*)(row + c * 8) : zero8();
 }
@@ -323,7 +341,7 @@ __device__ __forceinline__ Row get_row(const AttArgs& a, const Range& d, int kvh
     w.pos = make_uint2(0, 0);
     if (AX) {
         w.slope2 = a.slopes[w.head] * kLog2e;
-        w.pos = pack_pos(a.q_pos, a.qp_st, a.qp_sa, a.axes, w.token);
+        w.pos = pack_pos(load_pos<AX>(a.q_pos, a.qp_st, a.qp_sa, a.axes, w.token));
     }
     return w;
 }
@@ -415,13 +433,13 @@ __global__ __launch_bounds__(64 * NW, 2) void k_att_forward(AttArgs a) {
 
     const elem* k0 = (const elem*)a.k + (long long)kvh * a.k_sh + d.klo * a.k_st;
     const elem* v0 = (const elem*)a.v + (long long)kvh * a.v_sh + d.klo * a.v_st;
-    uint2 sp = make_uint2(0, 0);
+    int3 ahead = make_int3(0, 0, 0);
     auto fetch = [&](int t) {
         KeyTile::load(tk[t & 1], k0 + (long long)t * BN * a.k_st, a.k_st, d.lk - t * BN, a.width);
         KeyTile::load(tv[t & 1], v0 + (long long)t * BN * a.v_st, a.v_st, d.lk - t * BN, a.width);
         if (AX && threadIdx.x < BN)
-            sp = pack_pos(a.k_pos, a.kp_st, a.kp_sa, a.axes,
-                          d.klo + min(t * BN + (int)threadIdx.x, d.lk - 1));
+            ahead = load_pos<AX>(a.k_pos, a.kp_st, a.kp_sa, a.axes,
+                                 d.klo + min(t * BN + (int)threadIdx.x, d.lk - 1));
     };
     for (int b = 0; b < 2; ++b) {
         KeyTile::clear(tk[b], a.width);
@@ -434,6 +452,7 @@ __global__ __launch_bounds__(64 * NW, 2) void k_att_forward(AttArgs a) {
     const elem* qrow = (const elem*)a.q + row.token * a.q_st + row.head * a.q_sh;
 #pragma unroll
     for (int k = 0; k < kSteps; ++k) qf[k] = load_chunk(qrow, 2 * k + half, a.width);
+    settle(qf);
 
     acc16 o[kBlocks];
 #pragma unroll
@@ -445,8 +464,9 @@ __global__ __launch_bounds__(64 * NW, 2) void k_att_forward(AttArgs a) {
     for (int t = t0; t < t1; ++t) {
         const int buf = t & 1;
         if (AX && threadIdx.x < BN) {
-            kpx[buf][threadIdx.x] = sp.x;
-            if (AX == 3) kpy[buf][threadIdx.x] = sp.y;
+            const uint2 pos = pack_pos(ahead);
+            kpx[buf][threadIdx.x] = pos.x;
+            if (AX == 3) kpy[buf][threadIdx.x] = pos.y;
         }
         landed();
         __syncthreads();  // this tile is there, and all are done with the one before
@@ -628,13 +648,13 @@ __global__ __launch_bounds__(64 * NW, NW == 4 && W < 128 ? 2 : 1) void k_att_gra
 
     const elem* k0 = (const elem*)a.k + (long long)kvh * a.k_sh + d.klo * a.k_st;
     const elem* v0 = (const elem*)a.v + (long long)kvh * a.v_sh + d.klo * a.v_st;
-    uint2 sp = make_uint2(0, 0);
+    int3 ahead = make_int3(0, 0, 0);
     auto fetch = [&](int t) {
         KeyTile::load(tk[t & 1], k0 + (long long)t * BN * a.k_st, a.k_st, d.lk - t * BN, a.width);
         KeyTile::load(tv[t & 1], v0 + (long long)t * BN * a.v_st, a.v_st, d.lk - t * BN, a.width);
         if (AX && threadIdx.x < BN)
-            sp = pack_pos(a.k_pos, a.kp_st, a.kp_sa, a.axes,
-                          d.klo + min(t * BN + (int)threadIdx.x, d.lk - 1));
+            ahead = load_pos<AX>(a.k_pos, a.kp_st, a.kp_sa, a.axes,
+                                 d.klo + min(t * BN + (int)threadIdx.x, d.lk - 1));
     };
     for (int b = 0; b < 2; ++b) {
         KeyTile::clear(tk[b], a.width);
@@ -658,7 +678,10 @@ __global__ __launch_bounds__(64 * NW, NW == 4 && W < 128 ? 2 : 1) void k_att_gra
         for (int j = 0; j < 8; ++j) delta = __builtin_fmaf((float)gf[k][j], (float)of[j], delta);
     }
     delta += other_half(delta);
-    const float lse2 = a.lse[at] * kLog2e - kLift;
+    float lse2 = a.lse[at] * kLog2e - kLift;
+    settle(qf);
+    settle(gf);
+    asm volatile("" : "+v"(lse2));
 
     acc16 o[kBlocks], pk[kBlocks];
     float rest = 0.0f;
@@ -670,8 +693,9 @@ __global__ __launch_bounds__(64 * NW, NW == 4 && W < 128 ? 2 : 1) void k_att_gra
     for (int t = 0; t < t1; ++t) {
         const int buf = t & 1;
         if (AX && threadIdx.x < BN) {
-            kpx[buf][threadIdx.x] = sp.x;
-            if (AX == 3) kpy[buf][threadIdx.x] = sp.y;
+            const uint2 pos = pack_pos(ahead);
+            kpx[buf][threadIdx.x] = pos.x;
+            if (AX == 3) kpy[buf][threadIdx.x] = pos.y;
         }
         landed();
         __syncthreads();
@@ -788,18 +812,18 @@ __global__ __launch_bounds__(64 * NW, NW == 4 && W < 128 ? 2 : 1) void k_att_gra
     const int t1 = per_head * a.group;
 
     float s_lse = 0.0f, s_delta = 0.0f;
-    uint2 s_pos = make_uint2(0, 0);
-    auto fetch = [&](int t) {
-        const int g = t / per_head, i = (first_tile + t % per_head) * BM, head = kvh * a.group + g;
+    int3 s_pos = make_int3(0, 0, 0);
+    auto fetch = [&](int t, int g, int i) {
+        const int head = kvh * a.group + g;
         RowTile::load(tq[t & 1], (const elem*)a.q + (long long)head * a.q_sh + (long long)(d.qlo + i) * a.q_st,
                       a.q_st, d.lq - i, a.width);
         RowTile::load(tg[t & 1], (const elem*)a.g + (long long)head * a.g_sh + (long long)(d.qlo + i) * a.g_st,
                       a.g_st, d.lq - i, a.width);
         if (threadIdx.x < BM) {
             const long long q = d.qlo + min(i + (int)threadIdx.x, d.lq - 1);
-            s_lse = a.lse[q * a.heads + head] * kLog2e - kLift;
+            s_lse = a.lse[q * a.heads + head];
             s_delta = a.delta[q * a.heads + head];
-            if (AX) s_pos = pack_pos(a.q_pos, a.qp_st, a.qp_sa, a.axes, q);
+            s_pos = load_pos<AX>(a.q_pos, a.qp_st, a.qp_sa, a.axes, q);
         }
     };
     for (int b = 0; b < 2; ++b) {
@@ -807,7 +831,7 @@ __global__ __launch_bounds__(64 * NW, NW == 4 && W < 128 ? 2 : 1) void k_att_gra
         RowTile::clear(tg[b], a.width);
     }
     if (a.width < W) __syncthreads();
-    if (t1 > 0) fetch(0);
+    if (t1 > 0) fetch(0, 0, first_tile * BM);
 
     vec8 kf[kSteps], vf[kSteps];
     const elem* krow = (const elem*)a.k + token * a.k_st + kvh * a.k_sh;
@@ -818,7 +842,11 @@ __global__ __launch_bounds__(64 * NW, NW == 4 && W < 128 ? 2 : 1) void k_att_gra
         vf[k] = load_chunk(vrow, 2 * k + half, a.width);
     }
     uint2 kpos = make_uint2(0, 0);
-    if (AX && t1 > 0) kpos = pack_pos(a.k_pos, a.kp_st, a.kp_sa, a.axes, token);
+    if (AX && t1 > 0) kpos = pack_pos(load_pos<AX>(a.k_pos, a.kp_st, a.kp_sa, a.axes, token));
+    float slope2 = AX ? a.slopes[kvh * a.group] * kLog2e : 0.0f;
+    settle(kf);
+    settle(vf);
+    asm volatile("" : "+v"(kpos.x), "+v"(kpos.y), "+v"(slope2));
 
     acc16 gk[kBlocks], gv[kBlocks];
 #pragma unroll
@@ -830,14 +858,16 @@ __global__ __launch_bounds__(64 * NW, NW == 4 && W < 128 ? 2 : 1) void k_att_gra
     for (int t = 0; t < t1; ++t) {
         const int buf = t & 1;
         if (threadIdx.x < BM) {
-            rlse[buf][threadIdx.x] = s_lse;
+            rlse[buf][threadIdx.x] = s_lse * kLog2e - kLift;
             rdelta[buf][threadIdx.x] = -s_delta;
-            if (AX) rpx[buf][threadIdx.x] = s_pos.x;
-            if (AX == 3) rpy[buf][threadIdx.x] = s_pos.y;
+            const uint2 pos = pack_pos(s_pos);
+            if (AX) rpx[buf][threadIdx.x] = pos.x;
+            if (AX == 3) rpy[buf][threadIdx.x] = pos.y;
         }
         landed();
         __syncthreads();
-        if (t + 1 < t1) fetch(t + 1);
+        const bool turn = i + BM >= d.lq;  // the head's last tile
+        if (t + 1 < t1) fetch(t + 1, turn ? g + 1 : g, turn ? first_tile * BM : i + BM);
 
         const int ln = fresh(lane);
         acc16 s, dp, bent, sub;
@@ -869,7 +899,6 @@ __global__ __launch_bounds__(64 * NW, NW == 4 && W < 128 ? 2 : 1) void k_att_gra
             bent = s;
         }
         if (AX) {
-            const float slope2 = a.slopes[kvh * a.group + g] * kLog2e;
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
                 const uint4 x = *(const uint4*)(rpx[buf] + 8 * q + 4 * half);
@@ -918,7 +947,11 @@ __global__ __launch_bounds__(64 * NW, NW == 4 && W < 128 ? 2 : 1) void k_att_gra
             for (int b = 0; b < kBlocks; ++b) gk[b] = mma(col[c][b], ds, gk[b]);
         }
         i += BM;
-        if (i >= d.lq) i = first_tile * BM, ++g;
+        if (turn) {
+            i = first_tile * BM;
+            ++g;
+            if (AX && t + 1 < t1) slope2 = a.slopes[kvh * a.group + g] * kLog2e;
+        }
     }
     if (key >= lk) return;
     const long long at = token * a.kv_heads + kvh;
