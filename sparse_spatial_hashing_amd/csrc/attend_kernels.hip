@@ -73,22 +73,40 @@ __device__ __forceinline__ int swz(int row) {
     return (row >> 2) & 3;
 }
 
-// 16-byte chunk c of a tile row.
-__device__ __forceinline__ vec8 lds_chunk(const uint4* tile, int row, int c) {
-    return __builtin_bit_cast(vec8, tile[row * kChunks + (c ^ swz(row))]);
+// LDS as byte addresses. Tiles start at multiples of 256 bytes, so the chunk's
+// XOR works on the sum of a tile's address and a lane's place in it: from one
+// sum per lane, an operand's chunk is one XOR and its 16 or 32 rows are in the
+// instruction's offset.
+template <typename T>
+__device__ __forceinline__ unsigned lds_address(const T* p) {
+    return (unsigned)(size_t)(__attribute__((address_space(3))) const char*)p;
+}
+
+// Operand A of a product over the width, rows lane % 32: where in a tile.
+__device__ __forceinline__ unsigned rows_place(int lane) {
+    const int row = lane & 31;
+    return row * 2 * W + (((lane >> 5) ^ swz(row)) << 4);
+}
+// at: tile address + rows_place
+__device__ __forceinline__ vec8 lds_rows(unsigned at, int row0, int k) {
+    typedef const __attribute__((address_space(3))) vec8* P;
+    return *(P)((at ^ (k << 5)) + row0 * 2 * W);
 }
 
 // Operand A of a transposed product: rows are elements 32 b + lane % 32 of
-// the width, inner index the 16 tile rows from row0 in the order above.
-__device__ __forceinline__ vec8 lds_transposed(const uint4* tile, int row0, int b, int lane) {
-    typedef __attribute__((address_space(3))) short4v lds4;
-    const int row = row0 + 4 * (lane >> 5) + ((lane & 15) >> 2);
-    const int c = 4 * b + 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1);
-    const char* base = (const char*)tile;
-    const char* p0 = base + row * (2 * W) + ((c ^ swz(row)) << 4) + ((lane & 1) << 3);
-    const char* p1 = base + (row + 8) * (2 * W) + ((c ^ swz(row + 8)) << 4) + ((lane & 1) << 3);
-    const short4v x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4*)p0);
-    const short4v y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4*)p1);
+// the width, inner index 16 tile rows in the order above; where in a tile
+// the first four of eight rows are, and the others.
+__device__ __forceinline__ uint2 columns_place(int lane) {
+    const int row = 4 * (lane >> 5) + ((lane & 15) >> 2);
+    const int c = 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1), in = (lane & 1) << 3;
+    return make_uint2(row * 2 * W + ((c ^ swz(row)) << 4) + in,
+                      (row + 8) * 2 * W + ((c ^ swz(row + 8)) << 4) + in);
+}
+// row0: a multiple of 16, which swz() does not see
+__device__ __forceinline__ vec8 lds_columns(uint2 at, int row0, int b) {
+    typedef __attribute__((address_space(3))) short4v* P;
+    const short4v x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((P)((at.x ^ (b << 6)) + row0 * 2 * W));
+    const short4v y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((P)((at.y ^ (b << 6)) + row0 * 2 * W));
     typedef short short8v __attribute__((ext_vector_type(8)));
     const short8v z = __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7);
     return __builtin_bit_cast(vec8, z);
@@ -232,6 +250,14 @@ __device__ __forceinline__ void cap_block(const AttArgs& a, acc16& s) {
     }
 }
 
+// A lane or thread number again, as a value that places in LDS and memory are
+// computed from where they are used: kept over a loop, at a width of 128 they
+// push what the products need out of the registers.
+__device__ __forceinline__ int fresh(int x) {
+    if (W == 128) asm volatile("" : "+v"(x));
+    return x;
+}
+
 // A tile of ROWS rows of k or v (or q, grad_out), brought from HBM into LDS
 // without passing registers: a wavefront's load puts 64 consecutive 16-byte
 // chunks of LDS, so the XOR of swz() is on the side of the source. Rows past
@@ -249,7 +275,7 @@ struct Tile {
     // rows: that exist from `base` on (>= 1), stride in elements
     static __device__ __forceinline__ void load(uint4* tile, const elem* base, long long stride,
                                                 int rows, int width) {
-        const int r0 = threadIdx.x / kChunks, at = threadIdx.x % kChunks;
+        const int tid = fresh(threadIdx.x), r0 = tid / kChunks, at = tid % kChunks;
         const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
         constexpr int kStep = NT / kChunks;  // rows from one load to the next
         const unsigned to = lds_address(tile) + 1024u * wave;
@@ -268,9 +294,6 @@ struct Tile {
                 start(to + 16u * NT * p, base, (unsigned)min(r, rows - 1) * (unsigned)(2 * stride) + 16u * c);
         }
     }
-    static __device__ __forceinline__ unsigned lds_address(const uint4* p) {
-        return (unsigned)(size_t)(__attribute__((address_space(3))) const char*)p;
-    }
     // 64 chunks to LDS from `to` on. Written out: the compiler would wait for
     // the load before the next read of any LDS. Offsets inside a tile fit 32
     // bits: the host bounds the stride.
@@ -280,27 +303,66 @@ struct Tile {
     }
 };
 
-// The lane again, as a value the compiler computes LDS addresses from where
-// they are used: kept over the loop, a width of 128 has more of them than
-// registers.
-__device__ __forceinline__ int fresh(int lane) {
-    if (W == 128) asm volatile("" : "+v"(lane));
-    return lane;
-}
-
 // Nothing moves across: reads of LDS written above it are under way before
 // what is below, however few registers the compiler would rather use.
 __device__ __forceinline__ void fence() { __builtin_amdgcn_sched_barrier(0); }
 
 // The operands A of a product over the width with 32 rows of a tile.
-__device__ __forceinline__ void read_rows(const uint4* tile, int row0, int lane, vec8 (&x)[kSteps]) {
+__device__ __forceinline__ void read_rows(unsigned at, int row0, vec8 (&x)[kSteps]) {
 #pragma unroll
-    for (int k = 0; k < kSteps; ++k) x[k] = lds_chunk(tile, row0 + (lane & 31), 2 * k + (lane >> 5));
+    for (int k = 0; k < kSteps; ++k) x[k] = lds_rows(at, row0, k);
 }
 // The operands A of the transposed product over 16 rows of a tile.
-__device__ __forceinline__ void read_columns(const uint4* tile, int row0, int lane, vec8 (&x)[kBlocks]) {
+__device__ __forceinline__ void read_columns(uint2 at, int row0, vec8 (&x)[kBlocks]) {
 #pragma unroll
-    for (int b = 0; b < kBlocks; ++b) x[b] = lds_transposed(tile, row0, b, lane);
+    for (int b = 0; b < kBlocks; ++b) x[b] = lds_columns(at, row0, b);
+}
+
+// s += 32 rows of a tile times an operand in registers. At a width of 128 two
+// steps are read ahead, else all at once: the backward has no registers left.
+__device__ __forceinline__ void product(acc16& s, unsigned at, int row0, const vec8 (&f)[kSteps]) {
+    constexpr int kAhead = W == 128 ? 2 : kSteps;
+    vec8 x[2][kAhead];
+    auto read = [&](int j) {
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) x[j & 1][i] = lds_rows(at, row0, kAhead * j + i);
+    };
+    read(0);
+#pragma unroll
+    for (int j = 0; j < kSteps / kAhead; ++j) {
+        if (j + 1 < kSteps / kAhead) read(j + 1);
+        fence();
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) s = mma(x[j & 1][i], f[kAhead * j + i], s);
+    }
+}
+
+// Operands B that a wavefront keeps in LDS instead of registers, each lane its
+// own: at a width of 128 the backward's four sets and its sums do not fit the
+// 256 registers that let two wavefronts share a SIMD.
+constexpr int kKept = 64 * kSteps;  // 16-byte pieces per wavefront
+__device__ __forceinline__ void keep(uint4* kept, int lane, const vec8 (&x)[kSteps]) {
+#pragma unroll
+    for (int k = 0; k < kSteps; ++k) kept[64 * k + lane] = __builtin_bit_cast(uint4, x[k]);
+}
+// s += rows of the tile times the kept operand, two steps read ahead.
+__device__ __forceinline__ void product_kept(acc16& s, unsigned at, int row0, const uint4* kept, int lane) {
+    vec8 x[2][2], y[2][2];
+    auto read = [&](int j) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            x[j & 1][i] = lds_rows(at, row0, 2 * j + i);
+            y[j & 1][i] = __builtin_bit_cast(vec8, kept[64 * (2 * j + i) + lane]);
+        }
+    };
+    read(0);
+#pragma unroll
+    for (int j = 0; j < kSteps / 2; ++j) {
+        if (j + 1 < kSteps / 2) read(j + 1);
+        fence();
+#pragma unroll
+        for (int i = 0; i < 2; ++i) s = mma(x[j & 1][i], y[j & 1][i], s);
+    }
 }
 
 __device__ __forceinline__ void landed() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
@@ -403,8 +465,8 @@ __global__ __launch_bounds__(64 * NW, 2) void k_att_forward(AttArgs a) {
     constexpr int NT = 64 * NW;
     constexpr int NB = BN / 32;
     typedef Tile<BN, NT> KeyTile;
-    __shared__ __align__(16) uint4 tk[2][BN * kChunks];
-    __shared__ __align__(16) uint4 tv[2][BN * kChunks];
+    __shared__ __align__(256) uint4 tk[2][BN * kChunks];
+    __shared__ __align__(256) uint4 tv[2][BN * kChunks];
     __shared__ __align__(16) unsigned kpx[2][AX ? BN : 4], kpy[2][AX == 3 ? BN : 4];
 
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, half = lane >> 5;
@@ -472,11 +534,13 @@ __global__ __launch_bounds__(64 * NW, 2) void k_att_forward(AttArgs a) {
         __syncthreads();  // this tile is there, and all are done with the one before
         if (t + 1 < t1) fetch(t + 1);
 
-        const int ln = fresh(lane);
+        const unsigned k_at = lds_address(tk[0]) + rows_place(lane) + buf * sizeof(tk[0]);
+        uint2 v_at = columns_place(lane);
+        v_at.x += lds_address(tv[0]) + buf * sizeof(tv[0]), v_at.y += lds_address(tv[0]) + buf * sizeof(tv[0]);
         acc16 s[NB];
         vec8 kf[NB][kSteps], vf[2][kBlocks];
 #pragma unroll
-        for (int nb = 0; nb < NB; ++nb) read_rows(tk[buf], 32 * nb, ln, kf[nb]);
+        for (int nb = 0; nb < NB; ++nb) read_rows(k_at, 32 * nb, kf[nb]);
         fence();
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) {
@@ -485,7 +549,7 @@ __global__ __launch_bounds__(64 * NW, 2) void k_att_forward(AttArgs a) {
 #pragma unroll
             for (int k = 0; k < kSteps; ++k) s[nb] = mma(kf[nb][k], qf[k], s[nb]);
         }
-        read_columns(tv[buf], 0, ln, vf[0]);
+        read_columns(v_at, 0, vf[0]);
         fence();
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) {
@@ -531,7 +595,7 @@ __global__ __launch_bounds__(64 * NW, 2) void k_att_forward(AttArgs a) {
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
                 // the next 16 keys' values while these are worked on
-                if (2 * nb + c + 1 < 2 * NB) read_columns(tv[buf], 32 * nb + 16 * (c + 1), ln, vf[(c + 1) & 1]);
+                if (2 * nb + c + 1 < 2 * NB) read_columns(v_at, 32 * nb + 16 * (c + 1), vf[(c + 1) & 1]);
                 const vec8 p = round8(s[nb], c);
                 fence();
 #pragma unroll
@@ -622,13 +686,16 @@ __global__ __launch_bounds__(256) void k_att_join(AttArgs a) {
 // 32 bits.
 
 template <int AX, bool CAP, int NW, int BN>
-__global__ __launch_bounds__(64 * NW, NW == 4 && W < 128 ? 2 : 1) void k_att_grad_q(AttArgs a) {
+__global__ __launch_bounds__(64 * NW, NW == 4 || W < 128 ? 2 : 1) void k_att_grad_q(AttArgs a) {
     constexpr int NT = 64 * NW;
     constexpr int NB = BN / 32;
     typedef Tile<BN, NT> KeyTile;
-    __shared__ __align__(16) uint4 tk[2][BN * kChunks];
-    __shared__ __align__(16) uint4 tv[2][BN * kChunks];
+    __shared__ __align__(256) uint4 tk[2][BN * kChunks];
+    __shared__ __align__(256) uint4 tv[2][BN * kChunks];
     __shared__ __align__(16) unsigned kpx[2][AX ? BN : 4], kpy[2][AX == 3 ? BN : 4];
+
+    constexpr bool kKeep = W == 128 && NW == 4;
+    __shared__ uint4 kept[kKeep ? NW : 1][kKeep ? kKept : 1];
 
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, half = lane >> 5;
     const long long id = xcd_block(blockIdx.x, gridDim.x);
@@ -652,9 +719,10 @@ __global__ __launch_bounds__(64 * NW, NW == 4 && W < 128 ? 2 : 1) void k_att_gra
     auto fetch = [&](int t) {
         KeyTile::load(tk[t & 1], k0 + (long long)t * BN * a.k_st, a.k_st, d.lk - t * BN, a.width);
         KeyTile::load(tv[t & 1], v0 + (long long)t * BN * a.v_st, a.v_st, d.lk - t * BN, a.width);
-        if (AX && threadIdx.x < BN)
+        const int tid = fresh(threadIdx.x);
+        if (AX && tid < BN)
             ahead = load_pos<AX>(a.k_pos, a.kp_st, a.kp_sa, a.axes,
-                                 d.klo + min(t * BN + (int)threadIdx.x, d.lk - 1));
+                                 d.klo + min(t * BN + tid, d.lk - 1));
     };
     for (int b = 0; b < 2; ++b) {
         KeyTile::clear(tk[b], a.width);
@@ -680,7 +748,10 @@ __global__ __launch_bounds__(64 * NW, NW == 4 && W < 128 ? 2 : 1) void k_att_gra
     delta += other_half(delta);
     float lse2 = a.lse[at] * kLog2e - kLift;
     settle(qf);
-    settle(gf);
+    if (kKeep)
+        keep(kept[wave], lane, gf);
+    else
+        settle(gf);
     asm volatile("" : "+v"(lse2));
 
     acc16 o[kBlocks], pk[kBlocks];
@@ -692,41 +763,71 @@ __global__ __launch_bounds__(64 * NW, NW == 4 && W < 128 ? 2 : 1) void k_att_gra
 
     for (int t = 0; t < t1; ++t) {
         const int buf = t & 1;
-        if (AX && threadIdx.x < BN) {
+        const int tid = fresh(threadIdx.x);
+        if (AX && tid < BN) {
             const uint2 pos = pack_pos(ahead);
-            kpx[buf][threadIdx.x] = pos.x;
-            if (AX == 3) kpy[buf][threadIdx.x] = pos.y;
+            kpx[buf][tid] = pos.x;
+            if (AX == 3) kpy[buf][tid] = pos.y;
         }
         landed();
         __syncthreads();
         if (t + 1 < t1) fetch(t + 1);
         const bool masked = (t + 1) * BN > common;
         const int ln = fresh(lane);
+        const unsigned k_at = lds_address(tk[0]) + rows_place(ln) + buf * sizeof(tk[0]);
+        const unsigned v_at = lds_address(tv[0]) + rows_place(ln) + buf * sizeof(tv[0]);
+        uint2 kt_at = columns_place(ln);
+        kt_at.x += lds_address(tk[0]) + buf * sizeof(tk[0]), kt_at.y += lds_address(tk[0]) + buf * sizeof(tk[0]);
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) {
             acc16 s, dp, bent;
-            vec8 rows[kSteps], kt[2][kBlocks];
-            read_rows(tk[buf], 32 * nb, ln, rows);
-            fence();
 #pragma unroll
-            for (int r = 0; r < 16; ++r) s[r] = 0.0f, dp[r] = -delta;
-#pragma unroll
-            for (int k = 0; k < kSteps; ++k) s = mma(rows[k], qf[k], s);
-            read_rows(tv[buf], 32 * nb, ln, rows);
-            fence();
-#pragma unroll
-            for (int k = 0; k < kSteps; ++k) dp = mma(rows[k], gf[k], dp);
-            read_columns(tk[buf], 32 * nb, ln, kt[0]);
-            fence();
+            for (int r = 0; r < 16; ++r) s[r] = 0.0f;
+            product(s, k_at, 32 * nb, qf);
             scores<AX, CAP>(a, s, bent, row, lse2, kpx[buf] + (AX ? 32 * nb : 0),
                             kpy[buf] + (AX == 3 ? 32 * nb : 0), half);
 #pragma unroll
             for (int r = 0; r < 16; ++r) s[r] = exp2_(s[r]);
+            const int left = masked ? row.limit - (t * BN + 32 * nb) - 4 * half : 32;
             if (masked) {
-                const int left = row.limit - (t * BN + 32 * nb) - 4 * half;
 #pragma unroll
                 for (int r = 0; r < 16; ++r)
-                    if (8 * (r / 4) + r % 4 >= left) s[r] = dp[r] = 0.0f;
+                    if (8 * (r / 4) + r % 4 >= left) s[r] = 0.0f;
+            }
+            if (CAP) {
+#pragma unroll
+                for (int r = 0; r < 16; ++r) bent[r] = __builtin_fmaf(-bent[r], bent[r], 1.0f);
+            }
+            vec8 kt[2][kBlocks];
+            read_columns(kt_at, 32 * nb, kt[0]);
+            read_columns(kt_at, 32 * nb + 16, kt[1]);
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                acc16 flat = s;
+                if (CAP) {
+#pragma unroll
+                    for (int r = 0; r < 16; ++r) flat[r] *= bent[r];
+                }
+                const vec8 p = round8(flat, c);
+                fence();
+#pragma unroll
+                for (int b = 0; b < kBlocks; ++b) pk[b] = mma(kt[c][b], p, pk[b]);
+            }
+#pragma unroll
+            for (int r = 0; r < 16; ++r) dp[r] = -delta;
+            if (kKeep)
+                product_kept(dp, v_at, 32 * nb, kept[wave], ln);
+            else
+                product(dp, v_at, 32 * nb, gf);
+            if (kKeep) {  // again: no registers to hold them
+                read_columns(kt_at, 32 * nb, kt[0]);
+                read_columns(kt_at, 32 * nb + 16, kt[1]);
+            }
+            fence();
+            if (masked) {
+#pragma unroll
+                for (int r = 0; r < 16; ++r)
+                    if (8 * (r / 4) + r % 4 >= left) dp[r] = 0.0f;
             }
 #pragma unroll
             for (int r = 0; r < 16; ++r) {
@@ -735,22 +836,14 @@ __global__ __launch_bounds__(64 * NW, NW == 4 && W < 128 ? 2 : 1) void k_att_gra
             }
             if (CAP) {
 #pragma unroll
-                for (int r = 0; r < 16; ++r) {
-                    const float flat = __builtin_fmaf(-bent[r], bent[r], 1.0f);
-                    dp[r] *= flat;
-                    s[r] *= flat;
-                }
+                for (int r = 0; r < 16; ++r) dp[r] *= bent[r];
             }
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
-                if (c == 0) read_columns(tk[buf], 32 * nb + 16, ln, kt[1]);
-                const vec8 ds = round8(dp, c), p = round8(s, c);
+                const vec8 ds = round8(dp, c);
                 fence();
 #pragma unroll
-                for (int b = 0; b < kBlocks; ++b) {
-                    o[b] = mma(kt[c][b], ds, o[b]);
-                    pk[b] = mma(kt[c][b], p, pk[b]);
-                }
+                for (int b = 0; b < kBlocks; ++b) o[b] = mma(kt[c][b], ds, o[b]);
             }
         }
     }
@@ -781,14 +874,17 @@ __global__ __launch_bounds__(64 * NW, NW == 4 && W < 128 ? 2 : 1) void k_att_gra
 // grad_k^T = Q^T dS.
 
 template <int AX, bool CAP, int NW>
-__global__ __launch_bounds__(64 * NW, NW == 4 && W < 128 ? 2 : 1) void k_att_grad_kv(AttArgs a) {
+__global__ __launch_bounds__(64 * NW, NW == 4 || W < 128 ? 2 : 1) void k_att_grad_kv(AttArgs a) {
     constexpr int NT = 64 * NW;
     constexpr int BM = 32;
     typedef Tile<BM, NT> RowTile;
-    __shared__ __align__(16) uint4 tq[2][BM * kChunks];
-    __shared__ __align__(16) uint4 tg[2][BM * kChunks];
+    __shared__ __align__(256) uint4 tq[2][BM * kChunks];
+    __shared__ __align__(256) uint4 tg[2][BM * kChunks];
     __shared__ __align__(16) float rlse[2][BM], rdelta[2][BM];
     __shared__ __align__(16) unsigned rpx[2][BM], rpy[2][BM];
+
+    constexpr bool kKeep = W == 128 && NW == 4;
+    __shared__ uint4 kept[kKeep ? NW : 1][kKeep ? kKept : 1];
 
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, half = lane >> 5;
     const long long id = xcd_block(blockIdx.x, gridDim.x);
@@ -819,8 +915,9 @@ __global__ __launch_bounds__(64 * NW, NW == 4 && W < 128 ? 2 : 1) void k_att_gra
                       a.q_st, d.lq - i, a.width);
         RowTile::load(tg[t & 1], (const elem*)a.g + (long long)head * a.g_sh + (long long)(d.qlo + i) * a.g_st,
                       a.g_st, d.lq - i, a.width);
-        if (threadIdx.x < BM) {
-            const long long q = d.qlo + min(i + (int)threadIdx.x, d.lq - 1);
+        const int tid = fresh(threadIdx.x);
+        if (tid < BM) {
+            const long long q = d.qlo + min(i + tid, d.lq - 1);
             s_lse = a.lse[q * a.heads + head];
             s_delta = a.delta[q * a.heads + head];
             s_pos = load_pos<AX>(a.q_pos, a.qp_st, a.qp_sa, a.axes, q);
@@ -844,7 +941,10 @@ __global__ __launch_bounds__(64 * NW, NW == 4 && W < 128 ? 2 : 1) void k_att_gra
     uint2 kpos = make_uint2(0, 0);
     if (AX && t1 > 0) kpos = pack_pos(load_pos<AX>(a.k_pos, a.kp_st, a.kp_sa, a.axes, token));
     float slope2 = AX ? a.slopes[kvh * a.group] * kLog2e : 0.0f;
-    settle(kf);
+    if (kKeep)
+        keep(kept[wave], lane, kf);
+    else
+        settle(kf);
     settle(vf);
     asm volatile("" : "+v"(kpos.x), "+v"(kpos.y), "+v"(slope2));
 
@@ -857,12 +957,13 @@ __global__ __launch_bounds__(64 * NW, NW == 4 && W < 128 ? 2 : 1) void k_att_gra
     int g = 0, i = first_tile * BM;
     for (int t = 0; t < t1; ++t) {
         const int buf = t & 1;
-        if (threadIdx.x < BM) {
-            rlse[buf][threadIdx.x] = s_lse * kLog2e - kLift;
-            rdelta[buf][threadIdx.x] = -s_delta;
+        const int tid = fresh(threadIdx.x);
+        if (tid < BM) {
+            rlse[buf][tid] = s_lse * kLog2e - kLift;
+            rdelta[buf][tid] = -s_delta;
             const uint2 pos = pack_pos(s_pos);
-            if (AX) rpx[buf][threadIdx.x] = pos.x;
-            if (AX == 3) rpy[buf][threadIdx.x] = pos.y;
+            if (AX) rpx[buf][tid] = pos.x;
+            if (AX == 3) rpy[buf][tid] = pos.y;
         }
         landed();
         __syncthreads();
@@ -870,67 +971,75 @@ __global__ __launch_bounds__(64 * NW, NW == 4 && W < 128 ? 2 : 1) void k_att_gra
         if (t + 1 < t1) fetch(t + 1, turn ? g + 1 : g, turn ? first_tile * BM : i + BM);
 
         const int ln = fresh(lane);
-        acc16 s, dp, bent, sub;
-        vec8 rows[kSteps], col[2][kBlocks];
-        read_rows(tq[buf], 0, ln, rows);
-        fence();
+        const unsigned q_at = lds_address(tq[0]) + rows_place(ln) + buf * sizeof(tq[0]);
+        const unsigned g_at = lds_address(tg[0]) + rows_place(ln) + buf * sizeof(tg[0]);
+        uint2 qt_at = columns_place(ln), gt_at = qt_at;
+        qt_at.x += lds_address(tq[0]) + buf * sizeof(tq[0]), qt_at.y += lds_address(tq[0]) + buf * sizeof(tq[0]);
+        gt_at.x += lds_address(tg[0]) + buf * sizeof(tg[0]), gt_at.y += lds_address(tg[0]) + buf * sizeof(tg[0]);
+        acc16 s, dp, bent;
 #pragma unroll
         for (int r = 0; r < 16; ++r) s[r] = 0.0f;
-#pragma unroll
-        for (int k = 0; k < kSteps; ++k) s = mma(rows[k], kf[k], s);
-        read_rows(tg[buf], 0, ln, rows);
+        if (kKeep)
+            product_kept(s, q_at, 0, kept[wave], ln);
+        else
+            product(s, q_at, 0, kf);
+        if (CAP) {
+            cap_block(a, s);
+            bent = s;
+        }
+        const float by = CAP ? a.cap2 : a.scale2;
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
             const float4 ls = *(const float4*)(rlse[buf] + 8 * q + 4 * half);
-            sub[4 * q + 0] = -ls.x, sub[4 * q + 1] = -ls.y, sub[4 * q + 2] = -ls.z, sub[4 * q + 3] = -ls.w;
+            float t[4] = {-ls.x, -ls.y, -ls.z, -ls.w};
+            if (AX) {
+                const uint4 x = *(const uint4*)(rpx[buf] + 8 * q + 4 * half);
+                uint4 y = make_uint4(0, 0, 0, 0);
+                if (AX == 3) y = *(const uint4*)(rpy[buf] + 8 * q + 4 * half);
+                t[0] = __builtin_fmaf(-slope2, distance<AX>(kpos, x.x, y.x), t[0]);
+                t[1] = __builtin_fmaf(-slope2, distance<AX>(kpos, x.y, y.y), t[1]);
+                t[2] = __builtin_fmaf(-slope2, distance<AX>(kpos, x.z, y.z), t[2]);
+                t[3] = __builtin_fmaf(-slope2, distance<AX>(kpos, x.w, y.w), t[3]);
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) s[4 * q + j] = exp2_(__builtin_fmaf(s[4 * q + j], by, t[j]));
+        }
+        // every row of the tile sees every key of the block?
+        const bool masked = i + BM > d.lq || key_limit(a, d, i) < min(key0 + kAttRows * NW, lk);
+        unsigned seen = 0xffffu;
+        if (masked) {
+            seen = 0;
+#pragma unroll
+            for (int r = 0; r < 16; ++r) {
+                const int q = i + 8 * (r / 4) + 4 * half + r % 4;
+                if (q < d.lq && key < key_limit(a, d, q)) seen |= 1u << r;
+            }
+#pragma unroll
+            for (int r = 0; r < 16; ++r)
+                if (!(seen >> r & 1)) s[r] = 0.0f;
+        }
+        vec8 col[2][kBlocks];
+        read_columns(gt_at, 0, col[0]);
+        read_columns(gt_at, 16, col[1]);
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+            const vec8 p = round8(s, c);
+            fence();
+#pragma unroll
+            for (int b = 0; b < kBlocks; ++b) gv[b] = mma(col[c][b], p, gv[b]);
         }
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
             const float4 de = *(const float4*)(rdelta[buf] + 8 * q + 4 * half);
             dp[4 * q + 0] = de.x, dp[4 * q + 1] = de.y, dp[4 * q + 2] = de.z, dp[4 * q + 3] = de.w;
         }
+        product(dp, g_at, 0, vf);
+        read_columns(qt_at, 0, col[0]);
         fence();
+        if (masked) {
 #pragma unroll
-        for (int k = 0; k < kSteps; ++k) dp = mma(rows[k], vf[k], dp);
-        read_columns(tg[buf], 0, ln, col[0]);
-        fence();
-        if (CAP) {
-            cap_block(a, s);
-            bent = s;
-        }
-        if (AX) {
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const uint4 x = *(const uint4*)(rpx[buf] + 8 * q + 4 * half);
-                uint4 y = make_uint4(0, 0, 0, 0);
-                if (AX == 3) y = *(const uint4*)(rpy[buf] + 8 * q + 4 * half);
-                sub[4 * q + 0] = __builtin_fmaf(-slope2, distance<AX>(kpos, x.x, y.x), sub[4 * q + 0]);
-                sub[4 * q + 1] = __builtin_fmaf(-slope2, distance<AX>(kpos, x.y, y.y), sub[4 * q + 1]);
-                sub[4 * q + 2] = __builtin_fmaf(-slope2, distance<AX>(kpos, x.z, y.z), sub[4 * q + 2]);
-                sub[4 * q + 3] = __builtin_fmaf(-slope2, distance<AX>(kpos, x.w, y.w), sub[4 * q + 3]);
-            }
-        }
-        const float by = CAP ? a.cap2 : a.scale2;
-#pragma unroll
-        for (int r = 0; r < 16; ++r) s[r] = exp2_(__builtin_fmaf(s[r], by, sub[r]));
-        // every row of the tile sees every key of the block?
-        if (i + BM > d.lq || key_limit(a, d, i) < min(key0 + kAttRows * NW, lk)) {
-#pragma unroll
-            for (int r = 0; r < 16; ++r) {
-                const int q = i + 8 * (r / 4) + 4 * half + r % 4;
-                if (q >= d.lq || key >= key_limit(a, d, q)) s[r] = dp[r] = 0.0f;
-            }
-        }
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-            if (c == 0)
-                read_columns(tg[buf], 16, ln, col[1]);
-            else
-                read_columns(tq[buf], 0, ln, col[0]);
-            const vec8 p = round8(s, c);
-            fence();
-#pragma unroll
-            for (int b = 0; b < kBlocks; ++b) gv[b] = mma(col[c][b], p, gv[b]);
+            for (int r = 0; r < 16; ++r)
+                if (!(seen >> r & 1)) dp[r] = 0.0f;
         }
 #pragma unroll
         for (int r = 0; r < 16; ++r) dp[r] *= s[r];
@@ -940,7 +1049,7 @@ __global__ __launch_bounds__(64 * NW, NW == 4 && W < 128 ? 2 : 1) void k_att_gra
         }
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-            if (c == 0) read_columns(tq[buf], 16, ln, col[1]);
+            if (c == 0) read_columns(qt_at, 16, col[1]);
             const vec8 ds = round8(dp, c);
             fence();
 #pragma unroll
