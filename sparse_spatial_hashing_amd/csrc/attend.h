@@ -19,7 +19,8 @@ struct AttArgs {
     void* gk;
     void* gv;
     float* delta;         // [tq, heads]: sum of grad_out * out
-    float* part_o;        // split partials: [nsplit, tq * heads, width] f32
+    float* part_o;        // split partials, f32: [nsplit, tq * heads, width] (forward), or of
+                          // grad_k, then of grad_v, [nsplit, tk * kv_heads, width]
     float* part_ml;       // [nsplit, tq * heads, 2]: running maximum (base 2) and sum
     const int* q_offsets;
     const int* k_offsets;
@@ -30,10 +31,11 @@ struct AttArgs {
     long long q_st, q_sh, k_st, k_sh, v_st, v_sh, g_st, g_sh;
     long long qp_st, qp_sa, kp_st, kp_sa;
     int tq, tk, docs, heads, kv_heads, group, width, mask, axes;
-    int nsplit;           // key ranges a document's keys are split into (forward)
+    int nsplit;           // ranges a document's keys (forward) or queries (dK dV) are split into
     int tiles;            // row tiles (forward, dQ) or key tiles (dK dV) over all documents
     float scale;          // > 0
     float scale2;         // scale * log2(e)
+    float unscale2;       // 1 / scale2
     float cap_in;         // scale / cap
     float cap2;           // cap * log2(e); 0: no cap
 };

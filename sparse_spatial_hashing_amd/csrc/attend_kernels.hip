@@ -210,12 +210,22 @@ __device__ __forceinline__ uint2 pack_pos(int3 p) {
                       (unsigned)clampi(p.z, 0, 65535));
 }
 
-// |a - b| summed over the axes.
+// -slope2 |a - b|, the distance summed over the axes. The sums of absolute
+// differences (below 2^23) are added to the bits of 1.0, so f = 1 + d 2^-23
+// exactly, and with steep = slope2 2^23 one product-sum gives the bias rounded
+// once: no conversion.
 template <int AX>
-__device__ __forceinline__ float distance(uint2 p, unsigned x, unsigned y) {
-    unsigned d = __builtin_amdgcn_sad_u16(p.x, x, 0u);
+__device__ __forceinline__ float bias(uint2 p, unsigned x, unsigned y, float steep) {
+    unsigned d = __builtin_amdgcn_sad_u16(p.x, x, 0x3f800000u);
     if (AX == 3) d = __builtin_amdgcn_sad_u16(p.y, y, d);
-    return (float)d;
+    return __builtin_fmaf(__uint_as_float(d), -steep, steep);
+}
+
+// Scores are wanted less a number of the row. With a bias and no cap it goes
+// into the product's first summand; else into scores().
+template <int AX, bool CAP>
+__device__ __forceinline__ float first_summand(const AttArgs& a, float sub) {
+    return AX && !CAP ? -sub * a.unscale2 : 0.0f;
 }
 
 // tanh(u), u = score / cap, for a block's scores at once: where all are small,
@@ -340,28 +350,28 @@ __device__ __forceinline__ void product(acc16& s, unsigned at, int row0, const v
 // Operands B that a wavefront keeps in LDS instead of registers, each lane its
 // own: at a width of 128 the backward's four sets and its sums do not fit the
 // 256 registers that let two wavefronts share a SIMD.
-constexpr int kKept = 64 * kSteps;  // 16-byte pieces per wavefront
+// FROM, COUNT: the steps kept.
+template <int FROM, int COUNT>
 __device__ __forceinline__ void keep(uint4* kept, int lane, const vec8 (&x)[kSteps]) {
 #pragma unroll
-    for (int k = 0; k < kSteps; ++k) kept[64 * k + lane] = __builtin_bit_cast(uint4, x[k]);
+    for (int k = 0; k < COUNT; ++k) kept[64 * k + lane] = __builtin_bit_cast(uint4, x[FROM + k]);
 }
-// s += rows of the tile times the kept operand, two steps read ahead.
-__device__ __forceinline__ void product_kept(acc16& s, unsigned at, int row0, const uint4* kept, int lane) {
-    vec8 x[2][2], y[2][2];
-    auto read = [&](int j) {
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            x[j & 1][i] = lds_rows(at, row0, 2 * j + i);
-            y[j & 1][i] = __builtin_bit_cast(vec8, kept[64 * (2 * j + i) + lane]);
-        }
+// s += rows of the tile times an operand whose first COUNT steps are kept and
+// whose others are in f; a step read ahead.
+template <int COUNT>
+__device__ __forceinline__ void product_kept(acc16& s, unsigned at, int row0, const uint4* kept, int lane,
+                                             const vec8 (&f)[kSteps]) {
+    vec8 x[2], y[2];
+    auto read = [&](int k) {
+        x[k & 1] = lds_rows(at, row0, k);
+        if (k < COUNT) y[k & 1] = __builtin_bit_cast(vec8, kept[64 * k + lane]);
     };
     read(0);
 #pragma unroll
-    for (int j = 0; j < kSteps / 2; ++j) {
-        if (j + 1 < kSteps / 2) read(j + 1);
+    for (int k = 0; k < kSteps; ++k) {
+        if (k + 1 < kSteps) read(k + 1);
         fence();
-#pragma unroll
-        for (int i = 0; i < 2; ++i) s = mma(x[j & 1][i], y[j & 1][i], s);
+        s = mma(x[k & 1], k < COUNT ? y[k & 1] : f[k], s);
     }
 }
 
@@ -385,7 +395,7 @@ struct Row {
     bool real;
     long long token;     // of a row that exists (clamped)
     int limit;           // visible keys
-    float slope2;
+    float steep;         // slope log2(e) 2^23
     uint2 pos;
 };
 
@@ -399,44 +409,43 @@ __device__ __forceinline__ Row get_row(const AttArgs& a, const Range& d, int kvh
     w.head = kvh * a.group + rr % a.group;
     w.token = d.qlo + w.i;
     w.limit = w.real ? key_limit(a, d, w.i) : 0;
-    w.slope2 = 0.0f;
+    w.steep = 0.0f;
     w.pos = make_uint2(0, 0);
     if (AX) {
-        w.slope2 = a.slopes[w.head] * kLog2e;
+        w.steep = a.slopes[w.head] * kLog2e * 0x1p23f;
         w.pos = pack_pos(load_pos<AX>(a.q_pos, a.qp_st, a.qp_sa, a.axes, w.token));
     }
     return w;
 }
 
-// Base-2 scores less `sub` of a 32-key block, in place. AX: 0 no bias, 2 one or
-// two axes, 3 three. kpx, kpy: the block's packed key positions. CAP: bent
-// receives tanh(score / cap).
+// Base-2 scores less `sub` of a 32-key block, in place, from products that
+// started with first_summand(sub). AX: 0 no bias, 2 one or two axes, 3 three.
+// kpx, kpy: the block's packed key positions. CAP: bent receives
+// tanh(score / cap).
 template <int AX, bool CAP>
 __device__ __forceinline__ void scores(const AttArgs& a, acc16& s, acc16& bent, const Row& row,
                                        float sub, const unsigned* kpx, const unsigned* kpy, int half) {
-    acc16 t;
-    if (AX) {
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            const uint4 x = *(const uint4*)(kpx + 8 * q + 4 * half);
-            uint4 y = make_uint4(0, 0, 0, 0);
-            if (AX == 3) y = *(const uint4*)(kpy + 8 * q + 4 * half);
-            t[4 * q + 0] = __builtin_fmaf(-row.slope2, distance<AX>(row.pos, x.x, y.x), -sub);
-            t[4 * q + 1] = __builtin_fmaf(-row.slope2, distance<AX>(row.pos, x.y, y.y), -sub);
-            t[4 * q + 2] = __builtin_fmaf(-row.slope2, distance<AX>(row.pos, x.z, y.z), -sub);
-            t[4 * q + 3] = __builtin_fmaf(-row.slope2, distance<AX>(row.pos, x.w, y.w), -sub);
-        }
-    } else {
-#pragma unroll
-        for (int r = 0; r < 16; ++r) t[r] = -sub;
-    }
     if (CAP) {
         cap_block(a, s);
         bent = s;
     }
     const float by = CAP ? a.cap2 : a.scale2;
+    if (!AX) {
 #pragma unroll
-    for (int r = 0; r < 16; ++r) s[r] = __builtin_fmaf(s[r], by, t[r]);
+        for (int r = 0; r < 16; ++r) s[r] = __builtin_fmaf(s[r], by, -sub);
+        return;
+    }
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        const uint4 x = *(const uint4*)(kpx + 8 * q + 4 * half);
+        uint4 y = make_uint4(0, 0, 0, 0);
+        if (AX == 3) y = *(const uint4*)(kpy + 8 * q + 4 * half);
+        const float t[4] = {bias<AX>(row.pos, x.x, y.x, row.steep), bias<AX>(row.pos, x.y, y.y, row.steep),
+                            bias<AX>(row.pos, x.z, y.z, row.steep), bias<AX>(row.pos, x.w, y.w, row.steep)};
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            s[4 * q + j] = __builtin_fmaf(s[4 * q + j], by, CAP ? t[j] - sub : t[j]);
+    }
 }
 
 // Scores of keys from `limit` on become -inf; key0: the block's first key.
@@ -461,7 +470,7 @@ __device__ __forceinline__ long long xcd_block(long long bid, long long n) {
 // Key tiles are loaded one ahead into the other half of LDS.
 
 template <int AX, bool CAP, int NW, int BN>
-__global__ __launch_bounds__(64 * NW, 2) void k_att_forward(AttArgs a) {
+__global__ __launch_bounds__(64 * NW, NW == 4 && (W < 128 || AX == 0) ? 3 : 2) void k_att_forward(AttArgs a) {
     constexpr int NT = 64 * NW;
     constexpr int NB = BN / 32;
     typedef Tile<BN, NT> KeyTile;
@@ -534,20 +543,18 @@ __global__ __launch_bounds__(64 * NW, 2) void k_att_forward(AttArgs a) {
         __syncthreads();  // this tile is there, and all are done with the one before
         if (t + 1 < t1) fetch(t + 1);
 
-        const unsigned k_at = lds_address(tk[0]) + rows_place(lane) + buf * sizeof(tk[0]);
-        uint2 v_at = columns_place(lane);
+        const int ln = fresh(lane);
+        const unsigned k_at = lds_address(tk[0]) + rows_place(ln) + buf * sizeof(tk[0]);
+        uint2 v_at = columns_place(ln);
         v_at.x += lds_address(tv[0]) + buf * sizeof(tv[0]), v_at.y += lds_address(tv[0]) + buf * sizeof(tv[0]);
         acc16 s[NB];
-        vec8 kf[NB][kSteps], vf[2][kBlocks];
-#pragma unroll
-        for (int nb = 0; nb < NB; ++nb) read_rows(k_at, 32 * nb, kf[nb]);
-        fence();
+        vec8 vf[2][kBlocks];
+        const float start = first_summand<AX, CAP>(a, m);
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) {
 #pragma unroll
-            for (int r = 0; r < 16; ++r) s[nb][r] = 0.0f;
-#pragma unroll
-            for (int k = 0; k < kSteps; ++k) s[nb] = mma(kf[nb][k], qf[k], s[nb]);
+            for (int r = 0; r < 16; ++r) s[nb][r] = start;
+            product(s[nb], k_at, 32 * nb, qf);
         }
         read_columns(v_at, 0, vf[0]);
         fence();
@@ -695,7 +702,9 @@ __global__ __launch_bounds__(64 * NW, NW == 4 || W < 128 ? 2 : 1) void k_att_gra
     __shared__ __align__(16) unsigned kpx[2][AX ? BN : 4], kpy[2][AX == 3 ? BN : 4];
 
     constexpr bool kKeep = W == 128 && NW == 4;
-    __shared__ uint4 kept[kKeep ? NW : 1][kKeep ? kKept : 1];
+    constexpr int kKeepQ = kKeep ? 3 : 0;  // of q's steps, what LDS has left for two blocks a CU
+    __shared__ uint4 kept[kKeep ? NW : 1][kKeep ? 64 * kSteps : 1];
+    __shared__ uint4 kept_q[kKeep ? NW : 1][kKeep ? 64 * kKeepQ : 1];
 
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, half = lane >> 5;
     const long long id = xcd_block(blockIdx.x, gridDim.x);
@@ -748,12 +757,15 @@ __global__ __launch_bounds__(64 * NW, NW == 4 || W < 128 ? 2 : 1) void k_att_gra
     delta += other_half(delta);
     float lse2 = a.lse[at] * kLog2e - kLift;
     settle(qf);
-    if (kKeep)
-        keep(kept[wave], lane, gf);
-    else
+    if constexpr (kKeep) {
+        keep<0, kSteps>(kept[wave], lane, gf);
+        keep<0, kKeepQ>(kept_q[wave], lane, qf);
+    } else {
         settle(gf);
+    }
     asm volatile("" : "+v"(lse2));
 
+    const float start = first_summand<AX, CAP>(a, lse2);
     acc16 o[kBlocks], pk[kBlocks];
     float rest = 0.0f;
 #pragma unroll
@@ -782,8 +794,11 @@ __global__ __launch_bounds__(64 * NW, NW == 4 || W < 128 ? 2 : 1) void k_att_gra
         for (int nb = 0; nb < NB; ++nb) {
             acc16 s, dp, bent;
 #pragma unroll
-            for (int r = 0; r < 16; ++r) s[r] = 0.0f;
-            product(s, k_at, 32 * nb, qf);
+            for (int r = 0; r < 16; ++r) s[r] = start;
+            if constexpr (kKeep)
+                product_kept<kKeepQ>(s, k_at, 32 * nb, kept_q[wave], ln, qf);
+            else
+                product(s, k_at, 32 * nb, qf);
             scores<AX, CAP>(a, s, bent, row, lse2, kpx[buf] + (AX ? 32 * nb : 0),
                             kpy[buf] + (AX == 3 ? 32 * nb : 0), half);
 #pragma unroll
@@ -799,10 +814,16 @@ __global__ __launch_bounds__(64 * NW, NW == 4 || W < 128 ? 2 : 1) void k_att_gra
                 for (int r = 0; r < 16; ++r) bent[r] = __builtin_fmaf(-bent[r], bent[r], 1.0f);
             }
             vec8 kt[2][kBlocks];
-            read_columns(kt_at, 32 * nb, kt[0]);
-            read_columns(kt_at, 32 * nb + 16, kt[1]);
+            if (!kKeep) {
+                read_columns(kt_at, 32 * nb, kt[0]);
+                read_columns(kt_at, 32 * nb + 16, kt[1]);
+            }
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
+                if (kKeep) {  // read when used, and again below: registers for one set
+                    fence();
+                    read_columns(kt_at, 32 * nb + 16 * c, kt[c]);
+                }
                 acc16 flat = s;
                 if (CAP) {
 #pragma unroll
@@ -815,14 +836,10 @@ __global__ __launch_bounds__(64 * NW, NW == 4 || W < 128 ? 2 : 1) void k_att_gra
             }
 #pragma unroll
             for (int r = 0; r < 16; ++r) dp[r] = -delta;
-            if (kKeep)
-                product_kept(dp, v_at, 32 * nb, kept[wave], ln);
+            if constexpr (kKeep)
+                product_kept<kSteps>(dp, v_at, 32 * nb, kept[wave], ln, gf);
             else
                 product(dp, v_at, 32 * nb, gf);
-            if (kKeep) {  // again: no registers to hold them
-                read_columns(kt_at, 32 * nb, kt[0]);
-                read_columns(kt_at, 32 * nb + 16, kt[1]);
-            }
             fence();
             if (masked) {
 #pragma unroll
@@ -840,6 +857,10 @@ __global__ __launch_bounds__(64 * NW, NW == 4 || W < 128 ? 2 : 1) void k_att_gra
             }
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
+                if (kKeep) {
+                    fence();
+                    read_columns(kt_at, 32 * nb + 16 * c, kt[c]);
+                }
                 const vec8 ds = round8(dp, c);
                 fence();
 #pragma unroll
@@ -884,10 +905,12 @@ __global__ __launch_bounds__(64 * NW, NW == 4 || W < 128 ? 2 : 1) void k_att_gra
     __shared__ __align__(16) unsigned rpx[2][BM], rpy[2][BM];
 
     constexpr bool kKeep = W == 128 && NW == 4;
-    __shared__ uint4 kept[kKeep ? NW : 1][kKeep ? kKept : 1];
+    __shared__ uint4 kept[kKeep ? NW : 1][kKeep ? 64 * kSteps : 1];
 
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, half = lane >> 5;
-    const long long id = xcd_block(blockIdx.x, gridDim.x);
+    long long id = xcd_block(blockIdx.x, gridDim.x);
+    const int split = (int)(id % a.nsplit);
+    id /= a.nsplit;
     const int tile = (int)(id % a.tiles);  // causal: the first keys have the most rows
     const int kvh = (int)(id / a.tiles);
     int first;
@@ -905,7 +928,11 @@ __global__ __launch_bounds__(64 * NW, NW == 4 || W < 128 ? 2 : 1) void k_att_gra
     int i0 = 0;
     if (a.mask && d.prefix <= key0) i0 = max(0, key0 - (d.lk - d.lq));
     const int first_tile = i0 / BM, per_head = max(0, (d.lq + BM - 1) / BM - first_tile);
-    const int t1 = per_head * a.group;
+    // this split's share of the tiles
+    const long long tiles = (long long)per_head * a.group;
+    const int t0 = (int)(tiles * split / a.nsplit), t1 = (int)(tiles * (split + 1) / a.nsplit);
+    int g = per_head > 0 ? t0 / per_head : 0;
+    int i = (first_tile + t0 - g * per_head) * BM;
 
     float s_lse = 0.0f, s_delta = 0.0f;
     int3 s_pos = make_int3(0, 0, 0);
@@ -928,7 +955,7 @@ __global__ __launch_bounds__(64 * NW, NW == 4 || W < 128 ? 2 : 1) void k_att_gra
         RowTile::clear(tg[b], a.width);
     }
     if (a.width < W) __syncthreads();
-    if (t1 > 0) fetch(0, 0, first_tile * BM);
+    if (t0 < t1) fetch(t0, g, i);
 
     vec8 kf[kSteps], vf[kSteps];
     const elem* krow = (const elem*)a.k + token * a.k_st + kvh * a.k_sh;
@@ -939,14 +966,14 @@ __global__ __launch_bounds__(64 * NW, NW == 4 || W < 128 ? 2 : 1) void k_att_gra
         vf[k] = load_chunk(vrow, 2 * k + half, a.width);
     }
     uint2 kpos = make_uint2(0, 0);
-    if (AX && t1 > 0) kpos = pack_pos(load_pos<AX>(a.k_pos, a.kp_st, a.kp_sa, a.axes, token));
-    float slope2 = AX ? a.slopes[kvh * a.group] * kLog2e : 0.0f;
-    if (kKeep)
-        keep(kept[wave], lane, kf);
+    if (AX && t0 < t1) kpos = pack_pos(load_pos<AX>(a.k_pos, a.kp_st, a.kp_sa, a.axes, token));
+    float steep = AX && t0 < t1 ? a.slopes[kvh * a.group + g] * kLog2e * 0x1p23f : 0.0f;
+    if constexpr (kKeep)
+        keep<0, kSteps>(kept[wave], lane, kf);
     else
         settle(kf);
     settle(vf);
-    asm volatile("" : "+v"(kpos.x), "+v"(kpos.y), "+v"(slope2));
+    asm volatile("" : "+v"(kpos.x), "+v"(kpos.y), "+v"(steep));
 
     acc16 gk[kBlocks], gv[kBlocks];
 #pragma unroll
@@ -954,12 +981,12 @@ __global__ __launch_bounds__(64 * NW, NW == 4 || W < 128 ? 2 : 1) void k_att_gra
 #pragma unroll
         for (int r = 0; r < 16; ++r) gk[b][r] = gv[b][r] = 0.0f;
 
-    int g = 0, i = first_tile * BM;
-    for (int t = 0; t < t1; ++t) {
+    for (int t = t0; t < t1; ++t) {
         const int buf = t & 1;
         const int tid = fresh(threadIdx.x);
         if (tid < BM) {
-            rlse[buf][tid] = s_lse * kLog2e - kLift;
+            const float lse2 = s_lse * kLog2e - kLift;
+            rlse[buf][tid] = AX && !CAP ? first_summand<AX, CAP>(a, lse2) : -lse2;
             rdelta[buf][tid] = -s_delta;
             const uint2 pos = pack_pos(s_pos);
             if (AX) rpx[buf][tid] = pos.x;
@@ -978,9 +1005,13 @@ __global__ __launch_bounds__(64 * NW, NW == 4 || W < 128 ? 2 : 1) void k_att_gra
         gt_at.x += lds_address(tg[0]) + buf * sizeof(tg[0]), gt_at.y += lds_address(tg[0]) + buf * sizeof(tg[0]);
         acc16 s, dp, bent;
 #pragma unroll
-        for (int r = 0; r < 16; ++r) s[r] = 0.0f;
-        if (kKeep)
-            product_kept(s, q_at, 0, kept[wave], ln);
+        for (int q = 0; q < 4; ++q) {
+            float4 ls = make_float4(0, 0, 0, 0);
+            if (AX && !CAP) ls = *(const float4*)(rlse[buf] + 8 * q + 4 * half);
+            s[4 * q + 0] = ls.x, s[4 * q + 1] = ls.y, s[4 * q + 2] = ls.z, s[4 * q + 3] = ls.w;
+        }
+        if constexpr (kKeep)
+            product_kept<kSteps>(s, q_at, 0, kept[wave], ln, kf);
         else
             product(s, q_at, 0, kf);
         if (CAP) {
@@ -990,16 +1021,19 @@ __global__ __launch_bounds__(64 * NW, NW == 4 || W < 128 ? 2 : 1) void k_att_gra
         const float by = CAP ? a.cap2 : a.scale2;
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-            const float4 ls = *(const float4*)(rlse[buf] + 8 * q + 4 * half);
-            float t[4] = {-ls.x, -ls.y, -ls.z, -ls.w};
+            float t[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+            if (!AX || CAP) {
+                const float4 ls = *(const float4*)(rlse[buf] + 8 * q + 4 * half);
+                t[0] = ls.x, t[1] = ls.y, t[2] = ls.z, t[3] = ls.w;
+            }
             if (AX) {
                 const uint4 x = *(const uint4*)(rpx[buf] + 8 * q + 4 * half);
                 uint4 y = make_uint4(0, 0, 0, 0);
                 if (AX == 3) y = *(const uint4*)(rpy[buf] + 8 * q + 4 * half);
-                t[0] = __builtin_fmaf(-slope2, distance<AX>(kpos, x.x, y.x), t[0]);
-                t[1] = __builtin_fmaf(-slope2, distance<AX>(kpos, x.y, y.y), t[1]);
-                t[2] = __builtin_fmaf(-slope2, distance<AX>(kpos, x.z, y.z), t[2]);
-                t[3] = __builtin_fmaf(-slope2, distance<AX>(kpos, x.w, y.w), t[3]);
+                const float u[4] = {bias<AX>(kpos, x.x, y.x, steep), bias<AX>(kpos, x.y, y.y, steep),
+                                    bias<AX>(kpos, x.z, y.z, steep), bias<AX>(kpos, x.w, y.w, steep)};
+#pragma unroll
+                for (int j = 0; j < 4; ++j) t[j] = CAP ? t[j] + u[j] : u[j];
             }
 #pragma unroll
             for (int j = 0; j < 4; ++j) s[4 * q + j] = exp2_(__builtin_fmaf(s[4 * q + j], by, t[j]));
@@ -1059,11 +1093,26 @@ __global__ __launch_bounds__(64 * NW, NW == 4 || W < 128 ? 2 : 1) void k_att_gra
         if (turn) {
             i = first_tile * BM;
             ++g;
-            if (AX && t + 1 < t1) slope2 = a.slopes[kvh * a.group + g] * kLog2e;
+            if (AX && t + 1 < t1) steep = a.slopes[kvh * a.group + g] * kLog2e * 0x1p23f;
         }
     }
     if (key >= lk) return;
     const long long at = token * a.kv_heads + kvh;
+    if (a.nsplit > 1) {
+        const long long n = (long long)a.tk * a.kv_heads;
+        float* pk = a.part_o + ((long long)split * n + at) * a.width;
+        float* pv = pk + (long long)a.nsplit * n * a.width;
+#pragma unroll
+        for (int b = 0; b < kBlocks; ++b)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const int c = 32 * b + 8 * q + 4 * half;
+                if (c >= a.width) continue;
+                *(float4*)(pk + c) = make_float4(gk[b][4 * q], gk[b][4 * q + 1], gk[b][4 * q + 2], gk[b][4 * q + 3]);
+                *(float4*)(pv + c) = make_float4(gv[b][4 * q], gv[b][4 * q + 1], gv[b][4 * q + 2], gv[b][4 * q + 3]);
+            }
+        return;
+    }
     elem* outk = (elem*)a.gk + at * a.width;
     elem* outv = (elem*)a.gv + at * a.width;
 #pragma unroll
@@ -1083,12 +1132,34 @@ __global__ __launch_bounds__(64 * NW, NW == 4 || W < 128 ? 2 : 1) void k_att_gra
         }
 }
 
+// Splits of grad_k and grad_v added in order, four elements per thread.
+__global__ __launch_bounds__(256) void k_att_join_kv(AttArgs a) {
+    const long long n = (long long)a.tk * a.kv_heads * a.width;
+    const long long at = 4 * ((long long)blockIdx.x * 256 + threadIdx.x);
+    if (at >= n) return;
+    const float* parts[2] = {a.part_o + at, a.part_o + a.nsplit * n + at};
+    elem* outs[2] = {(elem*)a.gk + at, (elem*)a.gv + at};
+    const float by[2] = {a.scale * kUnlift, kUnlift};
+#pragma unroll
+    for (int w = 0; w < 2; ++w) {
+        float4 sum = *(const float4*)parts[w];
+        for (int s = 1; s < a.nsplit; ++s) {
+            const float4 x = *(const float4*)(parts[w] + s * n);
+            sum.x += x.x, sum.y += x.y, sum.z += x.z, sum.w += x.w;
+        }
+        vec4 r;
+        r[0] = (elem)(sum.x * by[w]), r[1] = (elem)(sum.y * by[w]);
+        r[2] = (elem)(sum.z * by[w]), r[3] = (elem)(sum.w * by[w]);
+        *(vec4*)outs[w] = r;
+    }
+}
+
 template <int AX, bool CAP, int NW>
 hipError_t launch(AttPass pass, const AttArgs& a, hipStream_t stream) {
     // keys of a tile: 64 where two tiles of k and v, twice, leave LDS for two blocks
     constexpr int BN = NW == 4 && W <= 64 ? 64 : 32;
     const dim3 block(64 * NW);
-    const long long blocks = (long long)a.tiles * a.kv_heads * (pass == kAttForward ? a.nsplit : 1);
+    const long long blocks = (long long)a.tiles * a.kv_heads * (pass == kAttGradQ ? 1 : a.nsplit);
     if (blocks <= 0 || blocks > 0x7fffffffll) return hipErrorInvalidValue;
     const dim3 grid((unsigned)blocks);
     if (pass == kAttForward) {
@@ -1103,6 +1174,12 @@ hipError_t launch(AttPass pass, const AttArgs& a, hipStream_t stream) {
         k_att_grad_q<AX, CAP, NW, BN><<<grid, block, 0, stream>>>(a);
     } else {
         k_att_grad_kv<AX, CAP, NW><<<grid, block, 0, stream>>>(a);
+        if (a.nsplit > 1) {
+            const hipError_t e = hipGetLastError();
+            if (e != hipSuccess) return e;
+            const long long n = (long long)a.tk * a.kv_heads * a.width / 4;
+            k_att_join_kv<<<dim3((unsigned)((n + 255) / 256)), dim3(256), 0, stream>>>(a);
+        }
     }
     return hipGetLastError();
 }

@@ -169,6 +169,15 @@ def test_attend_long(dtype, width, axes, cap, mask):
     _compare(s, q_at, k_at, more, cap, f"attend long w {width} axes {axes} cap {cap} {mask} {dtype}")
 
 
+@pytest.mark.parametrize("width,axes,cap,mask", [(128, 0, 0.0, "causal"), (64, 2, 0.0, "full"),
+                                                 (32, 0, 20.0, "prefix")])
+def test_attend_split_queries(width, axes, cap, mask):
+    """Few key blocks and many queries: grad_k and grad_v from parts."""
+    for lens in ([1100], [1500, 40, 0]):
+        s, q_at, k_at, more = _inputs(lens, lens, 4, 2, width, BF16, 12, axes, mask, first=2)
+        _compare(s, q_at, k_at, more, cap, f"attend split {lens} w {width} {mask}")
+
+
 @pytest.mark.parametrize("q_len", [1, 5])
 @pytest.mark.parametrize("heads,kv_heads,width,axes,cap", [(16, 4, 128, 0, 0.0), (8, 8, 64, 2, 0.0),
                                                            (4, 1, 80, 0, 20.0), (2, 2, 32, 3, 0.0)])
