@@ -656,17 +656,36 @@ __global__ __launch_bounds__(256) void k_att_join(AttArgs a) {
     const long long at = (long long)blockIdx.x * 4 + (threadIdx.x >> 6);
     if (at >= n) return;
     const int lane = threadIdx.x & 63;
-    float m = kLowest;
-    for (int s = 0; s < a.nsplit; ++s) m = fmaxf(m, a.part_ml[2 * (s * n + at)]);
-    float l = 0.0f, x = 0.0f, y = 0.0f;
-    for (int s = 0; s < a.nsplit; ++s) {
-        const float w = exp2_(a.part_ml[2 * (s * n + at)] - m);
-        const float* part = a.part_o + (s * n + at) * a.width;
-        l = __builtin_fmaf(w, a.part_ml[2 * (s * n + at) + 1], l);
-        if (2 * lane < a.width) {
-            const float2 p = *(const float2*)(part + 2 * lane);
-            x = __builtin_fmaf(w, p.x, x);
-            y = __builtin_fmaf(w, p.y, y);
+    // lane s holds split s (there are at most 64)
+    float m = kLowest, l = 0.0f;
+    if (lane < a.nsplit) {
+        m = a.part_ml[2 * (lane * n + at)];
+        l = a.part_ml[2 * (lane * n + at) + 1];
+    }
+    float top = m;
+#pragma unroll
+    for (int off = 32; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor(top, off));
+    const float weight = exp2_(m - top);
+    m = top;
+    l *= weight;
+#pragma unroll
+    for (int off = 32; off > 0; off >>= 1) l += __shfl_xor(l, off);
+    float x = 0.0f, y = 0.0f;
+    for (int s0 = 0; s0 < a.nsplit; s0 += 8) {
+        float2 p[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const int s = min(s0 + j, a.nsplit - 1);
+            p[j] = make_float2(0.0f, 0.0f);
+            if (2 * lane < a.width) p[j] = *(const float2*)(a.part_o + (s * n + at) * a.width + 2 * lane);
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const float w = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(weight), min(s0 + j, 63)));
+            if (s0 + j < a.nsplit) {
+                x = __builtin_fmaf(w, p[j].x, x);
+                y = __builtin_fmaf(w, p[j].y, y);
+            }
         }
     }
     const float inv = 1.0f / l;
@@ -693,7 +712,7 @@ __global__ __launch_bounds__(256) void k_att_join(AttArgs a) {
 // 32 bits.
 
 template <int AX, bool CAP, int NW, int BN>
-__global__ __launch_bounds__(64 * NW, NW == 4 || W < 128 ? 2 : 1) void k_att_grad_q(AttArgs a) {
+__global__ __launch_bounds__(64 * NW, NW == 1 && W == 32 ? 3 : NW == 4 || W < 128 ? 2 : 1) void k_att_grad_q(AttArgs a) {
     constexpr int NT = 64 * NW;
     constexpr int NB = BN / 32;
     typedef Tile<BN, NT> KeyTile;
@@ -895,7 +914,7 @@ __global__ __launch_bounds__(64 * NW, NW == 4 || W < 128 ? 2 : 1) void k_att_gra
 // grad_k^T = Q^T dS.
 
 template <int AX, bool CAP, int NW>
-__global__ __launch_bounds__(64 * NW, NW == 4 || W < 128 ? 2 : 1) void k_att_grad_kv(AttArgs a) {
+__global__ __launch_bounds__(64 * NW, NW == 1 && W == 32 ? 3 : NW == 4 || W < 128 ? 2 : 1) void k_att_grad_kv(AttArgs a) {
     constexpr int NT = 64 * NW;
     constexpr int BM = 32;
     typedef Tile<BM, NT> RowTile;

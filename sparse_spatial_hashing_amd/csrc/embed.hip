@@ -40,29 +40,41 @@ constexpr long long kMaxWidth = 65536;
 
 // ------------------------------------------------------------------ lookup --
 
-// LPR lanes (a power of two) share a row of `pieces` pieces of N elements.
-template <typename T, int N, typename Id>
+// 2^lpr_log lanes share a row of `pieces` pieces of N elements, and R rows,
+// one block's rows apart, so that R loads are under way in a thread.
+template <typename T, int N, typename Id, int R>
 __global__ __launch_bounds__(kBlock) void k_embed(const T* __restrict__ table, long long rows,
                                                   int width, long long stride,
                                                   const Id* __restrict__ ids, long long n,
                                                   float scale, T* __restrict__ out, int lpr_log) {
     const int lpr = 1 << lpr_log;
     const int pieces = width / N;
-    const long long tid = (long long)blockIdx.x * kBlock + threadIdx.x;
-    const long long i = tid >> lpr_log;
-    if (i >= n) return;
-    const long long id = (long long)ids[i];
-    const bool in = id >= 0 && id < rows;
-    const T* src = table + (in ? id : 0) * stride;
-    T* dst = out + i * width;
-    for (int p = (int)(tid & (lpr - 1)); p < pieces; p += lpr) {
-        float x[N];
+    const int per = kBlock >> lpr_log;  // rows of the block at a time
+    const long long first = (long long)blockIdx.x * per * R + (threadIdx.x >> lpr_log);
+    long long id[R];
 #pragma unroll
-        for (int j = 0; j < N; ++j) x[j] = 0.0f;
-        if (in) Pack<T, N>::load(src + p * N, x);
+    for (int r = 0; r < R; ++r) {
+        const long long i = first + r * per;
+        id[r] = (long long)ids[i < n ? i : n - 1];
+    }
+    for (int p = threadIdx.x & (lpr - 1); p < pieces; p += lpr) {
+        typename Pack<T, N>::vec raw[R];
 #pragma unroll
-        for (int j = 0; j < N; ++j) x[j] = in ? x[j] * scale : 0.0f;
-        Pack<T, N>::store(dst + p * N, x);
+        for (int r = 0; r < R; ++r) {
+            const bool in = id[r] >= 0 && id[r] < rows;
+            raw[r] = Pack<T, N>::raw(table + (in ? id[r] : 0) * stride + p * N);
+        }
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const long long i = first + r * per;
+            if (i >= n) continue;
+            const bool in = id[r] >= 0 && id[r] < rows;
+            float x[N];
+            Pack<T, N>::wide(raw[r], x);
+#pragma unroll
+            for (int j = 0; j < N; ++j) x[j] = in ? x[j] * scale : 0.0f;
+            Pack<T, N>::store(out + i * width + p * N, x);
+        }
     }
 }
 
@@ -497,10 +509,18 @@ int embed_run(const void* table, long long rows, long long width, long long stri
     const long long pieces = width / N;
     int lpr_log = 0;
     while ((1 << lpr_log) < pieces && lpr_log < 8) ++lpr_log;
-    const long long blocks = ((n << lpr_log) + kBlock - 1) / kBlock;
+    // Four rows per thread once that leaves eight wavefronts for every SIMD.
+    const long long threads = n << lpr_log;
+    const int r = threads >= 4ll * 8 * 64 * 1024 ? 4 : 1;
+    const long long per = (long long)(kBlock >> lpr_log) * r, blocks = (n + per - 1) / per;
     if (blocks > 0x7fffffffll) return VOX_EINVAL;
-    k_embed<T, N, Id><<<dim3((unsigned)blocks), dim3(kBlock), 0, stream>>>(
-        (const T*)table, rows, (int)width, stride, (const Id*)ids, n, scale, (T*)out, lpr_log);
+    const dim3 grid((unsigned)blocks), block(kBlock);
+    if (r == 4)
+        k_embed<T, N, Id, 4><<<grid, block, 0, stream>>>((const T*)table, rows, (int)width, stride,
+                                                         (const Id*)ids, n, scale, (T*)out, lpr_log);
+    else
+        k_embed<T, N, Id, 1><<<grid, block, 0, stream>>>((const T*)table, rows, (int)width, stride,
+                                                         (const Id*)ids, n, scale, (T*)out, lpr_log);
     return fail(hipGetLastError());
 }
 
@@ -548,7 +568,7 @@ bool grad_plan(long long n, long long rows, long long width, GradPlan* p) {
     }
     p->tiles = (int)((n + kTile - 1) / kTile);
     // few tokens: short runs, or too few groups of lanes have work
-    p->run = n <= kSmall ? 8 : n <= 262144 ? 32 : 64;
+    p->run = n <= kSmall ? 8 : n <= 262144 ? 32 : 128;
     p->runs = (n + p->run - 1) / p->run;
     long long o = 0;
     auto take = [&](long long bytes) {

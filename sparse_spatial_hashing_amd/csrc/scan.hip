@@ -245,6 +245,7 @@ constexpr int kParts = 128, kHeld = 32;
 template <bool GRAD>
 __global__ __launch_bounds__(1024) void k_scan_join(ScanArgs a) {
     __shared__ float muls[kParts][8], adds[kParts][8];
+    __shared__ float group_mul[kParts / 8][8], group_add[kParts / 8][8];
     const int lane = threadIdx.x & 7, part = threadIdx.x >> 3;
     const int c = blockIdx.x * 8 + lane;
     const bool on = c < a.width;
@@ -273,9 +274,27 @@ __global__ __launch_bounds__(1024) void k_scan_join(ScanArgs a) {
     muls[part][lane] = mul;
     adds[part][lane] = add;
     __syncthreads();
+    // over the shares before it, in groups of 8 whose last folds the group
+    const int group = part & ~7;
+    float before_mul = 1.0f, before_add = 0.0f;
+#pragma unroll
+    for (int j = 0; j < 7; ++j) {
+        if (group + j < part) {
+            const float u1 = muls[group + j][lane];
+            before_add = enter(u1, adds[group + j][lane], before_add);
+            before_mul = forgets(u1) ? u1 : before_mul * u1;
+        }
+    }
+    if ((part & 7) == 7) {
+        group_mul[part >> 3][lane] = forgets(mul) ? mul : before_mul * mul;
+        group_add[part >> 3][lane] = enter(mul, add, before_add);
+    }
+    __syncthreads();
     float h = 0.0f;  // nothing enters the first chunk: it starts a range
-#pragma unroll 8
-    for (int p = 0; p < part; ++p) h = enter(muls[p][lane], adds[p][lane], h);
+#pragma unroll
+    for (int g = 0; g < kParts / 8 - 1; ++g)
+        if (g < part >> 3) h = enter(group_mul[g][lane], group_add[g][lane], h);
+    h = enter(before_mul, before_add, h);
     for (int k = k0; k < k1; k += kHeld) {
         if (k1 - k0 > kHeld) load(k);
 #pragma unroll
