@@ -144,8 +144,9 @@ __device__ __forceinline__ int boundary(const int* offsets, int docs, int total,
 // + range, is <= t: that leaves every range at least ceil(length * per / size)
 // tiles without anyone knowing the lengths on the host. 64 ranges are tried
 // at once.
-__device__ __forceinline__ int find_range(const int* offsets, int docs, int total, int per,
-                                          int size, int t, int* first_tile) {
+template <int SIZE>
+__device__ __forceinline__ int find_range(const int* offsets, int docs, int total, int per, int t,
+                                          int* first_tile) {
     int lo = 0, n = docs + 2;
     const int lane = __lane_id();
     int first = 0;
@@ -153,7 +154,7 @@ __device__ __forceinline__ int find_range(const int* offsets, int docs, int tota
         const int step = (n + 63) / 64;
         const int b = lo + lane * step;
         const bool in = lane * step < n;
-        const int f = in ? (int)((long long)boundary(offsets, docs, total, b) * per / size) + b
+        const int f = in ? (int)((unsigned long long)boundary(offsets, docs, total, b) * per / SIZE) + b
                          : 0x7fffffff;
         const unsigned long long hit = __ballot(in && f <= t);
         const int cnt = max(1, (int)__popcll(hit));
@@ -458,9 +459,9 @@ __device__ __forceinline__ void hide(acc16& s, int key0, int limit, int half) {
 
 // Logical block: which (split, row tile, key head); consecutive ones share
 // keys and run on one XCD.
-__device__ __forceinline__ long long xcd_block(long long bid, long long n) {
-    const long long q = n / 8, r = n % 8;
-    const long long x = bid % 8, y = bid / 8;
+__device__ __forceinline__ unsigned xcd_block(unsigned bid, unsigned n) {
+    const unsigned q = n / 8, r = n % 8;
+    const unsigned x = bid % 8, y = bid / 8;
     return x * q + (x < r ? x : r) + y;
 }
 
@@ -479,14 +480,14 @@ __global__ __launch_bounds__(64 * NW, NW == 4 && (W < 128 || AX == 0) ? 3 : 2) v
     __shared__ __align__(16) unsigned kpx[2][AX ? BN : 4], kpy[2][AX == 3 ? BN : 4];
 
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, half = lane >> 5;
-    long long id = xcd_block(blockIdx.x, gridDim.x);
+    unsigned id = xcd_block(blockIdx.x, gridDim.x);
     const int split = (int)(id % a.nsplit);
     id /= a.nsplit;
     const int tile = a.tiles - 1 - (int)(id % a.tiles);  // long causal rows first
     const int kvh = (int)(id / a.tiles);
 
     int first;
-    const int range = find_range(a.q_offsets, a.docs, a.tq, a.group, kAttRows * NW, tile, &first);
+    const int range = find_range<kAttRows * NW>(a.q_offsets, a.docs, a.tq, a.group, tile, &first);
     const Range d = get_range(a, range);
     const int rows = d.lq * a.group;
     const long long row0l = (long long)(tile - first) * kAttRows * NW;
@@ -726,11 +727,11 @@ __global__ __launch_bounds__(64 * NW, NW == 1 && W == 32 ? 3 : NW == 4 || W < 12
     __shared__ uint4 kept_q[kKeep ? NW : 1][kKeep ? 64 * kKeepQ : 1];
 
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, half = lane >> 5;
-    const long long id = xcd_block(blockIdx.x, gridDim.x);
+    const unsigned id = xcd_block(blockIdx.x, gridDim.x);
     const int tile = a.tiles - 1 - (int)(id % a.tiles);
     const int kvh = (int)(id / a.tiles);
     int first;
-    const int range = find_range(a.q_offsets, a.docs, a.tq, a.group, kAttRows * NW, tile, &first);
+    const int range = find_range<kAttRows * NW>(a.q_offsets, a.docs, a.tq, a.group, tile, &first);
     const Range d = get_range(a, range);
     const int rows = d.lq * a.group;
     const long long row0l = (long long)(tile - first) * kAttRows * NW;
@@ -927,13 +928,13 @@ __global__ __launch_bounds__(64 * NW, NW == 1 && W == 32 ? 3 : NW == 4 || W < 12
     __shared__ uint4 kept[kKeep ? NW : 1][kKeep ? 64 * kSteps : 1];
 
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, half = lane >> 5;
-    long long id = xcd_block(blockIdx.x, gridDim.x);
+    unsigned id = xcd_block(blockIdx.x, gridDim.x);
     const int split = (int)(id % a.nsplit);
     id /= a.nsplit;
     const int tile = (int)(id % a.tiles);  // causal: the first keys have the most rows
     const int kvh = (int)(id / a.tiles);
     int first;
-    const int range = find_range(a.k_offsets, a.docs, a.tk, 1, kAttRows * NW, tile, &first);
+    const int range = find_range<kAttRows * NW>(a.k_offsets, a.docs, a.tk, 1, tile, &first);
     Range d = get_range(a, range);
     const int lk = max(0, boundary(a.k_offsets, a.docs, a.tk, range + 1) - d.klo);
     const long long key0l = (long long)(tile - first) * kAttRows * NW;
