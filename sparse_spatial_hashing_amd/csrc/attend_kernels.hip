@@ -1177,13 +1177,13 @@ __global__ __launch_bounds__(256) void k_att_join_kv(AttArgs a) {
 template <int AX, bool CAP, int NW>
 hipError_t launch(AttPass pass, const AttArgs& a, hipStream_t stream) {
     // keys of a tile: 64 where two tiles of k and v, twice, leave LDS for two blocks
-    constexpr int BN = NW == 4 && W <= 64 ? 64 : 32;
+    constexpr int BN = NW == 4 && W <= 64 ? 64 : 32, BF = NW == 4 && (W <= 64 || AX) ? 64 : 32;
     const dim3 block(64 * NW);
     const long long blocks = (long long)a.tiles * a.kv_heads * (pass == kAttGradQ ? 1 : a.nsplit);
     if (blocks <= 0 || blocks > 0x7fffffffll) return hipErrorInvalidValue;
     const dim3 grid((unsigned)blocks);
     if (pass == kAttForward) {
-        k_att_forward<AX, CAP, NW, BN><<<grid, block, 0, stream>>>(a);
+        k_att_forward<AX, CAP, NW, BF><<<grid, block, 0, stream>>>(a);
         if (a.nsplit > 1) {
             const hipError_t e = hipGetLastError();
             if (e != hipSuccess) return e;
