@@ -45,6 +45,9 @@ class _Attention(ctypes.Structure):
                 ("q_pos_stride", ctypes.c_int64 * 2), ("k_pos_stride", ctypes.c_int64 * 2)]
 
 
+# the current device's index and a device's current stream, without objects for them
+_current_device, _current_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
+
 # The same layout, packed at once: filling the structure field by field costs
 # more than the call it is for.
 _PACK = struct.Struct("@4i2q2i3P2f3P2i12q")
@@ -74,39 +77,47 @@ def _declare(lib) -> None:
 _declare(_lib)
 
 
-def _on_gpu(name: str, t: torch.Tensor, like: Optional[torch.Tensor] = None) -> None:
+_HALF = {torch.bfloat16: 1, torch.float16: 2}
+
+
+def _on_gpu(name: str, t: torch.Tensor, index: int = -1) -> int:
+    """The index of the tensor's GPU; the one given, if one is."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if not t.is_cuda:
+    own = t.get_device()
+    if own < 0:
         raise ValueError(f"{name} must be on a GPU device")
-    if like is not None and t.device != like.device:
-        raise ValueError(f"{name} is on {t.device}, not on {like.device}")
+    if own != index and index >= 0:
+        raise ValueError(f"{name} is on cuda:{own}, not on cuda:{index}")
+    return own
 
 
-def _floating(name: str, t: torch.Tensor, types, like: Optional[torch.Tensor] = None) -> int:
-    _on_gpu(name, t, like)
-    if t.dtype not in types:
-        raise ValueError(f"{name} must be one of {', '.join(str(d) for d in types)}, not {t.dtype}")
-    if like is not None and t.dtype != like.dtype:
-        raise ValueError(f"{name} is {t.dtype}, not {like.dtype}")
-    return _DTYPES[t.dtype]
+def _floating(name: str, t: torch.Tensor, like: Optional[torch.Tensor] = None, types=_DTYPES) -> int:
+    """The element type's code; on like's device and of its type, if it is given."""
+    _on_gpu(name, t, -1 if like is None else like.get_device())
+    dtype = t.dtype
+    if dtype not in types:
+        raise ValueError(f"{name} must be one of {', '.join(str(d) for d in types)}, not {dtype}")
+    if like is not None and dtype != like.dtype:
+        raise ValueError(f"{name} is {dtype}, not {like.dtype}")
+    return types[dtype]
 
 
-def _offsets(name: str, t: Optional[torch.Tensor], like: torch.Tensor) -> Optional[torch.Tensor]:
+def _offsets(name: str, t: Optional[torch.Tensor], index: int) -> Optional[torch.Tensor]:
     if t is None:
         return None
-    _on_gpu(name, t, like)
+    _on_gpu(name, t, index)
     if t.dtype != torch.int32 or t.dim() != 1 or t.shape[0] < 2:
         raise ValueError(f"{name} must be an int32 tensor of at least 2 offsets")
     return t.contiguous()
 
 
 def _state(name: str, t: Optional[torch.Tensor], docs: int, width: int,
-           like: torch.Tensor) -> Optional[torch.Tensor]:
+           index: int) -> Optional[torch.Tensor]:
     if t is None:
         return None
-    _on_gpu(name, t, like)
-    if t.dtype != torch.float32 or tuple(t.shape) != (docs, width):
+    _on_gpu(name, t, index)
+    if t.dtype != torch.float32 or t.shape != (docs, width):
         raise ValueError(f"{name} must be a float32 tensor of shape {(docs, width)}")
     return t.contiguous()
 
@@ -125,15 +136,13 @@ def _size(n: int, what: str) -> int:
     return n
 
 
-def _call(f, what: str, like: torch.Tensor, *args) -> None:
-    """f(*args, stream) on the current stream of the tensor's device."""
-    index = like.device.index
-    stream = torch._C._cuda_getCurrentRawStream(index)
-    if torch._C._cuda_getDevice() == index:
-        rc = f(*args, stream)
+def _call(f, what: str, index: int, *args) -> None:
+    """f(*args, stream) on the current stream of that GPU."""
+    if _current_device() == index:
+        rc = f(*args, _current_stream(index))
     else:
         with torch.cuda.device(index):
-            rc = f(*args, stream)
+            rc = f(*args, _current_stream(index))
     if rc:
         _check(rc, what)
 
@@ -144,23 +153,24 @@ def _workspace(nbytes: int, like: torch.Tensor) -> Optional[torch.Tensor]:
 
 # ------------------------------------------------------------------ embedding --
 
-def _check_ids(ids: torch.Tensor, like: torch.Tensor) -> torch.Tensor:
-    _on_gpu("ids", ids, like)
-    if ids.dtype not in (torch.int32, torch.int64):
+def _check_ids(ids: torch.Tensor, index: int) -> torch.Tensor:
+    _on_gpu("ids", ids, index)
+    if ids.dtype != torch.int32 and ids.dtype != torch.int64:
         raise ValueError("ids must be int32 or int64")
     return ids.contiguous()
 
 
 def _embed(table: torch.Tensor, ids: torch.Tensor, scale: float) -> torch.Tensor:
-    dtype = _floating("table", table, tuple(_DTYPES))
-    if table.dim() != 2 or table.shape[0] < 1 or table.shape[1] < 1:
+    dtype = _floating("table", table)
+    index = table.get_device()
+    if table.dim() != 2 or not table.numel():
         raise ValueError("table must be [rows, width]")
-    ids = _check_ids(ids, table)
-    if table.stride(1) != 1 and table.shape[1] > 1 or table.stride(0) < 0:
-        table = table.contiguous()
+    ids = _check_ids(ids, index)
     rows, width = table.shape
+    if table.stride(1) != 1 and width > 1 or table.stride(0) < 0:
+        table = table.contiguous()
     out = table.new_empty((*ids.shape, width))
-    _call(_lib.tok_embed, "tok_embed", table, table.data_ptr(), rows, width, table.stride(0), dtype,
+    _call(_lib.tok_embed, "tok_embed", index, table.data_ptr(), rows, width, table.stride(0), dtype,
           ids.data_ptr(), ids.element_size(), ids.numel(), scale, out.data_ptr())
     return out
 
@@ -171,8 +181,9 @@ def embed_grad(grad: torch.Tensor, ids: torch.Tensor, rows: int, *,
     sum of ``scale * grad[i]`` over the tokens i with ids[i] == r, in float32
     and in a fixed order (the same inputs give the same bits). grad is
     [*ids.shape, width]."""
-    dtype = _floating("grad", grad, tuple(_DTYPES))
-    ids = _check_ids(ids, grad)
+    dtype = _floating("grad", grad)
+    index = grad.get_device()
+    ids = _check_ids(ids, index)
     if grad.shape[:-1] != ids.shape or grad.dim() < 1:
         raise ValueError(f"grad must be [*ids.shape, width]: got {tuple(grad.shape)} "
                          f"for ids {tuple(ids.shape)}")
@@ -183,7 +194,7 @@ def embed_grad(grad: torch.Tensor, ids: torch.Tensor, rows: int, *,
     nbytes = _size(_lib.tok_embed_grad_workspace_bytes(n, rows, width),
                    "tok_embed_grad_workspace_bytes")
     out, ws = grad.new_empty((rows, width)), _workspace(nbytes, grad)
-    _call(_lib.tok_embed_grad, "tok_embed_grad", grad, flat.data_ptr(), flat.stride(0), dtype,
+    _call(_lib.tok_embed_grad, "tok_embed_grad", index, flat.data_ptr(), flat.stride(0), dtype,
           ids.data_ptr(), ids.element_size(), n, rows, width, float(scale), out.data_ptr(),
           _ptr(ws), nbytes)
     return out
@@ -216,7 +227,7 @@ def embed(table: torch.Tensor, ids: torch.Tensor, *, scale: float = 1.0) -> torc
 # ------------------------------------------------------------------ attention --
 
 def _heads(name: str, t: torch.Tensor, like: Optional[torch.Tensor] = None) -> torch.Tensor:
-    _floating(name, t, (torch.bfloat16, torch.float16), like)
+    _floating(name, t, like, _HALF)
     if t.dim() != 3:
         raise ValueError(f"{name} must be [tokens, heads, width]")
     # 16-byte pieces, tokens less than 64 MiB apart: copy what is laid out otherwise
@@ -227,11 +238,10 @@ def _heads(name: str, t: torch.Tensor, like: Optional[torch.Tensor] = None) -> t
     return t
 
 
-def _positions(name: str, t: Optional[torch.Tensor], tokens: int,
-               like: torch.Tensor) -> torch.Tensor:
+def _positions(name: str, t: Optional[torch.Tensor], tokens: int, index: int) -> torch.Tensor:
     if t is None:
         raise ValueError(f"slopes need {name}")
-    _on_gpu(name, t, like)
+    _on_gpu(name, t, index)
     if t.dtype != torch.int32 or t.dim() != 2 or t.shape[0] != tokens or not 1 <= t.shape[1] <= 3:
         raise ValueError(f"{name} must be an int32 tensor [{tokens}, 1 to 3 axes]")
     return t
@@ -251,15 +261,16 @@ def _attention(q, k, v, q_offsets, k_offsets, scale, cap, slopes, q_pos, k_pos, 
         raise ValueError(f"the head width must be a multiple of 8, at most 128: got {width}")
     if heads < 1 or kv_heads < 1 or heads % kv_heads:
         raise ValueError(f"{heads} query heads cannot share {kv_heads} key heads")
-    q_offsets, k_offsets = _offsets("q_offsets", q_offsets, q), _offsets("k_offsets", k_offsets, q)
+    index = q.get_device()
+    q_offsets, k_offsets = _offsets("q_offsets", q_offsets, index), _offsets("k_offsets", k_offsets, index)
     if (q_offsets is None) != (k_offsets is None):
         raise ValueError("pass both q_offsets and k_offsets, or neither")
     docs = 1 if q_offsets is None else q_offsets.shape[0] - 1
     if k_offsets is not None and k_offsets.shape[0] != docs + 1:
         raise ValueError("q_offsets and k_offsets must hold as many documents")
     if prefix is not None:
-        _on_gpu("prefix", prefix, q)
-        if prefix.dtype != torch.int32 or tuple(prefix.shape) != (docs,):
+        _on_gpu("prefix", prefix, index)
+        if prefix.dtype != torch.int32 or prefix.shape != (docs,):
             raise ValueError(f"prefix must be an int32 tensor of shape {(docs,)}")
         prefix = prefix.contiguous()
     scale = width ** -0.5 if scale is None else float(scale)
@@ -269,13 +280,13 @@ def _attention(q, k, v, q_offsets, k_offsets, scale, cap, slopes, q_pos, k_pos, 
         raise ValueError("cap must be finite, 0 for none")
     axes = 0
     if slopes is not None:
-        _on_gpu("slopes", slopes, q)
-        if slopes.dtype != torch.float32 or tuple(slopes.shape) != (heads,):
+        _on_gpu("slopes", slopes, index)
+        if slopes.dtype != torch.float32 or slopes.shape != (heads,):
             raise ValueError(f"slopes must be a float32 tensor of shape {(heads,)}")
         if slopes.requires_grad:
             raise ValueError("slopes are constants: no gradient is computed for them")
         slopes = slopes.contiguous()
-        q_pos, k_pos = _positions("q_pos", q_pos, tq, q), _positions("k_pos", k_pos, tk, q)
+        q_pos, k_pos = _positions("q_pos", q_pos, tq, index), _positions("k_pos", k_pos, tk, index)
         axes = q_pos.shape[1]
         if k_pos.shape[1] != axes:
             raise ValueError("q_pos and k_pos must have as many axes")
@@ -301,7 +312,7 @@ def _attend(q, k, v, want_lse, **more):
     nbytes = _size(_lib.tok_attend_workspace_bytes(a), "tok_attend_workspace_bytes")
     out, ws = q.new_empty(q.shape), _workspace(nbytes, q)
     lse = q.new_empty(q.shape[:2], dtype=torch.float32) if want_lse else None
-    _call(_lib.tok_attend, "tok_attend", q, a, q.data_ptr(), k.data_ptr(), v.data_ptr(),
+    _call(_lib.tok_attend, "tok_attend", q.get_device(), a, q.data_ptr(), k.data_ptr(), v.data_ptr(),
           out.data_ptr(), _ptr(lse), _ptr(ws), nbytes)
     return out, lse
 
@@ -320,8 +331,8 @@ def attend_grad(grad_out: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: tor
     a, kept = _attention(q, k, v, q_offsets, k_offsets, scale, cap, slopes, q_pos, k_pos, causal,
                          prefix, grad_out)
     q, k, v, g = kept[:4]
-    _floating("out", out, (q.dtype,), q)
-    _on_gpu("lse", lse, q)
+    _floating("out", out, q)
+    _on_gpu("lse", lse, q.get_device())
     if out.shape != q.shape or lse.dtype != torch.float32 or lse.shape != q.shape[:2]:
         raise ValueError("out and lse must be what attend returned for q")
     out, lse = out.contiguous(), lse.contiguous()
@@ -330,7 +341,7 @@ def attend_grad(grad_out: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: tor
     nbytes = _size(_lib.tok_attend_grad_workspace_bytes(a), "tok_attend_grad_workspace_bytes")
     gq, gk, gv = q.new_empty(q.shape), k.new_empty(k.shape), k.new_empty(k.shape)
     ws = _workspace(nbytes, q)
-    _call(_lib.tok_attend_grad, "tok_attend_grad", q, a, q.data_ptr(), k.data_ptr(), v.data_ptr(),
+    _call(_lib.tok_attend_grad, "tok_attend_grad", q.get_device(), a, q.data_ptr(), k.data_ptr(), v.data_ptr(),
           out.data_ptr(), lse.data_ptr(), g.data_ptr(), gq.data_ptr(), gk.data_ptr(), gv.data_ptr(),
           _ptr(ws), nbytes)
     return gq, gk, gv
@@ -389,11 +400,11 @@ def attend(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, *,
 # ----------------------------------------------------------------- recurrence --
 
 def _scan_args(gate, x, offsets):
-    dtype = _floating("gate", gate, tuple(_DTYPES))
-    _floating("x", x, tuple(_DTYPES), gate)
+    dtype = _floating("gate", gate)
+    _floating("x", x, gate)
     if gate.dim() != 2 or gate.shape != x.shape or gate.shape[1] < 1:
         raise ValueError("gate and x must both be [tokens, width]")
-    offsets = _offsets("offsets", offsets, gate)
+    offsets = _offsets("offsets", offsets, gate.get_device())
     docs = 1 if offsets is None else offsets.shape[0] - 1
     return dtype, gate.contiguous(), x.contiguous(), offsets, docs
 
@@ -401,14 +412,14 @@ def _scan_args(gate, x, offsets):
 def _scan(gate, x, offsets, state, reverse, want_carry):
     dtype, gate, x, offsets, docs = _scan_args(gate, x, offsets)
     t, width = x.shape
-    state = _state("state", state, docs, width, x)
+    state = _state("state", state, docs, width, x.get_device())
     y, last = x.new_empty((t, width)), x.new_empty((docs, width), dtype=torch.float32)
     carry = None
     if want_carry:
         carry = x.new_empty((-(-t // TOK_SCAN_RUN), width), dtype=torch.float32)
     nbytes = _size(_lib.tok_scan_workspace_bytes(t, width), "tok_scan_workspace_bytes")
     ws = _workspace(nbytes, x)
-    _call(_lib.tok_scan, "tok_scan", x, gate.data_ptr(), x.data_ptr(), dtype, t, width, _ptr(offsets),
+    _call(_lib.tok_scan, "tok_scan", x.get_device(), gate.data_ptr(), x.data_ptr(), dtype, t, width, _ptr(offsets),
           docs, bool(reverse), _ptr(state), y.data_ptr(), last.data_ptr(), _ptr(carry), _ptr(ws), nbytes)
     return y, last, carry
 
@@ -423,21 +434,21 @@ def gated_scan_grad(grad_y: torch.Tensor, gate: torch.Tensor, x: torch.Tensor,
     returned and the same other arguments."""
     dtype, gate, x, offsets, docs = _scan_args(gate, x, offsets)
     t, width = x.shape
-    _floating("grad_y", grad_y, (x.dtype,), x)
+    _floating("grad_y", grad_y, x)
     if grad_y.shape != x.shape:
         raise ValueError(f"grad_y must have x's shape {tuple(x.shape)}")
     grad_y = grad_y.contiguous()
-    _on_gpu("carry", carry, x)
+    _on_gpu("carry", carry, x.get_device())
     if carry.dtype != torch.float32 or tuple(carry.shape) != (-(-t // TOK_SCAN_RUN), width):
         raise ValueError("carry must be what gated_scan returned for x")
     carry = carry.contiguous()
-    state = _state("state", state, docs, width, x)
-    grad_state = _state("grad_state", grad_state, docs, width, x)
+    state = _state("state", state, docs, width, x.get_device())
+    grad_state = _state("grad_state", grad_state, docs, width, x.get_device())
     gg, gx = gate.new_empty((t, width)), x.new_empty((t, width))
     gs = x.new_empty((docs, width), dtype=torch.float32)
     nbytes = _size(_lib.tok_scan_workspace_bytes(t, width), "tok_scan_workspace_bytes")
     ws = _workspace(nbytes, x)
-    _call(_lib.tok_scan_grad, "tok_scan_grad", x, grad_y.data_ptr(), gate.data_ptr(), x.data_ptr(),
+    _call(_lib.tok_scan_grad, "tok_scan_grad", x.get_device(), grad_y.data_ptr(), gate.data_ptr(), x.data_ptr(),
           carry.data_ptr(), dtype, t, width, _ptr(offsets), docs, bool(reverse), _ptr(state),
           _ptr(grad_state), gg.data_ptr(), gx.data_ptr(), gs.data_ptr(), _ptr(ws), nbytes)
     return gg, gx, gs
