@@ -568,7 +568,7 @@ bool grad_plan(long long n, long long rows, long long width, GradPlan* p) {
     }
     p->tiles = (int)((n + kTile - 1) / kTile);
     // few tokens: short runs, or too few groups of lanes have work
-    p->run = n <= kSmall ? 8 : n <= 262144 ? 32 : 128;
+    p->run = n <= kSmall ? 8 : n <= 262144 ? 32 : 64;
     p->runs = (n + p->run - 1) / p->run;
     long long o = 0;
     auto take = [&](long long bytes) {

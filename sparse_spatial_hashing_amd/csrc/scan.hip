@@ -524,8 +524,9 @@ bool check(int dtype, long long t, long long width, const int32_t* offsets, int3
 
 // Steps per chunk. Short chunks fill the card (a wavefront walks a chunk of
 // 64 lanes of channels), long ones keep the chunks' sums few.
+// Up to 64 steps are one chunk: its walk takes less than two more launches.
 int chunk_of(long long t) {
-    int chunk = 32;
+    int chunk = t <= 64 ? 64 : 32;
     while (chunk < 1024 && (t + chunk - 1) / chunk > 4096) chunk *= 2;
     return chunk;
 }

@@ -403,15 +403,15 @@ def test_scan_long(t, width):
     gen = torch.Generator().manual_seed(t)
     gate, x, grad = (_randn((t, width), F32, gen, s) for s in (1.0, 1.0, 1.0))
     gate += 5.0
-    for at in ([0, t], [0, t // 3, t // 3 + 77, t, t, t]):
-        for reverse in (False, True):
-            want = ref.scan(gate, x, at, None, reverse, grad)
-            y, last, carry = ssh.gated_scan(gate.to(DEV), x.to(DEV), _at(at), reverse=reverse,
-                                            return_carry=True)
-            made = ssh.gated_scan_grad(grad.to(DEV), gate.to(DEV), x.to(DEV), carry, _at(at),
-                                       reverse=reverse)
-            for n, got in zip(("y", "last", "gg", "gx", "gs"), (y, last, *made)):
-                ref.check(got, *want[n], f"{n} t {t} {at[:3]} {reverse}")
+    for at, reverse in (([0, t], False), ([0, t // 3, t // 3 + 77, t, t, t], True)):
+        print(f"scan t {t} width {width} {at[:3]} reverse {reverse}", flush=True)
+        want = ref.scan(gate, x, at, None, reverse, grad)
+        y, last, carry = ssh.gated_scan(gate.to(DEV), x.to(DEV), _at(at), reverse=reverse,
+                                        return_carry=True)
+        made = ssh.gated_scan_grad(grad.to(DEV), gate.to(DEV), x.to(DEV), carry, _at(at),
+                                   reverse=reverse)
+        for n, got in zip(("y", "last", "gg", "gx", "gs"), (y, last, *made)):
+            ref.check(got, *want[n], f"{n} t {t} {at[:3]} {reverse}")
 
 
 def test_scan_saturated_gates():
@@ -497,3 +497,16 @@ def test_refusals_on_the_gpu():
             lambda: ssh.gated_scan_grad(x, x, x, x, at), lambda: ssh.gated_scan_grad(x[:2], x, x, x[:1], at)):
         with pytest.raises(ValueError):
             call()
+
+
+def test_example_learns():
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples",
+                        "pillar_tokens.py")
+    spec = importlib.util.spec_from_file_location("pillar_tokens", path)
+    example = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(example)
+    losses, answer = example.main(steps=20)
+    assert all(math.isfinite(v) for v in losses + answer)
+    assert losses[-1] < 0.5 * losses[0], losses
