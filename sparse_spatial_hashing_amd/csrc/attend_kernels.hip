@@ -90,7 +90,7 @@ __device__ __forceinline__ unsigned rows_place(int lane) {
 // at: tile address + rows_place
 __device__ __forceinline__ vec8 lds_rows(unsigned at, int row0, int k) {
     typedef const __attribute__((address_space(3))) vec8* P;
-    return *(P)((at ^ (k << 5)) + row0 * 2 * W);
+    return *(P)(size_t)((at ^ (k << 5)) + row0 * 2 * W);
 }
 
 // Operand A of a transposed product: rows are elements 32 b + lane % 32 of
@@ -105,8 +105,8 @@ __device__ __forceinline__ uint2 columns_place(int lane) {
 // row0: a multiple of 16, which swz() does not see
 __device__ __forceinline__ vec8 lds_columns(uint2 at, int row0, int b) {
     typedef __attribute__((address_space(3))) short4v* P;
-    const short4v x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((P)((at.x ^ (b << 6)) + row0 * 2 * W));
-    const short4v y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((P)((at.y ^ (b << 6)) + row0 * 2 * W));
+    const short4v x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((P)(size_t)((at.x ^ (b << 6)) + row0 * 2 * W));
+    const short4v y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((P)(size_t)((at.y ^ (b << 6)) + row0 * 2 * W));
     typedef short short8v __attribute__((ext_vector_type(8)));
     const short8v z = __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7);
     return __builtin_bit_cast(vec8, z);
@@ -318,11 +318,6 @@ struct Tile {
 // what is below, however few registers the compiler would rather use.
 __device__ __forceinline__ void fence() { __builtin_amdgcn_sched_barrier(0); }
 
-// The operands A of a product over the width with 32 rows of a tile.
-__device__ __forceinline__ void read_rows(unsigned at, int row0, vec8 (&x)[kSteps]) {
-#pragma unroll
-    for (int k = 0; k < kSteps; ++k) x[k] = lds_rows(at, row0, k);
-}
 // The operands A of the transposed product over 16 rows of a tile.
 __device__ __forceinline__ void read_columns(uint2 at, int row0, vec8 (&x)[kBlocks]) {
 #pragma unroll
@@ -471,7 +466,7 @@ __device__ __forceinline__ unsigned xcd_block(unsigned bid, unsigned n) {
 // Key tiles are loaded one ahead into the other half of LDS.
 
 template <int AX, bool CAP, int NW, int BN>
-__global__ __launch_bounds__(64 * NW, NW == 4 && (W < 128 || AX == 0) ? 3 : 2) void k_att_forward(AttArgs a) {
+__global__ __launch_bounds__(64 * NW, NW == 4 && (W < 128 || AX == 0) ? 3 : NW == 4 || W < 128 || AX == 0 ? 2 : 1) void k_att_forward(AttArgs a) {
     constexpr int NT = 64 * NW;
     constexpr int NB = BN / 32;
     typedef Tile<BN, NT> KeyTile;

@@ -237,8 +237,8 @@ __global__ __launch_bounds__(256) void k_scan_sum_grad(ScanArgs a) {
 // The state that enters each chunk, over the chunks' (mul, add), in place of
 // add: 8 channels of a block, 128 threads along the chunks, each first over its
 // own share, then over the shares before it, then over its own again. Up to
-// kHeld chunks of a share stay in registers, all loaded at once: with the 4096
-// chunks at most that chunk_of() makes of up to 4 M tokens, none is read twice.
+// kHeld chunks of a share stay in registers, all loaded at once: with the
+// 3072 chunks at most that chunk_of() makes of up to 3 M tokens, none is read twice.
 // grad: from the last chunk to the first.
 constexpr int kParts = 128, kHeld = 32;
 
@@ -522,12 +522,16 @@ bool check(int dtype, long long t, long long width, const int32_t* offsets, int3
            (reverse == 0 || reverse == 1);
 }
 
-// Steps per chunk. Short chunks fill the card (a wavefront walks a chunk of
-// 64 lanes of channels), long ones keep the chunks' sums few.
+// Steps per chunk: 32, doubled while there are more than 3072 chunks. Short
+// chunks fill the card (a wavefront walks a chunk of 64 lanes of channels),
+// long ones keep the chunks' sums few: 122,880 points of 128 channels train in
+// 167 us with 3840 chunks of 32 and in 162 with 1920 of 64; 163,000 pillars of
+// 256 channels take 114 us with 5100 chunks of 32, 103 with 2550 of 64 and 116
+// with 1280 of 128.
 // Up to 64 steps are one chunk: its walk takes less than two more launches.
 int chunk_of(long long t) {
     int chunk = t <= 64 ? 64 : 32;
-    while (chunk < 1024 && (t + chunk - 1) / chunk > 4096) chunk *= 2;
+    while (chunk < 1024 && (t + chunk - 1) / chunk > 3072) chunk *= 2;
     return chunk;
 }
 
@@ -537,6 +541,7 @@ int run(ScanArgs a, hipStream_t stream) {
     const dim3 block(lanes < 256 ? lanes : 256);
     const unsigned slabs = (unsigned)((a.width / V + block.x - 1) / block.x);
     // Documents of a few tokens (a decoding step): one launch over documents.
+    // 64 sequences of one token, 512 channels: 3.1 us; walked as one chunk 40.
     if (!GRAD && a.t <= 4096 && a.t <= 8ll * a.docs) {
         k_scan_doc<T, V><<<dim3(a.docs + 2, slabs), block, 0, stream>>>(a);
     } else {
@@ -560,14 +565,14 @@ int run(ScanArgs a, hipStream_t stream) {
     return e == hipSuccess ? VOX_OK : ssh_hip_fail(e);
 }
 
-// Channels per thread: as many as leave a wavefront's lanes in use, with
-// pieces of at most 8 bytes that every array is aligned for. `most` bounds
-// the registers.
+// Two channels per thread where every array is aligned for pairs and a
+// wavefront's lanes stay in use. (Four of 16 bits: sixteen frames of 256
+// channels took 105 us, with two 103: more wavefronts hide more.)
 template <typename T>
 int dispatch_type(const ScanArgs& a, bool grad, hipStream_t stream) {
     const void* elems[] = {a.gate, a.x, a.gy, a.y, a.ggate, a.gx};
     const void* floats[] = {a.state, a.last, a.carry, a.grad_last, a.grad_state};
-    int v = sizeof(T) == 4 || grad ? 2 : 4;
+    int v = 2;
     auto fits = [&](int n) {
         if (a.width % n || (n > 1 && a.width / n < kWave)) return false;
         for (const void* p : elems)
@@ -578,8 +583,6 @@ int dispatch_type(const ScanArgs& a, bool grad, hipStream_t stream) {
     };
     while (v > 1 && !fits(v)) v /= 2;
     if (grad) return v == 2 ? run<T, 2, true>(a, stream) : run<T, 1, true>(a, stream);
-    if constexpr (sizeof(T) == 2)
-        if (v == 4) return run<T, 4, false>(a, stream);
     return v == 2 ? run<T, 2, false>(a, stream) : run<T, 1, false>(a, stream);
 }
 
