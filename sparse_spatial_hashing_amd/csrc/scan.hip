@@ -31,6 +31,7 @@ struct ScanArgs {
     float* add;               // the state that enters it
     int t, width, docs, reverse;
     int chunk, chunks;        // steps of a chunk (a multiple of kRun)
+    int by_doc;               // a block walks a document, not a chunk
 };
 
 // a = sigmoid(f) and 1 - a, each to a few units in its last place: the smaller
@@ -305,22 +306,46 @@ __global__ __launch_bounds__(1024) void k_scan_join(ScanArgs a) {
     }
 }
 
-// Documents of no tokens pass their state through: kEmpty of them per block
-// past the chunks' own.
+// Documents of no tokens pass their state through.
+template <int V>
+__device__ __forceinline__ void pass_empty(const ScanArgs& a, const float* from, float* to, int doc,
+                                           int c) {
+    float h[V];
+    const Doc d = {0, 0, doc};
+    state_of<V>(from, d, a.width, c, h);
+    Pack<float, V>::store(to + (long long)doc * a.width + c, h);
+}
+
+// The steps of a block: a chunk, whose documents are found as it is walked, or
+// (by_doc) one document, or the tokens of none. Empty documents are dealt with
+// here, kEmpty of them in each block past the chunks' own; false: no steps.
 constexpr int kEmpty = 64;
 
 template <int V>
-__device__ __forceinline__ void pass_empty(const ScanArgs& a, const float* from, float* to, int c) {
-    if (!to || c >= a.width) return;
-    const int first = ((int)blockIdx.x - a.chunks) * kEmpty;
-    for (int doc = first; doc < min(a.docs, first + kEmpty); ++doc) {
-        const int lo = tok_boundary(a.offsets, a.docs, a.t, doc + 1);
-        if (tok_boundary(a.offsets, a.docs, a.t, doc + 2) > lo) continue;
-        float h[V];
-        const Doc d = {0, 0, doc};
-        state_of<V>(from, d, a.width, c, h);
-        Pack<float, V>::store(to + (long long)doc * a.width + c, h);
+__device__ __forceinline__ bool block_steps(const ScanArgs& a, const float* from, float* to, int c,
+                                            Doc* d, int* begin, int* end) {
+    const int block = blockIdx.x;
+    const bool writes = to && c < a.width;
+    if (a.by_doc) {
+        const int lo = tok_boundary(a.offsets, a.docs, a.t, block);
+        const int hi = max(lo, tok_boundary(a.offsets, a.docs, a.t, block + 1));
+        d->begin = *begin = a.reverse ? a.t - hi : lo;
+        d->end = *end = a.reverse ? a.t - lo : hi;
+        d->doc = block >= 1 && block <= a.docs ? block - 1 : -1;
+        if (hi == lo && d->doc >= 0 && writes) pass_empty<V>(a, from, to, d->doc, c);
+        return hi > lo;
     }
+    if (block < a.chunks) {
+        *begin = block * a.chunk;
+        *end = min(a.t, *begin + a.chunk);
+        return true;
+    }
+    const int first = (block - a.chunks) * kEmpty;
+    for (int doc = first; doc < min(a.docs, first + kEmpty) && writes; ++doc) {
+        const int lo = tok_boundary(a.offsets, a.docs, a.t, doc + 1);
+        if (tok_boundary(a.offsets, a.docs, a.t, doc + 2) <= lo) pass_empty<V>(a, from, to, doc, c);
+    }
+    return false;
 }
 
 // The recurrence over a chunk of steps, from the state that enters it.
@@ -328,22 +353,19 @@ template <typename T, int V>
 __global__ __launch_bounds__(256) void k_scan_run(ScanArgs a) {
     constexpr int kBatch = 8;
     const int c = (blockIdx.y * blockDim.x + threadIdx.x) * V;
-    const int begin = blockIdx.x * a.chunk, end = min(a.t, begin + a.chunk);
-    if ((int)blockIdx.x >= a.chunks) {
-        pass_empty<V>(a, a.state, a.last, c);
-        return;
-    }
+    Doc d = {0, 0, -1};
+    int begin, end;
+    if (!block_steps<V>(a, a.state, a.last, c, &d, &begin, &end)) return;
     const bool on = c < a.width;
     const Steps<T, V> gate(a, a.gate, on ? c : 0), x(a, a.x, on ? c : 0), y(a, a.y, on ? c : 0);
     float h[V];
 #pragma unroll
     for (int j = 0; j < V; ++j) h[j] = 0.0f;
-    if (a.chunks > 1 && on) Pack<float, V>::load(a.add + sum_at(a, blockIdx.x, c), h);
+    if (a.chunks > 1 && !a.by_doc && on) Pack<float, V>::load(a.add + sum_at(a, blockIdx.x, c), h);
     Walk walk;
-    Doc d = {0, 0, -1};
     for (int s = begin; s < end;) {
         if (s == begin || s == d.end) {
-            d = walk.at(a, s, a.reverse ? -1 : 1);
+            if (!a.by_doc) d = walk.at(a, s, a.reverse ? -1 : 1);
             if (s == d.begin) state_of<V>(a.state, d, a.width, on ? c : 0, h);
         }
         if (a.carry && s % kRun == 0 && on)
@@ -387,11 +409,9 @@ __global__ __launch_bounds__(256) void k_scan_run(ScanArgs a) {
 template <typename T, int V>
 __global__ __launch_bounds__(256) void k_scan_run_grad(ScanArgs a) {
     const int c = (blockIdx.y * blockDim.x + threadIdx.x) * V;
-    const int begin = blockIdx.x * a.chunk, end = min(a.t, begin + a.chunk);
-    if ((int)blockIdx.x >= a.chunks) {
-        pass_empty<V>(a, a.grad_last, a.grad_state, c);
-        return;
-    }
+    Doc d = {0, 0, -1};
+    int begin, end;
+    if (!block_steps<V>(a, a.grad_last, a.grad_state, c, &d, &begin, &end)) return;
     const bool on = c < a.width;
     const int cc = on ? c : 0;
     const Steps<T, V> gate(a, a.gate, cc), x(a, a.x, cc), grad(a, a.gy, cc);
@@ -399,12 +419,11 @@ __global__ __launch_bounds__(256) void k_scan_run_grad(ScanArgs a) {
     float back[V];
 #pragma unroll
     for (int j = 0; j < V; ++j) back[j] = 0.0f;
-    if (a.chunks > 1 && on) Pack<float, V>::load(a.add + sum_at(a, blockIdx.x, c), back);
+    if (a.chunks > 1 && !a.by_doc && on) Pack<float, V>::load(a.add + sum_at(a, blockIdx.x, c), back);
     Walk walk;
-    Doc d = {0, 0, -1};
     for (int s = end; s > begin;) {
         if (s == end || s == d.begin) {
-            d = walk.at(a, s - 1, a.reverse ? 1 : -1);
+            if (!a.by_doc) d = walk.at(a, s - 1, a.reverse ? 1 : -1);
             if (s == d.end) state_of<V>(a.grad_last, d, a.width, cc, back);
         }
         const int b = max(max(d.begin, begin), (s - 1) / kRun * kRun);
@@ -474,47 +493,6 @@ __global__ __launch_bounds__(256) void k_scan_run_grad(ScanArgs a) {
     }
 }
 
-// Forward, where documents are short: one block row per range, one thread per
-// channel, along the document.
-template <typename T, int V>
-__global__ __launch_bounds__(256) void k_scan_doc(ScanArgs a) {
-    constexpr int kBatch = 4;
-    const int c = (blockIdx.y * blockDim.x + threadIdx.x) * V;
-    if (c >= a.width) return;
-    const int range = blockIdx.x;
-    const int lo = tok_boundary(a.offsets, a.docs, a.t, range);
-    const int hi = max(lo, tok_boundary(a.offsets, a.docs, a.t, range + 1));
-    const Doc d = {a.reverse ? a.t - hi : lo, a.reverse ? a.t - lo : hi,
-                   range >= 1 && range <= a.docs ? range - 1 : -1};
-    const Steps<T, V> gate(a, a.gate, c), x(a, a.x, c), y(a, a.y, c);
-    float h[V];
-    state_of<V>(a.state, d, a.width, c, h);
-    for (int s = d.begin; s < d.end; s += kBatch) {
-        const int m = min(kBatch, d.end - s);
-        float g[kBatch][V], z[kBatch][V];
-#pragma unroll
-        for (int k = 0; k < kBatch; ++k) Pack<T, V>::load(gate.at(s + min(k, m - 1)), g[k]);
-#pragma unroll
-        for (int k = 0; k < kBatch; ++k) Pack<T, V>::load(x.at(s + min(k, m - 1)), z[k]);
-#pragma unroll
-        for (int k = 0; k < kBatch; ++k) {
-            if (k >= m) break;
-            if (a.carry && (s + k) % kRun == 0)
-                Pack<float, V>::store(a.carry + (long long)((s + k) / kRun) * a.width + c, h);
-            if (d.doc >= 0) {
-#pragma unroll
-                for (int j = 0; j < V; ++j) {
-                    float f, keep;
-                    gates(g[k][j], f, keep);
-                    h[j] = __builtin_fmaf(f, h[j], keep * z[k][j]);
-                }
-            }
-            Pack<T, V>::store((T*)y.at(s + k), h);
-        }
-    }
-    if (d.doc >= 0 && a.last) Pack<float, V>::store(a.last + (long long)d.doc * a.width + c, h);
-}
-
 bool check(int dtype, long long t, long long width, const int32_t* offsets, int32_t docs,
            int32_t reverse) {
     return tok_dtype_ok(dtype) && t >= 0 && t <= kMaxTokens && width >= 1 && width <= kMaxWidth &&
@@ -540,27 +518,25 @@ int run(ScanArgs a, hipStream_t stream) {
     const int lanes = (a.width / V + kWave - 1) / kWave * kWave;
     const dim3 block(lanes < 256 ? lanes : 256);
     const unsigned slabs = (unsigned)((a.width / V + block.x - 1) / block.x);
-    // Documents of a few tokens (a decoding step): one launch over documents.
-    // 64 sequences of one token, 512 channels: 3.1 us; walked as one chunk 40.
-    if (!GRAD && a.t <= 4096 && a.t <= 8ll * a.docs) {
-        k_scan_doc<T, V><<<dim3(a.docs + 2, slabs), block, 0, stream>>>(a);
-    } else {
-        if (a.chunks > 1) {
-            const dim3 grid((unsigned)a.chunks, slabs), join((unsigned)((a.width + 7) / 8));
-            if constexpr (GRAD) {
-                k_scan_sum_grad<T, V><<<grid, block, 0, stream>>>(a);
-                k_scan_join<true><<<join, dim3(1024), 0, stream>>>(a);
-            } else {
-                k_scan_sum<T, V><<<grid, block, 0, stream>>>(a);
-                k_scan_join<false><<<join, dim3(1024), 0, stream>>>(a);
-            }
+    // Documents of a few tokens on average (a decoding step): a block each, in
+    // one launch. 64 sequences of one token, 512 channels: 3.4 us; walked one
+    // after another as a chunk, 89.
+    a.by_doc = a.t <= 4096 && a.t <= 8ll * a.docs;
+    if (a.chunks > 1 && !a.by_doc) {
+        const dim3 grid((unsigned)a.chunks, slabs), join((unsigned)((a.width + 7) / 8));
+        if constexpr (GRAD) {
+            k_scan_sum_grad<T, V><<<grid, block, 0, stream>>>(a);
+            k_scan_join<true><<<join, dim3(1024), 0, stream>>>(a);
+        } else {
+            k_scan_sum<T, V><<<grid, block, 0, stream>>>(a);
+            k_scan_join<false><<<join, dim3(1024), 0, stream>>>(a);
         }
-        const dim3 grid((unsigned)(a.chunks + (a.docs + kEmpty - 1) / kEmpty), slabs);
-        if constexpr (GRAD)
-            k_scan_run_grad<T, V><<<grid, block, 0, stream>>>(a);
-        else
-            k_scan_run<T, V><<<grid, block, 0, stream>>>(a);
     }
+    const unsigned blocks = a.by_doc ? a.docs + 2 : a.chunks + (a.docs + kEmpty - 1) / kEmpty;
+    if constexpr (GRAD)
+        k_scan_run_grad<T, V><<<dim3(blocks, slabs), block, 0, stream>>>(a);
+    else
+        k_scan_run<T, V><<<dim3(blocks, slabs), block, 0, stream>>>(a);
     const hipError_t e = hipGetLastError();
     return e == hipSuccess ? VOX_OK : ssh_hip_fail(e);
 }
