@@ -1,5 +1,15 @@
 // Gated linear recurrence over packed documents (tokens.h), forward and
 // backward.
+//
+// A step maps a state to a h + b, and so does any run of steps, so a chunk's
+// effect is two numbers a channel: k_scan_sum computes them, k_scan_join turns
+// them into the state that enters each chunk, k_scan_run walks the chunks from
+// there. The backward is the same recurrence from the other end; its states
+// inside a run of kRun steps are computed again from the one saved before it.
+// Memory bounds all but k_scan_join, whose loads are all under way at once.
+// Sixteen frames, 163,000 pillars of 256 bf16 channels: sums 35 us (167 MB at
+// 4.8 TB/s), join 10, run 47 (250 MB at 5.3). 122,880 points of 128 fp32
+// channels: 21.5, 9, 32 and backward 21.5, 9, 55.
 
 #include <hip/hip_runtime.h>
 
@@ -239,7 +249,7 @@ __global__ __launch_bounds__(256) void k_scan_sum_grad(ScanArgs a) {
 // add: 8 channels of a block, 128 threads along the chunks, each first over its
 // own share, then over the shares before it, then over its own again. Up to
 // kHeld chunks of a share stay in registers, all loaded at once: with the
-// 3072 chunks at most that chunk_of() makes of up to 3 M tokens, none is read twice.
+// 3000 chunks at most that chunk_of() makes of up to 3 M tokens, none is read twice.
 // grad: from the last chunk to the first.
 constexpr int kParts = 128, kHeld = 32;
 
@@ -500,7 +510,7 @@ bool check(int dtype, long long t, long long width, const int32_t* offsets, int3
            (reverse == 0 || reverse == 1);
 }
 
-// Steps per chunk: 32, doubled while there are more than 3072 chunks. Short
+// Steps per chunk: 32, doubled while there are more than 3000 chunks. Short
 // chunks fill the card (a wavefront walks a chunk of 64 lanes of channels),
 // long ones keep the chunks' sums few: 122,880 points of 128 channels train in
 // 167 us with 3840 chunks of 32 and in 162 with 1920 of 64; 163,000 pillars of
@@ -509,7 +519,7 @@ bool check(int dtype, long long t, long long width, const int32_t* offsets, int3
 // Up to 64 steps are one chunk: its walk takes less than two more launches.
 int chunk_of(long long t) {
     int chunk = t <= 64 ? 64 : 32;
-    while (chunk < 1024 && (t + chunk - 1) / chunk > 3072) chunk *= 2;
+    while (chunk < 1024 && (t + chunk - 1) / chunk > 3000) chunk *= 2;
     return chunk;
 }
 
