@@ -65,7 +65,8 @@ int tok_embed(const void* table, int64_t rows, int64_t width, int64_t row_stride
  * tokens of a row are added in token order inside runs of a fixed length, and
  * the runs in order. grad rows are `grad_stride` elements apart.
  * Limits: 0 <= n <= 2^27, 1 <= rows <= 2^24, 1 <= width <= 65536.
- * The workspace needs no initial contents, 256-byte aligned.
+ * The workspace (0 bytes: NULL will do) needs no initial contents, 256-byte
+ * aligned.
  */
 int64_t tok_embed_grad_workspace_bytes(int64_t n, int64_t rows, int64_t width);
 int tok_embed_grad(const void* grad, int64_t grad_stride, int32_t dtype, const void* ids,

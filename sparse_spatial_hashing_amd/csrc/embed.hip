@@ -5,6 +5,7 @@
 // The gradient sorts (row, token) pairs by row with stable passes from the
 // lowest digit up, so the tokens of a row come out in token order, and sums
 // equal rows over runs of sorted pairs, a group of lanes per run:
+//   k_eg_tiny     up to kTiny tokens: no sort, all in one launch; or
 //   k_eg_small    up to kSmall tokens: one block sorts in LDS while the others
 //                 clear the gradient; or
 //   k_eg_zero, and per digit
@@ -317,20 +318,98 @@ __global__ __launch_bounds__(kSmallBlock) void k_eg_small(const Id* __restrict__
         for (int k = 0; k < E; ++k) {
             if (k < per && first + k * kWave < n) {
                 const unsigned at = seen[wave][(pair[k].x >> shift) & (digits - 1)] + rank[k];
-                if (last)
-                    out_pairs[at] = pair[k];
-                else
-                    local[at] = pair[k];
+                local[at] = pair[k];
             }
         }
-        if (last) break;
         __syncthreads();
+        if (last) break;
 #pragma unroll
         for (int k = 0; k < E; ++k) {
             if (k < per && first + k * kWave < n) pair[k] = local[first + k * kWave];
         }
         shift += bits;
         __syncthreads();
+    }
+    for (int i = threadIdx.x; i < n; i += kSmallBlock) out_pairs[i] = local[i];
+}
+
+// n <= kTiny tokens in one launch: the first `sums` blocks have a wavefront per
+// token, which adds the rows of its id if it is the id's first token; the
+// others clear the rows that no token has, kTinyRows each.
+constexpr int kTiny = 256, kTinyRows = 64;
+
+template <typename T, int N, typename Id>
+__global__ __launch_bounds__(kBlock) void k_eg_tiny(const T* __restrict__ grad, long long stride,
+                                                    const Id* __restrict__ ids, int n, long long rows,
+                                                    int width, float scale, T* __restrict__ out,
+                                                    int sums, int lanes_log) {
+    static_assert(kTiny <= kBlock && kTiny % kWave == 0, "an id per thread");
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    if ((int)blockIdx.x < sums) {
+        const int token = blockIdx.x * kWaves + wave;
+        if (token >= n) return;
+        const unsigned key = key_of(ids, token, rows);
+        if (key >= rows) return;
+        unsigned long long same[kTiny / kWave];
+#pragma unroll
+        for (int j = 0; j < kTiny / kWave; ++j) {
+            const int i = j * kWave + lane;
+            same[j] = __ballot(i < n && key_of(ids, i < n ? i : 0, rows) == key);
+        }
+        for (int col = lane * N; col < width; col += kWave * N) {
+            float acc[N];
+#pragma unroll
+            for (int j = 0; j < N; ++j) acc[j] = 0.0f;
+            bool first = true;
+#pragma unroll
+            for (int j = 0; j < kTiny / kWave; ++j) {
+                unsigned long long m = same[j];
+                while (m) {
+                    int at[kBatch];
+                    int count = 0;
+#pragma unroll
+                    for (int k = 0; k < kBatch; ++k) {
+                        at[k] = m ? j * kWave + __ffsll((long long)m) - 1 : at[k > 0 ? k - 1 : 0];
+                        count += m != 0;
+                        m &= m - 1;
+                    }
+                    if (first && at[0] != token) return;  // not the id's first token
+                    first = false;
+                    typename Pack<T, N>::vec x[kBatch];
+#pragma unroll
+                    for (int k = 0; k < kBatch; ++k)
+                        x[k] = Pack<T, N>::raw(grad + (long long)at[k] * stride + col);
+#pragma unroll
+                    for (int k = 0; k < kBatch; ++k) {
+                        float y[N];
+                        Pack<T, N>::wide(x[k], y);
+#pragma unroll
+                        for (int i = 0; i < N; ++i) acc[i] += k < count ? y[i] : 0.0f;
+                    }
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < N; ++j) acc[j] *= scale;
+            Pack<T, N>::store(out + (long long)key * width + col, acc);
+        }
+        return;
+    }
+    __shared__ int taken[kTinyRows];
+    if (threadIdx.x < kTinyRows) taken[threadIdx.x] = 0;
+    __syncthreads();
+    const long long row0 = (long long)((int)blockIdx.x - sums) * kTinyRows;
+    if ((int)threadIdx.x < n) {
+        const long long at = (long long)key_of(ids, threadIdx.x, rows) - row0;
+        if (at >= 0 && at < kTinyRows) taken[at] = 1;
+    }
+    __syncthreads();
+    float zero[N];
+#pragma unroll
+    for (int j = 0; j < N; ++j) zero[j] = 0.0f;
+    for (int r = threadIdx.x >> lanes_log; r < kTinyRows && row0 + r < rows; r += kBlock >> lanes_log) {
+        if (taken[r]) continue;
+        for (int col = (threadIdx.x & ((1 << lanes_log) - 1)) * N; col < width; col += N << lanes_log)
+            Pack<T, N>::store(out + (row0 + r) * width + col, zero);
     }
 }
 
@@ -583,6 +662,10 @@ bool grad_plan(long long n, long long rows, long long width, GradPlan* p) {
         o += (bytes + 255) / 256 * 256;
         return here;
     };
+    if (n <= kTiny) {
+        p->bytes = 0;
+        return true;
+    }
     for (int k = 0; k < 2; ++k) p->pairs[k] = k == 0 || n > kSmall ? take(8 * n) : 0;
     p->counts = n > kSmall ? take(4ll * kMaxDigits * p->tiles) : 0;
     p->totals = n > kSmall ? take(4ll * kMaxDigits) : 0;
@@ -626,14 +709,42 @@ int reduce_run(const GradPlan& p, const void* grad, long long stride, long long 
     return fail(hipGetLastError());
 }
 
+template <typename T, int N>
+int tiny_run(const void* grad, long long stride, const void* ids, int id_bytes, long long n,
+             long long rows, long long width, float scale, void* out, hipStream_t stream) {
+    int lanes_log = 0;
+    while ((1 << lanes_log) < width / N && lanes_log < 6) ++lanes_log;
+    const int sums = (int)((n + kWaves - 1) / kWaves);
+    const dim3 grid((unsigned)(sums + (rows + kTinyRows - 1) / kTinyRows)), block(kBlock);
+    if (id_bytes == 4)
+        k_eg_tiny<T, N, int32_t><<<grid, block, 0, stream>>>((const T*)grad, stride, (const int32_t*)ids,
+                                                             (int)n, rows, (int)width, scale, (T*)out,
+                                                             sums, lanes_log);
+    else
+        k_eg_tiny<T, N, int64_t><<<grid, block, 0, stream>>>((const T*)grad, stride, (const int64_t*)ids,
+                                                             (int)n, rows, (int)width, scale, (T*)out,
+                                                             sums, lanes_log);
+    return fail(hipGetLastError());
+}
+
 template <typename T>
 int grad_type(const GradPlan& p, const void* grad, long long stride, const void* ids, int id_bytes,
               long long n, long long rows, long long width, float scale, void* out, char* ws,
               hipStream_t stream) {
+    if (n <= kTiny) {
+        switch (piece(grad, out, width, stride, sizeof(T), 8)) {
+            case 8:
+                if constexpr (sizeof(T) == 2)
+                    return tiny_run<T, 8>(grad, stride, ids, id_bytes, n, rows, width, scale, out, stream);
+            case 4: return tiny_run<T, 4>(grad, stride, ids, id_bytes, n, rows, width, scale, out, stream);
+            case 2: return tiny_run<T, 2>(grad, stride, ids, id_bytes, n, rows, width, scale, out, stream);
+            default: return tiny_run<T, 1>(grad, stride, ids, id_bytes, n, rows, width, scale, out, stream);
+        }
+    }
     const long long bytes = rows * width * (long long)sizeof(T), pieces = bytes / 16;
     unsigned char* tail = (unsigned char*)out + pieces * 16;
     int rc;
-    if (n > 0 && n <= kSmall) {
+    if (n <= kSmall) {
         const long long blocks = pieces / (4 * kSmallBlock) + 1;
         const dim3 grid((unsigned)(1 + (blocks < 255 ? blocks : 255)));
         if (id_bytes == 4)
@@ -650,7 +761,7 @@ int grad_type(const GradPlan& p, const void* grad, long long stride, const void*
         k_eg_zero<<<dim3((unsigned)(blocks < 2048 ? blocks : 2048)), dim3(kBlock), 0, stream>>>(
             (uint4*)out, pieces, tail, (int)(bytes % 16));
         rc = fail(hipGetLastError());
-        for (int q = 0; n > 0 && rc == VOX_OK && q < p.passes; ++q) {
+        for (int q = 0; rc == VOX_OK && q < p.passes; ++q) {
             if (q > 0)
                 rc = sort_pass<int32_t, false>(p, q, nullptr, n, rows, ws, stream);
             else if (id_bytes == 4)
@@ -659,7 +770,7 @@ int grad_type(const GradPlan& p, const void* grad, long long stride, const void*
                 rc = sort_pass<int64_t, true>(p, q, ids, n, rows, ws, stream);
         }
     }
-    if (rc != VOX_OK || n == 0) return rc;
+    if (rc != VOX_OK) return rc;
     switch (piece(grad, out, width, stride, sizeof(T), 8)) {
         case 8:
             if constexpr (sizeof(T) == 2)
@@ -706,7 +817,7 @@ int tok_embed_grad(const void* grad, int64_t grad_stride, int32_t dtype, const v
     if (!out || (n && (!grad || !ids))) return VOX_EINVAL;
     const int bytes = tok_elem_bytes(dtype);
     if ((size_t)grad % bytes || (size_t)out % 16 || (size_t)ids % id_bytes) return VOX_EINVAL;
-    if (!workspace || ((size_t)workspace & 255) || workspace_bytes < p.bytes) return VOX_EWORKSPACE;
+    if (!workspace_ok(workspace, workspace_bytes, p.bytes)) return VOX_EWORKSPACE;
     char* ws = (char*)workspace;
     if (dtype == TOK_F32)
         return grad_type<float>(p, grad, grad_stride, ids, id_bytes, n, rows, width, scale, out, ws, stream);

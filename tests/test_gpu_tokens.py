@@ -49,7 +49,8 @@ def test_embed(dtype, width):
 
 @pytest.mark.parametrize("n,rows,spread", [(5000, 3, 1.0), (20000, 1, 1.0), (64, 1, 1.0), (65, 2, 1.0),
                                            (40000, 100000, 3.0), (9000, 700, 1.0), (4097, 5000, 8.0),
-                                           (130000, 60000, 2.0), (70000, 17, 1.0)])
+                                           (130000, 60000, 2.0), (70000, 17, 1.0), (256, 130, 1.0),
+                                           (255, 2, 1.0), (3, 100000, 1.0), (257, 65, 1.0)])
 @pytest.mark.parametrize("width,dtype", [(8, F32), (64, BF16), (33, F16)])
 def test_embed_grad_long_rows(n, rows, spread, width, dtype):
     """Rows with no token, one, and so many that they cross every border of the sum."""

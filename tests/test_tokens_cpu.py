@@ -150,8 +150,9 @@ def test_embedding_refuses():
     assert LIB.tok_embed_grad_workspace_bytes(4, 0, 4) == EINVAL
     assert LIB.tok_embed_grad_workspace_bytes(4, 2**24 + 1, 4) == EINVAL
     assert LIB.tok_embed_grad_workspace_bytes(2**27 + 1, 4, 4) == EINVAL
-    nbytes = LIB.tok_embed_grad_workspace_bytes(5, 10, 8)
-    good = [p, 8, 0, p, 4, 5, 10, 8, 1.0, p, p, nbytes, None]
+    assert LIB.tok_embed_grad_workspace_bytes(5, 10, 8) == 0  # a few tokens need none
+    nbytes = LIB.tok_embed_grad_workspace_bytes(5000, 10, 8)
+    good = [p, 8, 0, p, 4, 5000, 10, 8, 1.0, p, p, nbytes, None]
     for i, bad in ((1, -1), (2, 9), (4, 3), (5, -1), (6, 0), (7, 0), (0, None), (3, None), (9, None),
                    (0, p + 2), (3, p + 2), (9, p + 8)):
         args = list(good)
