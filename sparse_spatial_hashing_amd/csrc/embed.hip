@@ -8,8 +8,9 @@
 //   k_eg_tiny     up to kTiny tokens: no sort, all in one launch; or
 //   k_eg_small    up to kSmall tokens: one block sorts in LDS while the others
 //                 clear the gradient; or
-//   k_eg_zero, and per digit
-//   k_eg_count    digits of each tile of pairs, counted
+//   per digit
+//   k_eg_count    digits of each tile of pairs, counted (the first time other
+//                 blocks clear the gradient)
 //   k_eg_prefix   one block per digit: where each tile's entries of it start
 //   k_eg_scatter  pairs to their places (ranks by ballots, in input order)
 //   then
@@ -96,12 +97,27 @@ __device__ __forceinline__ uint2 pair_of(const Id* ids, const uint2* pairs, long
     return pairs[i];
 }
 
+__device__ __forceinline__ void clear(uint4* out, long long pieces, unsigned char* tail, int bytes,
+                                      long long block, long long blocks, int threads) {
+    const long long step = blocks * threads;
+    for (long long p = block * threads + threadIdx.x; p < pieces; p += step)
+        out[p] = make_uint4(0, 0, 0, 0);
+    if (block == 0 && (int)threadIdx.x < bytes) tail[threadIdx.x] = 0;
+}
+
+// Of the first pass, the blocks past the tiles' own clear the gradient.
 template <typename Id, bool FIRST>
 __global__ __launch_bounds__(kBlock) void k_eg_count(const Id* __restrict__ ids,
                                                      const uint2* __restrict__ pairs, long long n,
                                                      long long rows, int shift, int bits, int tiles,
-                                                     unsigned* __restrict__ counts) {
+                                                     unsigned* __restrict__ counts,
+                                                     uint4* __restrict__ out, long long pieces,
+                                                     unsigned char* __restrict__ tail, int bytes) {
     __shared__ unsigned hist[kMaxDigits];
+    if (FIRST && (int)blockIdx.x >= tiles) {
+        clear(out, pieces, tail, bytes, (int)blockIdx.x - tiles, (int)gridDim.x - tiles, kBlock);
+        return;
+    }
     const int digits = 1 << bits;
     for (int d = threadIdx.x; d < digits; d += kBlock) hist[d] = 0;
     __syncthreads();
@@ -228,19 +244,6 @@ __global__ __launch_bounds__(kBlock) void k_eg_scatter(
 }
 
 // ------------------------------------------------------------------ reduce --
-
-__device__ __forceinline__ void clear(uint4* out, long long pieces, unsigned char* tail, int bytes,
-                                      long long block, long long blocks, int threads) {
-    const long long step = blocks * threads;
-    for (long long p = block * threads + threadIdx.x; p < pieces; p += step)
-        out[p] = make_uint4(0, 0, 0, 0);
-    if (block == 0 && (int)threadIdx.x < bytes) tail[threadIdx.x] = 0;
-}
-
-__global__ __launch_bounds__(kBlock) void k_eg_zero(uint4* __restrict__ out, long long pieces,
-                                                    unsigned char* __restrict__ tail, int bytes) {
-    clear(out, pieces, tail, bytes, blockIdx.x, gridDim.x, kBlock);
-}
 
 // Block 0 sorts all n <= kSmall pairs, kept in registers and put in order
 // through LDS; the other blocks clear the gradient meanwhile. 12,000 tokens and
@@ -677,17 +680,20 @@ bool grad_plan(long long n, long long rows, long long width, GradPlan* p) {
 
 template <typename Id, bool FIRST>
 int sort_pass(const GradPlan& p, int q, const void* ids, long long n, long long rows, char* ws,
-              hipStream_t stream) {
+              void* out, long long bytes, hipStream_t stream) {
     const uint2* in = (const uint2*)(ws + p.pairs[(q + 1) & 1]);
-    uint2* out = (uint2*)(ws + p.pairs[q & 1]);
+    uint2* sorted = (uint2*)(ws + p.pairs[q & 1]);
     unsigned* counts = (unsigned*)(ws + p.counts);
     unsigned* totals = (unsigned*)(ws + p.totals);
     const dim3 tiles((unsigned)p.tiles), block(kBlock);
-    k_eg_count<Id, FIRST><<<tiles, block, 0, stream>>>((const Id*)ids, in, n, rows, p.shift[q],
-                                                       p.bits[q], p.tiles, counts);
+    const long long pieces = bytes / 16, clears = FIRST ? pieces / kBlock + 1 : 0;
+    const dim3 count((unsigned)(p.tiles + (clears < 1024 ? clears : 1024)));
+    k_eg_count<Id, FIRST><<<count, block, 0, stream>>>(
+        (const Id*)ids, in, n, rows, p.shift[q], p.bits[q], p.tiles, counts, (uint4*)out, pieces,
+        (unsigned char*)out + pieces * 16, (int)(bytes % 16));
     k_eg_prefix<<<dim3(1u << p.bits[q]), block, 0, stream>>>(counts, p.tiles, totals);
     k_eg_scatter<Id, FIRST><<<tiles, block, 0, stream>>>((const Id*)ids, in, n, rows, p.shift[q],
-                                                         p.bits[q], p.tiles, counts, totals, out);
+                                                         p.bits[q], p.tiles, counts, totals, sorted);
     return fail(hipGetLastError());
 }
 
@@ -757,17 +763,14 @@ int grad_type(const GradPlan& p, const void* grad, long long stride, const void*
                 (uint4*)out, pieces, tail, (int)(bytes % 16));
         rc = fail(hipGetLastError());
     } else {
-        const long long blocks = pieces / kBlock + 1;
-        k_eg_zero<<<dim3((unsigned)(blocks < 2048 ? blocks : 2048)), dim3(kBlock), 0, stream>>>(
-            (uint4*)out, pieces, tail, (int)(bytes % 16));
-        rc = fail(hipGetLastError());
+        rc = VOX_OK;
         for (int q = 0; rc == VOX_OK && q < p.passes; ++q) {
             if (q > 0)
-                rc = sort_pass<int32_t, false>(p, q, nullptr, n, rows, ws, stream);
+                rc = sort_pass<int32_t, false>(p, q, nullptr, n, rows, ws, out, bytes, stream);
             else if (id_bytes == 4)
-                rc = sort_pass<int32_t, true>(p, q, ids, n, rows, ws, stream);
+                rc = sort_pass<int32_t, true>(p, q, ids, n, rows, ws, out, bytes, stream);
             else
-                rc = sort_pass<int64_t, true>(p, q, ids, n, rows, ws, stream);
+                rc = sort_pass<int64_t, true>(p, q, ids, n, rows, ws, out, bytes, stream);
         }
     }
     if (rc != VOX_OK) return rc;
