@@ -106,9 +106,9 @@ typedef struct tok_attention {
     const int32_t* q_offsets;   /* device [docs + 1]; NULL: one document of all tokens */
     const int32_t* k_offsets;
     const int32_t* prefix;      /* device [docs] or NULL */
-    float scale;                /* > 0 */
+    float scale;                /* in [1e-30, 1e30] */
     float cap;                  /* 0: none */
-    const float* slopes;        /* device [heads]; NULL when axes is 0 */
+    const float* slopes;        /* device [heads], below 2^100; NULL when axes is 0 */
     const int32_t* q_pos;       /* device [tq, axes] */
     const int32_t* k_pos;       /* device [tk, axes] */
     int32_t axes;               /* 0 (no bias) to 3 */

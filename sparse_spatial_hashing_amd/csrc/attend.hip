@@ -32,7 +32,8 @@ bool check(const tok_attention* t) {
     if (t->docs < 1 || t->docs > kMaxDocs || (t->mask != 0 && t->mask != 1)) return false;
     if ((!t->q_offsets || !t->k_offsets) && t->docs != 1) return false;
     if (t->prefix && !t->mask) return false;
-    if (!(t->scale > 0.0f) || !isfinite(t->scale) || !(t->cap >= 0.0f) || !isfinite(t->cap))
+    // a scale that is used as a divisor too
+    if (!(t->scale >= 1e-30f) || !(t->scale <= 1e30f) || !(t->cap >= 0.0f) || !isfinite(t->cap))
         return false;
     if (t->axes < 0 || t->axes > 3 || t->reserved) return false;
     if (t->axes && (!t->slopes || (t->tq && !t->q_pos) || (t->tk && !t->k_pos))) return false;

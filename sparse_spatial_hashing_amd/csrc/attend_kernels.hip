@@ -895,7 +895,8 @@ __global__ __launch_bounds__(64 * NW, NW == 1 && W == 32 ? 3 : NW == 4 || W < 12
     }
     rest = (rest + other_half(rest)) * kUnlift;
     if (!row.real) return;
-    const bool none = a.lse[at] == -__builtin_inff();  // saw no key: no gradient
+    // saw no key, or one, whose weight is 1 whatever its score: no gradient
+    const bool none = row.limit <= 1;
     if (half == 0) a.delta[at] = delta + rest;
     elem* out = (elem*)a.gq + at * a.width;
 #pragma unroll
@@ -1064,15 +1065,18 @@ __global__ __launch_bounds__(64 * NW, NW == 1 && W == 32 ? 3 : NW == 4 || W < 12
 #pragma unroll
             for (int j = 0; j < 4; ++j) s[4 * q + j] = exp2_(__builtin_fmaf(s[4 * q + j], by, t[j]));
         }
-        // every row of the tile sees every key of the block?
-        const bool masked = i + BM > d.lq || key_limit(a, d, i) < min(key0 + kAttRows * NW, lk);
-        unsigned seen = 0xffffu;
+        // every row of the tile sees every key of the block, and two or more?
+        const int least = key_limit(a, d, i);
+        const bool masked = i + BM > d.lq || least < min(key0 + kAttRows * NW, lk) || least <= 1;
+        unsigned seen = 0xffffu, moved = 0xffffu;  // weights, and those that a score can change
         if (masked) {
-            seen = 0;
+            seen = moved = 0;
 #pragma unroll
             for (int r = 0; r < 16; ++r) {
                 const int q = i + 8 * (r / 4) + 4 * half + r % 4;
-                if (q < d.lq && key < key_limit(a, d, q)) seen |= 1u << r;
+                const int limit = key_limit(a, d, q);
+                if (q < d.lq && key < limit) seen |= 1u << r;
+                if (q < d.lq && key < limit && limit > 1) moved |= 1u << r;
             }
 #pragma unroll
             for (int r = 0; r < 16; ++r)
@@ -1099,7 +1103,7 @@ __global__ __launch_bounds__(64 * NW, NW == 1 && W == 32 ? 3 : NW == 4 || W < 12
         if (masked) {
 #pragma unroll
             for (int r = 0; r < 16; ++r)
-                if (!(seen >> r & 1)) dp[r] = 0.0f;
+                if (!(moved >> r & 1)) dp[r] = 0.0f;
         }
 #pragma unroll
         for (int r = 0; r < 16; ++r) dp[r] *= s[r];

@@ -6,7 +6,7 @@
 // lowest digit up, so the tokens of a row come out in token order, and sums
 // equal rows over runs of sorted pairs, a group of lanes per run:
 //   k_eg_tiny     up to kTiny tokens: no sort, all in one launch; or
-//   k_eg_small    up to kSmall tokens: one block sorts in LDS while the others
+//   k_eg_small    up to kSmall tokens: some blocks sort in LDS while the others
 //                 clear the gradient; or
 //   per digit
 //   k_eg_count    digits of each tile of pairs, counted (the first time other
@@ -33,8 +33,9 @@ constexpr int kPer = 8;                    // pairs per thread of a sort tile
 constexpr int kTile = kBlock * kPer;
 constexpr int kMaxBits = 9;                // bits of a digit, at most
 constexpr int kMaxDigits = 1 << kMaxBits;
-constexpr int kSmall = 16384;              // tokens that one block sorts
+constexpr int kSmall = 16384;              // tokens that are sorted in LDS
 constexpr int kSmallBlock = 1024;
+constexpr int kSmallSorts = 16;            // blocks that share the sort
 constexpr int kBatch = 8;                  // rows in flight per group of lanes
 constexpr long long kMaxN = 1ll << 27;
 constexpr long long kMaxRows = 1ll << 24;
@@ -245,14 +246,17 @@ __global__ __launch_bounds__(kBlock) void k_eg_scatter(
 
 // ------------------------------------------------------------------ reduce --
 
-// Block 0 sorts all n <= kSmall pairs, kept in registers and put in order
-// through LDS; the other blocks clear the gradient meanwhile. 12,000 tokens and
-// 110 MB of gradient: 31 us, of which clearing alone takes 24; through the
-// passes below the same sort takes seven launches, 30 us after the clearing.
+// kSmallSorts blocks sort n <= kSmall pairs, each those of its share of the
+// rows: it reads all ids, keeps its own in token order and counts those of
+// lower rows, which is where its own go. Pairs stay in registers and are put in
+// order through LDS. The other blocks clear the gradient meanwhile. 12,000
+// tokens and 110 MB of gradient: 20 us, which is what clearing alone takes; one
+// block sorting all took 28. Through the passes below the same sort takes seven
+// launches, 30 us after the clearing.
 template <typename Id>
 __global__ __launch_bounds__(kSmallBlock) void k_eg_small(const Id* __restrict__ ids, int n,
-                                                          long long rows, int passes, int bits_all,
-                                                          uint2* __restrict__ out_pairs,
+                                                          long long rows, int share, int passes,
+                                                          int bits_all, uint2* __restrict__ out_pairs,
                                                           uint4* __restrict__ out, long long pieces,
                                                           unsigned char* __restrict__ tail,
                                                           int bytes) {
@@ -260,27 +264,56 @@ __global__ __launch_bounds__(kSmallBlock) void k_eg_small(const Id* __restrict__
     __shared__ uint2 local[kSmall];
     __shared__ unsigned short seen[W][kMaxDigits];
     __shared__ unsigned wsum[kWsumWords];
-    if (blockIdx.x > 0) {
-        clear(out, pieces, tail, bytes, blockIdx.x - 1, gridDim.x - 1, kSmallBlock);
+    if (blockIdx.x >= kSmallSorts) {
+        clear(out, pieces, tail, bytes, blockIdx.x - kSmallSorts, gridDim.x - kSmallSorts, kSmallBlock);
         return;
     }
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int per = (n + kSmallBlock - 1) / kSmallBlock;  // <= E pairs per thread
-    const int first = wave * (per * kWave) + lane;
+    const unsigned lo = blockIdx.x * (unsigned)share;  // rows [lo, lo + share), `rows` the last of all
     uint2 pair[E];
     unsigned rank[E];
+    unsigned lower = 0, mine = 0;  // of this wavefront's tokens
+    {
+        const int per = (n + kSmallBlock - 1) / kSmallBlock;  // <= E per thread
+        const int first = wave * (per * kWave) + lane;
 #pragma unroll
-    for (int k = 0; k < E; ++k) {
-        pair[k] = make_uint2(0, 0);
-        if (k < per) {
-            const int i = first + k * kWave;
-            pair[k] = make_uint2(key_of(ids, i < n ? i : n - 1, rows), (unsigned)i);
+        for (int k = 0; k < E; ++k) {
+            pair[k] = make_uint2(0, 0);
+            if (k < per) {
+                const int i = first + k * kWave;
+                pair[k] = make_uint2(key_of(ids, i < n ? i : n - 1, rows), (unsigned)i);
+            }
         }
+        unsigned long long keep[E];
+#pragma unroll
+        for (int k = 0; k < E; ++k) {
+            const bool valid = k < per && first + k * kWave < n;
+            keep[k] = __ballot(valid && pair[k].x >= lo && pair[k].x - lo < (unsigned)share);
+            lower += (unsigned)__popcll(__ballot(valid && pair[k].x < lo));
+            rank[k] = mine + (unsigned)__popcll(keep[k] & lanes_below(lane));
+            mine += (unsigned)__popcll(keep[k]);
+        }
+        const unsigned sums[2] = {lane == 0 ? mine : 0u, lane == 0 ? lower : 0u};
+        unsigned before[2], total[2];
+        block_excl_scan_n<W, 2>(sums, wsum, before, total);
+        // the wavefront's first lane holds what the wavefronts before it keep
+        const unsigned base = (unsigned)__builtin_amdgcn_readfirstlane((int)before[0]);
+#pragma unroll
+        for (int k = 0; k < E; ++k)
+            if (keep[k] >> lane & 1) local[base + rank[k]] = make_uint2(pair[k].x - lo, pair[k].y);
+        n = (int)total[0];
+        lower = total[1];
     }
+    __syncthreads();
+    const int per = (n + kSmallBlock - 1) / kSmallBlock;
+    const int first = wave * (per * kWave) + lane;
     int shift = 0;
     for (int q = 0; q < passes; ++q) {
         const int bits = (bits_all - shift + passes - q - 1) / (passes - q);
         const int digits = 1 << bits;
+#pragma unroll
+        for (int k = 0; k < E; ++k)
+            if (k < per && first + k * kWave < n) pair[k] = local[first + k * kWave];
         for (int d = threadIdx.x; d < W * kMaxDigits / 2; d += kSmallBlock)
             ((unsigned*)&seen[0][0])[d] = 0;
         __syncthreads();
@@ -316,24 +349,16 @@ __global__ __launch_bounds__(kSmallBlock) void k_eg_small(const Id* __restrict__
             }
         }
         __syncthreads();
-        const bool last = q + 1 == passes;
 #pragma unroll
         for (int k = 0; k < E; ++k) {
-            if (k < per && first + k * kWave < n) {
-                const unsigned at = seen[wave][(pair[k].x >> shift) & (digits - 1)] + rank[k];
-                local[at] = pair[k];
-            }
+            if (k < per && first + k * kWave < n)
+                local[seen[wave][(pair[k].x >> shift) & (digits - 1)] + rank[k]] = pair[k];
         }
         __syncthreads();
-        if (last) break;
-#pragma unroll
-        for (int k = 0; k < E; ++k) {
-            if (k < per && first + k * kWave < n) pair[k] = local[first + k * kWave];
-        }
         shift += bits;
-        __syncthreads();
     }
-    for (int i = threadIdx.x; i < n; i += kSmallBlock) out_pairs[i] = local[i];
+    for (int i = threadIdx.x; i < n; i += kSmallBlock)
+        out_pairs[lower + i] = make_uint2(local[i].x + lo, local[i].y);
 }
 
 // n <= kTiny tokens in one launch: the first `sums` blocks have a wavefront per
@@ -635,7 +660,7 @@ int embed_type(const void* table, long long rows, long long width, long long str
 }
 
 struct GradPlan {
-    int passes, bits_all, bits[4], shift[4];
+    int passes, bits[4], shift[4];
     int tiles, run;
     long long runs;
     long long pairs[2], counts, totals, head, tail, bytes;  // workspace offsets
@@ -646,7 +671,6 @@ bool grad_plan(long long n, long long rows, long long width, GradPlan* p) {
         return false;
     int bits = 1;
     while ((rows >> bits) != 0) ++bits;  // keys 0 .. rows
-    p->bits_all = bits;
     p->passes = (bits + kMaxBits - 1) / kMaxBits;
     int at = 0;
     for (int q = 0; q < p->passes; ++q) {
@@ -752,14 +776,18 @@ int grad_type(const GradPlan& p, const void* grad, long long stride, const void*
     int rc;
     if (n <= kSmall) {
         const long long blocks = pieces / (4 * kSmallBlock) + 1;
-        const dim3 grid((unsigned)(1 + (blocks < 255 ? blocks : 255)));
+        const dim3 grid((unsigned)(kSmallSorts + (blocks < 240 ? blocks : 240)));
+        const int share = (int)((rows + kSmallSorts) / kSmallSorts);  // of keys 0 .. rows
+        int bits = 0;
+        while (((share - 1) >> bits) != 0) ++bits;
+        const int passes = (bits + kMaxBits - 1) / kMaxBits;
         if (id_bytes == 4)
             k_eg_small<int32_t><<<grid, dim3(kSmallBlock), 0, stream>>>(
-                (const int32_t*)ids, (int)n, rows, p.passes, p.bits_all, (uint2*)(ws + p.pairs[0]),
+                (const int32_t*)ids, (int)n, rows, share, passes, bits, (uint2*)(ws + p.pairs[0]),
                 (uint4*)out, pieces, tail, (int)(bytes % 16));
         else
             k_eg_small<int64_t><<<grid, dim3(kSmallBlock), 0, stream>>>(
-                (const int64_t*)ids, (int)n, rows, p.passes, p.bits_all, (uint2*)(ws + p.pairs[0]),
+                (const int64_t*)ids, (int)n, rows, share, passes, bits, (uint2*)(ws + p.pairs[0]),
                 (uint4*)out, pieces, tail, (int)(bytes % 16));
         rc = fail(hipGetLastError());
     } else {

@@ -274,8 +274,8 @@ def _attention(q, k, v, q_offsets, k_offsets, scale, cap, slopes, q_pos, k_pos, 
             raise ValueError(f"prefix must be an int32 tensor of shape {(docs,)}")
         prefix = prefix.contiguous()
     scale = width ** -0.5 if scale is None else float(scale)
-    if not 0.0 < scale < float("inf"):
-        raise ValueError("scale must be positive and finite")
+    if not 1e-30 <= scale <= 1e30:
+        raise ValueError("scale must be positive: from 1e-30 to 1e30")
     if not 0.0 <= cap < float("inf"):
         raise ValueError("cap must be finite, 0 for none")
     axes = 0

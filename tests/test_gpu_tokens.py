@@ -511,3 +511,15 @@ def test_example_learns():
     losses, answer = example.main(steps=20)
     assert all(math.isfinite(v) for v in losses + answer)
     assert losses[-1] < 0.5 * losses[0], losses
+
+
+def test_attend_one_visible_key_has_no_score_gradient():
+    """Its weight is 1 whatever its score: exactly no gradient of q and k."""
+    for q_lens, k_lens, mask in (([5, 3], [1, 1], "full"), ([40, 6], [40, 6], "causal"), ([300], [1], "full")):
+        for axes in (0, 2):
+            s, q_at, k_at, more = _inputs(q_lens, k_lens, 4, 2, 64, F16, 3, axes, mask)
+            made = _compare(s, q_at, k_at, more, 0.0, f"one key {q_lens} {k_lens} {mask}")
+            first = [a for a, n in zip(q_at, q_lens)] if mask == "causal" else slice(None)
+            assert not made["gq"][first].any()
+            if mask == "full":
+                assert not made["gk"].any()
