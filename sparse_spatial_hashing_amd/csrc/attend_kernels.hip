@@ -25,6 +25,7 @@
 #include <hip/hip_runtime.h>
 
 #include "attend.h"
+#include "token_ops.h"
 
 #ifndef ATT_WIDTH
 #error "ATT_WIDTH: 32, 64 or 128"
@@ -131,15 +132,6 @@ __device__ __forceinline__ float other_half(float x) { return __shfl_xor(x, 32);
 
 __device__ __forceinline__ int clampi(int x, int lo, int hi) { return min(max(x, lo), hi); }
 
-// Boundary b of the tokens' ranges: 0, offsets[0 .. docs], total. Range 0 and
-// range docs + 1 are the tokens of no document.
-__device__ __forceinline__ int boundary(const int* offsets, int docs, int total, int b) {
-    if (b <= 0) return 0;
-    if (b > docs + 1) return total;
-    if (!offsets) return b == 1 ? 0 : total;
-    return clampi(offsets[b - 1], 0, total);
-}
-
 // Tile t belongs to the last range whose first tile, floor(start * per / size)
 // + range, is <= t: that leaves every range at least ceil(length * per / size)
 // tiles without anyone knowing the lengths on the host. 64 ranges are tried
@@ -154,7 +146,7 @@ __device__ __forceinline__ int find_range(const int* offsets, int docs, int tota
         const int step = (n + 63) / 64;
         const int b = lo + lane * step;
         const bool in = lane * step < n;
-        const int f = in ? (int)((unsigned long long)boundary(offsets, docs, total, b) * per / SIZE) + b
+        const int f = in ? (int)((unsigned long long)tok_boundary(offsets, docs, total, b) * per / SIZE) + b
                          : 0x7fffffff;
         const unsigned long long hit = __ballot(in && f <= t);
         const int cnt = max(1, (int)__popcll(hit));
@@ -172,10 +164,10 @@ struct Range {
 
 __device__ __forceinline__ Range get_range(const AttArgs& a, int b) {
     Range r;
-    r.qlo = boundary(a.q_offsets, a.docs, a.tq, b);
-    r.lq = max(0, boundary(a.q_offsets, a.docs, a.tq, b + 1) - r.qlo);
-    r.klo = boundary(a.k_offsets, a.docs, a.tk, b);
-    r.lk = max(0, boundary(a.k_offsets, a.docs, a.tk, b + 1) - r.klo);
+    r.qlo = tok_boundary(a.q_offsets, a.docs, a.tq, b);
+    r.lq = max(0, tok_boundary(a.q_offsets, a.docs, a.tq, b + 1) - r.qlo);
+    r.klo = tok_boundary(a.k_offsets, a.docs, a.tk, b);
+    r.lk = max(0, tok_boundary(a.k_offsets, a.docs, a.tk, b + 1) - r.klo);
     r.prefix = 0;
     if (b == 0 || b == a.docs + 1) {
         r.lk = 0;  // rows of no document see nothing
@@ -467,8 +459,8 @@ __device__ __forceinline__ unsigned xcd_block(unsigned bid, unsigned n) {
 // Bound by vector instructions: with a bias a score takes 6 and an exp2 (the
 // bias 2, scale, half a max, sum, half a conversion), 1312 cycles per 32 x 64
 // scores against 512 of the matrix units at a width of 64. 12,000 tokens, 8
-// heads of 64, two axes: 412 us a call, 718 TFLOP/s; six prefixes of 2,300, 16
-// on 4 heads of 128, cap: 249, 721. One token of 16 scenes against 12,000 keys
+// heads of 64, two axes: 400 us a call, 737 TFLOP/s; six prefixes of 2,300, 16
+// on 4 heads of 128, cap: 239, 756. One token of 16 scenes against 12,000 keys
 // at most is bound by memory: 65 us, 4.8 TB/s, and 4.6 for the join.
 // Three wavefronts share a SIMD where they fit without spilling.
 
@@ -943,7 +935,7 @@ __global__ __launch_bounds__(64 * NW, NW == 1 && W == 32 ? 3 : NW == 4 || W < 12
     int first;
     const int range = find_range<kAttRows * NW>(a.k_offsets, a.docs, a.tk, 1, tile, &first);
     Range d = get_range(a, range);
-    const int lk = max(0, boundary(a.k_offsets, a.docs, a.tk, range + 1) - d.klo);
+    const int lk = max(0, tok_boundary(a.k_offsets, a.docs, a.tk, range + 1) - d.klo);
     const long long key0l = (long long)(tile - first) * kAttRows * NW;
     if (key0l < 0 || key0l >= lk) return;
     const int key0 = (int)key0l;
