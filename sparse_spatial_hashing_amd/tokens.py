@@ -11,7 +11,8 @@ holds (rows outside every frame give zeros).
 requires a gradient they run under torch's autograd with the library's
 backward kernels. ``embed_grad``, ``attend_grad`` and ``gated_scan_grad`` are
 the same backward passes as plain functions, for callers that keep their own
-tape or capture a step into a graph. Nothing is read back from the device and
+tape or capture a step into a graph (torch's autograd must not be captured
+while an eager graph of the same leaves is alive). Nothing is read back from the device and
 nothing synchronised; every call works on the current stream of its tensors'
 device, with outputs and workspace allocated by torch.
 """
