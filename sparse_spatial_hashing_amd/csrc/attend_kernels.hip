@@ -52,10 +52,10 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kLowest = -3.402823466e+38f;
 // The backward's weights are computed 2^kLift too large and the sums put right
-// at the end: bf16 has the range, and weights that exp2 would flush to zero
-// keep their gradient. fp16's largest weights times a gradient would overflow.
-constexpr float kLift = ATT_F16 ? 0.0f : 24.0f;
-constexpr float kUnlift = ATT_F16 ? 1.0f : 0x1p-24f;
+// at the end, so that weights of 2^-126 (bf16, exp2's limit) or 2^-28 (fp16,
+// whose largest number is 2^16) and less keep all their bits.
+constexpr float kLift = ATT_F16 ? 14.0f : 24.0f;
+constexpr float kUnlift = ATT_F16 ? 0x1p-14f : 0x1p-24f;
 constexpr float kRescale = 8.0f;  // running maximum may lag by this much (base 2)
 
 __device__ __forceinline__ acc16 mma(vec8 a, vec8 b, acc16 c) {
@@ -157,6 +157,40 @@ __device__ __forceinline__ int find_range(const int* offsets, int docs, int tota
     *first_tile = __builtin_amdgcn_readfirstlane(first);
     return __builtin_amdgcn_readfirstlane(lo);
 }
+
+// Score gradients have the size of grad_out times a weight, which fp16 cannot
+// hold at a loss's usual size and 12,000 keys, nor where grad_out . v is large.
+// There each column carries a power of two that its score gradients are
+// multiplied with before they are rounded, and its sums until the end: from
+// the first that are not zero on, chosen so that the largest comes to
+// 2^kAim, and again when one passes 2^kMost. bf16 has the range (by is 1).
+// Four frames of up to 4,096 in fp16, 8 heads on 2 of 128: 1,515 us forward and
+// backward, without 1,450; a grad_out of 1e-6 then left nothing of grad_q.
+struct Lift {
+    static constexpr int kAim = 8;
+    static constexpr float kMost = 0x1p15f;
+    float by = ATT_F16 ? 0x1p100f : 1.0f;
+
+    __device__ __forceinline__ void apply(acc16& ds, acc16 (&sums)[kBlocks]) {
+        if (!ATT_F16) return;
+        float top = 0.0f;
+#pragma unroll
+        for (int r = 0; r < 16; ++r) top = fmaxf(top, fabsf(ds[r]));
+        if (__any(top * by > kMost)) {
+            top = fmaxf(top, other_half(top));
+            const float was = by;
+            if (top * by > kMost) by = ldexpf(1.0f, kAim - __builtin_amdgcn_frexp_expf(top));
+            const float w = by / was;
+#pragma unroll
+            for (int b = 0; b < kBlocks; ++b)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) sums[b][r] *= w;
+        }
+#pragma unroll
+        for (int r = 0; r < 16; ++r) ds[r] *= by;
+    }
+    __device__ __forceinline__ float undo() const { return ATT_F16 ? 1.0f / by : 1.0f; }
+};
 
 struct Range {
     int qlo, lq, klo, lk, prefix;
@@ -785,6 +819,7 @@ __global__ __launch_bounds__(64 * NW, NW == 1 && W == 32 ? 3 : NW == 4 || W < 12
     const float start = first_summand<AX, CAP>(a, lse2);
     acc16 o[kBlocks], pk[kBlocks];
     float rest = 0.0f;
+    Lift lift;
 #pragma unroll
     for (int b = 0; b < kBlocks; ++b)
 #pragma unroll
@@ -872,6 +907,7 @@ __global__ __launch_bounds__(64 * NW, NW == 1 && W == 32 ? 3 : NW == 4 || W < 12
 #pragma unroll
                 for (int r = 0; r < 16; ++r) dp[r] *= bent[r];
             }
+            lift.apply(dp, o);
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
                 if (kKeep) {
@@ -886,6 +922,7 @@ __global__ __launch_bounds__(64 * NW, NW == 1 && W == 32 ? 3 : NW == 4 || W < 12
         }
     }
     rest = (rest + other_half(rest)) * kUnlift;
+    const float undo = lift.undo();
     if (!row.real) return;
     // saw no key, or one, whose weight is 1 whatever its score: no gradient
     const bool none = row.limit <= 1;
@@ -901,7 +938,7 @@ __global__ __launch_bounds__(64 * NW, NW == 1 && W == 32 ? 3 : NW == 4 || W < 12
 #pragma unroll
             for (int j = 0; j < 4; ++j)
                 x[j] = none ? (elem)0.0f
-                            : (elem)(__builtin_fmaf(-rest, pk[b][4 * q + j], o[b][4 * q + j]) * (a.scale * kUnlift));
+                            : (elem)(__builtin_fmaf(-rest, pk[b][4 * q + j], o[b][4 * q + j] * undo) * (a.scale * kUnlift));
             *(vec4*)(out + c) = x;
         }
 }
@@ -995,6 +1032,7 @@ __global__ __launch_bounds__(64 * NW, NW == 1 && W == 32 ? 3 : NW == 4 || W < 12
     asm volatile("" : "+v"(kpos.x), "+v"(kpos.y), "+v"(steep));
 
     acc16 gk[kBlocks], gv[kBlocks];
+    Lift lift;
 #pragma unroll
     for (int b = 0; b < kBlocks; ++b)
 #pragma unroll
@@ -1103,6 +1141,7 @@ __global__ __launch_bounds__(64 * NW, NW == 1 && W == 32 ? 3 : NW == 4 || W < 12
 #pragma unroll
             for (int r = 0; r < 16; ++r) dp[r] *= __builtin_fmaf(-bent[r], bent[r], 1.0f);
         }
+        lift.apply(dp, gk);
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
             if (c == 0) read_columns(qt_at, 16, col[1]);
@@ -1119,6 +1158,11 @@ __global__ __launch_bounds__(64 * NW, NW == 1 && W == 32 ? 3 : NW == 4 || W < 12
         }
     }
     if (key >= lk) return;
+    const float undo = lift.undo();
+#pragma unroll
+    for (int b = 0; b < kBlocks; ++b)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) gk[b][r] *= undo;
     const long long at = token * a.kv_heads + kvh;
     if (a.nsplit > 1) {
         const long long n = (long long)a.tk * a.kv_heads;

@@ -1,0 +1,88 @@
+"""Token operators on the GPU where the elements' type is narrow: values far
+below and above 1, against the 64-bit definitions. Bounds are those of
+token_reference with half a step of the type's smallest numbers instead of its
+smallest normal number."""
+import math
+
+import pytest
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+if not torch.cuda.is_available():
+    pytest.skip("no GPU", allow_module_level=True)
+
+import sparse_spatial_hashing_amd as ssh  # noqa: E402
+import token_reference as ref  # noqa: E402
+
+DEV = torch.device("cuda:0")
+BF16, F16, F32 = torch.bfloat16, torch.float16, torch.float32
+
+
+def _ends(lens):
+    return [0] + torch.tensor(lens).cumsum(0).tolist()
+
+
+def _at(ends):
+    return torch.tensor(ends, dtype=torch.int32, device=DEV)
+
+
+def _check(got, want, dtype, what):
+    """As ref.check, but results under the smallest normal number count too."""
+    tiny = torch.finfo(dtype).smallest_normal
+    ref.check(got, want[0], want[1] - tiny + tiny * ref.unit(dtype), what)
+
+
+def _gradients(q, k, v, grad, ends, what, **more):
+    scale = q.shape[2] ** -0.5
+    want = ref.attend(q, k, v, ends, ends, scale, grad=grad, **more)
+    print(what, flush=True)
+    m = dict({n: x.to(DEV) if isinstance(x, torch.Tensor) else x for n, x in more.items()},
+             q_offsets=_at(ends), k_offsets=_at(ends))
+    q, k, v, grad = (t.to(DEV) for t in (q, k, v, grad))
+    out, lse = ssh.attend(q, k, v, return_lse=True, **m)
+    return dict(zip(("gq", "gk", "gv"), ssh.attend_grad(grad, q, k, v, out, lse, **m))), want
+
+
+SIZES = [([2000], 64, 0, 0.0, False), ([40, 33, 7], 32, 3, 20.0, False), ([900, 300], 128, 2, 0.0, True),
+         ([60, 2], 128, 0, 30.0, True)]
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("size", [1e-6, 1e-3, 1e4])
+@pytest.mark.parametrize("lens,width,axes,cap,causal", SIZES)
+def test_gradients_of_any_size(dtype, size, lens, width, axes, cap, causal):
+    """Score gradients far under the type's smallest number, and over its largest. Large keys
+    bring grad_q back into range, large queries grad_k."""
+    gen = torch.Generator().manual_seed(width)
+    ends, heads = _ends(lens), 2
+    n = ends[-1]
+    more = dict(cap=cap, causal=causal)
+    if axes:
+        pos = (torch.rand((n, axes), generator=gen) * 40).int()
+        more.update(q_pos=pos, k_pos=pos, slopes=torch.tensor([0.125, 0.03125]))
+    grow = torch.exp2(torch.linspace(-6, 3, n))[:, None, None]  # along the tokens: later ones count most
+    for by, back in (("gq", False), ("gk", False), ("gq", True), ("gk", True)):
+        large, little = (50.0, 0.02) if size < 1 else (0.02, 0.02)
+        std = dict(gq=(little, large), gk=(large, little))[by]
+        q, k = (torch.randn((n, h, width), generator=gen) * s for h, s in zip((heads, 1), std))
+        v, grad = torch.randn((n, 1, width), generator=gen), torch.randn((n, heads, width), generator=gen)
+        v, grad = v * (grow.flip(0) if back else grow), grad * size / grow.max() * (grow if back else 1.0)
+        q, k, v, grad = (t.to(dtype) for t in (q, k, v, grad))
+        made, want = _gradients(q, k, v, grad, ends, f"{by} of size {size} {lens} w {width} {dtype}", **more)
+        _check(made[by], want[by], dtype, f"{by} of size {size} {lens} w {width} {dtype}")
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("lens,width", [([70], 64), ([30, 300], 128), ([500], 32)])
+def test_gradients_through_small_weights(dtype, lens, width):
+    """Keys of weights down to e^-16 and large gradients: grad_v keeps them."""
+    gen = torch.Generator().manual_seed(width)
+    ends = _ends(lens)
+    n = ends[-1]
+    q, k, v, grad = (torch.randn((n, 1, width), generator=gen) for _ in range(4))
+    q[..., 0], k[..., 0] = 4.0, torch.linspace(0, -16, n)[:, None] * width ** 0.5 / 4
+    made, want = _gradients(q.to(dtype), k.to(dtype), v.to(dtype), (grad * 500).to(dtype), ends,
+                            f"small weights {lens} w {width} {dtype}")
+    for name in ("gq", "gk", "gv"):
+        _check(made[name], want[name], dtype, f"{name} small weights {lens} w {width} {dtype}")
