@@ -57,6 +57,11 @@ constexpr float kLowest = -3.402823466e+38f;
 constexpr float kLift = ATT_F16 ? 14.0f : 24.0f;
 constexpr float kUnlift = ATT_F16 ? 0x1p-14f : 0x1p-24f;
 constexpr float kRescale = 8.0f;  // running maximum may lag by this much (base 2)
+// The forward's weights are computed less a number 2^kTop under the running
+// maximum: fp16 then holds them from 2^15 on down, with all their bits to 2^-21
+// of the largest (2^-14 without, and nothing under 2^-25: a dominant key hid
+// what 20,000 others of e^-17.5 its weight add up to).
+constexpr float kTop = ATT_F16 ? 7.0f : 0.0f;
 
 __device__ __forceinline__ acc16 mma(vec8 a, vec8 b, acc16 c) {
 #if ATT_F16
@@ -487,8 +492,9 @@ __device__ __forceinline__ unsigned xcd_block(unsigned bid, unsigned n) {
 }
 
 // ---- forward ---------------------------------------------------------------
-// Scores are computed less the running maximum m of the tiles before, so the
-// largest of a tile says how far m lags; up to 2^kRescale nothing is rescaled.
+// Scores are computed less m, kTop under the maximum of the tiles before, so
+// the largest of a tile says how far m lags; up to 2^kRescale nothing is
+// rescaled.
 // Key tiles are loaded one ahead into the other half of LDS.
 // Bound by vector instructions: with a bias a score takes 6 and an exp2 (the
 // bias 2, scale, half a max, sum, half a conversion), 1312 cycles per 32 x 64
@@ -602,11 +608,11 @@ __global__ __launch_bounds__(64 * NW, NW == 4 && (W < 128 || AX == 0) ? 3 : NW =
         for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
             for (int r = 0; r < 16; ++r) top = fmaxf(top, s[nb][r]);
-        if (t == t0 || __any(top > kRescale)) {
+        if (t == t0 || __any(top > kTop + kRescale)) {
             top = fmaxf(top, other_half(top));
             // a row's visible keys are its document's first ones: it sees some
             // in the first tile or none at all
-            const float up = t == t0 ? (top > -__builtin_inff() ? top : 0.0f) : fmaxf(top, 0.0f);
+            const float up = t == t0 ? (top > -__builtin_inff() ? top - kTop : 0.0f) : fmaxf(top - kTop, 0.0f);
             m += up;
             if (t > t0) {
                 const float w = exp2_(-up);

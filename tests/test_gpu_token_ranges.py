@@ -86,3 +86,29 @@ def test_gradients_through_small_weights(dtype, lens, width):
                             f"small weights {lens} w {width} {dtype}")
     for name in ("gq", "gk", "gv"):
         _check(made[name], want[name], dtype, f"{name} small weights {lens} w {width} {dtype}")
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("q_len,width,place,axes", [(1, 128, 0, 0), (1, 64, 0, 2), (40, 32, 0, 0), (150, 64, 0, 3),
+                                                    (150, 128, 0, 0), (70, 128, 5000, 2), (1, 80, 19999, 0)])
+def test_many_small_weights(dtype, q_len, width, place, axes):
+    """One key with nearly all the weight and a value of zero: the output is what 20,000 keys of
+    e^-17.5 its weight add up to."""
+    gen = torch.Generator().manual_seed(width)
+    n = 20000
+    q, k, v = (torch.randn((m, 1, width), generator=gen) * s for m, s in ((q_len, 0.1), (n, 0.1), (n, 0.1)))
+    q[..., 0], k[..., 0], k[place, 0, 0] = 4.0, 0.0, 17.5 * width ** 0.5 / 4
+    v += 1.0
+    v[place] = 0.0
+    q, k, v = (t.to(dtype) for t in (q, k, v))
+    more = {}
+    if axes:
+        more = dict(q_pos=torch.ones((q_len, axes), dtype=torch.int32),
+                    k_pos=torch.ones((n, axes), dtype=torch.int32), slopes=torch.tensor([0.5]))
+    want = ref.attend(q, k, v, [0, q_len], [0, n], width ** -0.5, **more)
+    what = f"small weights {q_len} w {width} at {place} {dtype}"
+    print(what, flush=True)
+    more = {name: t.to(DEV) for name, t in more.items()}
+    out, lse = ssh.attend(q.to(DEV), k.to(DEV), v.to(DEV), return_lse=True, **more)
+    _check(out, want["out"], dtype, what)
+    ref.check(lse, *want["lse"], what + " lse")
