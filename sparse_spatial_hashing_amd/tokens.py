@@ -14,7 +14,8 @@ the same backward passes as plain functions, for callers that keep their own
 tape or capture a step into a graph (torch's autograd must not be captured
 while an eager graph of the same leaves is alive). Nothing is read back from the device and
 nothing synchronised; every call works on the current stream of its tensors'
-device, with outputs and workspace allocated by torch.
+device, with outputs and workspace allocated by torch. Torch sees none of the
+kernels: forward-mode derivatives and tracing raise NotImplementedError.
 """
 from __future__ import annotations
 
@@ -23,6 +24,8 @@ import struct
 from typing import Optional, Tuple
 
 import torch
+from torch.autograd import forward_ad
+from torch.fx.experimental.proxy_tensor import get_proxy_mode
 
 from . import VoxError, _check, library
 
@@ -79,6 +82,19 @@ _declare(_lib)
 
 
 _HALF = {torch.bfloat16: 1, torch.float16: 2}
+# a proxy mode comes with a function mode, which is cheaper to ask for
+_jit_tracing, _function_modes = torch._C._is_tracing, torch._C._len_torch_function_stack
+
+
+def _unseen(what: str, *tensors) -> None:
+    """Refuses what would lose the kernels without a word: a tangent, which the outputs would
+    not carry, and tracing, which would record their allocation alone."""
+    if forward_ad._current_level >= 0:
+        for t in tensors:
+            if isinstance(t, torch.Tensor) and forward_ad.unpack_dual(t).tangent is not None:
+                raise NotImplementedError(f"{what} has no forward-mode derivative")
+    if _jit_tracing() or _function_modes() and get_proxy_mode() is not None:
+        raise NotImplementedError(f"{what} cannot be traced")
 
 
 def _on_gpu(name: str, t: torch.Tensor, index: int = -1) -> int:
@@ -162,6 +178,7 @@ def _check_ids(ids: torch.Tensor, index: int) -> torch.Tensor:
 
 
 def _embed(table: torch.Tensor, ids: torch.Tensor, scale: float) -> torch.Tensor:
+    _unseen("embed", table)
     dtype = _floating("table", table)
     index = table.get_device()
     if table.dim() != 2 or not table.numel():
@@ -182,6 +199,7 @@ def embed_grad(grad: torch.Tensor, ids: torch.Tensor, rows: int, *,
     sum of ``scale * grad[i]`` over the tokens i with ids[i] == r, in float32
     and in a fixed order (the same inputs give the same bits). grad is
     [*ids.shape, width]."""
+    _unseen("embed_grad", grad)
     dtype = _floating("grad", grad)
     index = grad.get_device()
     ids = _check_ids(ids, index)
@@ -308,6 +326,7 @@ def _attention(q, k, v, q_offsets, k_offsets, scale, cap, slopes, q_pos, k_pos, 
 
 
 def _attend(q, k, v, want_lse, **more):
+    _unseen("attend", q, k, v, more["slopes"])
     a, kept = _attention(q, k, v, **more)
     q, k, v = kept[:3]
     nbytes = _size(_lib.tok_attend_workspace_bytes(a), "tok_attend_workspace_bytes")
@@ -329,6 +348,7 @@ def attend_grad(grad_out: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: tor
     """Gradients of ``attend``'s q, k and v from that of its output, with the
     out and lse it returned and the same other arguments. Gradients of shared
     key heads are summed over their query heads in float32."""
+    _unseen("attend_grad", grad_out, q, k, v, out, lse, slopes)
     a, kept = _attention(q, k, v, q_offsets, k_offsets, scale, cap, slopes, q_pos, k_pos, causal,
                          prefix, grad_out)
     q, k, v, g = kept[:4]
@@ -411,6 +431,7 @@ def _scan_args(gate, x, offsets):
 
 
 def _scan(gate, x, offsets, state, reverse, want_carry):
+    _unseen("gated_scan", gate, x, state)
     dtype, gate, x, offsets, docs = _scan_args(gate, x, offsets)
     t, width = x.shape
     state = _state("state", state, docs, width, x.get_device())
@@ -433,6 +454,7 @@ def gated_scan_grad(grad_y: torch.Tensor, gate: torch.Tensor, x: torch.Tensor,
     """Gradients of ``gated_scan``'s gate, x and initial state from those of y
     and of the last state (``grad_state``, None: zeros), with the carry it
     returned and the same other arguments."""
+    _unseen("gated_scan_grad", grad_y, gate, x, carry, state, grad_state)
     dtype, gate, x, offsets, docs = _scan_args(gate, x, offsets)
     t, width = x.shape
     _floating("grad_y", grad_y, x)

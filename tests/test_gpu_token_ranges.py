@@ -112,3 +112,24 @@ def test_many_small_weights(dtype, q_len, width, place, axes):
     out, lse = ssh.attend(q.to(DEV), k.to(DEV), v.to(DEV), return_lse=True, **more)
     _check(out, want["out"], dtype, what)
     ref.check(lse, *want["lse"], what + " lse")
+
+
+def test_forward_mode_and_traces_are_refused_and_compilation_goes_round():
+    """torch sees no kernel: what would lose them raises, torch.compile leaves the call as it is."""
+    import torch.autograd.forward_ad as forward_ad
+    from torch.fx.experimental.proxy_tensor import make_fx
+    gen = torch.Generator().manual_seed(1)
+    table = torch.randn((9, 8), generator=gen).to(DEV)
+    ids = torch.randint(0, 9, (40,), generator=gen).to(DEV)
+    h = torch.randn((40, 2, 16), generator=gen).to(DEV, BF16)
+    calls = ((table, lambda t: ssh.embed(t, ids)), (h, lambda t: ssh.attend(t, h, h)),
+             (table, lambda t: ssh.gated_scan(t, table)[0]))
+    for t, call in calls:
+        with forward_ad.dual_level(), pytest.raises(NotImplementedError):
+            call(forward_ad.make_dual(t, torch.ones_like(t)))
+        with forward_ad.dual_level(), pytest.raises(NotImplementedError):
+            call(forward_ad.make_dual(t.clone().requires_grad_(), torch.ones_like(t)))
+        with pytest.raises(NotImplementedError):
+            make_fx(call)(t)
+        torch._dynamo.reset()
+        assert torch.equal(torch.compile(lambda x: call(x) * 2, backend="eager")(t), call(t) * 2)

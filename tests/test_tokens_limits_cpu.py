@@ -1,0 +1,53 @@
+"""What the token operators refuse, and where their limits lie, without a GPU."""
+import torch
+import torch.autograd.forward_ad as forward_ad
+import pytest
+from torch.fx.experimental.proxy_tensor import make_fx
+
+import sparse_spatial_hashing_amd as ssh
+from sparse_spatial_hashing_amd import tokens
+
+LIB = tokens._lib
+EINVAL = -1
+
+
+# name, and a call of one float tensor among the operator's arguments
+ROWS, HEADS = torch.zeros((4, 8)), torch.zeros((4, 1, 8), dtype=torch.bfloat16)
+IDS, PLACES, SLOPES = torch.zeros(4, dtype=torch.int32), torch.zeros((4, 1), dtype=torch.int32), torch.zeros(1)
+LSE, CARRY = torch.zeros((4, 1)), torch.zeros((1, 8))
+CALLS = {
+    "embed": (ROWS, lambda t: ssh.embed(t, IDS)),
+    "embed_grad": (ROWS, lambda t: ssh.embed_grad(t, IDS, 4)),
+    "attend q": (HEADS, lambda t: ssh.attend(t, HEADS, HEADS)),
+    "attend v": (HEADS, lambda t: ssh.attend(HEADS, HEADS, t)),
+    "attend slopes": (SLOPES, lambda t: ssh.attend(HEADS, HEADS, HEADS, slopes=t, q_pos=PLACES,
+                                                   k_pos=PLACES)),
+    "attend_grad": (HEADS, lambda t: ssh.attend_grad(t, HEADS, HEADS, HEADS, HEADS, LSE)),
+    "gated_scan": (ROWS, lambda t: ssh.gated_scan(ROWS, t)[0]),
+    "gated_scan state": (CARRY, lambda t: ssh.gated_scan(ROWS, ROWS, state=t)[0]),
+    "gated_scan_grad": (ROWS, lambda t: ssh.gated_scan_grad(t, ROWS, ROWS, CARRY)[0]),
+}
+
+
+@pytest.mark.parametrize("name", CALLS)
+def test_forward_mode_is_refused(name):
+    """A dual tensor's tangent would be lost without a word: the call refuses before any other check."""
+    t, call = CALLS[name]
+    with forward_ad.dual_level():
+        dual = forward_ad.make_dual(t, torch.ones_like(t))
+        with pytest.raises(NotImplementedError, match="forward-mode"):
+            call(dual)
+        with pytest.raises(ValueError, match="GPU"):  # no tangent: the next check
+            call(t)
+
+
+@pytest.mark.parametrize("name", CALLS)
+@pytest.mark.parametrize("how", [dict(), dict(pre_dispatch=True), dict(tracing_mode="fake"), "jit"])
+def test_tracing_is_refused(name, how):
+    """A trace would hold the outputs' allocation and no kernel."""
+    t, call = CALLS[name]
+    with pytest.raises(NotImplementedError, match="traced"):
+        if how == "jit":
+            torch.jit.trace(call, t)
+        else:
+            make_fx(call, **how)(t)
