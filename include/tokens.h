@@ -145,7 +145,7 @@ int tok_attend_grad(const tok_attention* args, const void* q, const void* k, con
  * TOK_SCAN_RUN tokens, [tok_scan_runs(t), width] float32, for tok_scan_grad.
  * The workspace (0 bytes: NULL will do) needs no initial contents, 256-byte
  * aligned.
- * Limits: t < 2^31, 1 <= width <= 65536, 1 <= docs <= 2^20.
+ * Limits: 0 <= t <= 2^31 - 2048, 1 <= width <= 65536, 1 <= docs <= 2^20.
  */
 #define TOK_SCAN_RUN 16
 int64_t tok_scan_runs(int64_t t);

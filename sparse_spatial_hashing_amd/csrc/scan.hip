@@ -20,7 +20,10 @@ int ssh_hip_fail(hipError_t e);  // records the error for vox_last_hip_error()
 namespace {
 
 constexpr int kRun = TOK_SCAN_RUN;
-constexpr long long kMaxTokens = 0x7fffffffll;
+constexpr int kMaxChunk = 1024;
+// Steps are counted in 32 bits: the end of a chunk that starts under t, and the
+// step after a batch that does, have to stay under 2^31.
+constexpr long long kMaxTokens = (1ll << 31) - 2 * kMaxChunk;
 constexpr long long kMaxWidth = 65536;
 constexpr int kMaxDocs = 1 << 20;
 
@@ -519,7 +522,7 @@ bool check(int dtype, long long t, long long width, const int32_t* offsets, int3
 // Up to 64 steps are one chunk: its walk takes less than two more launches.
 int chunk_of(long long t) {
     int chunk = t <= 64 ? 64 : 32;
-    while (chunk < 1024 && (t + chunk - 1) / chunk > 3000) chunk *= 2;
+    while (chunk < kMaxChunk && (t + chunk - 1) / chunk > 3000) chunk *= 2;
     return chunk;
 }
 

@@ -51,3 +51,16 @@ def test_tracing_is_refused(name, how):
             torch.jit.trace(call, t)
         else:
             make_fx(call, **how)(t)
+
+
+def test_recurrence_steps_stay_in_32_bits():
+    """The longest t accepted keeps the end of its last chunk (1024 steps at most) under 2^31."""
+    most, p = 2**31 - 2048, 4096
+    assert -(-most // 1024) * 1024 < 2**31
+    assert LIB.tok_scan_runs(most) == most // tokens.TOK_SCAN_RUN
+    nbytes = LIB.tok_scan_workspace_bytes(most, 1)
+    assert nbytes > 0
+    for t in (most + 1, 2**31 - 1024, 2**31 - 1):
+        assert LIB.tok_scan_runs(t) == EINVAL and LIB.tok_scan_workspace_bytes(t, 1) == EINVAL
+        assert LIB.tok_scan(p, p, 1, t, 1, p, 2, 0, p, p, p, p, p, 1 << 40, None) == EINVAL
+        assert LIB.tok_scan_grad(p, p, p, p, 1, t, 1, p, 2, 0, p, p, p, p, p, p, 1 << 40, None) == EINVAL
