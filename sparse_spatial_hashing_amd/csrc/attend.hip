@@ -13,7 +13,9 @@ int ssh_hip_fail(hipError_t e);  // records the error for vox_last_hip_error()
 
 namespace {
 
-constexpr long long kMaxElems = 0x7fffffffll;
+// Rows and keys are counted in 32 bits, and so is the end of a tile of up to
+// 128 that starts under the last.
+constexpr long long kMaxElems = (1ll << 31) - 2048;
 constexpr int kMaxDocs = 1 << 20;
 constexpr long long kMaxStride = 1ll << 25;
 

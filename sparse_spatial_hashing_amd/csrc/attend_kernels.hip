@@ -219,7 +219,7 @@ __device__ __forceinline__ Range get_range(const AttArgs& a, int b) {
 // Keys [0, limit) of the document are visible to its query i.
 __device__ __forceinline__ int key_limit(const AttArgs& a, const Range& d, int i) {
     if (!a.mask) return d.lk;
-    return clampi(max(d.prefix, min(d.lk, i + d.lk - d.lq + 1)), 0, d.lk);
+    return clampi(max(d.prefix, min(d.lk, i - d.lq + d.lk + 1)), 0, d.lk);
 }
 
 // A token's position as it is in memory, and packed for sad_u16: .x the last

@@ -1,4 +1,6 @@
 """What the token operators refuse, and where their limits lie, without a GPU."""
+import ctypes
+
 import torch
 import torch.autograd.forward_ad as forward_ad
 import pytest
@@ -64,3 +66,25 @@ def test_recurrence_steps_stay_in_32_bits():
         assert LIB.tok_scan_runs(t) == EINVAL and LIB.tok_scan_workspace_bytes(t, 1) == EINVAL
         assert LIB.tok_scan(p, p, 1, t, 1, p, 2, 0, p, p, p, p, p, 1 << 40, None) == EINVAL
         assert LIB.tok_scan_grad(p, p, p, p, 1, t, 1, p, 2, 0, p, p, p, p, p, p, 1 << 40, None) == EINVAL
+
+
+def _attention(**more):
+    base = dict(dtype=1, heads=1, kv_heads=1, width=8, tq=8, tk=8, docs=1, mask=0, scale=1.0, cap=0.0,
+                q_stride=(8, 8), k_stride=(8, 8), v_stride=(8, 8), g_stride=(8, 8))
+    base.update(more)
+    return ctypes.byref(tokens._Attention(**base))
+
+
+def test_attention_rows_stay_in_32_bits():
+    """The most rows and keys accepted keep the end of a tile (128 at most) under 2^31."""
+    most, p = 2**31 - 2048, 4096
+    for good in (dict(tq=most), dict(tk=most), dict(tq=most // 16, heads=16, q_stride=(128, 8))):
+        assert LIB.tok_attend_workspace_bytes(_attention(**good)) >= 0
+        assert LIB.tok_attend_grad_workspace_bytes(_attention(**good)) >= 0
+    for bad in (dict(tq=most + 1), dict(tk=most + 1), dict(tq=2**31 - 1, mask=1), dict(tk=2**31 - 100),
+                dict(tq=most // 16 + 1, heads=16, q_stride=(128, 8)),
+                dict(tk=most // 2 + 1, heads=2, kv_heads=2, k_stride=(16, 8))):
+        a = _attention(**bad)
+        assert LIB.tok_attend_workspace_bytes(a) == EINVAL and LIB.tok_attend_grad_workspace_bytes(a) == EINVAL
+        assert LIB.tok_attend(a, p, p, p, p, None, p, 1 << 60, None) == EINVAL
+        assert LIB.tok_attend_grad(a, *[p] * 10, 1 << 60, None) == EINVAL
