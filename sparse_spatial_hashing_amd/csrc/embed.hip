@@ -625,16 +625,22 @@ int embed_run(const void* table, long long rows, long long width, long long stri
     // (2,097,152 rows: 77 us a call, with one 91; 97 rows: the same).
     const long long threads = n << lpr_log;
     const int r = threads >= 4ll * 8 * 64 * 1024 ? 4 : 1;
-    const long long per = (long long)(kBlock >> lpr_log) * r, blocks = (n + per - 1) / per;
-    if (blocks > 0x7fffffffll) return VOX_EINVAL;
-    const dim3 grid((unsigned)blocks), block(kBlock);
-    if (r == 4)
-        k_embed<T, N, Id, 4><<<grid, block, 0, stream>>>((const T*)table, rows, (int)width, stride,
-                                                         (const Id*)ids, n, scale, (T*)out, lpr_log);
-    else
-        k_embed<T, N, Id, 1><<<grid, block, 0, stream>>>((const T*)table, rows, (int)width, stride,
-                                                         (const Id*)ids, n, scale, (T*)out, lpr_log);
-    return fail(hipGetLastError());
+    const long long per = (long long)(kBlock >> lpr_log) * r, slice = most_blocks(kBlock) * per;
+    for (long long first = 0; first < n; first += slice) {
+        const long long rest = n - first < slice ? n - first : slice;
+        const dim3 grid((unsigned)((rest + per - 1) / per)), block(kBlock);
+        const Id* from = (const Id*)ids + first;
+        T* to = (T*)out + first * width;
+        if (r == 4)
+            k_embed<T, N, Id, 4><<<grid, block, 0, stream>>>((const T*)table, rows, (int)width, stride, from,
+                                                             rest, scale, to, lpr_log);
+        else
+            k_embed<T, N, Id, 1><<<grid, block, 0, stream>>>((const T*)table, rows, (int)width, stride, from,
+                                                             rest, scale, to, lpr_log);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return fail(e);
+    }
+    return VOX_OK;
 }
 
 template <typename T, int N>

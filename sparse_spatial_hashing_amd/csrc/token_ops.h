@@ -16,6 +16,10 @@ inline bool tok_dtype_ok(int dtype) {
     return dtype == TOK_F32 || dtype == TOK_BF16 || dtype == TOK_F16;
 }
 
+// Blocks of one launch: of 2^32 threads or more along a dimension HIP leaves some
+// out, without an error.
+constexpr long long most_blocks(int threads) { return 0xffffffffll / threads; }
+
 // NULL will do where nothing is needed.
 inline bool workspace_ok(const void* p, long long bytes, long long need) {
     return need == 0 || (p && ((size_t)p & 255) == 0 && bytes >= need);

@@ -133,3 +133,18 @@ def test_forward_mode_and_traces_are_refused_and_compilation_goes_round():
             make_fx(call)(t)
         torch._dynamo.reset()
         assert torch.equal(torch.compile(lambda x: call(x) * 2, backend="eager")(t), call(t) * 2)
+
+
+def test_embed_more_rows_than_one_launch_holds():
+    """67 M rows of 129, four to a block: 2^24 blocks of 256 threads, one more than a launch takes."""
+    n, width = (1 << 26) + 5, 129
+    gen = torch.Generator().manual_seed(4)
+    table = torch.randn((50, width), generator=gen).to(DEV, F16)
+    ids = (torch.arange(n, device=DEV, dtype=torch.int32) * 7) % 53 - 2
+    print(f"embed {n} rows of {width}", flush=True)
+    out = ssh.embed(table, ids)
+    where = torch.cat([torch.arange(2000), torch.arange((1 << 26) - 2000, n),
+                       torch.randint(0, n, (100000,), generator=gen)]).to(DEV)
+    i = ids[where].long()
+    want = torch.where((i >= 0)[:, None] & (i < 50)[:, None], table[i.clamp(0, 49)], 0)
+    assert torch.equal(out[where], want)
