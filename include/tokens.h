@@ -101,7 +101,7 @@ typedef struct tok_attention {
     int32_t heads, kv_heads;    /* heads a multiple of kv_heads */
     int32_t width;
     int64_t tq, tk;             /* tokens; tq * heads, tk * kv_heads <= 2^31 - 2048 */
-    int32_t docs;               /* >= 1, at most 2^20 */
+    int32_t docs;               /* >= 1, at most 2^20; (docs + 2) * kv_heads <= 2^30 */
     int32_t mask;               /* 0: every key of the document; 1: causal / prefix */
     const int32_t* q_offsets;   /* device [docs + 1]; NULL: one document of all tokens */
     const int32_t* k_offsets;

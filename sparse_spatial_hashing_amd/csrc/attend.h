@@ -33,6 +33,7 @@ struct AttArgs {
     int tq, tk, docs, heads, kv_heads, group, width, mask, axes;
     int nsplit;           // ranges a document's keys (forward) or queries (dK dV) are split into
     int tiles;            // row tiles (forward, dQ) or key tiles (dK dV) over all documents
+    unsigned first_block; // of this launch, among all the pass's blocks
     float scale;          // > 0
     float scale2;         // scale * log2(e)
     float unscale2;       // 1 / scale2

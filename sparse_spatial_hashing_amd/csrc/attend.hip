@@ -17,6 +17,9 @@ namespace {
 // 128 that starts under the last.
 constexpr long long kMaxElems = (1ll << 31) - 2048;
 constexpr int kMaxDocs = 1 << 20;
+// Documents times key heads: every document may start a tile, and 2^26 more may
+// be full, which leaves the blocks of a pass under 2^31.
+constexpr long long kMaxStarts = 1ll << 30;
 constexpr long long kMaxStride = 1ll << 25;
 
 // 16-byte pieces; a tile of 64 tokens spans less than 2^32 bytes.
@@ -31,6 +34,7 @@ bool check(const tok_attention* t) {
     if (t->tq < 0 || t->tk < 0 || t->tq > kMaxElems || t->tk > kMaxElems ||
         t->tq * t->heads > kMaxElems || t->tk * t->kv_heads > kMaxElems)
         return false;
+    if ((t->docs + 2ll) * t->kv_heads > kMaxStarts) return false;
     if (t->docs < 1 || t->docs > kMaxDocs || (t->mask != 0 && t->mask != 1)) return false;
     if ((!t->q_offsets || !t->k_offsets) && t->docs != 1) return false;
     if (t->prefix && !t->mask) return false;

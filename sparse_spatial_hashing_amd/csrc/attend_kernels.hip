@@ -514,7 +514,7 @@ __global__ __launch_bounds__(64 * NW, NW == 4 && (W < 128 || AX == 0) ? 3 : NW =
     __shared__ __align__(16) unsigned kpx[2][AX ? BN : 4], kpy[2][AX == 3 ? BN : 4];
 
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, half = lane >> 5;
-    unsigned id = xcd_block(blockIdx.x, gridDim.x);
+    unsigned id = a.first_block + xcd_block(blockIdx.x, gridDim.x);
     const int split = (int)(id % a.nsplit);
     id /= a.nsplit;
     const int tile = a.tiles - 1 - (int)(id % a.tiles);  // long causal rows first
@@ -764,7 +764,7 @@ __global__ __launch_bounds__(64 * NW, NW == 1 && W == 32 ? 3 : NW == 4 || W < 12
     __shared__ uint4 kept_q[kKeep ? NW : 1][kKeep ? 64 * kKeepQ : 1];
 
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, half = lane >> 5;
-    const unsigned id = xcd_block(blockIdx.x, gridDim.x);
+    const unsigned id = a.first_block + xcd_block(blockIdx.x, gridDim.x);
     const int tile = a.tiles - 1 - (int)(id % a.tiles);
     const int kvh = (int)(id / a.tiles);
     int first;
@@ -970,7 +970,7 @@ __global__ __launch_bounds__(64 * NW, NW == 1 && W == 32 ? 3 : NW == 4 || W < 12
     __shared__ uint4 kept[kKeep ? NW : 1][kKeep ? 64 * kSteps : 1];
 
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, half = lane >> 5;
-    unsigned id = xcd_block(blockIdx.x, gridDim.x);
+    unsigned id = a.first_block + xcd_block(blockIdx.x, gridDim.x);
     const int split = (int)(id % a.nsplit);
     id /= a.nsplit;
     const int tile = (int)(id % a.tiles);  // causal: the first keys have the most rows
@@ -1230,28 +1230,28 @@ template <int AX, bool CAP, int NW>
 hipError_t launch(AttPass pass, const AttArgs& a, hipStream_t stream) {
     // keys of a tile: 64 where two tiles of k and v, twice, leave LDS for two blocks
     constexpr int BN = NW == 4 && W <= 64 ? 64 : 32, BF = NW == 4 && (W <= 64 || AX) ? 64 : 32;
-    const dim3 block(64 * NW);
-    const long long blocks = (long long)a.tiles * a.kv_heads * (pass == kAttGradQ ? 1 : a.nsplit);
-    if (blocks <= 0 || blocks > 0x7fffffffll) return hipErrorInvalidValue;
-    const dim3 grid((unsigned)blocks);
-    if (pass == kAttForward) {
-        k_att_forward<AX, CAP, NW, BF><<<grid, block, 0, stream>>>(a);
-        if (a.nsplit > 1) {
-            const hipError_t e = hipGetLastError();
-            if (e != hipSuccess) return e;
-            const long long n = (long long)a.tq * a.heads;
-            k_att_join<<<dim3((unsigned)((n + 3) / 4)), dim3(256), 0, stream>>>(a);
-        }
-    } else if (pass == kAttGradQ) {
-        k_att_grad_q<AX, CAP, NW, BN><<<grid, block, 0, stream>>>(a);
-    } else {
-        k_att_grad_kv<AX, CAP, NW><<<grid, block, 0, stream>>>(a);
-        if (a.nsplit > 1) {
-            const hipError_t e = hipGetLastError();
-            if (e != hipSuccess) return e;
-            const long long n = (long long)a.tk * a.kv_heads * a.width / 4;
-            k_att_join_kv<<<dim3((unsigned)((n + 255) / 256)), dim3(256), 0, stream>>>(a);
-        }
+    const unsigned blocks = (unsigned)a.tiles * a.kv_heads * (pass == kAttGradQ ? 1 : a.nsplit);
+    constexpr unsigned kMost = (unsigned)most_blocks(64 * NW);
+    for (unsigned first = 0; first < blocks; first += kMost) {
+        const dim3 grid(blocks - first < kMost ? blocks - first : kMost), block(64 * NW);
+        AttArgs slice = a;
+        slice.first_block = first;
+        if (pass == kAttForward)
+            k_att_forward<AX, CAP, NW, BF><<<grid, block, 0, stream>>>(slice);
+        else if (pass == kAttGradQ)
+            k_att_grad_q<AX, CAP, NW, BN><<<grid, block, 0, stream>>>(slice);
+        else
+            k_att_grad_kv<AX, CAP, NW><<<grid, block, 0, stream>>>(slice);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    // joins: few rows and keys, or nothing is split
+    if (pass == kAttForward && a.nsplit > 1) {
+        const long long n = (long long)a.tq * a.heads;
+        k_att_join<<<dim3((unsigned)((n + 3) / 4)), dim3(256), 0, stream>>>(a);
+    } else if (pass == kAttGradKV && a.nsplit > 1) {
+        const long long n = (long long)a.tk * a.kv_heads * a.width / 4;
+        k_att_join_kv<<<dim3((unsigned)((n + 255) / 256)), dim3(256), 0, stream>>>(a);
     }
     return hipGetLastError();
 }

@@ -148,3 +148,19 @@ def test_embed_more_rows_than_one_launch_holds():
     i = ids[where].long()
     want = torch.where((i >= 0)[:, None] & (i < 50)[:, None], table[i.clamp(0, 49)], 0)
     assert torch.equal(out[where], want)
+
+
+def test_attend_more_blocks_than_one_launch_holds():
+    """A million sequences of one token, 64 heads: 69 M blocks of a wavefront, 2^26 and more. The one
+    key's weight is 1, so the output is its value."""
+    n, heads, width = 1 << 20, 64, 8
+    at = torch.arange(n + 1, dtype=torch.int32, device=DEV)
+    gen = torch.Generator(device=DEV).manual_seed(5)
+    q, k, v, grad = (torch.randn((n, heads, width), generator=gen, device=DEV, dtype=BF16) for _ in range(4))
+    print(f"attend {n} documents, {heads} heads", flush=True)
+    out, lse = ssh.attend(q, k, v, q_offsets=at, k_offsets=at, return_lse=True)
+    assert torch.equal(out, v)
+    want = (q.float() * k.float()).sum(2) * width ** -0.5
+    assert ((lse - want).abs() <= 2.0 ** -18 * (1 + (q.float() * k.float()).abs().sum(2))).all()
+    gq, gk, gv = ssh.attend_grad(grad, q, k, v, out, lse, q_offsets=at, k_offsets=at)
+    assert torch.equal(gv, grad) and not gq.any() and not gk.any()

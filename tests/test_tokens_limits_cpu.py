@@ -88,3 +88,16 @@ def test_attention_rows_stay_in_32_bits():
         assert LIB.tok_attend_workspace_bytes(a) == EINVAL and LIB.tok_attend_grad_workspace_bytes(a) == EINVAL
         assert LIB.tok_attend(a, p, p, p, p, None, p, 1 << 60, None) == EINVAL
         assert LIB.tok_attend_grad(a, *[p] * 10, 1 << 60, None) == EINVAL
+
+
+def test_attention_blocks_stay_in_31_bits():
+    """A tile per document and key head, and one per 32 rows or keys, for as many as are accepted."""
+    strides = dict(q_stride=(8192, 8), k_stride=(8192, 8), v_stride=(8192, 8), g_stride=(8192, 8))
+    for docs, kv_heads, good in ((2**20, 1023, True), (2**20, 1024, False), (16382, 65536, True),
+                                 (16383, 65536, False)):
+        a = _attention(docs=docs, heads=kv_heads, kv_heads=kv_heads, tq=4, tk=4, q_offsets=16, k_offsets=16,
+                       **strides)
+        assert (LIB.tok_attend_workspace_bytes(a) >= 0) == good, (docs, kv_heads)
+        assert not good or 2**26 + (docs + 2) * kv_heads < 2**31
+        if not good:
+            assert LIB.tok_attend(a, *[4096] * 4, None, 4096, 1 << 60, None) == EINVAL
