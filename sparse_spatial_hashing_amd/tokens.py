@@ -249,10 +249,11 @@ def _heads(name: str, t: torch.Tensor, like: Optional[torch.Tensor] = None) -> t
     _floating(name, t, like, _HALF)
     if t.dim() != 3:
         raise ValueError(f"{name} must be [tokens, heads, width]")
-    # 16-byte pieces, tokens less than 64 MiB apart: copy what is laid out otherwise
+    # 16-byte pieces, tokens less than 64 MiB apart: copy what is laid out otherwise (of no
+    # tokens too, whose strides the library checks as well)
     by_token, by_head, by_element = t.stride()
     if (by_element != 1 or by_token & 7 or by_head & 7 or by_token >= 1 << 25 or t.data_ptr() & 15
-            or by_token < 0 or by_head < 0) and t.numel():
+            or by_token < 0 or by_head < 0):
         t = t.clone(memory_format=torch.contiguous_format)
     return t
 

@@ -164,3 +164,23 @@ def test_attend_more_blocks_than_one_launch_holds():
     assert ((lse - want).abs() <= 2.0 ** -18 * (1 + (q.float() * k.float()).abs().sum(2))).all()
     gq, gk, gv = ssh.attend_grad(grad, q, k, v, out, lse, q_offsets=at, k_offsets=at)
     assert torch.equal(gv, grad) and not gq.any() and not gk.any()
+
+
+def _odd(tokens, heads, width, of=13):
+    """A view whose strides are not whole 16-byte pieces."""
+    return torch.ones((tokens, heads, of), dtype=BF16, device=DEV)[..., 3:3 + width]
+
+
+@pytest.mark.parametrize("tq,tk", [(0, 0), (0, 5), (5, 0)])
+def test_attend_nothing_in_odd_strides(tq, tk):
+    """A layout that is copied where there are tokens does where there are none."""
+    leaves = [t.detach().requires_grad_() for t in (_odd(tq, 2, 8), _odd(tk, 1, 8), _odd(tk, 1, 8, 15))]
+    out, lse = ssh.attend(*leaves, return_lse=True)
+    assert out.shape == (tq, 2, 8) and not out.any() and torch.isneginf(lse).all()
+    for grad in (_odd(tq, 2, 8, 11), torch.ones((), dtype=BF16, device=DEV).expand(tq, 2, 8)):
+        made = torch.autograd.grad(out, leaves, grad, retain_graph=True)
+        assert all(g.shape == t.shape and not g.any() for g, t in zip(made, leaves))
+    at = torch.zeros(3, dtype=torch.int32, device=DEV)
+    with torch.no_grad():
+        assert not ssh.attend(*leaves, q_offsets=at, k_offsets=at).any()
+        assert not ssh.attend(leaves[0][3:], leaves[1][3:], leaves[2][3:]).any()
