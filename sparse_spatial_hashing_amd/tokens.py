@@ -219,9 +219,15 @@ def embed_grad(grad: torch.Tensor, ids: torch.Tensor, rows: int, *,
     return out
 
 
+_GRAD_ROWS, _GRAD_TOKENS = 1 << 24, 1 << 27  # of embed_grad
+
+
 class _Embed(torch.autograd.Function):
     @staticmethod
     def forward(ctx, table, ids, scale):
+        if table.dim() == 2 and (table.shape[0] > _GRAD_ROWS or ids.numel() > _GRAD_TOKENS):
+            raise ValueError(f"the gradient of a table holds at most {_GRAD_ROWS} rows and {_GRAD_TOKENS} "
+                             f"ids: got {table.shape[0]} and {ids.numel()}")
         ctx.save_for_backward(ids)
         ctx.rows, ctx.scale = table.shape[0], scale
         return _embed(table, ids, scale)
@@ -237,7 +243,8 @@ def embed(table: torch.Tensor, ids: torch.Tensor, *, scale: float = 1.0) -> torc
     """Rows of a table by token: ``scale * table[ids]``, [*ids.shape, width] in
     the table's type (float32, bf16 or fp16), rounded once. A row of zeros
     where an id is not in [0, rows) (-1 marks a point without a pillar).
-    ids: int32 or int64, any shape. Differentiable in the table."""
+    ids: int32 or int64, any shape. Differentiable in a table of at most 2^24
+    rows, by at most 2^27 ids."""
     if torch.is_grad_enabled() and isinstance(table, torch.Tensor) and table.requires_grad:
         return _Embed.apply(table, ids, float(scale))
     return _embed(table, ids, float(scale))

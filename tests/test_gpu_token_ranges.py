@@ -184,3 +184,17 @@ def test_attend_nothing_in_odd_strides(tq, tk):
     with torch.no_grad():
         assert not ssh.attend(*leaves, q_offsets=at, k_offsets=at).any()
         assert not ssh.attend(leaves[0][3:], leaves[1][3:], leaves[2][3:]).any()
+
+
+@pytest.mark.parametrize("rows,n", [((1 << 24) + 1, 3), (3, (1 << 27) + 1)])
+def test_embed_refuses_a_gradient_it_cannot_give(rows, n):
+    """Before the forward, not in the backward; without a gradient the same lookup runs."""
+    table = torch.ones((rows, 1), device=DEV, dtype=F16)
+    ids = torch.full((n,), rows - 1, dtype=torch.int32, device=DEV)
+    assert ssh.embed(table, ids).all()
+    with pytest.raises(ValueError, match="gradient"):
+        ssh.embed(table.requires_grad_(), ids)
+    with torch.no_grad():
+        assert ssh.embed(table, ids).all()
+    less = table.detach()[:1 << 24].requires_grad_()
+    assert ssh.embed(less, ids[:1000]).requires_grad
