@@ -274,6 +274,11 @@ def _positions(name: str, t: Optional[torch.Tensor], tokens: int, index: int) ->
     return t
 
 
+def _constant(slopes) -> None:
+    if isinstance(slopes, torch.Tensor) and slopes.requires_grad and torch.is_grad_enabled():
+        raise ValueError("slopes are constants: no gradient is computed for them")
+
+
 def _attention(q, k, v, q_offsets, k_offsets, scale, cap, slopes, q_pos, k_pos, causal, prefix,
                grad=None):
     """The checked arguments as the C structure, and the tensors it points to."""
@@ -310,8 +315,6 @@ def _attention(q, k, v, q_offsets, k_offsets, scale, cap, slopes, q_pos, k_pos, 
         _on_gpu("slopes", slopes, index)
         if slopes.dtype != torch.float32 or slopes.shape != (heads,):
             raise ValueError(f"slopes must be a float32 tensor of shape {(heads,)}")
-        if slopes.requires_grad:
-            raise ValueError("slopes are constants: no gradient is computed for them")
         slopes = slopes.contiguous()
         q_pos, k_pos = _positions("q_pos", q_pos, tq, index), _positions("k_pos", k_pos, tk, index)
         axes = q_pos.shape[1]
@@ -357,6 +360,7 @@ def attend_grad(grad_out: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: tor
     out and lse it returned and the same other arguments. Gradients of shared
     key heads are summed over their query heads in float32."""
     _unseen("attend_grad", grad_out, q, k, v, out, lse, slopes)
+    _constant(slopes)
     a, kept = _attention(q, k, v, q_offsets, k_offsets, scale, cap, slopes, q_pos, k_pos, causal,
                          prefix, grad_out)
     q, k, v, g = kept[:4]
@@ -415,9 +419,11 @@ def attend(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, *,
 
     Returns out [tq, heads, width], zeros where a query sees no key, and with
     ``return_lse`` also the log-sum-exp [tq, heads] float32 (-inf there, not
-    differentiable). Differentiable in q, k and v."""
+    differentiable). Differentiable in q, k and v; slopes that require a gradient
+    are refused unless gradients are off."""
     more = dict(q_offsets=q_offsets, k_offsets=k_offsets, scale=scale, cap=cap, slopes=slopes,
                 q_pos=q_pos, k_pos=k_pos, causal=causal, prefix=prefix)
+    _constant(slopes)
     if torch.is_grad_enabled() and any(isinstance(t, torch.Tensor) and t.requires_grad
                                        for t in (q, k, v)):
         out, lse = _Attend.apply(q, k, v, more)

@@ -198,3 +198,23 @@ def test_embed_refuses_a_gradient_it_cannot_give(rows, n):
         assert ssh.embed(table, ids).all()
     less = table.detach()[:1 << 24].requires_grad_()
     assert ssh.embed(less, ids[:1000]).requires_grad
+
+
+def test_attend_learned_slopes_without_gradients():
+    """Slopes of a parameter serve where gradients are off; elsewhere theirs would be lost."""
+    gen = torch.Generator().manual_seed(6)
+    q, k = (torch.randn((30, h, 32), generator=gen).to(DEV, BF16) for h in (4, 2))
+    pos = torch.randint(0, 50, (30, 2), generator=gen, dtype=torch.int32).to(DEV)
+    slopes = torch.tensor([0.5, 0.25, 0.1, 0.0], device=DEV)
+    learned = slopes.clone().requires_grad_()
+    m = dict(q_pos=pos, k_pos=pos)
+    want, lse = ssh.attend(q, k, k, slopes=slopes, return_lse=True, **m)
+    for off in (torch.no_grad(), torch.inference_mode()):
+        with off:
+            assert torch.equal(ssh.attend(q, k, k, slopes=learned, **m), want)
+            ssh.attend_grad(q, q, k, k, want, lse, slopes=learned, **m)
+    for call in (lambda: ssh.attend(q, k, k, slopes=learned, **m),
+                 lambda: ssh.attend(q.clone().requires_grad_(), k, k, slopes=learned, **m),
+                 lambda: ssh.attend_grad(q, q, k, k, want, lse, slopes=learned, **m)):
+        with pytest.raises(ValueError, match="slopes"):
+            call()
