@@ -107,7 +107,7 @@ typedef struct tok_attention {
     const int32_t* k_offsets;
     const int32_t* prefix;      /* device [docs] or NULL */
     float scale;                /* in [1e-30, 1e30] */
-    float cap;                  /* 0: none */
+    float cap;                  /* 0: none; else in [2^-126, 2^127] */
     const float* slopes;        /* device [heads], below 2^100; NULL when axes is 0 */
     const int32_t* q_pos;       /* device [tq, axes] */
     const int32_t* k_pos;       /* device [tk, axes] */

@@ -39,8 +39,9 @@ bool check(const tok_attention* t) {
     if ((!t->q_offsets || !t->k_offsets) && t->docs != 1) return false;
     if (t->prefix && !t->mask) return false;
     // a scale that is used as a divisor too
-    if (!(t->scale >= 1e-30f) || !(t->scale <= 1e30f) || !(t->cap >= 0.0f) || !isfinite(t->cap))
-        return false;
+    if (!(t->scale >= 1e-30f) || !(t->scale <= 1e30f)) return false;
+    // a cap whose product with log2(e) is finite
+    if (t->cap != 0.0f && (!(t->cap >= 0x1p-126f) || !(t->cap <= 0x1p127f))) return false;
     if (t->axes < 0 || t->axes > 3 || t->reserved) return false;
     if (t->axes && (!t->slopes || (t->tq && !t->q_pos) || (t->tk && !t->k_pos))) return false;
     const int64_t* strides[3] = {t->q_stride, t->k_stride, t->v_stride};
@@ -117,7 +118,8 @@ AttArgs make_args(const tok_attention& t, const Cut& c) {
     a.scale = t.scale;
     a.scale2 = (float)(t.scale * log2e);
     a.unscale2 = (float)(1.0 / (t.scale * log2e));
-    a.cap_in = t.cap > 0.0f ? (float)((double)t.scale / t.cap) : 0.0f;
+    // at most the largest float: a score of 0 stays 0, all others come to +-cap
+    a.cap_in = t.cap > 0.0f ? (float)fmin((double)t.scale / t.cap, 3.4e38) : 0.0f;
     a.cap2 = (float)(t.cap * log2e);
     return a;
 }

@@ -308,8 +308,8 @@ def _attention(q, k, v, q_offsets, k_offsets, scale, cap, slopes, q_pos, k_pos, 
     scale = width ** -0.5 if scale is None else float(scale)
     if not 1e-30 <= scale <= 1e30:
         raise ValueError("scale must be positive: from 1e-30 to 1e30")
-    if not 0.0 <= cap < float("inf"):
-        raise ValueError("cap must be finite, 0 for none")
+    if cap != 0.0 and not 2.0 ** -126 <= cap <= 2.0 ** 127:
+        raise ValueError("cap must be from 2^-126 to 2^127, or 0 for none")
     axes = 0
     if slopes is not None:
         _on_gpu("slopes", slopes, index)

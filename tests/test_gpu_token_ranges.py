@@ -218,3 +218,31 @@ def test_attend_learned_slopes_without_gradients():
                  lambda: ssh.attend_grad(q, q, k, k, want, lse, slopes=learned, **m)):
         with pytest.raises(ValueError, match="slopes"):
             call()
+
+
+@pytest.mark.parametrize("cap,scale", [(2.0**-126, 1.0), (1e-30, 1e30), (2.0**127, 0.25), (1e30, 0.25)])
+def test_attend_extreme_caps(cap, scale):
+    """A cap so small that scale / cap passes the floats (scores of exactly 0 among them), and one so
+    large that it bends nothing."""
+    gen = torch.Generator().manual_seed(8)
+    q, k, v, grad = (torch.randn((50, 1, 32), generator=gen).to(BF16) for _ in range(4))
+    q[3], k[7] = 0.0, 0.0
+    want = ref.attend(q, k, v, [0, 50], [0, 50], scale, cap=cap, grad=grad)
+    m = dict(cap=cap, scale=scale)
+    g = [t.to(DEV) for t in (q, k, v, grad)]
+    out, lse = ssh.attend(*g[:3], return_lse=True, **m)
+    ref.check(out, *want["out"], f"out cap {cap}")
+    ref.check(lse, *want["lse"], f"lse cap {cap}")
+    made = ssh.attend_grad(g[3], *g[:3], out, lse, **m)
+    for name, t in zip(("gq", "gk", "gv"), made):
+        if name == "gv" or cap > 1:  # bent flat: the formula's 64 bits leave 1e-30 of a gradient of 1e30
+            ref.check(t, *want[name], f"{name} cap {cap}")
+        else:
+            assert torch.isfinite(t).all()
+
+
+@pytest.mark.parametrize("cap", [1e-50, 2.0**-127, 2.5e38, 1e39, math.inf, math.nan, -1e-50])
+def test_attend_refuses_caps(cap):
+    h = torch.zeros((4, 2, 16), device=DEV, dtype=BF16)
+    with pytest.raises(ValueError):
+        ssh.attend(h, h, h, cap=cap)

@@ -101,3 +101,11 @@ def test_attention_blocks_stay_in_31_bits():
         assert not good or 2**26 + (docs + 2) * kv_heads < 2**31
         if not good:
             assert LIB.tok_attend(a, *[4096] * 4, None, 4096, 1 << 60, None) == EINVAL
+
+
+@pytest.mark.parametrize("cap,good", [(0.0, True), (2.0**-126, True), (30.0, True), (2.0**127, True),
+                                      (2.0**-127, False), (2.5e38, False), (-2.0**-126, False)])
+def test_attention_cap_limits(cap, good):
+    a = _attention(cap=cap)
+    assert (LIB.tok_attend_workspace_bytes(a) >= 0) == good
+    assert (LIB.tok_attend_grad_workspace_bytes(a) >= 0) == good
