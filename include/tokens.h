@@ -87,7 +87,8 @@ int tok_embed_grad(const void* grad, int64_t grad_stride, int32_t dtype, const v
  * A query that sees no key gets zeros and lse = -inf, and passes no gradient.
  * Scores, softmax statistics and sums are held in float32; the softmax
  * weights and the score gradients are rounded to the tensors' type before
- * they enter the second products. Keys of other documents, and rows of no
+ * they enter the second products, with powers of two taken out first where
+ * fp16 would not hold them. Keys of other documents, and rows of no
  * document, never enter a result whatever they hold; inside a document a
  * value that is not finite may reach every query of it.
  * Positions are int32 in [0, 65535] (values outside are clamped), 1 to 3 axes,
@@ -108,7 +109,8 @@ typedef struct tok_attention {
     const int32_t* prefix;      /* device [docs] or NULL */
     float scale;                /* in [1e-30, 1e30] */
     float cap;                  /* 0: none; else in [2^-126, 2^127] */
-    const float* slopes;        /* device [heads], below 2^100; NULL when axes is 0 */
+    const float* slopes;        /* device [heads]; NULL when axes is 0. slopes and, without a
+                                   cap, slopes / scale: magnitudes below 2^100 */
     const int32_t* q_pos;       /* device [tq, axes] */
     const int32_t* k_pos;       /* device [tk, axes] */
     int32_t axes;               /* 0 (no bias) to 3 */

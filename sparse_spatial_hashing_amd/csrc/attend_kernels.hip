@@ -17,6 +17,14 @@
 // keys in the order 4 h + (0..3), 8 + 4 h + (0..3); V^T is read with the same
 // order (two transposing LDS reads of four keys each). Nothing is shuffled.
 //
+// Roundings. What enters the second products (weights forward, weights and
+// score gradients backward) is rounded to the tensors' type, as the matrix
+// units of 16 bits take it: in 32 bits those products run at a sixteenth of the
+// rate, and a second product with what the rounding left would add half of the
+// forward's to it. It costs, against 64 bits, 2.0e-3 to 2.4e-3 of the output's
+// norm in bf16 where the output's own rounding costs 1.7e-3 (fp16 2.9e-4 and
+// 2.1e-4). Scores, maxima, sums and accumulators are in 32 bits.
+//
 // LDS tiles are rows of 2 * WIDTH bytes with the 16-byte chunks of a row
 // permuted by XOR with swz(row), so that both a read of one chunk of 16
 // consecutive rows and a transposing read of four consecutive rows times 64
@@ -52,8 +60,8 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kLowest = -3.402823466e+38f;
 // The backward's weights are computed 2^kLift too large and the sums put right
-// at the end, so that weights of 2^-126 (bf16, exp2's limit) or 2^-28 (fp16,
-// whose largest number is 2^16) and less keep all their bits.
+// at the end, so that they keep all their bits down to 2^-150 (bf16; exp2 ends
+// at 2^-126) and 2^-28 (fp16, which ends at 2^16 and has them from 2^-14 on).
 constexpr float kLift = ATT_F16 ? 14.0f : 24.0f;
 constexpr float kUnlift = ATT_F16 ? 0x1p-14f : 0x1p-24f;
 constexpr float kRescale = 8.0f;  // running maximum may lag by this much (base 2)
@@ -261,8 +269,9 @@ __device__ __forceinline__ float first_summand(const AttArgs& a, float sub) {
 }
 
 // tanh(u), u = score / cap, for a block's scores at once: where all are small,
-// u times a polynomial in u^2 (the minimax one of relative error 1.3e-8 on
-// |u| <= 0.5, found by the exchange method) in 6 instructions a score; else
+// u times a polynomial in u^2 (on |u| <= 0.5, found by the exchange method; with
+// the coefficients rounded its relative error is 2.9e-8, half a step of a float,
+// and 8.4e-8 as computed here) in 6 instructions a score; else
 // 1 - 2 / (exp(2 u) + 1), right at both ends (exp = 0 and inf), whose two
 // transcendentals alone take the time of 8.
 constexpr float kSmallTanh = 0.5f;
@@ -499,9 +508,11 @@ __device__ __forceinline__ unsigned xcd_block(unsigned bid, unsigned n) {
 // Bound by vector instructions: with a bias a score takes 6 and an exp2 (the
 // bias 2, scale, half a max, sum, half a conversion), 1312 cycles per 32 x 64
 // scores against 512 of the matrix units at a width of 64. 12,000 tokens, 8
-// heads of 64, two axes: 400 us a call, 737 TFLOP/s; six prefixes of 2,300, 16
-// on 4 heads of 128, cap: 239, 756. One token of 16 scenes against 12,000 keys
-// at most is bound by memory: 65 us, 4.8 TB/s, and 4.6 for the join.
+// heads of 64, two axes: 403 us a call, 732 TFLOP/s; six prefixes of 2,300, 16
+// on 4 heads of 128, cap: 242, 745 (of a card whose clock has settled; the first
+// tens of calls after a pause take up to 510 and 310). One token of 16 scenes
+// against 12,000 keys at most is bound by memory: 65 us, 4.8 TB/s, and 4.6 for
+// the join.
 // Three wavefronts share a SIMD where they fit without spilling.
 
 template <int AX, bool CAP, int NW, int BN>
@@ -747,7 +758,8 @@ __global__ __launch_bounds__(256) void k_att_join(AttArgs a) {
 // 32 bits.
 // Bound by the waits between one product's result and the next's operand, with
 // two wavefronts a SIMD to fill them: four frames of up to 4,096, 8 heads on 2
-// of 128, in 590 us, the matrix units busy for a third of it.
+// of 128, in 530 us (the first ten calls 555), the matrix units busy for a third
+// of it.
 
 template <int AX, bool CAP, int NW, int BN>
 __global__ __launch_bounds__(64 * NW, NW == 1 && W == 32 ? 3 : NW == 4 || W < 128 ? 2 : 1) void k_att_grad_q(AttArgs a) {
@@ -954,7 +966,8 @@ __global__ __launch_bounds__(64 * NW, NW == 1 && W == 32 ? 3 : NW == 4 || W < 12
 // the group after another: S = Q K^T and dP = grad_out V^T with a lane's column
 // one key, so P and dS are operand B of grad_v^T = grad_out^T P and
 // grad_k^T = Q^T dS. The weights' product goes before dP, so that fewer values
-// are alive at once. Bound as grad_q; the same frames in 580 us.
+// are alive at once. Bound as grad_q; the same frames in 511 us
+// (the first ten calls 541).
 
 template <int AX, bool CAP, int NW>
 __global__ __launch_bounds__(64 * NW, NW == 1 && W == 32 ? 3 : NW == 4 || W < 128 ? 2 : 1) void k_att_grad_kv(AttArgs a) {

@@ -47,8 +47,11 @@ struct ScanArgs {
     int by_doc;               // a block walks a document, not a chunk
 };
 
-// a = sigmoid(f) and 1 - a, each to a few units in its last place: the smaller
-// one is a quotient, the larger its difference from one.
+// a = sigmoid(f) and 1 - a: the smaller one is a quotient, the larger its
+// difference from one. The smaller's relative error is that of the exponent's
+// rounded argument and a few more roundings, at most (|f| + 8) 2^-24 while it is
+// a normal number (the argument's part: 15 of 2^-24 up to |f| = 20, 64 up to 87);
+// the larger's is a few roundings.
 __device__ __forceinline__ void gates(float f, float& a, float& keep) {
     const float e = __builtin_amdgcn_exp2f(-fabsf(f) * 1.4426950408889634f);
     const float lo = e * __builtin_amdgcn_rcpf(1.0f + e);

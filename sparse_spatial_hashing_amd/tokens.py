@@ -408,14 +408,21 @@ def attend(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, *,
     """Attention inside packed documents.
 
     q [tq, heads, width], k and v [tk, kv_heads, width] (bf16 or fp16, heads a
-    multiple of kv_heads, width a multiple of 8 up to 128, any strides), packed
-    by ``q_offsets`` and ``k_offsets`` (int32 [docs + 1]; None: one document).
+    multiple of kv_heads, width a multiple of 8 up to 128), packed by
+    ``q_offsets`` and ``k_offsets`` (int32 [docs + 1]; None: one document).
+    Tensors are read where they are if an element's stride is 1, tokens and heads
+    start at multiples of 16 bytes and tokens are less than 64 MiB apart; in any
+    other layout each call copies them first.
     Scores are ``scale * q.k`` (scale None: width ** -0.5), then
     ``cap * tanh(score / cap)`` when cap > 0, then less ``slopes[head]`` times
     the L1 distance of the positions (int32 [tokens, 1 to 3 axes] in
     [0, 65535]: the coords of voxelize). ``causal`` hides the keys after a
     query (the last query sees every key); ``prefix`` (int32 [docs]) makes the
     first keys of each document visible to all its queries, and the rest causal.
+
+    Caches with room to grow: give every cache two documents, its keys and, with
+    no queries, the room left: k_offsets [0, len0, room, room + len1, 2 room, ..],
+    q_offsets [0, 1, 1, 2, 2, ..]. What the room holds is not read.
 
     Returns out [tq, heads, width], zeros where a query sees no key, and with
     ``return_lse`` also the log-sum-exp [tq, heads] float32 (-inf there, not
