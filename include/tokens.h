@@ -13,7 +13,13 @@
  *   - attention between the tokens of a frame, with a bias that falls with
  *     their distance on the grid, forward and backward;
  *   - a gated linear recurrence along an order of the tokens, forward and
- *     backward.
+ *     backward;
+ *   - rotary positions: queries and keys turned by their places, and turned
+ *     back;
+ *   - attention with decay, whose cost grows with the tokens alone, forward,
+ *     backward and token by token;
+ *   - the loss of predicting a row of the table (the next pillar's cell), and
+ *     its gradients.
  * Frames are packed one after another: token tensors are [T, ...] and an
  * int32 array of `docs + 1` offsets on the device says where each frame
  * (document) starts and ends. Tokens before the first offset or from the last
@@ -165,6 +171,63 @@ int tok_scan_grad(const void* grad_y, const void* gate, const void* x, const flo
                   int32_t reverse, const float* state, const float* grad_last, void* grad_gate,
                   void* grad_x, float* grad_state, void* workspace, int64_t workspace_bytes,
                   hipStream_t stream);
+
+/* ---- rotary positions -------------------------------------------------------
+ *
+ * x [tokens, heads, width] (float32, bf16 or fp16), strides in elements, an
+ * element's 1. The first 2 * axes * pairs elements of a head are turned, axis
+ * by axis of the positions [tokens, axes] (int32, any value, 1 to 3 axes, strides
+ * in elements): pair p of axis c, elements (u, v), by the angle
+ * pos[t, c] * freqs[c, p]:
+ *   (u cos - v sin, u sin + v cos);  inverse 1: by the opposite angle.
+ * Axis c has the elements from 2 * c * pairs on; its pair p is the elements
+ * (p, pairs + p) of them, or interleaved (2 p, 2 p + 1). The rest of the head is
+ * copied. freqs [axes, pairs] is float64 (radians a position), contiguous: the
+ * angle is reduced to a turn in 64 bits, so that far positions lose nothing. Sines,
+ * cosines and products are in float32, rounded once to x's type. out is
+ * contiguous. The gradient of x is the gradient of out turned back.
+ * Limits: 0 <= tokens <= 2^31 - 1, 1 <= heads, width <= 65536; a finite
+ * frequency's product with a position below 2^52 turns.
+ */
+int tok_rotate(const void* x, int64_t tokens, int64_t heads, int64_t width, int64_t token_stride,
+               int64_t head_stride, int32_t dtype, const int32_t* pos, int64_t pos_stride,
+               int64_t axis_stride, int32_t axes, const double* freqs, int64_t pairs,
+               int32_t interleaved, int32_t inverse, void* out, hipStream_t stream);
+
+/* ---- loss over a table's rows -----------------------------------------------
+ *
+ * x [t, width] and table [rows, width], bf16 or fp16, rows x_stride and
+ * table_stride elements apart; ids [t] int32 (id_bytes 4) or int64 (8):
+ *   lse[i]  = log sum over r of exp(scale * x[i].table[r])
+ *   loss[i] = lse[i] - scale * x[i].table[ids[i]]
+ * both float32; 0 where ids[i] is not in [0, rows), and then nothing of x[i] is
+ * used. lse may be NULL. Logits are not kept: they are summed as they are made,
+ * and made again for the gradients, in pieces of the rows. Logits, maxima and sums
+ * are float32.
+ *
+ * The gradients, with w[i, r] = (exp(scale * x[i].table[r] - lse[i]) - [r is
+ * ids[i]]) * grad[i] for the gradient grad [t] float32 of the loss:
+ *   grad_x[i] = scale * sum over r of w[i, r] table[r]        [t, width]
+ *   grad_table[r] = scale * sum over i of w[i, r] x[i]        [rows, width]
+ * contiguous, in x's type, every row written. w is rounded to that type (fp16:
+ * after powers of two that bring the largest |grad| to 2^14), sums are float32.
+ * Limits: 0 <= t <= 2^27, 1 <= rows <= 2^31 - 2048; width a multiple of 8, at most
+ * 65536; strides multiples of 8, table_stride below 2^22; all bases 16-byte
+ * aligned; scale in [1e-30, 1e30]. The workspace needs no initial contents,
+ * 256-byte aligned.
+ */
+int64_t tok_row_loss_workspace_bytes(int64_t t, int64_t rows, int64_t width);
+int tok_row_loss(const void* x, int64_t x_stride, const void* table, int64_t table_stride,
+                 int32_t dtype, int64_t t, int64_t rows, int64_t width, const void* ids,
+                 int32_t id_bytes, float scale, float* loss, float* lse, void* workspace,
+                 int64_t workspace_bytes, hipStream_t stream);
+
+int64_t tok_row_loss_grad_workspace_bytes(int64_t t, int64_t rows, int64_t width);
+int tok_row_loss_grad(const float* grad, const void* x, int64_t x_stride, const void* table,
+                      int64_t table_stride, int32_t dtype, int64_t t, int64_t rows, int64_t width,
+                      const void* ids, int32_t id_bytes, const float* lse, float scale,
+                      void* grad_x, void* grad_table, void* workspace, int64_t workspace_bytes,
+                      hipStream_t stream);
 
 #ifdef __cplusplus
 }

@@ -661,3 +661,4 @@ def spherical(points: torch.Tensor, sph_min: Sequence[float], sph_cell: Sequence
 
 from .tokens import (attend, attend_grad, embed, embed_grad, gated_scan,  # noqa: E402,F401
                      gated_scan_grad)
+from .prediction import rotary_frequencies, rotate, row_loss, row_loss_grad  # noqa: E402,F401

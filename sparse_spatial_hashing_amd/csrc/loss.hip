@@ -1,0 +1,862 @@
+// The loss over a table's rows (tokens.h): softmax cross entropy of tokens against
+// every row, and its gradients, without the logits in memory.
+//
+// Products. Logits z = scale X W^T are taken as W X^T, so that a lane holds one
+// token's logits of many rows: the running maximum and sum stay in the lane. The
+// backward takes the logits again, a piece of the rows at a time, and writes
+// dZ = (exp(z - lse) - [row is the token's]) grad, rounded, to the workspace, from
+// where two products follow: grad_x += dZ W and grad_table = dZ^T X. A piece is as
+// many rows as keep dZ in the 256 MB of cache between HBM and the XCDs.
+//
+// Tiles of 32 of the inner index go straight from memory into three buffers of LDS
+// in turn. X and dZ are kept in pieces of 8 elements, [element / 8][token]: a tile
+// is then a few runs of memory, its rows and its columns are both read without
+// conflicts, tokens without a row and tokens past the last are zeros, and no
+// product asks for either.
+//
+// Roundings. dZ enters the products in the tensors' type; logits, maxima, sums and
+// gradients are summed in 32 bits. In fp16 dZ is taken 2^14 times the ratio of its
+// token's grad to the largest one's power of two: it keeps all its bits down to
+// 2^-28 of that.
+
+#include <hip/hip_runtime.h>
+
+#include "mma_ops.h"
+
+int ssh_hip_fail(hipError_t e);  // records the error for vox_last_hip_error()
+
+namespace {
+
+constexpr long long kMaxTokens = 1ll << 27;
+constexpr long long kMaxRows = (1ll << 31) - 2048;
+constexpr long long kMaxWidth = 65536;
+constexpr long long kMaxStride = 1ll << 22;  // 256 rows apart in 32 bits of bytes
+constexpr int kTokenPad = 128;               // tokens are laid out in whole tiles
+constexpr int kRowTile = 256;                // rows of a tile of logits
+constexpr int kStep = 32;                    // inner elements of a stage
+constexpr long long kPieceBytes = 128ll << 20;
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kLowest = -3.402823466e+38f;
+constexpr int kLift = 14;  // fp16: dZ is 2^kLift too large
+
+struct LossArgs {
+    const void* x;
+    const void* table;
+    const void* ids;
+    const float* grad;
+    const float* lse;
+    float* loss;
+    float* lse_out;
+    void* gx;
+    void* gt;
+    // workspace
+    uint4* xg;         // [width8, tokens_pad]: X in pieces
+    uint4* dz;         // [piece / 8, tokens_pad]
+    int* came;         // [tokens_pad]: the token's row, or -1
+    float* shift;      // [tokens_pad]: lse in base 2 (backward)
+    float* by;         // [tokens_pad]: grad times the lift (backward)
+    float* hit;        // [tokens_pad]: the logit of the token's row, base 2 (forward)
+    float2* part;      // [splits, tokens_pad]: maximum and sum (forward)
+    unsigned* top;     // the largest |grad|, its bits (fp16)
+    float* part_x;     // [x_splits, tokens, width]
+    float* part_t;     // [t_splits, piece rows, width] (t_splits > 1)
+    long long x_stride, t_stride;
+    int t, rows, width, width8, t_pad, id_bytes;
+    int splits, tiles;        // of the rows' tiles
+    int token_tiles;
+    int row0, piece;          // rows of a piece: a multiple of kRowTile, its last ones past the table's
+    int x_splits, t_splits, first;
+    int tokens_in;            // tokens that dZ is written for
+    float scale, scale2;
+};
+
+// A tile's stage by stage products. Blocks of 32: MA x NB per wavefront, WM x WN
+// wavefronts.
+template <typename T, int MA_, int NB_, int WM_, int WN_>
+struct Shape {
+    static constexpr int MA = MA_, NB = NB_, WM = WM_, WN = WN_;
+    static constexpr int BM = 32 * MA * WM, BN = 32 * NB * WN, NT = 64 * WM * WN;
+    static constexpr int kA = BM * kStep * 2, kB = BN * kStep * 2;  // bytes of a stage
+    static constexpr int kStage = kA + kB;
+    static constexpr int kALoads = BM * 4 / NT, kBLoads = (BN * 4 + NT - 1) / NT;
+    static constexpr int kLoads = kALoads + BN * 4 / NT;  // every wavefront's, at least
+};
+
+// The stages of a block: loads run two ahead of the products.
+template <int LOADS, typename Issue, typename Compute>
+__device__ __forceinline__ void stages(int total, Issue issue, Compute compute) {
+    if (total > 0) issue(0, 0);
+    if (total > 1) issue(1, 1);
+    int buf = 0;
+    for (int i = 0; i < total; ++i) {
+        if (i + 1 < total)
+            load_wait<LOADS>();
+        else
+            load_wait<0>();
+        __syncthreads();  // this stage is there, and all are done with the one before
+        const int ahead = buf == 0 ? 2 : buf - 1;
+        if (i + 2 < total) issue(i + 2, ahead);
+        compute(i, buf);
+        buf = buf == 2 ? 0 : buf + 1;
+    }
+}
+
+// ---- operands ----------------------------------------------------------------
+
+// Rows of a matrix in memory, the inner index along a row. In LDS 64 bytes a row,
+// its four pieces permuted by XOR with (row >> 2) & 3: 16 rows' pieces of one place
+// touch every bank once.
+template <typename T, int ROWS, int NT>
+struct RowsOfMatrix {
+    static __device__ __forceinline__ void load(unsigned to, const T* base, long long stride, int row0, int rows,
+                                                int k0, int width) {
+        constexpr int kPer = ROWS * 4 / NT;
+        const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+        const int r = threadIdx.x >> 2, at = threadIdx.x & 3;
+        if (row0 + ROWS <= rows && k0 + kStep <= width) {
+            const T* from = base + (long long)row0 * stride + k0;
+#pragma unroll
+            for (int p = 0; p < kPer; ++p) {
+                const int row = p * (NT / 4) + r;
+                load_to_lds(to + 1024u * wave + 16u * NT * p, from,
+                            (unsigned)row * (unsigned)(2 * stride) + 16u * (at ^ ((row >> 2) & 3)));
+            }
+            return;
+        }
+#pragma unroll
+        for (int p = 0; p < kPer; ++p) {
+            const int row = p * (NT / 4) + r, c = at ^ ((row >> 2) & 3);
+            const bool there = row0 + row < rows && k0 + 8 * c < width;
+            const void* from = there ? (const void*)(base + (row0 + row) * stride + k0 + 8 * c) : &kNothing;
+            load_to_lds(to + 1024u * wave + 16u * NT * p, from);
+        }
+    }
+    static __device__ __forceinline__ unsigned place(int row, int half) {
+        return row * 64 + ((half ^ ((row >> 2) & 3)) << 4);
+    }
+    // at: tile + place of row lane % 32; 32 rows on per block, step s of the stage
+    static __device__ __forceinline__ auto read(unsigned at, int block, int s) {
+        return lds_read<typename Mma<T>::vec8>((at ^ (s << 5)) + block * 2048);
+    }
+};
+
+// Rows of a matrix kept in pieces, [inner / 8][row]. In LDS [4][ROWS] pieces.
+template <typename T, int ROWS, int NT>
+struct RowsOfPieces {
+    static __device__ __forceinline__ void load(unsigned to, const uint4* base, long long pitch, int row0, int k0) {
+        constexpr int kPer = (ROWS * 4 + NT - 1) / NT;
+        const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+        const uint4* from = base + (long long)(k0 >> 3) * pitch + row0;
+#pragma unroll
+        for (int p = 0; p < kPer; ++p) {
+            const int i = p * NT + threadIdx.x;
+            if (p * NT + wave * 64 < ROWS * 4)
+                load_to_lds(to + 1024u * wave + 16u * NT * p,
+                            from + (long long)(i / ROWS) * pitch + i % ROWS);
+        }
+    }
+    static __device__ __forceinline__ unsigned place(int row, int half) { return (half * ROWS + row) * 16; }
+    static __device__ __forceinline__ auto read(unsigned at, int block, int s) {
+        return lds_read<typename Mma<T>::vec8>(at + s * (ROWS * 32) + block * 512);
+    }
+};
+
+// Columns of a matrix in memory whose rows are the inner index. In LDS COLS / 128
+// tiles of 32 rows of 256 bytes, the 16 pieces of a row permuted by XOR with a
+// number of the row that puts four rows of 64 bytes on all banks.
+template <typename T, int COLS, int NT>
+struct ColumnsOfMatrix {
+    static __device__ __forceinline__ int swz(int row) { return ((row & 3) << 2) | ((row >> 2) & 3); }
+    static __device__ __forceinline__ void load(unsigned to, const T* base, long long stride, int row0, int rows,
+                                                int col0, int width) {
+        constexpr int kPer = COLS * 4 / NT;
+        const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+#pragma unroll
+        for (int p = 0; p < kPer; ++p) {
+            const int i = p * NT + threadIdx.x;
+            const int row = (i >> 4) & 31, c = ((i & 15) ^ swz(row)) + 16 * (i >> 9);
+            const bool there = row0 + row < rows && col0 + 8 * c < width;
+            const void* from = there ? (const void*)(base + (row0 + row) * stride + col0 + 8 * c) : &kNothing;
+            load_to_lds(to + 1024u * wave + 16u * NT * p, from);
+        }
+    }
+    // Where the first four of a lane's eight inner rows are (first step, block 0 of a
+    // tile of 128), and the others.
+    static __device__ __forceinline__ uint2 place(int lane) {
+        const int row = 8 * (lane >> 5) + ((lane & 15) >> 2);
+        const int c = 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1), in = (lane & 1) << 3;
+        return make_uint2(row * 256 + ((c ^ swz(row)) << 4) + in, (row + 4) * 256 + ((c ^ swz(row + 4)) << 4) + in);
+    }
+    static __device__ __forceinline__ auto read(uint2 at, int block, int s) {
+        const unsigned on = s * 4096 + (block >> 2) * 8192, flip = (block & 3) << 6;
+        return lds_read_columns<typename Mma<T>::vec8>((at.x ^ flip) + on, (at.y ^ flip) + on);
+    }
+};
+
+// The same of a matrix kept in pieces, [column / 8][inner]. In LDS [COLS / 8][32]
+// pieces, the 32 of a column group permuted by XOR with 4 (group % 4).
+template <typename T, int COLS, int NT>
+struct ColumnsOfPieces {
+    static __device__ __forceinline__ void load(unsigned to, const uint4* base, long long pitch, int row0, int col0,
+                                                int cols) {
+        constexpr int kPer = COLS * 4 / NT;
+        const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+#pragma unroll
+        for (int p = 0; p < kPer; ++p) {
+            const int i = p * NT + threadIdx.x, group = i >> 5, row = (i & 31) ^ ((group & 3) << 2);
+            const uint4* from = base + (long long)((col0 >> 3) + group) * pitch + row0 + row;
+            load_to_lds(to + 1024u * wave + 16u * NT * p, col0 + 8 * group < cols ? from : &kNothing);
+        }
+    }
+    static __device__ __forceinline__ uint2 place(int lane) {
+        const int row = 8 * (lane >> 5) + ((lane & 15) >> 2);
+        const int c = 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1), in = (lane & 1) << 3;
+        return make_uint2(c * 512 + ((row ^ (c << 2)) << 4) + in, c * 512 + (((row + 4) ^ (c << 2)) << 4) + in);
+    }
+    static __device__ __forceinline__ auto read(uint2 at, int block, int s) {
+        return lds_read_columns<typename Mma<T>::vec8>((at.x ^ (s << 8)) + block * 2048,
+                                                       (at.y ^ (s << 8)) + block * 2048);
+    }
+};
+
+// ---- tokens in pieces --------------------------------------------------------
+
+__device__ __forceinline__ int id_of(const LossArgs& a, int t) {
+    const long long id = a.id_bytes == 4 ? ((const int*)a.ids)[t] : ((const long long*)a.ids)[t];
+    return id >= 0 && id < a.rows ? (int)id : -1;
+}
+
+// The largest |grad| of tokens that have a row, for fp16. Its bits compare as the
+// numbers do; a NaN or infinity is left out.
+__global__ __launch_bounds__(1024) void k_loss_top(LossArgs a) {
+    __shared__ float tops[16];
+    float top = 0.0f;
+    for (int t = threadIdx.x; t < a.t; t += 1024) {
+        const float g = id_of(a, t) >= 0 ? fabsf(a.grad[t]) : 0.0f;
+        top = g <= 3.402823466e+38f ? fmaxf(top, g) : top;
+    }
+#pragma unroll
+    for (int off = 32; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor(top, off));
+    if ((threadIdx.x & 63) == 0) tops[threadIdx.x >> 6] = top;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        for (int w = 1; w < 16; ++w) top = fmaxf(top, tops[w]);
+        *a.top = __float_as_uint(top);
+    }
+}
+
+// The exponent dZ is taken up by.
+template <typename T>
+__device__ __forceinline__ int lift_of(const LossArgs& a) {
+    if (sizeof(T) == 2 && __is_same(T, bf16_t)) return 0;
+    const float top = __uint_as_float(*a.top);
+    return top > 0.0f ? kLift - __builtin_amdgcn_frexp_expf(top) : 0;
+}
+
+// X as pieces, zeros where a token has no row, is past the last, or past the width.
+template <typename T, bool GRAD>
+__global__ __launch_bounds__(256) void k_loss_pack(LossArgs a) {
+    const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
+    const int c = (int)(i & 7) + 8 * blockIdx.y, t = (int)(i >> 3);
+    if (t >= a.t_pad) return;
+    const int id = t < a.t ? id_of(a, t) : -1;
+    if (c < a.width8) {
+        uint4 v = make_uint4(0, 0, 0, 0);
+        if (id >= 0 && 8 * c < a.width) v = *(const uint4*)((const T*)a.x + t * a.x_stride + 8 * c);
+        a.xg[(long long)c * a.t_pad + t] = v;
+    }
+    if (c == 0) {
+        a.came[t] = id;
+        if (GRAD) {
+            a.shift[t] = id >= 0 ? a.lse[t] * kLog2e : 0.0f;
+            a.by[t] = id >= 0 ? ldexpf(a.grad[t], lift_of<T>(a)) : 0.0f;
+        }
+    }
+}
+
+// ---- logits ------------------------------------------------------------------
+
+// Tiles [t0, t1) of the rows against a tile of tokens, from `first_row` on;
+// done(tile, acc) gets each tile's products.
+template <typename T, typename S, typename Done>
+__device__ __forceinline__ void logits(const LossArgs& a, char* lds, int first_row, int end_row, int t0, int t1,
+                                       int token0, Done done) {
+    typedef RowsOfMatrix<T, S::BM, S::NT> A;
+    typedef RowsOfPieces<T, S::BN, S::NT> B;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, half = lane >> 5;
+    const int steps = (a.width + kStep - 1) / kStep;
+    const unsigned base = lds_address(lds);
+    const unsigned a_at = base + A::place((wave / S::WN) * 32 * S::MA + (lane & 31), half);
+    const unsigned b_at = base + S::kA + B::place((wave % S::WN) * 32 * S::NB + (lane & 31), half);
+    int tile_in = t0, k_in = 0, tile = t0, k = 0;
+    acc16 acc[S::MA][S::NB];
+    stages<S::kLoads>(
+        (t1 - t0) * steps,
+        [&](int, int buf) {
+            const unsigned to = base + buf * S::kStage;
+            A::load(to, (const T*)a.table, a.t_stride, first_row + tile_in * S::BM, end_row, k_in * kStep, a.width);
+            B::load(to + S::kA, a.xg, a.t_pad, token0, k_in * kStep);
+            if (++k_in == steps) k_in = 0, ++tile_in;
+        },
+        [&](int, int buf) {
+            if (k == 0)
+#pragma unroll
+                for (int i = 0; i < S::MA; ++i)
+#pragma unroll
+                    for (int j = 0; j < S::NB; ++j) acc[i][j] = zero16();
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+                typename Mma<T>::vec8 x[S::MA], y[S::NB];
+#pragma unroll
+                for (int j = 0; j < S::NB; ++j) y[j] = B::read(b_at + buf * S::kStage, j, s);
+#pragma unroll
+                for (int i = 0; i < S::MA; ++i) x[i] = A::read(a_at + buf * S::kStage, i, s);
+#pragma unroll
+                for (int i = 0; i < S::MA; ++i)
+#pragma unroll
+                    for (int j = 0; j < S::NB; ++j) acc[i][j] = Mma<T>::mul(x[i], y[j], acc[i][j]);
+            }
+            if (++k == steps) {
+                done(tile, acc);
+                k = 0, ++tile;
+            }
+        });
+}
+
+// Maxima and sums over a share of the rows, and the logit of each token's own row.
+template <typename T, typename S>
+__global__ __launch_bounds__(S::NT, 2) void k_loss_sum(LossArgs a) {
+    __shared__ __align__(1024) char lds[3 * S::kStage];
+    const unsigned id = xcd_block(blockIdx.x, gridDim.x);
+    const int split = id / a.token_tiles, token0 = (id % a.token_tiles) * S::BN;
+    const int t0 = (int)((long long)a.tiles * split / a.splits), t1 = (int)((long long)a.tiles * (split + 1) / a.splits);
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, half = lane >> 5;
+    const int row_in = (wave / S::WN) * 32 * S::MA, token_in = (wave % S::WN) * 32 * S::NB + (lane & 31);
+
+    float m[S::NB], l[S::NB];
+    int came[S::NB];
+#pragma unroll
+    for (int j = 0; j < S::NB; ++j) m[j] = kLowest, l[j] = 0.0f, came[j] = a.came[token0 + token_in + 32 * j];
+
+    logits<T, S>(a, lds, 0, a.rows, t0, t1, token0, [&](int tile, acc16(&acc)[S::MA][S::NB]) {
+        const int row0 = tile * S::BM + row_in;
+        if (row0 + 32 * S::MA > a.rows) {
+#pragma unroll
+            for (int i = 0; i < S::MA; ++i)
+#pragma unroll
+                for (int j = 0; j < S::NB; ++j)
+#pragma unroll
+                    for (int r = 0; r < 16; ++r)
+                        if (row0 + 32 * i + acc_row(r, half) >= a.rows) acc[i][j][r] = -__builtin_inff();
+        }
+#pragma unroll
+        for (int j = 0; j < S::NB; ++j) {
+            const int mine = came[j] - row0;
+            if (__any(mine >= 0 && mine < 32 * S::MA)) {
+#pragma unroll
+                for (int i = 0; i < S::MA; ++i)
+#pragma unroll
+                    for (int r = 0; r < 16; ++r)
+                        if (mine == 32 * i + acc_row(r, half)) a.hit[token0 + token_in + 32 * j] = acc[i][j][r] * a.scale2;
+            }
+            float top = acc[0][j][0];
+#pragma unroll
+            for (int i = 0; i < S::MA; ++i)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) top = fmaxf(top, acc[i][j][r]);
+            top *= a.scale2;
+            if (__any(top > m[j] + 8.0f)) {
+                const float now = fmaxf(m[j], top);
+                l[j] *= __builtin_amdgcn_exp2f(m[j] - now);
+                m[j] = now;
+            }
+#pragma unroll
+            for (int i = 0; i < S::MA; ++i)
+#pragma unroll
+                for (int r = 0; r < 16; ++r)
+                    l[j] += __builtin_amdgcn_exp2f(__builtin_fmaf(acc[i][j][r], a.scale2, -m[j]));
+        }
+    });
+
+    // the halves of a wavefront, then the wavefronts that share tokens
+    __syncthreads();
+    float2* all = (float2*)lds;  // [2 WM][BN]
+#pragma unroll
+    for (int j = 0; j < S::NB; ++j)
+        all[(2 * (wave / S::WN) + half) * S::BN + token_in + 32 * j] = make_float2(m[j], l[j]);
+    __syncthreads();
+    for (int n = threadIdx.x; n < S::BN; n += S::NT) {
+        float top = kLowest, sum = 0.0f;
+#pragma unroll
+        for (int w = 0; w < 2 * S::WM; ++w) top = fmaxf(top, all[w * S::BN + n].x);
+#pragma unroll
+        for (int w = 0; w < 2 * S::WM; ++w)
+            sum += all[w * S::BN + n].y * __builtin_amdgcn_exp2f(all[w * S::BN + n].x - top);
+        a.part[(long long)split * a.t_pad + token0 + n] = make_float2(top, sum);
+    }
+}
+
+// A wavefront per token joins the shares, in order of their lanes.
+__global__ __launch_bounds__(256) void k_loss_join(LossArgs a) {
+    const int t = blockIdx.x * 4 + (threadIdx.x >> 6), lane = threadIdx.x & 63;
+    if (t >= a.t) return;
+    float m = kLowest, l = 0.0f;
+    for (int s = lane; s < a.splits; s += 64) {
+        const float2 p = a.part[(long long)s * a.t_pad + t];
+        const float now = fmaxf(m, p.x);
+        l = l * __builtin_amdgcn_exp2f(m - now) + p.y * __builtin_amdgcn_exp2f(p.x - now);
+        m = now;
+    }
+#pragma unroll
+    for (int off = 32; off > 0; off >>= 1) {
+        const float m1 = __shfl_xor(m, off), l1 = __shfl_xor(l, off), now = fmaxf(m, m1);
+        l = l * __builtin_amdgcn_exp2f(m - now) + l1 * __builtin_amdgcn_exp2f(m1 - now);
+        m = now;
+    }
+    if (lane) return;
+    const bool has = a.came[t] >= 0;
+    const float lse2 = m + __builtin_amdgcn_logf(l);
+    a.loss[t] = has ? (lse2 - a.hit[t]) * kLn2 : 0.0f;
+    if (a.lse_out) a.lse_out[t] = has ? lse2 * kLn2 : 0.0f;
+}
+
+// dZ of a piece of the rows.
+template <typename T, typename S>
+__global__ __launch_bounds__(S::NT, 2) void k_loss_dz(LossArgs a) {
+    __shared__ __align__(1024) char lds[3 * S::kStage];
+    const unsigned id = xcd_block(blockIdx.x, gridDim.x);
+    const int split = id / a.token_tiles, token0 = (id % a.token_tiles) * S::BN;
+    const int t0 = (int)((long long)a.tiles * split / a.splits), t1 = (int)((long long)a.tiles * (split + 1) / a.splits);
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, half = lane >> 5;
+    const int row_in = (wave / S::WN) * 32 * S::MA, token_in = (wave % S::WN) * 32 * S::NB + (lane & 31);
+
+    float shift[S::NB], by[S::NB];
+    int came[S::NB];
+#pragma unroll
+    for (int j = 0; j < S::NB; ++j) {
+        const int t = token0 + token_in + 32 * j;
+        shift[j] = a.shift[t], by[j] = a.by[t], came[j] = a.came[t] - a.row0;
+    }
+    logits<T, S>(a, lds, a.row0, a.rows, t0, t1, token0, [&](int tile, acc16(&acc)[S::MA][S::NB]) {
+        const int row0 = tile * S::BM + row_in;  // in the piece
+        const int left = a.rows - a.row0 - row0;
+#pragma unroll
+        for (int j = 0; j < S::NB; ++j) {
+            const int mine = came[j] - row0;
+            const bool any = __any(mine >= 0 && mine < 32 * S::MA);
+            uint4* to = a.dz + (long long)(row0 >> 3) * a.t_pad + token0 + token_in + 32 * j;
+#pragma unroll
+            for (int i = 0; i < S::MA; ++i) {
+                float p[16];
+#pragma unroll
+                for (int r = 0; r < 16; ++r)
+                    p[r] = __builtin_amdgcn_exp2f(__builtin_fmaf(acc[i][j][r], a.scale2, -shift[j]));
+                if (any)
+#pragma unroll
+                    for (int r = 0; r < 16; ++r)
+                        if (mine == 32 * i + acc_row(r, half)) p[r] -= 1.0f;
+#pragma unroll
+                for (int r = 0; r < 16; ++r) p[r] *= by[j];
+                if (left < 32 * S::MA)
+#pragma unroll
+                    for (int r = 0; r < 16; ++r)
+                        if (32 * i + acc_row(r, half) >= left) p[r] = 0.0f;
+#pragma unroll
+                for (int q = 0; q < 4; q += 2) {
+                    unsigned x0 = Mma<T>::pair(p[4 * q], p[4 * q + 1]), x1 = Mma<T>::pair(p[4 * q + 2], p[4 * q + 3]);
+                    unsigned y0 = Mma<T>::pair(p[4 * q + 4], p[4 * q + 5]), y1 = Mma<T>::pair(p[4 * q + 6], p[4 * q + 7]);
+                    trade_halves(x0, y0);
+                    trade_halves(x1, y1);
+                    to[(long long)(4 * i + q + half) * a.t_pad] = make_uint4(x0, x1, y0, y1);
+                }
+            }
+        }
+    });
+}
+
+// ---- the gradients' products ---------------------------------------------------
+
+// grad_x of a piece: [width x tokens] = W^T dZ over a share of the piece's rows,
+// added to what the pieces before left in its part.
+template <typename T, typename S>
+__global__ __launch_bounds__(S::NT, 2) void k_loss_grad_x(LossArgs a) {
+    typedef ColumnsOfMatrix<T, S::BM, S::NT> A;
+    typedef RowsOfPieces<T, S::BN, S::NT> B;
+    __shared__ __align__(1024) char lds[3 * S::kStage];
+    unsigned id = xcd_block(blockIdx.x, gridDim.x);
+    const int col_tiles = (a.width + S::BM - 1) / S::BM;
+    const int col0 = (id % col_tiles) * S::BM;
+    id /= col_tiles;
+    const int token0 = (id % a.token_tiles) * S::BN, split = id / a.token_tiles;
+    const int steps = a.piece / kStep;
+    const int k0 = (int)((long long)steps * split / a.x_splits), k1 = (int)((long long)steps * (split + 1) / a.x_splits);
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, half = lane >> 5;
+    const unsigned base = lds_address(lds);
+    const int a_block = (wave / S::WN) * S::MA;
+    const uint2 a_at = A::place(lane);
+    const unsigned b_at = base + S::kA + B::place((wave % S::WN) * 32 * S::NB + (lane & 31), half);
+    acc16 acc[S::MA][S::NB];
+#pragma unroll
+    for (int i = 0; i < S::MA; ++i)
+#pragma unroll
+        for (int j = 0; j < S::NB; ++j) acc[i][j] = zero16();
+    stages<S::kLoads>(
+        k1 - k0,
+        [&](int i, int buf) {
+            const unsigned to = base + buf * S::kStage;
+            const int k = (k0 + i) * kStep;
+            A::load(to, (const T*)a.table, a.t_stride, a.row0 + k, a.rows, col0, a.width);
+            B::load(to + S::kA, a.dz, a.t_pad, token0, k);
+        },
+        [&](int, int buf) {
+            const unsigned on = base + buf * S::kStage;
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+                typename Mma<T>::vec8 x[S::MA], y[S::NB];
+#pragma unroll
+                for (int j = 0; j < S::NB; ++j) y[j] = B::read(b_at + buf * S::kStage, j, s);
+#pragma unroll
+                for (int i = 0; i < S::MA; ++i) x[i] = A::read(make_uint2(a_at.x + on, a_at.y + on), a_block + i, s);
+#pragma unroll
+                for (int i = 0; i < S::MA; ++i)
+#pragma unroll
+                    for (int j = 0; j < S::NB; ++j) acc[i][j] = Mma<T>::mul(x[i], y[j], acc[i][j]);
+            }
+        });
+#pragma unroll
+    for (int j = 0; j < S::NB; ++j) {
+        const int t = token0 + (wave % S::WN) * 32 * S::NB + 32 * j + (lane & 31);
+        if (t >= a.t) continue;
+        float* to = a.part_x + ((long long)split * a.t + t) * a.width;
+#pragma unroll
+        for (int i = 0; i < S::MA; ++i)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const int c = col0 + 32 * (a_block + i) + 8 * q + 4 * half;
+                if (c >= a.width) continue;
+                float4 v = make_float4(acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]);
+                if (!a.first) {
+                    const float4 w = *(const float4*)(to + c);
+                    v.x += w.x, v.y += w.y, v.z += w.z, v.w += w.w;
+                }
+                *(float4*)(to + c) = v;
+            }
+    }
+}
+
+// grad_table of a piece: [width x rows] = X^T dZ over a share of the tokens.
+template <typename T, typename S>
+__global__ __launch_bounds__(S::NT, 2) void k_loss_grad_table(LossArgs a) {
+    typedef ColumnsOfPieces<T, S::BM, S::NT> A;
+    typedef ColumnsOfPieces<T, S::BN, S::NT> B;
+    __shared__ __align__(1024) char lds[3 * S::kStage];
+    unsigned id = xcd_block(blockIdx.x, gridDim.x);
+    const int col_tiles = (a.width + S::BM - 1) / S::BM, row_tiles = a.piece / S::BN;
+    const int col0 = (id % col_tiles) * S::BM;
+    id /= col_tiles;
+    const int row0 = (id % row_tiles) * S::BN, split = id / row_tiles;
+    const int steps = a.tokens_in / kStep;
+    const int k0 = (int)((long long)steps * split / a.t_splits), k1 = (int)((long long)steps * (split + 1) / a.t_splits);
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, half = lane >> 5;
+    const unsigned base = lds_address(lds);
+    const int a_block = (wave / S::WN) * S::MA, b_block = (wave % S::WN) * S::NB;
+    const uint2 at = A::place(lane);
+    acc16 acc[S::MA][S::NB];
+#pragma unroll
+    for (int i = 0; i < S::MA; ++i)
+#pragma unroll
+        for (int j = 0; j < S::NB; ++j) acc[i][j] = zero16();
+    stages<S::kLoads>(
+        k1 - k0,
+        [&](int i, int buf) {
+            const unsigned to = base + buf * S::kStage;
+            A::load(to, a.xg, a.t_pad, (k0 + i) * kStep, col0, a.width);
+            B::load(to + S::kA, a.dz, a.t_pad, (k0 + i) * kStep, row0, a.piece);
+        },
+        [&](int, int buf) {
+            const unsigned x_on = base + buf * S::kStage, y_on = x_on + S::kA;
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+                typename Mma<T>::vec8 x[S::MA], y[S::NB];
+#pragma unroll
+                for (int j = 0; j < S::NB; ++j) y[j] = B::read(make_uint2(at.x + y_on, at.y + y_on), b_block + j, s);
+#pragma unroll
+                for (int i = 0; i < S::MA; ++i) x[i] = A::read(make_uint2(at.x + x_on, at.y + x_on), a_block + i, s);
+#pragma unroll
+                for (int i = 0; i < S::MA; ++i)
+#pragma unroll
+                    for (int j = 0; j < S::NB; ++j) acc[i][j] = Mma<T>::mul(x[i], y[j], acc[i][j]);
+            }
+        });
+    const float down = ldexpf(a.scale, -lift_of<T>(a));
+#pragma unroll
+    for (int j = 0; j < S::NB; ++j) {
+        const int row = row0 + 32 * (b_block + j) + (lane & 31);  // of the piece
+        const bool there = a.row0 + row < a.rows;
+#pragma unroll
+        for (int i = 0; i < S::MA; ++i) {
+            const int c0 = col0 + 32 * (a_block + i);
+            if (a.t_splits > 1) {
+                float* to = a.part_t + ((long long)split * a.piece + row) * a.width;
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const int c = c0 + 8 * q + 4 * half;
+                    if (c < a.width)
+                        *(float4*)(to + c) = make_float4(acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2],
+                                                         acc[i][j][4 * q + 3]);
+                }
+                continue;
+            }
+            T* to = (T*)a.gt + (long long)(a.row0 + row) * a.width;
+#pragma unroll
+            for (int q = 0; q < 4; q += 2) {
+                float p[8];
+#pragma unroll
+                for (int r = 0; r < 8; ++r) p[r] = acc[i][j][4 * q + r] * down;
+                unsigned x0 = Mma<T>::pair(p[0], p[1]), x1 = Mma<T>::pair(p[2], p[3]);
+                unsigned y0 = Mma<T>::pair(p[4], p[5]), y1 = Mma<T>::pair(p[6], p[7]);
+                trade_halves(x0, y0);
+                trade_halves(x1, y1);
+                const int c = c0 + 8 * (q + half);
+                if (there && c < a.width) *(uint4*)(to + c) = make_uint4(x0, x1, y0, y1);
+            }
+        }
+    }
+}
+
+// Parts joined in order, rounded: n elements of out from `count` parts.
+template <typename T>
+__global__ __launch_bounds__(256) void k_loss_round(LossArgs a, const float* part, int count, long long n,
+                                                    long long pitch, T* out) {
+    const long long i = ((long long)blockIdx.x * 256 + threadIdx.x) * 8;
+    if (i >= n) return;
+    float s[8];
+    Pack<float, 8>::load(part + i, s);
+    for (int p = 1; p < count; ++p) {
+        float v[8];
+        Pack<float, 8>::load(part + p * pitch + i, v);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) s[j] += v[j];
+    }
+    const float down = ldexpf(a.scale, -lift_of<T>(a));
+#pragma unroll
+    for (int j = 0; j < 8; ++j) s[j] *= down;
+    Pack<T, 8>::store(out + i, s);
+}
+
+// Without a token: every row's gradient is zero.
+__global__ __launch_bounds__(256) void k_loss_clear(uint4* to, long long n) {
+    for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < n; i += 256ll * gridDim.x)
+        to[i] = make_uint4(0, 0, 0, 0);
+}
+
+// ---- host --------------------------------------------------------------------
+
+template <typename T>
+using Wide = Shape<T, 4, 2, 2, 2>;   // 256 x 128
+template <typename T>
+using Even = Shape<T, 2, 2, 2, 2>;   // 128 x 128
+template <typename T>
+using Slim = Shape<T, 2, 1, 4, 1>;   // 256 x 32: few tokens
+
+long long round256(long long n) { return (n + 255) / 256 * 256; }
+long long ceil_div(long long n, long long d) { return (n + d - 1) / d; }
+int clamp(long long n, long long lo, long long hi) { return (int)(n < lo ? lo : n > hi ? hi : n); }
+
+// How a call is cut: blocks enough for two on each of 256 CUs.
+struct Cut {
+    long long t_pad, width8;
+    int tiles, splits, token_tiles, slim;
+    int piece, pieces, x_splits, t_splits;
+};
+
+Cut cut(long long t, long long rows, long long width) {
+    Cut c;
+    c.t_pad = ceil_div(t, kTokenPad) * kTokenPad;
+    c.width8 = ceil_div(width, kStep) * (kStep / 8);
+    c.slim = t <= 32;
+    c.token_tiles = c.slim ? 1 : (int)(c.t_pad / 128);
+    c.tiles = (int)ceil_div(rows, kRowTile);
+    c.splits = clamp(4096 / c.token_tiles, 1, c.tiles);
+    long long piece = kPieceBytes / (2 * c.t_pad) / kRowTile * kRowTile;
+    if (piece < kRowTile) piece = kRowTile;
+    c.pieces = (int)ceil_div((long long)c.tiles * kRowTile, piece);
+    c.piece = (int)(ceil_div(c.tiles, c.pieces) * kRowTile);
+    c.pieces = (int)ceil_div((long long)c.tiles * kRowTile, c.piece);
+    const long long cols = ceil_div(width, width > 128 ? 256 : 128);
+    c.x_splits = clamp(512 / (cols * (c.t_pad / 128)), 1, c.piece / 512 > 1 ? c.piece / 512 : 1);
+    c.t_splits = clamp(512 / (cols * (c.piece / 128)), 1, c.t_pad / 512 > 1 ? c.t_pad / 512 : 1);
+    return c;
+}
+
+bool sizes_ok(int64_t t, int64_t rows, int64_t width) {
+    return t >= 0 && t <= kMaxTokens && rows >= 1 && rows <= kMaxRows && width >= 8 && width <= kMaxWidth &&
+           width % 8 == 0;
+}
+
+struct Layout {
+    long long xg, came, shift, by, hit, part, top, part_x, part_t, dz, total;
+};
+
+Layout layout(const Cut& c, long long t, long long width, bool grad) {
+    Layout l = {};
+    long long at = 0;
+    auto take = [&](long long bytes) {
+        const long long was = at;
+        at += round256(bytes);
+        return was;
+    };
+    l.xg = take(c.width8 * c.t_pad * 16);
+    l.came = take(c.t_pad * 4);
+    if (!grad) {
+        l.hit = take(c.t_pad * 4);
+        l.part = take(c.splits * c.t_pad * 8);
+    } else {
+        l.shift = take(c.t_pad * 4);
+        l.by = take(c.t_pad * 4);
+        l.top = take(4);
+        l.part_x = take(c.x_splits * t * width * 4);
+        l.part_t = take(c.t_splits > 1 ? (long long)c.t_splits * c.piece * width * 4 : 0);
+        l.dz = take((long long)c.piece / 8 * c.t_pad * 16);
+    }
+    l.total = at;
+    return l;
+}
+
+bool check(const void* x, int64_t x_stride, const void* table, int64_t table_stride, int32_t dtype, int64_t t,
+           int64_t rows, int64_t width, const void* ids, int32_t id_bytes, float scale) {
+    if (dtype != TOK_BF16 && dtype != TOK_F16) return false;
+    if (!sizes_ok(t, rows, width) || (id_bytes != 4 && id_bytes != 8)) return false;
+    if (x_stride < 0 || x_stride % 8 || table_stride < 0 || table_stride % 8 || table_stride >= kMaxStride) return false;
+    if (!(scale >= 1e-30f) || !(scale <= 1e30f)) return false;
+    if (!table || ((size_t)table & 15) || ((size_t)x & 15)) return false;
+    return t == 0 || (x && ids && (size_t)ids % id_bytes == 0);
+}
+
+LossArgs make_args(const void* x, int64_t x_stride, const void* table, int64_t table_stride, int64_t t, int64_t rows,
+                   int64_t width, const void* ids, int32_t id_bytes, float scale, const Cut& c, const Layout& l,
+                   char* ws) {
+    LossArgs a = {};
+    a.x = x, a.x_stride = x_stride, a.table = table, a.t_stride = table_stride;
+    a.t = (int)t, a.rows = (int)rows, a.width = (int)width, a.ids = ids, a.id_bytes = id_bytes;
+    a.scale = scale, a.scale2 = (float)(scale * 1.4426950408889634);
+    a.t_pad = (int)c.t_pad, a.width8 = (int)c.width8;
+    a.tiles = c.tiles, a.splits = c.splits, a.token_tiles = c.token_tiles;
+    a.xg = (uint4*)(ws + l.xg), a.came = (int*)(ws + l.came);
+    a.shift = (float*)(ws + l.shift), a.by = (float*)(ws + l.by), a.hit = (float*)(ws + l.hit);
+    a.part = (float2*)(ws + l.part), a.top = (unsigned*)(ws + l.top);
+    a.part_x = (float*)(ws + l.part_x), a.part_t = (float*)(ws + l.part_t), a.dz = (uint4*)(ws + l.dz);
+    a.piece = c.piece, a.x_splits = c.x_splits, a.t_splits = c.t_splits;
+    a.tokens_in = c.slim ? 32 : (int)c.t_pad;
+    return a;
+}
+
+dim3 pack_grid(const LossArgs& a) {
+    return dim3((unsigned)(a.t_pad / 32), (unsigned)ceil_div(a.width8, 8));
+}
+
+template <typename T>
+int forward(const LossArgs& a, const Cut& c, hipStream_t stream) {
+    k_loss_pack<T, false><<<pack_grid(a), dim3(256), 0, stream>>>(a);
+    const dim3 grid((unsigned)(c.token_tiles * c.splits));
+    if (c.slim)
+        k_loss_sum<T, Slim<T>><<<grid, dim3(Slim<T>::NT), 0, stream>>>(a);
+    else
+        k_loss_sum<T, Wide<T>><<<grid, dim3(Wide<T>::NT), 0, stream>>>(a);
+    k_loss_join<<<dim3((unsigned)ceil_div(a.t, 4)), dim3(256), 0, stream>>>(a);
+    const hipError_t e = hipGetLastError();
+    return e == hipSuccess ? VOX_OK : ssh_hip_fail(e);
+}
+
+template <typename T, typename S>
+void products(const LossArgs& a, hipStream_t stream) {
+    const long long cols = ceil_div(a.width, S::BM);
+    k_loss_grad_x<T, S><<<dim3((unsigned)(cols * (a.t_pad / S::BN) * a.x_splits)), dim3(S::NT), 0, stream>>>(a);
+    k_loss_grad_table<T, S><<<dim3((unsigned)(cols * (a.piece / S::BN) * a.t_splits)), dim3(S::NT), 0, stream>>>(a);
+}
+
+template <typename T>
+int backward(LossArgs a, const Cut& c, hipStream_t stream) {
+    if (__is_same(T, f16_t)) k_loss_top<<<dim3(1), dim3(1024), 0, stream>>>(a);
+    k_loss_pack<T, true><<<pack_grid(a), dim3(256), 0, stream>>>(a);
+    const int all = c.tiles * kRowTile;
+    for (int p = 0; p < c.pieces; ++p) {
+        a.row0 = p * c.piece;
+        a.piece = all - a.row0 < c.piece ? all - a.row0 : c.piece;
+        a.first = p == 0;
+        a.tiles = a.piece / kRowTile;
+        a.splits = clamp(2048 / c.token_tiles, 1, a.tiles);
+        LossArgs z = a;
+        const dim3 grid((unsigned)(z.token_tiles * z.splits));
+        if (c.slim)
+            k_loss_dz<T, Slim<T>><<<grid, dim3(Slim<T>::NT), 0, stream>>>(z);
+        else
+            k_loss_dz<T, Wide<T>><<<grid, dim3(Wide<T>::NT), 0, stream>>>(z);
+        a.token_tiles = (int)(c.t_pad / 128);
+        if (a.width > 128)
+            products<T, Wide<T>>(a, stream);
+        else
+            products<T, Even<T>>(a, stream);
+        a.token_tiles = c.token_tiles;
+        if (c.t_splits > 1) {
+            const long long there = a.rows - a.row0 < a.piece ? a.rows - a.row0 : a.piece, n = there * a.width;
+            k_loss_round<T><<<dim3((unsigned)ceil_div(n, 2048)), dim3(256), 0, stream>>>(
+                a, a.part_t, c.t_splits, n, (long long)a.piece * a.width, (T*)a.gt + (long long)a.row0 * a.width);
+        }
+    }
+    const long long n = (long long)a.t * a.width;
+    k_loss_round<T><<<dim3((unsigned)ceil_div(n, 2048)), dim3(256), 0, stream>>>(a, a.part_x, c.x_splits, n, n, (T*)a.gx);
+    const hipError_t e = hipGetLastError();
+    return e == hipSuccess ? VOX_OK : ssh_hip_fail(e);
+}
+
+}  // namespace
+
+extern "C" {
+
+int64_t tok_row_loss_workspace_bytes(int64_t t, int64_t rows, int64_t width) {
+    if (!sizes_ok(t, rows, width)) return VOX_EINVAL;
+    return t == 0 ? 0 : layout(cut(t, rows, width), t, width, false).total;
+}
+
+int64_t tok_row_loss_grad_workspace_bytes(int64_t t, int64_t rows, int64_t width) {
+    if (!sizes_ok(t, rows, width)) return VOX_EINVAL;
+    return t == 0 ? 0 : layout(cut(t, rows, width), t, width, true).total;
+}
+
+int tok_row_loss(const void* x, int64_t x_stride, const void* table, int64_t table_stride, int32_t dtype,
+                 int64_t t, int64_t rows, int64_t width, const void* ids, int32_t id_bytes, float scale, float* loss,
+                 float* lse, void* workspace, int64_t workspace_bytes, hipStream_t stream) {
+    if (!check(x, x_stride, table, table_stride, dtype, t, rows, width, ids, id_bytes, scale)) return VOX_EINVAL;
+    if (t == 0) return VOX_OK;
+    if (!loss || ((size_t)loss | (size_t)lse) % 4) return VOX_EINVAL;
+    const Cut c = cut(t, rows, width);
+    const Layout l = layout(c, t, width, false);
+    if (!workspace_ok(workspace, workspace_bytes, l.total)) return VOX_EWORKSPACE;
+    LossArgs a = make_args(x, x_stride, table, table_stride, t, rows, width, ids, id_bytes, scale, c, l, (char*)workspace);
+    a.loss = loss, a.lse_out = lse;
+    return dtype == TOK_BF16 ? forward<bf16_t>(a, c, stream) : forward<f16_t>(a, c, stream);
+}
+
+int tok_row_loss_grad(const float* grad, const void* x, int64_t x_stride, const void* table, int64_t table_stride,
+                      int32_t dtype, int64_t t, int64_t rows, int64_t width, const void* ids, int32_t id_bytes,
+                      const float* lse, float scale, void* grad_x, void* grad_table, void* workspace,
+                      int64_t workspace_bytes, hipStream_t stream) {
+    if (!check(x, x_stride, table, table_stride, dtype, t, rows, width, ids, id_bytes, scale)) return VOX_EINVAL;
+    if (!grad_table || (((size_t)grad_x | (size_t)grad_table) & 15)) return VOX_EINVAL;
+    if (t && (!grad || !lse || !grad_x || ((size_t)grad | (size_t)lse) % 4)) return VOX_EINVAL;
+    if (t == 0) {
+        k_loss_clear<<<dim3(2048), dim3(256), 0, stream>>>((uint4*)grad_table, rows * width / 8);
+        const hipError_t e = hipGetLastError();
+        return e == hipSuccess ? VOX_OK : ssh_hip_fail(e);
+    }
+    const Cut c = cut(t, rows, width);
+    const Layout l = layout(c, t, width, true);
+    if (!workspace_ok(workspace, workspace_bytes, l.total)) return VOX_EWORKSPACE;
+    LossArgs a = make_args(x, x_stride, table, table_stride, t, rows, width, ids, id_bytes, scale, c, l, (char*)workspace);
+    a.grad = grad, a.lse = lse, a.gx = grad_x, a.gt = grad_table;
+    return dtype == TOK_BF16 ? backward<bf16_t>(a, c, stream) : backward<f16_t>(a, c, stream);
+}
+
+}  // extern "C"
