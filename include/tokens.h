@@ -194,6 +194,59 @@ int tok_rotate(const void* x, int64_t tokens, int64_t heads, int64_t width, int6
                int64_t axis_stride, int32_t axes, const double* freqs, int64_t pairs,
                int32_t interleaved, int32_t inverse, void* out, hipStream_t stream);
 
+/* ---- attention with decay ---------------------------------------------------
+ *
+ * q [t, heads, width], k and v [t, kv_heads, width], bf16 or fp16, packed by
+ * offsets [docs + 1]; query head h reads key head h / (heads / kv_heads) and has a
+ * state S [width, width] of its own. Along each document, from its first token
+ * (reverse 0) or its last (reverse 1):
+ *   S = exp(-decay[h]) S + k v^T;  out[t] = scale * q S
+ * from the document's state (state [docs, heads, width, width] float32, S[i, j]
+ * of k's element i and v's j; NULL: zeros); last_state of the same shape (or NULL)
+ * receives S after its last step (the state itself for a document of no tokens).
+ * Tokens of no document get zeros and no gradient. decay is float32 on the device;
+ * negative values are taken as 0 and values over 1000 as 1000. States and sums are
+ * float32; documents of more than a token or two are taken in chunks of 32 tokens
+ * on matrix instructions, for which weights (q.k) exp(-decay n) and the copy of a state
+ * that q is multiplied with are rounded to the tensors' type. A value that is not finite may reach every
+ * token of its chunk of 32 and of the document after it, and none of another one.
+ * carry receives what tok_decay_attend_grad needs besides: tok_decay_carry_rows()
+ * states [heads, width, width] float32 (0: NULL will do). It is needed without
+ * gradients too: it is the call's workspace.
+ * Limits: t * heads and t at most 2^31 - 4096, 1 <= docs <= 2^20,
+ * (docs + 2) * heads <= 2^30; width a multiple of 8, at most 128; strides multiples of
+ * 8; all bases 16-byte aligned; scale in [1e-30, 1e30].
+ */
+typedef struct tok_decay {
+    int32_t dtype;              /* TOK_BF16 or TOK_F16 */
+    int32_t heads, kv_heads;    /* heads a multiple of kv_heads */
+    int32_t width;
+    int64_t t;                  /* tokens */
+    int32_t docs, reverse;
+    const int32_t* offsets;     /* device [docs + 1]; NULL: one document of all tokens */
+    const float* decay;         /* device [heads] */
+    float scale;
+    int32_t reserved;           /* 0 */
+    int64_t q_stride[2], k_stride[2], v_stride[2], g_stride[2]; /* token, head; g: grad_out */
+} tok_decay;
+
+/* Or VOX_EINVAL. */
+int64_t tok_decay_carry_rows(const tok_decay* args);
+int64_t tok_decay_grad_workspace_bytes(const tok_decay* args);
+
+int tok_decay_attend(const tok_decay* args, const void* q, const void* k, const void* v,
+                     const float* state, void* out, float* last_state, float* carry,
+                     hipStream_t stream);
+
+/* Gradients of q, k, v and state (grad_state, or NULL) from those of out and of
+ * last_state (grad_last, or NULL: zeros), with the carry of the forward call.
+ * Gradients of shared key heads are summed over their query heads in float32. */
+int tok_decay_attend_grad(const tok_decay* args, const void* q, const void* k, const void* v,
+                          const void* grad_out, const float* state, const float* carry,
+                          const float* grad_last, void* grad_q, void* grad_k, void* grad_v,
+                          float* grad_state, void* workspace, int64_t workspace_bytes,
+                          hipStream_t stream);
+
 /* ---- loss over a table's rows -----------------------------------------------
  *
  * x [t, width] and table [rows, width], bf16 or fp16, rows x_stride and
@@ -211,7 +264,7 @@ int tok_rotate(const void* x, int64_t tokens, int64_t heads, int64_t width, int6
  *   grad_table[r] = scale * sum over i of w[i, r] x[i]        [rows, width]
  * contiguous, in x's type, every row written. w is rounded to that type (fp16:
  * after powers of two that bring the largest |grad| to 2^14), sums are float32.
- * Limits: 0 <= t <= 2^27, 1 <= rows <= 2^31 - 2048; width a multiple of 8, at most
+ * Limits: 0 <= t <= 2^25, 1 <= rows <= 2^31 - 2048; width a multiple of 8, at most
  * 65536; strides multiples of 8, table_stride below 2^22; all bases 16-byte
  * aligned; scale in [1e-30, 1e30]. The workspace needs no initial contents,
  * 256-byte aligned.

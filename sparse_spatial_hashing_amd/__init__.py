@@ -661,4 +661,5 @@ def spherical(points: torch.Tensor, sph_min: Sequence[float], sph_cell: Sequence
 
 from .tokens import (attend, attend_grad, embed, embed_grad, gated_scan,  # noqa: E402,F401
                      gated_scan_grad)
-from .prediction import rotary_frequencies, rotate, row_loss, row_loss_grad  # noqa: E402,F401
+from .prediction import (decay_attend, decay_attend_grad, rotary_frequencies, rotate,  # noqa: E402,F401
+                         row_loss, row_loss_grad)

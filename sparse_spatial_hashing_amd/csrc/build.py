@@ -17,7 +17,7 @@ CSRC = os.path.dirname(os.path.abspath(__file__))
 HERE = os.path.dirname(CSRC)
 ROOT = os.path.dirname(HERE)
 SOURCES = [os.path.join(CSRC, f) for f in ("voxelize.hip", "spherical.hip", "embed.hip", "scan.hip",
-                                           "attend.hip", "rotate.hip", "loss.hip")]
+                                           "attend.hip", "rotate.hip", "decay.hip", "loss.hip")]
 # compiled once per element type and padded head width
 ATTENTION = os.path.join(CSRC, "attend_kernels.hip")
 UNITS = [(s, []) for s in SOURCES] + [(ATTENTION, [f"-DATT_WIDTH={w}", f"-DATT_F16={f}"])

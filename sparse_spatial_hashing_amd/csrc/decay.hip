@@ -1,0 +1,807 @@
+// Attention with decay (tokens.h): forward, backward, and token by token.
+//
+// S[t] = e^-r S[t-1] + k[t] v[t]^T, out[t] = scale q[t] S[t]. Over a chunk of 32
+// tokens, with S the state before it:
+//   out[i] = scale (e^-r(i+1) q[i] S + sum over j <= i of e^-r(i-j) (q[i].k[j]) v[j])
+//   S'     = e^-rm S + sum over j of e^-r(m-1-j) k[j] v[j]^T   (m tokens)
+// which is four small products on matrix instructions. A document is cut into
+// segments: k_decay_sum takes what each segment adds to a state, k_decay_join
+// turns that into the state that enters each segment, k_decay_run walks the
+// segments from there. The gradients are the same walk with other tensors in its
+// places: grad_q that of (grad, v, k) with the states transposed, and from the other
+// end grad_v that of (k, q, grad) and grad_k that of (v, grad, q).
+//
+// A block has W / 32 wavefronts, each with 32 columns of the state (all its rows) in
+// registers, W the padded width. Everything is taken transposed (out^T = S^T Q^T +
+// V^T P^T), so that registers that hold a result are, rounded, the next product's
+// operand: a state's column, 8 rows at a time, and a query's weights, 8 keys at a
+// time. For that the rows of K, and its columns, are read with bits 2 and 3 of their
+// number traded: register 8 c + j of half h then is row 16 c + 8 h + j.
+//
+// Roundings. The state is in 32 bits, and a result: v e^-r(m-1-j), which enters it, is
+// taken in two or three parts of the tensors' type that together hold 22 bits or more. Its
+// copy for the product with q, and the weights (q.k) e^-r(i-j), are rounded to the
+// tensors' type, as the 16-bit matrix instructions take them. In fp16 each of the three
+// is first multiplied with a power of two that brings its largest to about 1.
+//
+// Memory bounds it: k and v are read twice, all else once.
+
+#include <hip/hip_runtime.h>
+
+#include "mma_ops.h"
+
+int ssh_hip_fail(hipError_t e);  // records the error for vox_last_hip_error()
+
+namespace {
+
+constexpr long long kMaxElems = (1ll << 31) - 4096;
+constexpr int kMaxDocs = 1 << 20;
+constexpr int kChunk = 32;
+constexpr float kLog2e = 1.4426950408889634f;
+
+// A tensor in one of the walk's places.
+struct Place {
+    const void* p;
+    long long st, sh;  // token and head stride
+    int group;         // query heads that share one of its heads
+};
+
+struct DecayArgs {
+    Place q, k, v;
+    void* out;            // [t, out heads, width]; float32 with out_wide
+    const int* offsets;
+    const float* decay;
+    const float* state;   // [docs, heads, width, width] or null
+    float* last;          // or null
+    float* carry;         // [segments, heads, width, width]: sums, then the states that enter
+    int t, docs, heads, width;
+    int segment;          // tokens: a multiple of kChunk
+    int segments;
+    int back;             // walks from a document's last token
+    int turned;           // states are read transposed
+    int lag;              // 1: a state counts one token on; 0: it is that of the token itself
+    int out_wide;
+    float near_by, enter_by, leave_by;  // of tokens of a chunk, of the state, of what enters it
+    unsigned first_block;
+};
+
+// The document, and the part of it, of a segment number: the segments of range b start at
+// floor(start / segment) + b, which leaves every range enough without anyone knowing
+// the lengths on the host.
+struct Part {
+    int lo, n;       // the document's first token and its tokens
+    int doc;         // -1: of no document
+    int from, to;    // tokens of this segment, in the walk's order
+    bool none;       // no such segment
+    bool last;
+};
+
+__device__ __forceinline__ Part find_part(const DecayArgs& a, int slot) {
+    int lo = 0, n = a.docs + 2, first = 0;
+    const int lane = __lane_id();
+    while (n > 1) {
+        const int step = (n + kWave - 1) / kWave;
+        const int b = lo + lane * step;
+        const bool in = lane * step < n;
+        const int f = in ? tok_boundary(a.offsets, a.docs, a.t, b) / a.segment + b : 0x7fffffff;
+        const int cnt = max(1, (int)__popcll(__ballot(in && f <= slot)));
+        first = __shfl(f, cnt - 1);
+        lo += (cnt - 1) * step;
+        n = min(step, n - (cnt - 1) * step);
+    }
+    lo = __builtin_amdgcn_readfirstlane(lo);
+    first = __builtin_amdgcn_readfirstlane(first);
+    Part p;
+    p.lo = tok_boundary(a.offsets, a.docs, a.t, lo);
+    p.n = max(0, tok_boundary(a.offsets, a.docs, a.t, lo + 1) - p.lo);
+    p.doc = lo >= 1 && lo <= a.docs ? lo - 1 : -1;
+    const long long from = (long long)(slot - first) * a.segment;
+    p.none = from < 0 || (from > 0 && from >= p.n);
+    p.from = p.none ? 0 : (int)from;
+    p.to = min(p.n, p.from + a.segment);
+    p.last = p.to == p.n;
+    return p;
+}
+
+// decay * log2(e) of a head: never negative, and at most what leaves nothing of a token.
+__device__ __forceinline__ float rate_of(const DecayArgs& a, int head) {
+    return fminf(fmaxf(a.decay[head], 0.0f), 1000.0f) * kLog2e;
+}
+__device__ __forceinline__ float fall(float rate, int steps) {
+    return __builtin_amdgcn_exp2f(-rate * (float)steps);
+}
+
+template <typename T, int W>
+struct Decay {
+    typedef typename Mma<T>::vec8 vec8;
+    static constexpr int kWaves = W / 32, NT = 64 * kWaves;
+    static constexpr int kPieces = W / 8;           // of 16 bytes in a row
+    static constexpr int kTile = kChunk * W * 2;    // bytes
+    static constexpr int kBlocks = W / 32;
+    static constexpr bool kHalf = __is_same(T, f16_t);
+
+    static __device__ __forceinline__ int swz(int row) {
+        if (W == 128) return ((row & 3) << 2) | ((row >> 2) & 3);
+        if (W == 64) return (((row >> 1) & 1) << 2) | ((row >> 2) & 3);
+        return (row >> 2) & 3;
+    }
+    // bits 2 and 3 traded
+    static __device__ __forceinline__ int traded(int x) { return (x & ~12) | ((x & 4) << 1) | ((x & 8) >> 1); }
+
+    // A chunk's rows of one tensor to LDS; zeros past its end and the width.
+    static __device__ __forceinline__ void load(unsigned to, const Place& p, int head, const DecayArgs& a,
+                                                const Part& d, int at) {
+        const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+        const T* base = (const T*)p.p + (long long)(head / p.group) * p.sh;
+        const int left = d.to - at;
+        const int first = a.back ? d.lo + d.n - 1 - at : d.lo + at;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int n = i * NT + threadIdx.x, row = n / kPieces, c = (n % kPieces) ^ swz(row);
+            const int token = a.back ? first - row : first + row;
+            const bool there = row < left && 8 * c < a.width;
+            const void* from = there ? (const void*)(base + (long long)token * p.st + 8 * c) : &kNothing;
+            load_to_lds(to + 1024u * wave + 16u * NT * i, from);
+        }
+    }
+    // Operand of a product over the width: row number `row`, step s of 16.
+    static __device__ __forceinline__ unsigned row_place(int row, int half) {
+        return row * 2 * W + ((half ^ swz(row)) << 4);
+    }
+    static __device__ __forceinline__ vec8 read_row(unsigned at, int s) { return lds_read<vec8>(at ^ (s << 5)); }
+    // Operand of a product over the tokens: columns of block b, step s of 16 tokens.
+    // TRADED: with bits 2 and 3 of the column traded.
+    template <bool TRADED>
+    static __device__ __forceinline__ uint2 column_place(int lane) {
+        const int row = 8 * (lane >> 5) + ((lane & 15) >> 2);
+        const int four = TRADED ? ((lane & 1) << 1) | ((lane & 2) >> 1) : lane & 3;
+        const int c = 2 * ((lane >> 4) & 1) + (four >> 1), in = (four & 1) << 3;
+        return make_uint2(row * 2 * W + ((c ^ swz(row)) << 4) + in, (row + 4) * 2 * W + ((c ^ swz(row + 4)) << 4) + in);
+    }
+    static __device__ __forceinline__ vec8 read_column(uint2 at, int b, int s) {
+        const unsigned on = s * 32 * W, flip = b << 6;
+        return lds_read_columns<vec8>((at.x ^ flip) + on, (at.y ^ flip) + on);
+    }
+
+    // The power of two that brings x to about 1 (1 for 0 and what is not finite).
+    static __device__ __forceinline__ float to_one(float x) {
+        return x > 0.0f && x <= 3.402823466e+38f
+                   ? ldexpf(1.0f, min(max(-__builtin_amdgcn_frexp_expf(x), -120), 120)) : 1.0f;
+    }
+    static __device__ __forceinline__ float wave_max(float x) {
+#pragma unroll
+        for (int off = 32; off > 0; off >>= 1) x = fmaxf(x, __shfl_xor(x, off));
+        return x;
+    }
+
+    // This wavefront's columns of a state. Rows 16 c + 8 h + j of block b are
+    // registers 8 c + j.
+    typedef acc16 State[kBlocks];
+    static __device__ __forceinline__ void load_state(State& s, const float* from, int width, bool turned, int column,
+                                                      int half) {
+#pragma unroll
+        for (int b = 0; b < kBlocks; ++b)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                const int row = 32 * b + 16 * c + 8 * half;
+                const bool there = from && column < width && row < width;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) s[b][8 * c + j] = 0.0f;
+                if (there && turned) {
+                    float x[8];
+                    Pack<float, 4>::load(from + column * width + row, *(float(*)[4])x);
+                    Pack<float, 4>::load(from + column * width + row + 4, *(float(*)[4])(x + 4));
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) s[b][8 * c + j] = x[j];
+                } else if (there) {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) s[b][8 * c + j] = from[(row + j) * width + column];
+                }
+            }
+    }
+    static __device__ __forceinline__ void store_state(const State& s, float* to, int width, int column, int half) {
+        if (column >= width) return;
+#pragma unroll
+        for (int b = 0; b < kBlocks; ++b)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                const int row = 32 * b + 16 * c + 8 * half;
+                if (row >= width) continue;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) to[(row + j) * width + column] = s[b][8 * c + j];
+            }
+    }
+
+    // What v's rows are multiplied with on their way into the state: e^-r(m - lag - j)
+    // (1 for rows that are not there), and leave_by.
+    static __device__ __forceinline__ void leaving(float (&w)[16], const DecayArgs& a, float rate, int m, int half) {
+#pragma unroll
+        for (int r = 0; r < 16; ++r)
+            w[r] = fall(rate, max(0, m - a.lag - (16 * (r / 8) + 8 * half + r % 8))) * a.leave_by;
+    }
+
+    // S <- through S + K^T (w V) over a chunk in LDS. w V in one rounding, or (WHOLE) in
+    // as many parts as hold 22 bits or more of it: 2 of fp16, 3 of bf16.
+    template <bool WHOLE>
+    static __device__ __forceinline__ void advance(State& s, uint2 k_at, const vec8 (&v)[2], const float (&w)[16],
+                                                   float through) {
+        constexpr int kParts = !WHOLE ? 1 : kHalf ? 2 : 3;
+        float x[16];
+#pragma unroll
+        for (int r = 0; r < 16; ++r) x[r] = (float)v[r / 8][r % 8] * w[r];
+        float up = 1.0f;
+        if (kHalf) {
+            float top = 0.0f;
+#pragma unroll
+            for (int r = 0; r < 16; ++r) top = fmaxf(top, fabsf(x[r]));
+            up = to_one(wave_max(top));
+#pragma unroll
+            for (int r = 0; r < 16; ++r) x[r] *= up;
+        }
+        vec8 y[kParts][2];
+#pragma unroll
+        for (int part = 0; part < kParts; ++part)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) {
+                y[part][r / 8][r % 8] = (T)x[r];
+                x[r] -= (float)y[part][r / 8][r % 8];
+            }
+#pragma unroll
+        for (int b = 0; b < kBlocks; ++b) {
+            acc16 add = kHalf ? zero16() : s[b];
+            if (!kHalf)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) add[r] *= through;
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                const vec8 k = read_column(k_at, b, c);
+#pragma unroll
+                for (int part = kParts - 1; part >= 0; --part) add = Mma<T>::mul(k, y[part][c], add);
+            }
+            if (kHalf) {
+                const float down = 1.0f / up;
+#pragma unroll
+                for (int r = 0; r < 16; ++r) s[b][r] = __builtin_fmaf(add[r], down, s[b][r] * through);
+            } else {
+                s[b] = add;
+            }
+        }
+    }
+};
+
+// The segment and head of a block.
+__device__ __forceinline__ int block_of(const DecayArgs& a, int* head) {
+    const unsigned id = a.first_block + xcd_block(blockIdx.x, gridDim.x);
+    *head = id % a.heads;
+    return id / a.heads;
+}
+
+// What a segment adds to the state that enters it; nothing needs a document's last.
+template <typename T, int W>
+__global__ __launch_bounds__(2 * W) void k_decay_sum(DecayArgs a) {
+    typedef Decay<T, W> D;
+    __shared__ __align__(1024) char lds[3 * 2 * D::kTile];
+    int head;
+    const int slot = block_of(a, &head);
+    const Part d = find_part(a, slot);
+    if (d.none || d.doc < 0 || d.last) return;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, half = lane >> 5;
+    const float rate = rate_of(a, head);
+    const unsigned base = lds_address(lds);
+    const int chunks = a.segment / kChunk;  // whole: a document goes on after it
+    float w[16];
+    D::leaving(w, a, rate, kChunk, half);
+    const float through = fall(rate, kChunk);
+    const uint2 k_in = D::template column_place<true>(lane), v_in = D::template column_place<false>(lane);
+    typename D::State s;
+#pragma unroll
+    for (int b = 0; b < D::kBlocks; ++b) s[b] = zero16();
+    auto issue = [&](int c, int buf) {
+        const unsigned to = base + buf * 2 * D::kTile;
+        D::load(to, a.k, head, a, d, d.from + c * kChunk);
+        D::load(to + D::kTile, a.v, head, a, d, d.from + c * kChunk);
+    };
+    issue(0, 0);
+    if (chunks > 1) issue(1, 1);
+    int buf = 0;
+    for (int c = 0; c < chunks; ++c) {
+        if (c + 1 < chunks)
+            load_wait<4>();
+        else
+            load_wait<0>();
+        __syncthreads();
+        if (c + 2 < chunks) issue(c + 2, buf == 0 ? 2 : buf - 1);
+        const unsigned on = base + buf * 2 * D::kTile;
+        typename D::vec8 v[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            v[i] = D::read_column(make_uint2(v_in.x + on + D::kTile, v_in.y + on + D::kTile), wave, i);
+        D::template advance<true>(s, make_uint2(k_in.x + on, k_in.y + on), v, w, through);
+        buf = buf == 2 ? 0 : buf + 1;
+    }
+    D::store_state(s, a.carry + ((long long)slot * a.heads + head) * a.width * a.width, a.width,
+                   32 * wave + (lane & 31), half);
+}
+
+// The states that enter a document's segments, over their sums: four elements of a
+// state per thread, along the segments.
+__global__ __launch_bounds__(256) void k_decay_join(DecayArgs a, int slices) {
+    unsigned id = a.first_block + blockIdx.x;
+    const int slice = id % slices;
+    id /= slices;
+    const int head = id % a.heads, doc = id / a.heads;
+    const int lo = tok_boundary(a.offsets, a.docs, a.t, doc + 1);
+    const int n = max(0, tok_boundary(a.offsets, a.docs, a.t, doc + 2) - lo);
+    const int parts = (n + a.segment - 1) / a.segment;
+    if (parts <= 1) return;
+    const int size = a.width * a.width, at = (slice * 256 + (int)threadIdx.x) * 4;
+    if (at >= size) return;
+    const long long pitch = (long long)a.heads * size;
+    float* sum = a.carry + (long long)(lo / a.segment + doc + 1) * pitch + (long long)head * size + at;
+    const float through = fall(rate_of(a, head), a.segment);
+    float4 h = make_float4(0, 0, 0, 0);
+    if (a.state) {
+        const float* from = a.state + (long long)doc * pitch + (long long)head * size;
+        h = *(const float4*)(from + at);
+    }
+    constexpr int kAhead = 8;
+    for (int p = 0; p < parts; p += kAhead) {
+        float4 x[kAhead];
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) x[j] = *(const float4*)(sum + min(p + j, parts - 2) * pitch);
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) {
+            if (p + j < parts) *(float4*)(sum + (p + j) * pitch) = h;
+            h.x = __builtin_fmaf(through, h.x, x[j].x), h.y = __builtin_fmaf(through, h.y, x[j].y);
+            h.z = __builtin_fmaf(through, h.z, x[j].z), h.w = __builtin_fmaf(through, h.w, x[j].w);
+        }
+    }
+}
+
+// A segment from the state that enters it. WHOLE: its states are a result too.
+template <typename T, int W, bool WHOLE>
+__global__ __launch_bounds__(2 * W, 2) void k_decay_run(DecayArgs a) {
+    typedef Decay<T, W> D;
+    __shared__ __align__(1024) char lds[3 * 3 * D::kTile];
+    int head;
+    const int slot = block_of(a, &head);
+    const Part d = find_part(a, slot);
+    if (d.none) return;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, half = lane >> 5, i = lane & 31;
+    const long long out_row = (long long)a.heads * a.width;
+    if (d.doc < 0) {  // tokens of no document
+        for (int s = d.from; s < d.to; ++s)
+            for (int c = threadIdx.x; c < a.width; c += D::NT) {
+                const long long at = (d.lo + s) * out_row + head * a.width + c;
+                if (a.out_wide)
+                    ((float*)a.out)[at] = 0.0f;
+                else
+                    ((T*)a.out)[at] = (T)0.0f;
+            }
+        return;
+    }
+    const long long size = (long long)a.width * a.width;
+    const int column = 32 * wave + i;
+    const float rate = rate_of(a, head);
+    const unsigned base = lds_address(lds);
+    const int chunks = (d.to - d.from + kChunk - 1) / kChunk;
+    auto issue = [&](int c, int buf) {
+        const unsigned to = base + buf * 3 * D::kTile;
+        D::load(to, a.q, head, a, d, d.from + c * kChunk);
+        D::load(to + D::kTile, a.k, head, a, d, d.from + c * kChunk);
+        D::load(to + 2 * D::kTile, a.v, head, a, d, d.from + c * kChunk);
+    };
+    typename D::State s;
+    {
+        const float* from = d.from > 0 ? a.carry + ((long long)slot * a.heads + head) * size
+                            : a.state  ? a.state + ((long long)d.doc * a.heads + head) * size
+                                       : nullptr;
+        D::load_state(s, from, a.width, a.turned, column, half);
+    }
+    // settled here: inside the loop their wait would be for the tiles under way as well
+#pragma unroll
+    for (int b = 0; b < D::kBlocks; ++b) asm volatile("" : "+v"(s[b]));
+    if (chunks > 0) issue(0, 0);
+    if (chunks > 1) issue(1, 1);
+
+    float w[16], near[16];
+    D::leaving(w, a, rate, kChunk, half);
+#pragma unroll
+    for (int r = 0; r < 16; ++r) {
+        const int key = 16 * (r / 8) + 8 * half + r % 8;
+        near[r] = fall(rate, max(0, i - key)) * a.near_by;
+    }
+    const float entering = fall(rate, i + a.lag) * a.enter_by;
+    float through = fall(rate, kChunk);
+    const unsigned q_in = D::row_place(i, half), k_in = D::row_place(D::traded(i), half);
+    const uint2 kc_in = D::template column_place<true>(lane), vc_in = D::template column_place<false>(lane);
+
+    uint4 made[2];  // the chunk before, rounded, not yet stored
+    acc16 wide;
+    auto store = [&](int c) {
+        const int at = d.from + c * kChunk + i;
+        if (at >= d.to) return;
+        const long long token = a.back ? d.lo + d.n - 1 - at : d.lo + at;
+        const long long row = token * out_row + head * a.width;
+        if (a.out_wide) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const int col = 32 * wave + 8 * q + 4 * half;
+                if (col < a.width)
+                    *(float4*)((float*)a.out + row + col) =
+                        make_float4(wide[4 * q], wide[4 * q + 1], wide[4 * q + 2], wide[4 * q + 3]);
+            }
+            return;
+        }
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+            const int col = 32 * wave + 8 * (2 * q + half);
+            if (col < a.width) *(uint4*)((T*)a.out + row + col) = made[q];
+        }
+    };
+
+    int buf = 0;
+    for (int c = 0; c < chunks; ++c) {
+        if (c + 1 < chunks)
+            load_wait<6>();
+        else
+            load_wait<0>();
+        __syncthreads();  // this chunk is there, and all are done with the one before
+        if (c > 0) store(c - 1);
+        if (c + 2 < chunks) issue(c + 2, buf == 0 ? 2 : buf - 1);
+        const int m = min(kChunk, d.to - d.from - c * kChunk);
+        const unsigned on = base + buf * 3 * D::kTile;
+        const unsigned q_at = q_in + on, k_at = k_in + on + D::kTile;
+
+        acc16 p = zero16(), o = zero16();
+        float up_s = 1.0f;
+        if (D::kHalf) {
+            float top = 0.0f;
+#pragma unroll
+            for (int b = 0; b < D::kBlocks; ++b)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) top = fmaxf(top, fabsf(s[b][r]));
+            up_s = D::to_one(D::wave_max(top));
+        }
+#pragma unroll
+        for (int k = 0; k < W / 16; ++k) {
+            const typename D::vec8 q = D::read_row(q_at, k);
+            p = Mma<T>::mul(D::read_row(k_at, k), q, p);
+            typename D::vec8 x;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) x[j] = (T)(D::kHalf ? s[k / 2][8 * (k & 1) + j] * up_s : s[k / 2][8 * (k & 1) + j]);
+            o = Mma<T>::mul(x, q, o);
+        }
+        float up_p = 1.0f;
+#pragma unroll
+        for (int r = 0; r < 16; ++r) p[r] = i >= 16 * (r / 8) + 8 * half + r % 8 ? p[r] * near[r] : 0.0f;
+        if (D::kHalf) {
+            float top = 0.0f;
+#pragma unroll
+            for (int r = 0; r < 16; ++r) top = fmaxf(top, fabsf(p[r]));
+            up_p = D::to_one(fmaxf(top, __shfl_xor(top, 32)));
+#pragma unroll
+            for (int r = 0; r < 16; ++r) p[r] *= up_p;
+        }
+        const float in = D::kHalf ? entering * (up_p / up_s) : entering;
+#pragma unroll
+        for (int r = 0; r < 16; ++r) o[r] *= in;
+        typename D::vec8 v[2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            v[j] = D::read_column(make_uint2(vc_in.x + on + 2 * D::kTile, vc_in.y + on + 2 * D::kTile), wave, j);
+            typename D::vec8 x;
+#pragma unroll
+            for (int r = 0; r < 8; ++r) x[r] = (T)p[8 * j + r];
+            o = Mma<T>::mul(v[j], x, o);
+        }
+        const float out_by = D::kHalf ? 1.0f / up_p : 1.0f;
+#pragma unroll
+        for (int r = 0; r < 16; ++r) wide[r] = o[r] * out_by;
+        if (!a.out_wide) {
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                unsigned x0 = Mma<T>::pair(wide[8 * q], wide[8 * q + 1]), x1 = Mma<T>::pair(wide[8 * q + 2], wide[8 * q + 3]);
+                unsigned y0 = Mma<T>::pair(wide[8 * q + 4], wide[8 * q + 5]), y1 = Mma<T>::pair(wide[8 * q + 6], wide[8 * q + 7]);
+                trade_halves(x0, y0);
+                trade_halves(x1, y1);
+                made[q] = make_uint4(x0, x1, y0, y1);
+            }
+        }
+        if (m < kChunk) {
+            D::leaving(w, a, rate, m, half);
+            through = fall(rate, m);
+        }
+        if (c + 1 < chunks || a.last)
+            D::template advance<WHOLE>(s, make_uint2(kc_in.x + on + D::kTile, kc_in.y + on + D::kTile), v, w, through);
+        buf = buf == 2 ? 0 : buf + 1;
+    }
+    if (chunks > 0) store(chunks - 1);
+    if (d.last && a.last) D::store_state(s, a.last + ((long long)d.doc * a.heads + head) * size, a.width, column, half);
+}
+
+// Documents of one token or two: a block per document and head holds the state and
+// goes through the tokens, all in 32 bits. A thread has four columns and every
+// (threads / columns)th row.
+constexpr int kStepThreads = 256;
+
+template <typename T, int W>
+__global__ __launch_bounds__(kStepThreads) void k_decay_step(DecayArgs a) {
+    constexpr int kColumns = W / 4, kGroups = kStepThreads / kColumns, kRows = (W + kGroups - 1) / kGroups;
+    __shared__ float4 parts[kGroups][kColumns];
+    const unsigned id = a.first_block + blockIdx.x;
+    const int head = id % a.heads, range = id / a.heads;  // 0 and docs + 1: of no document
+    const int lo = tok_boundary(a.offsets, a.docs, a.t, range);
+    const int n = max(0, tok_boundary(a.offsets, a.docs, a.t, range + 1) - lo);
+    const long long out_row = (long long)a.heads * a.width;
+    T* out = (T*)a.out + head * a.width;
+    if (range < 1 || range > a.docs) {
+        for (int s = 0; s < n; ++s)
+            for (int c = threadIdx.x; c < a.width; c += kStepThreads) out[(lo + s) * out_row + c] = (T)0.0f;
+        return;
+    }
+    const long long at = ((long long)(range - 1) * a.heads + head) * a.width * a.width;
+    const int c = (threadIdx.x % kColumns) * 4, group = threadIdx.x / kColumns;
+    const bool on = c < a.width;
+    const float through = fall(rate_of(a, head), 1);
+    float4 s[kRows];
+#pragma unroll
+    for (int j = 0; j < kRows; ++j) {
+        const int row = group + j * kGroups;
+        s[j] = a.state && on && row < a.width ? *(const float4*)(a.state + at + row * a.width + c) : make_float4(0, 0, 0, 0);
+    }
+    for (int step = 0; step < n; ++step) {
+        const long long token = a.back ? lo + n - 1 - step : lo + step;
+        const T* q = (const T*)a.q.p + token * a.q.st + head * a.q.sh;
+        const T* k = (const T*)a.k.p + token * a.k.st + (head / a.k.group) * a.k.sh;
+        const T* v = (const T*)a.v.p + token * a.v.st + (head / a.v.group) * a.v.sh;
+        float x[4] = {0, 0, 0, 0};
+        if (on) Pack<T, 4>::load(v + c, x);
+        float4 o = make_float4(0, 0, 0, 0);
+#pragma unroll
+        for (int j = 0; j < kRows; ++j) {
+            const int row = group + j * kGroups;
+            if (row >= a.width) continue;
+            const float kr = (float)k[row], qr = (float)q[row];
+            s[j].x = __builtin_fmaf(through, s[j].x, kr * x[0]), s[j].y = __builtin_fmaf(through, s[j].y, kr * x[1]);
+            s[j].z = __builtin_fmaf(through, s[j].z, kr * x[2]), s[j].w = __builtin_fmaf(through, s[j].w, kr * x[3]);
+            o.x = __builtin_fmaf(qr, s[j].x, o.x), o.y = __builtin_fmaf(qr, s[j].y, o.y);
+            o.z = __builtin_fmaf(qr, s[j].z, o.z), o.w = __builtin_fmaf(qr, s[j].w, o.w);
+        }
+        if (step > 0) __syncthreads();
+        parts[group][threadIdx.x % kColumns] = o;
+        __syncthreads();
+        for (int e = threadIdx.x; e < a.width; e += kStepThreads) {
+            float sum = 0.0f;
+#pragma unroll
+            for (int g = 0; g < kGroups; ++g) sum += ((const float*)parts[g])[e];
+            out[token * out_row + e] = (T)(sum * a.enter_by);
+        }
+    }
+    if (!a.last || !on) return;
+#pragma unroll
+    for (int j = 0; j < kRows; ++j) {
+        const int row = group + j * kGroups;
+        if (row < a.width) *(float4*)(a.last + at + row * a.width + c) = s[j];
+    }
+}
+
+// Gradients of shared heads: the query heads' parts, in order, rounded.
+template <typename T>
+__global__ __launch_bounds__(256) void k_decay_share(const float* part, T* out, long long n, int group, int width,
+                                                     unsigned first_block) {
+    const long long i = (((long long)first_block + blockIdx.x) * 256 + threadIdx.x) * 8;
+    if (i >= n) return;
+    const long long head = i / width;  // of all tokens' heads
+    const float* from = part + head * group * width + i % width;
+    float s[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+    for (int g = 0; g < group; ++g) {
+        float x[8];
+        Pack<float, 8>::load(from + (long long)g * width, x);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) s[j] += x[j];
+    }
+    Pack<T, 8>::store(out + i, s);
+}
+
+// ---- host --------------------------------------------------------------------
+
+long long round256(long long n) { return (n + 255) / 256 * 256; }
+int padded(int width) { return width <= 32 ? 32 : width <= 64 ? 64 : 128; }
+
+bool stride_ok(const int64_t s[2]) { return s[0] % 8 == 0 && s[1] % 8 == 0 && s[0] >= 0 && s[1] >= 0; }
+
+bool check(const tok_decay* t) {
+    if (!t || (t->dtype != TOK_BF16 && t->dtype != TOK_F16)) return false;
+    if (t->heads < 1 || t->kv_heads < 1 || t->heads % t->kv_heads || t->heads > 65536) return false;
+    if (t->width < 8 || t->width > 128 || t->width % 8) return false;
+    if (t->t < 0 || t->t > kMaxElems || t->t * t->heads > kMaxElems) return false;
+    if (t->docs < 1 || t->docs > kMaxDocs || (t->docs + 2ll) * t->heads > (1ll << 30)) return false;
+    if ((t->reverse != 0 && t->reverse != 1) || t->reserved || (!t->offsets && t->docs != 1) || !t->decay) return false;
+    if (!(t->scale >= 1e-30f) || !(t->scale <= 1e30f)) return false;
+    return stride_ok(t->q_stride) && stride_ok(t->k_stride) && stride_ok(t->v_stride);
+}
+
+bool by_step(const tok_decay& t) { return t.t <= 2ll * t.docs; }
+
+// Tokens of a segment: as many as leave a block's worth of segments and heads for every
+// place the card has (two blocks of four wavefronts a CU, and as many more as they
+// have fewer), since every segment passes memory with its state four times.
+int segment_of(const tok_decay& t) {
+    if (by_step(t)) return (int)((t.t + 127) / 128 * 128) + 128;  // one: no state is kept in between
+    const long long places = 512ll * 128 / padded(t.width);
+    long long n = (t.t * t.heads + places - 1) / places;
+    n = (n + kChunk - 1) / kChunk * kChunk;
+    if (n < 128) n = 128;
+    if (n > 65536) n = 65536;
+    return (int)n;
+}
+// No document can have a second segment.
+bool whole(const tok_decay& t) { return by_step(t) || t.t <= segment_of(t); }
+
+long long slots(const tok_decay& t) { return t.t / segment_of(t) + t.docs + 2; }
+long long state_elems(const tok_decay& t) { return (long long)t.heads * t.width * t.width; }
+
+Place place(const void* p, const int64_t s[2], int group) { return {p, s[0], s[1], group}; }
+
+DecayArgs make_args(const tok_decay& t) {
+    DecayArgs a = {};
+    a.offsets = t.offsets, a.decay = t.decay;
+    a.t = (int)t.t, a.docs = t.docs, a.heads = t.heads, a.width = t.width;
+    a.segment = segment_of(t);
+    a.segments = (int)slots(t);
+    a.back = t.reverse, a.lag = 1;
+    a.near_by = a.enter_by = t.scale, a.leave_by = 1.0f;
+    return a;
+}
+
+template <typename Launch>
+void in_launches(long long blocks, int threads, Launch launch) {
+    const long long most = most_blocks(threads) / 8 * 8;
+    for (long long b = 0; b < blocks; b += most)
+        launch((unsigned)b, dim3((unsigned)(blocks - b < most ? blocks - b : most)));
+}
+
+template <typename T, int W>
+void sums(DecayArgs a, hipStream_t stream) {
+    in_launches((long long)a.segments * a.heads, 2 * W, [&](unsigned first, dim3 grid) {
+        a.first_block = first;
+        k_decay_sum<T, W><<<grid, dim3(2 * W), 0, stream>>>(a);
+    });
+    const int slices = (a.width * a.width + 1023) / 1024;
+    in_launches((long long)a.docs * a.heads * slices, 256, [&](unsigned first, dim3 grid) {
+        a.first_block = first;
+        k_decay_join<<<grid, dim3(256), 0, stream>>>(a, slices);
+    });
+}
+
+template <typename T, int W, bool WHOLE>
+void walk(DecayArgs a, hipStream_t stream) {
+    in_launches((long long)a.segments * a.heads, 2 * W, [&](unsigned first, dim3 grid) {
+        a.first_block = first;
+        k_decay_run<T, W, WHOLE><<<grid, dim3(2 * W), 0, stream>>>(a);
+    });
+}
+
+template <typename T, int W>
+int forward(const tok_decay& t, DecayArgs a, hipStream_t stream) {
+    if (by_step(t)) {
+        in_launches((a.docs + 2ll) * a.heads, kStepThreads, [&](unsigned first, dim3 grid) {
+            a.first_block = first;
+            k_decay_step<T, W><<<grid, dim3(kStepThreads), 0, stream>>>(a);
+        });
+    } else {
+        if (!whole(t)) sums<T, W>(a, stream);
+        walk<T, W, true>(a, stream);
+    }
+    const hipError_t e = hipGetLastError();
+    return e == hipSuccess ? VOX_OK : ssh_hip_fail(e);
+}
+
+struct Gradients {
+    Place q, k, v, g;
+    const float *state, *grad_last;
+    float *carry, *back_carry, *part;  // part: float32 gradients by query head, or null
+    void *gq, *gk, *gv;
+    float* grad_state;
+    int group;
+};
+
+template <typename T, int W>
+int backward(const tok_decay& t, const DecayArgs& base, const Gradients& g, hipStream_t stream) {
+    DecayArgs a = base;  // grad_q: grad against v and k, along the forward's states
+    a.q = g.g, a.k = g.v, a.v = g.k, a.out = g.gq, a.state = g.state, a.carry = g.carry, a.turned = 1;
+    walk<T, W, false>(a, stream);
+    a = base;  // grad_v, then grad_k, from the other end
+    a.back = !base.back, a.lag = 0, a.enter_by = 1.0f, a.leave_by = base.near_by;
+    a.q = g.k, a.k = g.q, a.v = g.g, a.state = g.grad_last, a.carry = g.back_carry;
+    a.out = g.part ? (void*)g.part : g.gv, a.out_wide = g.part != nullptr, a.last = g.grad_state;
+    if (!whole(t)) sums<T, W>(a, stream);
+    walk<T, W, true>(a, stream);
+    const long long n = (long long)a.t * (a.heads / g.group) * a.width;
+    auto join = [&](void* to) {
+        if (!g.part) return;
+        in_launches((n + 2047) / 2048, 256, [&](unsigned first, dim3 grid) {
+            k_decay_share<T><<<grid, dim3(256), 0, stream>>>(g.part, (T*)to, n, g.group, a.width, first);
+        });
+    };
+    join(g.gv);
+    a.q = g.v, a.k = g.g, a.v = g.q, a.turned = 1, a.last = nullptr;
+    a.out = g.part ? (void*)g.part : g.gk;
+    walk<T, W, false>(a, stream);
+    join(g.gk);
+    const hipError_t e = hipGetLastError();
+    return e == hipSuccess ? VOX_OK : ssh_hip_fail(e);
+}
+
+template <typename T, typename F>
+int by_width(int width, F f) {
+    if (width <= 32) return f(std::integral_constant<int, 32>());
+    if (width <= 64) return f(std::integral_constant<int, 64>());
+    return f(std::integral_constant<int, 128>());
+}
+
+bool aligned16(const void* p) { return ((size_t)p & 15) == 0; }
+
+long long carry_elems(const tok_decay& t) { return whole(t) ? 0 : slots(t) * state_elems(t); }
+long long part_elems(const tok_decay& t) { return t.heads == t.kv_heads ? 0 : t.t * t.heads * t.width; }
+
+}  // namespace
+
+extern "C" {
+
+int64_t tok_decay_carry_rows(const tok_decay* t) {
+    if (!check(t)) return VOX_EINVAL;
+    return whole(*t) ? 0 : slots(*t);
+}
+
+int64_t tok_decay_grad_workspace_bytes(const tok_decay* t) {
+    if (!check(t)) return VOX_EINVAL;
+    return round256(carry_elems(*t) * 4) + round256(part_elems(*t) * 4);
+}
+
+int tok_decay_attend(const tok_decay* t, const void* q, const void* k, const void* v, const float* state, void* out,
+                     float* last_state, float* carry, hipStream_t stream) {
+    if (!check(t)) return VOX_EINVAL;
+    if (t->t && (!q || !k || !v || !out)) return VOX_EINVAL;
+    if (!whole(*t) && !carry) return VOX_EINVAL;
+    const void* all[] = {q, k, v, out, state, last_state, carry};
+    for (const void* p : all)
+        if (!aligned16(p)) return VOX_EINVAL;
+    DecayArgs a = make_args(*t);
+    const int group = t->heads / t->kv_heads;
+    a.q = place(q, t->q_stride, 1), a.k = place(k, t->k_stride, group), a.v = place(v, t->v_stride, group);
+    a.state = state, a.out = out, a.last = last_state, a.carry = carry;
+    return by_width<void>(t->width, [&](auto w) {
+        return t->dtype == TOK_BF16 ? forward<bf16_t, decltype(w)::value>(*t, a, stream)
+                                    : forward<f16_t, decltype(w)::value>(*t, a, stream);
+    });
+}
+
+int tok_decay_attend_grad(const tok_decay* t, const void* q, const void* k, const void* v, const void* grad_out,
+                          const float* state, const float* carry, const float* grad_last, void* grad_q, void* grad_k,
+                          void* grad_v, float* grad_state, void* workspace, int64_t workspace_bytes,
+                          hipStream_t stream) {
+    if (!check(t) || !stride_ok(t->g_stride)) return VOX_EINVAL;
+    if (t->t && (!q || !k || !v || !grad_out || !grad_q || !grad_k || !grad_v)) return VOX_EINVAL;
+    if (!whole(*t) && !carry) return VOX_EINVAL;
+    const void* all[] = {q, k, v, grad_out, state, carry, grad_last, grad_q, grad_k, grad_v, grad_state};
+    for (const void* p : all)
+        if (!aligned16(p)) return VOX_EINVAL;
+    if (!workspace_ok(workspace, workspace_bytes, tok_decay_grad_workspace_bytes(t))) return VOX_EWORKSPACE;
+    const DecayArgs a = make_args(*t);
+    const int group = t->heads / t->kv_heads;
+    Gradients g = {};
+    g.q = place(q, t->q_stride, 1), g.k = place(k, t->k_stride, group), g.v = place(v, t->v_stride, group);
+    g.g = place(grad_out, t->g_stride, 1);
+    g.state = state, g.grad_last = grad_last, g.carry = const_cast<float*>(carry);
+    g.back_carry = (float*)workspace;
+    g.part = group > 1 ? (float*)((char*)workspace + round256(carry_elems(*t) * 4)) : nullptr;
+    g.gq = grad_q, g.gk = grad_k, g.gv = grad_v, g.grad_state = grad_state, g.group = group;
+    return by_width<void>(t->width, [&](auto w) {
+        return t->dtype == TOK_BF16 ? backward<bf16_t, decltype(w)::value>(*t, a, g, stream)
+                                    : backward<f16_t, decltype(w)::value>(*t, a, g, stream);
+    });
+}
+
+}  // extern "C"

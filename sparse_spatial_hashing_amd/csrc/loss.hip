@@ -27,7 +27,7 @@ int ssh_hip_fail(hipError_t e);  // records the error for vox_last_hip_error()
 
 namespace {
 
-constexpr long long kMaxTokens = 1ll << 27;
+constexpr long long kMaxTokens = 1ll << 25;  // a wavefront for each, in one launch
 constexpr long long kMaxRows = (1ll << 31) - 2048;
 constexpr long long kMaxWidth = 65536;
 constexpr long long kMaxStride = 1ll << 22;  // 256 rows apart in 32 bits of bytes
@@ -629,20 +629,20 @@ __global__ __launch_bounds__(S::NT, 2) void k_loss_grad_table(LossArgs a) {
 template <typename T>
 __global__ __launch_bounds__(256) void k_loss_round(LossArgs a, const float* part, int count, long long n,
                                                     long long pitch, T* out) {
-    const long long i = ((long long)blockIdx.x * 256 + threadIdx.x) * 8;
-    if (i >= n) return;
-    float s[8];
-    Pack<float, 8>::load(part + i, s);
-    for (int p = 1; p < count; ++p) {
-        float v[8];
-        Pack<float, 8>::load(part + p * pitch + i, v);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) s[j] += v[j];
-    }
     const float down = ldexpf(a.scale, -lift_of<T>(a));
+    for (long long i = ((long long)blockIdx.x * 256 + threadIdx.x) * 8; i < n; i += 2048ll * gridDim.x) {
+        float s[8];
+        Pack<float, 8>::load(part + i, s);
+        for (int p = 1; p < count; ++p) {
+            float v[8];
+            Pack<float, 8>::load(part + p * pitch + i, v);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) s[j] *= down;
-    Pack<T, 8>::store(out + i, s);
+            for (int j = 0; j < 8; ++j) s[j] += v[j];
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) s[j] *= down;
+        Pack<T, 8>::store(out + i, s);
+    }
 }
 
 // Without a token: every row's gradient is zero.
@@ -801,12 +801,12 @@ int backward(LossArgs a, const Cut& c, hipStream_t stream) {
         a.token_tiles = c.token_tiles;
         if (c.t_splits > 1) {
             const long long there = a.rows - a.row0 < a.piece ? a.rows - a.row0 : a.piece, n = there * a.width;
-            k_loss_round<T><<<dim3((unsigned)ceil_div(n, 2048)), dim3(256), 0, stream>>>(
+            k_loss_round<T><<<dim3(clamp(ceil_div(n, 2048), 1, 1 << 20)), dim3(256), 0, stream>>>(
                 a, a.part_t, c.t_splits, n, (long long)a.piece * a.width, (T*)a.gt + (long long)a.row0 * a.width);
         }
     }
     const long long n = (long long)a.t * a.width;
-    k_loss_round<T><<<dim3((unsigned)ceil_div(n, 2048)), dim3(256), 0, stream>>>(a, a.part_x, c.x_splits, n, n, (T*)a.gx);
+    k_loss_round<T><<<dim3(clamp(ceil_div(n, 2048), 1, 1 << 20)), dim3(256), 0, stream>>>(a, a.part_x, c.x_splits, n, n, (T*)a.gx);
     const hipError_t e = hipGetLastError();
     return e == hipSuccess ? VOX_OK : ssh_hip_fail(e);
 }

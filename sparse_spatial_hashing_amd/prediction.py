@@ -15,12 +15,28 @@ from __future__ import annotations
 
 import ctypes
 import math
+import struct
 from typing import Optional, Tuple
 
 import torch
 
-from .tokens import (_HALF, _call, _check_ids, _floating, _lib, _on_gpu, _ptr, _size, _unseen,
-                     _workspace)
+from .tokens import (_DTYPES, _HALF, _address, _call, _check_ids, _floating, _heads, _lib,
+                     _offsets, _on_gpu, _ptr, _size, _unseen, _workspace)
+
+
+class _Decay(ctypes.Structure):
+    """Mirror of ``tok_decay``."""
+    _fields_ = [("dtype", ctypes.c_int32), ("heads", ctypes.c_int32), ("kv_heads", ctypes.c_int32),
+                ("width", ctypes.c_int32), ("t", ctypes.c_int64), ("docs", ctypes.c_int32),
+                ("reverse", ctypes.c_int32), ("offsets", ctypes.c_void_p), ("decay", ctypes.c_void_p),
+                ("scale", ctypes.c_float), ("reserved", ctypes.c_int32),
+                ("q_stride", ctypes.c_int64 * 2), ("k_stride", ctypes.c_int64 * 2),
+                ("v_stride", ctypes.c_int64 * 2), ("g_stride", ctypes.c_int64 * 2)]
+
+
+# the same layout, packed at once
+_PACK = struct.Struct("@4iq2i2Pfi8q")
+assert _PACK.size == ctypes.sizeof(_Decay)
 
 
 def _declare(lib) -> None:
@@ -28,6 +44,10 @@ def _declare(lib) -> None:
     loss = [vp, i64, vp, i64, i32, i64, i64, i64, vp, i32]
     for name, result, args in (
             ("tok_rotate", i32, [vp] + [i64] * 5 + [i32, vp, i64, i64, i32, vp, i64, i32, i32, vp, vp]),
+            ("tok_decay_carry_rows", i64, [vp]),
+            ("tok_decay_grad_workspace_bytes", i64, [vp]),
+            ("tok_decay_attend", i32, [vp] * 9),
+            ("tok_decay_attend_grad", i32, [vp] * 13 + [i64, vp]),
             ("tok_row_loss_workspace_bytes", i64, [i64] * 3),
             ("tok_row_loss_grad_workspace_bytes", i64, [i64] * 3),
             ("tok_row_loss", i32, loss + [f32, vp, vp, vp, i64, vp]),
@@ -128,6 +148,139 @@ def rotate(x: torch.Tensor, pos: torch.Tensor, freqs: torch.Tensor, *, interleav
     if torch.is_grad_enabled() and isinstance(x, torch.Tensor) and x.requires_grad:
         return _Rotate.apply(x, pos, freqs, bool(interleaved), bool(inverse))
     return _rotate(x, pos, freqs, bool(interleaved), bool(inverse))
+
+
+# -------------------------------------------------------- attention with decay --
+
+def _states(name: str, t: Optional[torch.Tensor], shape, index: int) -> Optional[torch.Tensor]:
+    if t is None:
+        return None
+    _on_gpu(name, t, index)
+    if t.dtype != torch.float32 or t.shape != shape:
+        raise ValueError(f"{name} must be a float32 tensor of shape {shape}")
+    t = t.contiguous()
+    return t.clone() if t.data_ptr() & 15 else t
+
+
+def _decay_args(q, k, v, decay, offsets, scale, reverse, grad=None):
+    """The checked arguments as the C structure, the tensors it points to, the documents, and
+    the states' shape."""
+    q, k, v = _heads("q", q), _heads("k", k, q), _heads("v", v, q)
+    t, heads, width = q.shape
+    kv_heads = k.shape[1]
+    if v.shape != k.shape or k.shape[0] != t or k.shape[2] != width:
+        raise ValueError(f"k and v must be [tokens, heads, width] for q's tokens and width: got {tuple(k.shape)} "
+                         f"and {tuple(v.shape)} for {tuple(q.shape)}")
+    if not 8 <= width <= 128 or width % 8:
+        raise ValueError(f"the head width must be a multiple of 8, at most 128: got {width}")
+    if heads < 1 or kv_heads < 1 or heads % kv_heads:
+        raise ValueError(f"{heads} query heads cannot share {kv_heads} key heads")
+    index = q.get_device()
+    _on_gpu("decay", decay, index)
+    if decay.dtype != torch.float32 or decay.shape != (heads,):
+        raise ValueError(f"decay must be a float32 tensor of shape {(heads,)}")
+    decay, offsets = decay.contiguous(), _offsets("offsets", offsets, index)
+    docs = 1 if offsets is None else offsets.shape[0] - 1
+    scale = width ** -0.5 if scale is None else float(scale)
+    if not 1e-30 <= scale <= 1e30:
+        raise ValueError("scale must be positive: from 1e-30 to 1e30")
+    g_stride = (0, 0)
+    if grad is not None:
+        grad = _heads("grad_out", grad, q)
+        if grad.shape != q.shape:
+            raise ValueError(f"grad_out must have q's shape {tuple(q.shape)}")
+        g_stride = grad.stride()[:2]
+    a = _PACK.pack(_DTYPES[q.dtype], heads, kv_heads, width, t, docs, bool(reverse), _address(offsets),
+                   decay.data_ptr(), scale, 0, *q.stride()[:2], *k.stride()[:2], *v.stride()[:2], *g_stride)
+    return a, (q, k, v, grad, decay, offsets), (docs, heads, width, width)
+
+
+def _decay_attend(q, k, v, decay, offsets, state, scale, reverse, want_state):
+    _unseen("decay_attend", q, k, v, decay, state)
+    a, kept, shape = _decay_args(q, k, v, decay, offsets, scale, reverse)
+    q, k, v = kept[:3]
+    state = _states("state", state, shape, q.get_device())
+    rows = _size(_lib.tok_decay_carry_rows(a), "tok_decay_carry_rows")
+    out = q.new_empty(q.shape)
+    last = q.new_empty(shape, dtype=torch.float32) if want_state else None
+    carry = q.new_empty((rows, *shape[1:]), dtype=torch.float32)
+    _call(_lib.tok_decay_attend, "tok_decay_attend", q.get_device(), a, q.data_ptr(), k.data_ptr(), v.data_ptr(),
+          _ptr(state), out.data_ptr(), _ptr(last), carry.data_ptr())
+    return out, last, carry
+
+
+def decay_attend_grad(grad_out: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
+                      decay: torch.Tensor, carry: torch.Tensor, offsets: Optional[torch.Tensor] = None, *,
+                      state: Optional[torch.Tensor] = None, grad_state: Optional[torch.Tensor] = None,
+                      scale: Optional[float] = None, reverse: bool = False):
+    """Gradients of ``decay_attend``'s q, k, v and initial state (None without one) from
+    those of its output and of the last state (``grad_state``, None: zeros), with the carry
+    it returned and the same other arguments. Gradients of shared key heads are summed over
+    their query heads in float32."""
+    _unseen("decay_attend_grad", grad_out, q, k, v, decay, carry, state, grad_state)
+    a, kept, shape = _decay_args(q, k, v, decay, offsets, scale, reverse, grad_out)
+    q, k, v, g = kept[:4]
+    index = q.get_device()
+    state, grad_state = _states("state", state, shape, index), _states("grad_state", grad_state, shape, index)
+    rows = _size(_lib.tok_decay_carry_rows(a), "tok_decay_carry_rows")
+    carry = _states("carry", carry, (rows, *shape[1:]), index)
+    if carry is None:
+        raise ValueError("carry must be what decay_attend returned")
+    nbytes = _size(_lib.tok_decay_grad_workspace_bytes(a), "tok_decay_grad_workspace_bytes")
+    gq, gk, gv = q.new_empty(q.shape), k.new_empty(k.shape), v.new_empty(v.shape)
+    gs = None if state is None else torch.empty_like(state)
+    ws = _workspace(nbytes, q)
+    _call(_lib.tok_decay_attend_grad, "tok_decay_attend_grad", index, a, q.data_ptr(), k.data_ptr(), v.data_ptr(),
+          g.data_ptr(), _ptr(state), carry.data_ptr(), _ptr(grad_state), gq.data_ptr(), gk.data_ptr(), gv.data_ptr(),
+          _ptr(gs), _ptr(ws), nbytes)
+    return gq, gk, gv, gs
+
+
+class _DecayAttend(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, q, k, v, decay, offsets, state, scale, reverse):
+        out, last, carry = _decay_attend(q, k, v, decay, offsets, state, scale, reverse, True)
+        ctx.save_for_backward(q, k, v, decay, carry, offsets, state)
+        ctx.how = dict(scale=scale, reverse=reverse)
+        ctx.mark_non_differentiable(carry)
+        return out, last, carry
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, grad, grad_last, _):
+        q, k, v, decay, carry, offsets, state = ctx.saved_tensors
+        gq, gk, gv, gs = decay_attend_grad(grad, q, k, v, decay, carry, offsets, state=state, grad_state=grad_last,
+                                           **ctx.how)
+        return gq, gk, gv, None, None, gs, None, None
+
+
+def decay_attend(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, decay: torch.Tensor,
+                 offsets: Optional[torch.Tensor] = None, *, state: Optional[torch.Tensor] = None,
+                 scale: Optional[float] = None, reverse: bool = False, return_state: bool = True,
+                 return_carry: bool = False):
+    """Attention whose weights fall with the distance along a document alone, at a cost
+    that grows with the tokens: ``S = exp(-decay) S + k v^T; out = scale * q S`` per head.
+
+    q [tokens, heads, width], k and v [tokens, kv_heads, width] (bf16 or fp16, heads a
+    multiple of kv_heads, width a multiple of 8 up to 128; layouts as for ``attend``),
+    packed by ``offsets`` (int32 [docs + 1]; None: one document). decay float32 [heads],
+    not negative (0 forgets nothing); scale None: width ** -0.5. ``state`` float32
+    [docs, heads, width, width] (of k's elements by v's) is S before each document's first
+    token (None: zeros). ``reverse`` runs from each document's last token to its first.
+
+    Returns (out [tokens, heads, width], zeros outside every document; the states after each
+    document's last step, or None without ``return_state``), and with ``return_carry`` the
+    saved states that ``decay_attend_grad`` takes. One call with documents of one token
+    each is a step of decoding. Differentiable in q, k, v and state; a decay that requires
+    a gradient is refused unless gradients are off."""
+    if isinstance(decay, torch.Tensor) and decay.requires_grad and torch.is_grad_enabled():
+        raise ValueError("decay is a constant: no gradient is computed for it")
+    if torch.is_grad_enabled() and any(isinstance(t, torch.Tensor) and t.requires_grad for t in (q, k, v, state)):
+        out, last, carry = _DecayAttend.apply(q, k, v, decay, offsets, state, scale, bool(reverse))
+        last = last if return_state else None
+    else:
+        out, last, carry = _decay_attend(q, k, v, decay, offsets, state, scale, bool(reverse), return_state)
+    return (out, last, carry) if return_carry else (out, last)
 
 
 # ------------------------------------------------------------------------ loss --

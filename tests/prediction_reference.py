@@ -74,3 +74,84 @@ def row_loss(x, table, ids, scale, grad=None):
         tol["gt"] = scale * ((b_off + E * (len(came) + 8) * b.abs()).T @ y.abs()) * 1.01 \
             + u * val["gt"].abs() * 1.01 + small
     return {n: (val[n], tol[n]) for n in val}
+
+
+# -------------------------------------------------------- attention with decay --
+
+def decay_attend(q, k, v, decay, at, scale, state=None, reverse=False, grad=None, grad_state=None):
+    """{"out", "last" and with grad "gq", "gk", "gv", "gs"}: (value, bound)."""
+    u = unit(q.dtype)
+    heads, width = q.shape[1:]
+    share, docs = heads // k.shape[1], len(at) - 1
+    shape = (docs, heads, width, width)
+    zeros = torch.zeros(shape, dtype=torch.float64)
+    s0 = zeros if state is None else state.double()
+    val = {"out": torch.zeros(q.shape, dtype=torch.float64), "last": s0.clone()}
+    if grad is not None:
+        b0 = zeros if grad_state is None else grad_state.double()
+        val.update({n: torch.zeros(x.shape, dtype=torch.float64) for n, x in (("gq", q), ("gk", k), ("gv", v))})
+        val["gs"] = b0.clone()
+    tol = {n: torch.zeros_like(x) for n, x in val.items()}
+    for d in range(docs):
+        n = at[d + 1] - at[d]
+        rows = torch.arange(at[d], at[d + 1])
+        if reverse:
+            rows = rows.flip(0)
+        i = torch.arange(n, dtype=torch.float64)
+        for h in range(heads):
+            r, g = float(decay[h]), h // share
+            x, y, z = q[rows, h].double(), k[rows, g].double(), v[rows, g].double()
+            apart = i[:, None] - i[None]
+            w = torch.where(apart >= 0, torch.exp(-r * apart.clamp(min=0)), 0.0)
+            since, until, all_ = torch.exp(-r * (i + 1)), torch.exp(-r * (n - 1 - i)), math.exp(-r * n)
+            # Of a weight: its exponent's roundings, and one for each chunk passed; of a sum: one
+            # for each term and each product of `width`. Weights that small no longer count
+            # are covered by the smallest normal number of the end.
+            slack = E * (4 * r * n * (r * n < 100) + 400 * (r * n >= 100) + 2 * n + 2 * width + 80)
+            # what fp16 drops under the largest of a product's operand: 2^-24 of it
+            drop = 2.0 ** -23 if q.dtype == torch.float16 else 0.0
+
+            def add(name, where, value, size, rel, low=0.0):
+                val[name][where] += value
+                tol[name][where] += size * (rel + slack) * 1.05 + low
+
+            def low(a, b, c):
+                """Dropped bits, where a row of |a| meets sums of |b| by |c| over n tokens or a state."""
+                if not drop or not n:
+                    return 0.0
+                top = lambda t: float(t.abs().max()) if t.numel() else 0.0
+                return 3 * drop * width * top(a) * top(b) * top(c) * float(w.sum(1).max() + 32)
+
+            S, S_abs = s0[d, h], s0[d, h].abs()
+            s_low = drop * width * float(S_abs.max()) if drop else 0.0
+            top = lambda t: float(t.abs().max()) if t.numel() else 0.0
+            add("out", (rows, h), scale * ((w * (x @ y.T)) @ z + since[:, None] * (x @ S)),
+                scale * ((w * (x.abs() @ y.abs().T)) @ z.abs() + since[:, None] * (x.abs() @ S_abs)), 2 * u,
+                scale * (low(x, y, z) + s_low * top(x)))
+            val["last"][d, h] = all_ * S + (until[:, None] * y).T @ z
+            tol["last"][d, h] = (all_ * S_abs + (until[:, None] * y.abs()).T @ z.abs()) * (slack + 8 * E) \
+                + (2.0 ** -24 * top(y) * top(z) * float(until.sum()) if drop else 0.0)
+            if grad is None:
+                continue
+            b = grad[rows, h].double()
+            B, B_abs = b0[d, h], b0[d, h].abs()
+            b_low = drop * width * float(B_abs.max()) if drop else 0.0
+            add("gq", (rows, h), scale * ((w * (b @ z.T)) @ y + since[:, None] * (b @ S.T)),
+                scale * ((w * (b.abs() @ z.abs().T)) @ y.abs() + since[:, None] * (b.abs() @ S_abs.T)), 2 * u,
+                scale * (low(b, z, y) + s_low * top(b)))
+            add("gk", (rows, g), scale * (w * (b @ z.T)).T @ x + until[:, None] * (z @ B.T),
+                scale * (w * (b.abs() @ z.abs().T)).T @ x.abs() + until[:, None] * (z.abs() @ B_abs.T), 2 * u,
+                scale * low(z, b, x) + b_low * top(z))
+            add("gv", (rows, g), scale * (w * (x @ y.T)).T @ b + until[:, None] * (y @ B),
+                scale * (w * (x.abs() @ y.abs().T)).T @ b.abs() + until[:, None] * (y.abs() @ B_abs), 2 * u,
+                scale * low(y, x, b) + b_low * top(y))
+            val["gs"][d, h] = all_ * B + scale * (since[:, None] * x).T @ b
+            tol["gs"][d, h] = (all_ * B_abs + scale * (since[:, None] * x.abs()).T @ b.abs()) * (slack + 8 * E) \
+                + (2.0 ** -24 * scale * top(x) * top(b) * float(since.sum()) if drop else 0.0)
+    small = torch.finfo(q.dtype).smallest_normal
+    for name in tol:
+        if name in ("last", "gs"):
+            tol[name] = tol[name] + torch.finfo(torch.float32).smallest_normal
+        else:
+            tol[name] = tol[name] + u * val[name].abs() * 1.05 + small
+    return {n: (val[n], tol[n]) for n in val}

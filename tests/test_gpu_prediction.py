@@ -111,3 +111,64 @@ def test_row_loss(dtype, width):
 def test_row_loss_odd_widths(width):
     x, table, ids, grad = _loss_case(70, 300, width, BF16, width)
     _loss_compare(x, table, ids, grad, 0.7, f"row_loss width {width}")
+
+
+# -------------------------------------------------------- attention with decay --
+
+def _ends(lens, first=0):
+    return [first] + [first + n for n in itertools.accumulate(lens)]
+
+
+def _at(ends):
+    return torch.tensor(ends, dtype=torch.int32, device=DEV)
+
+
+def _decay_case(lens, heads, kv_heads, width, dtype, seed, first=0, state=True):
+    gen = torch.Generator().manual_seed(seed)
+    at = _ends(lens, first)
+    t = at[-1] + first
+    s = dict(q=_randn((t, heads, width), dtype, gen), k=_randn((t, kv_heads, width), dtype, gen),
+             v=_randn((t, kv_heads, width), dtype, gen),
+             decay=2.0 ** (-1.0 - 9.0 * torch.arange(heads) / heads), grad=_randn((t, heads, width), dtype, gen))
+    s["decay"][-1] = 0.0
+    shape = (len(lens), heads, width, width)
+    s["state"] = torch.randn(shape, generator=gen) * 3.0 if state else None
+    s["grad_state"] = torch.randn(shape, generator=gen) if state else None
+    return s, at
+
+
+def _decay_compare(s, at, what, reverse=False, scale=None):
+    print(what, flush=True)
+    width = s["q"].shape[2]
+    by = width ** -0.5 if scale is None else scale
+    want = ref.decay_attend(s["q"], s["k"], s["v"], s["decay"], at, by, s["state"], reverse, s["grad"], s["grad_state"])
+    g = {n: x.to(DEV) if x is not None else None for n, x in s.items()}
+    more = dict(state=g["state"], scale=scale, reverse=reverse)
+    out, last, carry = ssh.decay_attend(g["q"], g["k"], g["v"], g["decay"], _at(at), return_carry=True, **more)
+    grads = ssh.decay_attend_grad(g["grad"], g["q"], g["k"], g["v"], g["decay"], carry, _at(at),
+                                  grad_state=g["grad_state"], **more)
+    made = dict(zip(("gq", "gk", "gv", "gs"), grads), out=out, last=last)
+    for n, x in made.items():
+        if x is not None:
+            check(x, *want[n], f"{what} {n}")
+    return made
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("reverse", [False, True])
+@pytest.mark.parametrize("width,heads,kv_heads", [(8, 1, 1), (32, 2, 2), (40, 2, 1), (64, 3, 3), (96, 4, 2), (128, 2, 2)])
+def test_decay_attend(dtype, reverse, width, heads, kv_heads):
+    for lens, first, state in (([1, 1, 1], 0, True), ([3, 0, 70, 33, 1], 0, True), ([200], 2, False),
+                               ([31, 32, 64, 5], 3, True), ([0, 0], 1, True)):
+        s, at = _decay_case(lens, heads, kv_heads, width, dtype, width + len(lens), first, state)
+        _decay_compare(s, at, f"decay {dtype} {lens} first {first} width {width} heads {heads}/{kv_heads}", reverse)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("width,heads,kv_heads,lens", [(128, 2, 1, [700, 1500, 128]), (64, 2, 2, [1, 2100, 129, 0, 256]),
+                                                       (32, 4, 2, [3000])])
+def test_decay_attend_segments(dtype, width, heads, kv_heads, lens):
+    """Documents of several segments, whole ones and ends."""
+    s, at = _decay_case(lens, heads, kv_heads, width, dtype, 7, 1)
+    _decay_compare(s, at, f"decay segments {dtype} {lens} width {width}")
+    _decay_compare(s, at, f"decay segments reverse {dtype} {lens} width {width}", True, 0.3)
