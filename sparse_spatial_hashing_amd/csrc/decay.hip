@@ -46,22 +46,28 @@ struct Place {
     int group;         // query heads that share one of its heads
 };
 
-struct DecayArgs {
+// A walk along the documents: which tensors are in which places, and from which end.
+struct Walk {
     Place q, k, v;
-    void* out;            // [t, out heads, width]; float32 with out_wide
-    const int* offsets;
-    const float* decay;
+    void* out;            // [t, heads, width]; float32 with out_wide
     const float* state;   // [docs, heads, width, width] or null
     float* last;          // or null
     float* carry;         // [segments, heads, width, width]: sums, then the states that enter
-    int t, docs, heads, width;
-    int segment;          // tokens: a multiple of kChunk
-    int segments;
-    int back;             // walks from a document's last token
+    int back;             // from a document's last token
     int turned;           // states are read transposed
     int lag;              // 1: a state counts one token on; 0: it is that of the token itself
     int out_wide;
     float near_by, enter_by, leave_by;  // of tokens of a chunk, of the state, of what enters it
+};
+
+struct DecayArgs {
+    Walk walk[3];
+    int walks;
+    const int* offsets;
+    const float* decay;
+    int t, docs, heads, width;
+    int segment;          // tokens: a multiple of kChunk
+    int segments;
     unsigned first_block;
 };
 
@@ -79,6 +85,7 @@ struct Part {
 __device__ __forceinline__ Part find_part(const DecayArgs& a, int slot) {
     int lo = 0, n = a.docs + 2, first = 0;
     const int lane = __lane_id();
+    if (a.segment >= a.t) lo = first = slot, n = 1;  // one segment a range: nothing to search
     while (n > 1) {
         const int step = (n + kWave - 1) / kWave;
         const int b = lo + lane * step;
@@ -118,6 +125,9 @@ struct Decay {
     static constexpr int kPieces = W / 8;           // of 16 bytes in a row
     static constexpr int kTile = kChunk * W * 2;    // bytes
     static constexpr int kBlocks = W / 32;
+    // Chunks in LDS at once: at the smallest width, one less lets three wavefronts share a
+    // SIMD.
+    static constexpr int kBuffers = W == 32 ? 2 : 3;
     static constexpr bool kHalf = __is_same(T, f16_t);
 
     static __device__ __forceinline__ int swz(int row) {
@@ -128,22 +138,37 @@ struct Decay {
     // bits 2 and 3 traded
     static __device__ __forceinline__ int traded(int x) { return (x & ~12) | ((x & 4) << 1) | ((x & 8) >> 1); }
 
-    // A chunk's rows of one tensor to LDS; zeros past its end and the width.
-    static __device__ __forceinline__ void load(unsigned to, const Place& p, int head, const DecayArgs& a,
-                                                const Part& d, int at) {
-        const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-        const T* base = (const T*)p.p + (long long)(head / p.group) * p.sh;
-        const int left = d.to - at;
-        const int first = a.back ? d.lo + d.n - 1 - at : d.lo + at;
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int n = i * NT + threadIdx.x, row = n / kPieces, c = (n % kPieces) ^ swz(row);
-            const int token = a.back ? first - row : first + row;
-            const bool there = row < left && 8 * c < a.width;
-            const void* from = there ? (const void*)(base + (long long)token * p.st + 8 * c) : &kNothing;
-            load_to_lds(to + 1024u * wave + 16u * NT * i, from);
+    // The rows of one tensor, chunk by chunk, to LDS.
+    struct Rows {
+        const T* base;     // the segment's first row in the walk's order
+        long long step;    // to the next row
+        unsigned offset;   // of this lane's piece, in a whole chunk: from its lowest address on
+
+        __device__ __forceinline__ Rows(const Place& p, int head, const Walk& w, const Part& d) {
+            const int first = w.back ? d.lo + d.n - 1 - d.from : d.lo + d.from;
+            base = (const T*)p.p + (long long)(head / p.group) * p.sh + first * p.st;
+            step = w.back ? -p.st : p.st;
+            const int row = threadIdx.x / kPieces, c = (threadIdx.x % kPieces) ^ swz(row);
+            offset = (unsigned)(w.back ? kChunk / 2 - 1 - row : row) * (unsigned)(2 * p.st) + 16u * c;
         }
-    }
+        // Chunk c of `left` rows from there on; zeros past its end and the width.
+        __device__ __forceinline__ void load(unsigned to, int chunk, int left, int width) const {
+            const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+            const T* from = base + (long long)chunk * kChunk * step;
+            if (left >= kChunk && width == W) {
+                const T* low = step < 0 ? from + (kChunk / 2 - 1) * step : from;
+                load_to_lds(to + 1024u * wave, low, offset);
+                load_to_lds(to + 1024u * wave + 16u * NT, low + kChunk / 2 * step, offset);
+                return;
+            }
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int n = i * NT + threadIdx.x, row = n / kPieces, c = (n % kPieces) ^ swz(row);
+                const bool there = row < left && 8 * c < width;
+                load_to_lds(to + 1024u * wave + 16u * NT * i, there ? (const void*)(from + row * step + 8 * c) : &kNothing);
+            }
+        }
+    };
     // Operand of a product over the width: row number `row`, step s of 16.
     static __device__ __forceinline__ unsigned row_place(int row, int half) {
         return row * 2 * W + ((half ^ swz(row)) << 4);
@@ -214,29 +239,30 @@ struct Decay {
 
     // What v's rows are multiplied with on their way into the state: e^-r(m - lag - j)
     // (1 for rows that are not there), and leave_by.
-    static __device__ __forceinline__ void leaving(float (&w)[16], const DecayArgs& a, float rate, int m, int half) {
+    static __device__ __forceinline__ void leaving(float (&w)[16], const Walk& a, float rate, int m, int half) {
 #pragma unroll
         for (int r = 0; r < 16; ++r)
             w[r] = fall(rate, max(0, m - a.lag - (16 * (r / 8) + 8 * half + r % 8))) * a.leave_by;
     }
 
-    // S <- through S + K^T (w V) over a chunk in LDS. w V in one rounding, or (WHOLE) in
-    // as many parts as hold 22 bits or more of it: 2 of fp16, 3 of bf16.
-    template <bool WHOLE>
-    static __device__ __forceinline__ void advance(State& s, uint2 k_at, const vec8 (&v)[2], const float (&w)[16],
-                                                   float through) {
-        constexpr int kParts = !WHOLE ? 1 : kHalf ? 2 : 3;
+    // S <- S + by K^T (w V) over a chunk in LDS, w V in as many parts as hold 22 bits or
+    // more of it: 2 of fp16, 3 of bf16.
+    static __device__ __forceinline__ void advance(State& s, uint2 k_at, const vec8 (&v)[2], const float (&w)[16], float by) {
+        constexpr int kParts = kHalf ? 2 : 3;
         float x[16];
 #pragma unroll
         for (int r = 0; r < 16; ++r) x[r] = (float)v[r / 8][r % 8] * w[r];
-        float up = 1.0f;
         if (kHalf) {
             float top = 0.0f;
 #pragma unroll
             for (int r = 0; r < 16; ++r) top = fmaxf(top, fabsf(x[r]));
-            up = to_one(wave_max(top));
+            const float up = to_one(wave_max(top));
 #pragma unroll
             for (int r = 0; r < 16; ++r) x[r] *= up;
+            by /= up;
+        } else {
+#pragma unroll
+            for (int r = 0; r < 16; ++r) x[r] *= by;
         }
         vec8 y[kParts][2];
 #pragma unroll
@@ -248,41 +274,66 @@ struct Decay {
             }
 #pragma unroll
         for (int b = 0; b < kBlocks; ++b) {
-            acc16 add = kHalf ? zero16() : s[b];
-            if (!kHalf)
-#pragma unroll
-                for (int r = 0; r < 16; ++r) add[r] *= through;
+            acc16 add = zero16();
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
                 const vec8 k = read_column(k_at, b, c);
 #pragma unroll
-                for (int part = kParts - 1; part >= 0; --part) add = Mma<T>::mul(k, y[part][c], add);
+                for (int part = kParts - 1; part >= 0; --part) {
+                    if (kHalf)
+                        add = Mma<T>::mul(k, y[part][c], add);
+                    else
+                        s[b] = Mma<T>::mul(k, y[part][c], s[b]);
+                }
             }
-            if (kHalf) {
-                const float down = 1.0f / up;
+            if (kHalf)
 #pragma unroll
-                for (int r = 0; r < 16; ++r) s[b][r] = __builtin_fmaf(add[r], down, s[b][r] * through);
-            } else {
-                s[b] = add;
-            }
+                for (int r = 0; r < 16; ++r) s[b][r] = __builtin_fmaf(add[r], by, s[b][r]);
         }
     }
+
+    // The state that is kept falls by e^-rm with every chunk. That is applied to its
+    // registers only when it comes to 2^-kFall; until then what enters is taken that much
+    // larger. (Each further power of two would cost the state a 2^-24 of its precision.)
+    struct Fall {
+        static constexpr float kFall = 8.0f;
+        int tokens = 0;  // since then
+        // What the registers are to be multiplied with.
+        __device__ __forceinline__ float now(float rate) const { return fall(rate, tokens); }
+        // A chunk of m tokens passes; the factor for what enters after it.
+        __device__ __forceinline__ float pass(State& s, float rate, int m, bool apply) {
+            tokens += m;
+            const float exponent = rate * (float)tokens;
+            if (!apply && exponent <= kFall) return __builtin_amdgcn_exp2f(exponent);
+            const float by = __builtin_amdgcn_exp2f(-exponent);
+#pragma unroll
+            for (int b = 0; b < kBlocks; ++b)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) s[b][r] *= by;
+            tokens = 0;
+            return 1.0f;
+        }
+    };
 };
 
-// The segment and head of a block.
-__device__ __forceinline__ int block_of(const DecayArgs& a, int* head) {
-    const unsigned id = a.first_block + xcd_block(blockIdx.x, gridDim.x);
+// The segment, head and walk of a block: walks of one part of a document run together,
+// since they read the same tensors.
+__device__ __forceinline__ int block_of(const DecayArgs& a, int* head, int* walk) {
+    unsigned id = a.first_block + xcd_block(blockIdx.x, gridDim.x);
+    *walk = id % a.walks;
+    id /= a.walks;
     *head = id % a.heads;
     return id / a.heads;
 }
 
 // What a segment adds to the state that enters it; nothing needs a document's last.
 template <typename T, int W>
-__global__ __launch_bounds__(2 * W) void k_decay_sum(DecayArgs a) {
+__global__ __launch_bounds__(2 * W, 2) void k_decay_sum(DecayArgs a) {
     typedef Decay<T, W> D;
-    __shared__ __align__(1024) char lds[3 * 2 * D::kTile];
-    int head;
-    const int slot = block_of(a, &head);
+    __shared__ __align__(1024) char lds[D::kBuffers * 2 * D::kTile];
+    int head, role;
+    const int slot = block_of(a, &head, &role);
+    const Walk& walk = a.walk[0];
     const Part d = find_part(a, slot);
     if (d.none || d.doc < 0 || d.last) return;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, half = lane >> 5;
@@ -290,36 +341,38 @@ __global__ __launch_bounds__(2 * W) void k_decay_sum(DecayArgs a) {
     const unsigned base = lds_address(lds);
     const int chunks = a.segment / kChunk;  // whole: a document goes on after it
     float w[16];
-    D::leaving(w, a, rate, kChunk, half);
-    const float through = fall(rate, kChunk);
+    D::leaving(w, walk, rate, kChunk, half);
     const uint2 k_in = D::template column_place<true>(lane), v_in = D::template column_place<false>(lane);
     typename D::State s;
 #pragma unroll
     for (int b = 0; b < D::kBlocks; ++b) s[b] = zero16();
+    typename D::Fall fallen;
+    const typename D::Rows k(walk.k, head, walk, d), v(walk.v, head, walk, d);
     auto issue = [&](int c, int buf) {
         const unsigned to = base + buf * 2 * D::kTile;
-        D::load(to, a.k, head, a, d, d.from + c * kChunk);
-        D::load(to + D::kTile, a.v, head, a, d, d.from + c * kChunk);
+        k.load(to, c, kChunk, a.width);
+        v.load(to + D::kTile, c, kChunk, a.width);
     };
     issue(0, 0);
-    if (chunks > 1) issue(1, 1);
+    if (D::kBuffers > 2 && chunks > 1) issue(1, 1);
     int buf = 0;
     for (int c = 0; c < chunks; ++c) {
-        if (c + 1 < chunks)
+        if (D::kBuffers > 2 && c + 1 < chunks)
             load_wait<4>();
         else
             load_wait<0>();
         __syncthreads();
-        if (c + 2 < chunks) issue(c + 2, buf == 0 ? 2 : buf - 1);
+        if (c + D::kBuffers - 1 < chunks) issue(c + D::kBuffers - 1, buf == 0 ? D::kBuffers - 1 : buf - 1);
         const unsigned on = base + buf * 2 * D::kTile;
-        typename D::vec8 v[2];
+        typename D::vec8 x[2];
 #pragma unroll
         for (int i = 0; i < 2; ++i)
-            v[i] = D::read_column(make_uint2(v_in.x + on + D::kTile, v_in.y + on + D::kTile), wave, i);
-        D::template advance<true>(s, make_uint2(k_in.x + on, k_in.y + on), v, w, through);
-        buf = buf == 2 ? 0 : buf + 1;
+            x[i] = D::read_column(make_uint2(v_in.x + on + D::kTile, v_in.y + on + D::kTile), wave, i);
+        const float by = fallen.pass(s, rate, kChunk, c + 1 == chunks);
+        D::advance(s, make_uint2(k_in.x + on, k_in.y + on), x, w, by);
+        buf = buf == D::kBuffers - 1 ? 0 : buf + 1;
     }
-    D::store_state(s, a.carry + ((long long)slot * a.heads + head) * a.width * a.width, a.width,
+    D::store_state(s, walk.carry + ((long long)slot * a.heads + head) * a.width * a.width, a.width,
                    32 * wave + (lane & 31), half);
 }
 
@@ -337,11 +390,12 @@ __global__ __launch_bounds__(256) void k_decay_join(DecayArgs a, int slices) {
     const int size = a.width * a.width, at = (slice * 256 + (int)threadIdx.x) * 4;
     if (at >= size) return;
     const long long pitch = (long long)a.heads * size;
-    float* sum = a.carry + (long long)(lo / a.segment + doc + 1) * pitch + (long long)head * size + at;
+    const Walk& walk = a.walk[0];
+    float* sum = walk.carry + (long long)(lo / a.segment + doc + 1) * pitch + (long long)head * size + at;
     const float through = fall(rate_of(a, head), a.segment);
     float4 h = make_float4(0, 0, 0, 0);
-    if (a.state) {
-        const float* from = a.state + (long long)doc * pitch + (long long)head * size;
+    if (walk.state) {
+        const float* from = walk.state + (long long)doc * pitch + (long long)head * size;
         h = *(const float4*)(from + at);
     }
     constexpr int kAhead = 8;
@@ -358,25 +412,27 @@ __global__ __launch_bounds__(256) void k_decay_join(DecayArgs a, int slices) {
     }
 }
 
-// A segment from the state that enters it. WHOLE: its states are a result too.
-template <typename T, int W, bool WHOLE>
-__global__ __launch_bounds__(2 * W, 2) void k_decay_run(DecayArgs a) {
+// A segment from the state that enters it.
+template <typename T, int W>
+__global__ __launch_bounds__(2 * W, W == 32 ? 3 : 2) void k_decay_run(DecayArgs a) {
     typedef Decay<T, W> D;
-    __shared__ __align__(1024) char lds[3 * 3 * D::kTile];
-    int head;
-    const int slot = block_of(a, &head);
+    __shared__ __align__(1024) char lds[D::kBuffers * 3 * D::kTile];
+    int head, role;
+    const int slot = block_of(a, &head, &role);
+    const Walk& walk = a.walk[role];
     const Part d = find_part(a, slot);
     if (d.none) return;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, half = lane >> 5, i = lane & 31;
     const long long out_row = (long long)a.heads * a.width;
+    const bool out_wide = walk.out_wide;
     if (d.doc < 0) {  // tokens of no document
         for (int s = d.from; s < d.to; ++s)
             for (int c = threadIdx.x; c < a.width; c += D::NT) {
                 const long long at = (d.lo + s) * out_row + head * a.width + c;
-                if (a.out_wide)
-                    ((float*)a.out)[at] = 0.0f;
+                if (out_wide)
+                    ((float*)walk.out)[at] = 0.0f;
                 else
-                    ((T*)a.out)[at] = (T)0.0f;
+                    ((T*)walk.out)[at] = (T)0.0f;
             }
         return;
     }
@@ -385,34 +441,36 @@ __global__ __launch_bounds__(2 * W, 2) void k_decay_run(DecayArgs a) {
     const float rate = rate_of(a, head);
     const unsigned base = lds_address(lds);
     const int chunks = (d.to - d.from + kChunk - 1) / kChunk;
+    const typename D::Rows q_rows(walk.q, head, walk, d), k_rows(walk.k, head, walk, d), v_rows(walk.v, head, walk, d);
     auto issue = [&](int c, int buf) {
         const unsigned to = base + buf * 3 * D::kTile;
-        D::load(to, a.q, head, a, d, d.from + c * kChunk);
-        D::load(to + D::kTile, a.k, head, a, d, d.from + c * kChunk);
-        D::load(to + 2 * D::kTile, a.v, head, a, d, d.from + c * kChunk);
+        const int left = d.to - d.from - c * kChunk;
+        q_rows.load(to, c, left, a.width);
+        k_rows.load(to + D::kTile, c, left, a.width);
+        v_rows.load(to + 2 * D::kTile, c, left, a.width);
     };
+    if (chunks > 0) issue(0, 0);
+    if (D::kBuffers > 2 && chunks > 1) issue(1, 1);
     typename D::State s;
     {
-        const float* from = d.from > 0 ? a.carry + ((long long)slot * a.heads + head) * size
-                            : a.state  ? a.state + ((long long)d.doc * a.heads + head) * size
-                                       : nullptr;
-        D::load_state(s, from, a.width, a.turned, column, half);
+        const float* from = d.from > 0   ? walk.carry + ((long long)slot * a.heads + head) * size
+                            : walk.state ? walk.state + ((long long)d.doc * a.heads + head) * size
+                                         : nullptr;
+        D::load_state(s, from, a.width, walk.turned, column, half);
     }
     // settled here: inside the loop their wait would be for the tiles under way as well
 #pragma unroll
     for (int b = 0; b < D::kBlocks; ++b) asm volatile("" : "+v"(s[b]));
-    if (chunks > 0) issue(0, 0);
-    if (chunks > 1) issue(1, 1);
 
     float w[16], near[16];
-    D::leaving(w, a, rate, kChunk, half);
+    D::leaving(w, walk, rate, kChunk, half);
 #pragma unroll
     for (int r = 0; r < 16; ++r) {
         const int key = 16 * (r / 8) + 8 * half + r % 8;
-        near[r] = fall(rate, max(0, i - key)) * a.near_by;
+        near[r] = fall(rate, max(0, i - key)) * walk.near_by;
     }
-    const float entering = fall(rate, i + a.lag) * a.enter_by;
-    float through = fall(rate, kChunk);
+    const float entering = fall(rate, i + walk.lag) * walk.enter_by;
+    typename D::Fall fallen;
     const unsigned q_in = D::row_place(i, half), k_in = D::row_place(D::traded(i), half);
     const uint2 kc_in = D::template column_place<true>(lane), vc_in = D::template column_place<false>(lane);
 
@@ -421,14 +479,14 @@ __global__ __launch_bounds__(2 * W, 2) void k_decay_run(DecayArgs a) {
     auto store = [&](int c) {
         const int at = d.from + c * kChunk + i;
         if (at >= d.to) return;
-        const long long token = a.back ? d.lo + d.n - 1 - at : d.lo + at;
+        const long long token = walk.back ? d.lo + d.n - 1 - at : d.lo + at;
         const long long row = token * out_row + head * a.width;
-        if (a.out_wide) {
+        if (out_wide) {
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
                 const int col = 32 * wave + 8 * q + 4 * half;
                 if (col < a.width)
-                    *(float4*)((float*)a.out + row + col) =
+                    *(float4*)((float*)walk.out + row + col) =
                         make_float4(wide[4 * q], wide[4 * q + 1], wide[4 * q + 2], wide[4 * q + 3]);
             }
             return;
@@ -436,19 +494,19 @@ __global__ __launch_bounds__(2 * W, 2) void k_decay_run(DecayArgs a) {
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
             const int col = 32 * wave + 8 * (2 * q + half);
-            if (col < a.width) *(uint4*)((T*)a.out + row + col) = made[q];
+            if (col < a.width) *(uint4*)((T*)walk.out + row + col) = made[q];
         }
     };
 
     int buf = 0;
     for (int c = 0; c < chunks; ++c) {
-        if (c + 1 < chunks)
+        if (D::kBuffers > 2 && c + 1 < chunks)
             load_wait<6>();
         else
             load_wait<0>();
         __syncthreads();  // this chunk is there, and all are done with the one before
         if (c > 0) store(c - 1);
-        if (c + 2 < chunks) issue(c + 2, buf == 0 ? 2 : buf - 1);
+        if (c + D::kBuffers - 1 < chunks) issue(c + D::kBuffers - 1, buf == 0 ? D::kBuffers - 1 : buf - 1);
         const int m = min(kChunk, d.to - d.from - c * kChunk);
         const unsigned on = base + buf * 3 * D::kTile;
         const unsigned q_at = q_in + on, k_at = k_in + on + D::kTile;
@@ -483,7 +541,7 @@ __global__ __launch_bounds__(2 * W, 2) void k_decay_run(DecayArgs a) {
 #pragma unroll
             for (int r = 0; r < 16; ++r) p[r] *= up_p;
         }
-        const float in = D::kHalf ? entering * (up_p / up_s) : entering;
+        const float in = entering * fallen.now(rate) * (D::kHalf ? up_p / up_s : 1.0f);
 #pragma unroll
         for (int r = 0; r < 16; ++r) o[r] *= in;
         typename D::vec8 v[2];
@@ -498,7 +556,7 @@ __global__ __launch_bounds__(2 * W, 2) void k_decay_run(DecayArgs a) {
         const float out_by = D::kHalf ? 1.0f / up_p : 1.0f;
 #pragma unroll
         for (int r = 0; r < 16; ++r) wide[r] = o[r] * out_by;
-        if (!a.out_wide) {
+        if (!out_wide) {
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
                 unsigned x0 = Mma<T>::pair(wide[8 * q], wide[8 * q + 1]), x1 = Mma<T>::pair(wide[8 * q + 2], wide[8 * q + 3]);
@@ -508,16 +566,15 @@ __global__ __launch_bounds__(2 * W, 2) void k_decay_run(DecayArgs a) {
                 made[q] = make_uint4(x0, x1, y0, y1);
             }
         }
-        if (m < kChunk) {
-            D::leaving(w, a, rate, m, half);
-            through = fall(rate, m);
+        if (m < kChunk) D::leaving(w, walk, rate, m, half);
+        if (c + 1 < chunks || walk.last) {
+            const float by = fallen.pass(s, rate, m, c + 1 == chunks);
+            D::advance(s, make_uint2(kc_in.x + on + D::kTile, kc_in.y + on + D::kTile), v, w, by);
         }
-        if (c + 1 < chunks || a.last)
-            D::template advance<WHOLE>(s, make_uint2(kc_in.x + on + D::kTile, kc_in.y + on + D::kTile), v, w, through);
-        buf = buf == 2 ? 0 : buf + 1;
+        buf = buf == D::kBuffers - 1 ? 0 : buf + 1;
     }
     if (chunks > 0) store(chunks - 1);
-    if (d.last && a.last) D::store_state(s, a.last + ((long long)d.doc * a.heads + head) * size, a.width, column, half);
+    if (d.last && walk.last) D::store_state(s, walk.last + ((long long)d.doc * a.heads + head) * size, a.width, column, half);
 }
 
 // Documents of one token or two: a block per document and head holds the state and
@@ -529,12 +586,13 @@ template <typename T, int W>
 __global__ __launch_bounds__(kStepThreads) void k_decay_step(DecayArgs a) {
     constexpr int kColumns = W / 4, kGroups = kStepThreads / kColumns, kRows = (W + kGroups - 1) / kGroups;
     __shared__ float4 parts[kGroups][kColumns];
+    const Walk& walk = a.walk[0];
     const unsigned id = a.first_block + blockIdx.x;
     const int head = id % a.heads, range = id / a.heads;  // 0 and docs + 1: of no document
     const int lo = tok_boundary(a.offsets, a.docs, a.t, range);
     const int n = max(0, tok_boundary(a.offsets, a.docs, a.t, range + 1) - lo);
     const long long out_row = (long long)a.heads * a.width;
-    T* out = (T*)a.out + head * a.width;
+    T* out = (T*)walk.out + head * a.width;
     if (range < 1 || range > a.docs) {
         for (int s = 0; s < n; ++s)
             for (int c = threadIdx.x; c < a.width; c += kStepThreads) out[(lo + s) * out_row + c] = (T)0.0f;
@@ -548,13 +606,13 @@ __global__ __launch_bounds__(kStepThreads) void k_decay_step(DecayArgs a) {
 #pragma unroll
     for (int j = 0; j < kRows; ++j) {
         const int row = group + j * kGroups;
-        s[j] = a.state && on && row < a.width ? *(const float4*)(a.state + at + row * a.width + c) : make_float4(0, 0, 0, 0);
+        s[j] = walk.state && on && row < a.width ? *(const float4*)(walk.state + at + row * a.width + c) : make_float4(0, 0, 0, 0);
     }
     for (int step = 0; step < n; ++step) {
-        const long long token = a.back ? lo + n - 1 - step : lo + step;
-        const T* q = (const T*)a.q.p + token * a.q.st + head * a.q.sh;
-        const T* k = (const T*)a.k.p + token * a.k.st + (head / a.k.group) * a.k.sh;
-        const T* v = (const T*)a.v.p + token * a.v.st + (head / a.v.group) * a.v.sh;
+        const long long token = walk.back ? lo + n - 1 - step : lo + step;
+        const T* q = (const T*)walk.q.p + token * walk.q.st + head * walk.q.sh;
+        const T* k = (const T*)walk.k.p + token * walk.k.st + (head / walk.k.group) * walk.k.sh;
+        const T* v = (const T*)walk.v.p + token * walk.v.st + (head / walk.v.group) * walk.v.sh;
         float x[4] = {0, 0, 0, 0};
         if (on) Pack<T, 4>::load(v + c, x);
         float4 o = make_float4(0, 0, 0, 0);
@@ -575,25 +633,26 @@ __global__ __launch_bounds__(kStepThreads) void k_decay_step(DecayArgs a) {
             float sum = 0.0f;
 #pragma unroll
             for (int g = 0; g < kGroups; ++g) sum += ((const float*)parts[g])[e];
-            out[token * out_row + e] = (T)(sum * a.enter_by);
+            out[token * out_row + e] = (T)(sum * walk.enter_by);
         }
     }
-    if (!a.last || !on) return;
+    if (!walk.last || !on) return;
 #pragma unroll
     for (int j = 0; j < kRows; ++j) {
         const int row = group + j * kGroups;
-        if (row < a.width) *(float4*)(a.last + at + row * a.width + c) = s[j];
+        if (row < a.width) *(float4*)(walk.last + at + row * a.width + c) = s[j];
     }
 }
 
-// Gradients of shared heads: the query heads' parts, in order, rounded.
+// Gradients of shared heads: the query heads' parts, in order, rounded. Of two tensors,
+// the second's parts behind the first's.
 template <typename T>
-__global__ __launch_bounds__(256) void k_decay_share(const float* part, T* out, long long n, int group, int width,
-                                                     unsigned first_block) {
+__global__ __launch_bounds__(256) void k_decay_share(const float* part, T* out0, T* out1, long long n, int group,
+                                                     int width, unsigned first_block) {
     const long long i = (((long long)first_block + blockIdx.x) * 256 + threadIdx.x) * 8;
-    if (i >= n) return;
-    const long long head = i / width;  // of all tokens' heads
-    const float* from = part + head * group * width + i % width;
+    if (i >= 2 * n) return;
+    const long long at = i < n ? i : i - n;
+    const float* from = part + (i < n ? 0 : n * group) + at / width * group * width + at % width;
     float s[8] = {0, 0, 0, 0, 0, 0, 0, 0};
     for (int g = 0; g < group; ++g) {
         float x[8];
@@ -601,7 +660,7 @@ __global__ __launch_bounds__(256) void k_decay_share(const float* part, T* out, 
 #pragma unroll
         for (int j = 0; j < 8; ++j) s[j] += x[j];
     }
-    Pack<T, 8>::store(out + i, s);
+    Pack<T, 8>::store((i < n ? out0 : out1) + at, s);
 }
 
 // ---- host --------------------------------------------------------------------
@@ -623,21 +682,29 @@ bool check(const tok_decay* t) {
 }
 
 bool by_step(const tok_decay& t) { return t.t <= 2ll * t.docs; }
+// Short documents that fill the card with one block each (and head): no segments, which
+// saves two launches of sums. (At worst one document holds all 16,384 tokens.)
+bool by_doc(const tok_decay& t) { return t.t <= 64ll * t.docs && t.t <= 16384 && (long long)t.docs * t.heads >= 512; }
 
-// Tokens of a segment: as many as leave a block's worth of segments and heads for every
-// place the card has (two blocks of four wavefronts a CU, and as many more as they
-// have fewer), since every segment passes memory with its state four times.
+// Tokens of a segment: as many as leave a block for every place the card has (two blocks of
+// four wavefronts a CU, and as many more as they have fewer) and none for a second round,
+// counting the segments that documents' ends and the tokens of none may add; every
+// segment passes memory with its state four times. 122,880 tokens of 8 heads of 128: 536
+// blocks take 320 us, 512 take 234.
 int segment_of(const tok_decay& t) {
-    if (by_step(t)) return (int)((t.t + 127) / 128 * 128) + 128;  // one: no state is kept in between
-    const long long places = 512ll * 128 / padded(t.width);
-    long long n = (t.t * t.heads + places - 1) / places;
+    if (by_step(t) || by_doc(t)) return (int)((t.t + 127) / 128 * 128) + 128;  // one
+    const long long each = 512ll * 128 / padded(t.width) / t.heads;  // of a head
+    long long n = each - t.docs - 2;
+    if (n < each / 2) n = each / 2;
+    if (n < 1) n = 1;
+    n = (t.t + n - 1) / n;
     n = (n + kChunk - 1) / kChunk * kChunk;
     if (n < 128) n = 128;
     if (n > 65536) n = 65536;
     return (int)n;
 }
 // No document can have a second segment.
-bool whole(const tok_decay& t) { return by_step(t) || t.t <= segment_of(t); }
+bool whole(const tok_decay& t) { return t.t <= segment_of(t); }
 
 long long slots(const tok_decay& t) { return t.t / segment_of(t) + t.docs + 2; }
 long long state_elems(const tok_decay& t) { return (long long)t.heads * t.width * t.width; }
@@ -650,8 +717,9 @@ DecayArgs make_args(const tok_decay& t) {
     a.t = (int)t.t, a.docs = t.docs, a.heads = t.heads, a.width = t.width;
     a.segment = segment_of(t);
     a.segments = (int)slots(t);
-    a.back = t.reverse, a.lag = 1;
-    a.near_by = a.enter_by = t.scale, a.leave_by = 1.0f;
+    a.walks = 1;
+    a.walk[0].back = t.reverse, a.walk[0].lag = 1;
+    a.walk[0].near_by = a.walk[0].enter_by = t.scale, a.walk[0].leave_by = 1.0f;
     return a;
 }
 
@@ -662,8 +730,10 @@ void in_launches(long long blocks, int threads, Launch launch) {
         launch((unsigned)b, dim3((unsigned)(blocks - b < most ? blocks - b : most)));
 }
 
+// The states that enter the segments of walk 0.
 template <typename T, int W>
-void sums(DecayArgs a, hipStream_t stream) {
+void states(DecayArgs a, hipStream_t stream) {
+    a.walks = 1;
     in_launches((long long)a.segments * a.heads, 2 * W, [&](unsigned first, dim3 grid) {
         a.first_block = first;
         k_decay_sum<T, W><<<grid, dim3(2 * W), 0, stream>>>(a);
@@ -675,11 +745,11 @@ void sums(DecayArgs a, hipStream_t stream) {
     });
 }
 
-template <typename T, int W, bool WHOLE>
-void walk(DecayArgs a, hipStream_t stream) {
-    in_launches((long long)a.segments * a.heads, 2 * W, [&](unsigned first, dim3 grid) {
+template <typename T, int W>
+void run(DecayArgs a, hipStream_t stream) {
+    in_launches((long long)a.segments * a.heads * a.walks, 2 * W, [&](unsigned first, dim3 grid) {
         a.first_block = first;
-        k_decay_run<T, W, WHOLE><<<grid, dim3(2 * W), 0, stream>>>(a);
+        k_decay_run<T, W><<<grid, dim3(2 * W), 0, stream>>>(a);
     });
 }
 
@@ -691,8 +761,8 @@ int forward(const tok_decay& t, DecayArgs a, hipStream_t stream) {
             k_decay_step<T, W><<<grid, dim3(kStepThreads), 0, stream>>>(a);
         });
     } else {
-        if (!whole(t)) sums<T, W>(a, stream);
-        walk<T, W, true>(a, stream);
+        if (!whole(t)) states<T, W>(a, stream);
+        run<T, W>(a, stream);
     }
     const hipError_t e = hipGetLastError();
     return e == hipSuccess ? VOX_OK : ssh_hip_fail(e);
@@ -708,28 +778,29 @@ struct Gradients {
 };
 
 template <typename T, int W>
-int backward(const tok_decay& t, const DecayArgs& base, const Gradients& g, hipStream_t stream) {
-    DecayArgs a = base;  // grad_q: grad against v and k, along the forward's states
-    a.q = g.g, a.k = g.v, a.v = g.k, a.out = g.gq, a.state = g.state, a.carry = g.carry, a.turned = 1;
-    walk<T, W, false>(a, stream);
-    a = base;  // grad_v, then grad_k, from the other end
-    a.back = !base.back, a.lag = 0, a.enter_by = 1.0f, a.leave_by = base.near_by;
-    a.q = g.k, a.k = g.q, a.v = g.g, a.state = g.grad_last, a.carry = g.back_carry;
-    a.out = g.part ? (void*)g.part : g.gv, a.out_wide = g.part != nullptr, a.last = g.grad_state;
-    if (!whole(t)) sums<T, W>(a, stream);
-    walk<T, W, true>(a, stream);
+int backward(const tok_decay& t, DecayArgs a, const Gradients& g, hipStream_t stream) {
     const long long n = (long long)a.t * (a.heads / g.group) * a.width;
-    auto join = [&](void* to) {
-        if (!g.part) return;
-        in_launches((n + 2047) / 2048, 256, [&](unsigned first, dim3 grid) {
-            k_decay_share<T><<<grid, dim3(256), 0, stream>>>(g.part, (T*)to, n, g.group, a.width, first);
+    // grad_v and the state's gradient, from the other end
+    Walk& v = a.walk[0];
+    Walk& q = a.walk[2];
+    q = v;
+    v.back = !v.back, v.lag = 0, v.leave_by = v.enter_by, v.enter_by = 1.0f;
+    v.q = g.k, v.k = g.q, v.v = g.g, v.state = g.grad_last, v.carry = g.back_carry, v.last = g.grad_state;
+    v.out = g.part ? (void*)g.part : g.gv, v.out_wide = g.part != nullptr;
+    if (!whole(t)) states<T, W>(a, stream);
+    // grad_k along the same states
+    Walk& k = a.walk[1];
+    k = v;
+    k.q = g.v, k.k = g.g, k.v = g.q, k.turned = 1, k.last = nullptr;
+    k.out = g.part ? (void*)(g.part + n * g.group) : g.gk;
+    // grad_q: grad against v and k, along the forward's
+    q.q = g.g, q.k = g.v, q.v = g.k, q.out = g.gq, q.state = g.state, q.carry = g.carry, q.turned = 1;
+    a.walks = 3;
+    run<T, W>(a, stream);
+    if (g.part)
+        in_launches((2 * n + 2047) / 2048, 256, [&](unsigned first, dim3 grid) {
+            k_decay_share<T><<<grid, dim3(256), 0, stream>>>(g.part, (T*)g.gv, (T*)g.gk, n, g.group, a.width, first);
         });
-    };
-    join(g.gv);
-    a.q = g.v, a.k = g.g, a.v = g.q, a.turned = 1, a.last = nullptr;
-    a.out = g.part ? (void*)g.part : g.gk;
-    walk<T, W, false>(a, stream);
-    join(g.gk);
     const hipError_t e = hipGetLastError();
     return e == hipSuccess ? VOX_OK : ssh_hip_fail(e);
 }
@@ -744,7 +815,7 @@ int by_width(int width, F f) {
 bool aligned16(const void* p) { return ((size_t)p & 15) == 0; }
 
 long long carry_elems(const tok_decay& t) { return whole(t) ? 0 : slots(t) * state_elems(t); }
-long long part_elems(const tok_decay& t) { return t.heads == t.kv_heads ? 0 : t.t * t.heads * t.width; }
+long long part_elems(const tok_decay& t) { return t.heads == t.kv_heads ? 0 : 2 * t.t * t.heads * t.width; }
 
 }  // namespace
 
@@ -770,8 +841,9 @@ int tok_decay_attend(const tok_decay* t, const void* q, const void* k, const voi
         if (!aligned16(p)) return VOX_EINVAL;
     DecayArgs a = make_args(*t);
     const int group = t->heads / t->kv_heads;
-    a.q = place(q, t->q_stride, 1), a.k = place(k, t->k_stride, group), a.v = place(v, t->v_stride, group);
-    a.state = state, a.out = out, a.last = last_state, a.carry = carry;
+    Walk& w = a.walk[0];
+    w.q = place(q, t->q_stride, 1), w.k = place(k, t->k_stride, group), w.v = place(v, t->v_stride, group);
+    w.state = state, w.out = out, w.last = last_state, w.carry = carry;
     return by_width<void>(t->width, [&](auto w) {
         return t->dtype == TOK_BF16 ? forward<bf16_t, decltype(w)::value>(*t, a, stream)
                                     : forward<f16_t, decltype(w)::value>(*t, a, stream);
