@@ -34,7 +34,7 @@ constexpr long long kMaxStride = 1ll << 22;  // 256 rows apart in 32 bits of byt
 constexpr int kTokenPad = 128;               // tokens are laid out in whole tiles
 constexpr int kRowTile = 256;                // rows of a tile of logits
 constexpr int kStep = 32;                    // inner elements of a stage
-constexpr long long kPieceBytes = 128ll << 20;
+constexpr long long kPieceBytes = 256ll << 20;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kLowest = -3.402823466e+38f;
@@ -83,21 +83,28 @@ struct Shape {
     static constexpr int kLoads = kALoads + BN * 4 / NT;  // every wavefront's, at least
 };
 
-// The stages of a block: loads run two ahead of the products.
-template <int LOADS, typename Issue, typename Compute>
+// The stages of a block: loads run two ahead of the products. Memory operations of a
+// wavefront end in the order they were issued, so a stage is there when no more are
+// under way than were issued after its loads: the next stage's, and the stores of a
+// tile that ended with the stage before, or the one before that. compute() says how
+// many those are (0, or STORES).
+template <int LOADS, int STORES, typename Issue, typename Compute>
 __device__ __forceinline__ void stages(int total, Issue issue, Compute compute) {
     if (total > 0) issue(0, 0);
     if (total > 1) issue(1, 1);
-    int buf = 0;
+    int buf = 0, since = 2;
     for (int i = 0; i < total; ++i) {
-        if (i + 1 < total)
-            load_wait<LOADS>();
-        else
+        if (i + 1 == total)
             load_wait<0>();
+        else if (STORES && since < 2)
+            load_wait<LOADS + STORES>();
+        else
+            load_wait<LOADS>();
         __syncthreads();  // this stage is there, and all are done with the one before
         const int ahead = buf == 0 ? 2 : buf - 1;
         if (i + 2 < total) issue(i + 2, ahead);
-        compute(i, buf);
+        ++since;
+        if (compute(i, buf)) since = 0;
         buf = buf == 2 ? 0 : buf + 1;
     }
 }
@@ -279,7 +286,7 @@ __global__ __launch_bounds__(256) void k_loss_pack(LossArgs a) {
 
 // Tiles [t0, t1) of the rows against a tile of tokens, from `first_row` on;
 // done(tile, acc) gets each tile's products.
-template <typename T, typename S, typename Done>
+template <typename T, typename S, int STORES, typename Done>
 __device__ __forceinline__ void logits(const LossArgs& a, char* lds, int first_row, int end_row, int t0, int t1,
                                        int token0, Done done) {
     typedef RowsOfMatrix<T, S::BM, S::NT> A;
@@ -291,7 +298,7 @@ __device__ __forceinline__ void logits(const LossArgs& a, char* lds, int first_r
     const unsigned b_at = base + S::kA + B::place((wave % S::WN) * 32 * S::NB + (lane & 31), half);
     int tile_in = t0, k_in = 0, tile = t0, k = 0;
     acc16 acc[S::MA][S::NB];
-    stages<S::kLoads>(
+    stages<S::kLoads, STORES>(
         (t1 - t0) * steps,
         [&](int, int buf) {
             const unsigned to = base + buf * S::kStage;
@@ -317,10 +324,10 @@ __device__ __forceinline__ void logits(const LossArgs& a, char* lds, int first_r
 #pragma unroll
                     for (int j = 0; j < S::NB; ++j) acc[i][j] = Mma<T>::mul(x[i], y[j], acc[i][j]);
             }
-            if (++k == steps) {
-                done(tile, acc);
-                k = 0, ++tile;
-            }
+            if (++k < steps) return false;
+            done(tile, acc);
+            k = 0, ++tile;
+            return true;
         });
 }
 
@@ -339,7 +346,7 @@ __global__ __launch_bounds__(S::NT, 2) void k_loss_sum(LossArgs a) {
 #pragma unroll
     for (int j = 0; j < S::NB; ++j) m[j] = kLowest, l[j] = 0.0f, came[j] = a.came[token0 + token_in + 32 * j];
 
-    logits<T, S>(a, lds, 0, a.rows, t0, t1, token0, [&](int tile, acc16(&acc)[S::MA][S::NB]) {
+    logits<T, S, 0>(a, lds, 0, a.rows, t0, t1, token0, [&](int tile, acc16(&acc)[S::MA][S::NB]) {
         const int row0 = tile * S::BM + row_in;
         if (row0 + 32 * S::MA > a.rows) {
 #pragma unroll
@@ -429,7 +436,8 @@ __global__ __launch_bounds__(S::NT, 2) void k_loss_dz(LossArgs a) {
     const int split = id / a.token_tiles, token0 = (id % a.token_tiles) * S::BN;
     const int t0 = (int)((long long)a.tiles * split / a.splits), t1 = (int)((long long)a.tiles * (split + 1) / a.splits);
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, half = lane >> 5;
-    const int row_in = (wave / S::WN) * 32 * S::MA, token_in = (wave % S::WN) * 32 * S::NB + (lane & 31);
+    const int row_in = __builtin_amdgcn_readfirstlane((wave / S::WN) * 32 * S::MA);
+    const int token_in = (wave % S::WN) * 32 * S::NB + (lane & 31);
 
     float shift[S::NB], by[S::NB];
     int came[S::NB];
@@ -438,20 +446,22 @@ __global__ __launch_bounds__(S::NT, 2) void k_loss_dz(LossArgs a) {
         const int t = token0 + token_in + 32 * j;
         shift[j] = a.shift[t], by[j] = a.by[t], came[j] = a.came[t] - a.row0;
     }
-    logits<T, S>(a, lds, a.row0, a.rows, t0, t1, token0, [&](int tile, acc16(&acc)[S::MA][S::NB]) {
+    const int token_at = __builtin_amdgcn_readfirstlane((wave % S::WN) * 32 * S::NB);
+    const unsigned lane_at = half * a.t_pad + (lane & 31);
+    logits<T, S, S::MA * S::NB * 2>(a, lds, a.row0, a.rows, t0, t1, token0, [&](int tile, acc16(&acc)[S::MA][S::NB]) {
         const int row0 = tile * S::BM + row_in;  // in the piece
         const int left = a.rows - a.row0 - row0;
+        uint4* to = a.dz + (long long)(row0 >> 3) * a.t_pad + token0 + token_at;
 #pragma unroll
         for (int j = 0; j < S::NB; ++j) {
             const int mine = came[j] - row0;
             const bool any = __any(mine >= 0 && mine < 32 * S::MA);
-            uint4* to = a.dz + (long long)(row0 >> 3) * a.t_pad + token0 + token_in + 32 * j;
 #pragma unroll
             for (int i = 0; i < S::MA; ++i) {
-                float p[16];
+                acc16& p = acc[i][j];
 #pragma unroll
                 for (int r = 0; r < 16; ++r)
-                    p[r] = __builtin_amdgcn_exp2f(__builtin_fmaf(acc[i][j][r], a.scale2, -shift[j]));
+                    p[r] = __builtin_amdgcn_exp2f(__builtin_fmaf(p[r], a.scale2, -shift[j]));
                 if (any)
 #pragma unroll
                     for (int r = 0; r < 16; ++r)
@@ -468,7 +478,8 @@ __global__ __launch_bounds__(S::NT, 2) void k_loss_dz(LossArgs a) {
                     unsigned y0 = Mma<T>::pair(p[4 * q + 4], p[4 * q + 5]), y1 = Mma<T>::pair(p[4 * q + 6], p[4 * q + 7]);
                     trade_halves(x0, y0);
                     trade_halves(x1, y1);
-                    to[(long long)(4 * i + q + half) * a.t_pad] = make_uint4(x0, x1, y0, y1);
+                    uint4* row = to + (long long)(4 * i + q) * a.t_pad + 32 * j;
+                    row[lane_at] = make_uint4(x0, x1, y0, y1);
                 }
             }
         }
@@ -501,7 +512,7 @@ __global__ __launch_bounds__(S::NT, 2) void k_loss_grad_x(LossArgs a) {
     for (int i = 0; i < S::MA; ++i)
 #pragma unroll
         for (int j = 0; j < S::NB; ++j) acc[i][j] = zero16();
-    stages<S::kLoads>(
+    stages<S::kLoads, 0>(
         k1 - k0,
         [&](int i, int buf) {
             const unsigned to = base + buf * S::kStage;
@@ -523,6 +534,7 @@ __global__ __launch_bounds__(S::NT, 2) void k_loss_grad_x(LossArgs a) {
 #pragma unroll
                     for (int j = 0; j < S::NB; ++j) acc[i][j] = Mma<T>::mul(x[i], y[j], acc[i][j]);
             }
+            return false;
         });
 #pragma unroll
     for (int j = 0; j < S::NB; ++j) {
@@ -567,7 +579,7 @@ __global__ __launch_bounds__(S::NT, 2) void k_loss_grad_table(LossArgs a) {
     for (int i = 0; i < S::MA; ++i)
 #pragma unroll
         for (int j = 0; j < S::NB; ++j) acc[i][j] = zero16();
-    stages<S::kLoads>(
+    stages<S::kLoads, 0>(
         k1 - k0,
         [&](int i, int buf) {
             const unsigned to = base + buf * S::kStage;
@@ -588,6 +600,7 @@ __global__ __launch_bounds__(S::NT, 2) void k_loss_grad_table(LossArgs a) {
 #pragma unroll
                     for (int j = 0; j < S::NB; ++j) acc[i][j] = Mma<T>::mul(x[i], y[j], acc[i][j]);
             }
+            return false;
         });
     const float down = ldexpf(a.scale, -lift_of<T>(a));
 #pragma unroll
@@ -786,7 +799,7 @@ int backward(LossArgs a, const Cut& c, hipStream_t stream) {
         a.piece = all - a.row0 < c.piece ? all - a.row0 : c.piece;
         a.first = p == 0;
         a.tiles = a.piece / kRowTile;
-        a.splits = clamp(2048 / c.token_tiles, 1, a.tiles);
+        a.splits = clamp(512 / c.token_tiles, 1, a.tiles);
         LossArgs z = a;
         const dim3 grid((unsigned)(z.token_tiles * z.splits));
         if (c.slim)
