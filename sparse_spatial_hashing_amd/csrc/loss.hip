@@ -110,33 +110,42 @@ __device__ __forceinline__ void stages(int total, Issue issue, Compute compute) 
 }
 
 // ---- operands ----------------------------------------------------------------
+//
+// load() brings a stage to LDS; what of an address is a lane's own is computed once, in
+// 32 bits.
 
 // Rows of a matrix in memory, the inner index along a row. In LDS 64 bytes a row,
 // its four pieces permuted by XOR with (row >> 2) & 3: 16 rows' pieces of one place
 // touch every bank once.
 template <typename T, int ROWS, int NT>
 struct RowsOfMatrix {
-    static __device__ __forceinline__ void load(unsigned to, const T* base, long long stride, int row0, int rows,
-                                                int k0, int width) {
+    const T* base;
+    long long stride;
+    int rows, width;
+    unsigned offset;
+
+    __device__ __forceinline__ RowsOfMatrix(const void* p, long long st, int n, int w)
+        : base((const T*)p), stride(st), rows(n), width(w) {
+        const int row = threadIdx.x >> 2;
+        offset = (unsigned)row * (unsigned)(2 * st) + 16u * ((threadIdx.x & 3) ^ ((row >> 2) & 3));
+    }
+    __device__ __forceinline__ void load(unsigned to, int row0, int k0) const {
         constexpr int kPer = ROWS * 4 / NT;
+        static_assert(NT / 4 % 16 == 0, "the permutation is that of the first load's rows");
         const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-        const int r = threadIdx.x >> 2, at = threadIdx.x & 3;
+        const T* from = base + row0 * stride + k0;
         if (row0 + ROWS <= rows && k0 + kStep <= width) {
-            const T* from = base + (long long)row0 * stride + k0;
 #pragma unroll
-            for (int p = 0; p < kPer; ++p) {
-                const int row = p * (NT / 4) + r;
-                load_to_lds(to + 1024u * wave + 16u * NT * p, from,
-                            (unsigned)row * (unsigned)(2 * stride) + 16u * (at ^ ((row >> 2) & 3)));
-            }
+            for (int p = 0; p < kPer; ++p)
+                load_to_lds(to + 1024u * wave + 16u * NT * p, from + p * (NT / 4) * stride, offset);
             return;
         }
+        const int r = threadIdx.x >> 2, c = (threadIdx.x & 3) ^ ((r >> 2) & 3);
 #pragma unroll
         for (int p = 0; p < kPer; ++p) {
-            const int row = p * (NT / 4) + r, c = at ^ ((row >> 2) & 3);
+            const int row = p * (NT / 4) + r;
             const bool there = row0 + row < rows && k0 + 8 * c < width;
-            const void* from = there ? (const void*)(base + (row0 + row) * stride + k0 + 8 * c) : &kNothing;
-            load_to_lds(to + 1024u * wave + 16u * NT * p, from);
+            load_to_lds(to + 1024u * wave + 16u * NT * p, there ? (const void*)(from + row * stride + 8 * c) : &kNothing);
         }
     }
     static __device__ __forceinline__ unsigned place(int row, int half) {
@@ -151,17 +160,21 @@ struct RowsOfMatrix {
 // Rows of a matrix kept in pieces, [inner / 8][row]. In LDS [4][ROWS] pieces.
 template <typename T, int ROWS, int NT>
 struct RowsOfPieces {
-    static __device__ __forceinline__ void load(unsigned to, const uint4* base, long long pitch, int row0, int k0) {
+    const uint4* base;
+    long long pitch;
+    unsigned offset;
+
+    __device__ __forceinline__ RowsOfPieces(const uint4* p, long long step) : base(p), pitch(step) {
+        offset = ((threadIdx.x / ROWS) * (unsigned)step + threadIdx.x % ROWS) * 16u;
+    }
+    __device__ __forceinline__ void load(unsigned to, int row0, int k0) const {
         constexpr int kPer = (ROWS * 4 + NT - 1) / NT;
         const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-        const uint4* from = base + (long long)(k0 >> 3) * pitch + row0;
+        const uint4* from = base + (k0 >> 3) * pitch + row0;
 #pragma unroll
-        for (int p = 0; p < kPer; ++p) {
-            const int i = p * NT + threadIdx.x;
+        for (int p = 0; p < kPer; ++p)
             if (p * NT + wave * 64 < ROWS * 4)
-                load_to_lds(to + 1024u * wave + 16u * NT * p,
-                            from + (long long)(i / ROWS) * pitch + i % ROWS);
-        }
+                load_to_lds(to + 1024u * wave + 16u * NT * p, from + p * (NT / ROWS) * pitch, offset);
     }
     static __device__ __forceinline__ unsigned place(int row, int half) { return (half * ROWS + row) * 16; }
     static __device__ __forceinline__ auto read(unsigned at, int block, int s) {
@@ -174,18 +187,34 @@ struct RowsOfPieces {
 // number of the row that puts four rows of 64 bytes on all banks.
 template <typename T, int COLS, int NT>
 struct ColumnsOfMatrix {
+    const T* base;
+    long long stride;
+    int rows, left;   // columns from the first on
+    unsigned offset;
+
     static __device__ __forceinline__ int swz(int row) { return ((row & 3) << 2) | ((row >> 2) & 3); }
-    static __device__ __forceinline__ void load(unsigned to, const T* base, long long stride, int row0, int rows,
-                                                int col0, int width) {
+    __device__ __forceinline__ ColumnsOfMatrix(const void* p, long long st, int n, int col0, int width)
+        : base((const T*)p + col0), stride(st), rows(n), left(width - col0) {
+        const int row = threadIdx.x >> 4;
+        offset = (unsigned)row * (unsigned)(2 * st) + 16u * ((threadIdx.x & 15) ^ swz(row));
+    }
+    __device__ __forceinline__ void load(unsigned to, int row0) const {
         constexpr int kPer = COLS * 4 / NT;
+        static_assert(NT == 256, "16 rows of 128 columns a load");
         const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+        const T* from = base + row0 * stride;
+        if (row0 + kStep <= rows && left >= COLS) {
+#pragma unroll
+            for (int p = 0; p < kPer; ++p)
+                load_to_lds(to + 1024u * wave + 16u * NT * p, from + (p & 1) * 16 * stride + (p >> 1) * 128, offset);
+            return;
+        }
+        const int r = threadIdx.x >> 4, c = (threadIdx.x & 15) ^ swz(r);
 #pragma unroll
         for (int p = 0; p < kPer; ++p) {
-            const int i = p * NT + threadIdx.x;
-            const int row = (i >> 4) & 31, c = ((i & 15) ^ swz(row)) + 16 * (i >> 9);
-            const bool there = row0 + row < rows && col0 + 8 * c < width;
-            const void* from = there ? (const void*)(base + (row0 + row) * stride + col0 + 8 * c) : &kNothing;
-            load_to_lds(to + 1024u * wave + 16u * NT * p, from);
+            const int row = (p & 1) * 16 + r, col = 8 * c + (p >> 1) * 128;
+            const bool there = row0 + row < rows && col < left;
+            load_to_lds(to + 1024u * wave + 16u * NT * p, there ? (const void*)(from + row * stride + col) : &kNothing);
         }
     }
     // Where the first four of a lane's eight inner rows are (first step, block 0 of a
@@ -205,16 +234,22 @@ struct ColumnsOfMatrix {
 // pieces, the 32 of a column group permuted by XOR with 4 (group % 4).
 template <typename T, int COLS, int NT>
 struct ColumnsOfPieces {
-    static __device__ __forceinline__ void load(unsigned to, const uint4* base, long long pitch, int row0, int col0,
-                                                int cols) {
+    const uint4* base;
+    long long pitch;
+    unsigned offset;
+
+    __device__ __forceinline__ ColumnsOfPieces(const uint4* p, long long step, int col0)
+        : base(p + (long long)(col0 >> 3) * step), pitch(step) {
+        const int group = threadIdx.x >> 5, row = (threadIdx.x & 31) ^ ((group & 3) << 2);
+        offset = (group * (unsigned)step + row) * 16u;
+    }
+    __device__ __forceinline__ void load(unsigned to, int row0) const {
         constexpr int kPer = COLS * 4 / NT;
+        static_assert(NT / 32 % 4 == 0, "the permutation is that of the first load's groups");
         const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
 #pragma unroll
-        for (int p = 0; p < kPer; ++p) {
-            const int i = p * NT + threadIdx.x, group = i >> 5, row = (i & 31) ^ ((group & 3) << 2);
-            const uint4* from = base + (long long)((col0 >> 3) + group) * pitch + row0 + row;
-            load_to_lds(to + 1024u * wave + 16u * NT * p, col0 + 8 * group < cols ? from : &kNothing);
-        }
+        for (int p = 0; p < kPer; ++p)
+            load_to_lds(to + 1024u * wave + 16u * NT * p, base + row0 + p * (NT / 32) * pitch, offset);
     }
     static __device__ __forceinline__ uint2 place(int lane) {
         const int row = 8 * (lane >> 5) + ((lane & 15) >> 2);
@@ -296,14 +331,16 @@ __device__ __forceinline__ void logits(const LossArgs& a, char* lds, int first_r
     const unsigned base = lds_address(lds);
     const unsigned a_at = base + A::place((wave / S::WN) * 32 * S::MA + (lane & 31), half);
     const unsigned b_at = base + S::kA + B::place((wave % S::WN) * 32 * S::NB + (lane & 31), half);
+    const A table(a.table, a.t_stride, end_row, a.width);
+    const B tokens(a.xg, a.t_pad);
     int tile_in = t0, k_in = 0, tile = t0, k = 0;
     acc16 acc[S::MA][S::NB];
     stages<S::kLoads, STORES>(
         (t1 - t0) * steps,
         [&](int, int buf) {
             const unsigned to = base + buf * S::kStage;
-            A::load(to, (const T*)a.table, a.t_stride, first_row + tile_in * S::BM, end_row, k_in * kStep, a.width);
-            B::load(to + S::kA, a.xg, a.t_pad, token0, k_in * kStep);
+            table.load(to, first_row + tile_in * S::BM, k_in * kStep);
+            tokens.load(to + S::kA, token0, k_in * kStep);
             if (++k_in == steps) k_in = 0, ++tile_in;
         },
         [&](int, int buf) {
@@ -504,6 +541,8 @@ __global__ __launch_bounds__(S::NT, 2) void k_loss_grad_x(LossArgs a) {
     const int k0 = (int)((long long)steps * split / a.x_splits), k1 = (int)((long long)steps * (split + 1) / a.x_splits);
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, half = lane >> 5;
     const unsigned base = lds_address(lds);
+    const A table(a.table, a.t_stride, a.rows, col0, a.width);
+    const B dz(a.dz, a.t_pad);
     const int a_block = (wave / S::WN) * S::MA;
     const uint2 a_at = A::place(lane);
     const unsigned b_at = base + S::kA + B::place((wave % S::WN) * 32 * S::NB + (lane & 31), half);
@@ -516,9 +555,8 @@ __global__ __launch_bounds__(S::NT, 2) void k_loss_grad_x(LossArgs a) {
         k1 - k0,
         [&](int i, int buf) {
             const unsigned to = base + buf * S::kStage;
-            const int k = (k0 + i) * kStep;
-            A::load(to, (const T*)a.table, a.t_stride, a.row0 + k, a.rows, col0, a.width);
-            B::load(to + S::kA, a.dz, a.t_pad, token0, k);
+            table.load(to, a.row0 + (k0 + i) * kStep);
+            dz.load(to + S::kA, token0, (k0 + i) * kStep);
         },
         [&](int, int buf) {
             const unsigned on = base + buf * S::kStage;
@@ -572,6 +610,8 @@ __global__ __launch_bounds__(S::NT, 2) void k_loss_grad_table(LossArgs a) {
     const int k0 = (int)((long long)steps * split / a.t_splits), k1 = (int)((long long)steps * (split + 1) / a.t_splits);
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, half = lane >> 5;
     const unsigned base = lds_address(lds);
+    const A tokens(a.xg, a.t_pad, col0);
+    const B dz(a.dz, a.t_pad, row0);
     const int a_block = (wave / S::WN) * S::MA, b_block = (wave % S::WN) * S::NB;
     const uint2 at = A::place(lane);
     acc16 acc[S::MA][S::NB];
@@ -583,8 +623,8 @@ __global__ __launch_bounds__(S::NT, 2) void k_loss_grad_table(LossArgs a) {
         k1 - k0,
         [&](int i, int buf) {
             const unsigned to = base + buf * S::kStage;
-            A::load(to, a.xg, a.t_pad, (k0 + i) * kStep, col0, a.width);
-            B::load(to + S::kA, a.dz, a.t_pad, (k0 + i) * kStep, row0, a.piece);
+            tokens.load(to, (k0 + i) * kStep);
+            dz.load(to + S::kA, (k0 + i) * kStep);
         },
         [&](int, int buf) {
             const unsigned x_on = base + buf * S::kStage, y_on = x_on + S::kA;
@@ -687,7 +727,8 @@ struct Cut {
 Cut cut(long long t, long long rows, long long width) {
     Cut c;
     c.t_pad = ceil_div(t, kTokenPad) * kTokenPad;
-    c.width8 = ceil_div(width, kStep) * (kStep / 8);
+    // whole tiles of columns: past the width they are zeros
+    c.width8 = ceil_div(width, width > 128 ? 256 : 128) * (width > 128 ? 32 : 16);
     c.slim = t <= 32;
     c.token_tiles = c.slim ? 1 : (int)(c.t_pad / 128);
     c.tiles = (int)ceil_div(rows, kRowTile);
