@@ -38,6 +38,7 @@ constexpr long long kPieceBytes = 256ll << 20;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kLowest = -3.402823466e+38f;
+constexpr int kSumBlocks = 4096, kDzBlocks = 512;
 constexpr int kLift = 14;  // fp16: dZ is 2^kLift too large
 
 struct LossArgs {
@@ -75,12 +76,22 @@ struct LossArgs {
 // wavefronts.
 template <typename T, int MA_, int NB_, int WM_, int WN_>
 struct Shape {
+    static constexpr int kWidth = 0;  // the width goes by in stages
     static constexpr int MA = MA_, NB = NB_, WM = WM_, WN = WN_;
     static constexpr int BM = 32 * MA * WM, BN = 32 * NB * WN, NT = 64 * WM * WN;
     static constexpr int kA = BM * kStep * 2, kB = BN * kStep * 2;  // bytes of a stage
     static constexpr int kStage = kA + kB;
     static constexpr int kALoads = BM * 4 / NT, kBLoads = (BN * 4 + NT - 1) / NT;
     static constexpr int kLoads = kALoads + BN * 4 / NT;  // every wavefront's, at least
+};
+
+// Tiles of logits of narrow tokens: a wavefront keeps its 64 tokens' whole width (W at most)
+// in registers, and a stage is a tile: BM rows of all their width.
+template <typename T, int W>
+struct Narrow {
+    static constexpr int kWidth = W, MA = W == 128 ? 1 : 2, NB = 2, WM = 2, WN = 2;
+    static constexpr int BM = 32 * MA * WM, BN = 32 * NB * WN, NT = 64 * WM * WN;
+    static constexpr int kStage = BM * W * 2, kLoads = BM * (W / 8) / NT;
 };
 
 // The stages of a block: loads run two ahead of the products. Memory operations of a
@@ -154,6 +165,53 @@ struct RowsOfMatrix {
     // at: tile + place of row lane % 32; 32 rows on per block, step s of the stage
     static __device__ __forceinline__ auto read(unsigned at, int block, int s) {
         return lds_read<typename Mma<T>::vec8>((at ^ (s << 5)) + block * 2048);
+    }
+};
+
+// Whole rows of a matrix of W columns at most, zeros past its width. In LDS 2 W bytes a row,
+// its pieces permuted so that 16 rows' pieces of one place touch every bank once.
+template <typename T, int W, int ROWS, int NT>
+struct WholeRows {
+    static constexpr int kPieces = W / 8;
+    const T* base;
+    long long stride;
+    int rows, width;
+    unsigned offset;
+
+    static __device__ __forceinline__ int swz(int row) {
+        if (W == 128) return ((row & 3) << 2) | ((row >> 2) & 3);
+        if (W == 64) return (((row >> 1) & 1) << 2) | ((row >> 2) & 3);
+        return (row >> 2) & 3;
+    }
+    __device__ __forceinline__ WholeRows(const void* p, long long st, int n, int w)
+        : base((const T*)p), stride(st), rows(n), width(w) {
+        const int row = threadIdx.x / kPieces;
+        offset = (unsigned)row * (unsigned)(2 * st) + 16u * ((threadIdx.x % kPieces) ^ swz(row));
+    }
+    __device__ __forceinline__ void load(unsigned to, int row0) const {
+        constexpr int kPer = ROWS * kPieces / NT;
+        static_assert(NT / kPieces % 16 == 0, "the permutation is that of the first load's rows");
+        const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+        const T* from = base + row0 * stride;
+        if (row0 + ROWS <= rows && width == W) {
+#pragma unroll
+            for (int p = 0; p < kPer; ++p)
+                load_to_lds(to + 1024u * wave + 16u * NT * p, from + p * (NT / kPieces) * stride, offset);
+            return;
+        }
+        const int r = threadIdx.x / kPieces, c = (threadIdx.x % kPieces) ^ swz(r);
+#pragma unroll
+        for (int p = 0; p < kPer; ++p) {
+            const int row = p * (NT / kPieces) + r;
+            const bool there = row0 + row < rows && 8 * c < width;
+            load_to_lds(to + 1024u * wave + 16u * NT * p, there ? (const void*)(from + row * stride + 8 * c) : &kNothing);
+        }
+    }
+    static __device__ __forceinline__ unsigned place(int row, int half) {
+        return row * 2 * W + ((half ^ swz(row)) << 4);
+    }
+    static __device__ __forceinline__ auto read(unsigned at, int block, int s) {
+        return lds_read<typename Mma<T>::vec8>((at ^ (s << 5)) + block * 64 * W);
     }
 };
 
@@ -320,10 +378,50 @@ __global__ __launch_bounds__(256) void k_loss_pack(LossArgs a) {
 // ---- logits ------------------------------------------------------------------
 
 // Tiles [t0, t1) of the rows against a tile of tokens, from `first_row` on;
-// done(tile, acc) gets each tile's products.
+// done(tile, acc) gets each tile's products and stores STORES times, or not at all.
+// 12,000 tokens of 128 by 214,272 rows: tokens in registers
 template <typename T, typename S, int STORES, typename Done>
 __device__ __forceinline__ void logits(const LossArgs& a, char* lds, int first_row, int end_row, int t0, int t1,
                                        int token0, Done done) {
+    if constexpr (S::kWidth) {
+        typedef WholeRows<T, S::kWidth, S::BM, S::NT> A;
+        const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, half = lane >> 5;
+        const unsigned base = lds_address(lds);
+        const unsigned a_at = base + A::place((wave / S::WN) * 32 * S::MA + (lane & 31), half);
+        const A table(a.table, a.t_stride, end_row, a.width);
+        constexpr int kSteps = S::kWidth / 16;
+        typename Mma<T>::vec8 y[kSteps][S::NB];
+#pragma unroll
+        for (int s = 0; s < kSteps; ++s)
+#pragma unroll
+            for (int j = 0; j < S::NB; ++j)
+                y[s][j] = __builtin_bit_cast(typename Mma<T>::vec8,
+                                             a.xg[(long long)(2 * s + half) * a.t_pad + token0 +
+                                                  (wave % S::WN) * 32 * S::NB + 32 * j + (lane & 31)]);
+        // settled here: inside the loop their wait would be for the tiles under way as well
+#pragma unroll
+        for (int s = 0; s < kSteps; ++s)
+#pragma unroll
+            for (int j = 0; j < S::NB; ++j) asm volatile("" : "+v"(y[s][j]));
+        stages<S::kLoads, STORES>(
+            t1 - t0, [&](int i, int buf) { table.load(base + buf * S::kStage, first_row + (t0 + i) * S::BM); },
+            [&](int i, int buf) {
+                acc16 acc[S::MA][S::NB];
+#pragma unroll
+                for (int m = 0; m < S::MA; ++m) {
+#pragma unroll
+                    for (int j = 0; j < S::NB; ++j) acc[m][j] = zero16();
+#pragma unroll
+                    for (int s = 0; s < kSteps; ++s) {
+                        const typename Mma<T>::vec8 x = A::read(a_at + buf * S::kStage, m, s);
+#pragma unroll
+                        for (int j = 0; j < S::NB; ++j) acc[m][j] = Mma<T>::mul(x, y[s][j], acc[m][j]);
+                    }
+                }
+                done(t0 + i, acc);
+                return true;
+            });
+    } else {
     typedef RowsOfMatrix<T, S::BM, S::NT> A;
     typedef RowsOfPieces<T, S::BN, S::NT> B;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, half = lane >> 5;
@@ -366,6 +464,7 @@ __device__ __forceinline__ void logits(const LossArgs& a, char* lds, int first_r
             k = 0, ++tile;
             return true;
         });
+    }
 }
 
 // Maxima and sums over a share of the rows, and the logit of each token's own row.
@@ -404,22 +503,31 @@ __global__ __launch_bounds__(S::NT, 2) void k_loss_sum(LossArgs a) {
                     for (int r = 0; r < 16; ++r)
                         if (mine == 32 * i + acc_row(r, half)) a.hit[token0 + token_in + 32 * j] = acc[i][j][r] * a.scale2;
             }
-            float top = acc[0][j][0];
-#pragma unroll
-            for (int i = 0; i < S::MA; ++i)
-#pragma unroll
-                for (int r = 0; r < 16; ++r) top = fmaxf(top, acc[i][j][r]);
-            top *= a.scale2;
-            if (__any(top > m[j] + 8.0f)) {
-                const float now = fmaxf(m[j], top);
-                l[j] *= __builtin_amdgcn_exp2f(m[j] - now);
-                m[j] = now;
-            }
+            // Less the maximum so far. When their sum says that it lags by far (or is the
+            // first tile's), it is brought up to date, and they are taken again.
+            float sum = 0.0f;
 #pragma unroll
             for (int i = 0; i < S::MA; ++i)
 #pragma unroll
                 for (int r = 0; r < 16; ++r)
-                    l[j] += __builtin_amdgcn_exp2f(__builtin_fmaf(acc[i][j][r], a.scale2, -m[j]));
+                    sum += __builtin_amdgcn_exp2f(__builtin_fmaf(acc[i][j][r], a.scale2, -m[j]));
+            if (__any(!(sum <= 0x1p40f))) {
+                float top = acc[0][j][0];
+#pragma unroll
+                for (int i = 0; i < S::MA; ++i)
+#pragma unroll
+                    for (int r = 0; r < 16; ++r) top = fmaxf(top, acc[i][j][r]);
+                const float now = fmaxf(m[j], top * a.scale2);
+                l[j] *= __builtin_amdgcn_exp2f(m[j] - now);
+                m[j] = now;
+                sum = 0.0f;
+#pragma unroll
+                for (int i = 0; i < S::MA; ++i)
+#pragma unroll
+                    for (int r = 0; r < 16; ++r)
+                        sum += __builtin_amdgcn_exp2f(__builtin_fmaf(acc[i][j][r], a.scale2, -m[j]));
+            }
+            l[j] += sum;
         }
     });
 
@@ -711,6 +819,8 @@ using Wide = Shape<T, 4, 2, 2, 2>;   // 256 x 128
 template <typename T>
 using Even = Shape<T, 2, 2, 2, 2>;   // 128 x 128
 template <typename T>
+using Logit = Even<T>;
+template <typename T>
 using Slim = Shape<T, 2, 1, 4, 1>;   // 256 x 32: few tokens
 
 long long round256(long long n) { return (n + 255) / 256 * 256; }
@@ -720,7 +830,7 @@ int clamp(long long n, long long lo, long long hi) { return (int)(n < lo ? lo : 
 // How a call is cut: blocks enough for two on each of 256 CUs.
 struct Cut {
     long long t_pad, width8;
-    int tiles, splits, token_tiles, slim;
+    int splits, slim;  // splits: at most
     int piece, pieces, x_splits, t_splits;
 };
 
@@ -730,14 +840,13 @@ Cut cut(long long t, long long rows, long long width) {
     // whole tiles of columns: past the width they are zeros
     c.width8 = ceil_div(width, width > 128 ? 256 : 128) * (width > 128 ? 32 : 16);
     c.slim = t <= 32;
-    c.token_tiles = c.slim ? 1 : (int)(c.t_pad / 128);
-    c.tiles = (int)ceil_div(rows, kRowTile);
-    c.splits = clamp(4096 / c.token_tiles, 1, c.tiles);
+    const long long tiles = ceil_div(rows, kRowTile), token_tiles = c.slim ? 1 : c.t_pad / kTokenPad;
+    c.splits = clamp(kSumBlocks / token_tiles, 1, 4 * tiles);
     long long piece = kPieceBytes / (2 * c.t_pad) / kRowTile * kRowTile;
     if (piece < kRowTile) piece = kRowTile;
-    c.pieces = (int)ceil_div((long long)c.tiles * kRowTile, piece);
-    c.piece = (int)(ceil_div(c.tiles, c.pieces) * kRowTile);
-    c.pieces = (int)ceil_div((long long)c.tiles * kRowTile, c.piece);
+    c.pieces = (int)ceil_div(tiles * kRowTile, piece);
+    c.piece = (int)(ceil_div(tiles, c.pieces) * kRowTile);
+    c.pieces = (int)ceil_div(tiles * kRowTile, c.piece);
     const long long cols = ceil_div(width, width > 128 ? 256 : 128);
     c.x_splits = clamp(512 / (cols * (c.t_pad / 128)), 1, c.piece / 512 > 1 ? c.piece / 512 : 1);
     c.t_splits = clamp(512 / (cols * (c.piece / 128)), 1, c.t_pad / 512 > 1 ? c.t_pad / 512 : 1);
@@ -796,7 +905,6 @@ LossArgs make_args(const void* x, int64_t x_stride, const void* table, int64_t t
     a.t = (int)t, a.rows = (int)rows, a.width = (int)width, a.ids = ids, a.id_bytes = id_bytes;
     a.scale = scale, a.scale2 = (float)(scale * 1.4426950408889634);
     a.t_pad = (int)c.t_pad, a.width8 = (int)c.width8;
-    a.tiles = c.tiles, a.splits = c.splits, a.token_tiles = c.token_tiles;
     a.xg = (uint4*)(ws + l.xg), a.came = (int*)(ws + l.came);
     a.shift = (float*)(ws + l.shift), a.by = (float*)(ws + l.by), a.hit = (float*)(ws + l.hit);
     a.part = (float2*)(ws + l.part), a.top = (unsigned*)(ws + l.top);
@@ -810,21 +918,46 @@ dim3 pack_grid(const LossArgs& a) {
     return dim3((unsigned)(a.t_pad / 32), (unsigned)ceil_div(a.width8, 8));
 }
 
+// A launch over tiles of the rows by tiles of the tokens, `blocks` of them if there are as many.
+template <typename S, typename F>
+void over_tiles(LossArgs a, long long rows, long long tokens, int blocks, F f) {
+    a.tiles = (int)ceil_div(rows, S::BM);
+    a.token_tiles = (int)ceil_div(tokens, S::BN);
+    a.splits = clamp(blocks / a.token_tiles, 1, a.tiles);
+    f(a, dim3((unsigned)(a.token_tiles * a.splits)), dim3(S::NT));
+}
+
 template <typename T>
 int forward(const LossArgs& a, const Cut& c, hipStream_t stream) {
     k_loss_pack<T, false><<<pack_grid(a), dim3(256), 0, stream>>>(a);
-    const dim3 grid((unsigned)(c.token_tiles * c.splits));
+    int splits = 0;
+    auto sum = [&](auto shape) {
+        typedef decltype(shape) S;
+        over_tiles<S>(a, a.rows, a.t, kSumBlocks, [&](const LossArgs& z, dim3 grid, dim3 block) {
+            splits = z.splits;
+            k_loss_sum<T, S><<<grid, block, 0, stream>>>(z);
+        });
+    };
     if (c.slim)
-        k_loss_sum<T, Slim<T>><<<grid, dim3(Slim<T>::NT), 0, stream>>>(a);
+        sum(Slim<T>());
+    else if (a.width <= 32)
+        sum(Narrow<T, 32>());
+    else if (a.width <= 64)
+        sum(Narrow<T, 64>());
+    else if (a.width <= 128)
+        sum(Narrow<T, 128>());
     else
-        k_loss_sum<T, Wide<T>><<<grid, dim3(Wide<T>::NT), 0, stream>>>(a);
-    k_loss_join<<<dim3((unsigned)ceil_div(a.t, 4)), dim3(256), 0, stream>>>(a);
+        sum(Logit<T>());
+    LossArgs z = a;
+    z.splits = splits;
+    k_loss_join<<<dim3((unsigned)ceil_div(a.t, 4)), dim3(256), 0, stream>>>(z);
     const hipError_t e = hipGetLastError();
     return e == hipSuccess ? VOX_OK : ssh_hip_fail(e);
 }
 
 template <typename T, typename S>
-void products(const LossArgs& a, hipStream_t stream) {
+void products(LossArgs a, hipStream_t stream) {
+    a.token_tiles = a.t_pad / S::BN;
     const long long cols = ceil_div(a.width, S::BM);
     k_loss_grad_x<T, S><<<dim3((unsigned)(cols * (a.t_pad / S::BN) * a.x_splits)), dim3(S::NT), 0, stream>>>(a);
     k_loss_grad_table<T, S><<<dim3((unsigned)(cols * (a.piece / S::BN) * a.t_splits)), dim3(S::NT), 0, stream>>>(a);
@@ -834,25 +967,31 @@ template <typename T>
 int backward(LossArgs a, const Cut& c, hipStream_t stream) {
     if (__is_same(T, f16_t)) k_loss_top<<<dim3(1), dim3(1024), 0, stream>>>(a);
     k_loss_pack<T, true><<<pack_grid(a), dim3(256), 0, stream>>>(a);
-    const int all = c.tiles * kRowTile;
+    const long long all = ceil_div(a.rows, kRowTile) * kRowTile;
     for (int p = 0; p < c.pieces; ++p) {
         a.row0 = p * c.piece;
-        a.piece = all - a.row0 < c.piece ? all - a.row0 : c.piece;
+        a.piece = (int)(all - a.row0 < c.piece ? all - a.row0 : c.piece);
         a.first = p == 0;
-        a.tiles = a.piece / kRowTile;
-        a.splits = clamp(512 / c.token_tiles, 1, a.tiles);
-        LossArgs z = a;
-        const dim3 grid((unsigned)(z.token_tiles * z.splits));
+        auto dz = [&](auto shape) {
+            typedef decltype(shape) S;
+            over_tiles<S>(a, a.piece, a.tokens_in, kDzBlocks, [&](const LossArgs& z, dim3 grid, dim3 block) {
+                k_loss_dz<T, S><<<grid, block, 0, stream>>>(z);
+            });
+        };
         if (c.slim)
-            k_loss_dz<T, Slim<T>><<<grid, dim3(Slim<T>::NT), 0, stream>>>(z);
+            dz(Slim<T>());
+        else if (a.width <= 32)
+            dz(Narrow<T, 32>());
+        else if (a.width <= 64)
+            dz(Narrow<T, 64>());
+        else if (a.width <= 128)
+            dz(Narrow<T, 128>());
         else
-            k_loss_dz<T, Wide<T>><<<grid, dim3(Wide<T>::NT), 0, stream>>>(z);
-        a.token_tiles = (int)(c.t_pad / 128);
+            dz(Logit<T>());
         if (a.width > 128)
             products<T, Wide<T>>(a, stream);
         else
             products<T, Even<T>>(a, stream);
-        a.token_tiles = c.token_tiles;
         if (c.t_splits > 1) {
             const long long there = a.rows - a.row0 < a.piece ? a.rows - a.row0 : a.piece, n = there * a.width;
             k_loss_round<T><<<dim3(clamp(ceil_div(n, 2048), 1, 1 << 20)), dim3(256), 0, stream>>>(
