@@ -112,12 +112,36 @@ __device__ __forceinline__ void stages(int total, Issue issue, Compute compute) 
         else
             load_wait<LOADS>();
         __syncthreads();  // this stage is there, and all are done with the one before
-        const int ahead = buf == 0 ? 2 : buf - 1;
-        if (i + 2 < total) issue(i + 2, ahead);
         ++since;
-        if (compute(i, buf)) since = 0;
+        // compute() starts the loads when its first reads of LDS are under way
+        const bool stored = compute(i, buf, [&] {
+            if (i + 2 < total) issue(i + 2, buf == 0 ? 2 : buf - 1);
+        });
+        if (stored) since = 0;
         buf = buf == 2 ? 0 : buf + 1;
     }
+}
+
+// Both steps of a stage: what is read, then multiplied.
+template <typename T, typename S, typename ReadA, typename ReadB, typename Next>
+__device__ __forceinline__ void products(acc16 (&acc)[S::MA][S::NB], ReadA read_a, ReadB read_b, Next next) {
+    typename Mma<T>::vec8 x[2][S::MA], y[2][S::NB];
+    auto read = [&](int s) {
+#pragma unroll
+        for (int j = 0; j < S::NB; ++j) y[s][j] = read_b(j, s);
+#pragma unroll
+        for (int i = 0; i < S::MA; ++i) x[s][i] = read_a(i, s);
+    };
+    read(0);
+    next();
+    read(1);
+    fence();
+#pragma unroll
+    for (int s = 0; s < 2; ++s)
+#pragma unroll
+        for (int i = 0; i < S::MA; ++i)
+#pragma unroll
+            for (int j = 0; j < S::NB; ++j) acc[i][j] = Mma<T>::mul(x[s][i], y[s][j], acc[i][j]);
 }
 
 // ---- operands ----------------------------------------------------------------
@@ -405,7 +429,8 @@ __device__ __forceinline__ void logits(const LossArgs& a, char* lds, int first_r
             for (int j = 0; j < S::NB; ++j) asm volatile("" : "+v"(y[s][j]));
         stages<S::kLoads, STORES>(
             t1 - t0, [&](int i, int buf) { table.load(base + buf * S::kStage, first_row + (t0 + i) * S::BM); },
-            [&](int i, int buf) {
+            [&](int i, int buf, auto next) {
+                next();
                 acc16 acc[S::MA][S::NB];
 #pragma unroll
                 for (int m = 0; m < S::MA; ++m) {
@@ -441,24 +466,15 @@ __device__ __forceinline__ void logits(const LossArgs& a, char* lds, int first_r
             tokens.load(to + S::kA, token0, k_in * kStep);
             if (++k_in == steps) k_in = 0, ++tile_in;
         },
-        [&](int, int buf) {
+        [&](int, int buf, auto next) {
             if (k == 0)
 #pragma unroll
                 for (int i = 0; i < S::MA; ++i)
 #pragma unroll
                     for (int j = 0; j < S::NB; ++j) acc[i][j] = zero16();
-#pragma unroll
-            for (int s = 0; s < 2; ++s) {
-                typename Mma<T>::vec8 x[S::MA], y[S::NB];
-#pragma unroll
-                for (int j = 0; j < S::NB; ++j) y[j] = B::read(b_at + buf * S::kStage, j, s);
-#pragma unroll
-                for (int i = 0; i < S::MA; ++i) x[i] = A::read(a_at + buf * S::kStage, i, s);
-#pragma unroll
-                for (int i = 0; i < S::MA; ++i)
-#pragma unroll
-                    for (int j = 0; j < S::NB; ++j) acc[i][j] = Mma<T>::mul(x[i], y[j], acc[i][j]);
-            }
+            products<T, S>(
+                acc, [&](int m, int s) { return A::read(a_at + buf * S::kStage, m, s); },
+                [&](int j, int s) { return B::read(b_at + buf * S::kStage, j, s); }, next);
             if (++k < steps) return false;
             done(tile, acc);
             k = 0, ++tile;
@@ -666,20 +682,11 @@ __global__ __launch_bounds__(S::NT, 2) void k_loss_grad_x(LossArgs a) {
             table.load(to, a.row0 + (k0 + i) * kStep);
             dz.load(to + S::kA, token0, (k0 + i) * kStep);
         },
-        [&](int, int buf) {
+        [&](int, int buf, auto next) {
             const unsigned on = base + buf * S::kStage;
-#pragma unroll
-            for (int s = 0; s < 2; ++s) {
-                typename Mma<T>::vec8 x[S::MA], y[S::NB];
-#pragma unroll
-                for (int j = 0; j < S::NB; ++j) y[j] = B::read(b_at + buf * S::kStage, j, s);
-#pragma unroll
-                for (int i = 0; i < S::MA; ++i) x[i] = A::read(make_uint2(a_at.x + on, a_at.y + on), a_block + i, s);
-#pragma unroll
-                for (int i = 0; i < S::MA; ++i)
-#pragma unroll
-                    for (int j = 0; j < S::NB; ++j) acc[i][j] = Mma<T>::mul(x[i], y[j], acc[i][j]);
-            }
+            products<T, S>(
+                acc, [&](int m, int s) { return A::read(make_uint2(a_at.x + on, a_at.y + on), a_block + m, s); },
+                [&](int j, int s) { return B::read(b_at + buf * S::kStage, j, s); }, next);
             return false;
         });
 #pragma unroll
@@ -734,20 +741,11 @@ __global__ __launch_bounds__(S::NT, 2) void k_loss_grad_table(LossArgs a) {
             tokens.load(to, (k0 + i) * kStep);
             dz.load(to + S::kA, (k0 + i) * kStep);
         },
-        [&](int, int buf) {
+        [&](int, int buf, auto next) {
             const unsigned x_on = base + buf * S::kStage, y_on = x_on + S::kA;
-#pragma unroll
-            for (int s = 0; s < 2; ++s) {
-                typename Mma<T>::vec8 x[S::MA], y[S::NB];
-#pragma unroll
-                for (int j = 0; j < S::NB; ++j) y[j] = B::read(make_uint2(at.x + y_on, at.y + y_on), b_block + j, s);
-#pragma unroll
-                for (int i = 0; i < S::MA; ++i) x[i] = A::read(make_uint2(at.x + x_on, at.y + x_on), a_block + i, s);
-#pragma unroll
-                for (int i = 0; i < S::MA; ++i)
-#pragma unroll
-                    for (int j = 0; j < S::NB; ++j) acc[i][j] = Mma<T>::mul(x[i], y[j], acc[i][j]);
-            }
+            products<T, S>(
+                acc, [&](int m, int s) { return A::read(make_uint2(at.x + x_on, at.y + x_on), a_block + m, s); },
+                [&](int j, int s) { return B::read(make_uint2(at.x + y_on, at.y + y_on), b_block + j, s); }, next);
             return false;
         });
     const float down = ldexpf(a.scale, -lift_of<T>(a));
@@ -956,7 +954,7 @@ int forward(const LossArgs& a, const Cut& c, hipStream_t stream) {
 }
 
 template <typename T, typename S>
-void products(LossArgs a, hipStream_t stream) {
+void gradients(LossArgs a, hipStream_t stream) {
     a.token_tiles = a.t_pad / S::BN;
     const long long cols = ceil_div(a.width, S::BM);
     k_loss_grad_x<T, S><<<dim3((unsigned)(cols * (a.t_pad / S::BN) * a.x_splits)), dim3(S::NT), 0, stream>>>(a);
@@ -989,9 +987,9 @@ int backward(LossArgs a, const Cut& c, hipStream_t stream) {
         else
             dz(Logit<T>());
         if (a.width > 128)
-            products<T, Wide<T>>(a, stream);
+            gradients<T, Wide<T>>(a, stream);
         else
-            products<T, Even<T>>(a, stream);
+            gradients<T, Even<T>>(a, stream);
         if (c.t_splits > 1) {
             const long long there = a.rows - a.row0 < a.piece ? a.rows - a.row0 : a.piece, n = there * a.width;
             k_loss_round<T><<<dim3(clamp(ceil_div(n, 2048), 1, 1 << 20)), dim3(256), 0, stream>>>(
