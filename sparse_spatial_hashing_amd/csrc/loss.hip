@@ -38,7 +38,6 @@ constexpr long long kPieceBytes = 256ll << 20;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kLowest = -3.402823466e+38f;
-constexpr int kSumBlocks = 4096, kDzBlocks = 512;
 constexpr int kLift = 14;  // fp16: dZ is 2^kLift too large
 
 struct LossArgs {
@@ -77,6 +76,7 @@ struct LossArgs {
 template <typename T, int MA_, int NB_, int WM_, int WN_>
 struct Shape {
     static constexpr int kWidth = 0;  // the width goes by in stages
+    static constexpr bool kOnce = NB_ == 1;  // a block's tokens are read from memory about once
     static constexpr int MA = MA_, NB = NB_, WM = WM_, WN = WN_;
     static constexpr int BM = 32 * MA * WM, BN = 32 * NB * WN, NT = 64 * WM * WN;
     static constexpr int kA = BM * kStep * 2, kB = BN * kStep * 2;  // bytes of a stage
@@ -89,6 +89,7 @@ struct Shape {
 // in registers, and a stage is a tile: BM rows of all their width.
 template <typename T, int W>
 struct Narrow {
+    static constexpr bool kOnce = true;
     static constexpr int kWidth = W, MA = W == 128 ? 1 : 2, NB = 2, WM = 2, WN = 2;
     static constexpr int BM = 32 * MA * WM, BN = 32 * NB * WN, NT = 64 * WM * WN;
     static constexpr int kStage = BM * W * 2, kLoads = BM * (W / 8) / NT;
@@ -98,11 +99,13 @@ struct Narrow {
 // wavefront end in the order they were issued, so a stage is there when no more are
 // under way than were issued after its loads: the next stage's, and the stores of a
 // tile that ended with the stage before, or the one before that. compute() says how
-// many those are (0, or STORES).
-template <int LOADS, int STORES, typename Issue, typename Compute>
-__device__ __forceinline__ void stages(int total, Issue issue, Compute compute) {
+// many those are (0, or STORES). begin() is what else there is to load, under way with the
+// first stages.
+template <int LOADS, int STORES, typename Begin, typename Issue, typename Compute>
+__device__ __forceinline__ void stages(int total, Begin begin, Issue issue, Compute compute) {
     if (total > 0) issue(0, 0);
     if (total > 1) issue(1, 1);
+    begin();
     int buf = 0, since = 2;
     for (int i = 0; i < total; ++i) {
         if (i + 1 == total)
@@ -122,8 +125,10 @@ __device__ __forceinline__ void stages(int total, Issue issue, Compute compute) 
     }
 }
 
-// Both steps of a stage: what is read, then multiplied.
-template <typename T, typename S, typename ReadA, typename ReadB, typename Next>
+// Both steps of a stage: what is read, then multiplied. EAGER: all is read before the first
+// product, for which an epilogue that keeps its own numbers leaves no registers at the
+// widest shape (reads of spilled ones would wait for the loads under way).
+template <typename T, typename S, bool EAGER, typename ReadA, typename ReadB, typename Next>
 __device__ __forceinline__ void products(acc16 (&acc)[S::MA][S::NB], ReadA read_a, ReadB read_b, Next next) {
     typename Mma<T>::vec8 x[2][S::MA], y[2][S::NB];
     auto read = [&](int s) {
@@ -132,16 +137,21 @@ __device__ __forceinline__ void products(acc16 (&acc)[S::MA][S::NB], ReadA read_
 #pragma unroll
         for (int i = 0; i < S::MA; ++i) x[s][i] = read_a(i, s);
     };
-    read(0);
-    next();
-    read(1);
-    fence();
-#pragma unroll
-    for (int s = 0; s < 2; ++s)
+    auto multiply = [&](int s) {
 #pragma unroll
         for (int i = 0; i < S::MA; ++i)
 #pragma unroll
             for (int j = 0; j < S::NB; ++j) acc[i][j] = Mma<T>::mul(x[s][i], y[s][j], acc[i][j]);
+    };
+    read(0);
+    next();
+    if (EAGER) {
+        read(1);
+        fence();
+    }
+    multiply(0);
+    if (!EAGER) read(1);
+    multiply(1);
 }
 
 // ---- operands ----------------------------------------------------------------
@@ -165,9 +175,10 @@ struct RowsOfMatrix {
         offset = (unsigned)row * (unsigned)(2 * st) + 16u * ((threadIdx.x & 3) ^ ((row >> 2) & 3));
     }
     __device__ __forceinline__ void load(unsigned to, int row0, int k0) const {
-        constexpr int kPer = ROWS * 4 / NT;
+        constexpr int kPer = (ROWS * 4 + NT - 1) / NT;
         static_assert(NT / 4 % 16 == 0, "the permutation is that of the first load's rows");
         const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+        if (ROWS * 4 < NT && wave * 64 >= ROWS * 4) return;
         const T* from = base + row0 * stride + k0;
         if (row0 + ROWS <= rows && k0 + kStep <= width) {
 #pragma unroll
@@ -390,12 +401,10 @@ __global__ __launch_bounds__(256) void k_loss_pack(LossArgs a) {
         if (id >= 0 && 8 * c < a.width) v = *(const uint4*)((const T*)a.x + t * a.x_stride + 8 * c);
         a.xg[(long long)c * a.t_pad + t] = v;
     }
-    if (c == 0) {
+    if (GRAD && c == 0) {
         a.came[t] = id;
-        if (GRAD) {
-            a.shift[t] = id >= 0 ? a.lse[t] * kLog2e : 0.0f;
-            a.by[t] = id >= 0 ? ldexpf(a.grad[t], lift_of<T>(a)) : 0.0f;
-        }
+        a.shift[t] = id >= 0 ? a.lse[t] * kLog2e : 0.0f;
+        a.by[t] = id >= 0 ? ldexpf(a.grad[t], lift_of<T>(a)) : 0.0f;
     }
 }
 
@@ -403,8 +412,9 @@ __global__ __launch_bounds__(256) void k_loss_pack(LossArgs a) {
 
 // Tiles [t0, t1) of the rows against a tile of tokens, from `first_row` on;
 // done(tile, acc) gets each tile's products and stores STORES times, or not at all.
-// 12,000 tokens of 128 by 214,272 rows: tokens in registers
-template <typename T, typename S, int STORES, typename Done>
+// PACKED: the tokens are read as pieces, else from x. (4,096 of 512, which every tile of rows
+// reads again: 972 us from pieces, 1,106 from x.)
+template <typename T, typename S, int STORES, bool PACKED, typename Done>
 __device__ __forceinline__ void logits(const LossArgs& a, char* lds, int first_row, int end_row, int t0, int t1,
                                        int token0, Done done) {
     if constexpr (S::kWidth) {
@@ -415,20 +425,28 @@ __device__ __forceinline__ void logits(const LossArgs& a, char* lds, int first_r
         const A table(a.table, a.t_stride, end_row, a.width);
         constexpr int kSteps = S::kWidth / 16;
         typename Mma<T>::vec8 y[kSteps][S::NB];
+        auto begin = [&] {
 #pragma unroll
         for (int s = 0; s < kSteps; ++s)
 #pragma unroll
             for (int j = 0; j < S::NB; ++j)
-                y[s][j] = __builtin_bit_cast(typename Mma<T>::vec8,
-                                             a.xg[(long long)(2 * s + half) * a.t_pad + token0 +
-                                                  (wave % S::WN) * 32 * S::NB + 32 * j + (lane & 31)]);
+            {
+                const int t = token0 + (wave % S::WN) * 32 * S::NB + 32 * j + (lane & 31), c = 2 * s + half;
+                uint4 piece = make_uint4(0, 0, 0, 0);
+                if (PACKED)
+                    piece = a.xg[(long long)c * a.t_pad + t];
+                else if (t < a.t && 8 * c < a.width)
+                    piece = *(const uint4*)((const T*)a.x + t * a.x_stride + 8 * c);
+                y[s][j] = __builtin_bit_cast(typename Mma<T>::vec8, piece);
+            }
         // settled here: inside the loop their wait would be for the tiles under way as well
 #pragma unroll
         for (int s = 0; s < kSteps; ++s)
 #pragma unroll
             for (int j = 0; j < S::NB; ++j) asm volatile("" : "+v"(y[s][j]));
+        };
         stages<S::kLoads, STORES>(
-            t1 - t0, [&](int i, int buf) { table.load(base + buf * S::kStage, first_row + (t0 + i) * S::BM); },
+            t1 - t0, begin, [&](int i, int buf) { table.load(base + buf * S::kStage, first_row + (t0 + i) * S::BM); },
             [&](int i, int buf, auto next) {
                 next();
                 acc16 acc[S::MA][S::NB];
@@ -448,18 +466,23 @@ __device__ __forceinline__ void logits(const LossArgs& a, char* lds, int first_r
             });
     } else {
     typedef RowsOfMatrix<T, S::BM, S::NT> A;
-    typedef RowsOfPieces<T, S::BN, S::NT> B;
+    typedef std::conditional_t<PACKED, RowsOfPieces<T, S::BN, S::NT>, RowsOfMatrix<T, S::BN, S::NT>> B;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, half = lane >> 5;
     const int steps = (a.width + kStep - 1) / kStep;
     const unsigned base = lds_address(lds);
     const unsigned a_at = base + A::place((wave / S::WN) * 32 * S::MA + (lane & 31), half);
     const unsigned b_at = base + S::kA + B::place((wave % S::WN) * 32 * S::NB + (lane & 31), half);
     const A table(a.table, a.t_stride, end_row, a.width);
-    const B tokens(a.xg, a.t_pad);
+    const B tokens = [&] {
+        if constexpr (PACKED)
+            return B(a.xg, a.t_pad);
+        else
+            return B(a.x, a.x_stride, a.t, a.width);
+    }();
     int tile_in = t0, k_in = 0, tile = t0, k = 0;
     acc16 acc[S::MA][S::NB];
     stages<S::kLoads, STORES>(
-        (t1 - t0) * steps,
+        (t1 - t0) * steps, [] {},
         [&](int, int buf) {
             const unsigned to = base + buf * S::kStage;
             table.load(to, first_row + tile_in * S::BM, k_in * kStep);
@@ -472,7 +495,7 @@ __device__ __forceinline__ void logits(const LossArgs& a, char* lds, int first_r
                 for (int i = 0; i < S::MA; ++i)
 #pragma unroll
                     for (int j = 0; j < S::NB; ++j) acc[i][j] = zero16();
-            products<T, S>(
+            products<T, S, S::MA * S::NB < 8>(
                 acc, [&](int m, int s) { return A::read(a_at + buf * S::kStage, m, s); },
                 [&](int j, int s) { return B::read(b_at + buf * S::kStage, j, s); }, next);
             if (++k < steps) return false;
@@ -496,9 +519,12 @@ __global__ __launch_bounds__(S::NT, 2) void k_loss_sum(LossArgs a) {
     float m[S::NB], l[S::NB];
     int came[S::NB];
 #pragma unroll
-    for (int j = 0; j < S::NB; ++j) m[j] = kLowest, l[j] = 0.0f, came[j] = a.came[token0 + token_in + 32 * j];
+    for (int j = 0; j < S::NB; ++j) {
+        const int t = token0 + token_in + 32 * j;
+        m[j] = kLowest, l[j] = 0.0f, came[j] = t < a.t ? id_of(a, t) : -1;
+    }
 
-    logits<T, S, 0>(a, lds, 0, a.rows, t0, t1, token0, [&](int tile, acc16(&acc)[S::MA][S::NB]) {
+    logits<T, S, 0, !S::kOnce>(a, lds, 0, a.rows, t0, t1, token0, [&](int tile, acc16(&acc)[S::MA][S::NB]) {
         const int row0 = tile * S::BM + row_in;
         if (row0 + 32 * S::MA > a.rows) {
 #pragma unroll
@@ -570,10 +596,18 @@ __global__ __launch_bounds__(256) void k_loss_join(LossArgs a) {
     const int t = blockIdx.x * 4 + (threadIdx.x >> 6), lane = threadIdx.x & 63;
     if (t >= a.t) return;
     float m = kLowest, l = 0.0f;
-    for (int s = lane; s < a.splits; s += 64) {
-        const float2 p = a.part[(long long)s * a.t_pad + t];
-        const float now = fmaxf(m, p.x);
-        l = l * __builtin_amdgcn_exp2f(m - now) + p.y * __builtin_amdgcn_exp2f(p.x - now);
+    constexpr int kAhead = 8;
+    for (int s = lane; s < a.splits; s += 64 * kAhead) {
+        float2 p[kAhead];
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j)
+            p[j] = s + 64 * j < a.splits ? a.part[(long long)(s + 64 * j) * a.t_pad + t] : make_float2(kLowest, 0.0f);
+        float now = m;
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) now = fmaxf(now, p[j].x);
+        l *= __builtin_amdgcn_exp2f(m - now);
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) l += p[j].y * __builtin_amdgcn_exp2f(p[j].x - now);
         m = now;
     }
 #pragma unroll
@@ -583,7 +617,7 @@ __global__ __launch_bounds__(256) void k_loss_join(LossArgs a) {
         m = now;
     }
     if (lane) return;
-    const bool has = a.came[t] >= 0;
+    const bool has = id_of(a, t) >= 0;
     const float lse2 = m + __builtin_amdgcn_logf(l);
     a.loss[t] = has ? (lse2 - a.hit[t]) * kLn2 : 0.0f;
     if (a.lse_out) a.lse_out[t] = has ? lse2 * kLn2 : 0.0f;
@@ -609,7 +643,7 @@ __global__ __launch_bounds__(S::NT, 2) void k_loss_dz(LossArgs a) {
     }
     const int token_at = __builtin_amdgcn_readfirstlane((wave % S::WN) * 32 * S::NB);
     const unsigned lane_at = half * a.t_pad + (lane & 31);
-    logits<T, S, S::MA * S::NB * 2>(a, lds, a.row0, a.rows, t0, t1, token0, [&](int tile, acc16(&acc)[S::MA][S::NB]) {
+    logits<T, S, S::MA * S::NB * 2, true>(a, lds, a.row0, a.rows, t0, t1, token0, [&](int tile, acc16(&acc)[S::MA][S::NB]) {
         const int row0 = tile * S::BM + row_in;  // in the piece
         const int left = a.rows - a.row0 - row0;
         uint4* to = a.dz + (long long)(row0 >> 3) * a.t_pad + token0 + token_at;
@@ -676,7 +710,7 @@ __global__ __launch_bounds__(S::NT, 2) void k_loss_grad_x(LossArgs a) {
 #pragma unroll
         for (int j = 0; j < S::NB; ++j) acc[i][j] = zero16();
     stages<S::kLoads, 0>(
-        k1 - k0,
+        k1 - k0, [] {},
         [&](int i, int buf) {
             const unsigned to = base + buf * S::kStage;
             table.load(to, a.row0 + (k0 + i) * kStep);
@@ -684,7 +718,7 @@ __global__ __launch_bounds__(S::NT, 2) void k_loss_grad_x(LossArgs a) {
         },
         [&](int, int buf, auto next) {
             const unsigned on = base + buf * S::kStage;
-            products<T, S>(
+            products<T, S, true>(
                 acc, [&](int m, int s) { return A::read(make_uint2(a_at.x + on, a_at.y + on), a_block + m, s); },
                 [&](int j, int s) { return B::read(b_at + buf * S::kStage, j, s); }, next);
             return false;
@@ -735,7 +769,7 @@ __global__ __launch_bounds__(S::NT, 2) void k_loss_grad_table(LossArgs a) {
 #pragma unroll
         for (int j = 0; j < S::NB; ++j) acc[i][j] = zero16();
     stages<S::kLoads, 0>(
-        k1 - k0,
+        k1 - k0, [] {},
         [&](int i, int buf) {
             const unsigned to = base + buf * S::kStage;
             tokens.load(to, (k0 + i) * kStep);
@@ -743,7 +777,7 @@ __global__ __launch_bounds__(S::NT, 2) void k_loss_grad_table(LossArgs a) {
         },
         [&](int, int buf, auto next) {
             const unsigned x_on = base + buf * S::kStage, y_on = x_on + S::kA;
-            products<T, S>(
+            products<T, S, true>(
                 acc, [&](int m, int s) { return A::read(make_uint2(at.x + x_on, at.y + x_on), a_block + m, s); },
                 [&](int j, int s) { return B::read(make_uint2(at.x + y_on, at.y + y_on), b_block + j, s); }, next);
             return false;
@@ -784,23 +818,25 @@ __global__ __launch_bounds__(S::NT, 2) void k_loss_grad_table(LossArgs a) {
     }
 }
 
-// Parts joined in order, rounded: n elements of out from `count` parts.
+// Parts joined in order, rounded: n elements of out from `count` parts. A thread has four
+// elements and loads eight parts at once.
 template <typename T>
 __global__ __launch_bounds__(256) void k_loss_round(LossArgs a, const float* part, int count, long long n,
                                                     long long pitch, T* out) {
     const float down = ldexpf(a.scale, -lift_of<T>(a));
-    for (long long i = ((long long)blockIdx.x * 256 + threadIdx.x) * 8; i < n; i += 2048ll * gridDim.x) {
-        float s[8];
-        Pack<float, 8>::load(part + i, s);
-        for (int p = 1; p < count; ++p) {
-            float v[8];
-            Pack<float, 8>::load(part + p * pitch + i, v);
+    for (long long i = ((long long)blockIdx.x * 256 + threadIdx.x) * 4; i < n; i += 1024ll * gridDim.x) {
+        float4 s = make_float4(0, 0, 0, 0);
+        constexpr int kAhead = 8;
+        for (int p = 0; p < count; p += kAhead) {
+            float4 v[kAhead];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) s[j] += v[j];
+            for (int j = 0; j < kAhead; ++j) v[j] = *(const float4*)(part + min(p + j, count - 1) * pitch + i);
+#pragma unroll
+            for (int j = 0; j < kAhead; ++j)
+                if (p + j < count) s.x += v[j].x, s.y += v[j].y, s.z += v[j].z, s.w += v[j].w;
         }
-#pragma unroll
-        for (int j = 0; j < 8; ++j) s[j] *= down;
-        Pack<T, 8>::store(out + i, s);
+        const float r[4] = {s.x * down, s.y * down, s.z * down, s.w * down};
+        Pack<T, 4>::store(out + i, r);
     }
 }
 
@@ -817,13 +853,16 @@ using Wide = Shape<T, 4, 2, 2, 2>;   // 256 x 128
 template <typename T>
 using Even = Shape<T, 2, 2, 2, 2>;   // 128 x 128
 template <typename T>
-using Logit = Even<T>;
-template <typename T>
 using Slim = Shape<T, 2, 1, 4, 1>;   // 256 x 32: few tokens
 
 long long round256(long long n) { return (n + 255) / 256 * 256; }
 long long ceil_div(long long n, long long d) { return (n + d - 1) / d; }
 int clamp(long long n, long long lo, long long hi) { return (int)(n < lo ? lo : n > hi ? hi : n); }
+
+int splits_of(long long tiles, long long token_tiles, int blocks) {
+    const long long most = tiles / 8;
+    return clamp(most * token_tiles < blocks ? blocks / token_tiles : clamp(most, 1, 4096 / token_tiles > 1 ? 4096 / token_tiles : 1), 1, tiles);
+}
 
 // How a call is cut: blocks enough for two on each of 256 CUs.
 struct Cut {
@@ -839,7 +878,7 @@ Cut cut(long long t, long long rows, long long width) {
     c.width8 = ceil_div(width, width > 128 ? 256 : 128) * (width > 128 ? 32 : 16);
     c.slim = t <= 32;
     const long long tiles = ceil_div(rows, kRowTile), token_tiles = c.slim ? 1 : c.t_pad / kTokenPad;
-    c.splits = clamp(kSumBlocks / token_tiles, 1, 4 * tiles);
+    c.splits = clamp(4096 / token_tiles, 1, 4 * tiles);
     long long piece = kPieceBytes / (2 * c.t_pad) / kRowTile * kRowTile;
     if (piece < kRowTile) piece = kRowTile;
     c.pieces = (int)ceil_div(tiles * kRowTile, piece);
@@ -868,12 +907,12 @@ Layout layout(const Cut& c, long long t, long long width, bool grad) {
         at += round256(bytes);
         return was;
     };
-    l.xg = take(c.width8 * c.t_pad * 16);
-    l.came = take(c.t_pad * 4);
+    if (grad || (!c.slim && width > 128)) l.xg = take(c.width8 * c.t_pad * 16);
     if (!grad) {
         l.hit = take(c.t_pad * 4);
         l.part = take(c.splits * c.t_pad * 8);
     } else {
+        l.came = take(c.t_pad * 4);
         l.shift = take(c.t_pad * 4);
         l.by = take(c.t_pad * 4);
         l.top = take(4);
@@ -916,22 +955,28 @@ dim3 pack_grid(const LossArgs& a) {
     return dim3((unsigned)(a.t_pad / 32), (unsigned)ceil_div(a.width8, 8));
 }
 
-// A launch over tiles of the rows by tiles of the tokens, `blocks` of them if there are as many.
+// Blocks that the card holds at once.
+template <typename S>
+constexpr int places() { return 256 * (160 * 1024 / (3 * S::kStage) < 3 ? 160 * 1024 / (3 * S::kStage) : 3); }
+
+// A launch over tiles of the rows by tiles of the tokens: eight tiles of rows or more to a block
+// while that fills every place of the card (`blocks`), then as many as fill them.
 template <typename S, typename F>
 void over_tiles(LossArgs a, long long rows, long long tokens, int blocks, F f) {
     a.tiles = (int)ceil_div(rows, S::BM);
     a.token_tiles = (int)ceil_div(tokens, S::BN);
-    a.splits = clamp(blocks / a.token_tiles, 1, a.tiles);
+    a.splits = splits_of(a.tiles, a.token_tiles, blocks);
     f(a, dim3((unsigned)(a.token_tiles * a.splits)), dim3(S::NT));
 }
 
 template <typename T>
 int forward(const LossArgs& a, const Cut& c, hipStream_t stream) {
-    k_loss_pack<T, false><<<pack_grid(a), dim3(256), 0, stream>>>(a);
+    const bool packed = !c.slim && a.width > 128;
+    if (packed) k_loss_pack<T, false><<<pack_grid(a), dim3(256), 0, stream>>>(a);
     int splits = 0;
     auto sum = [&](auto shape) {
         typedef decltype(shape) S;
-        over_tiles<S>(a, a.rows, a.t, kSumBlocks, [&](const LossArgs& z, dim3 grid, dim3 block) {
+        over_tiles<S>(a, a.rows, a.t, places<S>(), [&](const LossArgs& z, dim3 grid, dim3 block) {
             splits = z.splits;
             k_loss_sum<T, S><<<grid, block, 0, stream>>>(z);
         });
@@ -945,7 +990,7 @@ int forward(const LossArgs& a, const Cut& c, hipStream_t stream) {
     else if (a.width <= 128)
         sum(Narrow<T, 128>());
     else
-        sum(Logit<T>());
+        sum(Even<T>());
     LossArgs z = a;
     z.splits = splits;
     k_loss_join<<<dim3((unsigned)ceil_div(a.t, 4)), dim3(256), 0, stream>>>(z);
@@ -972,7 +1017,7 @@ int backward(LossArgs a, const Cut& c, hipStream_t stream) {
         a.first = p == 0;
         auto dz = [&](auto shape) {
             typedef decltype(shape) S;
-            over_tiles<S>(a, a.piece, a.tokens_in, kDzBlocks, [&](const LossArgs& z, dim3 grid, dim3 block) {
+            over_tiles<S>(a, a.piece, a.tokens_in, places<S>(), [&](const LossArgs& z, dim3 grid, dim3 block) {
                 k_loss_dz<T, S><<<grid, block, 0, stream>>>(z);
             });
         };
@@ -985,19 +1030,19 @@ int backward(LossArgs a, const Cut& c, hipStream_t stream) {
         else if (a.width <= 128)
             dz(Narrow<T, 128>());
         else
-            dz(Logit<T>());
+            dz(Wide<T>());
         if (a.width > 128)
             gradients<T, Wide<T>>(a, stream);
         else
             gradients<T, Even<T>>(a, stream);
         if (c.t_splits > 1) {
             const long long there = a.rows - a.row0 < a.piece ? a.rows - a.row0 : a.piece, n = there * a.width;
-            k_loss_round<T><<<dim3(clamp(ceil_div(n, 2048), 1, 1 << 20)), dim3(256), 0, stream>>>(
+            k_loss_round<T><<<dim3(clamp(ceil_div(n, 1024), 1, 1 << 20)), dim3(256), 0, stream>>>(
                 a, a.part_t, c.t_splits, n, (long long)a.piece * a.width, (T*)a.gt + (long long)a.row0 * a.width);
         }
     }
     const long long n = (long long)a.t * a.width;
-    k_loss_round<T><<<dim3(clamp(ceil_div(n, 2048), 1, 1 << 20)), dim3(256), 0, stream>>>(a, a.part_x, c.x_splits, n, n, (T*)a.gx);
+    k_loss_round<T><<<dim3(clamp(ceil_div(n, 1024), 1, 1 << 20)), dim3(256), 0, stream>>>(a, a.part_x, c.x_splits, n, n, (T*)a.gx);
     const hipError_t e = hipGetLastError();
     return e == hipSuccess ? VOX_OK : ssh_hip_fail(e);
 }
