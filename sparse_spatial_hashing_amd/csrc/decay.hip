@@ -477,11 +477,11 @@ __global__ __launch_bounds__(2 * W, W == 32 ? 3 : 2) void k_decay_run(DecayArgs 
     uint4 made[2];  // the chunk before, rounded, not yet stored
     acc16 wide;
     auto store = [&](int c) {
-        const int at = d.from + c * kChunk + i;
-        if (at >= d.to) return;
-        const long long token = walk.back ? d.lo + d.n - 1 - at : d.lo + at;
-        const long long row = token * out_row + head * a.width;
         if (out_wide) {
+            const int at = d.from + c * kChunk + i;
+            if (at >= d.to) return;
+            const long long token = walk.back ? d.lo + d.n - 1 - at : d.lo + at;
+            const long long row = token * out_row + head * a.width;
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
                 const int col = 32 * wave + 8 * q + 4 * half;
@@ -493,8 +493,9 @@ __global__ __launch_bounds__(2 * W, W == 32 ? 3 : 2) void k_decay_run(DecayArgs 
         }
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
-            const int col = 32 * wave + 8 * (2 * q + half);
-            if (col < a.width) *(uint4*)((T*)walk.out + row + col) = made[q];
+            const int at = d.from + c * kChunk + 16 * q + (lane & 15), col = 32 * wave + 8 * quarter_piece(lane);
+            const long long token = walk.back ? d.lo + d.n - 1 - at : d.lo + at;
+            if (at < d.to && col < a.width) *(uint4*)((T*)walk.out + token * out_row + head * a.width + col) = made[q];
         }
     };
 
@@ -565,6 +566,7 @@ __global__ __launch_bounds__(2 * W, W == 32 ? 3 : 2) void k_decay_run(DecayArgs 
                 trade_halves(x1, y1);
                 made[q] = make_uint4(x0, x1, y0, y1);
             }
+            trade_quarters(made[0], made[1]);
         }
         if (m < kChunk) D::leaving(w, walk, rate, m, half);
         if (c + 1 < chunks || walk.last) {

@@ -786,7 +786,6 @@ __global__ __launch_bounds__(S::NT, 2) void k_loss_grad_table(LossArgs a) {
 #pragma unroll
     for (int j = 0; j < S::NB; ++j) {
         const int row = row0 + 32 * (b_block + j) + (lane & 31);  // of the piece
-        const bool there = a.row0 + row < a.rows;
 #pragma unroll
         for (int i = 0; i < S::MA; ++i) {
             const int c0 = col0 + 32 * (a_block + i);
@@ -801,18 +800,24 @@ __global__ __launch_bounds__(S::NT, 2) void k_loss_grad_table(LossArgs a) {
                 }
                 continue;
             }
-            T* to = (T*)a.gt + (long long)(a.row0 + row) * a.width;
+            uint4 made[2];
 #pragma unroll
-            for (int q = 0; q < 4; q += 2) {
+            for (int q = 0; q < 2; ++q) {
                 float p[8];
 #pragma unroll
-                for (int r = 0; r < 8; ++r) p[r] = acc[i][j][4 * q + r] * down;
+                for (int r = 0; r < 8; ++r) p[r] = acc[i][j][8 * q + r] * down;
                 unsigned x0 = Mma<T>::pair(p[0], p[1]), x1 = Mma<T>::pair(p[2], p[3]);
                 unsigned y0 = Mma<T>::pair(p[4], p[5]), y1 = Mma<T>::pair(p[6], p[7]);
                 trade_halves(x0, y0);
                 trade_halves(x1, y1);
-                const int c = c0 + 8 * (q + half);
-                if (there && c < a.width) *(uint4*)(to + c) = make_uint4(x0, x1, y0, y1);
+                made[q] = make_uint4(x0, x1, y0, y1);
+            }
+            trade_quarters(made[0], made[1]);
+            const int c = c0 + 8 * quarter_piece(lane);
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                const long long at = a.row0 + row0 + 32 * (b_block + j) + 16 * q + (lane & 15);
+                if (at < a.rows && c < a.width) *(uint4*)((T*)a.gt + at * a.width + c) = made[q];
             }
         }
     }

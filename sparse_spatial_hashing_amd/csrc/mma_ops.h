@@ -100,6 +100,23 @@ __device__ __forceinline__ void trade_halves(unsigned& x, unsigned& y) {
     x = r[0], y = r[1];
 }
 
+// A block of 32 x 32 results, rounded and traded in halves, is two pieces of 16 bytes per lane:
+// lane % 32's, pieces half and 2 + half of its four. Traded here between groups of 16
+// lanes: x is that of lane % 16, y of 16 + lane % 16, both piece quarter_piece(lane), so
+// that a store writes 64 bytes in a row. (Of 32 bytes in a row, stores took a third of the
+// decay kernel's time.)
+__device__ __forceinline__ void trade_quarters(uint4& x, uint4& y) {
+    auto swap = [](unsigned& a, unsigned& b) {
+        const auto r = __builtin_amdgcn_permlane16_swap(a, b, false, false);
+        a = r[0], b = r[1];
+    };
+    swap(x.x, y.x);
+    swap(x.y, y.y);
+    swap(x.z, y.z);
+    swap(x.w, y.w);
+}
+__device__ __forceinline__ int quarter_piece(int lane) { return ((lane >> 4) & 1) * 2 + (lane >> 5); }
+
 // Consecutive logical blocks run on one XCD.
 __device__ __forceinline__ unsigned xcd_block(unsigned bid, unsigned n) {
     return (unsigned)xcd_tile(bid, n);
