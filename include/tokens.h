@@ -205,7 +205,7 @@ int tok_rotate(const void* x, int64_t tokens, int64_t heads, int64_t width, int6
  * of k's element i and v's j; NULL: zeros); last_state of the same shape (or NULL)
  * receives S after its last step (the state itself for a document of no tokens).
  * Tokens of no document get zeros and no gradient. decay is float32 on the device;
- * negative values are taken as 0 and values over 1000 as 1000. States and sums are
+ * negative values (and NaN) are taken as 0 and values over 1000 as 1000. States and sums are
  * float32; documents of more than a token or two are taken in chunks of 32 tokens
  * on matrix instructions, for which weights (q.k) exp(-decay n) and the copy of a state
  * that q is multiplied with are rounded to the tensors' type. A value that is not finite may reach every
@@ -215,7 +215,7 @@ int tok_rotate(const void* x, int64_t tokens, int64_t heads, int64_t width, int6
  * gradients too: it is the call's workspace.
  * Limits: t * heads and t at most 2^31 - 4096, 1 <= docs <= 2^20,
  * (docs + 2) * heads <= 2^30; width a multiple of 8, at most 128; strides multiples of
- * 8; all bases 16-byte aligned; scale in [1e-30, 1e30].
+ * 8, the token strides below 2^25; all bases 16-byte aligned; scale in [1e-30, 1e30].
  */
 typedef struct tok_decay {
     int32_t dtype;              /* TOK_BF16 or TOK_F16 */
@@ -265,8 +265,7 @@ int tok_decay_attend_grad(const tok_decay* args, const void* q, const void* k, c
  * contiguous, in x's type, every row written. w is rounded to that type (fp16:
  * after powers of two that bring the largest |grad| to 2^14), sums are float32.
  * Limits: 0 <= t <= 2^25, 1 <= rows <= 2^31 - 2048; width a multiple of 8, at most
- * 65536; strides multiples of 8, table_stride below 2^22; all bases 16-byte
- * aligned; scale in [1e-30, 1e30]. The workspace needs no initial contents,
+ * 65536; strides multiples of 8 below 2^22; all bases 16-byte aligned; scale in [1e-30, 1e30]. The workspace needs no initial contents,
  * 256-byte aligned.
  */
 int64_t tok_row_loss_workspace_bytes(int64_t t, int64_t rows, int64_t width);

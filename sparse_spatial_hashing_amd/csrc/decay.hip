@@ -28,6 +28,8 @@
 
 #include <hip/hip_runtime.h>
 
+#include <type_traits>
+
 #include "mma_ops.h"
 
 int ssh_hip_fail(hipError_t e);  // records the error for vox_last_hip_error()
@@ -670,7 +672,10 @@ __global__ __launch_bounds__(256) void k_decay_share(const float* part, T* out0,
 long long round256(long long n) { return (n + 255) / 256 * 256; }
 int padded(int width) { return width <= 32 ? 32 : width <= 64 ? 64 : 128; }
 
-bool stride_ok(const int64_t s[2]) { return s[0] % 8 == 0 && s[1] % 8 == 0 && s[0] >= 0 && s[1] >= 0; }
+// 16-byte pieces; a chunk's rows lie within 2^32 bytes.
+bool stride_ok(const int64_t s[2]) {
+    return s[0] % 8 == 0 && s[1] % 8 == 0 && s[0] >= 0 && s[1] >= 0 && s[0] < 1ll << 25;
+}
 
 bool check(const tok_decay* t) {
     if (!t || (t->dtype != TOK_BF16 && t->dtype != TOK_F16)) return false;

@@ -21,6 +21,8 @@
 
 #include <hip/hip_runtime.h>
 
+#include <type_traits>
+
 #include "mma_ops.h"
 
 int ssh_hip_fail(hipError_t e);  // records the error for vox_last_hip_error()
@@ -58,7 +60,7 @@ struct LossArgs {
     float* by;         // [tokens_pad]: grad times the lift (backward)
     float* hit;        // [tokens_pad]: the logit of the token's row, base 2 (forward)
     float2* part;      // [splits, tokens_pad]: maximum and sum (forward)
-    unsigned* top;     // the largest |grad|, its bits (fp16)
+    float* top;        // [tops]: the largest |grad| of each share of the tokens (fp16)
     float* part_x;     // [x_splits, tokens, width]
     float* part_t;     // [t_splits, piece rows, width] (t_splits > 1)
     long long x_stride, t_stride;
@@ -68,6 +70,7 @@ struct LossArgs {
     int row0, piece;          // rows of a piece: a multiple of kRowTile, its last ones past the table's
     int x_splits, t_splits, first;
     int tokens_in;            // tokens that dZ is written for
+    int tops;
     float scale, scale2;
 };
 
@@ -362,12 +365,13 @@ __device__ __forceinline__ int id_of(const LossArgs& a, int t) {
     return id >= 0 && id < a.rows ? (int)id : -1;
 }
 
-// The largest |grad| of tokens that have a row, for fp16. Its bits compare as the
-// numbers do; a NaN or infinity is left out.
+// The largest |grad| of tokens that have a row, for fp16, over each block's share; what is
+// not finite is left out.
+constexpr int kTops = 64;
 __global__ __launch_bounds__(1024) void k_loss_top(LossArgs a) {
     __shared__ float tops[16];
     float top = 0.0f;
-    for (int t = threadIdx.x; t < a.t; t += 1024) {
+    for (int t = blockIdx.x * 1024 + threadIdx.x; t < a.t; t += 1024 * gridDim.x) {
         const float g = id_of(a, t) >= 0 ? fabsf(a.grad[t]) : 0.0f;
         top = g <= 3.402823466e+38f ? fmaxf(top, g) : top;
     }
@@ -377,7 +381,7 @@ __global__ __launch_bounds__(1024) void k_loss_top(LossArgs a) {
     __syncthreads();
     if (threadIdx.x == 0) {
         for (int w = 1; w < 16; ++w) top = fmaxf(top, tops[w]);
-        *a.top = __float_as_uint(top);
+        a.top[blockIdx.x] = top;
     }
 }
 
@@ -385,7 +389,8 @@ __global__ __launch_bounds__(1024) void k_loss_top(LossArgs a) {
 template <typename T>
 __device__ __forceinline__ int lift_of(const LossArgs& a) {
     if (sizeof(T) == 2 && __is_same(T, bf16_t)) return 0;
-    const float top = __uint_as_float(*a.top);
+    float top = 0.0f;
+    for (int b = 0; b < a.tops; ++b) top = fmaxf(top, a.top[b]);
     return top > 0.0f ? kLift - __builtin_amdgcn_frexp_expf(top) : 0;
 }
 
@@ -553,13 +558,14 @@ __global__ __launch_bounds__(S::NT, 2) void k_loss_sum(LossArgs a) {
 #pragma unroll
                 for (int r = 0; r < 16; ++r)
                     sum += __builtin_amdgcn_exp2f(__builtin_fmaf(acc[i][j][r], a.scale2, -m[j]));
-            if (__any(!(sum <= 0x1p40f))) {
+            const bool lags = !(sum <= 0x1p40f);
+            if (__any(lags)) {
                 float top = acc[0][j][0];
 #pragma unroll
                 for (int i = 0; i < S::MA; ++i)
 #pragma unroll
                     for (int r = 0; r < 16; ++r) top = fmaxf(top, acc[i][j][r]);
-                const float now = fmaxf(m[j], top * a.scale2);
+                const float now = lags ? fmaxf(m[j], top * a.scale2) : m[j];
                 l[j] *= __builtin_amdgcn_exp2f(m[j] - now);
                 m[j] = now;
                 sum = 0.0f;
@@ -920,7 +926,7 @@ Layout layout(const Cut& c, long long t, long long width, bool grad) {
         l.came = take(c.t_pad * 4);
         l.shift = take(c.t_pad * 4);
         l.by = take(c.t_pad * 4);
-        l.top = take(4);
+        l.top = take(kTops * 4);
         l.part_x = take(c.x_splits * t * width * 4);
         l.part_t = take(c.t_splits > 1 ? (long long)c.t_splits * c.piece * width * 4 : 0);
         l.dz = take((long long)c.piece / 8 * c.t_pad * 16);
@@ -933,7 +939,9 @@ bool check(const void* x, int64_t x_stride, const void* table, int64_t table_str
            int64_t rows, int64_t width, const void* ids, int32_t id_bytes, float scale) {
     if (dtype != TOK_BF16 && dtype != TOK_F16) return false;
     if (!sizes_ok(t, rows, width) || (id_bytes != 4 && id_bytes != 8)) return false;
-    if (x_stride < 0 || x_stride % 8 || table_stride < 0 || table_stride % 8 || table_stride >= kMaxStride) return false;
+    if (x_stride < 0 || x_stride % 8 || x_stride >= kMaxStride || table_stride < 0 || table_stride % 8 ||
+        table_stride >= kMaxStride)
+        return false;
     if (!(scale >= 1e-30f) || !(scale <= 1e30f)) return false;
     if (!table || ((size_t)table & 15) || ((size_t)x & 15)) return false;
     return t == 0 || (x && ids && (size_t)ids % id_bytes == 0);
@@ -949,7 +957,7 @@ LossArgs make_args(const void* x, int64_t x_stride, const void* table, int64_t t
     a.t_pad = (int)c.t_pad, a.width8 = (int)c.width8;
     a.xg = (uint4*)(ws + l.xg), a.came = (int*)(ws + l.came);
     a.shift = (float*)(ws + l.shift), a.by = (float*)(ws + l.by), a.hit = (float*)(ws + l.hit);
-    a.part = (float2*)(ws + l.part), a.top = (unsigned*)(ws + l.top);
+    a.part = (float2*)(ws + l.part), a.top = (float*)(ws + l.top);
     a.part_x = (float*)(ws + l.part_x), a.part_t = (float*)(ws + l.part_t), a.dz = (uint4*)(ws + l.dz);
     a.piece = c.piece, a.x_splits = c.x_splits, a.t_splits = c.t_splits;
     a.tokens_in = c.slim ? 32 : (int)c.t_pad;
@@ -1013,7 +1021,8 @@ void gradients(LossArgs a, hipStream_t stream) {
 
 template <typename T>
 int backward(LossArgs a, const Cut& c, hipStream_t stream) {
-    if (__is_same(T, f16_t)) k_loss_top<<<dim3(1), dim3(1024), 0, stream>>>(a);
+    a.tops = clamp(ceil_div(a.t, 8192), 1, kTops);
+    if (__is_same(T, f16_t)) k_loss_top<<<dim3(a.tops), dim3(1024), 0, stream>>>(a);
     k_loss_pack<T, true><<<pack_grid(a), dim3(256), 0, stream>>>(a);
     const long long all = ceil_div(a.rows, kRowTile) * kRowTile;
     for (int p = 0; p < c.pieces; ++p) {

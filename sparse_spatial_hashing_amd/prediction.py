@@ -90,7 +90,7 @@ def rotary_frequencies(rotated: int, *, base: float = 10000.0, axes: int = 1, st
 
 
 def _rotate(x, pos, freqs, interleaved, inverse):
-    _unseen("rotate", x)
+    _unseen("rotate", x, freqs)
     dtype = _floating("x", x)
     index = x.get_device()
     if x.dim() != 3 or x.shape[1] < 1 or x.shape[2] < 1:
@@ -144,7 +144,10 @@ def rotate(x: torch.Tensor, pos: torch.Tensor, freqs: torch.Tensor, *, interleav
     the 2 * pairs elements of every head from 2 * c * pairs on, element p with
     element pairs + p, or ``interleaved`` 2 p with 2 p + 1; the rest of the head is
     copied. ``inverse`` turns the other way. Returns a contiguous tensor of x's
-    shape and type, rounded once. Differentiable in x."""
+    shape and type, rounded once. Differentiable in x; freqs that require a gradient are
+    refused unless gradients are off."""
+    if isinstance(freqs, torch.Tensor) and freqs.requires_grad and torch.is_grad_enabled():
+        raise ValueError("freqs are constants: no gradient is computed for them")
     if torch.is_grad_enabled() and isinstance(x, torch.Tensor) and x.requires_grad:
         return _Rotate.apply(x, pos, freqs, bool(interleaved), bool(inverse))
     return _rotate(x, pos, freqs, bool(interleaved), bool(inverse))
