@@ -63,6 +63,9 @@ def row_loss(x, table, ids, scale, grad=None):
         b = (p - one) * g[:, None]
         r = off + lse_off[:, None] + 16 * E
         b_off = p * g.abs()[:, None] * r + b.abs() * (u + 4 * E)
+        # an exponential under float32's smallest normal number is 0, and so is its product under it:
+        # off by at most that number, and by it times grad
+        b_off = b_off + 2.0 ** -126 * (1 + g.abs()[:, None])
         if x.dtype == torch.float16 and g.numel():
             b_off = b_off + 2.0 ** -37 * g.abs().max()  # half the smallest step, lifted by 2^13 at least
         small = torch.finfo(x.dtype).smallest_normal
