@@ -7,7 +7,13 @@ mixes them along their order (``gated_scan``). Training regresses how full each
 pillar is; afterwards one new token per frame attends to the frame's kept keys
 and continues the recurrence from its last state, as a decoding step does.
 
-    python examples/pillar_tokens.py [steps]
+With ``next`` it learns what comes next instead: queries and keys are turned by their
+places (``rotate``), tokens mix along their order at a cost that grows with their
+number alone (``decay_attend``), and each token's output is compared with the learned
+rows of all cells (``row_loss``); afterwards one new token per frame continues from the
+kept states and says how likely a cell is.
+
+    python examples/pillar_tokens.py [steps] [next]
 """
 import math
 import os
@@ -65,6 +71,30 @@ class PillarTokens(torch.nn.Module):
         return self.full(x + mixed).squeeze(1), state
 
 
+class NextPillar(torch.nn.Module):
+    """Which cell the next pillar of a frame is in, from the pillars before it."""
+
+    def __init__(self, cells, width=64, heads=4):
+        super().__init__()
+        self.width, self.heads = width, heads
+        self.cells = torch.nn.Parameter(torch.randn(cells, width) * width ** -0.5)
+        self.features = torch.nn.Linear(4, width)
+        self.qkv = torch.nn.Linear(width, 3 * width, bias=False)
+        self.register_buffer("decay", 2.0 ** -(1.0 + 2.0 * torch.arange(heads)))
+        self.register_buffer("freqs", ssh.rotary_frequencies(width // heads, axes=2, device="cpu"))
+
+    def forward(self, means, ids, places, offsets, state=None):
+        x = self.features(means) + ssh.embed(self.cells, ids, scale=math.sqrt(self.width))
+        qkv = self.qkv(x).to(torch.bfloat16).unflatten(1, (3 * self.heads, -1))
+        turned = ssh.rotate(qkv[:, :2 * self.heads], places, self.freqs)
+        mixed, state = ssh.decay_attend(*turned.split(self.heads, 1), qkv[:, 2 * self.heads:], self.decay, offsets,
+                                        state=state)
+        return (x + mixed.flatten(1).float()).to(torch.bfloat16), state
+
+    def loss(self, x, ids):
+        return ssh.row_loss(x, self.cells.to(torch.bfloat16), ids)
+
+
 def frames_of(device, counts=(4168, 3000, 1200)):
     """Frames of the tiny configuration, voxelized and packed."""
     p = get_config("tiny").params
@@ -108,7 +138,38 @@ def main(steps=30, device="cuda"):
     return [float(v) for v in losses], answer.tolist()
 
 
+def main_next(steps=30, device="cuda"):
+    torch.manual_seed(0)
+    inputs, _, p = frames_of(device)
+    _, ids, _, offsets = inputs
+    last = offsets[1:].long() - 1
+    following = ids.roll(-1)
+    following[last] = -1                # what follows a frame's last pillar is not known
+    model = NextPillar(p.grid[0] * p.grid[1]).to(device)
+    optimizer = torch.optim.Adam(model.parameters(), lr=3e-3)
+    losses = []
+    for _ in range(steps):
+        x, _ = model(*inputs)
+        loss = model.loss(x, following).sum() / (following >= 0).sum()
+        optimizer.zero_grad()
+        loss.backward()
+        optimizer.step()
+        losses.append(loss.detach())
+    with torch.no_grad():
+        # each frame but its last pillar, then that pillar alone from the kept states
+        frames = offsets.shape[0] - 1
+        kept = torch.ones(ids.shape[0], dtype=torch.bool, device=device)
+        kept[last] = False
+        ends = offsets - torch.arange(frames + 1, dtype=torch.int32, device=device)
+        _, state = model(*(t[kept] for t in inputs[:3]), ends)
+        one = torch.arange(frames + 1, dtype=torch.int32, device=device)
+        x, _ = model(*(t[last] for t in inputs[:3]), one, state)
+        answer = model.loss(x, ids[last])   # as likely as the same cell once more
+    return [float(v) for v in losses], answer.tolist(), model
+
+
 if __name__ == "__main__":
-    losses, answer = main(int(sys.argv[1]) if len(sys.argv) > 1 else 30)
+    steps = int(sys.argv[1]) if len(sys.argv) > 1 else 30
+    losses, answer = main_next(steps)[:2] if sys.argv[2:] == ["next"] else main(steps)
     print("loss", " ".join(f"{v:.4f}" for v in losses[:3]), "...", f"{losses[-1]:.4f}")
     print("answers", " ".join(f"{v:.3f}" for v in answer))

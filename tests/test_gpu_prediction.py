@@ -729,3 +729,27 @@ def test_refusals_on_the_gpu():
                  lambda: ssh.row_loss_grad(lse.half(), x, table, ids, lse)):
         with pytest.raises(ValueError):
             call()
+
+
+def test_example_of_the_next_pillar():
+    """It runs, every parameter has a gradient, and the loss's is that of its definition."""
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "pillar_tokens.py")
+    spec = importlib.util.spec_from_file_location("pillar_tokens_next", path)
+    example = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(example)
+    losses, answer, model = example.main_next(steps=4)
+    assert len(losses) == 4 and len(answer) == 3 and all(math.isfinite(v) for v in losses + answer)
+    for name, p in model.named_parameters():
+        assert p.grad.isfinite().all() and p.grad.any(), name
+    (means, ids, places, offsets), _, _ = example.frames_of(DEV, counts=(300,))
+    x = model(means, ids, places, offsets)[0].detach().requires_grad_()
+    following = ids.roll(-1)
+    following[-1] = -1
+    loss = model.loss(x, following)
+    grad = torch.autograd.grad(loss.sum(), x)[0]
+    table = model.cells.detach().bfloat16()
+    want = _on_gpu(ref.row_loss, x.detach(), table, following, 1.0, grad=torch.ones(ids.shape[0]))
+    check(loss, *want["loss"], "loss")
+    check(grad, *want["gx"], "gradient")
