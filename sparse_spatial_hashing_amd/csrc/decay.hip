@@ -454,10 +454,12 @@ __global__ __launch_bounds__(2 * W, W == 32 ? 3 : 2) void k_decay_run(DecayArgs 
     if (chunks > 0) issue(0, 0);
     if (D::kBuffers > 2 && chunks > 1) issue(1, 1);
     typename D::State s;
+    bool some = true;  // the state holds something
     {
         const float* from = d.from > 0   ? walk.carry + ((long long)slot * a.heads + head) * size
                             : walk.state ? walk.state + ((long long)d.doc * a.heads + head) * size
                                          : nullptr;
+        some = from != nullptr;
         D::load_state(s, from, a.width, walk.turned, column, half);
     }
     // settled here: inside the loop their wait would be for the tiles under way as well
@@ -465,7 +467,7 @@ __global__ __launch_bounds__(2 * W, W == 32 ? 3 : 2) void k_decay_run(DecayArgs 
     for (int b = 0; b < D::kBlocks; ++b) asm volatile("" : "+v"(s[b]));
 
     float w[16], near[16];
-    D::leaving(w, walk, rate, kChunk, half);
+    if (chunks > 1 || walk.last) D::leaving(w, walk, rate, kChunk, half);
 #pragma unroll
     for (int r = 0; r < 16; ++r) {
         const int key = 16 * (r / 8) + 8 * half + r % 8;
@@ -516,7 +518,7 @@ __global__ __launch_bounds__(2 * W, W == 32 ? 3 : 2) void k_decay_run(DecayArgs 
 
         acc16 p = zero16(), o = zero16();
         float up_s = 1.0f;
-        if (D::kHalf) {
+        if (D::kHalf && some) {
             float top = 0.0f;
 #pragma unroll
             for (int b = 0; b < D::kBlocks; ++b)
@@ -570,8 +572,9 @@ __global__ __launch_bounds__(2 * W, W == 32 ? 3 : 2) void k_decay_run(DecayArgs 
             }
             trade_quarters(made[0], made[1]);
         }
-        if (m < kChunk) D::leaving(w, walk, rate, m, half);
         if (c + 1 < chunks || walk.last) {
+            if (m < kChunk) D::leaving(w, walk, rate, m, half);
+            some = true;
             const float by = fallen.pass(s, rate, m, c + 1 == chunks);
             D::advance(s, make_uint2(kc_in.x + on + D::kTile, kc_in.y + on + D::kTile), v, w, by);
         }

@@ -103,8 +103,7 @@ __device__ __forceinline__ void trade_halves(unsigned& x, unsigned& y) {
 // A block of 32 x 32 results, rounded and traded in halves, is two pieces of 16 bytes per lane:
 // lane % 32's, pieces half and 2 + half of its four. Traded here between groups of 16
 // lanes: x is that of lane % 16, y of 16 + lane % 16, both piece quarter_piece(lane), so
-// that a store writes 64 bytes in a row. (Of 32 bytes in a row, stores took a third of the
-// decay kernel's time.)
+// that a store writes 64 bytes in a row.
 __device__ __forceinline__ void trade_quarters(uint4& x, uint4& y) {
     auto swap = [](unsigned& a, unsigned& b) {
         const auto r = __builtin_amdgcn_permlane16_swap(a, b, false, false);

@@ -4,7 +4,7 @@
 // Bound by memory: every element is read and written once. A thread takes one
 // piece of a token (16 bytes where the sizes allow it, or two pieces of as much
 // that hold the two halves of its pairs), computes the angles' sines and cosines
-// once and goes through the token's heads with them.
+// and turns a head or two of the token with them.
 
 #include <hip/hip_runtime.h>
 
@@ -16,6 +16,7 @@ namespace {
 
 constexpr long long kMaxTokens = (1ll << 31) - 1;
 constexpr int kThreads = 256;
+constexpr int kHeads = 2;  // of a thread, at most
 
 struct RotateArgs {
     const void* x;
@@ -57,7 +58,7 @@ __global__ __launch_bounds__(kThreads) void k_rotate(RotateArgs a) {
     const int h0 = group * a.per, h1 = min(a.heads, h0 + a.per);
     const T* x = (const T*)a.x + token * a.x_st;
     T* out = (T*)a.out + token * a.heads * a.width;
-    constexpr int kAhead = 4;  // heads whose loads are under way together
+    constexpr int kAhead = kHeads;  // all loads are under way together
 
     if (unit >= a.turned_units) {  // past the part that is turned
         const int at = 2 * a.axes * a.pairs + (unit - a.turned_units) * V;
@@ -129,10 +130,11 @@ template <typename T, int V, bool INTER>
 int launch(RotateArgs a, long long tokens, hipStream_t stream) {
     a.turned_units = a.axes * a.pairs / (INTER ? V / 2 : V);
     a.units = a.turned_units + (a.width - 2 * a.axes * a.pairs) / V;
-    // All heads to a thread while that leaves a thread for each of 256 lanes on
-    // 256 CUs, so that an angle is computed once; else fewer.
-    a.per = a.heads;
-    while (a.per > 1 && tokens * a.units * ((a.heads + a.per - 1) / a.per) < 65536) a.per = (a.per + 1) / 2;
+    // An angle is computed once for two heads: 122,880 tokens of 10 heads of 128 take 113 us
+    // (5.5 TB/s), 161 with a head each (the angles' instructions bound it), 118 with three
+    // and 130 with all ten (a wavefront then reads far apart). One head while that fills
+    // the card.
+    a.per = tokens * a.units * ((a.heads + 1) / 2) < 65536 ? 1 : a.heads < kHeads ? a.heads : kHeads;
     a.groups = (a.heads + a.per - 1) / a.per;
     a.items = tokens * a.groups * a.units;
     const long long blocks = (a.items + kThreads - 1) / kThreads, most = most_blocks(kThreads);
