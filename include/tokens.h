@@ -207,8 +207,9 @@ int tok_rotate(const void* x, int64_t tokens, int64_t heads, int64_t width, int6
  * Tokens of no document get zeros and no gradient. decay is float32 on the device;
  * negative values (and NaN) are taken as 0 and values over 1000 as 1000. States and sums are
  * float32; documents of more than a token or two are taken in chunks of 32 tokens
- * on matrix instructions, for which weights (q.k) exp(-decay n) and the copy of a state
- * that q is multiplied with are rounded to the tensors' type. A value that is not finite may reach every
+ * on matrix instructions, for which the copy of a state that q is multiplied with is
+ * rounded to the tensors' type (in fp16 after a power of two that brings the largest of
+ * 32 columns to about 1; under 2^-14 of it bits are lost). A value that is not finite may reach every
  * token of its chunk of 32 and of the document after it, and none of another one.
  * carry receives what tok_decay_attend_grad needs besides: tok_decay_carry_rows()
  * states [heads, width, width] float32 (0: NULL will do). It is needed without
@@ -263,7 +264,8 @@ int tok_decay_attend_grad(const tok_decay* args, const void* q, const void* k, c
  *   grad_x[i] = scale * sum over r of w[i, r] table[r]        [t, width]
  *   grad_table[r] = scale * sum over i of w[i, r] x[i]        [rows, width]
  * contiguous, in x's type, every row written. w is rounded to that type (fp16:
- * after powers of two that bring the largest |grad| to 2^14), sums are float32.
+ * after a power of two that brings the largest |grad| to 2^14; under 2^-28 of that
+ * bits are lost), of up to 256 tokens in two parts; sums are float32.
  * Limits: 0 <= t <= 2^25, 1 <= rows <= 2^31 - 2048; width a multiple of 8, at most
  * 65536; strides multiples of 8 below 2^22; all bases 16-byte aligned; scale in [1e-30, 1e30]. The workspace needs no initial contents,
  * 256-byte aligned.

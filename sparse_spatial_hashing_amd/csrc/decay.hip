@@ -19,10 +19,12 @@
 // number traded: register 8 c + j of half h then is row 16 c + 8 h + j.
 //
 // Roundings. The state is in 32 bits, and a result: v e^-r(m-1-j), which enters it, is
-// taken in two or three parts of the tensors' type that together hold 22 bits or more. Its
-// copy for the product with q, and the weights (q.k) e^-r(i-j), are rounded to the
-// tensors' type, as the 16-bit matrix instructions take them. In fp16 each of the three
-// is first multiplied with a power of two that brings its largest to about 1.
+// taken in two or three parts of the tensors' type that together hold 22 bits or more. The
+// weights (q.k) e^-r(i-j) are taken in two parts: a few tokens' outputs are a few weights'
+// and would show each one's rounding. The state's copy for the product with q is rounded
+// to the tensors' type, as the 16-bit matrix instructions take it: a sum of `width` such
+// roundings. In fp16 each of the three is first multiplied with a power of two that
+// brings its largest to about 1.
 //
 // Memory bounds it: k and v are read twice, all else once.
 
@@ -553,9 +555,10 @@ __global__ __launch_bounds__(2 * W, W == 32 ? 3 : 2) void k_decay_run(DecayArgs 
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
             v[j] = D::read_column(make_uint2(vc_in.x + on + 2 * D::kTile, vc_in.y + on + 2 * D::kTile), wave, j);
-            typename D::vec8 x;
+            typename D::vec8 x, rest;
 #pragma unroll
-            for (int r = 0; r < 8; ++r) x[r] = (T)p[8 * j + r];
+            for (int r = 0; r < 8; ++r) x[r] = (T)p[8 * j + r], rest[r] = (T)(p[8 * j + r] - (float)x[r]);
+            o = Mma<T>::mul(v[j], rest, o);
             o = Mma<T>::mul(v[j], x, o);
         }
         const float out_by = D::kHalf ? 1.0f / up_p : 1.0f;

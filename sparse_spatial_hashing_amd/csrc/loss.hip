@@ -15,7 +15,11 @@
 // product asks for either.
 //
 // Roundings. dZ enters the products in the tensors' type; logits, maxima, sums and
-// gradients are summed in 32 bits. In fp16 dZ is taken 2^14 times the ratio of its
+// gradients are summed in 32 bits. A token's gradient is nearly one dZ's multiple of its
+// row, and shows its rounding: of many tokens that is one rounding more of random sign
+// beside the result's own, of a few it may be twice as much. Up to kTwice tokens
+// therefore go through the backward twice, the second time with what the rounding of dZ
+// left, which costs nothing while both fit the tile of 128. In fp16 dZ is taken 2^14 times the ratio of its
 // token's grad to the largest one's power of two: it keeps all its bits down to
 // 2^-28 of that.
 
@@ -40,6 +44,7 @@ constexpr long long kPieceBytes = 256ll << 20;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kLowest = -3.402823466e+38f;
+constexpr int kTwice = 256;
 constexpr int kLift = 14;  // fp16: dZ is 2^kLift too large
 
 struct LossArgs {
@@ -65,6 +70,7 @@ struct LossArgs {
     float* part_t;     // [t_splits, piece rows, width] (t_splits > 1)
     long long x_stride, t_stride;
     int t, rows, width, width8, t_pad, id_bytes;
+    int t_all;         // t, or twice as much: tokens of the backward
     int splits, tiles;        // of the rows' tiles
     int token_tiles;
     int row0, piece;          // rows of a piece: a multiple of kRowTile, its last ones past the table's
@@ -400,16 +406,17 @@ __global__ __launch_bounds__(256) void k_loss_pack(LossArgs a) {
     const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
     const int c = (int)(i & 7) + 8 * blockIdx.y, t = (int)(i >> 3);
     if (t >= a.t_pad) return;
-    const int id = t < a.t ? id_of(a, t) : -1;
+    const int from = t < a.t ? t : t - a.t;  // of the second time
+    const int id = t < (GRAD ? a.t_all : a.t) ? id_of(a, from) : -1;
     if (c < a.width8) {
         uint4 v = make_uint4(0, 0, 0, 0);
-        if (id >= 0 && 8 * c < a.width) v = *(const uint4*)((const T*)a.x + t * a.x_stride + 8 * c);
+        if (id >= 0 && 8 * c < a.width) v = *(const uint4*)((const T*)a.x + from * a.x_stride + 8 * c);
         a.xg[(long long)c * a.t_pad + t] = v;
     }
     if (GRAD && c == 0) {
         a.came[t] = id;
-        a.shift[t] = id >= 0 ? a.lse[t] * kLog2e : 0.0f;
-        a.by[t] = id >= 0 ? ldexpf(a.grad[t], lift_of<T>(a)) : 0.0f;
+        a.shift[t] = id >= 0 ? a.lse[from] * kLog2e : 0.0f;
+        a.by[t] = id >= 0 ? ldexpf(a.grad[from], lift_of<T>(a)) : 0.0f;
     }
 }
 
@@ -642,6 +649,7 @@ __global__ __launch_bounds__(S::NT, 2) void k_loss_dz(LossArgs a) {
 
     float shift[S::NB], by[S::NB];
     int came[S::NB];
+    const bool twice = a.t_all > a.t;
 #pragma unroll
     for (int j = 0; j < S::NB; ++j) {
         const int t = token0 + token_in + 32 * j;
@@ -669,6 +677,9 @@ __global__ __launch_bounds__(S::NT, 2) void k_loss_dz(LossArgs a) {
                         if (mine == 32 * i + acc_row(r, half)) p[r] -= 1.0f;
 #pragma unroll
                 for (int r = 0; r < 16; ++r) p[r] *= by[j];
+                if (twice && token0 + token_in + 32 * j >= a.t)
+#pragma unroll
+                    for (int r = 0; r < 16; ++r) p[r] -= (float)(T)p[r];
                 if (left < 32 * S::MA)
 #pragma unroll
                     for (int r = 0; r < 16; ++r)
@@ -732,8 +743,10 @@ __global__ __launch_bounds__(S::NT, 2) void k_loss_grad_x(LossArgs a) {
 #pragma unroll
     for (int j = 0; j < S::NB; ++j) {
         const int t = token0 + (wave % S::WN) * 32 * S::NB + 32 * j + (lane & 31);
-        if (t >= a.t) continue;
-        float* to = a.part_x + ((long long)split * a.t + t) * a.width;
+        if (t >= a.t_all) continue;
+        // the second time's are further parts
+        const long long part = t < a.t ? 2 * split : 2 * split + 1;
+        float* to = a.part_x + ((a.t_all > a.t ? part : split) * a.t + (t < a.t ? t : t - a.t)) * a.width;
 #pragma unroll
         for (int i = 0; i < S::MA; ++i)
 #pragma unroll
@@ -877,17 +890,18 @@ int splits_of(long long tiles, long long token_tiles, int blocks) {
 
 // How a call is cut: blocks enough for two on each of 256 CUs.
 struct Cut {
-    long long t_pad, width8;
+    long long t_pad, width8, t_all;
     int splits, slim;  // splits: at most
     int piece, pieces, x_splits, t_splits;
 };
 
-Cut cut(long long t, long long rows, long long width) {
+Cut cut(long long t, long long rows, long long width, bool grad) {
     Cut c;
-    c.t_pad = ceil_div(t, kTokenPad) * kTokenPad;
+    c.t_all = grad && t <= kTwice ? 2 * t : t;
+    c.t_pad = ceil_div(c.t_all, kTokenPad) * kTokenPad;
     // whole tiles of columns: past the width they are zeros
     c.width8 = ceil_div(width, width > 128 ? 256 : 128) * (width > 128 ? 32 : 16);
-    c.slim = t <= 32;
+    c.slim = c.t_all <= 32;
     const long long tiles = ceil_div(rows, kRowTile), token_tiles = c.slim ? 1 : c.t_pad / kTokenPad;
     c.splits = clamp(4096 / token_tiles, 1, 4 * tiles);
     long long piece = kPieceBytes / (2 * c.t_pad) / kRowTile * kRowTile;
@@ -927,7 +941,7 @@ Layout layout(const Cut& c, long long t, long long width, bool grad) {
         l.shift = take(c.t_pad * 4);
         l.by = take(c.t_pad * 4);
         l.top = take(kTops * 4);
-        l.part_x = take(c.x_splits * t * width * 4);
+        l.part_x = take((long long)c.x_splits * c.t_all * width * 4);
         l.part_t = take(c.t_splits > 1 ? (long long)c.t_splits * c.piece * width * 4 : 0);
         l.dz = take((long long)c.piece / 8 * c.t_pad * 16);
     }
@@ -954,7 +968,7 @@ LossArgs make_args(const void* x, int64_t x_stride, const void* table, int64_t t
     a.x = x, a.x_stride = x_stride, a.table = table, a.t_stride = table_stride;
     a.t = (int)t, a.rows = (int)rows, a.width = (int)width, a.ids = ids, a.id_bytes = id_bytes;
     a.scale = scale, a.scale2 = (float)(scale * 1.4426950408889634);
-    a.t_pad = (int)c.t_pad, a.width8 = (int)c.width8;
+    a.t_pad = (int)c.t_pad, a.width8 = (int)c.width8, a.t_all = (int)c.t_all;
     a.xg = (uint4*)(ws + l.xg), a.came = (int*)(ws + l.came);
     a.shift = (float*)(ws + l.shift), a.by = (float*)(ws + l.by), a.hit = (float*)(ws + l.hit);
     a.part = (float2*)(ws + l.part), a.top = (float*)(ws + l.top);
@@ -1056,7 +1070,7 @@ int backward(LossArgs a, const Cut& c, hipStream_t stream) {
         }
     }
     const long long n = (long long)a.t * a.width;
-    k_loss_round<T><<<dim3(clamp(ceil_div(n, 1024), 1, 1 << 20)), dim3(256), 0, stream>>>(a, a.part_x, c.x_splits, n, n, (T*)a.gx);
+    k_loss_round<T><<<dim3(clamp(ceil_div(n, 1024), 1, 1 << 20)), dim3(256), 0, stream>>>(a, a.part_x, c.x_splits * (a.t_all > a.t ? 2 : 1), n, n, (T*)a.gx);
     const hipError_t e = hipGetLastError();
     return e == hipSuccess ? VOX_OK : ssh_hip_fail(e);
 }
@@ -1067,12 +1081,12 @@ extern "C" {
 
 int64_t tok_row_loss_workspace_bytes(int64_t t, int64_t rows, int64_t width) {
     if (!sizes_ok(t, rows, width)) return VOX_EINVAL;
-    return t == 0 ? 0 : layout(cut(t, rows, width), t, width, false).total;
+    return t == 0 ? 0 : layout(cut(t, rows, width, false), t, width, false).total;
 }
 
 int64_t tok_row_loss_grad_workspace_bytes(int64_t t, int64_t rows, int64_t width) {
     if (!sizes_ok(t, rows, width)) return VOX_EINVAL;
-    return t == 0 ? 0 : layout(cut(t, rows, width), t, width, true).total;
+    return t == 0 ? 0 : layout(cut(t, rows, width, true), t, width, true).total;
 }
 
 int tok_row_loss(const void* x, int64_t x_stride, const void* table, int64_t table_stride, int32_t dtype,
@@ -1081,7 +1095,7 @@ int tok_row_loss(const void* x, int64_t x_stride, const void* table, int64_t tab
     if (!check(x, x_stride, table, table_stride, dtype, t, rows, width, ids, id_bytes, scale)) return VOX_EINVAL;
     if (t == 0) return VOX_OK;
     if (!loss || ((size_t)loss | (size_t)lse) % 4) return VOX_EINVAL;
-    const Cut c = cut(t, rows, width);
+    const Cut c = cut(t, rows, width, false);
     const Layout l = layout(c, t, width, false);
     if (!workspace_ok(workspace, workspace_bytes, l.total)) return VOX_EWORKSPACE;
     LossArgs a = make_args(x, x_stride, table, table_stride, t, rows, width, ids, id_bytes, scale, c, l, (char*)workspace);
@@ -1101,7 +1115,7 @@ int tok_row_loss_grad(const float* grad, const void* x, int64_t x_stride, const 
         const hipError_t e = hipGetLastError();
         return e == hipSuccess ? VOX_OK : ssh_hip_fail(e);
     }
-    const Cut c = cut(t, rows, width);
+    const Cut c = cut(t, rows, width, true);
     const Layout l = layout(c, t, width, true);
     if (!workspace_ok(workspace, workspace_bytes, l.total)) return VOX_EWORKSPACE;
     LossArgs a = make_args(x, x_stride, table, table_stride, t, rows, width, ids, id_bytes, scale, c, l, (char*)workspace);
