@@ -241,8 +241,8 @@ def decay_attend_grad(grad_out: torch.Tensor, q: torch.Tensor, k: torch.Tensor, 
 
 class _DecayAttend(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, q, k, v, decay, offsets, state, scale, reverse):
-        out, last, carry = _decay_attend(q, k, v, decay, offsets, state, scale, reverse, True)
+    def forward(ctx, q, k, v, decay, offsets, state, scale, reverse, want_state):
+        out, last, carry = _decay_attend(q, k, v, decay, offsets, state, scale, reverse, want_state)
         ctx.save_for_backward(q, k, v, decay, carry, offsets, state)
         ctx.how = dict(scale=scale, reverse=reverse)
         ctx.mark_non_differentiable(carry)
@@ -254,7 +254,7 @@ class _DecayAttend(torch.autograd.Function):
         q, k, v, decay, carry, offsets, state = ctx.saved_tensors
         gq, gk, gv, gs = decay_attend_grad(grad, q, k, v, decay, carry, offsets, state=state, grad_state=grad_last,
                                            **ctx.how)
-        return gq, gk, gv, None, None, gs, None, None
+        return gq, gk, gv, None, None, gs, None, None, None
 
 
 def decay_attend(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, decay: torch.Tensor,
@@ -279,8 +279,7 @@ def decay_attend(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, decay: torch
     if isinstance(decay, torch.Tensor) and decay.requires_grad and torch.is_grad_enabled():
         raise ValueError("decay is a constant: no gradient is computed for it")
     if torch.is_grad_enabled() and any(isinstance(t, torch.Tensor) and t.requires_grad for t in (q, k, v, state)):
-        out, last, carry = _DecayAttend.apply(q, k, v, decay, offsets, state, scale, bool(reverse))
-        last = last if return_state else None
+        out, last, carry = _DecayAttend.apply(q, k, v, decay, offsets, state, scale, bool(reverse), bool(return_state))
     else:
         out, last, carry = _decay_attend(q, k, v, decay, offsets, state, scale, bool(reverse), return_state)
     return (out, last, carry) if return_carry else (out, last)

@@ -62,7 +62,8 @@ def row_loss(x, table, ids, scale, grad=None):
         one[torch.arange(len(came)), came] = 1.0
         b = (p - one) * g[:, None]
         r = off + lse_off[:, None] + 16 * E
-        b_off = p * g.abs()[:, None] * r + b.abs() * (u + 4 * E)
+        # rounded to the type: of up to 256 tokens in two parts
+        b_off = p * g.abs()[:, None] * r + b.abs() * ((u if t > 256 else u * u) + 4 * E)
         # an exponential under float32's smallest normal number is 0, and so is its product under it:
         # off by at most that number, and by it times grad
         b_off = b_off + 2.0 ** -126 * (1 + g.abs()[:, None])
@@ -125,11 +126,16 @@ def decay_attend(q, k, v, decay, at, scale, state=None, reverse=False, grad=None
                 top = lambda t: float(t.abs().max()) if t.numel() else 0.0
                 return 3 * drop * width * top(a) * top(b) * top(c) * float(w.sum(1).max() + 32)
 
+            # A state's copy is rounded once. Weights within 32 tokens, and what enters a state, are in
+            # parts of u^2 and less: documents of up to 32 tokens without a state round no copy.
+            def parts(state):
+                return 2 * u * u if n <= 32 and not state.any() else u + 2 * u * u
+
             S, S_abs = s0[d, h], s0[d, h].abs()
             s_low = drop * width * float(S_abs.max()) if drop else 0.0
             top = lambda t: float(t.abs().max()) if t.numel() else 0.0
             add("out", (rows, h), scale * ((w * (x @ y.T)) @ z + since[:, None] * (x @ S)),
-                scale * ((w * (x.abs() @ y.abs().T)) @ z.abs() + since[:, None] * (x.abs() @ S_abs)), 2 * u,
+                scale * ((w * (x.abs() @ y.abs().T)) @ z.abs() + since[:, None] * (x.abs() @ S_abs)), parts(S),
                 scale * (low(x, y, z) + s_low * top(x)))
             val["last"][d, h] = all_ * S + (until[:, None] * y).T @ z
             tol["last"][d, h] = (all_ * S_abs + (until[:, None] * y.abs()).T @ z.abs()) * (slack + 8 * E) \
@@ -140,13 +146,13 @@ def decay_attend(q, k, v, decay, at, scale, state=None, reverse=False, grad=None
             B, B_abs = b0[d, h], b0[d, h].abs()
             b_low = drop * width * float(B_abs.max()) if drop else 0.0
             add("gq", (rows, h), scale * ((w * (b @ z.T)) @ y + since[:, None] * (b @ S.T)),
-                scale * ((w * (b.abs() @ z.abs().T)) @ y.abs() + since[:, None] * (b.abs() @ S_abs.T)), 2 * u,
+                scale * ((w * (b.abs() @ z.abs().T)) @ y.abs() + since[:, None] * (b.abs() @ S_abs.T)), parts(S),
                 scale * (low(b, z, y) + s_low * top(b)))
             add("gk", (rows, g), scale * (w * (b @ z.T)).T @ x + until[:, None] * (z @ B.T),
-                scale * (w * (b.abs() @ z.abs().T)).T @ x.abs() + until[:, None] * (z.abs() @ B_abs.T), 2 * u,
+                scale * (w * (b.abs() @ z.abs().T)).T @ x.abs() + until[:, None] * (z.abs() @ B_abs.T), parts(B),
                 scale * low(z, b, x) + b_low * top(z))
             add("gv", (rows, g), scale * (w * (x @ y.T)).T @ b + until[:, None] * (y @ B),
-                scale * (w * (x.abs() @ y.abs().T)).T @ b.abs() + until[:, None] * (y.abs() @ B_abs), 2 * u,
+                scale * (w * (x.abs() @ y.abs().T)).T @ b.abs() + until[:, None] * (y.abs() @ B_abs), parts(B),
                 scale * low(y, x, b) + b_low * top(y))
             val["gs"][d, h] = all_ * B + scale * (since[:, None] * x).T @ b
             tol["gs"][d, h] = (all_ * B_abs + scale * (since[:, None] * x.abs()).T @ b.abs()) * (slack + 8 * E) \
