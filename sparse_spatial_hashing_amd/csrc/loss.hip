@@ -6,13 +6,24 @@
 // backward takes the logits again, a piece of the rows at a time, and writes
 // dZ = (exp(z - lse) - [row is the token's]) grad, rounded, to the workspace, from
 // where two products follow: grad_x += dZ W and grad_table = dZ^T X. A piece is as
-// many rows as keep dZ in the 256 MB of cache between HBM and the XCDs.
+// many rows as dZ of 256 MB holds, about what the cache between HBM and the XCDs does
+// (4,096 tokens of 512 by 214,272 rows: 4.0 ms; 4.5 with pieces of 128 MB, whose partial
+// sums of grad_x pass memory twice as often, and 3.9 with 2 GB).
 //
 // Tiles of 32 of the inner index go straight from memory into three buffers of LDS
 // in turn. X and dZ are kept in pieces of 8 elements, [element / 8][token]: a tile
 // is then a few runs of memory, its rows and its columns are both read without
 // conflicts, tokens without a row and tokens past the last are zeros, and no
-// product asks for either.
+// product asks for either. Tokens of up to 128 elements stay in registers while the rows go
+// by, and forward come from x itself.
+//
+// Bounds. The matrix units are busy 50 and 42% of the gradients' products (1,060 and 920
+// TFLOP/s of a step on 4,096 tokens of 512; a library product of 8192 cubed reaches 1,185
+// to 1,290): two wavefronts a SIMD wait for LDS and barriers. In the logits' passes the
+// exponentials come on top, an exp2 and two more instructions a logit forward, three and
+// the rounding backward, between the products of the other blocks of a CU: 925 TFLOP/s
+// forward and 756 for dZ at a width of 512, 1,000 at 128. A few tokens against all rows
+// are bound by memory: 110 MB in 22 us.
 //
 // Roundings. dZ enters the products in the tensors' type; logits, maxima, sums and
 // gradients are summed in 32 bits. A token's gradient is nearly one dZ's multiple of its
@@ -442,15 +453,15 @@ __device__ __forceinline__ void logits(const LossArgs& a, char* lds, int first_r
         for (int s = 0; s < kSteps; ++s)
 #pragma unroll
             for (int j = 0; j < S::NB; ++j)
-            {
-                const int t = token0 + (wave % S::WN) * 32 * S::NB + 32 * j + (lane & 31), c = 2 * s + half;
-                uint4 piece = make_uint4(0, 0, 0, 0);
-                if (PACKED)
-                    piece = a.xg[(long long)c * a.t_pad + t];
-                else if (t < a.t && 8 * c < a.width)
-                    piece = *(const uint4*)((const T*)a.x + t * a.x_stride + 8 * c);
-                y[s][j] = __builtin_bit_cast(typename Mma<T>::vec8, piece);
-            }
+                {
+                    const int t = token0 + (wave % S::WN) * 32 * S::NB + 32 * j + (lane & 31), c = 2 * s + half;
+                    uint4 piece = make_uint4(0, 0, 0, 0);
+                    if (PACKED)
+                        piece = a.xg[(long long)c * a.t_pad + t];
+                    else if (t < a.t && 8 * c < a.width)
+                        piece = *(const uint4*)((const T*)a.x + t * a.x_stride + 8 * c);
+                    y[s][j] = __builtin_bit_cast(typename Mma<T>::vec8, piece);
+                }
         // settled here: inside the loop their wait would be for the tiles under way as well
 #pragma unroll
         for (int s = 0; s < kSteps; ++s)
@@ -477,44 +488,44 @@ __device__ __forceinline__ void logits(const LossArgs& a, char* lds, int first_r
                 return true;
             });
     } else {
-    typedef RowsOfMatrix<T, S::BM, S::NT> A;
-    typedef std::conditional_t<PACKED, RowsOfPieces<T, S::BN, S::NT>, RowsOfMatrix<T, S::BN, S::NT>> B;
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, half = lane >> 5;
-    const int steps = (a.width + kStep - 1) / kStep;
-    const unsigned base = lds_address(lds);
-    const unsigned a_at = base + A::place((wave / S::WN) * 32 * S::MA + (lane & 31), half);
-    const unsigned b_at = base + S::kA + B::place((wave % S::WN) * 32 * S::NB + (lane & 31), half);
-    const A table(a.table, a.t_stride, end_row, a.width);
-    const B tokens = [&] {
-        if constexpr (PACKED)
-            return B(a.xg, a.t_pad);
-        else
-            return B(a.x, a.x_stride, a.t, a.width);
-    }();
-    int tile_in = t0, k_in = 0, tile = t0, k = 0;
-    acc16 acc[S::MA][S::NB];
-    stages<S::kLoads, STORES>(
-        (t1 - t0) * steps, [] {},
-        [&](int, int buf) {
-            const unsigned to = base + buf * S::kStage;
-            table.load(to, first_row + tile_in * S::BM, k_in * kStep);
-            tokens.load(to + S::kA, token0, k_in * kStep);
-            if (++k_in == steps) k_in = 0, ++tile_in;
-        },
-        [&](int, int buf, auto next) {
-            if (k == 0)
+        typedef RowsOfMatrix<T, S::BM, S::NT> A;
+        typedef std::conditional_t<PACKED, RowsOfPieces<T, S::BN, S::NT>, RowsOfMatrix<T, S::BN, S::NT>> B;
+        const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, half = lane >> 5;
+        const int steps = (a.width + kStep - 1) / kStep;
+        const unsigned base = lds_address(lds);
+        const unsigned a_at = base + A::place((wave / S::WN) * 32 * S::MA + (lane & 31), half);
+        const unsigned b_at = base + S::kA + B::place((wave % S::WN) * 32 * S::NB + (lane & 31), half);
+        const A table(a.table, a.t_stride, end_row, a.width);
+        const B tokens = [&] {
+            if constexpr (PACKED)
+                return B(a.xg, a.t_pad);
+            else
+                return B(a.x, a.x_stride, a.t, a.width);
+        }();
+        int tile_in = t0, k_in = 0, tile = t0, k = 0;
+        acc16 acc[S::MA][S::NB];
+        stages<S::kLoads, STORES>(
+            (t1 - t0) * steps, [] {},
+            [&](int, int buf) {
+                const unsigned to = base + buf * S::kStage;
+                table.load(to, first_row + tile_in * S::BM, k_in * kStep);
+                tokens.load(to + S::kA, token0, k_in * kStep);
+                if (++k_in == steps) k_in = 0, ++tile_in;
+            },
+            [&](int, int buf, auto next) {
+                if (k == 0)
 #pragma unroll
-                for (int i = 0; i < S::MA; ++i)
+                    for (int i = 0; i < S::MA; ++i)
 #pragma unroll
-                    for (int j = 0; j < S::NB; ++j) acc[i][j] = zero16();
-            products<T, S, S::MA * S::NB < 8>(
-                acc, [&](int m, int s) { return A::read(a_at + buf * S::kStage, m, s); },
-                [&](int j, int s) { return B::read(b_at + buf * S::kStage, j, s); }, next);
-            if (++k < steps) return false;
-            done(tile, acc);
-            k = 0, ++tile;
-            return true;
-        });
+                        for (int j = 0; j < S::NB; ++j) acc[i][j] = zero16();
+                products<T, S, S::MA * S::NB < 8>(
+                    acc, [&](int m, int s) { return A::read(a_at + buf * S::kStage, m, s); },
+                    [&](int j, int s) { return B::read(b_at + buf * S::kStage, j, s); }, next);
+                if (++k < steps) return false;
+                done(tile, acc);
+                k = 0, ++tile;
+                return true;
+            });
     }
 }
 
@@ -883,12 +894,17 @@ long long round256(long long n) { return (n + 255) / 256 * 256; }
 long long ceil_div(long long n, long long d) { return (n + d - 1) / d; }
 int clamp(long long n, long long lo, long long hi) { return (int)(n < lo ? lo : n > hi ? hi : n); }
 
-int splits_of(long long tiles, long long token_tiles, int blocks) {
-    const long long most = tiles / 8;
-    return clamp(most * token_tiles < blocks ? blocks / token_tiles : clamp(most, 1, 4096 / token_tiles > 1 ? 4096 / token_tiles : 1), 1, tiles);
+// Shares that the tiles of rows are cut into: of eight tiles or more while those fill the
+// card's places (and up to 4,096 blocks), else as many as fill them. Fewer tiles than
+// that to a block and its beginning counts: 997 tokens by 13,391 rows take 63 us with 768
+// blocks and 75 with one for each of 1,680 tiles.
+int splits_of(long long tiles, long long token_tiles, int places) {
+    const long long of_eight = tiles / 8, most = 4096 / token_tiles;
+    const long long n = of_eight * token_tiles < places ? places / token_tiles : of_eight < most ? of_eight : most;
+    return clamp(n, 1, tiles);
 }
 
-// How a call is cut: blocks enough for two on each of 256 CUs.
+// How a call is cut: the gradients' products into blocks enough for two on each of 256 CUs.
 struct Cut {
     long long t_pad, width8, t_all;
     int splits, slim;  // splits: at most
@@ -986,13 +1002,12 @@ dim3 pack_grid(const LossArgs& a) {
 template <typename S>
 constexpr int places() { return 256 * (160 * 1024 / (3 * S::kStage) < 3 ? 160 * 1024 / (3 * S::kStage) : 3); }
 
-// A launch over tiles of the rows by tiles of the tokens: eight tiles of rows or more to a block
-// while that fills every place of the card (`blocks`), then as many as fill them.
+// A launch over tiles of the rows by tiles of the tokens.
 template <typename S, typename F>
-void over_tiles(LossArgs a, long long rows, long long tokens, int blocks, F f) {
+void over_tiles(LossArgs a, long long rows, long long tokens, F f) {
     a.tiles = (int)ceil_div(rows, S::BM);
     a.token_tiles = (int)ceil_div(tokens, S::BN);
-    a.splits = splits_of(a.tiles, a.token_tiles, blocks);
+    a.splits = splits_of(a.tiles, a.token_tiles, places<S>());
     f(a, dim3((unsigned)(a.token_tiles * a.splits)), dim3(S::NT));
 }
 
@@ -1003,7 +1018,7 @@ int forward(const LossArgs& a, const Cut& c, hipStream_t stream) {
     int splits = 0;
     auto sum = [&](auto shape) {
         typedef decltype(shape) S;
-        over_tiles<S>(a, a.rows, a.t, places<S>(), [&](const LossArgs& z, dim3 grid, dim3 block) {
+        over_tiles<S>(a, a.rows, a.t, [&](const LossArgs& z, dim3 grid, dim3 block) {
             splits = z.splits;
             k_loss_sum<T, S><<<grid, block, 0, stream>>>(z);
         });
@@ -1045,7 +1060,7 @@ int backward(LossArgs a, const Cut& c, hipStream_t stream) {
         a.first = p == 0;
         auto dz = [&](auto shape) {
             typedef decltype(shape) S;
-            over_tiles<S>(a, a.piece, a.tokens_in, places<S>(), [&](const LossArgs& z, dim3 grid, dim3 block) {
+            over_tiles<S>(a, a.piece, a.tokens_in, [&](const LossArgs& z, dim3 grid, dim3 block) {
                 k_loss_dz<T, S><<<grid, block, 0, stream>>>(z);
             });
         };
