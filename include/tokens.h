@@ -205,12 +205,13 @@ int tok_rotate(const void* x, int64_t tokens, int64_t heads, int64_t width, int6
  * of k's element i and v's j; NULL: zeros); last_state of the same shape (or NULL)
  * receives S after its last step (the state itself for a document of no tokens).
  * Tokens of no document get zeros and no gradient. decay is float32 on the device;
- * negative values (and NaN) are taken as 0 and values over 1000 as 1000. States and sums are
- * float32; documents of more than a token or two are taken in chunks of 32 tokens
- * on matrix instructions, for which the copy of a state that q is multiplied with is
- * rounded to the tensors' type (in fp16 after a power of two that brings the largest of
- * 32 columns to about 1; under 2^-14 of it bits are lost). A value that is not finite may reach every
- * token of its chunk of 32 and of the document after it, and none of another one.
+ * negative values (and NaN) are taken as 0 and values over 1000 as 1000. States and
+ * sums are float32; documents of more than a token or two are taken in chunks of 32
+ * tokens on matrix instructions, for which the copy of a state that q is multiplied
+ * with is rounded to the tensors' type (in fp16 after a power of two that brings the
+ * largest of 32 columns to about 1; under 2^-14 of it bits are lost). A value that is
+ * not finite may reach every token of its chunk of 32 and of the document after it,
+ * and none of another one.
  * carry receives what tok_decay_attend_grad needs besides: tok_decay_carry_rows()
  * states [heads, width, width] float32 (0: NULL will do). It is needed without
  * gradients too: it is the call's workspace.
@@ -263,12 +264,13 @@ int tok_decay_attend_grad(const tok_decay* args, const void* q, const void* k, c
  * ids[i]]) * grad[i] for the gradient grad [t] float32 of the loss:
  *   grad_x[i] = scale * sum over r of w[i, r] table[r]        [t, width]
  *   grad_table[r] = scale * sum over i of w[i, r] x[i]        [rows, width]
- * contiguous, in x's type, every row written. w is rounded to that type (fp16:
+ * contiguous, in x's type, every row written; one of the two may be NULL and is not
+ * computed then. w is rounded to that type (fp16:
  * after a power of two that brings the largest |grad| to 2^14; under 2^-28 of that
  * bits are lost), of up to 256 tokens in two parts; sums are float32.
  * Limits: 0 <= t <= 2^25, 1 <= rows <= 2^31 - 2048; width a multiple of 8, at most
- * 65536; strides multiples of 8 below 2^22; all bases 16-byte aligned; scale in [1e-30, 1e30]. The workspace needs no initial contents,
- * 256-byte aligned.
+ * 65536; strides multiples of 8 below 2^22; all bases 16-byte aligned; scale in
+ * [1e-30, 1e30]. The workspace needs no initial contents, 256-byte aligned.
  */
 int64_t tok_row_loss_workspace_bytes(int64_t t, int64_t rows, int64_t width);
 int tok_row_loss(const void* x, int64_t x_stride, const void* table, int64_t table_stride,

@@ -62,7 +62,7 @@ struct Walk {
     void* out;            // [t, heads, width]; float32 with out_wide
     const float* state;   // [docs, heads, width, width] or null
     float* last;          // or null
-    float* carry;         // [segments, heads, width, width]: sums, then the states that enter
+    float* carry;         // [rows, heads, width, width]: sums, then the states after them
     int back;             // from a document's last token
     int turned;           // states are read transposed
     int lag;              // 1: a state counts one token on; 0: it is that of the token itself
@@ -90,6 +90,8 @@ struct Part {
     int from, to;    // tokens of this segment, in the walk's order
     bool none;       // no such segment
     bool last;
+    int row;         // of carry, for the state after it: floor(lo / segment) + its number, which
+                     // no other segment but a document's last (whose state is not kept) has
 };
 
 __device__ __forceinline__ Part find_part(const DecayArgs& a, int slot) {
@@ -117,6 +119,7 @@ __device__ __forceinline__ Part find_part(const DecayArgs& a, int slot) {
     p.from = p.none ? 0 : (int)from;
     p.to = min(p.n, p.from + a.segment);
     p.last = p.to == p.n;
+    p.row = slot - lo;
     return p;
 }
 
@@ -382,12 +385,12 @@ __global__ __launch_bounds__(2 * W, 2) void k_decay_sum(DecayArgs a) {
         D::advance(s, make_uint2(k_in.x + on, k_in.y + on), x, w, by);
         buf = buf == D::kBuffers - 1 ? 0 : buf + 1;
     }
-    D::store_state(s, walk.carry + ((long long)slot * a.heads + head) * a.width * a.width, a.width,
+    D::store_state(s, walk.carry + ((long long)d.row * a.heads + head) * a.width * a.width, a.width,
                    32 * wave + (lane & 31), half);
 }
 
-// The states that enter a document's segments, over their sums: four elements of a
-// state per thread, along the segments.
+// The states after a document's segments but the last, over their sums: four elements of
+// a state per thread, along the segments.
 __global__ __launch_bounds__(256) void k_decay_join(DecayArgs a, int slices) {
     unsigned id = a.first_block + blockIdx.x;
     const int slice = id % slices;
@@ -395,13 +398,13 @@ __global__ __launch_bounds__(256) void k_decay_join(DecayArgs a, int slices) {
     const int head = id % a.heads, doc = id / a.heads;
     const int lo = tok_boundary(a.offsets, a.docs, a.t, doc + 1);
     const int n = max(0, tok_boundary(a.offsets, a.docs, a.t, doc + 2) - lo);
-    const int parts = (n + a.segment - 1) / a.segment;
-    if (parts <= 1) return;
+    const int parts = (n + a.segment - 1) / a.segment - 1;
+    if (parts < 1) return;
     const int size = a.width * a.width, at = (slice * 256 + (int)threadIdx.x) * 4;
     if (at >= size) return;
     const long long pitch = (long long)a.heads * size;
     const Walk& walk = a.walk[0];
-    float* sum = walk.carry + (long long)(lo / a.segment + doc + 1) * pitch + (long long)head * size + at;
+    float* sum = walk.carry + (long long)(lo / a.segment) * pitch + (long long)head * size + at;
     const float through = fall(rate_of(a, head), a.segment);
     float4 h = make_float4(0, 0, 0, 0);
     if (walk.state) {
@@ -412,14 +415,74 @@ __global__ __launch_bounds__(256) void k_decay_join(DecayArgs a, int slices) {
     for (int p = 0; p < parts; p += kAhead) {
         float4 x[kAhead];
 #pragma unroll
-        for (int j = 0; j < kAhead; ++j) x[j] = *(const float4*)(sum + min(p + j, parts - 2) * pitch);
+        for (int j = 0; j < kAhead; ++j) x[j] = *(const float4*)(sum + min(p + j, parts - 1) * pitch);
 #pragma unroll
         for (int j = 0; j < kAhead; ++j) {
-            if (p + j < parts) *(float4*)(sum + (p + j) * pitch) = h;
             h.x = __builtin_fmaf(through, h.x, x[j].x), h.y = __builtin_fmaf(through, h.y, x[j].y);
             h.z = __builtin_fmaf(through, h.z, x[j].z), h.w = __builtin_fmaf(through, h.w, x[j].w);
+            if (p + j < parts) *(float4*)(sum + (p + j) * pitch) = h;
         }
     }
+}
+
+// A segment of a token or two, all in 32 bits: the block holds the state, four columns and
+// kRows rows of it to a thread, and goes through the tokens. It is read and written once: 64
+// sequences of 16 heads of 128, 134 MB, take 27 us (5.0 TB/s), 256 of them 106. A kernel of
+// its own for a call of few tokens a document took 24, but 925 us for 255 steps next to one
+// document of 257 tokens, token by token, where this takes 130.
+constexpr int kFew = 2;
+
+template <typename T, int W>
+__device__ __forceinline__ void step_through(const DecayArgs& a, const Walk& walk, const Part& d, int head,
+                                             const float* from, float* parts) {
+    constexpr int kColumns = W / 4, kGroups = 8, kRows = W / kGroups, kPiece = kRows < 8 ? kRows : 8;
+    static_assert(kColumns * kGroups == 2 * W, "a thread for each");
+    const int c = (threadIdx.x % kColumns) * 4, group = threadIdx.x / kColumns, row = group * kRows;
+    const bool on = c < a.width;
+    const long long out_row = (long long)a.heads * a.width;
+    const float through = fall(rate_of(a, head), 1);
+    float4 s[kRows];
+#pragma unroll
+    for (int j = 0; j < kRows; ++j)
+        s[j] = from && on && row + j < a.width ? *(const float4*)(from + (row + j) * a.width + c) : make_float4(0, 0, 0, 0);
+    for (int at = d.from; at < d.to; ++at) {
+        const long long token = walk.back ? d.lo + d.n - 1 - at : d.lo + at;
+        const T* q = (const T*)walk.q.p + token * walk.q.st + head * walk.q.sh + row;
+        const T* k = (const T*)walk.k.p + token * walk.k.st + (head / walk.k.group) * walk.k.sh + row;
+        const T* v = (const T*)walk.v.p + token * walk.v.st + (head / walk.v.group) * walk.v.sh;
+        float x[4] = {0, 0, 0, 0};
+        if (on) Pack<T, 4>::load(v + c, x);
+        float4 o = make_float4(0, 0, 0, 0);
+#pragma unroll
+        for (int p = 0; p < kRows; p += kPiece) {
+            float kr[kPiece], qr[kPiece];
+#pragma unroll
+            for (int j = 0; j < kPiece; ++j) kr[j] = qr[j] = 0.0f;
+            if (row + p < a.width) Pack<T, kPiece>::load(k + p, kr), Pack<T, kPiece>::load(q + p, qr);
+#pragma unroll
+            for (int j = 0; j < kPiece; ++j) {
+                float4& e = s[p + j];
+                e.x = __builtin_fmaf(through, e.x, kr[j] * x[0]), e.y = __builtin_fmaf(through, e.y, kr[j] * x[1]);
+                e.z = __builtin_fmaf(through, e.z, kr[j] * x[2]), e.w = __builtin_fmaf(through, e.w, kr[j] * x[3]);
+                o.x = __builtin_fmaf(qr[j], e.x, o.x), o.y = __builtin_fmaf(qr[j], e.y, o.y);
+                o.z = __builtin_fmaf(qr[j], e.z, o.z), o.w = __builtin_fmaf(qr[j], e.w, o.w);
+            }
+        }
+        if (at > d.from) __syncthreads();
+        *(float4*)(parts + group * W + c) = o;
+        __syncthreads();
+        if ((int)threadIdx.x < a.width) {
+            float sum = 0.0f;
+#pragma unroll
+            for (int g = 0; g < kGroups; ++g) sum += parts[g * W + threadIdx.x];
+            ((T*)walk.out)[token * out_row + head * a.width + threadIdx.x] = (T)(sum * walk.enter_by);
+        }
+    }
+    if (!d.last || !walk.last || !on) return;
+    float* to = walk.last + ((long long)d.doc * a.heads + head) * a.width * a.width;
+#pragma unroll
+    for (int j = 0; j < kRows; ++j)
+        if (row + j < a.width) *(float4*)(to + (row + j) * a.width + c) = s[j];
 }
 
 // A segment from the state that enters it.
@@ -447,6 +510,13 @@ __global__ __launch_bounds__(2 * W, W == 32 ? 3 : 2) void k_decay_run(DecayArgs 
         return;
     }
     const long long size = (long long)a.width * a.width;
+    const float* from = d.from > 0   ? walk.carry + ((long long)(d.row - 1) * a.heads + head) * size
+                        : walk.state ? walk.state + ((long long)d.doc * a.heads + head) * size
+                                     : nullptr;
+    if (a.walks == 1 && d.to - d.from <= kFew) {  // forward
+        step_through<T, W>(a, walk, d, head, from, (float*)lds);
+        return;
+    }
     const int column = 32 * wave + i;
     const float rate = rate_of(a, head);
     const unsigned base = lds_address(lds);
@@ -462,14 +532,8 @@ __global__ __launch_bounds__(2 * W, W == 32 ? 3 : 2) void k_decay_run(DecayArgs 
     if (chunks > 0) issue(0, 0);
     if (D::kBuffers > 2 && chunks > 1) issue(1, 1);
     typename D::State s;
-    bool some = true;  // the state holds something
-    {
-        const float* from = d.from > 0   ? walk.carry + ((long long)slot * a.heads + head) * size
-                            : walk.state ? walk.state + ((long long)d.doc * a.heads + head) * size
-                                         : nullptr;
-        some = from != nullptr;
-        D::load_state(s, from, a.width, walk.turned, column, half);
-    }
+    bool some = from != nullptr;  // the state holds something
+    D::load_state(s, from, a.width, walk.turned, column, half);
     // settled here: inside the loop their wait would be for the tiles under way as well
 #pragma unroll
     for (int b = 0; b < D::kBlocks; ++b) asm volatile("" : "+v"(s[b]));
@@ -593,73 +657,6 @@ __global__ __launch_bounds__(2 * W, W == 32 ? 3 : 2) void k_decay_run(DecayArgs 
     if (d.last && walk.last) D::store_state(s, walk.last + ((long long)d.doc * a.heads + head) * size, a.width, column, half);
 }
 
-// Documents of one token or two: a block per document and head holds the state and
-// goes through the tokens, all in 32 bits. A thread has four columns and every
-// (threads / columns)th row.
-constexpr int kStepThreads = 256;
-
-template <typename T, int W>
-__global__ __launch_bounds__(kStepThreads) void k_decay_step(DecayArgs a) {
-    constexpr int kColumns = W / 4, kGroups = kStepThreads / kColumns, kRows = (W + kGroups - 1) / kGroups;
-    __shared__ float4 parts[kGroups][kColumns];
-    const Walk& walk = a.walk[0];
-    const unsigned id = a.first_block + blockIdx.x;
-    const int head = id % a.heads, range = id / a.heads;  // 0 and docs + 1: of no document
-    const int lo = tok_boundary(a.offsets, a.docs, a.t, range);
-    const int n = max(0, tok_boundary(a.offsets, a.docs, a.t, range + 1) - lo);
-    const long long out_row = (long long)a.heads * a.width;
-    T* out = (T*)walk.out + head * a.width;
-    if (range < 1 || range > a.docs) {
-        for (int s = 0; s < n; ++s)
-            for (int c = threadIdx.x; c < a.width; c += kStepThreads) out[(lo + s) * out_row + c] = (T)0.0f;
-        return;
-    }
-    const long long at = ((long long)(range - 1) * a.heads + head) * a.width * a.width;
-    const int c = (threadIdx.x % kColumns) * 4, group = threadIdx.x / kColumns;
-    const bool on = c < a.width;
-    const float through = fall(rate_of(a, head), 1);
-    float4 s[kRows];
-#pragma unroll
-    for (int j = 0; j < kRows; ++j) {
-        const int row = group + j * kGroups;
-        s[j] = walk.state && on && row < a.width ? *(const float4*)(walk.state + at + row * a.width + c) : make_float4(0, 0, 0, 0);
-    }
-    for (int step = 0; step < n; ++step) {
-        const long long token = walk.back ? lo + n - 1 - step : lo + step;
-        const T* q = (const T*)walk.q.p + token * walk.q.st + head * walk.q.sh;
-        const T* k = (const T*)walk.k.p + token * walk.k.st + (head / walk.k.group) * walk.k.sh;
-        const T* v = (const T*)walk.v.p + token * walk.v.st + (head / walk.v.group) * walk.v.sh;
-        float x[4] = {0, 0, 0, 0};
-        if (on) Pack<T, 4>::load(v + c, x);
-        float4 o = make_float4(0, 0, 0, 0);
-#pragma unroll
-        for (int j = 0; j < kRows; ++j) {
-            const int row = group + j * kGroups;
-            if (row >= a.width) continue;
-            const float kr = (float)k[row], qr = (float)q[row];
-            s[j].x = __builtin_fmaf(through, s[j].x, kr * x[0]), s[j].y = __builtin_fmaf(through, s[j].y, kr * x[1]);
-            s[j].z = __builtin_fmaf(through, s[j].z, kr * x[2]), s[j].w = __builtin_fmaf(through, s[j].w, kr * x[3]);
-            o.x = __builtin_fmaf(qr, s[j].x, o.x), o.y = __builtin_fmaf(qr, s[j].y, o.y);
-            o.z = __builtin_fmaf(qr, s[j].z, o.z), o.w = __builtin_fmaf(qr, s[j].w, o.w);
-        }
-        if (step > 0) __syncthreads();
-        parts[group][threadIdx.x % kColumns] = o;
-        __syncthreads();
-        for (int e = threadIdx.x; e < a.width; e += kStepThreads) {
-            float sum = 0.0f;
-#pragma unroll
-            for (int g = 0; g < kGroups; ++g) sum += ((const float*)parts[g])[e];
-            out[token * out_row + e] = (T)(sum * walk.enter_by);
-        }
-    }
-    if (!walk.last || !on) return;
-#pragma unroll
-    for (int j = 0; j < kRows; ++j) {
-        const int row = group + j * kGroups;
-        if (row < a.width) *(float4*)(walk.last + at + row * a.width + c) = s[j];
-    }
-}
-
 // Gradients of shared heads: the query heads' parts, in order, rounded. Of two tensors,
 // the second's parts behind the first's.
 template <typename T>
@@ -700,10 +697,12 @@ bool check(const tok_decay* t) {
     return stride_ok(t->q_stride) && stride_ok(t->k_stride) && stride_ok(t->v_stride);
 }
 
-bool by_step(const tok_decay& t) { return t.t <= 2ll * t.docs; }
-// Short documents that fill the card with one block each (and head): no segments, which
-// saves two launches of sums. (At worst one document holds all 16,384 tokens.)
-bool by_doc(const tok_decay& t) { return t.t <= 64ll * t.docs && t.t <= 16384 && (long long)t.docs * t.heads >= 512; }
+// Short documents that fill the card with one block each (and head), or steps of decoding: no
+// segments, which saves two launches, each some 5 us of a call of 14. (At worst one document
+// holds all 16,384 tokens.)
+bool by_doc(const tok_decay& t) {
+    return t.t <= 16384 && (t.t <= 2ll * t.docs || (t.t <= 64ll * t.docs && (long long)t.docs * t.heads >= 512));
+}
 
 // Tokens of a segment: as many as leave a block for every place the card has (two blocks of
 // four wavefronts a CU, and as many more as they have fewer) and none for a second round,
@@ -711,7 +710,7 @@ bool by_doc(const tok_decay& t) { return t.t <= 64ll * t.docs && t.t <= 16384 &&
 // segment passes memory with its state four times. 122,880 tokens of 8 heads of 128: 536
 // blocks take 320 us, 504 take 240.
 int segment_of(const tok_decay& t) {
-    if (by_step(t) || by_doc(t)) return (int)((t.t + 127) / 128 * 128) + 128;  // one
+    if (by_doc(t)) return (int)((t.t + 127) / 128 * 128) + 128;  // one
     const long long each = 512ll * 128 / padded(t.width) / t.heads;  // of a head
     long long n = each - t.docs - 2;
     if (n < each / 2) n = each / 2;
@@ -774,15 +773,8 @@ void run(DecayArgs a, hipStream_t stream) {
 
 template <typename T, int W>
 int forward(const tok_decay& t, DecayArgs a, hipStream_t stream) {
-    if (by_step(t)) {
-        in_launches((a.docs + 2ll) * a.heads, kStepThreads, [&](unsigned first, dim3 grid) {
-            a.first_block = first;
-            k_decay_step<T, W><<<grid, dim3(kStepThreads), 0, stream>>>(a);
-        });
-    } else {
-        if (!whole(t)) states<T, W>(a, stream);
-        run<T, W>(a, stream);
-    }
+    if (!whole(t)) states<T, W>(a, stream);
+    run<T, W>(a, stream);
     const hipError_t e = hipGetLastError();
     return e == hipSuccess ? VOX_OK : ssh_hip_fail(e);
 }
@@ -833,7 +825,8 @@ int by_width(int width, F f) {
 
 bool aligned16(const void* p) { return ((size_t)p & 15) == 0; }
 
-long long carry_elems(const tok_decay& t) { return whole(t) ? 0 : slots(t) * state_elems(t); }
+long long carry_rows(const tok_decay& t) { return whole(t) ? 0 : t.t / segment_of(t); }
+long long carry_elems(const tok_decay& t) { return carry_rows(t) * state_elems(t); }
 long long part_elems(const tok_decay& t) { return t.heads == t.kv_heads ? 0 : 2 * t.t * t.heads * t.width; }
 
 }  // namespace
@@ -842,7 +835,7 @@ extern "C" {
 
 int64_t tok_decay_carry_rows(const tok_decay* t) {
     if (!check(t)) return VOX_EINVAL;
-    return whole(*t) ? 0 : slots(*t);
+    return carry_rows(*t);
 }
 
 int64_t tok_decay_grad_workspace_bytes(const tok_decay* t) {

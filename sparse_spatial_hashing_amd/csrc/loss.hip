@@ -1044,8 +1044,10 @@ template <typename T, typename S>
 void gradients(LossArgs a, hipStream_t stream) {
     a.token_tiles = a.t_pad / S::BN;
     const long long cols = ceil_div(a.width, S::BM);
-    k_loss_grad_x<T, S><<<dim3((unsigned)(cols * (a.t_pad / S::BN) * a.x_splits)), dim3(S::NT), 0, stream>>>(a);
-    k_loss_grad_table<T, S><<<dim3((unsigned)(cols * (a.piece / S::BN) * a.t_splits)), dim3(S::NT), 0, stream>>>(a);
+    if (a.gx)
+        k_loss_grad_x<T, S><<<dim3((unsigned)(cols * (a.t_pad / S::BN) * a.x_splits)), dim3(S::NT), 0, stream>>>(a);
+    if (a.gt)
+        k_loss_grad_table<T, S><<<dim3((unsigned)(cols * (a.piece / S::BN) * a.t_splits)), dim3(S::NT), 0, stream>>>(a);
 }
 
 template <typename T>
@@ -1078,14 +1080,16 @@ int backward(LossArgs a, const Cut& c, hipStream_t stream) {
             gradients<T, Wide<T>>(a, stream);
         else
             gradients<T, Even<T>>(a, stream);
-        if (c.t_splits > 1) {
+        if (a.gt && c.t_splits > 1) {
             const long long there = a.rows - a.row0 < a.piece ? a.rows - a.row0 : a.piece, n = there * a.width;
             k_loss_round<T><<<dim3(clamp(ceil_div(n, 1024), 1, 1 << 20)), dim3(256), 0, stream>>>(
                 a, a.part_t, c.t_splits, n, (long long)a.piece * a.width, (T*)a.gt + (long long)a.row0 * a.width);
         }
     }
     const long long n = (long long)a.t * a.width;
-    k_loss_round<T><<<dim3(clamp(ceil_div(n, 1024), 1, 1 << 20)), dim3(256), 0, stream>>>(a, a.part_x, c.x_splits * (a.t_all > a.t ? 2 : 1), n, n, (T*)a.gx);
+    if (a.gx)
+        k_loss_round<T><<<dim3(clamp(ceil_div(n, 1024), 1, 1 << 20)), dim3(256), 0, stream>>>(
+            a, a.part_x, c.x_splits * (a.t_all > a.t ? 2 : 1), n, n, (T*)a.gx);
     const hipError_t e = hipGetLastError();
     return e == hipSuccess ? VOX_OK : ssh_hip_fail(e);
 }
@@ -1123,9 +1127,10 @@ int tok_row_loss_grad(const float* grad, const void* x, int64_t x_stride, const 
                       const float* lse, float scale, void* grad_x, void* grad_table, void* workspace,
                       int64_t workspace_bytes, hipStream_t stream) {
     if (!check(x, x_stride, table, table_stride, dtype, t, rows, width, ids, id_bytes, scale)) return VOX_EINVAL;
-    if (!grad_table || (((size_t)grad_x | (size_t)grad_table) & 15)) return VOX_EINVAL;
-    if (t && (!grad || !lse || !grad_x || ((size_t)grad | (size_t)lse) % 4)) return VOX_EINVAL;
+    if ((t && !grad_x && !grad_table) || (((size_t)grad_x | (size_t)grad_table) & 15)) return VOX_EINVAL;
+    if (t && (!grad || !lse || ((size_t)grad | (size_t)lse) % 4)) return VOX_EINVAL;
     if (t == 0) {
+        if (!grad_table) return VOX_OK;
         k_loss_clear<<<dim3(2048), dim3(256), 0, stream>>>((uint4*)grad_table, rows * width / 8);
         const hipError_t e = hipGetLastError();
         return e == hipSuccess ? VOX_OK : ssh_hip_fail(e);

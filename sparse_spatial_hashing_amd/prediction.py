@@ -335,6 +335,10 @@ def row_loss_grad(grad_loss: torch.Tensor, x: torch.Tensor, table: torch.Tensor,
                   lse: torch.Tensor, *, scale: float = 1.0) -> Tuple[torch.Tensor, torch.Tensor]:
     """Gradients of ``row_loss``'s x and table from that of the loss (float32
     [*ids.shape]), with the lse it returned and the same other arguments."""
+    return _row_loss_grad(grad_loss, x, table, ids, lse, scale, True, True)
+
+
+def _row_loss_grad(grad_loss, x, table, ids, lse, scale, want_x, want_table):
     _unseen("row_loss_grad", grad_loss, x, table, lse)
     kept, args, scale = _loss_args(x, table, ids, scale)
     t, rows, width = args[5:8]
@@ -345,13 +349,13 @@ def row_loss_grad(grad_loss: torch.Tensor, x: torch.Tensor, table: torch.Tensor,
             raise ValueError(f"{name} must be a float32 tensor of shape {tuple(ids.shape)}")
     grad_loss, lse = grad_loss.contiguous(), lse.contiguous()
     nbytes = _size(_lib.tok_row_loss_grad_workspace_bytes(t, rows, width), "tok_row_loss_grad_workspace_bytes")
-    gx, gt = x.new_empty((t, width)), x.new_empty((rows, width))
+    gx = x.new_empty((t, width)) if want_x else None
+    gt = x.new_empty((rows, width)) if want_table else None
     ws = _workspace(nbytes, x)
     _call(_lib.tok_row_loss_grad, "tok_row_loss_grad", index, grad_loss.data_ptr(), *args, lse.data_ptr(), scale,
-          gx.data_ptr(), gt.data_ptr(), _ptr(ws), nbytes)
-    if width != x.shape[-1]:
-        gx, gt = gx[:, :x.shape[-1]].contiguous(), gt[:, :x.shape[-1]].contiguous()
-    return gx.view(x.shape), gt
+          _address(gx), _address(gt), _ptr(ws), nbytes)
+    gx, gt = (g if g is None or width == x.shape[-1] else g[:, :x.shape[-1]].contiguous() for g in (gx, gt))
+    return None if gx is None else gx.view(x.shape), gt
 
 
 class _RowLoss(torch.autograd.Function):
@@ -366,7 +370,7 @@ class _RowLoss(torch.autograd.Function):
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, grad, _):
-        gx, gt = row_loss_grad(grad, *ctx.saved_tensors, scale=ctx.scale)
+        gx, gt = _row_loss_grad(grad, *ctx.saved_tensors, ctx.scale, *ctx.needs_input_grad[:2])
         return gx, gt, None, None
 
 
@@ -382,7 +386,7 @@ def row_loss(x: torch.Tensor, table: torch.Tensor, ids: torch.Tensor, *, scale: 
     and stays under some hundred MiB. With ``return_lse`` also the log of the sum
     (float32, 0 without a row, not differentiable). A width that is no multiple of 8
     is copied into one that is, by each call; so are rows off 16 bytes or 8 MiB and
-    more apart. Differentiable in x and table, always both."""
+    more apart. Differentiable in x and table; what needs no gradient costs none."""
     if torch.is_grad_enabled() and any(isinstance(v, torch.Tensor) and v.requires_grad for v in (x, table)):
         loss, lse = _RowLoss.apply(x, table, ids, scale)
     else:

@@ -181,6 +181,22 @@ def test_decay_attend_segments(dtype, width, heads, kv_heads, lens):
     _decay_compare(s, at, f"decay segments reverse {dtype} {lens} width {width}", True, 0.3)
 
 
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("reverse", [False, True])
+@pytest.mark.parametrize("width,heads,kv_heads", [(8, 2, 1), (40, 1, 1), (128, 2, 2)])
+def test_decay_steps_next_to_documents(dtype, reverse, width, heads, kv_heads):
+    """Sequences that take a step, and some that begin, in one call."""
+    for lens, first in (([1] * 40 + [75] + [0, 2, 0, 1, 33], 0), ([0] * 300 + [400], 2), ([129, 1, 130, 2, 1], 1)):
+        s, at = _decay_case(lens, heads, kv_heads, width, dtype, 17, first)
+        _decay_compare(s, at, f"decay steps and documents {dtype} {len(lens)} width {width}", reverse)
+
+
+def test_decay_steps_of_many_sequences():
+    """More tokens than documents of one segment may have."""
+    s, at = _decay_case([1] * 16000 + [900, 2] + [1] * 100, 1, 1, 8, BF16, 19)
+    _decay_compare(s, at, "decay steps of many")
+
+
 def _on_gpu(f, *args, **more):
     """The 64-bit reference with its work on the GPU, its results back on the host."""
     move = lambda x, d: x.to(d) if isinstance(x, torch.Tensor) else x
@@ -530,6 +546,23 @@ def test_row_loss_strides_and_autograd():
     leaf = wide_x[:, :64].to(DEV).requires_grad_()
     ssh.row_loss(leaf[:60], leaf[:80], ids[:60].to(DEV)).mean().backward()  # both from one tensor
     assert leaf.grad[:60].any() and leaf.grad[60:80].any() and not leaf.grad[80:].any()
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("t,rows,width", [(0, 9, 16), (7, 40, 24), (300, 700, 100), (500, 9000, 136)])
+def test_row_loss_one_gradient(dtype, t, rows, width):
+    """The same as of both, where the other is of a constant."""
+    gen = torch.Generator().manual_seed(t)
+    x, table = _randn((t, width), dtype, gen).to(DEV), _randn((rows, width), dtype, gen).to(DEV)
+    ids, grad = torch.randint(0, rows, (t,), generator=gen).to(DEV), torch.rand(t, generator=gen).to(DEV)
+    _, lse = ssh.row_loss(x, table, ids, return_lse=True)
+    both = ssh.row_loss_grad(grad, x, table, ids, lse)
+    for n in (0, 1):
+        leaves = [x.clone(), table.clone()]
+        leaves[n].requires_grad_()
+        print(f"row loss, one gradient {dtype} {t} {rows} {width} {n}", flush=True)
+        ssh.row_loss(*leaves, ids).backward(grad)
+        assert torch.equal(leaves[n].grad, both[n]) and leaves[1 - n].grad is None
 
 
 def test_row_loss_writes_nothing_outside():
