@@ -450,10 +450,9 @@ __device__ __forceinline__ void logits(const LossArgs& a, char* lds, int first_r
         typename Mma<T>::vec8 y[kSteps][S::NB];
         auto begin = [&] {
 #pragma unroll
-        for (int s = 0; s < kSteps; ++s)
+            for (int s = 0; s < kSteps; ++s)
 #pragma unroll
-            for (int j = 0; j < S::NB; ++j)
-                {
+                for (int j = 0; j < S::NB; ++j) {
                     const int t = token0 + (wave % S::WN) * 32 * S::NB + 32 * j + (lane & 31), c = 2 * s + half;
                     uint4 piece = make_uint4(0, 0, 0, 0);
                     if (PACKED)
@@ -462,11 +461,11 @@ __device__ __forceinline__ void logits(const LossArgs& a, char* lds, int first_r
                         piece = *(const uint4*)((const T*)a.x + t * a.x_stride + 8 * c);
                     y[s][j] = __builtin_bit_cast(typename Mma<T>::vec8, piece);
                 }
-        // settled here: inside the loop their wait would be for the tiles under way as well
+            // settled here: inside the loop their wait would be for the tiles under way as well
 #pragma unroll
-        for (int s = 0; s < kSteps; ++s)
+            for (int s = 0; s < kSteps; ++s)
 #pragma unroll
-            for (int j = 0; j < S::NB; ++j) asm volatile("" : "+v"(y[s][j]));
+                for (int j = 0; j < S::NB; ++j) asm volatile("" : "+v"(y[s][j]));
         };
         stages<S::kLoads, STORES>(
             t1 - t0, begin, [&](int i, int buf) { table.load(base + buf * S::kStage, first_row + (t0 + i) * S::BM); },
@@ -714,11 +713,9 @@ __global__ __launch_bounds__(S::NT, 2) void k_loss_dz(LossArgs a) {
 // grad_x of a piece: [width x tokens] = W^T dZ over a share of the piece's rows,
 // added to what the pieces before left in its part.
 template <typename T, typename S>
-__global__ __launch_bounds__(S::NT, 2) void k_loss_grad_x(LossArgs a) {
+__device__ __forceinline__ void grad_x(const LossArgs& a, unsigned id, char* lds) {
     typedef ColumnsOfMatrix<T, S::BM, S::NT> A;
     typedef RowsOfPieces<T, S::BN, S::NT> B;
-    __shared__ __align__(1024) char lds[3 * S::kStage];
-    unsigned id = xcd_block(blockIdx.x, gridDim.x);
     const int col_tiles = (a.width + S::BM - 1) / S::BM;
     const int col0 = (id % col_tiles) * S::BM;
     id /= col_tiles;
@@ -776,11 +773,9 @@ __global__ __launch_bounds__(S::NT, 2) void k_loss_grad_x(LossArgs a) {
 
 // grad_table of a piece: [width x rows] = X^T dZ over a share of the tokens.
 template <typename T, typename S>
-__global__ __launch_bounds__(S::NT, 2) void k_loss_grad_table(LossArgs a) {
+__device__ __forceinline__ void grad_table(const LossArgs& a, unsigned id, char* lds) {
     typedef ColumnsOfPieces<T, S::BM, S::NT> A;
     typedef ColumnsOfPieces<T, S::BN, S::NT> B;
-    __shared__ __align__(1024) char lds[3 * S::kStage];
-    unsigned id = xcd_block(blockIdx.x, gridDim.x);
     const int col_tiles = (a.width + S::BM - 1) / S::BM, row_tiles = a.piece / S::BN;
     const int col0 = (id % col_tiles) * S::BM;
     id /= col_tiles;
@@ -853,25 +848,41 @@ __global__ __launch_bounds__(S::NT, 2) void k_loss_grad_table(LossArgs a) {
     }
 }
 
+// Both in one launch, the first x_blocks blocks grad_x's.
+template <typename T, typename S>
+__global__ __launch_bounds__(S::NT, 2) void k_loss_grads(LossArgs a, unsigned x_blocks) {
+    __shared__ __align__(1024) char lds[3 * S::kStage];
+    if (blockIdx.x < x_blocks)
+        grad_x<T, S>(a, xcd_block(blockIdx.x, x_blocks), lds);
+    else
+        grad_table<T, S>(a, xcd_block(blockIdx.x - x_blocks, gridDim.x - x_blocks), lds);
+}
+
 // Parts joined in order, rounded: n elements of out from `count` parts. A thread has four
 // elements and loads eight parts at once.
+struct Joined {
+    const float* part;
+    int count;
+    long long n, pitch;
+    void* out;
+};
 template <typename T>
-__global__ __launch_bounds__(256) void k_loss_round(LossArgs a, const float* part, int count, long long n,
-                                                    long long pitch, T* out) {
+__global__ __launch_bounds__(256) void k_loss_round(LossArgs a, Joined first, Joined second) {
     const float down = ldexpf(a.scale, -lift_of<T>(a));
-    for (long long i = ((long long)blockIdx.x * 256 + threadIdx.x) * 4; i < n; i += 1024ll * gridDim.x) {
+    const Joined& b = blockIdx.y ? second : first;
+    for (long long i = ((long long)blockIdx.x * 256 + threadIdx.x) * 4; i < b.n; i += 1024ll * gridDim.x) {
         float4 s = make_float4(0, 0, 0, 0);
         constexpr int kAhead = 8;
-        for (int p = 0; p < count; p += kAhead) {
+        for (int p = 0; p < b.count; p += kAhead) {
             float4 v[kAhead];
 #pragma unroll
-            for (int j = 0; j < kAhead; ++j) v[j] = *(const float4*)(part + min(p + j, count - 1) * pitch + i);
+            for (int j = 0; j < kAhead; ++j) v[j] = *(const float4*)(b.part + min(p + j, b.count - 1) * b.pitch + i);
 #pragma unroll
             for (int j = 0; j < kAhead; ++j)
-                if (p + j < count) s.x += v[j].x, s.y += v[j].y, s.z += v[j].z, s.w += v[j].w;
+                if (p + j < b.count) s.x += v[j].x, s.y += v[j].y, s.z += v[j].z, s.w += v[j].w;
         }
         const float r[4] = {s.x * down, s.y * down, s.z * down, s.w * down};
-        Pack<T, 4>::store(out + i, r);
+        Pack<T, 4>::store((T*)b.out + i, r);
     }
 }
 
@@ -1044,10 +1055,9 @@ template <typename T, typename S>
 void gradients(LossArgs a, hipStream_t stream) {
     a.token_tiles = a.t_pad / S::BN;
     const long long cols = ceil_div(a.width, S::BM);
-    if (a.gx)
-        k_loss_grad_x<T, S><<<dim3((unsigned)(cols * (a.t_pad / S::BN) * a.x_splits)), dim3(S::NT), 0, stream>>>(a);
-    if (a.gt)
-        k_loss_grad_table<T, S><<<dim3((unsigned)(cols * (a.piece / S::BN) * a.t_splits)), dim3(S::NT), 0, stream>>>(a);
+    const long long x_blocks = a.gx ? cols * (a.t_pad / S::BN) * a.x_splits : 0;
+    const long long blocks = x_blocks + (a.gt ? cols * (a.piece / S::BN) * a.t_splits : 0);
+    k_loss_grads<T, S><<<dim3((unsigned)blocks), dim3(S::NT), 0, stream>>>(a, (unsigned)x_blocks);
 }
 
 template <typename T>
@@ -1080,16 +1090,19 @@ int backward(LossArgs a, const Cut& c, hipStream_t stream) {
             gradients<T, Wide<T>>(a, stream);
         else
             gradients<T, Even<T>>(a, stream);
-        if (a.gt && c.t_splits > 1) {
-            const long long there = a.rows - a.row0 < a.piece ? a.rows - a.row0 : a.piece, n = there * a.width;
-            k_loss_round<T><<<dim3(clamp(ceil_div(n, 1024), 1, 1 << 20)), dim3(256), 0, stream>>>(
-                a, a.part_t, c.t_splits, n, (long long)a.piece * a.width, (T*)a.gt + (long long)a.row0 * a.width);
-        }
+        const bool last = p + 1 == c.pieces;
+        const long long there = a.rows - a.row0 < a.piece ? a.rows - a.row0 : a.piece, n = (long long)a.t * a.width;
+        Joined joined[2] = {};
+        int jobs = 0;
+        if (a.gt && c.t_splits > 1)
+            joined[jobs++] = {a.part_t, c.t_splits, there * a.width, (long long)a.piece * a.width,
+                              (T*)a.gt + (long long)a.row0 * a.width};
+        if (a.gx && last) joined[jobs++] = {a.part_x, c.x_splits * (a.t_all > a.t ? 2 : 1), n, n, a.gx};
+        const long long most = joined[0].n > joined[1].n ? joined[0].n : joined[1].n;
+        if (jobs)
+            k_loss_round<T><<<dim3(clamp(ceil_div(most, 1024), 1, 1 << 20), jobs), dim3(256), 0, stream>>>(
+                a, joined[0], joined[1]);
     }
-    const long long n = (long long)a.t * a.width;
-    if (a.gx)
-        k_loss_round<T><<<dim3(clamp(ceil_div(n, 1024), 1, 1 << 20)), dim3(256), 0, stream>>>(
-            a, a.part_x, c.x_splits * (a.t_all > a.t ? 2 : 1), n, n, (T*)a.gx);
     const hipError_t e = hipGetLastError();
     return e == hipSuccess ? VOX_OK : ssh_hip_fail(e);
 }
