@@ -7,8 +7,8 @@
 // dZ = (exp(z - lse) - [row is the token's]) grad, rounded, to the workspace, from
 // where two products follow: grad_x += dZ W and grad_table = dZ^T X. A piece is as
 // many rows as dZ of 256 MB holds, about what the cache between HBM and the XCDs does
-// (4,096 tokens of 512 by 214,272 rows: 4.0 ms; 4.5 with pieces of 128 MB, whose partial
-// sums of grad_x pass memory twice as often, and 3.9 with 2 GB).
+// (4,096 tokens of 512 by 214,272 rows: 4.1 ms; 4.5 with pieces of 128 MB, whose partial
+// sums of grad_x pass memory twice as often, and 4.0 with 2 GB).
 //
 // Tiles of 32 of the inner index go straight from memory into three buffers of LDS
 // in turn. X and dZ are kept in pieces of 8 elements, [element / 8][token]: a tile
@@ -17,13 +17,14 @@
 // product asks for either. Tokens of up to 128 elements stay in registers while the rows go
 // by, and forward come from x itself.
 //
-// Bounds. The matrix units are busy 50 and 42% of the gradients' products (1,060 and 920
-// TFLOP/s of a step on 4,096 tokens of 512; a library product of 8192 cubed reaches 1,185
-// to 1,290): two wavefronts a SIMD wait for LDS and barriers. In the logits' passes the
-// exponentials come on top, an exp2 and two more instructions a logit forward, three and
-// the rounding backward, between the products of the other blocks of a CU: 925 TFLOP/s
-// forward and 756 for dZ at a width of 512, 1,000 at 128. A few tokens against all rows
-// are bound by memory: 110 MB in 22 us.
+// Bounds. 4,096 tokens of 512 by 214,272 rows take 3.84 ms, of which the forward's logits
+// 0.96 (937 TFLOP/s, matrix units busy 47%), dZ in seven pieces 1.19 (760, 34%), the two
+// gradients' products 1.67 (1,080, 54%); a library product of 8192 cubed reaches 1,185 to
+// 1,290. Two wavefronts a SIMD wait for LDS and barriers; in the logits' passes the
+// exponentials come on top, an exp2 and two more instructions a logit forward, three, the
+// rounding and 250 MB of stores a piece backward, between the products of a CU's other blocks.
+// A frame of 12,000 tokens of 128 by as many rows, forward: 0.67 ms (990 TFLOP/s, 47%). A
+// few tokens are bound by memory: 110 MB in 22 us.
 //
 // Roundings. dZ enters the products in the tensors' type; logits, maxima, sums and
 // gradients are summed in 32 bits. A token's gradient is nearly one dZ's multiple of its
@@ -915,7 +916,9 @@ int splits_of(long long tiles, long long token_tiles, int places) {
     return clamp(n, 1, tiles);
 }
 
-// How a call is cut: the gradients' products into blocks enough for two on each of 256 CUs.
+// How a call is cut: each gradient's product into blocks enough for one on each of 256 CUs,
+// since both run together (4,096 tokens of 512 by 214,272 rows: 3.9 ms; 4.1 with twice as many,
+// whose partial sums pass memory twice as often, 4.5 with half).
 struct Cut {
     long long t_pad, width8, t_all;
     int splits, slim;  // splits: at most
@@ -937,8 +940,8 @@ Cut cut(long long t, long long rows, long long width, bool grad) {
     c.piece = (int)(ceil_div(tiles, c.pieces) * kRowTile);
     c.pieces = (int)ceil_div(tiles * kRowTile, c.piece);
     const long long cols = ceil_div(width, width > 128 ? 256 : 128);
-    c.x_splits = clamp(512 / (cols * (c.t_pad / 128)), 1, c.piece / 512 > 1 ? c.piece / 512 : 1);
-    c.t_splits = clamp(512 / (cols * (c.piece / 128)), 1, c.t_pad / 512 > 1 ? c.t_pad / 512 : 1);
+    c.x_splits = clamp(256 / (cols * (c.t_pad / 128)), 1, c.piece / 512 > 1 ? c.piece / 512 : 1);
+    c.t_splits = clamp(256 / (cols * (c.piece / 128)), 1, c.t_pad / 512 > 1 ? c.t_pad / 512 : 1);
     return c;
 }
 
