@@ -90,8 +90,7 @@ struct Part {
     int from, to;    // tokens of this segment, in the walk's order
     bool none;       // no such segment
     bool last;
-    int row;         // of carry, for the state after it: floor(lo / segment) + its number, which
-                     // no other segment but a document's last (whose state is not kept) has
+    int row;         // of carry, for the state after it
 };
 
 __device__ __forceinline__ Part find_part(const DecayArgs& a, int slot) {
@@ -121,6 +120,25 @@ __device__ __forceinline__ Part find_part(const DecayArgs& a, int slot) {
     p.last = p.to == p.n;
     p.row = slot - lo;
     return p;
+}
+
+// A document's segment whose state goes to `row` of carry, if it has one there. Segment p of a
+// document, if not its last, has row floor(lo / segment) + p.
+__device__ __forceinline__ Part row_of(const DecayArgs& a, int doc, int row) {
+    Part p;
+    p.doc = doc;
+    p.lo = __builtin_amdgcn_readfirstlane(tok_boundary(a.offsets, a.docs, a.t, doc + 1));
+    p.n = max(0, tok_boundary(a.offsets, a.docs, a.t, doc + 2) - p.lo);
+    p.row = row < 0 ? p.lo / a.segment : row;  // below zero: its first
+    p.from = __builtin_amdgcn_readfirstlane((p.row - p.lo / a.segment) * a.segment);
+    p.to = p.from + a.segment;
+    p.last = false;
+    p.none = doc < 0 || doc >= a.docs || p.from < 0 || p.n - p.from <= a.segment;
+    return p;
+}
+// The document that a row is of: the last token of the row's stretch of `segment` tokens is its.
+__device__ __forceinline__ int doc_of_row(const DecayArgs& a, int row) {
+    return tok_range(a.offsets, a.docs, a.t, (row + 1) * a.segment - 1) - 1;
 }
 
 // decay * log2(e) of a head: never negative, and at most what leaves nothing of a token.
@@ -345,10 +363,10 @@ __global__ __launch_bounds__(2 * W, 2) void k_decay_sum(DecayArgs a) {
     typedef Decay<T, W> D;
     __shared__ __align__(1024) char lds[D::kBuffers * 2 * D::kTile];
     int head, role;
-    const int slot = block_of(a, &head, &role);
+    const int row = block_of(a, &head, &role);
+    const Part d = row_of(a, doc_of_row(a, row), row);
+    if (d.none) return;
     const Walk& walk = a.walk[0];
-    const Part d = find_part(a, slot);
-    if (d.none || d.doc < 0 || d.last) return;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, half = lane >> 5;
     const float rate = rate_of(a, head);
     const unsigned base = lds_address(lds);
@@ -390,25 +408,27 @@ __global__ __launch_bounds__(2 * W, 2) void k_decay_sum(DecayArgs a) {
 }
 
 // The states after a document's segments but the last, over their sums: four elements of
-// a state per thread, along the segments.
-__global__ __launch_bounds__(256) void k_decay_join(DecayArgs a, int slices) {
+// a state per thread, along the segments. Blocks go by documents or by the rows of carry,
+// whichever are fewer (16 frames take 285 us a call, 290 by rows; 3,000 windows of 40, 8 heads of
+// 64, 294 us, 387 with a block for every document and each of its segments).
+__global__ __launch_bounds__(256) void k_decay_join(DecayArgs a, int slices, bool by_row) {
     unsigned id = a.first_block + blockIdx.x;
     const int slice = id % slices;
     id /= slices;
-    const int head = id % a.heads, doc = id / a.heads;
-    const int lo = tok_boundary(a.offsets, a.docs, a.t, doc + 1);
-    const int n = max(0, tok_boundary(a.offsets, a.docs, a.t, doc + 2) - lo);
-    const int parts = (n + a.segment - 1) / a.segment - 1;
-    if (parts < 1) return;
+    const int head = id % a.heads;
+    const int which = id / a.heads;
+    const Part d = by_row ? row_of(a, doc_of_row(a, which), which) : row_of(a, which, -1);
+    if (d.none || d.from > 0) return;  // one for each document
+    const int parts = (d.n - 1) / a.segment;
     const int size = a.width * a.width, at = (slice * 256 + (int)threadIdx.x) * 4;
     if (at >= size) return;
     const long long pitch = (long long)a.heads * size;
     const Walk& walk = a.walk[0];
-    float* sum = walk.carry + (long long)(lo / a.segment) * pitch + (long long)head * size + at;
+    float* sum = walk.carry + d.row * pitch + (long long)head * size + at;
     const float through = fall(rate_of(a, head), a.segment);
     float4 h = make_float4(0, 0, 0, 0);
     if (walk.state) {
-        const float* from = walk.state + (long long)doc * pitch + (long long)head * size;
+        const float* from = walk.state + (long long)d.doc * pitch + (long long)head * size;
         h = *(const float4*)(from + at);
     }
     constexpr int kAhead = 8;
@@ -698,10 +718,13 @@ bool check(const tok_decay* t) {
 }
 
 // Short documents that fill the card with one block each (and head), or steps of decoding: no
-// segments, which saves two launches, each some 5 us of a call of 14. (At worst one document
-// holds all 16,384 tokens.)
+// segments, which saves two launches (500 of 30 tokens, 8 heads of 32: 19 us for 25; 256 steps
+// of 16 heads of 128: 106 for 118). The host knows no lengths, and one document may hold nearly
+// all tokens, in one block a head (8,000 next to 400 of 20, 8 heads of 32: 340 us, 44 with
+// segments); a wider state takes longer over them and has less to save.
 bool by_doc(const tok_decay& t) {
-    return t.t <= 16384 && (t.t <= 2ll * t.docs || (t.t <= 64ll * t.docs && (long long)t.docs * t.heads >= 512));
+    return t.t <= 16384 * 32 / padded(t.width) &&
+           (t.t <= 2ll * t.docs || (t.t <= 64ll * t.docs && (long long)t.docs * t.heads >= 512));
 }
 
 // Tokens of a segment: as many as leave a block for every place the card has (two blocks of
@@ -752,14 +775,16 @@ void in_launches(long long blocks, int threads, Launch launch) {
 template <typename T, int W>
 void states(DecayArgs a, hipStream_t stream) {
     a.walks = 1;
-    in_launches((long long)a.segments * a.heads, 2 * W, [&](unsigned first, dim3 grid) {
+    const long long rows = a.t / a.segment;
+    in_launches(rows * a.heads, 2 * W, [&](unsigned first, dim3 grid) {
         a.first_block = first;
         k_decay_sum<T, W><<<grid, dim3(2 * W), 0, stream>>>(a);
     });
     const int slices = (a.width * a.width + 1023) / 1024;
-    in_launches((long long)a.docs * a.heads * slices, 256, [&](unsigned first, dim3 grid) {
+    const bool by_row = rows < a.docs;
+    in_launches((by_row ? rows : a.docs) * a.heads * slices, 256, [&](unsigned first, dim3 grid) {
         a.first_block = first;
-        k_decay_join<<<grid, dim3(256), 0, stream>>>(a, slices);
+        k_decay_join<<<grid, dim3(256), 0, stream>>>(a, slices, by_row);
     });
 }
 

@@ -277,8 +277,8 @@ def test_decay_refuses_pointers_and_workspaces():
 
 
 def test_decay_keeps_states_only_for_documents_of_several_segments():
-    for more in (dict(t=0), dict(t=1), dict(t=64, docs=64, offsets=16), dict(t=128), dict(t=9000, docs=500, offsets=16),
-                 dict(t=2**14, docs=2**13, offsets=16)):
+    for more in (dict(t=0), dict(t=1), dict(t=64, docs=64, offsets=16), dict(t=128), dict(t=8000, docs=500, offsets=16),
+                 dict(t=2**13, docs=2**12, offsets=16)):
         assert LIB.tok_decay_carry_rows(_decay(**more)) == 0, more
     for more in (dict(t=300), dict(t=20000), dict(t=20000, docs=500, offsets=16), dict(t=2**29 - 4096),
                  dict(t=2**21, docs=2**20, offsets=16)):
