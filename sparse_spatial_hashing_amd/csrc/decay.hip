@@ -731,10 +731,14 @@ bool by_doc(const tok_decay& t) {
 // four wavefronts a CU, and as many more as they have fewer) and none for a second round,
 // counting the segments that documents' ends and the tokens of none may add; every
 // segment passes memory with its state four times. 122,880 tokens of 8 heads of 128: 536
-// blocks take 320 us, 504 take 240.
+// blocks take 320 us, 504 take 240. Many documents end within a segment each and leave blocks
+// short; at a width of 64 twice as many segments even that out (16 frames of 8,400 to 12,000
+// tokens: 257 us for 276, 64 of 1,400 to 2,000: 165 for 214), at 32 and 128 their states cost
+// more than that gives (117 us for 111, 348 for 332).
 int segment_of(const tok_decay& t) {
     if (by_doc(t)) return (int)((t.t + 127) / 128 * 128) + 128;  // one
-    const long long each = 512ll * 128 / padded(t.width) / t.heads;  // of a head
+    const bool twice = padded(t.width) == 64 && t.docs >= 16;
+    const long long each = 512ll * 128 / padded(t.width) * (twice ? 2 : 1) / t.heads;  // of a head
     long long n = each - t.docs - 2;
     if (n < each / 2) n = each / 2;
     if (n < 1) n = 1;
