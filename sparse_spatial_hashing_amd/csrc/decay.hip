@@ -30,8 +30,8 @@
 // sums two more, where five would do. 122,880 tokens of 8 heads of 128: sums 118 us (504 MB,
 // 4.3 TB/s), their prefix 15, the walk 240 (1 GB, 4.2), the gradients' three walks 680.
 // Without its products the walk takes 216 us, without its loads 185: with two blocks on a
-// CU, memory and products overlap nearly whole. Sixteen frames of 8 heads of 64: 96, 7 and
-// 183 (668 MB, 3.7), of which the stores are 60; ragged frames leave some blocks short.
+// CU, memory and products overlap nearly whole. Sixteen frames of 8 heads of 64: 88, 12 and
+// 165 (668 MB, 4.0).
 // Windows of a few dozen tokens pay for each block's beginning: 14 us forward, 28 backward.
 
 #include <hip/hip_runtime.h>
@@ -409,7 +409,7 @@ __global__ __launch_bounds__(2 * W, 2) void k_decay_sum(DecayArgs a) {
 
 // The states after a document's segments but the last, over their sums: four elements of
 // a state per thread, along the segments. Blocks go by documents or by the rows of carry,
-// whichever are fewer (16 frames take 285 us a call, 290 by rows; 3,000 windows of 40, 8 heads of
+// whichever are fewer (16 frames took 285 us a call, 290 by rows; 3,000 windows of 40, 8 heads of
 // 64, 294 us, 387 with a block for every document and each of its segments).
 __global__ __launch_bounds__(256) void k_decay_join(DecayArgs a, int slices, bool by_row) {
     unsigned id = a.first_block + blockIdx.x;
