@@ -423,6 +423,50 @@ def test_row_loss_long(dtype, t, rows, width):
     assert torch.equal(loss, ssh.row_loss(*args, scale=1.5)) and all(torch.equal(a, b) for a, b in zip((gx, gt), again))
 
 
+@pytest.mark.parametrize("width", [48, 200])
+def test_row_loss_rows_far_apart(width):
+    """Rows and tokens 8 MiB apart: past 2^32 bytes, and the widest strides that are read in place."""
+    t, rows, stride = 290, 700, 2**22 - 8
+    x, table, ids, grad = _loss_case(t, rows, width, BF16, 31)
+    far = torch.empty(rows * stride, dtype=BF16, device=DEV).view(rows, stride)
+    at, from_table = far[:t, 1000:1000 + width], far[:, :width]
+    at.copy_(x)
+    from_table.copy_(table)
+    print(f"row_loss far apart {width}", flush=True)
+    want = ref.row_loss(x, table, ids, 1.0, grad)
+    loss, lse = ssh.row_loss(at, from_table, ids.to(DEV), return_lse=True)
+    gx, gt = ssh.row_loss_grad(grad.to(DEV), at, from_table, ids.to(DEV), lse)
+    for n, v in (("loss", loss), ("lse", lse), ("gx", gx), ("gt", gt)):
+        check(v, *want[n], n)
+
+
+def test_row_loss_millions_of_tokens():
+    """dZ of 256 rows past 2^32 bytes; every token stands for one of a few hundred."""
+    t, rows, width, few = 8400000, 300, 8, 400
+    x, table, ids, grad = _loss_case(few, rows, width, BF16, 37)
+    which = torch.randint(0, few, (t,), generator=torch.Generator().manual_seed(2))
+    print("row_loss millions", flush=True)
+    want = ref.row_loss(x, table, ids, 1.0, grad)
+    d = which.to(DEV)
+    args = x.to(DEV)[d], table.to(DEV), ids.to(DEV)[d]
+    loss, lse = ssh.row_loss(*args, return_lse=True)
+    gx, gt = ssh.row_loss_grad(grad.to(DEV)[d], *args, lse)
+    for n, v in (("loss", loss), ("lse", lse), ("gx", gx)):
+        value, bound = want[n]
+        for b in (0, t // 2, t - 5000):
+            at = which[b:b + 5000]
+            check(v[b:b + 5000], value[at], bound[at], n)
+    # the table's gradient, token by token of the few: how often each came
+    total, bound = torch.zeros(gt.shape, dtype=torch.float64), torch.zeros(gt.shape, dtype=torch.float64)
+    for i, n in enumerate(torch.bincount(which, minlength=few).tolist()):
+        value, tol = ref.row_loss(x[i:i + 1], table, ids[i:i + 1], 1.0, grad[i:i + 1])["gt"]
+        total += n * value
+        bound += n * (tol + value.abs() * 2.0 ** -8)  # of one token dZ is in two parts there, in one here
+    # t additions of at most the terms' absolute sum, whose 2^-8 is in the bound, at 2^-24 for
+    # each of the at most t / 32 + 2 that a sum passes
+    check(gt, total, bound * (1 + (t / 32 + 2) * 2.0 ** -24 / 2.0 ** -8) + total.abs() * 2.0 ** -8, "gt")
+
+
 @pytest.mark.parametrize("width", [32, 256])
 def test_row_loss_several_pieces(width):
     """More rows than a piece of dZ holds (256 MB of 20,000 tokens: 6,656 rows), the last one short."""
