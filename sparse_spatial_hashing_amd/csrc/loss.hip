@@ -57,6 +57,7 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kLowest = -3.402823466e+38f;
 constexpr int kTwice = 256;
+constexpr int kBand = 8;  // tiles of tokens
 constexpr int kLift = 14;  // fp16: dZ is 2^kLift too large
 
 struct LossArgs {
@@ -434,6 +435,20 @@ __global__ __launch_bounds__(256) void k_loss_pack(LossArgs a) {
 
 // ---- logits ------------------------------------------------------------------
 
+// The share of the rows and the tile of tokens of a block. Blocks that run together on an XCD
+// are of a few tiles of tokens and a few shares: both stay in its L2 (20,000 tokens of 512 by
+// 214,272 rows forward: 4,660 us, 6,140 with all tiles of tokens before the next share). Where tokens
+// stay in registers all read one share's rows.
+template <typename S>
+__device__ __forceinline__ void place_of(const LossArgs& a, int* split, int* token0) {
+    const int id = xcd_block(blockIdx.x, gridDim.x);
+    const int most = S::kWidth ? a.token_tiles : kBand;
+    const int first = id / (most * a.splits) * most, in = id % (most * a.splits);
+    const int here = min(most, a.token_tiles - first);
+    *split = in / here;
+    *token0 = (first + in % here) * S::BN;
+}
+
 // Tiles [t0, t1) of the rows against a tile of tokens, from `first_row` on;
 // done(tile, acc) gets each tile's products and stores STORES times, or not at all.
 // PACKED: the tokens are read as pieces, else from x. (4,096 of 512, which every tile of rows
@@ -533,8 +548,8 @@ __device__ __forceinline__ void logits(const LossArgs& a, char* lds, int first_r
 template <typename T, typename S>
 __global__ __launch_bounds__(S::NT, 2) void k_loss_sum(LossArgs a) {
     __shared__ __align__(1024) char lds[3 * S::kStage];
-    const unsigned id = xcd_block(blockIdx.x, gridDim.x);
-    const int split = id / a.token_tiles, token0 = (id % a.token_tiles) * S::BN;
+    int split, token0;
+    place_of<S>(a, &split, &token0);
     const int t0 = (int)((long long)a.tiles * split / a.splits), t1 = (int)((long long)a.tiles * (split + 1) / a.splits);
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, half = lane >> 5;
     const int row_in = (wave / S::WN) * 32 * S::MA, token_in = (wave % S::WN) * 32 * S::NB + (lane & 31);
@@ -651,8 +666,8 @@ __global__ __launch_bounds__(256) void k_loss_join(LossArgs a) {
 template <typename T, typename S>
 __global__ __launch_bounds__(S::NT, 2) void k_loss_dz(LossArgs a) {
     __shared__ __align__(1024) char lds[3 * S::kStage];
-    const unsigned id = xcd_block(blockIdx.x, gridDim.x);
-    const int split = id / a.token_tiles, token0 = (id % a.token_tiles) * S::BN;
+    int split, token0;
+    place_of<S>(a, &split, &token0);
     const int t0 = (int)((long long)a.tiles * split / a.splits), t1 = (int)((long long)a.tiles * (split + 1) / a.splits);
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, half = lane >> 5;
     const int row_in = __builtin_amdgcn_readfirstlane((wave / S::WN) * 32 * S::MA);
@@ -916,9 +931,40 @@ int splits_of(long long tiles, long long token_tiles, int places) {
     return clamp(n, 1, tiles);
 }
 
-// How a call is cut: each gradient's product into blocks enough for one on each of 256 CUs,
-// since both run together (4,096 tokens of 512 by 214,272 rows: 3.9 ms; 4.1 with twice as many,
-// whose partial sums pass memory twice as often, 4.5 with half).
+// When the last of a launch's blocks is done, `first` of them of a steps, then `second` of b, on
+// `places` at once.
+long long finish(long long places, long long first, long long a, long long second, long long b) {
+    struct { long long at, n; } free[64] = {{0, places}};
+    int count = 1;
+    long long end = 0;
+    for (int kind = 0; kind < 2; ++kind) {
+        long long left = kind ? second : first;
+        const long long steps = kind ? b : a;
+        // whole rounds at once: what is left over is at most two more
+        if (left > 4 * places) {
+            const long long rounds = left / places - 2;
+            for (int i = 0; i < count; ++i) free[i].at += rounds * steps;
+            left -= rounds * places;
+        }
+        while (left > 0) {
+            int next = 0;
+            for (int i = 1; i < count; ++i)
+                if (free[i].at < free[next].at) next = i;
+            const long long n = left < free[next].n ? left : free[next].n, at = free[next].at + steps;
+            left -= n;
+            if (n == free[next].n || count == 64)
+                free[next].at = at;
+            else
+                free[next].n -= n, free[count++] = {at, n};
+            end = at > end ? at : end;
+        }
+        for (int i = 0; i < count; ++i)
+            if (free[i].at > end) end = free[i].at;
+    }
+    return end;
+}
+
+// How a call is cut.
 struct Cut {
     long long t_pad, width8, t_all;
     int splits, slim;  // splits: at most
@@ -940,8 +986,30 @@ Cut cut(long long t, long long rows, long long width, bool grad) {
     c.piece = (int)(ceil_div(tiles, c.pieces) * kRowTile);
     c.pieces = (int)ceil_div(tiles * kRowTile, c.piece);
     const long long cols = ceil_div(width, width > 128 ? 256 : 128);
-    c.x_splits = clamp(256 / (cols * (c.t_pad / 128)), 1, c.piece / 512 > 1 ? c.piece / 512 : 1);
-    c.t_splits = clamp(256 / (cols * (c.piece / 128)), 1, c.t_pad / 512 > 1 ? c.t_pad / 512 : 1);
+    // Both gradients' products into blocks enough for one on each of 256 CUs, since they run
+    // together (4,096 tokens of 512 by 214,272 rows: 3.9 ms; 4.1 with twice as many, whose partial
+    // sums pass memory twice as often, 4.5 with half).
+    const long long x_tiles = cols * (c.t_pad / 128), t_tiles = cols * (c.piece / 128);
+    c.x_splits = clamp(256 / x_tiles, 1, c.piece / 512 > 1 ? c.piece / 512 : 1);
+    c.t_splits = clamp(256 / t_tiles, 1, c.t_pad / 512 > 1 ? c.t_pad / 512 : 1);
+    if (!grad) return c;
+    // A few blocks more than the card holds begin when the others are done. Where another pair of
+    // powers of two ends a quarter sooner it is taken: a step takes about a microsecond with every
+    // place taken, and so do 5 MB of partial sums. (Backward of 20,000 tokens of 512 by 214,272
+    // rows: 15.6 ms, 18.5 else; of 1,024 by 13,391 rows 1.93 and 2.28. Gains that are smaller by
+    // this count were none: 20,000 of 256 by 214,272 rows 10.2 ms, 9.3 without.)
+    const long long places = width > 128 ? 512 : 768;
+    auto parts = [&](long long x, long long t1) { return 8 * width * (x * c.t_all + (t1 > 1 ? t1 * c.piece : 0)) / 5000000; };
+    auto steps = [&](long long x, long long t1) {
+        return finish(places, x_tiles * x, ceil_div(c.piece / kStep, x), t_tiles * t1, ceil_div(c.t_pad / kStep, t1));
+    };
+    long long best = (parts(c.x_splits, c.t_splits) + steps(c.x_splits, c.t_splits)) * 3 / 4;
+    for (long long x = 1; x == 1 || (x <= 512 && x * 256 <= c.piece); x *= 2)
+        for (long long t1 = 1; t1 == 1 || (t1 <= 256 && t1 * 512 <= c.t_pad); t1 *= 2) {
+            if (parts(x, t1) >= best) break;
+            const long long time = parts(x, t1) + steps(x, t1);
+            if (time < best) best = time, c.x_splits = (int)x, c.t_splits = (int)t1;
+        }
     return c;
 }
 
