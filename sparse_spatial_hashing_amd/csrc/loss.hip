@@ -17,13 +17,13 @@
 // product asks for either. Tokens of up to 128 elements stay in registers while the rows go
 // by, and forward come from x itself.
 //
-// Bounds. 4,096 tokens of 512 by 214,272 rows take 3.84 ms, of which the forward's logits
-// 0.96 (937 TFLOP/s, matrix units busy 47%), dZ in seven pieces 1.19 (760, 34%), the two
-// gradients' products 1.67 (1,080, 54%); a library product of 8192 cubed reaches 1,185 to
+// Bounds. 4,096 tokens of 512 by 214,272 rows take 3.76 ms, of which the forward's logits
+// 0.95 (951 TFLOP/s, matrix units busy 47%), dZ in seven pieces 1.18 (764, 34%), the two
+// gradients' products 1.59 (1,130, 57%); a library product of 8192 cubed reaches 1,185 to
 // 1,290. Two wavefronts a SIMD wait for LDS and barriers; in the logits' passes the
 // exponentials come on top, an exp2 and two more instructions a logit forward, three, the
 // rounding and 250 MB of stores a piece backward, between the products of a CU's other blocks.
-// A frame of 12,000 tokens of 128 by as many rows, forward: 0.67 ms (990 TFLOP/s, 47%). A
+// A frame of 12,000 tokens of 128 by as many rows, forward: 0.66 ms (1,000 TFLOP/s, 48%). A
 // few tokens are bound by memory: 110 MB in 22 us.
 //
 // Roundings. dZ enters the products in the tensors' type; logits, maxima, sums and
