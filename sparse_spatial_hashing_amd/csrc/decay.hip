@@ -431,7 +431,7 @@ __global__ __launch_bounds__(256) void k_decay_join(DecayArgs a, int slices, boo
         const float* from = walk.state + (long long)d.doc * pitch + (long long)head * size;
         h = *(const float4*)(from + at);
     }
-    constexpr int kAhead = 8;
+    constexpr int kAhead = 16;
     for (int p = 0; p < parts; p += kAhead) {
         float4 x[kAhead];
 #pragma unroll
@@ -734,7 +734,10 @@ bool by_doc(const tok_decay& t) {
 // blocks take 320 us, 504 take 240. Many documents end within a segment each and leave blocks
 // short; at a width of 64 twice as many segments even that out (16 frames of 8,400 to 12,000
 // tokens: 257 us for 276, 64 of 1,400 to 2,000: 165 for 214), at 32 and 128 their states cost
-// more than that gives (117 us for 111, 348 for 332).
+// more than that gives (117 us for 111, 348 for 332). Few narrow heads would have many segments
+// of 128 tokens, which their states are joined along one after the other: at least so many
+// tokens that the join and a segment's chunks take about as long (100,000 tokens of 2 heads of
+// 32: 58 us, 90 without).
 int segment_of(const tok_decay& t) {
     if (by_doc(t)) return (int)((t.t + 127) / 128 * 128) + 128;  // one
     const bool twice = padded(t.width) == 64 && t.docs >= 16;
@@ -744,6 +747,7 @@ int segment_of(const tok_decay& t) {
     if (n < 1) n = 1;
     n = (t.t + n - 1) / n;
     n = (n + kChunk - 1) / kChunk * kChunk;
+    while (n * n < 2 * (t.t / t.docs)) n += kChunk;
     if (n < 128) n = 128;
     if (n > 65536) n = 65536;
     return (int)n;
