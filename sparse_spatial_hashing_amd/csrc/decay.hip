@@ -38,6 +38,7 @@
 
 #include <type_traits>
 
+#include "decay_parts.h"
 #include "mma_ops.h"
 
 int ssh_hip_fail(hipError_t e);  // records the error for vox_last_hip_error()
@@ -116,7 +117,7 @@ __device__ __forceinline__ Part find_part(const DecayArgs& a, int slot) {
     const long long from = (long long)(slot - first) * a.segment;
     p.none = from < 0 || (from > 0 && from >= p.n);
     p.from = p.none ? 0 : (int)from;
-    p.to = min(p.n, p.from + a.segment);
+    p.to = part_end(p.from, p.n, a.segment);
     p.last = p.to == p.n;
     p.row = slot - lo;
     return p;
@@ -131,9 +132,9 @@ __device__ __forceinline__ Part row_of(const DecayArgs& a, int doc, int row) {
     p.n = max(0, tok_boundary(a.offsets, a.docs, a.t, doc + 2) - p.lo);
     p.row = row < 0 ? p.lo / a.segment : row;  // below zero: its first
     p.from = __builtin_amdgcn_readfirstlane((p.row - p.lo / a.segment) * a.segment);
-    p.to = p.from + a.segment;
     p.last = false;
     p.none = doc < 0 || doc >= a.docs || p.from < 0 || p.n - p.from <= a.segment;
+    p.to = p.none ? p.from : part_end(p.from, p.n, a.segment);
     return p;
 }
 // The document that a row is of: the last token of the row's stretch of `segment` tokens is its.

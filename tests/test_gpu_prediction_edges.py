@@ -1,0 +1,54 @@
+"""Rotary positions, attention with decay and the loss over a table's rows at the edges
+of what they take: the longest documents, extreme numbers, gradients nobody asked for."""
+import math
+
+import pytest
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+if not torch.cuda.is_available():
+    pytest.skip("no GPU", allow_module_level=True)
+
+import sparse_spatial_hashing_amd as ssh  # noqa: E402
+
+DEV = torch.device("cuda:0")
+BF16, F16, F32 = torch.bfloat16, torch.float16, torch.float32
+
+
+@pytest.mark.parametrize("reverse", [False, True])
+def test_decay_the_longest_document(reverse):
+    """As many tokens as a call takes, in the widest segments: the last one's end is near 2^31.
+
+    All tokens are alike and a state falls by half: away from where a walk begins it is twice what a
+    token adds."""
+    torch.cuda.empty_cache()
+    if torch.cuda.mem_get_info()[0] < 150 << 30:
+        pytest.skip("needs 150 GiB")
+    t = 2**31 - 4096
+    one = lambda x: torch.tensor(x, dtype=BF16, device=DEV).view(1, 1, 8).expand(t, 1, 8)
+    q, k, v, g = one([0.5] * 8), one([0.5] * 8), one([c / 4 for c in range(1, 9)]), one([1.0] * 8)
+    decay = torch.tensor([math.log(2.0)], device=DEV)
+    print(f"decay of {t} tokens, reverse {reverse}", flush=True)
+    out, last, carry = ssh.decay_attend(q, k, v, decay, scale=1.0, reverse=reverse, return_carry=True)
+    assert t // 65536 == carry.shape[0]
+    value = v[0, 0].double().cpu()
+
+    def alike(x, want, what):
+        # away from both ends, and through the last segments
+        for lo in (100, 2**30 - 50, t - 140000):
+            for at in range(lo, min(lo + 139900, t - 100), 35000):
+                part = x[at:min(at + 35000, t - 100)].cpu().double()
+                # the state's copy, the result and some 2^-20 of sums
+                assert ((part - want).abs() <= want.abs() * (2.0 ** -7)).all(), (what, at)
+
+    alike(out, 4.0 * value, "out")
+    assert ((last[0, 0].cpu().double() - value).abs() <= value * 2.0 ** -18).all()
+    del out, last
+    gq, gk, gv, gs = ssh.decay_attend_grad(g, q, k, v, decay, carry, scale=1.0, reverse=reverse)
+    assert gs is None
+    alike(gq, torch.full((8,), 9.0).double(), "gq")
+    alike(gk, torch.full((8,), 9.0).double(), "gk")
+    alike(gv, torch.full((8,), 4.0).double(), "gv")
+    del gq, gk, gv
+    torch.cuda.empty_cache()
