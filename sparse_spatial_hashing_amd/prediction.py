@@ -246,12 +246,17 @@ class _DecayAttend(torch.autograd.Function):
         ctx.save_for_backward(q, k, v, decay, carry, offsets, state)
         ctx.how = dict(scale=scale, reverse=reverse)
         ctx.mark_non_differentiable(carry)
+        ctx.set_materialize_grads(False)  # no zeros for a state that nothing used, nor for carry
         return out, last, carry
 
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, grad, grad_last, _):
+        if grad is None and grad_last is None:
+            return (None,) * 9
         q, k, v, decay, carry, offsets, state = ctx.saved_tensors
+        if grad is None:
+            grad = q.new_zeros(q.shape)
         gq, gk, gv, gs = decay_attend_grad(grad, q, k, v, decay, carry, offsets, state=state, grad_state=grad_last,
                                            **ctx.how)
         return gq, gk, gv, None, None, gs, None, None, None
@@ -365,11 +370,14 @@ class _RowLoss(torch.autograd.Function):
         ctx.save_for_backward(x, table, ids, lse)
         ctx.scale = scale
         ctx.mark_non_differentiable(lse)
+        ctx.set_materialize_grads(False)  # no zeros for lse
         return loss, lse
 
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, grad, _):
+        if grad is None:
+            return (None,) * 4
         gx, gt = _row_loss_grad(grad, *ctx.saved_tensors, ctx.scale, *ctx.needs_input_grad[:2])
         return gx, gt, None, None
 

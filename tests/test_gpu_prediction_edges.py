@@ -52,3 +52,48 @@ def test_decay_the_longest_document(reverse):
     alike(gv, torch.full((8,), 4.0).double(), "gv")
     del gq, gk, gv
     torch.cuda.empty_cache()
+
+
+def test_decay_an_unused_state_costs_nothing_in_the_backward():
+    """The last state is returned and not used: no memory of its size, and the gradients are those without it."""
+    gen = torch.Generator(device=DEV).manual_seed(1)
+    docs, heads, width = 300, 4, 64
+    at = torch.arange(docs + 1, dtype=torch.int32, device=DEV) * 40
+    q, k, v, g = (torch.randn((40 * docs, heads, width), generator=gen, device=DEV).to(BF16) for _ in range(4))
+    decay = torch.full((heads,), 0.1, device=DEV)
+    size = 4 * docs * heads * width * width
+    made = []
+    for how in ("unused", "not returned"):
+        leaves = [x.clone().requires_grad_() for x in (q, k, v)]
+        out, last = ssh.decay_attend(*leaves, decay, at, return_state=how == "unused")
+        torch.cuda.synchronize()
+        torch.cuda.reset_peak_memory_stats()
+        before = torch.cuda.memory_allocated()
+        out.backward(g)
+        peak = torch.cuda.max_memory_allocated() - before
+        # the gradients, and the sums that the backward's own walk keeps: a row for each segment
+        # but a document's last, and none of these has two
+        rows = ssh.decay_attend(q, k, v, decay, at, return_carry=True)[2].shape[0]
+        most = 3 * 2 * q.numel() + 4 * rows * heads * width * width + (1 << 20)
+        assert peak <= most, (how, peak, most)
+        assert most - 6 * q.numel() < size
+        made.append([x.grad for x in leaves])
+    assert all(torch.equal(a, b) for a, b in zip(*made))
+    zero = torch.zeros((docs, heads, width, width), device=DEV)
+    carry = ssh.decay_attend(q, k, v, decay, at, return_carry=True)[2]
+    want = ssh.decay_attend_grad(g, q, k, v, decay, carry, at, grad_state=zero)
+    assert all(torch.equal(a, b) for a, b in zip(made[0], want[:3]))
+
+
+def test_decay_gradient_of_the_state_alone():
+    gen = torch.Generator(device=DEV).manual_seed(2)
+    q, k, v = (torch.randn((90, 2, 32), generator=gen, device=DEV).to(BF16).requires_grad_() for _ in range(3))
+    state = torch.randn((1, 2, 32, 32), generator=gen, device=DEV).requires_grad_()
+    decay, g = torch.full((2,), 0.05, device=DEV), torch.randn((1, 2, 32, 32), generator=gen, device=DEV)
+    out, last, carry = ssh.decay_attend(q, k, v, decay, state=state, return_carry=True)
+    made = torch.autograd.grad(last, (q, k, v, state), g)
+    want = ssh.decay_attend_grad(torch.zeros_like(out), q.detach(), k.detach(), v.detach(), decay, carry,
+                                 state=state.detach(), grad_state=g)
+    assert not made[0].any() and all(torch.equal(a, b) for a, b in zip(made, want))
+    (none,) = torch.autograd.grad(ssh.row_loss(q.flatten(1), k.flatten(1)[:50], torch.full((90,), -1, device=DEV)).sum(), q)
+    assert not none.any()
