@@ -49,6 +49,7 @@ constexpr long long kMaxElems = (1ll << 31) - 4096;
 constexpr int kMaxDocs = 1 << 20;
 constexpr int kChunk = 32;
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLargest = 3.402823466e+38f;
 
 // A tensor in one of the walk's places.
 struct Place {
@@ -222,7 +223,7 @@ struct Decay {
 
     // The power of two that brings x to about 1 (1 for 0 and what is not finite).
     static __device__ __forceinline__ float to_one(float x) {
-        return x > 0.0f && x <= 3.402823466e+38f
+        return x > 0.0f && x <= kLargest
                    ? ldexpf(1.0f, min(max(-__builtin_amdgcn_frexp_expf(x), -120), 120)) : 1.0f;
     }
     static __device__ __forceinline__ float wave_max(float x) {
@@ -635,11 +636,14 @@ __global__ __launch_bounds__(2 * W, W == 32 ? 3 : 2) void k_decay_run(DecayArgs 
             float top = 0.0f;
 #pragma unroll
             for (int r = 0; r < 16; ++r) top = fmaxf(top, fabsf(p[r]));
-            up_p = D::to_one(fmaxf(top, __shfl_xor(top, 32)));
+            // No further than 2^60: what is less is nothing in 16 bits, and the state's share is taken up as far.
+            up_p = fminf(D::to_one(fmaxf(top, __shfl_xor(top, 32))), 0x1p60f);
 #pragma unroll
             for (int r = 0; r < 16; ++r) p[r] *= up_p;
         }
-        const float in = entering * fallen.now(rate) * (D::kHalf ? up_p / up_s : 1.0f);
+        // Finite, so that what is zero stays so.
+        float in = entering * fallen.now(rate);
+        if (D::kHalf) in = fminf(fminf(in / up_s, kLargest) * up_p, kLargest);
 #pragma unroll
         for (int r = 0; r < 16; ++r) o[r] *= in;
         typename D::vec8 v[2];

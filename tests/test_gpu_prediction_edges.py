@@ -11,6 +11,7 @@ if not torch.cuda.is_available():
     pytest.skip("no GPU", allow_module_level=True)
 
 import sparse_spatial_hashing_amd as ssh  # noqa: E402
+from test_gpu_prediction import _decay_compare  # noqa: E402
 
 DEV = torch.device("cuda:0")
 BF16, F16, F32 = torch.bfloat16, torch.float16, torch.float32
@@ -97,3 +98,27 @@ def test_decay_gradient_of_the_state_alone():
     assert not made[0].any() and all(torch.equal(a, b) for a, b in zip(made, want))
     (none,) = torch.autograd.grad(ssh.row_loss(q.flatten(1), k.flatten(1)[:50], torch.full((90,), -1, device=DEV)).sum(), q)
     assert not none.any()
+
+
+@pytest.mark.parametrize("rate", [85.0, 42.0, 12.0])
+@pytest.mark.parametrize("scale", [1.0, 1e-3])
+def test_decay_fp16_weights_far_under_the_state(rate, scale):
+    """A query that meets nothing of the nearest keys: its weights are of 2^-120 and less next to a
+    state of thousands, of which e^-rate is left by the token and soon nothing. No inf by zero."""
+    apart = max(1, round(84 / rate))  # tokens to the nearest key that a query meets
+    t, width = 90, 16
+    q, k = torch.zeros((t, 1, width), dtype=F16), torch.zeros((t, 1, width), dtype=F16)
+    i = torch.arange(t)
+    q[i, 0, i % 13] = 1.0
+    k[i, 0, (i + apart) % 13] = 1.0  # q[i] meets k[i - apart], and every thirteenth before it
+    gen = torch.Generator().manual_seed(3)
+    s = dict(q=q, k=k, v=torch.randn((t, 1, width), generator=gen).to(F16), decay=torch.tensor([rate]),
+             grad=torch.randn((t, 1, width), generator=gen).to(F16), state=torch.full((1, 1, width, width), 4000.0),
+             grad_state=torch.full((1, 1, width, width), -3000.0))
+    for reverse in (False, True):
+        _decay_compare(s, [0, t], f"fp16 weights under the state, rate {rate} scale {scale}", reverse, scale)
+    # queries of nothing next to a state near the largest number
+    s["q"] = torch.zeros_like(q)
+    g = {n: x.to(DEV) for n, x in s.items()}
+    out, _ = ssh.decay_attend(g["q"], g["k"], g["v"], g["decay"], state=torch.full_like(g["state"], 3e38), scale=scale)
+    assert not out.any()
