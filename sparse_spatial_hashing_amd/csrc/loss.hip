@@ -692,6 +692,8 @@ __global__ __launch_bounds__(S::NT, 2) void k_loss_dz(LossArgs a) {
         for (int j = 0; j < S::NB; ++j) {
             const int mine = came[j] - row0;
             const bool any = __any(mine >= 0 && mine < 32 * S::MA);
+            // without a row: 0 also by a row that is not finite
+            const bool none = came[j] < -a.row0, some_none = __any(none);
 #pragma unroll
             for (int i = 0; i < S::MA; ++i) {
                 acc16& p = acc[i][j];
@@ -704,6 +706,9 @@ __global__ __launch_bounds__(S::NT, 2) void k_loss_dz(LossArgs a) {
                         if (mine == 32 * i + acc_row(r, half)) p[r] -= 1.0f;
 #pragma unroll
                 for (int r = 0; r < 16; ++r) p[r] *= by[j];
+                if (some_none)
+#pragma unroll
+                    for (int r = 0; r < 16; ++r) p[r] = none ? 0.0f : p[r];
                 if (twice && token0 + token_in + 32 * j >= a.t)
 #pragma unroll
                     for (int r = 0; r < 16; ++r) p[r] -= (float)(T)p[r];
@@ -769,6 +774,7 @@ __device__ __forceinline__ void grad_x(const LossArgs& a, unsigned id, char* lds
     for (int j = 0; j < S::NB; ++j) {
         const int t = token0 + (wave % S::WN) * 32 * S::NB + 32 * j + (lane & 31);
         if (t >= a.t_all) continue;
+        const bool none = a.came[t] < 0;
         // the second time's are further parts
         const long long part = t < a.t ? 2 * split : 2 * split + 1;
         float* to = a.part_x + ((a.t_all > a.t ? part : split) * a.t + (t < a.t ? t : t - a.t)) * a.width;
@@ -779,6 +785,7 @@ __device__ __forceinline__ void grad_x(const LossArgs& a, unsigned id, char* lds
                 const int c = col0 + 32 * (a_block + i) + 8 * q + 4 * half;
                 if (c >= a.width) continue;
                 float4 v = make_float4(acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]);
+                if (none) v = make_float4(0, 0, 0, 0);
                 if (!a.first) {
                     const float4 w = *(const float4*)(to + c);
                     v.x += w.x, v.y += w.y, v.z += w.z, v.w += w.w;

@@ -11,7 +11,9 @@ if not torch.cuda.is_available():
     pytest.skip("no GPU", allow_module_level=True)
 
 import sparse_spatial_hashing_amd as ssh  # noqa: E402
-from test_gpu_prediction import _decay_compare  # noqa: E402
+import prediction_reference as ref  # noqa: E402
+from test_gpu_prediction import _decay_compare, _loss_case  # noqa: E402
+from token_reference import check  # noqa: E402
 
 DEV = torch.device("cuda:0")
 BF16, F16, F32 = torch.bfloat16, torch.float16, torch.float32
@@ -122,3 +124,32 @@ def test_decay_fp16_weights_far_under_the_state(rate, scale):
     g = {n: x.to(DEV) for n, x in s.items()}
     out, _ = ssh.decay_attend(g["q"], g["k"], g["v"], g["decay"], state=torch.full_like(g["state"], 3e38), scale=scale)
     assert not out.any()
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("t,width", [(5, 64), (9, 200), (100, 32), (300, 128), (300, 200), (700, 72)])
+def test_row_loss_rows_of_minus_infinity(dtype, t, width):
+    """Rows ruled out by -inf against an element that is 1 in every token: their weights are 0, whatever
+    tokens without a row, and the places past the last token, would make of such a row."""
+    rows = 500
+    x, table, ids, grad = _loss_case(t, rows, width, dtype, t + width, none=0.2)
+    ids[0] = -1
+    x[:, 0] = 1.0
+    out = torch.zeros(rows, dtype=torch.bool)
+    out[3::7] = True
+    ids[(ids >= 0) & out[ids.clamp(min=0)]] -= 1
+    left = (~out).cumsum(0) - 1
+    few = torch.where(ids >= 0, left[ids.clamp(min=0)], -1)
+    want = ref.row_loss(x, table[~out], few, 1.0, grad)
+    table[out, 0] = -math.inf
+    args = x.to(DEV), table.to(DEV), ids.to(DEV)
+    print(f"row loss, rows of -inf, {dtype} {t} {width}", flush=True)
+    loss, lse = ssh.row_loss(*args, return_lse=True)
+    gx, gt = (v.cpu() for v in ssh.row_loss_grad(grad.to(DEV), *args, lse))
+    check(loss, *want["loss"], "loss")
+    check(lse, *want["lse"], "lse")
+    check(gt[~out], *want["gt"], "gt")
+    assert not gt[out].any()
+    # element 0 of a token's gradient is 0 times -inf
+    check(gx[:, 1:], *(v[:, 1:] for v in want["gx"]), "gx")
+    assert not gx[ids < 0].any()
