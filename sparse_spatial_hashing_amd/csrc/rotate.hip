@@ -178,7 +178,7 @@ int tok_rotate(const void* x, int64_t tokens, int64_t heads, int64_t width, int6
                int64_t axis_stride, int32_t axes, const double* freqs, int64_t pairs,
                int32_t interleaved, int32_t inverse, void* out, hipStream_t stream) {
     if (!tok_dtype_ok(dtype) || tokens < 0 || tokens > kMaxTokens || heads < 1 || heads > 65536 || width < 1 ||
-        width > 65536 || axes < 1 || axes > 3 || pairs < 1 || 2 * axes * pairs > width || token_stride < 0 ||
+        width > 65536 || axes < 1 || axes > 3 || pairs < 1 || pairs > width / (2 * axes) || token_stride < 0 ||
         head_stride < 0 || pos_stride < 0 || axis_stride < 0)
         return VOX_EINVAL;
     if ((interleaved != 0 && interleaved != 1) || (inverse != 0 && inverse != 1)) return VOX_EINVAL;
