@@ -413,6 +413,12 @@ __device__ __forceinline__ int lift_of(const LossArgs& a) {
     for (int b = 0; b < a.tops; ++b) top = fmaxf(top, a.top[b]);
     return top > 0.0f ? kLift - __builtin_amdgcn_frexp_expf(top) : 0;
 }
+// What sums of lifted weights are multiplied with: finite, so that zeros stay so (where it would not
+// be, the smallest such sum passes fp16's largest number).
+template <typename T>
+__device__ __forceinline__ float down_of(const LossArgs& a) {
+    return fminf(ldexpf(a.scale, -lift_of<T>(a)), -kLowest);
+}
 
 // X as pieces, zeros where a token has no row, is past the last, or past the width.
 template <typename T, bool GRAD>
@@ -831,7 +837,7 @@ __device__ __forceinline__ void grad_table(const LossArgs& a, unsigned id, char*
                 [&](int j, int s) { return B::read(make_uint2(at.x + y_on, at.y + y_on), b_block + j, s); }, next);
             return false;
         });
-    const float down = ldexpf(a.scale, -lift_of<T>(a));
+    const float down = down_of<T>(a);
 #pragma unroll
     for (int j = 0; j < S::NB; ++j) {
         const int row = row0 + 32 * (b_block + j) + (lane & 31);  // of the piece
@@ -892,7 +898,7 @@ struct Joined {
 };
 template <typename T>
 __global__ __launch_bounds__(256) void k_loss_round(LossArgs a, Joined first, Joined second) {
-    const float down = ldexpf(a.scale, -lift_of<T>(a));
+    const float down = down_of<T>(a);
     const Joined& b = blockIdx.y ? second : first;
     for (long long i = ((long long)blockIdx.x * 256 + threadIdx.x) * 4; i < b.n; i += 1024ll * gridDim.x) {
         float4 s = make_float4(0, 0, 0, 0);

@@ -153,3 +153,30 @@ def test_row_loss_rows_of_minus_infinity(dtype, t, width):
     # element 0 of a token's gradient is 0 times -inf
     check(gx[:, 1:], *(v[:, 1:] for v in want["gx"]), "gx")
     assert not gx[ids < 0].any()
+
+
+@pytest.mark.parametrize("t", [9, 300])
+@pytest.mark.parametrize("size,scale", [(1e38, 4e4), (1e38, 1.0), (1e-38, 1.0), (1e-44, 1e30)])
+def test_row_loss_fp16_gradients_at_the_ends_of_float32(t, size, scale):
+    """The power of two that weights are taken up by may take scale past the largest float: elements
+    that are 0 stay 0, what passes fp16's largest number is infinite, and none is NaN."""
+    gen = torch.Generator().manual_seed(t)
+    x, table = (torch.randn((n, 40), generator=gen) * min(1.0, scale ** -0.5) for n in (t, 70))
+    if scale > 1e5:
+        x, table = torch.zeros_like(x), torch.sign(table)  # no logits pass the largest float
+    x[:, 5] = 0.0
+    table[:, 5] = 0.0
+    x, table, ids = x.half(), table.half(), torch.randint(0, 70, (t,), generator=gen)
+    grad = torch.full((t,), size)
+    want = ref.row_loss(x, table, ids, scale, grad)
+    args = x.to(DEV), table.to(DEV), ids.to(DEV)
+    print(f"row loss, gradients of {size} by {scale}", flush=True)
+    loss, lse = ssh.row_loss(*args, scale=scale, return_lse=True)
+    for n, v in zip(("gx", "gt"), ssh.row_loss_grad(grad.to(DEV), *args, lse, scale=scale)):
+        value, bound = want[n]
+        v = v.cpu().double()
+        assert not v[:, 5].any() and not v.isnan().any(), n
+        if size < 1 or scale == 1.0:
+            over = value.abs() + bound > 65504
+            assert (v[over] * value[over].sign() > 65504 - 2 * bound[over]).all(), n
+            check(torch.where(over, 0, v), torch.where(over, 0, value), bound, n)
