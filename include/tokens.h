@@ -270,7 +270,10 @@ int tok_decay_attend_grad(const tok_decay* args, const void* q, const void* k, c
  * bits are lost), of up to 256 tokens in two parts; sums are float32.
  * Limits: 0 <= t <= 2^25, 1 <= rows <= 2^31 - 2048; width a multiple of 8, at most
  * 65536; strides multiples of 8 below 2^22; all bases 16-byte aligned; scale in
- * [1e-30, 1e30]. The workspace needs no initial contents, 256-byte aligned.
+ * [1e-30, 1e30]. The workspace needs no initial contents, 256-byte aligned. It holds x once (a width
+ * over 128 rounded up to whole 256s; forward only then, and of more than 32 tokens), for gradients x in
+ * float32 besides and an eighth of x where tokens are more than 2^19, 12 bytes a token, and up to 768 MiB
+ * that do not grow with the tokens.
  */
 int64_t tok_row_loss_workspace_bytes(int64_t t, int64_t rows, int64_t width);
 int tok_row_loss(const void* x, int64_t x_stride, const void* table, int64_t table_stride,

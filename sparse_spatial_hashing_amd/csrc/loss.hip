@@ -72,19 +72,21 @@ struct LossArgs {
     void* gx;
     void* gt;
     // workspace
-    uint4* xg;         // [width8, tokens_pad]: X in pieces
-    uint4* dz;         // [piece / 8, tokens_pad]
-    int* came;         // [tokens_pad]: the token's row, or -1
-    float* shift;      // [tokens_pad]: lse in base 2 (backward)
-    float* by;         // [tokens_pad]: grad times the lift (backward)
-    float* hit;        // [tokens_pad]: the logit of the token's row, base 2 (forward)
-    float2* part;      // [splits, tokens_pad]: maximum and sum (forward)
+    uint4* xg;         // [width8, x_pad]: X in pieces
+    uint4* dz;         // [piece / 8, t_pad]
+    int* came;         // [x_pad]: the token's row, or -1
+    float* shift;      // [x_pad]: lse in base 2 (backward)
+    float* by;         // [x_pad]: grad times the lift (backward)
+    float* hit;        // [x_pad]: the logit of the token's row, base 2 (forward)
+    float2* part;      // [splits, x_pad]: maximum and sum (forward)
     float* top;        // [tops]: the largest |grad| of each share of the tokens (fp16)
     float* part_x;     // [x_splits, tokens, width]
-    float* part_t;     // [t_splits, piece rows, width] (t_splits > 1)
+    float* part_t;     // [bands, t_splits, piece rows, width], or null: grad_table's blocks round themselves
     long long x_stride, t_stride;
-    int t, rows, width, width8, t_pad, id_bytes;
+    int t, rows, width, width8, id_bytes;
+    int x_pad, t_pad;  // tokens laid out, all of them and those of a band
     int t_all;         // t, or twice as much: tokens of the backward
+    int x_tokens;      // t of all bands
     int splits, tiles;        // of the rows' tiles
     int token_tiles;
     int row0, piece;          // rows of a piece: a multiple of kRowTile, its last ones past the table's
@@ -347,25 +349,31 @@ struct ColumnsOfMatrix {
 };
 
 // The same of a matrix kept in pieces, [column / 8][inner]. In LDS [COLS / 8][32]
-// pieces, the 32 of a column group permuted by XOR with 4 (group % 4).
-template <typename T, int COLS, int NT>
+// pieces, the 32 of a column group permuted by XOR with 4 (group % 4). Of a last group before COLS / 8
+// the last one is read in place of those past it.
+template <typename T, int COLS, int NT, bool LAST = false>
 struct ColumnsOfPieces {
+    static constexpr int kPer = COLS * 4 / NT, kGroups = NT / 32;
     const uint4* base;
     long long pitch;
-    unsigned offset;
+    int last;
+    unsigned offset[LAST ? kPer : 1];
 
-    __device__ __forceinline__ ColumnsOfPieces(const uint4* p, long long step, int col0)
-        : base(p + (long long)(col0 >> 3) * step), pitch(step) {
+    __device__ __forceinline__ ColumnsOfPieces(const uint4* p, long long step, int col0, int groups = 0)
+        : base(p + (long long)(col0 >> 3) * step), pitch(step), last(groups - 1 - (col0 >> 3)) {
+        static_assert(kGroups % 4 == 0, "the permutation is that of the first load's groups");
         const int group = threadIdx.x >> 5, row = (threadIdx.x & 31) ^ ((group & 3) << 2);
-        offset = (group * (unsigned)step + row) * 16u;
+#pragma unroll
+        for (int l = 0; l < (LAST ? kPer : 1); ++l)
+            offset[l] = ((LAST ? min(group, last - first(l)) : group) * (unsigned)step + row) * 16u;
     }
+    // The first group of load l.
+    __device__ __forceinline__ int first(int l) const { return LAST && last < l * kGroups ? 0 : l * kGroups; }
     __device__ __forceinline__ void load(unsigned to, int row0) const {
-        constexpr int kPer = COLS * 4 / NT;
-        static_assert(NT / 32 % 4 == 0, "the permutation is that of the first load's groups");
         const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
 #pragma unroll
-        for (int p = 0; p < kPer; ++p)
-            load_to_lds(to + 1024u * wave + 16u * NT * p, base + row0 + p * (NT / 32) * pitch, offset);
+        for (int l = 0; l < kPer; ++l)
+            load_to_lds(to + 1024u * wave + 16u * NT * l, base + row0 + first(l) * pitch, offset[LAST ? l : 0]);
     }
     static __device__ __forceinline__ uint2 place(int lane) {
         const int row = 8 * (lane >> 5) + ((lane & 15) >> 2);
@@ -425,13 +433,13 @@ template <typename T, bool GRAD>
 __global__ __launch_bounds__(256) void k_loss_pack(LossArgs a) {
     const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
     const int c = (int)(i & 7) + 8 * blockIdx.y, t = (int)(i >> 3);
-    if (t >= a.t_pad) return;
+    if (t >= a.x_pad) return;
     const int from = t < a.t ? t : t - a.t;  // of the second time
     const int id = t < (GRAD ? a.t_all : a.t) ? id_of(a, from) : -1;
     if (c < a.width8) {
         uint4 v = make_uint4(0, 0, 0, 0);
         if (id >= 0 && 8 * c < a.width) v = *(const uint4*)((const T*)a.x + from * a.x_stride + 8 * c);
-        a.xg[(long long)c * a.t_pad + t] = v;
+        a.xg[(long long)c * a.x_pad + t] = v;
     }
     if (GRAD && c == 0) {
         a.came[t] = id;
@@ -478,10 +486,11 @@ __device__ __forceinline__ void logits(const LossArgs& a, char* lds, int first_r
                 for (int j = 0; j < S::NB; ++j) {
                     const int t = token0 + (wave % S::WN) * 32 * S::NB + 32 * j + (lane & 31), c = 2 * s + half;
                     uint4 piece = make_uint4(0, 0, 0, 0);
-                    if (PACKED)
-                        piece = a.xg[(long long)c * a.t_pad + t];
-                    else if (t < a.t && 8 * c < a.width)
+                    if (PACKED) {
+                        if (c < a.width8) piece = a.xg[(long long)c * a.x_pad + t];
+                    } else if (t < a.t && 8 * c < a.width) {
                         piece = *(const uint4*)((const T*)a.x + t * a.x_stride + 8 * c);
+                    }
                     y[s][j] = __builtin_bit_cast(typename Mma<T>::vec8, piece);
                 }
             // settled here: inside the loop their wait would be for the tiles under way as well
@@ -520,7 +529,7 @@ __device__ __forceinline__ void logits(const LossArgs& a, char* lds, int first_r
         const A table(a.table, a.t_stride, end_row, a.width);
         const B tokens = [&] {
             if constexpr (PACKED)
-                return B(a.xg, a.t_pad);
+                return B(a.xg, a.x_pad);
             else
                 return B(a.x, a.x_stride, a.t, a.width);
         }();
@@ -633,7 +642,7 @@ __global__ __launch_bounds__(S::NT, 2) void k_loss_sum(LossArgs a) {
 #pragma unroll
         for (int w = 0; w < 2 * S::WM; ++w)
             sum += all[w * S::BN + n].y * __builtin_amdgcn_exp2f(all[w * S::BN + n].x - top);
-        a.part[(long long)split * a.t_pad + token0 + n] = make_float2(top, sum);
+        a.part[(long long)split * a.x_pad + token0 + n] = make_float2(top, sum);
     }
 }
 
@@ -647,7 +656,7 @@ __global__ __launch_bounds__(256) void k_loss_join(LossArgs a) {
         float2 p[kAhead];
 #pragma unroll
         for (int j = 0; j < kAhead; ++j)
-            p[j] = s + 64 * j < a.splits ? a.part[(long long)(s + 64 * j) * a.t_pad + t] : make_float2(kLowest, 0.0f);
+            p[j] = s + 64 * j < a.splits ? a.part[(long long)(s + 64 * j) * a.x_pad + t] : make_float2(kLowest, 0.0f);
         float now = m;
 #pragma unroll
         for (int j = 0; j < kAhead; ++j) now = fmaxf(now, p[j].x);
@@ -783,7 +792,7 @@ __device__ __forceinline__ void grad_x(const LossArgs& a, unsigned id, char* lds
         const bool none = a.came[t] < 0;
         // the second time's are further parts
         const long long part = t < a.t ? 2 * split : 2 * split + 1;
-        float* to = a.part_x + ((a.t_all > a.t ? part : split) * a.t + (t < a.t ? t : t - a.t)) * a.width;
+        float* to = a.part_x + ((a.t_all > a.t ? part : split) * a.x_tokens + (t < a.t ? t : t - a.t)) * a.width;
 #pragma unroll
         for (int i = 0; i < S::MA; ++i)
 #pragma unroll
@@ -804,7 +813,7 @@ __device__ __forceinline__ void grad_x(const LossArgs& a, unsigned id, char* lds
 // grad_table of a piece: [width x rows] = X^T dZ over a share of the tokens.
 template <typename T, typename S>
 __device__ __forceinline__ void grad_table(const LossArgs& a, unsigned id, char* lds) {
-    typedef ColumnsOfPieces<T, S::BM, S::NT> A;
+    typedef ColumnsOfPieces<T, S::BM, S::NT, S::BM == 128> A;  // the widest's columns are all there
     typedef ColumnsOfPieces<T, S::BN, S::NT> B;
     const int col_tiles = (a.width + S::BM - 1) / S::BM, row_tiles = a.piece / S::BN;
     const int col0 = (id % col_tiles) * S::BM;
@@ -814,7 +823,7 @@ __device__ __forceinline__ void grad_table(const LossArgs& a, unsigned id, char*
     const int k0 = (int)((long long)steps * split / a.t_splits), k1 = (int)((long long)steps * (split + 1) / a.t_splits);
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, half = lane >> 5;
     const unsigned base = lds_address(lds);
-    const A tokens(a.xg, a.t_pad, col0);
+    const A tokens(a.xg, a.x_pad, col0, a.width8);
     const B dz(a.dz, a.t_pad, row0);
     const int a_block = (wave / S::WN) * S::MA, b_block = (wave % S::WN) * S::NB;
     const uint2 at = A::place(lane);
@@ -844,7 +853,7 @@ __device__ __forceinline__ void grad_table(const LossArgs& a, unsigned id, char*
 #pragma unroll
         for (int i = 0; i < S::MA; ++i) {
             const int c0 = col0 + 32 * (a_block + i);
-            if (a.t_splits > 1) {
+            if (a.part_t) {
                 float* to = a.part_t + ((long long)split * a.piece + row) * a.width;
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
@@ -981,6 +990,8 @@ long long finish(long long places, long long first, long long a, long long secon
 // How a call is cut.
 struct Cut {
     long long t_pad, width8, t_all;
+    long long band;    // tokens that dZ is written for at once, whole tiles
+    int bands;
     int splits, slim;  // splits: at most
     int piece, pieces, x_splits, t_splits;
 };
@@ -989,13 +1000,16 @@ Cut cut(long long t, long long rows, long long width, bool grad) {
     Cut c;
     c.t_all = grad && t <= kTwice ? 2 * t : t;
     c.t_pad = ceil_div(c.t_all, kTokenPad) * kTokenPad;
-    // whole tiles of columns: past the width they are zeros
-    c.width8 = ceil_div(width, width > 128 ? 256 : 128) * (width > 128 ? 32 : 16);
     c.slim = c.t_all <= 32;
+    // whole tiles of columns of the widest shape, and stages where they are read: zeros past the width
+    c.width8 = width > 128 ? ceil_div(width, 256) * 32 : c.slim ? ceil_div(width, kStep) * (kStep / 8) : width / 8;
+    // so many tokens that 256 rows' dZ is a piece of its own
+    c.bands = (int)ceil_div(c.t_pad * 2 * kRowTile, kPieceBytes);
+    c.band = ceil_div(ceil_div(c.t_pad, c.bands), kTokenPad) * kTokenPad;
+    c.bands = (int)ceil_div(c.t_pad, c.band);
     const long long tiles = ceil_div(rows, kRowTile), token_tiles = c.slim ? 1 : c.t_pad / kTokenPad;
     c.splits = clamp(4096 / token_tiles, 1, 4 * tiles);
-    long long piece = kPieceBytes / (2 * c.t_pad) / kRowTile * kRowTile;
-    if (piece < kRowTile) piece = kRowTile;
+    const long long piece = kPieceBytes / (2 * c.band) / kRowTile * kRowTile;
     c.pieces = (int)ceil_div(tiles * kRowTile, piece);
     c.piece = (int)(ceil_div(tiles, c.pieces) * kRowTile);
     c.pieces = (int)ceil_div(tiles * kRowTile, c.piece);
@@ -1003,9 +1017,9 @@ Cut cut(long long t, long long rows, long long width, bool grad) {
     // Both gradients' products into blocks enough for one on each of 256 CUs, since they run
     // together (4,096 tokens of 512 by 214,272 rows: 3.9 ms; 4.1 with twice as many, whose partial
     // sums pass memory twice as often, 4.5 with half).
-    const long long x_tiles = cols * (c.t_pad / 128), t_tiles = cols * (c.piece / 128);
+    const long long x_tiles = cols * (c.band / 128), t_tiles = cols * (c.piece / 128);
     c.x_splits = clamp(256 / x_tiles, 1, c.piece / 512 > 1 ? c.piece / 512 : 1);
-    c.t_splits = clamp(256 / t_tiles, 1, c.t_pad / 512 > 1 ? c.t_pad / 512 : 1);
+    c.t_splits = clamp(256 / t_tiles, 1, c.band / 512 > 1 ? c.band / 512 : 1);
     if (!grad) return c;
     // A few blocks more than the card holds begin when the others are done. Where another pair of
     // powers of two ends a quarter sooner it is taken: a step takes about a microsecond with every
@@ -1015,11 +1029,11 @@ Cut cut(long long t, long long rows, long long width, bool grad) {
     const long long places = width > 128 ? 512 : 768;
     auto parts = [&](long long x, long long t1) { return 8 * width * (x * c.t_all + (t1 > 1 ? t1 * c.piece : 0)) / 5000000; };
     auto steps = [&](long long x, long long t1) {
-        return finish(places, x_tiles * x, ceil_div(c.piece / kStep, x), t_tiles * t1, ceil_div(c.t_pad / kStep, t1));
+        return finish(places, x_tiles * x, ceil_div(c.piece / kStep, x), t_tiles * t1, ceil_div(c.band / kStep, t1));
     };
     long long best = (parts(c.x_splits, c.t_splits) + steps(c.x_splits, c.t_splits)) * 3 / 4;
     for (long long x = 1; x == 1 || (x <= 512 && x * 256 <= c.piece); x *= 2)
-        for (long long t1 = 1; t1 == 1 || (t1 <= 256 && t1 * 512 <= c.t_pad); t1 *= 2) {
+        for (long long t1 = 1; t1 == 1 || (t1 <= 256 && t1 * 512 <= c.band); t1 *= 2) {
             if (parts(x, t1) >= best) break;
             const long long time = parts(x, t1) + steps(x, t1);
             if (time < best) best = time, c.x_splits = (int)x, c.t_splits = (int)t1;
@@ -1035,6 +1049,9 @@ bool sizes_ok(int64_t t, int64_t rows, int64_t width) {
 struct Layout {
     long long xg, came, shift, by, hit, part, top, part_x, part_t, dz, total;
 };
+
+// grad_table goes through sums in memory: of shares of the tokens, or of their bands.
+bool parts_of_table(const Cut& c) { return c.t_splits > 1 || c.bands > 1; }
 
 Layout layout(const Cut& c, long long t, long long width, bool grad) {
     Layout l = {};
@@ -1054,8 +1071,8 @@ Layout layout(const Cut& c, long long t, long long width, bool grad) {
         l.by = take(c.t_pad * 4);
         l.top = take(kTops * 4);
         l.part_x = take((long long)c.x_splits * c.t_all * width * 4);
-        l.part_t = take(c.t_splits > 1 ? (long long)c.t_splits * c.piece * width * 4 : 0);
-        l.dz = take((long long)c.piece / 8 * c.t_pad * 16);
+        l.part_t = take(parts_of_table(c) ? (long long)c.bands * c.t_splits * c.piece * width * 4 : 0);
+        l.dz = take((long long)c.piece / 8 * c.band * 16);
     }
     l.total = at;
     return l;
@@ -1080,18 +1097,19 @@ LossArgs make_args(const void* x, int64_t x_stride, const void* table, int64_t t
     a.x = x, a.x_stride = x_stride, a.table = table, a.t_stride = table_stride;
     a.t = (int)t, a.rows = (int)rows, a.width = (int)width, a.ids = ids, a.id_bytes = id_bytes;
     a.scale = scale, a.scale2 = (float)(scale * 1.4426950408889634);
-    a.t_pad = (int)c.t_pad, a.width8 = (int)c.width8, a.t_all = (int)c.t_all;
+    a.x_pad = (int)c.t_pad, a.t_pad = (int)c.band, a.x_tokens = a.t;
+    a.width8 = (int)c.width8, a.t_all = (int)c.t_all;
     a.xg = (uint4*)(ws + l.xg), a.came = (int*)(ws + l.came);
     a.shift = (float*)(ws + l.shift), a.by = (float*)(ws + l.by), a.hit = (float*)(ws + l.hit);
     a.part = (float2*)(ws + l.part), a.top = (float*)(ws + l.top);
-    a.part_x = (float*)(ws + l.part_x), a.part_t = (float*)(ws + l.part_t), a.dz = (uint4*)(ws + l.dz);
+    a.part_x = (float*)(ws + l.part_x), a.part_t = parts_of_table(c) ? (float*)(ws + l.part_t) : nullptr, a.dz = (uint4*)(ws + l.dz);
     a.piece = c.piece, a.x_splits = c.x_splits, a.t_splits = c.t_splits;
-    a.tokens_in = c.slim ? 32 : (int)c.t_pad;
+    a.tokens_in = c.slim ? 32 : (int)c.band;
     return a;
 }
 
 dim3 pack_grid(const LossArgs& a) {
-    return dim3((unsigned)(a.t_pad / 32), (unsigned)ceil_div(a.width8, 8));
+    return dim3((unsigned)(a.x_pad / 32), (unsigned)ceil_div(a.width8, 8));
 }
 
 // Blocks that the card holds at once.
@@ -1138,9 +1156,9 @@ int forward(const LossArgs& a, const Cut& c, hipStream_t stream) {
 
 template <typename T, typename S>
 void gradients(LossArgs a, hipStream_t stream) {
-    a.token_tiles = a.t_pad / S::BN;
+    a.token_tiles = (int)ceil_div(a.tokens_in, S::BN);
     const long long cols = ceil_div(a.width, S::BM);
-    const long long x_blocks = a.gx ? cols * (a.t_pad / S::BN) * a.x_splits : 0;
+    const long long x_blocks = a.gx ? cols * a.token_tiles * a.x_splits : 0;
     const long long blocks = x_blocks + (a.gt ? cols * (a.piece / S::BN) * a.t_splits : 0);
     k_loss_grads<T, S><<<dim3((unsigned)blocks), dim3(S::NT), 0, stream>>>(a, (unsigned)x_blocks);
 }
@@ -1155,32 +1173,42 @@ int backward(LossArgs a, const Cut& c, hipStream_t stream) {
         a.row0 = p * c.piece;
         a.piece = (int)(all - a.row0 < c.piece ? all - a.row0 : c.piece);
         a.first = p == 0;
-        auto dz = [&](auto shape) {
-            typedef decltype(shape) S;
-            over_tiles<S>(a, a.piece, a.tokens_in, [&](const LossArgs& z, dim3 grid, dim3 block) {
-                k_loss_dz<T, S><<<grid, block, 0, stream>>>(z);
-            });
-        };
-        if (c.slim)
-            dz(Slim<T>());
-        else if (a.width <= 32)
-            dz(Narrow<T, 32>());
-        else if (a.width <= 64)
-            dz(Narrow<T, 64>());
-        else if (a.width <= 128)
-            dz(Narrow<T, 128>());
-        else
-            dz(Wide<T>());
-        if (a.width > 128)
-            gradients<T, Wide<T>>(a, stream);
-        else
-            gradients<T, Even<T>>(a, stream);
+        for (int band = 0; band < c.bands; ++band) {
+            const long long from = band * c.band, left = c.t_pad - from;
+            LossArgs b = a;
+            if (c.bands > 1) {  // no token goes through twice
+                b.tokens_in = (int)(left < c.band ? left : c.band);
+                b.t = b.t_all = (int)(a.t - from < c.band ? a.t - from : c.band);
+                b.xg += from, b.came += from, b.shift += from, b.by += from, b.part_x += from * a.width;
+                b.part_t += (long long)band * a.t_splits * a.piece * a.width;
+            }
+            auto dz = [&](auto shape) {
+                typedef decltype(shape) S;
+                over_tiles<S>(b, b.piece, b.tokens_in, [&](const LossArgs& z, dim3 grid, dim3 block) {
+                    k_loss_dz<T, S><<<grid, block, 0, stream>>>(z);
+                });
+            };
+            if (c.slim)
+                dz(Slim<T>());
+            else if (a.width <= 32)
+                dz(Narrow<T, 32>());
+            else if (a.width <= 64)
+                dz(Narrow<T, 64>());
+            else if (a.width <= 128)
+                dz(Narrow<T, 128>());
+            else
+                dz(Wide<T>());
+            if (a.width > 128)
+                gradients<T, Wide<T>>(b, stream);
+            else
+                gradients<T, Even<T>>(b, stream);
+        }
         const bool last = p + 1 == c.pieces;
         const long long there = a.rows - a.row0 < a.piece ? a.rows - a.row0 : a.piece, n = (long long)a.t * a.width;
         Joined joined[2] = {};
         int jobs = 0;
-        if (a.gt && c.t_splits > 1)
-            joined[jobs++] = {a.part_t, c.t_splits, there * a.width, (long long)a.piece * a.width,
+        if (a.gt && a.part_t)
+            joined[jobs++] = {a.part_t, c.bands * c.t_splits, there * a.width, (long long)a.piece * a.width,
                               (T*)a.gt + (long long)a.row0 * a.width};
         if (a.gx && last) joined[jobs++] = {a.part_x, c.x_splits * (a.t_all > a.t ? 2 : 1), n, n, a.gx};
         const long long most = joined[0].n > joined[1].n ? joined[0].n : joined[1].n;

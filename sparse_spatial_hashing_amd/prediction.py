@@ -390,8 +390,9 @@ def row_loss(x: torch.Tensor, table: torch.Tensor, ids: torch.Tensor, *, scale: 
     x [*ids.shape, width] and table [rows, width] (bf16 or fp16: the table of
     ``embed``, or a product's weight), ids int32 or int64. float32 [*ids.shape]; 0
     where an id is not in [0, rows), and nothing passes to or from that token.
-    Logits are never in memory as a whole: their workspace grows with the tokens
-    and stays under some hundred MiB. With ``return_lse`` also the log of the sum
+    Logits are never in memory as a whole: a call's workspace is x once more where it is
+    wider than 128 (to whole 256s), the gradients' that and x in float32 (six bytes an
+    element and a little more), 12 bytes a token, and up to 768 MiB besides. With ``return_lse`` also the log of the sum
     (float32, 0 without a row, not differentiable). A width that is no multiple of 8
     is copied into one that is, by each call; so are rows off 16 bytes or 8 MiB and
     more apart. Differentiable in x and table; what needs no gradient costs none."""

@@ -180,3 +180,28 @@ def test_row_loss_fp16_gradients_at_the_ends_of_float32(t, size, scale):
             over = value.abs() + bound > 65504
             assert (v[over] * value[over].sign() > 65504 - 2 * bound[over]).all(), n
             check(torch.where(over, 0, v), torch.where(over, 0, value), bound, n)
+
+
+@pytest.mark.parametrize("dtype,t,rows,width", [(F16, 600_001, 300, 136), (BF16, 540_000, 260, 40),
+                                                (BF16, 1_100_000, 60, 24), (F16, 524_289, 40, 8)])
+def test_row_loss_bands_of_tokens(dtype, t, rows, width):
+    """More tokens than 256 rows' weights are kept for at once (2^19): the table's gradient is summed over
+    bands of them, a token's own over pieces of the rows."""
+    x, table, ids, grad = _loss_case(t, rows, width, dtype, 41, size=1e-3)
+    x, table, ids, grad = (v.to(DEV) for v in (x, table, ids, grad))
+    x[ids < 0] = math.nan
+    print(f"row loss, bands, {dtype} {t} {rows} {width}", flush=True)
+    with torch.device(DEV):
+        want = ref.row_loss(x, table, ids, 1.0, grad)
+    loss, lse = ssh.row_loss(x, table, ids, return_lse=True)
+    both = ssh.row_loss_grad(grad, x, table, ids, lse)
+    for n, v in zip(("loss", "lse", "gx", "gt"), (loss, lse, *both)):
+        value, bound = want[n]
+        off = (v.double() - value).abs()
+        assert (off <= bound).all(), (n, float((off / bound.clamp(min=1e-300)).nan_to_num(1e30).max()))
+    del want
+    for n in (0, 1):
+        leaves = [x.clone(), table.clone()]
+        leaves[n].requires_grad_()
+        (made,) = torch.autograd.grad(ssh.row_loss(*leaves, ids), leaves[n], grad)
+        assert torch.equal(made, both[n])
