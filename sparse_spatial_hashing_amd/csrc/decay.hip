@@ -737,21 +737,30 @@ bool by_doc(const tok_decay& t) {
 // counting the segments that documents' ends and the tokens of none may add; every
 // segment passes memory with its state four times. 122,880 tokens of 8 heads of 128: 536
 // blocks take 320 us, 504 take 240. Many documents end within a segment each and leave blocks
-// short; at a width of 64 twice as many segments even that out (16 frames of 8,400 to 12,000
-// tokens: 257 us for 276, 64 of 1,400 to 2,000: 165 for 214), at 32 and 128 their states cost
-// more than that gives (117 us for 111, 348 for 332). Few narrow heads would have many segments
+// short, which twice as many segments even out. They are taken where two rounds of them end before
+// one of the others by a fiftieth, a block's beginning and state counted as 3/4 of the width in tokens,
+// and a segment as no longer than a document. (Forward of 8 heads of 64, once and twice: 136,000 tokens in
+// 4 documents 215 us and 220, in 12 227 and 217, in 24 240 and 223, in 64 272 and 219, in 128, no
+// longer than one segment each, 164 and 209; 34,000 tokens in 16 documents 59 and 67, in 64 76 and
+// 69; 2 heads, 136,000 in 16 58 and 69, in 256 76 and 68.) Few narrow heads would have many segments
 // of 128 tokens, which their states are joined along one after the other: at least so many
 // tokens that the join and a segment's chunks take about as long (100,000 tokens of 2 heads of
-// 32: 58 us, 90 without).
+// 32: 59 us, 114 without).
 int segment_of(const tok_decay& t) {
     if (by_doc(t)) return (int)((t.t + 127) / 128 * 128) + 128;  // one
-    const bool twice = padded(t.width) == 64 && t.docs >= 16;
-    const long long each = 512ll * 128 / padded(t.width) * (twice ? 2 : 1) / t.heads;  // of a head
-    long long n = each - t.docs - 2;
-    if (n < each / 2) n = each / 2;
-    if (n < 1) n = 1;
-    n = (t.t + n - 1) / n;
-    n = (n + kChunk - 1) / kChunk * kChunk;
+    const long long each = 512ll * 128 / padded(t.width) / t.heads;  // blocks of a head
+    auto length = [&](long long blocks) {
+        long long n = blocks - t.docs - 2;
+        if (n < blocks / 2) n = blocks / 2;
+        if (n < 1) n = 1;
+        n = (t.t + n - 1) / n;
+        return (n + kChunk - 1) / kChunk * kChunk;
+    };
+    const long long doc = (t.t + t.docs - 1) / t.docs, more = 3 * padded(t.width) / 4;
+    auto takes = [&](long long n) { return (n < doc ? n : doc) + more; };
+    long long n = length(each);
+    const long long half = length(2 * each);
+    if (2 * 50 * takes(half) < 49 * takes(n)) n = half;
     while (n * n < 2 * (t.t / t.docs)) n += kChunk;
     if (n < 128) n = 128;
     if (n > 65536) n = 65536;

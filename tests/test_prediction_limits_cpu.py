@@ -1,5 +1,7 @@
 """Where the limits of rotary positions, attention with decay and the loss over a table's
 rows lie, without a GPU."""
+import ctypes
+
 from sparse_spatial_hashing_amd import prediction
 
 LIB = prediction._lib
@@ -31,3 +33,21 @@ def test_workspaces_of_the_loss():
     # where x is small
     assert LIB.tok_row_loss_grad_workspace_bytes(1 << 20, 4, 8) < 321 * mib
     assert LIB.tok_row_loss_grad_workspace_bytes(1 << 22, 4, 8) < 513 * mib
+
+
+def _states_kept(t, docs, heads, width):
+    strides = (heads * width, width)
+    return LIB.tok_decay_carry_rows(ctypes.byref(prediction._Decay(
+        dtype=1, heads=heads, kv_heads=heads, width=width, t=t, docs=docs, offsets=4096, decay=4096, scale=1.0,
+        q_stride=strides, k_stride=strides, v_stride=strides, g_stride=strides)))
+
+
+def test_more_segments_where_documents_end_in_them():
+    """Twice as many where that evens out what documents' ends leave: not from a number of documents on."""
+    each = lambda heads, width: 512 * 128 // width // heads
+    for t, docs, heads, width in ((136000, 16, 8, 64), (163000, 16, 8, 64), (136000, 64, 8, 64), (34000, 64, 8, 64),
+                                  (136000, 24, 8, 128), (136000, 256, 2, 64)):
+        assert _states_kept(t, docs, heads, width) > 1.2 * each(heads, width), (t, docs, heads, width)
+    for t, docs, heads, width in ((34000, 16, 8, 64), (136000, 16, 2, 64), (136000, 128, 8, 64), (136000, 4, 8, 64),
+                                  (144001, 4, 8, 32), (136000, 64, 2, 64), (34000, 24, 8, 64), (100, 1, 8, 64)):
+        assert _states_kept(t, docs, heads, width) <= each(heads, width), (t, docs, heads, width)
