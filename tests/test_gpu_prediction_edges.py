@@ -12,7 +12,7 @@ if not torch.cuda.is_available():
 
 import sparse_spatial_hashing_amd as ssh  # noqa: E402
 import prediction_reference as ref  # noqa: E402
-from test_gpu_prediction import _decay_compare, _loss_case  # noqa: E402
+from test_gpu_prediction import _decay_case, _decay_compare, _loss_case, _on_gpu  # noqa: E402
 from token_reference import check  # noqa: E402
 
 DEV = torch.device("cuda:0")
@@ -205,3 +205,28 @@ def test_row_loss_bands_of_tokens(dtype, t, rows, width):
         leaves[n].requires_grad_()
         (made,) = torch.autograd.grad(ssh.row_loss(*leaves, ids), leaves[n], grad)
         assert torch.equal(made, both[n])
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("reverse", [False, True])
+@pytest.mark.parametrize("width,heads,kv_heads,lens", [
+    (32, 2, 1, [20000, 3000]), (128, 1, 1, [9000, 40]), (64, 16, 4, [9000, 7011]), (40, 12, 6, [12000]),
+    (64, 8, 8, [370 + 17 * (i % 20) for i in range(64)])])
+def test_decay_gradients_of_longer_segments(dtype, reverse, width, heads, kv_heads, lens):
+    """Segments of more than 128 tokens (the last case: twice as many as places, since documents end in them)."""
+    s, at = _decay_case(lens, heads, kv_heads, width, dtype, 43, 5)
+    g = {n: x.to(DEV) for n, x in s.items()}
+    offsets = torch.tensor(at, dtype=torch.int32, device=DEV)
+    print(f"decay, longer segments, {dtype} {len(lens)} documents, width {width} heads {heads}/{kv_heads}", flush=True)
+    more = dict(state=g["state"], reverse=reverse)
+    out, last, carry = ssh.decay_attend(g["q"], g["k"], g["v"], g["decay"], offsets, return_carry=True, **more)
+    rows = carry.shape[0]
+    assert s["q"].shape[0] // rows > 128, rows
+    assert len(lens) < 64 or rows > 512 * 128 // width // heads  # doubled
+    made = dict(zip(("gq", "gk", "gv", "gs"),
+                    ssh.decay_attend_grad(g["grad"], g["q"], g["k"], g["v"], g["decay"], carry, offsets,
+                                          grad_state=g["grad_state"], **more)), out=out, last=last)
+    want = _on_gpu(ref.decay_attend, s["q"], s["k"], s["v"], s["decay"], at, width ** -0.5, s["state"], reverse,
+                   s["grad"], s["grad_state"])
+    for n, x in made.items():
+        check(x, *want[n], n)
