@@ -48,6 +48,7 @@ namespace {
 constexpr long long kMaxElems = (1ll << 31) - 4096;
 constexpr int kMaxDocs = 1 << 20;
 constexpr int kChunk = 32;
+constexpr int kAlone = 256;  // tokens of a segment in a call of one launch (of 512: 3,000 next to 300 75 -> 83 us)
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLargest = 3.402823466e+38f;
 
@@ -80,6 +81,7 @@ struct DecayArgs {
     int t, docs, heads, width;
     int segment;          // tokens: a multiple of kChunk
     int segments;
+    int more;             // of them, in a call of one launch, those that begin inside a document
     unsigned first_block;
 };
 
@@ -130,7 +132,7 @@ __device__ __forceinline__ Part row_of(const DecayArgs& a, int doc, int row) {
     Part p;
     p.doc = doc;
     p.lo = __builtin_amdgcn_readfirstlane(tok_boundary(a.offsets, a.docs, a.t, doc + 1));
-    p.n = max(0, tok_boundary(a.offsets, a.docs, a.t, doc + 2) - p.lo);
+    p.n = max(0, __builtin_amdgcn_readfirstlane(tok_boundary(a.offsets, a.docs, a.t, doc + 2)) - p.lo);
     p.row = row < 0 ? p.lo / a.segment : row;  // below zero: its first
     p.from = __builtin_amdgcn_readfirstlane((p.row - p.lo / a.segment) * a.segment);
     p.last = false;
@@ -141,6 +143,31 @@ __device__ __forceinline__ Part row_of(const DecayArgs& a, int doc, int row) {
 // The document that a row is of: the last token of the row's stretch of `segment` tokens is its.
 __device__ __forceinline__ int doc_of_row(const DecayArgs& a, int row) {
     return tok_range(a.offsets, a.docs, a.t, (row + 1) * a.segment - 1) - 1;
+}
+
+// A document's first tokens, or further ones of a document longer than a segment, where every block
+// starts from the document's beginning: the numbers below a.more are those of rows of carry, whose
+// segments' successors they are, the longest way first; then one for each range.
+__device__ __forceinline__ Part alone_part(const DecayArgs& a, int slot) {
+    Part p;
+    if (slot < a.more) {
+        const int row = a.more - 1 - slot;
+        p = row_of(a, doc_of_row(a, row), row);
+        if (p.none) return p;
+        p.from = p.to;
+        p.to = part_end(p.from, p.n, a.segment);
+    } else {
+        const int range = slot - a.more;
+        p.lo = __builtin_amdgcn_readfirstlane(tok_boundary(a.offsets, a.docs, a.t, range));
+        p.n = max(0, __builtin_amdgcn_readfirstlane(tok_boundary(a.offsets, a.docs, a.t, range + 1)) - p.lo);
+        p.doc = range >= 1 && range <= a.docs ? range - 1 : -1;
+        p.from = 0;
+        p.to = p.doc < 0 ? p.n : part_end(0, p.n, a.segment);
+        p.none = false;
+    }
+    p.last = p.to == p.n;
+    p.row = 0;
+    return p;
 }
 
 // decay * log2(e) of a head: never negative, and at most what leaves nothing of a token.
@@ -351,34 +378,25 @@ struct Decay {
 
 // The segment, head and walk of a block: walks of one part of a document run together,
 // since they read the same tensors.
-__device__ __forceinline__ int block_of(const DecayArgs& a, int* head, int* walk) {
-    unsigned id = a.first_block + xcd_block(blockIdx.x, gridDim.x);
+__device__ __forceinline__ int block_of(const DecayArgs& a, int* head, int* walk, unsigned apart = 0) {
+    // the first `apart` blocks of a launch one by one over the XCDs
+    const unsigned bid = blockIdx.x;
+    unsigned id = a.first_block + (bid < apart ? bid : apart + xcd_block(bid - apart, gridDim.x - apart));
     *walk = id % a.walks;
     id /= a.walks;
     *head = id % a.heads;
     return id / a.heads;
 }
 
-// What a segment adds to the state that enters it; nothing needs a document's last.
+// S <- what it is after the first chunks of a part of a document, all of them whole.
 template <typename T, int W>
-__global__ __launch_bounds__(2 * W, 2) void k_decay_sum(DecayArgs a) {
+__device__ __forceinline__ void add_chunks(typename Decay<T, W>::State& s, const DecayArgs& a, const Walk& walk,
+                                           const Part& d, int head, int chunks, float rate, unsigned base) {
     typedef Decay<T, W> D;
-    __shared__ __align__(1024) char lds[D::kBuffers * 2 * D::kTile];
-    int head, role;
-    const int row = block_of(a, &head, &role);
-    const Part d = row_of(a, doc_of_row(a, row), row);
-    if (d.none) return;
-    const Walk& walk = a.walk[0];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, half = lane >> 5;
-    const float rate = rate_of(a, head);
-    const unsigned base = lds_address(lds);
-    const int chunks = a.segment / kChunk;  // whole: a document goes on after it
     float w[16];
     D::leaving(w, walk, rate, kChunk, half);
     const uint2 k_in = D::template column_place<true>(lane), v_in = D::template column_place<false>(lane);
-    typename D::State s;
-#pragma unroll
-    for (int b = 0; b < D::kBlocks; ++b) s[b] = zero16();
     typename D::Fall fallen;
     const typename D::Rows k(walk.k, head, walk, d), v(walk.v, head, walk, d);
     auto issue = [&](int c, int buf) {
@@ -405,8 +423,26 @@ __global__ __launch_bounds__(2 * W, 2) void k_decay_sum(DecayArgs a) {
         D::advance(s, make_uint2(k_in.x + on, k_in.y + on), x, w, by);
         buf = buf == D::kBuffers - 1 ? 0 : buf + 1;
     }
+}
+
+// What a segment adds to the state that enters it; nothing needs a document's last.
+template <typename T, int W>
+__global__ __launch_bounds__(2 * W, 2) void k_decay_sum(DecayArgs a) {
+    typedef Decay<T, W> D;
+    __shared__ __align__(1024) char lds[D::kBuffers * 2 * D::kTile];
+    int head, role;
+    const int row = block_of(a, &head, &role);
+    const Part d = row_of(a, doc_of_row(a, row), row);
+    if (d.none) return;
+    const Walk& walk = a.walk[0];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    typename D::State s;
+#pragma unroll
+    for (int b = 0; b < D::kBlocks; ++b) s[b] = zero16();
+    // whole chunks: a document goes on after it
+    add_chunks<T, W>(s, a, walk, d, head, a.segment / kChunk, rate_of(a, head), lds_address(lds));
     D::store_state(s, walk.carry + ((long long)d.row * a.heads + head) * a.width * a.width, a.width,
-                   32 * wave + (lane & 31), half);
+                   32 * wave + (lane & 31), lane >> 5);
 }
 
 // The states after a document's segments but the last, over their sums: four elements of
@@ -507,15 +543,16 @@ __device__ __forceinline__ void step_through(const DecayArgs& a, const Walk& wal
         if (row + j < a.width) *(float4*)(to + (row + j) * a.width + c) = s[j];
 }
 
-// A segment from the state that enters it.
-template <typename T, int W>
+// A segment from the state that enters it. ALONE: that is not in carry, and a block that does not
+// begin with its document takes the state up to there first.
+template <typename T, int W, bool ALONE>
 __global__ __launch_bounds__(2 * W, W == 32 ? 3 : 2) void k_decay_run(DecayArgs a) {
     typedef Decay<T, W> D;
     __shared__ __align__(1024) char lds[D::kBuffers * 3 * D::kTile];
     int head, role;
-    const int slot = block_of(a, &head, &role);
+    const int slot = block_of(a, &head, &role, ALONE && a.first_block == 0 ? a.more * a.heads * a.walks : 0);
     const Walk& walk = a.walk[role];
-    const Part d = find_part(a, slot);
+    const Part d = ALONE ? alone_part(a, slot) : find_part(a, slot);
     if (d.none) return;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, half = lane >> 5, i = lane & 31;
     const long long out_row = (long long)a.heads * a.width;
@@ -532,16 +569,27 @@ __global__ __launch_bounds__(2 * W, W == 32 ? 3 : 2) void k_decay_run(DecayArgs 
         return;
     }
     const long long size = (long long)a.width * a.width;
-    const float* from = d.from > 0   ? walk.carry + ((long long)(d.row - 1) * a.heads + head) * size
-                        : walk.state ? walk.state + ((long long)d.doc * a.heads + head) * size
-                                     : nullptr;
-    if (a.walks == 1 && d.to - d.from <= kFew) {  // forward
+    const float* from = d.from > 0 && !ALONE ? walk.carry + ((long long)(d.row - 1) * a.heads + head) * size
+                        : walk.state             ? walk.state + ((long long)d.doc * a.heads + head) * size
+                                                 : nullptr;
+    const bool later = ALONE && d.from > 0;
+    if (a.walks == 1 && d.to - d.from <= kFew && !later) {  // forward
         step_through<T, W>(a, walk, d, head, from, (float*)lds);
         return;
     }
     const int column = 32 * wave + i;
     const float rate = rate_of(a, head);
     const unsigned base = lds_address(lds);
+    typename D::State s;
+    bool some = from != nullptr;  // the state holds something
+    if (later) {
+        D::load_state(s, from, a.width, walk.turned, column, half);
+        Part whole = d;
+        whole.from = 0;
+        add_chunks<T, W>(s, a, walk, whole, head, d.from / kChunk, rate, base);
+        __syncthreads();  // all are done with the last tiles
+        some = true;
+    }
     const int chunks = (d.to - d.from + kChunk - 1) / kChunk;
     const typename D::Rows q_rows(walk.q, head, walk, d), k_rows(walk.k, head, walk, d), v_rows(walk.v, head, walk, d);
     auto issue = [&](int c, int buf) {
@@ -553,9 +601,7 @@ __global__ __launch_bounds__(2 * W, W == 32 ? 3 : 2) void k_decay_run(DecayArgs 
     };
     if (chunks > 0) issue(0, 0);
     if (D::kBuffers > 2 && chunks > 1) issue(1, 1);
-    typename D::State s;
-    bool some = from != nullptr;  // the state holds something
-    D::load_state(s, from, a.width, walk.turned, column, half);
+    if (!later) D::load_state(s, from, a.width, walk.turned, column, half);
     // settled here: inside the loop their wait would be for the tiles under way as well
 #pragma unroll
     for (int b = 0; b < D::kBlocks; ++b) asm volatile("" : "+v"(s[b]));
@@ -591,7 +637,9 @@ __global__ __launch_bounds__(2 * W, W == 32 ? 3 : 2) void k_decay_run(DecayArgs 
         }
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
-            const int at = d.from + c * kChunk + 16 * q + (lane & 15), col = 32 * wave + 8 * quarter_piece(lane);
+            int l = lane;
+            if (ALONE && W == 32) asm volatile("" : "+v"(l));  // else one register is spilled around the loop
+            const int at = d.from + c * kChunk + 16 * q + (l & 15), col = 32 * wave + 8 * quarter_piece(l);
             const long long token = walk.back ? d.lo + d.n - 1 - at : d.lo + at;
             if (at < d.to && col < a.width) *(uint4*)((T*)walk.out + token * out_row + head * a.width + col) = made[q];
         }
@@ -723,10 +771,14 @@ bool check(const tok_decay* t) {
 }
 
 // Short documents that fill the card with one block each (and head), or steps of decoding: no
-// segments, which saves two launches (500 of 30 tokens, 8 heads of 32: 19 us for 25; 256 steps
-// of 16 heads of 128: 106 for 118). The host knows no lengths, and one document may hold nearly
-// all tokens, in one block a head (8,000 next to 400 of 20, 8 heads of 32: 340 us, 44 with
-// segments); a wider state takes longer over them and has less to save.
+// states kept and one launch, not three (546 of 30 tokens, 8 heads of 32: 13 us for 18; 256 steps
+// of 16 heads of 128: 25 for 35). The host knows no lengths, and one document may hold nearly all
+// tokens. Its segments of kAlone tokens go to blocks of their own there, of which each takes the
+// state up to where it begins first, at a third of the walk's time a token. Forward of a prompt next
+// to as many steps as it has tokens, 8 heads (in one launch; in three; with a block a document):
+// 2,048 of 64 56, 74 and 142 us, 2,048 of 128 120, 163 and 224, 8,192 of 32 176, 108 and 390.
+// Among fewer short ones it costs most: 8,000 tokens next to 400 of 20, 8 heads of 32: 175, 40 and 336.
+// It ends at 16,384 tokens of width 32 and fewer of wider ones.
 bool by_doc(const tok_decay& t) {
     return t.t <= 16384 * 32 / padded(t.width) &&
            (t.t <= 2ll * t.docs || (t.t <= 64ll * t.docs && (long long)t.docs * t.heads >= 512));
@@ -811,17 +863,22 @@ void states(DecayArgs a, hipStream_t stream) {
 }
 
 template <typename T, int W>
-void run(DecayArgs a, hipStream_t stream) {
+void run(const tok_decay& t, DecayArgs a, hipStream_t stream) {
+    const bool alone = by_doc(t);
+    if (alone) a.segment = kAlone, a.more = a.t / kAlone, a.segments = t.docs + 2 + a.more;
     in_launches((long long)a.segments * a.heads * a.walks, 2 * W, [&](unsigned first, dim3 grid) {
         a.first_block = first;
-        k_decay_run<T, W><<<grid, dim3(2 * W), 0, stream>>>(a);
+        if (alone)
+            k_decay_run<T, W, true><<<grid, dim3(2 * W), 0, stream>>>(a);
+        else
+            k_decay_run<T, W, false><<<grid, dim3(2 * W), 0, stream>>>(a);
     });
 }
 
 template <typename T, int W>
 int forward(const tok_decay& t, DecayArgs a, hipStream_t stream) {
     if (!whole(t)) states<T, W>(a, stream);
-    run<T, W>(a, stream);
+    run<T, W>(t, a, stream);
     const hipError_t e = hipGetLastError();
     return e == hipSuccess ? VOX_OK : ssh_hip_fail(e);
 }
@@ -854,7 +911,7 @@ int backward(const tok_decay& t, DecayArgs a, const Gradients& g, hipStream_t st
     // grad_q: grad against v and k, along the forward's
     q.q = g.g, q.k = g.v, q.v = g.k, q.out = g.gq, q.state = g.state, q.carry = g.carry, q.turned = 1;
     a.walks = 3;
-    run<T, W>(a, stream);
+    run<T, W>(t, a, stream);
     if (g.part)
         in_launches((2 * n + 2047) / 2048, 256, [&](unsigned first, dim3 grid) {
             k_decay_share<T><<<grid, dim3(256), 0, stream>>>(g.part, (T*)g.gv, (T*)g.gk, n, g.group, a.width, first);

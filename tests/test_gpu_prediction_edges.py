@@ -230,3 +230,64 @@ def test_decay_gradients_of_longer_segments(dtype, reverse, width, heads, kv_hea
                    s["grad"], s["grad_state"])
     for n, x in made.items():
         check(x, *want[n], n)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("reverse", [False, True])
+@pytest.mark.parametrize("width,heads,kv_heads", [(8, 2, 1), (32, 2, 2), (64, 2, 1), (128, 2, 2)])
+def test_decay_long_documents_among_short_ones(dtype, reverse, width, heads, kv_heads):
+    """Calls that go by one launch: documents of more than 256 tokens take several blocks there, each from
+    the document's beginning on."""
+    for lens, first, state in (([1] * 150 + [900] + [1] * 150 + [1], 0, True),
+                               ([3, 0] * 100 + [257, 256, 513, 258, 0] + [4] * 60, 7, False),
+                               ([0] * 300 + [1283], 2, True)):
+        s, at = _decay_case(lens, heads, kv_heads, width, dtype, 47, first, state)
+        made = _decay_compare(s, at, f"decay, long ones among short, {dtype} {len(lens)} width {width}", reverse)
+        carry = ssh.decay_attend(*(s[n].to(DEV) for n in "qkv"), s["decay"].to(DEV),
+                                 torch.tensor(at, dtype=torch.int32, device=DEV), return_carry=True)[2]
+        assert carry.shape[0] == 0
+        # the same inputs give the same bits
+        again = _decay_compare(s, at, "again", reverse)
+        assert all(made[n] is None or torch.equal(made[n], again[n]) for n in made)
+
+
+@pytest.mark.parametrize("how", ["rising and back", "falling", "past the end", "jumps", "right"])
+@pytest.mark.parametrize("reverse", [False, True])
+@pytest.mark.parametrize("heads,kv_heads,width", [(2, 1, 32), (2, 2, 72)])
+def test_decay_one_launch_writes_nothing_outside(how, reverse, heads, kv_heads, width):
+    """Wrong offsets of calls that go by one launch, with every output inside a fence."""
+    from sparse_spatial_hashing_amd import prediction
+    from test_gpu_token_paths import Fenced
+    lib, stream = prediction._lib, torch.cuda.current_stream().cuda_stream
+    t, docs = 1100, 600
+    gen = torch.Generator(device=DEV).manual_seed(5)
+    jumps = torch.randint(-50, t + 50, (docs + 1,), generator=torch.Generator().manual_seed(6)).tolist()
+    ends = {"rising and back": [0] * 200 + [t] * 200 + [300] * 201, "falling": [t - 2 * i for i in range(docs + 1)],
+            "past the end": [-2**31] * 100 + [5] * 200 + [2**31 - 1] * 301, "jumps": jumps,
+            "right": list(range(300)) + [t - 300 + i for i in range(301)]}[how]
+    q, k, v, g = (torch.randn((t, h, width), generator=gen, device=DEV).to(BF16)
+                  for h in (heads, kv_heads, kv_heads, heads))
+    shape = (docs, heads, width, width)
+    state, gl = (torch.randn(shape, generator=gen, device=DEV) for _ in range(2))
+    decay, offsets = torch.full((heads,), 0.01, device=DEV), torch.tensor(ends, dtype=torch.int32, device=DEV)
+    a, kept, _ = prediction._decay_args(q, k, v, decay, offsets, None, reverse, g)
+    assert lib.tok_decay_carry_rows(a) == 0
+    f = Fenced()
+    out, last = f.take(q.shape, BF16), f.take(shape, F32)
+    print(f"fenced decay in one launch, {how} reverse {reverse} width {width}", flush=True)
+    assert lib.tok_decay_attend(a, q.data_ptr(), k.data_ptr(), v.data_ptr(), state.data_ptr(), out.data_ptr(),
+                                last.data_ptr(), None, stream) == 0
+    f.check()
+    nbytes = lib.tok_decay_grad_workspace_bytes(a)
+    ws, made = f.take((nbytes,), torch.uint8) if nbytes else None, [f.take(x.shape, BF16) for x in (q, k, v)]
+    gs = f.take(shape, F32)
+    assert lib.tok_decay_attend_grad(a, q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), state.data_ptr(), None,
+                                     gl.data_ptr(), *[x.data_ptr() for x in made], gs.data_ptr(),
+                                     None if ws is None else ws.data_ptr(), nbytes, stream) == 0
+    f.check()
+    if how == "right":
+        m = dict(state=state, reverse=reverse)
+        want = ssh.decay_attend(q, k, v, decay, offsets, return_carry=True, **m)
+        grads = ssh.decay_attend_grad(g, q, k, v, decay, want[2], offsets, grad_state=gl, **m)
+        for x, y in zip((out, last, *made, gs), (*want[:2], *grads)):
+            assert torch.equal(x, y)
