@@ -183,9 +183,10 @@ int tok_scan_grad(const void* grad_y, const void* gate, const void* x, const flo
  * Axis c has the elements from 2 * c * pairs on; its pair p is the elements
  * (p, pairs + p) of them, or interleaved (2 p, 2 p + 1). The rest of the head is
  * copied. freqs [axes, pairs] is float64 (radians a position), contiguous: the
- * angle is reduced to a turn in 64 bits, so that far positions lose nothing. Sines,
- * cosines and products are in float32, rounded once to x's type. out is
- * contiguous. The gradient of x is the gradient of out turned back.
+ * angle is reduced to a turn in 64 bits, with what their roundings leave, and is
+ * right to 2^-25 of a turn however far the position. Sines, cosines and products
+ * are in float32, rounded once to x's type. out is contiguous. The gradient of x
+ * is the gradient of out turned back.
  * Limits: 0 <= tokens <= 2^31 - 1, 1 <= heads, width <= 65536; a finite
  * frequency's product with a position below 2^52 turns.
  */

@@ -291,3 +291,25 @@ def test_decay_one_launch_writes_nothing_outside(how, reverse, heads, kv_heads, 
         grads = ssh.decay_attend_grad(g, q, k, v, decay, want[2], offsets, grad_state=gl, **m)
         for x, y in zip((out, last, *made, gs), (*want[:2], *grads)):
             assert torch.equal(x, y)
+
+
+def test_rotate_far_and_fast():
+    """The turn is right to 2^-25 wherever it is: positions and frequencies of 2^31 turns and far more, against
+    their exact product."""
+    from decimal import Decimal, getcontext
+    getcontext().prec = 60
+    whole = 2 * Decimal("3.14159265358979323846264338327950288419716939937510582097494459230781640628620899")
+    freqs = [1.0, 3.0, 10.0, 0.1, 1e-4, 1234.5678, 1e6 / 3]
+    positions = [2**31 - 1, -2**31, 2**31 - 2, 1987654321, -1234567891, 2**30 + 1, 99991, -1, 0]
+    x = torch.zeros((len(positions), 1, 2 * len(freqs)), device=DEV)
+    x[..., :len(freqs)] = 1.0
+    got = ssh.rotate(x, torch.tensor(positions, dtype=torch.int32, device=DEV),
+                     torch.tensor([freqs], dtype=torch.float64, device=DEV)).cpu().double()[:, 0]
+    # the turn, two steps of a sine near 1, and the products'
+    bound = 2 * math.pi * 2.0 ** -25 + 4 * 2.0 ** -24
+    for i, p in enumerate(positions):
+        for j, f in enumerate(freqs):
+            turns = Decimal(p) * Decimal(f) / whole
+            angle = float((turns - turns.to_integral_value()) * whole)
+            assert abs(got[i, j] - math.cos(angle)) <= bound, (p, f)
+            assert abs(got[i, len(freqs) + j] - math.sin(angle)) <= bound, (p, f)
