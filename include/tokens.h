@@ -243,7 +243,8 @@ int tok_decay_attend(const tok_decay* args, const void* q, const void* k, const 
 
 /* Gradients of q, k, v and state (grad_state, or NULL) from those of out and of
  * last_state (grad_last, or NULL: zeros), with the carry of the forward call.
- * Gradients of shared key heads are summed over their query heads in float32. */
+ * Gradients of shared key heads are summed over their query heads in float32, whose
+ * parts are in the workspace: 8 bytes an element of q. */
 int tok_decay_attend_grad(const tok_decay* args, const void* q, const void* k, const void* v,
                           const void* grad_out, const float* state, const float* carry,
                           const float* grad_last, void* grad_q, void* grad_k, void* grad_v,

@@ -23,16 +23,18 @@
 // weights (q.k) e^-r(i-j) are taken in two parts: a few tokens' outputs are a few weights'
 // and would show each one's rounding. The state's copy for the product with q is rounded
 // to the tensors' type, as the 16-bit matrix instructions take it: a sum of `width` such
-// roundings. In fp16 each of the three is first multiplied with a power of two that
-// brings its largest to about 1.
+// roundings, 2.3e-3 of an output in bf16 where the result's own are 1.7e-3. (In two parts it
+// would show none: a training step over 122,880 tokens of 8 heads of 128 1,390 us for 1,205, the
+// gradients at widths of 64 and less up to 10% more.) In fp16 each of the three is first multiplied
+// with a power of two that brings its largest to about 1.
 //
-// Bounds. k and v are read twice, all else once; the gradients read nine tensors and the
-// sums two more, where five would do. 122,880 tokens of 8 heads of 128: sums 118 us (504 MB,
-// 4.3 TB/s), their prefix 15, the walk 240 (1 GB, 4.2), the gradients' three walks 680.
-// Without its products the walk takes 216 us, without its loads 185: with two blocks on a
-// CU, memory and products overlap nearly whole. Sixteen frames of 8 heads of 64: 88, 12 and
-// 165 (668 MB, 4.0).
-// Windows of a few dozen tokens pay for each block's beginning: 14 us forward, 28 backward.
+// Bounds. k and v are read twice, all else once; the gradients' walks read 7.3 tensors' bytes of
+// nine that they ask for and the sums two more, where five would do. 122,880 tokens of 8 heads of
+// 128: sums 117 us (530 MB, 4.5 TB/s), their prefix 15, the walk 243 (1.04 GB, 4.3), the gradients'
+// three walks 676 (2.6 GB, 3.9). Without its products the walk takes 216 us, without its loads 185:
+// with two blocks on a CU, memory and products overlap nearly whole. Sixteen frames of 8 heads of
+// 64: 87, 12 and 163 (707 MB, 4.3).
+// Windows of a few dozen tokens pay for each block's beginning: 14 us forward, 30 backward.
 
 #include <hip/hip_runtime.h>
 
@@ -376,8 +378,8 @@ struct Decay {
     };
 };
 
-// The segment, head and walk of a block: walks of one part of a document run together,
-// since they read the same tensors.
+// The segment, head and walk of a block. Walks of one segment run together: the gradients of v and k
+// read the same rows of four tensors, from the document's other end than that of q.
 __device__ __forceinline__ int block_of(const DecayArgs& a, int* head, int* walk, unsigned apart = 0) {
     // the first `apart` blocks of a launch one by one over the XCDs
     const unsigned bid = blockIdx.x;
@@ -447,7 +449,7 @@ __global__ __launch_bounds__(2 * W, 2) void k_decay_sum(DecayArgs a) {
 
 // The states after a document's segments but the last, over their sums: four elements of
 // a state per thread, along the segments. Blocks go by documents or by the rows of carry,
-// whichever are fewer (16 frames took 285 us a call, 290 by rows; 3,000 windows of 40, 8 heads of
+// whichever are fewer (16 frames took 2% more by rows; 3,000 windows of 40, 8 heads of
 // 64, 294 us, 387 with a block for every document and each of its segments).
 __global__ __launch_bounds__(256) void k_decay_join(DecayArgs a, int slices, bool by_row) {
     unsigned id = a.first_block + blockIdx.x;

@@ -7,8 +7,9 @@
 // dZ = (exp(z - lse) - [row is the token's]) grad, rounded, to the workspace, from
 // where two products follow: grad_x += dZ W and grad_table = dZ^T X. A piece is as
 // many rows as dZ of 256 MB holds, about what the cache between HBM and the XCDs does
-// (4,096 tokens of 512 by 214,272 rows: 4.1 ms; 4.5 with pieces of 128 MB, whose partial
-// sums of grad_x pass memory twice as often, and 4.0 with 2 GB).
+// (a training step of 4,096 tokens of 512 by 214,272 rows: a tenth more with pieces of 128 MB,
+// whose partial sums of grad_x pass memory twice as often, 3% less with 2 GB). Where 256 rows of all
+// tokens are more than that, tokens go by bands.
 //
 // Tiles of 32 of the inner index go straight from memory into three buffers of LDS
 // in turn. X and dZ are kept in pieces of 8 elements, [element / 8][token]: a tile
@@ -17,13 +18,13 @@
 // product asks for either. Tokens of up to 128 elements stay in registers while the rows go
 // by, and forward come from x itself.
 //
-// Bounds. 4,096 tokens of 512 by 214,272 rows take 3.76 ms, of which the forward's logits
-// 0.95 (951 TFLOP/s, matrix units busy 47%), dZ in seven pieces 1.18 (764, 34%), the two
-// gradients' products 1.59 (1,130, 57%); a library product of 8192 cubed reaches 1,185 to
-// 1,290. Two wavefronts a SIMD wait for LDS and barriers; in the logits' passes the
+// Bounds. 4,096 tokens of 512 by 214,272 rows take 3.8 ms, of which the forward's logits
+// 0.94 (956 TFLOP/s, matrix units busy 47%), dZ in seven pieces 1.22 (737, 32%), the two
+// gradients' products 1.65 (1,090, 53%; 1.59 to 1.68 with where their loops come to lie in 128 bytes);
+// a library product of 8192 cubed reaches 1,185 to 1,290. Two wavefronts a SIMD wait for LDS and barriers; in the logits' passes the
 // exponentials come on top, an exp2 and two more instructions a logit forward, three, the
 // rounding and 250 MB of stores a piece backward, between the products of a CU's other blocks.
-// A frame of 12,000 tokens of 128 by as many rows, forward: 0.66 ms (1,000 TFLOP/s, 48%). A
+// A frame of 12,000 tokens of 128 by as many rows, forward: 0.65 ms (1,010 TFLOP/s, 47%). A
 // few tokens are bound by memory: 110 MB in 22 us.
 //
 // Roundings. dZ enters the products in the tensors' type; logits, maxima, sums and
@@ -1015,8 +1016,8 @@ Cut cut(long long t, long long rows, long long width, bool grad) {
     c.pieces = (int)ceil_div(tiles * kRowTile, c.piece);
     const long long cols = ceil_div(width, width > 128 ? 256 : 128);
     // Both gradients' products into blocks enough for one on each of 256 CUs, since they run
-    // together (4,096 tokens of 512 by 214,272 rows: 3.9 ms; 4.1 with twice as many, whose partial
-    // sums pass memory twice as often, 4.5 with half).
+    // together (a training step of 4,096 tokens of 512 by 214,272 rows: 5% more with twice as many,
+    // whose partial sums pass memory twice as often, 15% more with half).
     const long long x_tiles = cols * (c.band / 128), t_tiles = cols * (c.piece / 128);
     c.x_splits = clamp(256 / x_tiles, 1, c.piece / 512 > 1 ? c.piece / 512 : 1);
     c.t_splits = clamp(256 / t_tiles, 1, c.band / 512 > 1 ? c.band / 512 : 1);

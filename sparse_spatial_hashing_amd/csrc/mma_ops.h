@@ -71,7 +71,9 @@ __device__ __forceinline__ V lds_read_columns(unsigned first, unsigned second) {
 
 // 16 bytes per lane from memory to LDS, a wavefront's 64 pieces one after another
 // from `to` on. Written out: the compiler would wait for the load before the next
-// read of any LDS. load_wait() and a barrier come before a read.
+// read of any LDS. load_wait() and a barrier come before a read. m0 is a reserved register: the
+// compiler keeps nothing there from one instruction that needs it to another, and warns of a clobber
+// that names it; in these kernels nothing else uses it.
 __device__ __forceinline__ void load_to_lds(unsigned to, const void* base, unsigned offset) {
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
                  :: "s"(to), "v"(offset), "s"(base) : "memory");

@@ -5,7 +5,7 @@
 // piece of a token (16 bytes where the sizes allow it, or two pieces of as much
 // that hold the two halves of its pairs), computes the angles' sines and cosines
 // and turns a head or two of the token with them (122,880 tokens of 10 heads of 128 in
-// bf16: 113 us, 5.6 TB/s with the cache's share; with 1, 3 or 10 heads 161, 118 and 130).
+// bf16: 113 us, 5.6 TB/s, where a large copy reaches 5.2; with 1, 3 or 10 heads 161, 118 and 130).
 
 #include <hip/hip_runtime.h>
 
@@ -137,7 +137,7 @@ int launch(RotateArgs a, long long tokens, hipStream_t stream) {
     a.turned_units = a.axes * a.pairs / (INTER ? V / 2 : V);
     a.units = a.turned_units + (a.width - 2 * a.axes * a.pairs) / V;
     // An angle is computed once for two heads: 122,880 tokens of 10 heads of 128 take 113 us
-    // (5.5 TB/s), 161 with a head each (the angles' instructions bound it), 118 with three
+    // (5.6 TB/s), 161 with a head each (the angles' instructions bound it), 118 with three
     // and 130 with all ten (a wavefront then reads far apart). One head while that fills
     // the card.
     a.per = tokens * a.units * ((a.heads + 1) / 2) < 65536 ? 1 : a.heads < kHeads ? a.heads : kHeads;
