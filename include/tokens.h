@@ -275,7 +275,7 @@ int tok_decay_attend_grad(const tok_decay* args, const void* q, const void* k, c
  * [1e-30, 1e30]. The workspace needs no initial contents, 256-byte aligned. It holds x once (a width
  * over 128 rounded up to whole 256s; forward only then, and of more than 32 tokens), for gradients x in
  * float32 besides and an eighth of x where tokens are more than 2^19, 12 bytes a token, and up to 768 MiB
- * that do not grow with the tokens.
+ * that do not grow with the tokens (three times as much at widths over 4096).
  */
 int64_t tok_row_loss_workspace_bytes(int64_t t, int64_t rows, int64_t width);
 int tok_row_loss(const void* x, int64_t x_stride, const void* table, int64_t table_stride,

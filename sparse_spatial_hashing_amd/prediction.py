@@ -392,7 +392,8 @@ def row_loss(x: torch.Tensor, table: torch.Tensor, ids: torch.Tensor, *, scale: 
     where an id is not in [0, rows), and nothing passes to or from that token.
     Logits are never in memory as a whole: a call's workspace is x once more where it is
     wider than 128 (to whole 256s), the gradients' that and x in float32 (six bytes an
-    element and a little more), 12 bytes a token, and up to 768 MiB besides. With ``return_lse`` also the log of the sum
+    element and a little more), 12 bytes a token, and up to 768 MiB besides (three times as
+    much at widths over 4096). With ``return_lse`` also the log of the sum
     (float32, 0 without a row, not differentiable). A width that is no multiple of 8
     is copied into one that is, by each call; so are rows off 16 bytes or 8 MiB and
     more apart. Differentiable in x and table; what needs no gradient costs none."""

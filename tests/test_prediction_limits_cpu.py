@@ -30,6 +30,8 @@ def test_workspaces_of_the_loss():
                 assert LIB.tok_row_loss_grad_workspace_bytes(t, rows, width) <= \
                     laid + 4 * t * width + t * width // 4 + 768 * mib, \
                     (t, rows, width)
+    for t, rows, width in ((64, 487505351, 59096), (257, 1 << 24, 65536), (4096, 214272, 32768), (16, 1 << 20, 65536)):
+        assert LIB.tok_row_loss_grad_workspace_bytes(t, rows, width) <= 7 * t * (width + 256) + 3 * 768 * mib
     # where x is small
     assert LIB.tok_row_loss_grad_workspace_bytes(1 << 20, 4, 8) < 321 * mib
     assert LIB.tok_row_loss_grad_workspace_bytes(1 << 22, 4, 8) < 513 * mib
