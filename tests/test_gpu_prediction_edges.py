@@ -313,3 +313,45 @@ def test_rotate_far_and_fast():
             angle = float((turns - turns.to_integral_value()) * whole)
             assert abs(got[i, j] - math.cos(angle)) <= bound, (p, f)
             assert abs(got[i, len(freqs) + j] - math.sin(angle)) <= bound, (p, f)
+
+
+def test_graphs_of_long_documents_and_bands():
+    from test_gpu_tokens import _replays
+    s, at = _decay_case([1] * 200 + [700] + [2] * 100, 2, 1, 64, BF16, 53)
+    g, offsets = {n: x.to(DEV) for n, x in s.items()}, torch.tensor(at, dtype=torch.int32, device=DEV)
+    x, table, ids, grad = (v.to(DEV) for v in _loss_case(524_300, 40, 8, BF16, 59))
+
+    def step():
+        out, last, carry = ssh.decay_attend(g["q"], g["k"], g["v"], g["decay"], offsets, state=g["state"],
+                                            return_carry=True)
+        grads = ssh.decay_attend_grad(g["grad"], g["q"], g["k"], g["v"], g["decay"], carry, offsets, state=g["state"],
+                                      grad_state=g["grad_state"])
+        loss, lse = ssh.row_loss(x, table, ids, return_lse=True)
+        return (out, last, *grads, loss, *ssh.row_loss_grad(grad, x, table, ids, lse))
+
+    _replays(step, [g["q"], g["k"], g["v"], g["grad"], g["state"], x, table, grad])
+
+
+def test_two_streams_at_once():
+    """The same operators on two streams over the same tensors, workspaces of their own."""
+    s, at = _decay_case([1] * 200 + [900] + [2] * 100, 2, 1, 64, BF16, 61)
+    g, offsets = {n: x.to(DEV) for n, x in s.items()}, torch.tensor(at, dtype=torch.int32, device=DEV)
+    x, table, ids, grad = (v.to(DEV) for v in _loss_case(3000, 5000, 136, F16, 67))
+
+    def run():
+        made = ssh.decay_attend(g["q"], g["k"], g["v"], g["decay"], offsets, state=g["state"], return_carry=True)
+        grads = ssh.decay_attend_grad(g["grad"], g["q"], g["k"], g["v"], g["decay"], made[2], offsets, state=g["state"])
+        loss, lse = ssh.row_loss(x, table, ids, return_lse=True)
+        return (*made[:2], *grads, loss, *ssh.row_loss_grad(grad, x, table, ids, lse))
+
+    want = run()
+    sides, made = [torch.cuda.Stream() for _ in range(2)], []
+    for side in sides:
+        side.wait_stream(torch.cuda.current_stream())
+    for _ in range(3):
+        for side in sides:
+            with torch.cuda.stream(side):
+                made.append(run())
+    torch.cuda.synchronize()
+    for got in made:
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
