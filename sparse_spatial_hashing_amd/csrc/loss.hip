@@ -19,9 +19,9 @@
 // by, and forward come from x itself.
 //
 // Bounds. 4,096 tokens of 512 by 214,272 rows take 3.8 ms, of which the forward's logits
-// 0.94 (956 TFLOP/s, matrix units busy 47%), dZ in seven pieces 1.22 (737, 32%), the two
-// gradients' products 1.65 (1,090, 53%; 1.59 to 1.68 with where their loops come to lie in 128 bytes);
-// a library product of 8192 cubed reaches 1,185 to 1,290. Two wavefronts a SIMD wait for LDS and barriers; in the logits' passes the
+// 0.94 (956 TFLOP/s, matrix units busy 47%), dZ in seven pieces 1.22 (737, 33%), the two
+// gradients' products 1.62 (1,110, 57%); a library product of 8192 cubed reaches 1,185 to
+// 1,290. Two wavefronts a SIMD wait for LDS and barriers; in the logits' passes the
 // exponentials come on top, an exp2 and two more instructions a logit forward, three, the
 // rounding and 250 MB of stores a piece backward, between the products of a CU's other blocks.
 // A frame of 12,000 tokens of 128 by as many rows, forward: 0.65 ms (1,010 TFLOP/s, 47%). A
@@ -133,6 +133,9 @@ __device__ __forceinline__ void stages(int total, Begin begin, Issue issue, Comp
     if (total > 1) issue(1, 1);
     begin();
     int buf = 0, since = 2;
+    // The loop's place in 64 bytes of code does not change with what comes before it (4,096 tokens of
+    // 512 by 214,272 rows, gradients: 2,832 us, 2,815 to 2,875 without).
+    asm volatile(".p2align 6");
     for (int i = 0; i < total; ++i) {
         if (i + 1 == total)
             load_wait<0>();
