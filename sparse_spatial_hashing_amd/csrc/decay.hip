@@ -30,10 +30,10 @@
 //
 // Bounds. k and v are read twice, all else once; the gradients' walks read 7.3 tensors' bytes of
 // nine that they ask for and the sums two more, where five would do. 122,880 tokens of 8 heads of
-// 128: sums 117 us (530 MB, 4.5 TB/s), their prefix 15, the walk 243 (1.04 GB, 4.3), the gradients'
-// three walks 676 (2.6 GB, 3.9). Without its products the walk takes 216 us, without its loads 185:
+// 128: sums 116 us (530 MB, 4.5 TB/s), their prefix 15, the walk 248 (1.04 GB, 4.2), the gradients'
+// three walks 692 (2.6 GB, 3.8). Without its products the walk takes 216 us, without its loads 185:
 // with two blocks on a CU, memory and products overlap nearly whole. Sixteen frames of 8 heads of
-// 64: 87, 12 and 163 (707 MB, 4.3).
+// 64: 87, 12 and 164 (707 MB, 4.3).
 // Windows of a few dozen tokens pay for each block's beginning: 14 us forward, 30 backward.
 
 #include <hip/hip_runtime.h>

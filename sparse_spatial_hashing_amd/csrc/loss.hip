@@ -19,8 +19,8 @@
 // by, and forward come from x itself.
 //
 // Bounds. 4,096 tokens of 512 by 214,272 rows take 3.8 ms, of which the forward's logits
-// 0.94 (956 TFLOP/s, matrix units busy 47%), dZ in seven pieces 1.22 (737, 33%), the two
-// gradients' products 1.62 (1,110, 57%); a library product of 8192 cubed reaches 1,185 to
+// 0.95 (947 TFLOP/s, matrix units busy 47%), dZ in seven pieces 1.23 (733, 33%), the two
+// gradients' products 1.60 (1,124, 57%); a library product of 8192 cubed reaches 1,185 to
 // 1,290. Two wavefronts a SIMD wait for LDS and barriers; in the logits' passes the
 // exponentials come on top, an exp2 and two more instructions a logit forward, three, the
 // rounding and 250 MB of stores a piece backward, between the products of a CU's other blocks.
